@@ -20,6 +20,7 @@ CHUNK = 64
 
 # (name, restype, argtypes) of every function declared in include/gdn.h
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F = ctypes.c_int64, ctypes.c_float
 _SIGNATURES = [
     ("gdn_version", _I, []),
     ("gdn_status_string", ctypes.c_char_p, [_I]),
@@ -36,6 +37,10 @@ _SIGNATURES = [
     ("gdn_kda_decode_step", _I, [_P] * 7 + [_I] * 6 + [_P]),
     ("gdn_decoupled_chunk_fwd", _I, [_P] * 10 + [_I] * 9 + [_P, _SZ, _P]),
     ("gdn_decoupled_decode_step", _I, [_P] * 8 + [_I] * 6 + [_P]),
+    ("gdn_recurrent_fwd", _I, [_P] * 10 + [_I] * 7 + [_L] * 3 + [_I] * 3 + [_P]),
+    ("gdn_qk_norm_fwd", _I, [_P] * 8 + [_I] * 4 + [_L] * 4 + [_I, _F, _I, _I, _F, _F, _I, _I, _P]),
+    ("gdn_qk_norm_bwd_workspace_bytes", _SZ, [_I] * 4),
+    ("gdn_qk_norm_bwd", _I, [_P] * 12 + [_I] * 4 + [_L] * 8 + [_I, _F, _I, _I, _F, _F, _I, _I, _P, _SZ, _P]),
 ]
 
 _lib = None
@@ -362,3 +367,217 @@ def gdn_decoupled_decode_step(q, k, v, g, erase, write, state, o=None, *, o_dtyp
                                          _DTYPE.get(o.dtype, -1), _stream(q.device, stream))
     _check(st, "gdn_decoupled_decode_step")
     return o
+
+
+def _same_gpu(device, **ts):
+    """Raise ValueError unless every given tensor is on this GPU (any strides)."""
+    if device.type != "cuda":
+        raise ValueError("gdn: every tensor must be on a GPU")
+    for name, t in ts.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"gdn: {name} is on {t.device}, expected {device}")
+
+
+def _dense(**ts):
+    for name, t in ts.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"gdn: {name} must be contiguous")
+
+
+def _call(name, device, stream, made, *args):
+    """Run an entry point on `stream` (default: the current one of `device`) with `device` current. `made`: tensors
+    allocated by this call; on a stream of the caller's choice the allocator is told that they are in use there."""
+    fn = getattr(lib(), name)
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream(device, stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device, stream))
+    _check(st, name)
+
+
+def _token_stride(t, name, tail):
+    """The stride between tokens of t [..., *tail dims]: its leading dimensions must collapse to one."""
+    lead, strides = t.shape[:-tail], t.stride()[:-tail]
+    stride = None
+    for n, s in zip(reversed(lead), reversed(strides)):
+        if n == 1:
+            continue
+        if stride is None:
+            stride, span = s, s * n
+        elif s != span:
+            raise ValueError(f"gdn: the leading dimensions of {name} (shape {tuple(t.shape)}, strides {t.stride()}) "
+                             "do not form one token dimension of a single stride")
+        else:
+            span = s * n
+    return 0 if stride is None else stride
+
+
+def _row_strides(t, name):
+    """Token and head strides of t [..., heads, d] with contiguous channels."""
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"gdn: the last dimension of {name} must be contiguous")
+    return (_token_stride(t, name, 2) if t.numel() else 0), (t.stride(-2) if t.shape[-2] > 1 else 0)
+
+
+def gdn_recurrent_fwd(q, k, v, g, beta, states, slots, cu_seqlens=None, out_slots=None, o=None, *,
+                      o_dtype=torch.float32, stream=None):
+    """Runs of tokens on a pool of states. q, k [T,H,dk], v [T,HV,dv] (fp32 or bf16; token strides are free, HV a
+    multiple of H); g [T,HV] or, channel-wise, [T,HV,dk], beta [T,HV] fp32; states [n_slots,HV,dv,dk] fp32, updated
+    in place; slots int32 [N], the slot of each sequence (outside the pool: a padded entry, o = 0); cu_seqlens
+    int32 [N+1], or None: one token per sequence; out_slots int32 [T], or None: with it the state after token t goes
+    to slot out_slots[t] (outside the pool: not kept) instead of the last one to the sequence's own slot.
+    Slots written must be distinct. Returns o [T,HV,dv] in o_dtype; rows that no sequence covers are not written."""
+    if q.dim() != 3 or q.dtype not in _IN:
+        raise ValueError(f"gdn: q must be [T, H, d_k] float32 or bfloat16, got {tuple(q.shape)} {q.dtype}")
+    T, H, dk = q.shape
+    if v.dim() != 3:
+        raise ValueError(f"gdn: v must be [T, HV, d_v], got shape {tuple(v.shape)}")
+    HV, dv = v.shape[1:]
+    if H < 1 or HV < H or HV % H:
+        raise ValueError(f"gdn: the {HV} value heads must be a multiple of the {H} query heads")
+    _expect(k, "k", q.shape, (q.dtype,))
+    _expect(v, "v", (T, HV, dv), (q.dtype,))
+    channels = g.dim() == 3
+    _expect(g, "g", (T, HV, dk) if channels else (T, HV), _F32)
+    _expect(beta, "beta", (T, HV), _F32)
+    if states.dim() != 4:
+        raise ValueError(f"gdn: states must be [n_slots, HV, d_v, d_k], got shape {tuple(states.shape)}")
+    _expect(states, "states", (states.shape[0], HV, dv, dk), _F32)
+    if slots.dim() != 1 or slots.dtype != torch.int32:
+        raise ValueError("gdn: slots must be a 1-D int32 tensor")
+    N = slots.numel()
+    if cu_seqlens is None and T != N:
+        raise ValueError(f"gdn: {T} tokens for {N} sequences without cu_seqlens")
+    _expect(cu_seqlens, "cu_seqlens", (N + 1,), (torch.int32,))
+    _expect(out_slots, "out_slots", (T,), (torch.int32,))
+    _expect(o, "o", (T, HV, dv), _IN)
+    _same_gpu(q.device, k=k, v=v, g=g, beta=beta, states=states, slots=slots, cu_seqlens=cu_seqlens,
+              out_slots=out_slots, o=o)
+    _dense(g=g, beta=beta, states=states, slots=slots, cu_seqlens=cu_seqlens, out_slots=out_slots, o=o)
+    strides = []
+    for name, t, d in (("q", q, dk), ("k", k, dk), ("v", v, dv)):
+        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+            raise ValueError(f"gdn: the heads of {name} must follow each other densely within a token")
+        strides.append(t.stride(0) if t.shape[0] > 1 else 0)
+    made = ()
+    if o is None:
+        o = torch.empty((T, HV, dv), dtype=o_dtype, device=q.device)
+        made = (o,)
+    _call("gdn_recurrent_fwd", q.device, stream, made, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(states),
+          _ptr(slots), _ptr(cu_seqlens), _ptr(out_slots), _ptr(o), T, N, H, HV, dk, dv, states.shape[0], *strides,
+          int(channels), _DTYPE.get(q.dtype, -1), _DTYPE.get(o.dtype, -1))
+    return o
+
+
+_NORM = {"l2": 0, "rms": 1}
+_ROPE = {"half": 0, "interleaved": 1}
+
+
+def _check_norm_args(q, k, q_weight, k_weight, positions, inv_freq, norm, layout):
+    if q.dim() < 3 or q.dtype not in _IN:
+        raise ValueError(f"gdn: q must be [..., heads, d] float32 or bfloat16, got {tuple(q.shape)} {q.dtype}")
+    lead, hq, d = q.shape[:-2], q.shape[-2], q.shape[-1]
+    if k.dim() != q.dim():
+        raise ValueError(f"gdn: k has shape {tuple(k.shape)}, expected {tuple(lead)} + (heads, {d})")
+    hk = k.shape[-2]
+    _expect(k, "k", (*lead, hk, d), (q.dtype,))
+    if norm not in _NORM:
+        raise ValueError(f"gdn: norm must be one of {sorted(_NORM)}, got {norm!r}")
+    if layout not in _ROPE:
+        raise ValueError(f"gdn: layout must be one of {sorted(_ROPE)}, got {layout!r}")
+    _expect(q_weight, "q_weight", (d,), _F32)
+    _expect(k_weight, "k_weight", (d,), _F32)
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("gdn: positions and inv_freq go together")
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32:
+            raise ValueError("gdn: inv_freq must be a 1-D float32 tensor of rot / 2 frequencies")
+        rot = 2 * inv_freq.numel()
+        _expect(positions, "positions", lead, (torch.int32,))
+    _same_gpu(q.device, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq)
+    _dense(q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq)
+    tokens = 1
+    for n in lead:
+        tokens *= n
+    return tokens, hq, hk, d, rot
+
+
+def gdn_qk_norm_fwd(q, k, q_weight=None, k_weight=None, *, positions=None, inv_freq=None, norm="l2", eps=1e-6,
+                    q_scale=1.0, layout="half", rope_scale=1.0, out_dtype=None, q_out=None, k_out=None, stream=None):
+    """Norm of every head of q [..., Hq, d] and k [..., Hk, d] (fp32 or bf16, views of a fused projection allowed),
+    with the rotary rotation in the same pass: norm "l2" (unit vectors) or "rms", times the weights [d] fp32 (None:
+    ones), rotated over the first 2 * len(inv_freq) channels by positions [...] int32 times inv_freq, in
+    layout "half" or "interleaved", those channels times rope_scale; q times q_scale. Returns q and k, dense, in out_dtype
+    (default the dtype of q; fp32 is allowed for bf16 inputs)."""
+    tokens, hq, hk, d, rot = _check_norm_args(q, k, q_weight, k_weight, positions, inv_freq, norm, layout)
+    qs, ks = _row_strides(q, "q"), _row_strides(k, "k")
+    made = []
+    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        _expect(t, name, like.shape, _IN)
+    if q_out is not None and k_out is not None and q_out.dtype != k_out.dtype:
+        raise ValueError("gdn: q_out and k_out must have one dtype")
+    given = q_out if q_out is not None else k_out
+    od = given.dtype if given is not None else (out_dtype or q.dtype)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=od, device=q.device)
+        made.append(q_out)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=od, device=q.device)
+        made.append(k_out)
+    _same_gpu(q.device, q_out=q_out, k_out=k_out)
+    _dense(q_out=q_out, k_out=k_out)
+    _call("gdn_qk_norm_fwd", q.device, stream, made, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+          _ptr(inv_freq), _ptr(q_out), _ptr(k_out), tokens, hq, hk, d, *qs, *ks, _NORM[norm], eps, rot, _ROPE[layout],
+          q_scale, rope_scale, _DTYPE.get(q.dtype, -1), _DTYPE.get(od, -1))
+    return q_out, k_out
+
+
+def gdn_qk_norm_bwd_workspace_bytes(tokens, hq, hk, d) -> int:
+    return lib().gdn_qk_norm_bwd_workspace_bytes(tokens, hq, hk, d)
+
+
+def gdn_qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, *, positions=None, inv_freq=None, norm="l2",
+                    eps=1e-6, q_scale=1.0, layout="half", rope_scale=1.0, dq=None, dk=None, need_dw=None,
+                    workspace=None, stream=None):
+    """Backward pass of gdn_qk_norm_fwd with the same arguments: from the gradients dq_out, dk_out of its outputs
+    (dense, the dtype of q, or fp32) returns dq, dk (the dtype of q; given ones may be views with strides, as of a fused
+    gradient) and dq_weight, dk_weight (fp32 [d], None unless need_dw; default: for the weights that are given)."""
+    tokens, hq, hk, d, rot = _check_norm_args(q, k, q_weight, k_weight, positions, inv_freq, norm, layout)
+    gt = (q.dtype, torch.float32)
+    _expect(dq_out, "dq_out", q.shape, gt)
+    _expect(dk_out, "dk_out", k.shape, (dq_out.dtype,))
+    _expect(dq, "dq", q.shape, (q.dtype,))
+    _expect(dk, "dk", k.shape, (q.dtype,))
+    made = []
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        made.append(dq)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        made.append(dk)
+    dqw = dkw = None
+    if need_dw or (need_dw is None and q_weight is not None):
+        dqw = torch.empty(d, dtype=torch.float32, device=q.device)
+    if need_dw or (need_dw is None and k_weight is not None):
+        dkw = torch.empty(d, dtype=torch.float32, device=q.device)
+    made += [dqw, dkw]
+    if dqw is not None or dkw is not None:
+        need = gdn_qk_norm_bwd_workspace_bytes(tokens, hq, hk, d)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            made.append(workspace)
+    _same_gpu(q.device, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk, workspace=workspace)
+    _dense(dq_out=dq_out, dk_out=dk_out, workspace=workspace)
+    strides = [s for t, name in ((q, "q"), (k, "k"), (dq, "dq"), (dk, "dk")) for s in _row_strides(t, name)]
+    _call("gdn_qk_norm_bwd", q.device, stream, made, _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight),
+          _ptr(k_weight), _ptr(positions), _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), tokens, hq, hk, d,
+          *strides, _NORM[norm], eps, rot, _ROPE[layout], q_scale, rope_scale, _DTYPE.get(q.dtype, -1),
+          _DTYPE.get(dq_out.dtype, -1), _ptr(workspace),
+          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return dq, dk, dqw, dkw

@@ -421,3 +421,145 @@ GDN_EXPORT int gdn_decoupled_decode_step(const void* q, const void* k, const voi
     return gdn::launch_decode(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK
                                                                                 : GDN_ERR_HIP;
 }
+
+GDN_EXPORT int gdn_recurrent_fwd(const void* q, const void* k, const void* v, const float* g_log_alpha,
+                                 const float* beta, float* states, const int32_t* slots,
+                                 const int32_t* cu_seqlens, const int32_t* out_slots, void* o, int T, int N,
+                                 int H, int HV, int dk, int dv, int n_slots, int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, int channel_gate, int dtype, int o_dtype, void* stream) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_DTYPE;
+    if (o_dtype != GDN_F32 && o_dtype != GDN_BF16) return GDN_ERR_DTYPE;
+    if (!head_dim_ok(dk) || !head_dim_ok(dv)) return GDN_ERR_UNSUPPORTED;
+    if (N < 0 || T < 0 || H < 1 || HV < H || HV % H != 0 || HV > 32768 || n_slots < 0) return GDN_ERR_SHAPE;
+    if (!cu_seqlens && T != N) return GDN_ERR_SHAPE;
+    // a work-group of 256 threads per (sequence, value head, tile of state rows), fewer than 2^32 threads in all
+    if ((long long)N * HV >= 1 << 21) return GDN_ERR_SHAPE;
+    if (q_stride < 0 || k_stride < 0 || v_stride < 0) return GDN_ERR_SHAPE;
+    if (T == 0 || N == 0) return GDN_OK;   // no token: nothing to read or write
+    if (!q || !k || !v || !g_log_alpha || !beta || !slots || !o || (!states && n_slots > 0)) return GDN_ERR_NULL;
+    const void* al16[] = {q, k, v, o, states};
+    for (const void* x : al16)
+        if (!aligned(x, 16)) return GDN_ERR_ALIGN;
+    const void* al4[] = {beta, slots, cu_seqlens, out_slots};
+    for (const void* x : al4)
+        if (!aligned(x, 4)) return GDN_ERR_ALIGN;
+    if (!aligned(g_log_alpha, channel_gate ? 16 : 4)) return GDN_ERR_ALIGN;
+    const int per16 = dtype == GDN_BF16 ? 8 : 4;   // elements of 16 bytes
+    if (q_stride % per16 || k_stride % per16 || v_stride % per16) return GDN_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int chk = debug_check_offsets(cu_seqlens, N, T, s);
+    if (chk != GDN_OK) return chk;
+    gdn::RecurrentProblem p{};
+    p.q = q; p.k = k; p.v = v; p.g = g_log_alpha; p.beta = beta; p.states = states;
+    p.slots = slots; p.cu_seqlens = cu_seqlens; p.out_slots = out_slots; p.o = o;
+    p.q_token = q_stride; p.k_token = k_stride; p.v_token = v_stride;
+    p.T = T; p.N = N; p.H = H; p.HV = HV; p.dk = dk; p.dv = dv; p.n_slots = n_slots;
+    p.bf16 = dtype == GDN_BF16;
+    p.o_bf16 = o_dtype == GDN_BF16;
+    p.channel_gate = channel_gate != 0;
+    return gdn::launch_recurrent(p, s) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+namespace {
+// Checks shared by both directions of the q/k norm; fills the shared part of the problem.
+int check_norm(const void* q, const void* k, const float* q_weight, const float* k_weight, const int32_t* positions,
+               const float* inv_freq, int tokens, int hq, int hk, int d, int64_t q_token, int64_t q_head,
+               int64_t k_token, int64_t k_head, int norm, float eps, int rot, int rope, float q_scale,
+               float rope_scale, int dtype, int y_dtype, gdn::NormProblem* p) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_DTYPE;
+    if (y_dtype != GDN_F32 && !(y_dtype == GDN_BF16 && dtype == GDN_BF16)) return GDN_ERR_DTYPE;
+    if (norm != GDN_NORM_L2 && norm != GDN_NORM_RMS) return GDN_ERR_UNSUPPORTED;
+    if (rope != GDN_ROPE_HALF && rope != GDN_ROPE_INTERLEAVED) return GDN_ERR_UNSUPPORTED;
+    if (d < 8 || d > 256 || d % 8) return GDN_ERR_UNSUPPORTED;
+    if (rot < 0 || rot > d || rot % (rope == GDN_ROPE_HALF ? 16 : 2)) return GDN_ERR_UNSUPPORTED;
+    if (tokens < 0 || hq < 1 || hk < 1 || hq > 32768 || hk > 32768) return GDN_ERR_SHAPE;
+    if (!(eps > 0.f)) return GDN_ERR_SHAPE;
+    // work-groups of 256 threads on 32 rows or more, fewer than 2^32 threads in all
+    if ((long long)tokens * (hq + hk) > (1LL << 28)) return GDN_ERR_SHAPE;
+    const int64_t strides[] = {q_token, q_head, k_token, k_head};
+    for (int64_t x : strides)
+        if (x < 0) return GDN_ERR_SHAPE;
+    if (tokens > 0 && (!q || !k || (rot > 0 && (!positions || !inv_freq)))) return GDN_ERR_NULL;
+    const void* al16[] = {q, k, q_weight, k_weight};
+    for (const void* x : al16)
+        if (!aligned(x, 16)) return GDN_ERR_ALIGN;
+    if (!aligned(positions, 4) || !aligned(inv_freq, 4)) return GDN_ERR_ALIGN;
+    const int per16 = dtype == GDN_BF16 ? 8 : 4;   // elements of 16 bytes
+    for (int64_t x : strides)
+        if (x % per16) return GDN_ERR_ALIGN;
+    p->q = q; p->k = k; p->q_weight = q_weight; p->k_weight = k_weight;
+    p->q_token = q_token; p->q_head = q_head; p->k_token = k_token; p->k_head = k_head;
+    p->positions = positions; p->inv_freq = inv_freq;
+    p->tokens = tokens; p->hq = hq; p->hk = hk; p->d = d; p->rot = rot;
+    p->interleaved = rope == GDN_ROPE_INTERLEAVED;
+    p->x_bf16 = dtype == GDN_BF16;
+    p->y_bf16 = y_dtype == GDN_BF16;
+    p->inv_n = norm == GDN_NORM_RMS ? 1.f / d : 1.f;
+    p->eps = eps; p->q_scale = q_scale; p->rope_scale = rope_scale;
+    return GDN_OK;
+}
+}  // namespace
+
+GDN_EXPORT int gdn_qk_norm_fwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                               const int32_t* positions, const float* inv_freq, void* q_out, void* k_out,
+                               int tokens, int hq, int hk, int d, int64_t q_token_stride, int64_t q_head_stride,
+                               int64_t k_token_stride, int64_t k_head_stride, int norm, float eps, int rot,
+                               int rope, float q_scale, float rope_scale, int dtype, int out_dtype, void* stream) {
+    gdn::NormProblem p{};
+    const int st = check_norm(q, k, q_weight, k_weight, positions, inv_freq, tokens, hq, hk, d, q_token_stride,
+                              q_head_stride, k_token_stride, k_head_stride, norm, eps, rot, rope, q_scale, rope_scale,
+                              dtype, out_dtype, &p);
+    if (st != GDN_OK) return st;
+    if (tokens > 0 && (!q_out || !k_out)) return GDN_ERR_NULL;
+    if (!aligned(q_out, 16) || !aligned(k_out, 16)) return GDN_ERR_ALIGN;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    return gdn::launch_qk_norm(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+GDN_EXPORT size_t gdn_qk_norm_bwd_workspace_bytes(int tokens, int hq, int hk, int d) {
+    if (tokens < 0 || hq < 1 || hk < 1 || hq > 32768 || hk > 32768 || d < 8 || d > 256 || d % 8) return 0;
+    if ((long long)tokens * (hq + hk) > (1LL << 28)) return 0;
+    return (size_t)gdn::norm_grad_blocks((long)tokens * (hq + hk)) * 2 * d * sizeof(float);
+}
+
+GDN_EXPORT int gdn_qk_norm_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                               const float* q_weight, const float* k_weight, const int32_t* positions,
+                               const float* inv_freq, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                               int tokens, int hq, int hk, int d, int64_t q_token_stride, int64_t q_head_stride,
+                               int64_t k_token_stride, int64_t k_head_stride, int64_t dq_token_stride,
+                               int64_t dq_head_stride, int64_t dk_token_stride, int64_t dk_head_stride, int norm,
+                               float eps, int rot, int rope, float q_scale, float rope_scale, int dtype,
+                               int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    gdn::NormProblem p{};
+    const int st = check_norm(q, k, q_weight, k_weight, positions, inv_freq, tokens, hq, hk, d, q_token_stride,
+                              q_head_stride, k_token_stride, k_head_stride, norm, eps, rot, rope, q_scale, rope_scale,
+                              dtype, out_dtype, &p);
+    if (st != GDN_OK) return st;
+    const int64_t strides[] = {dq_token_stride, dq_head_stride, dk_token_stride, dk_head_stride};
+    for (int64_t x : strides)
+        if (x < 0) return GDN_ERR_SHAPE;
+    // rows of an output must not lie over each other (a stride of 0 is how an expanded tensor looks)
+    if ((tokens > 1 && (dq_token_stride < d || dk_token_stride < d)) || (hq > 1 && dq_head_stride < d) ||
+        (hk > 1 && dk_head_stride < d))
+        return GDN_ERR_SHAPE;
+    if (tokens > 0 && (!dq_out || !dk_out || !dq || !dk)) return GDN_ERR_NULL;
+    const void* al16[] = {dq_out, dk_out, dq, dk};
+    for (const void* x : al16)
+        if (!aligned(x, 16)) return GDN_ERR_ALIGN;
+    for (int64_t x : strides)
+        if (x % (p.x_bf16 ? 8 : 4)) return GDN_ERR_ALIGN;
+    if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return GDN_ERR_ALIGN;
+    if (dq_weight || dk_weight) {
+        const size_t need = gdn_qk_norm_bwd_workspace_bytes(tokens, hq, hk, d);
+        if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return GDN_ERR_ALIGN;
+    }
+    p.backward = 1;
+    p.dq_in = dq_out; p.dk_in = dk_out; p.dq_out = dq; p.dk_out = dk;
+    p.dq_token = dq_token_stride; p.dq_head = dq_head_stride;
+    p.dk_token = dk_token_stride; p.dk_head = dk_head_stride;
+    p.dqw = dq_weight; p.dkw = dk_weight;
+    p.partial = static_cast<float*>(workspace);
+    return gdn::launch_qk_norm(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}

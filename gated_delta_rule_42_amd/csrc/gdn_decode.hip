@@ -21,22 +21,6 @@
 
 namespace gdn {
 
-// One DPP lane permutation within each 16-lane row (control word fixed at compile time).
-template <int CTRL>
-__device__ __forceinline__ float dpp_f32(float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
-}
-
-// Sum over the 16 lanes of a DPP row (all 16 lanes receive the total):
-// swap neighbours, swap pairs, mirror within 8, mirror within 16.
-__device__ __forceinline__ float row16_sum(float x) {
-    x += dpp_f32<0xB1>(x);   // quad_perm [1,0,3,2]
-    x += dpp_f32<0x4E>(x);   // quad_perm [2,3,0,1]
-    x += dpp_f32<0x141>(x);  // row_half_mirror
-    x += dpp_f32<0x140>(x);  // row_mirror
-    return x;
-}
-
 // One work-group per (sequence, head). Its 256 lanes form 16 groups of 16; group g owns
 // rows g, g+16, ...; within a group, lane l16 owns the columns 4 l16 + 0..3 of each 64-column
 // half of a row, so that every load and store of the state covers whole 256-byte runs

@@ -405,6 +405,23 @@ __device__ __forceinline__ float wave_inclusive_sum(float x) {
     return x;
 }
 
+// ------------------------------------------------------------------ row sums
+// One DPP lane permutation within each 16-lane row (control word fixed at compile time).
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+
+// Sum over the 16 lanes of a DPP row (all 16 lanes receive the total):
+// swap neighbours, swap pairs, mirror within 8, mirror within 16.
+__device__ __forceinline__ float row16_sum(float x) {
+    x += dpp_f32<0xB1>(x);   // quad_perm [1,0,3,2]
+    x += dpp_f32<0x4E>(x);   // quad_perm [2,3,0,1]
+    x += dpp_f32<0x141>(x);  // row_half_mirror
+    x += dpp_f32<0x140>(x);  // row_mirror
+    return x;
+}
+
 // acc (16x16 fp32 tile) += A[16 x 4] B[4 x 16] on the fp32 matrix core: lane l gives
 // A[l % 16][l / 16] and B[l / 16][l % 16]; acc holds rows 4 (l / 16) + 0..3 of column l % 16.
 __device__ __forceinline__ f32x4_t mfma4(float a, float b, f32x4_t acc) {

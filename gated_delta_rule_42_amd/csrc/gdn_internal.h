@@ -208,6 +208,53 @@ struct DecodeProblem {
 
 hipError_t launch_decode(const DecodeProblem& p, hipStream_t s);
 
+// Runs of tokens on a pool of states (gdn_recurrent.hip).
+struct RecurrentProblem {
+    const void* q;               // [T, H, dk], token stride q_token
+    const void* k;
+    const void* v;               // [T, HV, dv], token stride v_token
+    const float* g;              // [T, HV] or (channel_gate) [T, HV, dk]
+    const float* beta;           // [T, HV]
+    float* states;               // [n_slots, HV, dv, dk]
+    const int32_t* slots;        // [N] slot of each sequence; outside [0, n_slots): the sequence is skipped
+    const int32_t* cu_seqlens;   // [N + 1], or NULL: one token per sequence
+    const int32_t* out_slots;    // [T] slot taking the state after each token, or NULL
+    void* o;                     // [T, HV, dv]
+    long q_token, k_token, v_token;
+    int T, N, H, HV, dk, dv, n_slots;
+    int bf16, o_bf16, channel_gate;
+};
+hipError_t launch_recurrent(const RecurrentProblem& p, hipStream_t s);
+
+// Per-head norm and rotation of queries and keys (gdn_qknorm.hip). Strides in elements; a row's channels are contiguous.
+struct NormProblem {
+    const void* q;               // [tokens, hq, d]
+    const void* k;               // [tokens, hk, d]
+    long q_token, q_head, k_token, k_head;
+    const float* q_weight;       // [d] or NULL (ones)
+    const float* k_weight;
+    const int32_t* positions;    // [tokens] (rot > 0)
+    const float* inv_freq;       // [rot / 2]
+    void* q_out;                 // forward: dense [tokens, hq, d], [tokens, hk, d]
+    void* k_out;
+    const void* dq_in;           // backward: dense gradients of the outputs
+    const void* dk_in;
+    void* dq_out;                // backward: gradients of the inputs, with strides
+    void* dk_out;
+    long dq_token, dq_head, dk_token, dk_head;
+    float* dqw;                  // backward: [d] or NULL
+    float* dkw;
+    float* partial;              // backward with weight gradients: [norm_grad_blocks, 2, d]
+    long tokens;
+    int hq, hk, d, rot, interleaved;
+    int x_bf16, y_bf16;          // types of q, k (and their gradients) and of the outputs (and theirs)
+    int backward;
+    float inv_n, eps, q_scale, rope_scale;
+};
+constexpr int kNormGradBlocks = 1024;
+int norm_grad_blocks(long nrows);
+hipError_t launch_qk_norm(const NormProblem& p, hipStream_t s);
+
 // gdn_chunk_fwd's host-side argument checks, leaving out the workspace; returns a gdn_status.
 int chunk_fwd_check(const void* q, const void* k, const void* v, const float* g_log_alpha, const float* beta,
                     const float* h0, const void* o, const float* hT, const int32_t* cu_seqlens, int chunk,

@@ -363,6 +363,89 @@ int gdn_decoupled_decode_step(const void *q, const void *k, const void *v, const
                               const float *erase, const float *write, float *state, void *o, int N,
                               int H, int dk, int dv, int dtype, int o_dtype, void *stream);
 
+/*
+ * Recurrent form for serving: runs of tokens of N sequences, each applied to its state in a
+ * pool, token by token (the recurrence at the top of this file; with channel_gate the
+ * channel-wise decay of gdn_kda_chunk_fwd). One call takes a batch of single new tokens, of draft
+ * tokens to be verified, or of short prompts, in any mix of lengths; for prompts of some
+ * hundred tokens and more the chunked entry points are faster.
+ *
+ *   q, k        [T, H, dk]  dtype; token t starts at element t * q_stride (k_stride), its heads
+ *               follow each other densely
+ *   v           [T, HV, dv] dtype, token stride v_stride. HV is a multiple of H: value head j
+ *               uses q and k of head j / (HV / H)
+ *   g_log_alpha [T, HV] fp32, or with channel_gate [T, HV, dk] (16-byte aligned); <= 0
+ *   beta        [T, HV] fp32
+ *   states      [n_slots, HV, dv, dk] fp32, the pool
+ *   slots       int32 [N] device array: the slot of each sequence's state. A sequence whose slot
+ *               is negative or >= n_slots is a padded entry: o is 0 for its tokens and no state is
+ *               read or written
+ *   cu_seqlens  int32 [N + 1] device array, sequence n has the tokens cu[n] .. cu[n+1] - 1 (none:
+ *               its state stays as it is), or NULL: one token per sequence (T = N). Offsets outside
+ *               [0, T] are clamped; rows of o that no sequence covers are left as they were
+ *   out_slots   NULL: the state after a sequence's last token replaces the one in its slot. Else
+ *               int32 [T]: the state after token t is written to slot out_slots[t] (not written where that
+ *               is negative or >= n_slots), and the sequence's own slot is written only if named there
+ *   o           [T, HV, dv] o_dtype, dense
+ * The slots that one call writes must be distinct from each other and from the slots that other
+ * sequences of the call read; a sequence may write the slot it reads. Where this is broken the
+ * contents of those slots are undefined (accesses stay inside the pool). All arithmetic
+ * is fp32; a bf16 o is the fp32 result rounded to nearest even. Strides are in elements, multiples of 16 bytes.
+ * dk, dv in {64, 128}; HV <= 32768; N * HV < 2^21. T = 0 or N = 0 does nothing.
+ */
+int gdn_recurrent_fwd(const void *q, const void *k, const void *v, const float *g_log_alpha,
+                      const float *beta, float *states, const int32_t *slots,
+                      const int32_t *cu_seqlens, const int32_t *out_slots, void *o, int T, int N,
+                      int H, int HV, int dk, int dv, int n_slots, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, int channel_gate, int dtype, int o_dtype, void *stream);
+
+/*
+ * The norm that turns raw query and key projections into what the entry points above take (unit
+ * vectors), for each head, with the rotary position rotation in the same pass. For a row x [d]
+ * of one token and head, with n = 1 (GDN_NORM_L2) or n = d (GDN_NORM_RMS):
+ *     y = scale * R(p) (w * x * (sum x^2 / n + eps)^(-1/2)),   scale = q_scale for q, 1 for k.
+ * R(p) turns pairs of the first `rot` channels by the angle positions[token] * inv_freq[j], j < rot / 2,
+ * and multiplies them by rope_scale: channels (j, j + rot/2) in the half layout (GDN_ROPE_HALF),
+ * (2j, 2j + 1) in the interleaved one. Scaled frequencies for long contexts are a matter of
+ * inv_freq and rope_scale. Angles are formed in fp64, everything else in fp32.
+ *
+ *   q, k        [tokens, hq, d], [tokens, hk, d] dtype, channels contiguous, with token and head
+ *               strides in elements (views of a fused projection need no copy)
+ *   q_weight, k_weight  fp32 [d] (16-byte aligned) or NULL (ones)
+ *   positions   int32 [tokens], inv_freq fp32 [rot / 2]; not used when rot = 0
+ *   q_out, k_out  dense [tokens, hq, d], [tokens, hk, d] out_dtype (GDN_BF16 only for bf16 inputs)
+ *   d           a multiple of 8, 8 .. 256; rot 0 .. d, a multiple of 2 (half layout: of 16)
+ *   eps > 0; hq, hk >= 1; tokens * (hq + hk) <= 2^28
+ * Pointers and strides are multiples of 16 bytes. A row of zeros gives zeros. Sums of squares are
+ * fp32: rows of magnitudes above about 1e18 overflow.
+ */
+typedef enum { GDN_NORM_L2 = 0, GDN_NORM_RMS = 1 } gdn_norm;
+typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope;
+int gdn_qk_norm_fwd(const void *q, const void *k, const float *q_weight, const float *k_weight,
+                    const int32_t *positions, const float *inv_freq, void *q_out, void *k_out,
+                    int tokens, int hq, int hk, int d, int64_t q_token_stride, int64_t q_head_stride,
+                    int64_t k_token_stride, int64_t k_head_stride, int norm, float eps, int rot,
+                    int rope, float q_scale, float rope_scale, int dtype, int out_dtype, void *stream);
+
+/*
+ * Backward pass of gdn_qk_norm_fwd: from the gradients dq_out, dk_out of its outputs (dense, of type
+ * out_dtype) the gradients dq, dk of q and k (of type dtype, with strides, so that they can be written
+ * into the gradient of a fused projection) and, where not NULL, of the weights (fp32 [d]; defined
+ * also for weights of NULL). The weights' gradients are sums over all tokens and heads in a fixed order and take
+ * a workspace of gdn_qk_norm_bwd_workspace_bytes(...) bytes, 256-byte aligned (fp32 [work-groups, 2, d]); without them none is used. The
+ * other arguments are the forward call's. dq and dk may be q and k themselves (with their strides) or
+ * dense over dq_out, dk_out where the types agree; other overlaps are undefined.
+ */
+size_t gdn_qk_norm_bwd_workspace_bytes(int tokens, int hq, int hk, int d);
+int gdn_qk_norm_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out,
+                    const float *q_weight, const float *k_weight, const int32_t *positions,
+                    const float *inv_freq, void *dq, void *dk, float *dq_weight, float *dk_weight,
+                    int tokens, int hq, int hk, int d, int64_t q_token_stride, int64_t q_head_stride,
+                    int64_t k_token_stride, int64_t k_head_stride, int64_t dq_token_stride,
+                    int64_t dq_head_stride, int64_t dk_token_stride, int64_t dk_head_stride, int norm,
+                    float eps, int rot, int rope, float q_scale, float rope_scale, int dtype,
+                    int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
