@@ -34,6 +34,8 @@ _SIGNATURES = [
     ("gdn_chunk_bwd", _I, [_P] * 15 + [_I] * 9 + [_P, _SZ, _P]),
     ("gdn_kda_chunk_fwd_workspace_bytes", _SZ, [_I] * 9),
     ("gdn_kda_chunk_fwd", _I, [_P] * 9 + [_I] * 9 + [_P, _SZ, _P]),
+    ("gdn_kda_chunk_bwd_workspace_bytes", _SZ, [_I] * 9),
+    ("gdn_kda_chunk_bwd", _I, [_P] * 15 + [_I] * 9 + [_P, _SZ, _P]),
     ("gdn_kda_decode_step", _I, [_P] * 7 + [_I] * 6 + [_P]),
     ("gdn_decoupled_chunk_fwd", _I, [_P] * 10 + [_I] * 9 + [_P, _SZ, _P]),
     ("gdn_decoupled_decode_step", _I, [_P] * 8 + [_I] * 6 + [_P]),
@@ -581,3 +583,36 @@ def gdn_qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, *, posit
           _DTYPE.get(dq_out.dtype, -1), _ptr(workspace),
           workspace.numel() * workspace.element_size() if workspace is not None else 0)
     return dq, dk, dqw, dkw
+
+
+def gdn_kda_chunk_bwd_workspace_bytes(B, T, H, dk, dv, N, varlen, chunk=CHUNK, dtype=torch.bfloat16) -> int:
+    return lib().gdn_kda_chunk_bwd_workspace_bytes(B, T, H, dk, dv, N, int(bool(varlen)), chunk, _DTYPE[dtype])
+
+
+def gdn_kda_chunk_bwd(q, k, v, g, beta, do, h0=None, dhT=None, cu_seqlens=None, chunk=CHUNK, *, grad_dtype=None,
+                      need_dh0=True, workspace=None, stream=None):
+    """Backward pass of gdn_kda_chunk_fwd: as gdn_chunk_bwd, with g [B,T,H,dk] fp32. Returns dq, dk, dv (grad_dtype,
+    default the dtype of q; fp32 is allowed for bf16 inputs), dg [B,T,H,dk] and dbeta [B,T,H] fp32 and dh0 [N,H,dv,dk]
+    fp32 (None unless need_dh0)."""
+    B, T, H, dk, dv, N = _check_chunk_args(q, k, v, g, beta, h0, cu_seqlens, hT=dhT, g_channels=True)
+    _expect(do, "do", (B, T, H, dv), (q.dtype,))
+    dev = q.device
+    _same_gpu(dev, k=k, v=v, g=g, beta=beta, do=do, h0=h0, dhT=dhT, cu_seqlens=cu_seqlens, workspace=workspace)
+    _dense(q=q, k=k, v=v, g=g, beta=beta, do=do, h0=h0, dhT=dhT, cu_seqlens=cu_seqlens, workspace=workspace)
+    gd = grad_dtype or q.dtype
+    dq = torch.empty(q.shape, dtype=gd, device=dev)
+    dk_ = torch.empty(k.shape, dtype=gd, device=dev)
+    dv_ = torch.empty(v.shape, dtype=gd, device=dev)
+    dg = torch.empty(g.shape, dtype=torch.float32, device=dev)
+    db = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+    dh0 = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev) if need_dh0 else None
+    made = [dq, dk_, dv_, dg, db, dh0]
+    need = gdn_kda_chunk_bwd_workspace_bytes(B, T, H, dk, dv, N, cu_seqlens is not None, chunk, q.dtype)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _call("gdn_kda_chunk_bwd", dev, stream, made, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(do),
+          _ptr(dhT), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dg), _ptr(db), _ptr(dh0), _ptr(cu_seqlens), chunk, B, T, H, dk,
+          dv, N, _DTYPE.get(q.dtype, -1), _DTYPE.get(gd, -1), _ptr(workspace),
+          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return dq, dk_, dv_, dg, db, dh0

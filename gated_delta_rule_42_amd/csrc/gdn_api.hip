@@ -383,6 +383,73 @@ GDN_EXPORT int gdn_decoupled_chunk_fwd(const void* q, const void* k, const void*
                          H, dk, dv, N, dtype, o_dtype, workspace, workspace_bytes, stream);
 }
 
+GDN_EXPORT size_t gdn_kda_chunk_bwd_workspace_bytes(int B, int T, int H, int dk, int dv, int N, int varlen,
+                                                    int chunk, int dtype) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return 0;
+    if (chunk != 64 || !head_dim_ok(dk) || !head_dim_ok(dv)) return 0;
+    if (shape_check(B, T, H, dk, dv, N, varlen != 0) != GDN_OK) return 0;
+    return gdn::kda_bwd_workspace_layout(B, T, H, dk, dv, N, varlen != 0).total;
+}
+
+GDN_EXPORT int gdn_kda_chunk_bwd(const void* q, const void* k, const void* v, const float* g_log_alpha,
+                                 const float* beta, const float* h0, const void* d_o, const float* dhT,
+                                 void* dq, void* dk_out, void* dv_out, float* dg, float* dbeta, float* dh0,
+                                 const int32_t* cu_seqlens, int chunk, int B, int T, int H, int dk, int dv,
+                                 int N, int dtype, int grad_dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_DTYPE;
+    if (grad_dtype != GDN_F32 && !(grad_dtype == GDN_BF16 && dtype == GDN_BF16)) return GDN_ERR_DTYPE;
+    if (chunk != 64) return GDN_ERR_UNSUPPORTED;
+    if (!head_dim_ok(dk) || !head_dim_ok(dv)) return GDN_ERR_UNSUPPORTED;
+    const int sc = shape_check(B, T, H, dk, dv, N, cu_seqlens != nullptr);
+    if (sc != GDN_OK) return sc;
+    const long long tokens = (long long)B * T;
+    if (tokens > 0 && (!q || !k || !v || !g_log_alpha || !beta || !d_o || !dq || !dk_out || !dv_out || !dg || !dbeta))
+        return GDN_ERR_NULL;
+    const void* al16[] = {q, k, v, d_o, dq, dk_out, dv_out, h0, dhT, dh0, g_log_alpha, dg};
+    for (const void* x : al16)
+        if (x && !aligned(x, 16)) return GDN_ERR_ALIGN;
+    const void* al4[] = {beta, dbeta, cu_seqlens};
+    for (const void* x : al4)
+        if (x && !aligned(x, 4)) return GDN_ERR_ALIGN;
+    const gdn::KdaBwdLayout w = gdn::kda_bwd_workspace_layout(B, T, H, dk, dv, N, cu_seqlens != nullptr);
+    if (w.fwd.nc_bound * H > 0x7fffffffL) return GDN_ERR_SHAPE;
+    // the walks: a work-group of 256 threads per (sequence, head, 32 columns), fewer than 2^32 threads in all
+    if ((long long)N * H >= 1 << 21) return GDN_ERR_SHAPE;
+    if (w.total > 0 && (!workspace || workspace_bytes < w.total)) return GDN_ERR_WORKSPACE;
+    if (workspace && !aligned(workspace, 256)) return GDN_ERR_ALIGN;
+    char* base = static_cast<char*>(workspace);
+    gdn::KdaBwdProblem b{};
+    gdn::ChunkProblem& P = b.f;
+    P.q = q; P.k = k; P.v = v; P.g = g_log_alpha; P.beta = beta; P.h0 = h0;
+    P.cu_seqlens = cu_seqlens;
+    P.B = B; P.T = T; P.H = H; P.dk = dk; P.dv = dv; P.N = N;
+    P.bf16 = dtype == GDN_BF16;
+    P.nc_bound = w.fwd.nc_bound;
+    P.nc_per_seq = (T + 63) / 64;
+    P.chunk_base = cu_seqlens ? reinterpret_cast<int32_t*>(base + w.fwd.off_base) : nullptr;
+    if (w.fwd.nc_bound > 0) {
+        P.mmat = base + w.fwd.off_m;
+        P.pmat = base + w.fwd.off_p;
+        P.khat = reinterpret_cast<float*>(base + w.fwd.off_kh);
+        P.qhat = reinterpret_cast<float*>(base + w.fwd.off_qh);
+        P.kdec = reinterpret_cast<float*>(base + w.fwd.off_kd);
+        P.lam = reinterpret_cast<float*>(base + w.fwd.off_lam);
+        P.tmat = reinterpret_cast<float*>(base + w.off_t);
+        P.states = reinterpret_cast<float*>(base + w.off_states);
+        b.dstates = reinterpret_cast<float*>(base + w.off_dstates);
+        b.delta = reinterpret_cast<float*>(base + w.off_delta);
+        b.ymat = reinterpret_cast<float*>(base + w.off_y);
+    }
+    b.d_o = d_o; b.dhT = dhT;
+    b.dq = dq; b.dk = dk_out; b.dv = dv_out; b.dg = dg; b.dbeta = dbeta; b.dh0 = dh0;
+    b.grad_bf16 = grad_dtype == GDN_BF16;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int chk = debug_check_offsets(cu_seqlens, N, T, s);
+    if (chk != GDN_OK) return chk;
+    return gdn::launch_kda_chunk_bwd(b, s) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
 GDN_EXPORT int gdn_kda_decode_step(const void* q, const void* k, const void* v, const float* g_log_alpha,
                                    const float* beta, float* state, void* o, int N, int H, int dk,
                                    int dv, int dtype, int o_dtype, void* stream) {

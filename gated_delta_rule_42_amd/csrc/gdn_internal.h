@@ -190,6 +190,36 @@ struct KdaLayout {
 KdaLayout kda_workspace_layout(int B, int T, int H, int dk, int N, int varlen, int elem);
 hipError_t launch_kda_chunk_fwd(const ChunkProblem& p, hipStream_t s);
 
+// The log decay that the backward pass takes for any smaller one: e^-104 is below half of fp32's smallest number.
+constexpr float kMinLogDecay = -104.f;
+
+// The channel-wise stage 1 with fp32 operators and products for either input type, and T into p.tmat.
+hipError_t launch_kda_prepare_f32(const ChunkProblem& p, hipStream_t s);
+
+// Backward pass of the channel-wise rule (gdn_kda_bwd.hip). `f`: the forward problem with the fp32 regions of stage 1, tmat
+// and states set.
+struct KdaBwdProblem {
+    ChunkProblem f;
+    const void* d_o;             // [B,T,H,dv], type of q
+    const float* dhT;            // NULL: zero
+    void* dq;                    // [B,T,H,dk], fp32 or bf16 (grad_bf16)
+    void* dk;
+    void* dv;                    // [B,T,H,dv]
+    float* dg;                   // [B,T,H,dk]
+    float* dbeta;                // [B,T,H]
+    float* dh0;                  // [N,H,dv,dk] or NULL
+    float* dstates;              // [nc_bound, H, dv, dk] gradient reaching the state behind each chunk
+    float* delta;                // [nc_bound, H, 64, dv] Delta
+    float* ymat;                 // [nc_bound, H, 64, dv] T^T dDelta
+    int grad_bf16;
+};
+struct KdaBwdLayout {
+    KdaLayout fwd;
+    size_t off_t, off_states, off_dstates, off_delta, off_y, total;
+};
+KdaBwdLayout kda_bwd_workspace_layout(int B, int T, int H, int dk, int dv, int N, int varlen);
+hipError_t launch_kda_chunk_bwd(const KdaBwdProblem& p, hipStream_t s);
+
 struct DecodeProblem {
     const void* q;
     const void* k;

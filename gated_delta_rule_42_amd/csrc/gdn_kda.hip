@@ -469,21 +469,23 @@ struct KdaPrepStage {
 // decoupled gates (DEC) the erased read runs along E * K, so A's left operand is E * K (held
 // in the Q buffer until A is formed, then Q is moved there from its raw copy in P), Kh is
 // E * K * e^gamma, V is scaled by the write gate in stage 2 and Mmat is T itself.
-template <typename TIn, int DK, bool DEC>
+// F32OP: fp32 operators and fp32 products for either input type (the backward pass, which also takes T itself).
+template <typename TIn, int DK, bool DEC, bool F32OP = sizeof(TIn) == 4>
 __global__ __launch_bounds__(kKdaPrepThreads) void kda_prepare_kernel(ChunkProblem p) {
     using SM = KdaPrepSmem<DK>;
     constexpr int PK = SM::PK, PF = SM::PF;
-    constexpr bool F16 = sizeof(TIn) == 2;  // off-diagonal Gram blocks on the fp16 matrix core
+    constexpr bool F16 = !F32OP;  // off-diagonal Gram blocks on the fp16 matrix core
     // bf16: the operators go out as the LDS images the DMA-fed stage 2 copies
     // (kda_propagate_dma_kernel); fp32: row-major
-    constexpr bool IMG = sizeof(TIn) == 2;
+    constexpr bool IMG = !F32OP;
     static_assert(KdaOffdiag<DK>::BYTES <= (int)sizeof(SM::T), "off-diagonal scratch fits in T");
     __shared__ SM sm;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int H = p.H;
     const long nunits = p.nc_bound * H;
     const TIn* qp = static_cast<const TIn*>(p.q);
-    using TM = typename Operand<TIn>::type;   // operators are written as fp16 for bf16 inputs
+    // operators are written as fp16 for bf16 inputs
+    using TM = typename std::conditional<F32OP, float, typename Operand<TIn>::type>::type;
     TM* khat = reinterpret_cast<TM*>(p.khat);
     TM* qhat = reinterpret_cast<TM*>(p.qhat);
     TM* kdec = reinterpret_cast<TM*>(p.kdec);
@@ -509,6 +511,16 @@ __global__ __launch_bounds__(kKdaPrepThreads) void kda_prepare_kernel(ChunkProbl
         // of one phase are formed there instead of being hoisted out of the unit loop and held
         // (or spilled) through the others.
         __syncthreads();  // the previous unit is done with LDS
+        if constexpr (F32OP && !DEC) {
+            // backward pass: e^g is 0 in fp32 from kMinLogDecay down, and a smaller g would only cost the
+            // differences of gamma behind it their digits
+            if (p.tmat) {
+#pragma unroll
+                for (int it = 0; it < KdaPrepStage<TIn, DK, DEC>::NP; ++it)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) stage.g[it][e] = fmaxf(stage.g[it][e], kMinLogDecay);
+            }
+        }
         stage.store(sm, opaque(tid));
         __syncthreads();
         // gamma (rows past the chunk's end add 0) and Kh, Qh, Kd, lam to the workspace
@@ -572,6 +584,14 @@ __global__ __launch_bounds__(kKdaPrepThreads) void kda_prepare_kernel(ChunkProbl
                      make_float4(mv[4 * q4], mv[4 * q4 + 1], mv[4 * q4 + 2], mv[4 * q4 + 3]));
                 put4(static_cast<TM*>(p.pmat) + widx * 4096 + o,
                      make_float4(pv[4 * q4], pv[4 * q4 + 1], pv[4 * q4 + 2], pv[4 * q4 + 3]));
+                if constexpr (F32OP && !DEC) {
+                    if (p.tmat) {   // backward pass: T, its upper blocks zero like Mmat's
+                        const bool in = (c0 >> 4) <= (r >> 4);
+                        const float* t4 = &sm.T[r * PF + c0 + 4 * q4];
+                        *reinterpret_cast<float4*>(p.tmat + widx * 4096 + o) =
+                            in ? make_float4(t4[0], t4[1], t4[2], t4[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
             }
         }
         unit = nxt; ok = nok; bos = nbos; len = nlen;
@@ -1051,6 +1071,21 @@ KdaLayout kda_workspace_layout(int B, int T, int H, int dk, int N, int varlen, i
     w.total = w.off_lam + units * dk * 4;
     if (w.nc_bound == 0) w.total = al(varlen ? (size_t)(2 * N + 1) * 4 : 0);
     return w;
+}
+
+template <typename TIn, int DK>
+static hipError_t kda_prepare_f32(const ChunkProblem& p, hipStream_t s) {
+    static std::atomic<int> resident[64];
+    const long units = p.nc_bound * p.H;
+    if (units == 0) return hipSuccess;
+    const auto kern = kda_prepare_kernel<TIn, DK, false, true>;
+    const long cap = resident_blocks(kern, kKdaPrepThreads, resident, 1);
+    return launch(kern, dim3((unsigned)(units < cap ? units : cap)), dim3(kKdaPrepThreads), s, p);
+}
+
+hipError_t launch_kda_prepare_f32(const ChunkProblem& p, hipStream_t s) {
+    if (p.bf16) return p.dk == 64 ? kda_prepare_f32<uint16_t, 64>(p, s) : kda_prepare_f32<uint16_t, 128>(p, s);
+    return p.dk == 64 ? kda_prepare_f32<float, 64>(p, s) : kda_prepare_f32<float, 128>(p, s);
 }
 
 template <typename TIn, typename TO, int DK, int DV>

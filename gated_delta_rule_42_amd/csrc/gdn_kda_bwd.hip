@@ -1,0 +1,708 @@
+// Backward pass of the chunkwise gated delta rule with a channel-wise decay, for gfx950.
+//
+// The forward pass of one chunk (gdn_kda.hip), with gamma the in-chunk inclusive cumulative sum of g per channel:
+//     Kh = K e^gamma,  Qh = Q e^gamma,  Kd = K e^{gamma_last - gamma},  lam = e^{gamma_last}
+//     A = strict_lower(diag(beta) G),  G[r,i] = sum_c k_r k_i e^{gamma_r - gamma_i},   T = (I + A)^{-1},  M = T diag(beta)
+//     P = lower(sum_c q_r k_i e^{gamma_r - gamma_i})
+//     R = V - Kh S^T,   D = M R,   O = Qh S^T + P D,   S' = S Diag(lam) + D^T Kd.
+// Its adjoint, from dO and the gradient dS' that reaches the state behind the chunk:
+//     dD = P^T dO + Kd dS'^T,   Y = T^T dD,   dR = beta Y = dV
+//     dS = dS' Diag(lam) + dO^T Qh - dR^T Kh                           (to the chunk before)
+//     dP = lower(dO D^T),   dA = -strict_lower(Y D^T)
+//     with the decayed in-chunk sums  aq_r = sum_i dP[r,i] k_i e^{gamma_r - gamma_i},
+//         al_r = sum_i dA[r,i] k_i e^{gamma_r - gamma_i},
+//         ar_i = sum_r (dP[r,i] q_r + dA[r,i] beta_r k_r) e^{gamma_r - gamma_i}:
+//     dq = e^gamma (dO S) + aq,   l = al - e^gamma (Y S),   x = e^{gamma_last - gamma} (D dS')
+//     dk = beta l + x + ar,   dbeta_r = Y_r . V_r + k_r . l_r
+//     dgamma = q dq + k (beta l - x - ar),   and into every row of dg: sum_r k x + lam colsum(S dS')
+//     dg = the reverse cumulative sum of dgamma in the chunk + that.
+// (dbeta needs no second look at A: sum_i dA[r,i] G[r,i] = k_r . al_r, and Y_r . R_r = Y_r . V_r - (Y S)_r . Kh_r.)
+//
+// Four kernels: the forward pass's stage 1 with fp32 operators (which also keeps T); a walk over the chunks of each sequence
+// that keeps the state entering each chunk and D; the reverse walk that keeps dS' and Y; and one that takes
+// every chunk by itself. All arithmetic is fp32 for both input types (fp32 matrix core, 16x16x4): dg is a reverse cumulative
+// sum of differences, so rounding any product operand to 16 bits would show in it many times over.
+// No e^{-gamma} is formed: a product over rows of different 16-row blocks is factored through gamma at the block
+// boundary between them (both factors at most 1), and a pair inside a block takes its own decay.
+#include "gdn_device.h"
+#include "gdn_internal.h"
+
+#include <type_traits>
+
+namespace gdn {
+
+// Four consecutive input elements as fp32.
+__device__ __forceinline__ float4 kb_in4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 kb_in4(const uint16_t* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(bf16_lo_half(w.x), bf16_hi_half(w.x), bf16_lo_half(w.y), bf16_hi_half(w.y));
+}
+__device__ __forceinline__ void kb_out4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void kb_out4(uint16_t* p, float4 x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+}
+
+// One element through a buffer resource (per-lane byte offset), as fp32.
+template <typename TIn>
+__device__ __forceinline__ float buf_in(__amdgpu_buffer_rsrc_t r, int off) {
+    if constexpr (sizeof(TIn) == 2) return to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+    else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+template <typename TG>
+__device__ __forceinline__ void buf_out(__amdgpu_buffer_rsrc_t r, int off, float x) {
+    if constexpr (sizeof(TG) == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(x), r, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
+}
+
+// A [64, W] fp32 matrix of the workspace on its way into LDS (row pitch P), 256 threads: 16-byte pieces in
+// registers, loaded a chunk ahead.
+template <int W, int P>
+struct WalkTile {
+    static constexpr int NV = 64 * W / 4 / 256;
+    f32x4_t x[NV];
+    __device__ __forceinline__ void load(const float* src, int tid) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = *reinterpret_cast<const f32x4_t*>(src + 4 * (tid + 256 * i));
+    }
+    __device__ __forceinline__ void store(float* dst, int tid) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = 4 * (tid + 256 * i);
+            *reinterpret_cast<f32x4_t*>(&dst[(e / W) * P + e % W]) = x[i];
+        }
+    }
+};
+
+// ------------------------------------------------------------------- the two walks
+// One work-group of four waves per (sequence, head, 32-column tile of d_v). Wave w has the 16 columns cg = w & 1 and the
+// half hf = w >> 1 of the d_k channels: S^T [dk/2, 16] in accumulator registers. Per chunk each wave forms its half of the
+// products over d_k for all 64 rows, the two halves are added through LDS, the triangular product (M, or T^T) is shared
+// by row tiles ({0, 3} and {1, 2}: five block products each), and each wave updates its own channels. The next
+// chunk's operands are in flight in registers meanwhile.
+template <int DK>
+struct alignas(16) KdaStateSmem {
+    static constexpr int PK = DK + 4, PC = 68;
+    float Kh[64 * PK];
+    float Kd[64 * PK];
+    float M[64 * PC];
+    float lam[DK];
+    f32x4_t ex[4][4][64];    // each wave's partial products, row tile by row tile
+    f32x4_t ex2[2][4][64];   // the triangular product, per column group
+};
+
+struct Chain {   // the chunks of the work-group's (sequence, head)
+    long pair, sbos, seos, cbase, nchunks;
+    int h, tile;
+};
+template <int NTILE>
+__device__ __forceinline__ Chain chain_of(const ChunkProblem& p) {
+    Chain c;
+    const long slot = blockIdx.x / NTILE;
+    c.tile = (int)(blockIdx.x % NTILE);
+    // packed sequences are taken longest first (the chunk table's order)
+    const int n = p.cu_seqlens ? p.chunk_base[p.N + 1 + (int)(slot / p.H)] : (int)(slot / p.H);
+    c.h = (int)(slot % p.H);
+    c.pair = (long)n * p.H + c.h;
+    seq_range(p, n, c.sbos, c.seos);
+    c.cbase = (p.cu_seqlens == nullptr) ? (long)n * p.nc_per_seq : (long)p.chunk_base[n];
+    c.nchunks = (c.seos - c.sbos + 63) / 64;
+    if (c.cbase + c.nchunks > p.nc_bound) c.nchunks = max(0L, p.nc_bound - c.cbase);
+    return c;
+}
+
+// The value rows 16 t + 4 lq + m, column `col`, of a chunk's [len, H, DV] tokens (zeros past the end).
+template <typename TIn, int DV>
+__device__ __forceinline__ void load_cols(f32x4_t (&x)[4], const TIn* base, long bos, int len, int H, int h, int col, int lq) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int r = 16 * t + 4 * lq + m;
+            x[t][m] = r < len ? to_f32(base[((bos + r) * H + h) * DV + col]) : 0.f;
+        }
+}
+
+template <typename TIn, int DK, int DV>
+__global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
+    using SM = KdaStateSmem<DK>;
+    constexpr int PK = SM::PK, PC = SM::PC, HK = DK / 2, NJ = HK / 16;
+    __shared__ SM sm;
+    const ChunkProblem& p = b.f;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, lq = lane >> 4;
+    const int cg = wave & 1, hf = wave >> 1;
+    const Chain c = chain_of<DV / 32>(p);
+    const int H = p.H, col = 32 * c.tile + 16 * cg + l16;
+
+    f32x4_t ST[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        ST[j] = p.h0 ? *reinterpret_cast<const f32x4_t*>(p.h0 + (c.pair * DV + col) * DK + hf * HK + 16 * j + 4 * lq)
+                     : f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    WalkTile<DK, PK> kh, kd;
+    WalkTile<64, PC> mt;
+    f32x4_t v[4];
+    float lam = 0.f;
+    auto fetch = [&](long jc) {
+        const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
+        kh.load(p.khat + widx * 64 * DK, tid);
+        kd.load(p.kdec + widx * 64 * DK, tid);
+        mt.load(static_cast<const float*>(p.mmat) + widx * 4096, tid);
+        if (tid < DK) lam = p.lam[widx * DK + tid];
+        load_cols<TIn, DV>(v, static_cast<const TIn*>(p.v), bos, (int)min(64L, c.seos - bos), H, c.h, col, lq);
+    };
+    if (c.nchunks > 0) fetch(0);
+    for (long jc = 0; jc < c.nchunks; ++jc) {
+        const long widx = (c.cbase + jc) * H + c.h;
+        __syncthreads();   // the previous chunk's operands are dead
+        kh.store(sm.Kh, tid);
+        kd.store(sm.Kd, tid);
+        mt.store(sm.M, tid);
+        if (tid < DK) sm.lam[tid] = lam;
+        f32x4_t X[4], D[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) D[t] = v[t];   // V, until R is formed
+        __syncthreads();
+        if (jc + 1 < c.nchunks) fetch(jc + 1);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            *reinterpret_cast<f32x4_t*>(p.states + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = ST[j];
+        // this half of X = Kh S^T
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const f32x4_t a = *reinterpret_cast<const f32x4_t*>(&sm.Kh[(16 * t + l16) * PK + hf * HK + 16 * j + 4 * lq]);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) X[t] = mfma4(a[s], ST[j][s], X[t]);
+            }
+            sm.ex[wave][t][lane] = X[t];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) X[t] = D[t] - (X[t] + sm.ex[wave ^ 2][t][lane]);   // R
+        // D = M R on the wave's row tiles
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            auto rows = [&](auto tc) {
+                constexpr int t = decltype(tc)::value;
+                f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int t2 = 0; t2 <= t; ++t2) {
+                    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(&sm.M[(16 * t + l16) * PC + 16 * t2 + 4 * lq]);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) d = mfma4(a[s], X[t2][s], d);
+                }
+                sm.ex2[cg][t][lane] = d;
+                float* dst = b.delta + (widx * 64 + 16 * t + 4 * lq) * DV + col;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) dst[m * DV] = d[m];
+            };
+            if (hf == 0) { if (i == 0) rows(std::integral_constant<int, 0>{}); else rows(std::integral_constant<int, 3>{}); }
+            else { if (i == 0) rows(std::integral_constant<int, 1>{}); else rows(std::integral_constant<int, 2>{}); }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) D[t] = sm.ex2[cg][t][lane];
+        // S^T <- Diag(lam) S^T + Kd^T D on the wave's channels
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            f32x4_t acc;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc[m] = ST[j][m] * sm.lam[hf * HK + 16 * j + 4 * lq + m];
+#pragma unroll
+            for (int t2 = 0; t2 < 4; ++t2)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    acc = mfma4(sm.Kd[(16 * t2 + 4 * lq + s) * PK + hf * HK + 16 * j + l16], D[t2][s], acc);
+            ST[j] = acc;
+        }
+    }
+}
+
+template <int DK>
+struct alignas(16) KdaRevSmem {
+    static constexpr int PK = DK + 4, PC = 68;
+    float Kh[64 * PK];
+    float Qh[64 * PK];
+    float Kd[64 * PK];
+    float P[64 * PC];
+    float T[64 * PC];
+    float lam[DK];
+    float beta[64];
+    f32x4_t ex[4][4][64];
+    f32x4_t ex2[2][4][64];
+};
+
+template <typename TIn, int DK, int DV>
+__global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
+    using SM = KdaRevSmem<DK>;
+    constexpr int PK = SM::PK, PC = SM::PC, HK = DK / 2, NJ = HK / 16;
+    __shared__ SM sm;
+    const ChunkProblem& p = b.f;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, lq = lane >> 4;
+    const int cg = wave & 1, hf = wave >> 1;
+    const Chain c = chain_of<DV / 32>(p);
+    const int H = p.H, col = 32 * c.tile + 16 * cg + l16;
+
+    f32x4_t dST[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        dST[j] = b.dhT ? *reinterpret_cast<const f32x4_t*>(b.dhT + (c.pair * DV + col) * DK + hf * HK + 16 * j + 4 * lq)
+                       : f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    WalkTile<DK, PK> kh, qh, kd;
+    WalkTile<64, PC> pt, tt;
+    f32x4_t dof[4];
+    float lam = 0.f, beta = 0.f;
+    auto fetch = [&](long jc) {
+        const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
+        const int len = (int)min(64L, c.seos - bos);
+        kh.load(p.khat + widx * 64 * DK, tid);
+        qh.load(p.qhat + widx * 64 * DK, tid);
+        kd.load(p.kdec + widx * 64 * DK, tid);
+        pt.load(static_cast<const float*>(p.pmat) + widx * 4096, tid);
+        tt.load(p.tmat + widx * 4096, tid);
+        if (tid < DK) lam = p.lam[widx * DK + tid];
+        if (tid < 64) beta = tid < len ? p.beta[(bos + tid) * H + c.h] : 0.f;
+        load_cols<TIn, DV>(dof, static_cast<const TIn*>(b.d_o), bos, len, H, c.h, col, lq);
+    };
+    if (c.nchunks > 0) fetch(c.nchunks - 1);
+    for (long jc = c.nchunks - 1; jc >= 0; --jc) {
+        const long widx = (c.cbase + jc) * H + c.h;
+        __syncthreads();   // the previous chunk's operands are dead
+        kh.store(sm.Kh, tid);
+        qh.store(sm.Qh, tid);
+        kd.store(sm.Kd, tid);
+        pt.store(sm.P, tid);
+        tt.store(sm.T, tid);
+        if (tid < DK) sm.lam[tid] = lam;
+        if (tid < 64) sm.beta[tid] = beta;
+        f32x4_t dO[4], X[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) dO[t] = dof[t];
+        __syncthreads();
+        if (jc > 0) fetch(jc - 1);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            *reinterpret_cast<f32x4_t*>(b.dstates + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = dST[j];
+        // this wave's share of dD = Kd dS'^T + P^T dO: its half of the channels, and of P's rows (tiles {0, 3}, {1, 2})
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const f32x4_t a = *reinterpret_cast<const f32x4_t*>(&sm.Kd[(16 * t + l16) * PK + hf * HK + 16 * j + 4 * lq]);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) X[t] = mfma4(a[s], dST[j][s], X[t]);
+            }
+        }
+        auto prow = [&](auto tc) {
+            constexpr int t2 = decltype(tc)::value;
+#pragma unroll
+            for (int t = 0; t <= t2; ++t)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) X[t] = mfma4(sm.P[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16], dO[t2][s], X[t]);
+        };
+        if (hf == 0) { prow(std::integral_constant<int, 0>{}); prow(std::integral_constant<int, 3>{}); }
+        else { prow(std::integral_constant<int, 1>{}); prow(std::integral_constant<int, 2>{}); }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) sm.ex[wave][t][lane] = X[t];
+        // dS'^T Diag(lam) + Qh^T dO on the wave's channels
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) dST[j][m] *= sm.lam[hf * HK + 16 * j + 4 * lq + m];
+#pragma unroll
+            for (int t2 = 0; t2 < 4; ++t2)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    dST[j] = mfma4(sm.Qh[(16 * t2 + 4 * lq + s) * PK + hf * HK + 16 * j + l16], dO[t2][s], dST[j]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) X[t] += sm.ex[wave ^ 2][t][lane];   // dD
+        // Y = T^T dD on the wave's row tiles
+        auto yrow = [&](auto tc) {
+            constexpr int t = decltype(tc)::value;
+            f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t2 = t; t2 < 4; ++t2)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) y = mfma4(sm.T[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16], X[t2][s], y);
+            sm.ex2[cg][t][lane] = y;
+            float* dst = b.ymat + (widx * 64 + 16 * t + 4 * lq) * DV + col;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) dst[m * DV] = y[m];
+        };
+        if (hf == 0) { yrow(std::integral_constant<int, 0>{}); yrow(std::integral_constant<int, 3>{}); }
+        else { yrow(std::integral_constant<int, 1>{}); yrow(std::integral_constant<int, 2>{}); }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {   // -dR
+            X[t] = sm.ex2[cg][t][lane];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) X[t][m] *= -sm.beta[16 * t + 4 * lq + m];
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int t2 = 0; t2 < 4; ++t2)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    dST[j] = mfma4(sm.Kh[(16 * t2 + 4 * lq + s) * PK + hf * HK + 16 * j + l16], X[t2][s], dST[j]);
+    }
+    if (b.dh0) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            *reinterpret_cast<f32x4_t*>(b.dh0 + (c.pair * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = dST[j];
+    }
+}
+
+// ------------------------------------------------------------------- gradients of each chunk
+// One work-group per (chunk, head), a wave per 16 channels (c0 = 16 wave). Two register layouts of a wave's
+// [64 rows, 16 channels]: the accumulator layout (rows 16 t + 4 lq + m) of the products, and the block layout (lane
+// (lq, l16) has rows 16 lq .. 16 lq + 15 of channel c0 + l16), in which gamma is scanned, the pairs inside a block are
+// summed and the gradients are formed. An accumulator goes to the block layout through a private LDS tile.
+template <int DV, int NW>
+struct alignas(16) KdaGradSmem {
+    static constexpr int PV = DV + 4, PC = 68, PT = 17;
+    union {
+        struct { float D[64 * PV], Y[64 * PV], dO[64 * PV]; } in;
+        float turn[NW][64 * PT];
+    };
+    float dP[64 * PC];
+    float dA[64 * PC];
+    float beta[64];
+    float yv[64];
+    float part[NW][64];
+};
+
+// Keeps the compiler from moving memory accesses across: without it, it reads the operands of whole unrolled sections
+// ahead and spills what it read.
+__device__ __forceinline__ void pin() { asm volatile("" ::: "memory"); }
+
+// Makes the compiler have x in a register at this point of the program.
+__device__ __forceinline__ void hold(float& x) { asm volatile("" : "+v"(x)); }
+
+// Orders a wave's own LDS writes before its reads of what other lanes wrote.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <typename TIn, typename TG, int DK, int DV>
+__global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
+    constexpr int NW = DK / 16, NT = 64 * NW;
+    using SM = KdaGradSmem<DV, NW>;
+    constexpr int PV = SM::PV, PC = SM::PC, PT = SM::PT, NU = DV / 16;
+    __shared__ SM sm;
+    const ChunkProblem& p = b.f;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, lq = lane >> 4;
+    const int H = p.H, ch = 16 * wave + l16;
+    const long unit = blockIdx.x;
+    long bos;
+    int len;
+    if (!locate_chunk(p, unit / H, bos, len)) return;   // packed: past the last chunk
+    const int h = (int)(unit % H);
+    {
+        // q, k, g of the lane's rows and channel, through resources that end at the chunk's last token
+        float k[16], q[16], gm[16];
+        const long base = (bos * H + h) * DK;
+        {
+            constexpr int EB = (int)sizeof(TIn);
+            const unsigned rows = (unsigned)((len - 1) * H * DK + DK);
+            const auto kr = make_rsrc(static_cast<const TIn*>(p.k) + base, rows * EB);
+            const auto qr = make_rsrc(static_cast<const TIn*>(p.q) + base, rows * EB);
+            const auto gr = make_rsrc(p.g + base, rows * 4);
+            const int o0 = 16 * lq * H * DK + ch;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int o = o0 + r * H * DK;
+                k[r] = buf_in<TIn>(kr, o * EB);
+                q[r] = buf_in<TIn>(qr, o * EB);
+                gm[r] = fmaxf(buf_in<float>(gr, o * 4), kMinLogDecay);
+            }
+        }
+        // D, Y and dO into LDS; dV = beta Y and Y . V on the way (a row's DV / 4 threads are consecutive lanes)
+        if (tid < 64) sm.beta[tid] = tid < len ? p.beta[(bos + tid) * H + h] : 0.f;
+        for (int i = tid; i < 64 * DV / 4; i += NT) {
+            const int r = i / (DV / 4), cc = 4 * (i % (DV / 4));
+            const float4 d = *reinterpret_cast<const float4*>(b.delta + (unit * 64 + r) * DV + cc);
+            const float4 y = *reinterpret_cast<const float4*>(b.ymat + (unit * 64 + r) * DV + cc);
+            float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+            float yv = 0.f;
+            if (r < len) {
+                const long o = ((bos + r) * H + h) * DV + cc;
+                const float bt = p.beta[(bos + r) * H + h];
+                g = kb_in4(static_cast<const TIn*>(b.d_o) + o);
+                const float4 v = kb_in4(static_cast<const TIn*>(p.v) + o);
+                yv = y.x * v.x + y.y * v.y + y.z * v.z + y.w * v.w;
+                kb_out4(static_cast<TG*>(b.dv) + o, make_float4(bt * y.x, bt * y.y, bt * y.z, bt * y.w));
+            }
+            *reinterpret_cast<float4*>(&sm.in.D[r * PV + cc]) = d;
+            *reinterpret_cast<float4*>(&sm.in.Y[r * PV + cc]) = y;
+            *reinterpret_cast<float4*>(&sm.in.dO[r * PV + cc]) = g;
+            yv = row16_sum(yv);
+            if constexpr (DV == 128) yv += __shfl_xor(yv, 16, 64);
+            if (cc == 0) sm.yv[r] = yv;
+        }
+        __syncthreads();
+
+        // dP and dA tile by tile (the ten lower tiles of each; zeros above)
+        for (int job = wave; job < 32; job += NW) {
+            const int I = job >> 3, J = (job >> 1) & 3;
+            const float* L = (job & 1) ? sm.in.Y : sm.in.dO;
+            float* out = (job & 1) ? sm.dA : sm.dP;
+            f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+            if (J <= I) {
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&L[(16 * I + l16) * PV + 16 * u + 4 * lq]);
+                    const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&sm.in.D[(16 * J + l16) * PV + 16 * u + 4 * lq]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc = mfma4(x[e], y[e], acc);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int r = 16 * I + 4 * lq + m, i = 16 * J + l16;
+                out[r * PC + i] = (job & 1) ? (i < r ? -acc[m] : 0.f) : (i <= r ? acc[m] : 0.f);
+            }
+        }
+        // dO S, Y S and D dS' on the wave's channels; colsum(S dS')
+        f32x4_t aq[4], ay[4], ad[4];
+        float sds = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) aq[t] = ay[t] = ad[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        {
+            const float* sp = p.states + unit * DV * DK + ch;
+            const float* dp = b.dstates + unit * DV * DK + ch;
+#pragma unroll 2
+            for (int u = 0; u < NU; ++u) {
+                float s[4], d[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[e] = sp[(16 * u + 4 * lq + e) * DK];
+                    d[e] = dp[(16 * u + 4 * lq + e) * DK];
+                    sds += s[e] * d[e];
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int a = (16 * t + l16) * PV + 16 * u + 4 * lq;
+                    const f32x4_t o = *reinterpret_cast<const f32x4_t*>(&sm.in.dO[a]);
+                    const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&sm.in.Y[a]);
+                    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sm.in.D[a]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        aq[t] = mfma4(o[e], s[e], aq[t]);
+                        ay[t] = mfma4(y[e], s[e], ay[t]);
+                        ad[t] = mfma4(x[e], d[e], ad[t]);
+                    }
+                }
+            }
+            sds += __shfl_xor(sds, 16, 64);
+            sds += __shfl_xor(sds, 32, 64);
+        }
+        __syncthreads();   // dP and dA are whole; D, Y, dO are dead
+
+        // gamma of the lane's rows; a[r] = e^{g_r}, the decay from the row above
+        float a[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            a[r] = __expf(gm[r]);
+            if (r > 0) gm[r] += gm[r - 1];
+        }
+        {
+            const float t0 = __shfl(gm[15], l16, 64), t1 = __shfl(gm[15], 16 + l16, 64), t2 = __shfl(gm[15], 32 + l16, 64);
+            const float pre = (lq > 0 ? t0 : 0.f) + (lq > 1 ? t1 : 0.f) + (lq > 2 ? t2 : 0.f);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) gm[r] += pre;
+        }
+        float end[4];   // gamma at the last row of each block
+#pragma unroll
+        for (int B = 0; B < 4; ++B) end[B] = __shfl(gm[15], 16 * B + l16, 64);
+
+        float* turn = sm.turn[wave];
+        auto to_block = [&](const f32x4_t (&x)[4], float (&y)[16]) {
+            wave_lds_fence();
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) turn[(16 * t + 4 * lq + m) * PT + l16] = x[t][m];
+            wave_lds_fence();
+#pragma unroll
+            for (int r = 0; r < 16; ++r) y[r] = turn[(16 * lq + r) * PT + l16];
+        };
+        const float ref = lq == 0 ? 0.f : lq == 1 ? end[0] : lq == 2 ? end[1] : end[2];   // gamma before the lane's block
+        const float own = gm[15];
+        float dq[16], l[16], x[16], ar[16], w[16];
+        to_block(aq, w);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dq[r] = __expf(gm[r]) * w[r];
+        to_block(ay, w);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) l[r] = -__expf(gm[r]) * w[r];
+        to_block(ad, w);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = __expf(end[3] - gm[r]) * w[r];
+
+        // pairs of different blocks. Rows of block I against all rows before it, through gamma at the row before
+        // block I: step s takes row s of every block (lane lq its own), blocks I and later as zeros.
+#pragma unroll
+        for (int t = 0; t < 4; ++t) aq[t] = ay[t] = ad[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int I = 1; I < 4; ++I)
+#pragma unroll
+            for (int s4 = 0; s4 < 4; ++s4) {
+                pin();
+                const int o = (16 * I + l16) * PC + 16 * lq + 4 * s4;
+                const f32x4_t vp = *reinterpret_cast<const f32x4_t*>(&sm.dP[o]);
+                const f32x4_t va = *reinterpret_cast<const f32x4_t*>(&sm.dA[o]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int s = 4 * s4 + e;
+                    const float kb = lq < I ? k[s] * __expf(end[I - 1] - gm[s]) : 0.f;
+                    aq[I] = mfma4(vp[e], kb, aq[I]);
+                    ay[I] = mfma4(va[e], kb, ay[I]);
+                }
+            }
+        // Columns of block J against all rows behind it, through gamma at the block's last row.
+#pragma unroll
+        for (int J = 0; J < 3; ++J)
+#pragma unroll
+            for (int s = 0; s < 16; ++s) {
+                if (s % 4 == 0) pin();
+                const int o = (16 * lq + s) * PC + 16 * J + l16;
+                const float e = lq > J ? __expf(gm[s] - end[J]) : 0.f;
+                ad[J] = mfma4(sm.dP[o], q[s] * e, ad[J]);
+                ad[J] = mfma4(sm.dA[o], sm.beta[16 * lq + s] * k[s] * e, ad[J]);
+            }
+        to_block(aq, w);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dq[r] += __expf(gm[r] - ref) * w[r];
+        to_block(ay, w);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) l[r] += __expf(gm[r] - ref) * w[r];
+        to_block(ad, w);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) ar[r] = __expf(own - gm[r]) * w[r];
+
+        // pairs inside the lane's block: w[i] holds e^{gamma_r - gamma_i}, decayed row by row
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            pin();
+            const float* pr = &sm.dP[(16 * lq + r) * PC + 16 * lq];
+            const float* pa = &sm.dA[(16 * lq + r) * PC + 16 * lq];
+            const float bk = sm.beta[16 * lq + r] * k[r];
+            w[r] = 1.f;
+#pragma unroll
+            for (int i4 = 0; i4 <= r / 4; ++i4) {
+                const f32x4_t vp = *reinterpret_cast<const f32x4_t*>(pr + 4 * i4);
+                const f32x4_t va = *reinterpret_cast<const f32x4_t*>(pa + 4 * i4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * i4 + e;
+                    if (i > r) continue;
+                    if (i < r) w[i] *= a[r];
+                    const float ke = w[i] * k[i];
+                    dq[r] += vp[e] * ke;
+                    if (i < r) l[r] += va[e] * ke;
+                    ar[i] += (i < r ? vp[e] * q[r] + va[e] * bk : vp[e] * q[r]) * w[i];
+                }
+            }
+            // the row's sums are formed here, not at their use at the end
+            hold(dq[r]);
+            hold(l[r]);
+#pragma unroll
+            for (int i = 0; i <= r; ++i) hold(ar[i]);
+        }
+        // gradients
+        float kx = 0.f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float bl = sm.beta[16 * lq + r] * l[r];
+            kx += k[r] * x[r];
+            w[r] = q[r] * dq[r] + k[r] * (bl - x[r] - ar[r]);
+            const float db = row16_sum(k[r] * l[r]);
+            if (l16 == 0) sm.part[wave][16 * lq + r] = db;
+            l[r] = bl + x[r] + ar[r];   // dk
+        }
+        kx += __shfl_xor(kx, 16, 64);
+        kx += __shfl_xor(kx, 32, 64);
+        kx += __expf(end[3]) * sds;
+#pragma unroll
+        for (int r = 14; r >= 0; --r) w[r] += w[r + 1];
+        const float b1 = __shfl(w[0], 16 + l16, 64), b2 = __shfl(w[0], 32 + l16, 64), b3 = __shfl(w[0], 48 + l16, 64);
+        const float tail = kx + (lq < 3 ? b3 : 0.f) + (lq < 2 ? b2 : 0.f) + (lq < 1 ? b1 : 0.f);
+        {
+            constexpr int EB = (int)sizeof(TG);
+            const unsigned rows = (unsigned)((len - 1) * H * DK + DK);
+            const auto qr = make_rsrc(static_cast<TG*>(b.dq) + base, rows * EB);
+            const auto kr = make_rsrc(static_cast<TG*>(b.dk) + base, rows * EB);
+            const auto gr = make_rsrc(b.dg + base, rows * 4);
+            const int o0 = 16 * lq * H * DK + ch;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int o = o0 + r * H * DK;
+                buf_out<TG>(qr, o * EB, dq[r]);
+                buf_out<TG>(kr, o * EB, l[r]);
+                buf_out<float>(gr, o * 4, w[r] + tail);
+            }
+        }
+        __syncthreads();
+        if (tid < len) {
+            float s = sm.yv[tid];
+#pragma unroll
+            for (int i = 0; i < NW; ++i) s += sm.part[i][tid];
+            b.dbeta[(bos + tid) * H + h] = s;
+        }
+    }
+}
+
+// -------------------------------------------------------------------- launchers
+KdaBwdLayout kda_bwd_workspace_layout(int B, int T, int H, int dk, int dv, int N, int varlen) {
+    auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    KdaBwdLayout w{};
+    w.fwd = kda_workspace_layout(B, T, H, dk, N, varlen, 4);
+    const size_t units = (size_t)w.fwd.nc_bound * H;
+    w.off_t = al(w.fwd.total);
+    w.off_states = al(w.off_t + units * 4096 * 4);
+    w.off_dstates = al(w.off_states + units * dv * dk * 4);
+    w.off_delta = al(w.off_dstates + units * dv * dk * 4);
+    w.off_y = al(w.off_delta + units * 64 * dv * 4);
+    w.total = units ? w.off_y + units * 64 * dv * 4 : w.fwd.total;
+    return w;
+}
+
+template <typename TIn, int DK, int DV>
+static hipError_t kda_bwd_launch(const KdaBwdProblem& b, hipStream_t s) {
+    const ChunkProblem& p = b.f;
+    const long pairs = (long)p.N * p.H, units = p.nc_bound * p.H;
+    if (pairs == 0) return hipSuccess;
+    const dim3 walks((unsigned)(pairs * (DV / 32)));
+    hipError_t e = launch(kda_bwd_states_kernel<TIn, DK, DV>, walks, dim3(256), s, b);
+    if (e == hipSuccess) e = launch(kda_bwd_reverse_kernel<TIn, DK, DV>, walks, dim3(256), s, b);
+    if (e != hipSuccess || units == 0) return e;
+    const dim3 grid((unsigned)units);
+    return b.grad_bf16 ? launch(kda_bwd_grad_kernel<TIn, uint16_t, DK, DV>, grid, dim3(DK * 4), s, b)
+                       : launch(kda_bwd_grad_kernel<TIn, float, DK, DV>, grid, dim3(DK * 4), s, b);
+}
+
+template <typename TIn>
+static hipError_t kda_bwd_dispatch(const KdaBwdProblem& b, hipStream_t s) {
+    if (b.f.dk == 64)
+        return b.f.dv == 64 ? kda_bwd_launch<TIn, 64, 64>(b, s) : kda_bwd_launch<TIn, 64, 128>(b, s);
+    return b.f.dv == 64 ? kda_bwd_launch<TIn, 128, 64>(b, s) : kda_bwd_launch<TIn, 128, 128>(b, s);
+}
+
+hipError_t launch_kda_chunk_bwd(const KdaBwdProblem& b, hipStream_t s) {
+    hipError_t e = launch_chunk_base(b.f, s);
+    if (e == hipSuccess) e = launch_kda_prepare_f32(b.f, s);
+    if (e != hipSuccess) return e;
+    return b.f.bf16 ? kda_bwd_dispatch<uint16_t>(b, s) : kda_bwd_dispatch<float>(b, s);
+}
+
+}  // namespace gdn

@@ -330,6 +330,26 @@ int gdn_kda_chunk_fwd(const void *q, const void *k, const void *v, const float *
                       void *stream);
 
 /*
+ * Backward pass of gdn_kda_chunk_fwd: arguments as in gdn_chunk_bwd except
+ *   g_log_alpha, dg [B, T, H, dk] fp32 (16-byte aligned)
+ *   workspace   at least gdn_kda_chunk_bwd_workspace_bytes(...) bytes: the regions of
+ *               gdn_kda_chunk_fwd_workspace_bytes for fp32 inputs, then fp32 T [nc, H, 64, 64], the
+ *               states entering each chunk [nc, H, dv, dk], the gradients reaching the state behind
+ *               each chunk (same), Delta [nc, H, 64, dv] and T^T dDelta (same)
+ * and N * H < 2^21. All arithmetic is fp32 for both input types (products on the fp32 matrix core);
+ * bf16 gradients are the fp32 results rounded to nearest even. dg and dbeta of a token depend on its own
+ * sequence only; rows of the outputs that no sequence covers are not written.
+ */
+size_t gdn_kda_chunk_bwd_workspace_bytes(int B, int T, int H, int dk, int dv, int N, int varlen,
+                                         int chunk, int dtype);
+int gdn_kda_chunk_bwd(const void *q, const void *k, const void *v, const float *g_log_alpha,
+                      const float *beta, const float *h0, const void *d_o, const float *dhT,
+                      void *dq, void *dk_out, void *dv_out, float *dg, float *dbeta, float *dh0,
+                      const int32_t *cu_seqlens, int chunk, int B, int T, int H, int dk, int dv,
+                      int N, int dtype, int grad_dtype, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
  * One decode step of the channel-wise-decay operator, arguments as in gdn_decode_step except
  * g_log_alpha [N, H, dk] fp32 (16-byte aligned). Per state row s_i: s~ = s_i * alpha,
  * c_i = beta (v_i - s~ . k), s_i <- s~ + c_i k, o_i = s~ . q + c_i (k . q).
