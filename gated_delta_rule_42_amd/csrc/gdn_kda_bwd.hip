@@ -110,17 +110,26 @@ __device__ __forceinline__ Chain chain_of(const ChunkProblem& p) {
     return c;
 }
 
-// The value rows 16 t + 4 lq + m, column `col`, of a chunk's [len, H, DV] tokens (zeros past the end).
+// The rows 16 t + 4 lq + m of column `col` of a chunk's [len, H, DV] tokens, as loaded (zeros past the end): converted
+// where they are used, since a conversion at the load would wait for it.
 template <typename TIn, int DV>
-__device__ __forceinline__ void load_cols(f32x4_t (&x)[4], const TIn* base, long bos, int len, int H, int h, int col, int lq) {
+struct TokenCols {
+    uint32_t x[4][4];
+    __device__ __forceinline__ void load(const void* src, long bos, int len, int H, int h, int col, int lq) {
+        constexpr int EB = (int)sizeof(TIn);
+        const auto rs = make_rsrc(static_cast<const TIn*>(src) + (bos * H + h) * DV, (unsigned)((len - 1) * H * DV + DV) * EB);
+        const int o0 = (4 * lq * H * DV + col) * EB;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int r = 16 * t + 4 * lq + m;
-            x[t][m] = r < len ? to_f32(base[((bos + r) * H + h) * DV + col]) : 0.f;
-        }
-}
+            for (int m = 0; m < 4; ++m) {
+                const int o = o0 + (16 * t + m) * H * DV * EB;
+                if constexpr (EB == 2) x[t][m] = __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0);
+                else x[t][m] = __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
+            }
+    }
+    __device__ __forceinline__ float at(int t, int m) const { return __uint_as_float(sizeof(TIn) == 2 ? x[t][m] << 16 : x[t][m]); }
+};
 
 template <typename TIn, int DK, int DV>
 __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
@@ -141,7 +150,7 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
 
     WalkTile<DK, PK> kh, kd;
     WalkTile<64, PC> mt;
-    f32x4_t v[4];
+    TokenCols<TIn, DV> v;
     float lam = 0.f;
     auto fetch = [&](long jc) {
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
@@ -149,7 +158,7 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
         kd.load(p.kdec + widx * 64 * DK, tid);
         mt.load(static_cast<const float*>(p.mmat) + widx * 4096, tid);
         if (tid < DK) lam = p.lam[widx * DK + tid];
-        load_cols<TIn, DV>(v, static_cast<const TIn*>(p.v), bos, (int)min(64L, c.seos - bos), H, c.h, col, lq);
+        v.load(p.v, bos, (int)min(64L, c.seos - bos), H, c.h, col, lq);
     };
     if (c.nchunks > 0) fetch(0);
     for (long jc = 0; jc < c.nchunks; ++jc) {
@@ -161,7 +170,7 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
         if (tid < DK) sm.lam[tid] = lam;
         f32x4_t X[4], D[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) D[t] = v[t];   // V, until R is formed
+        for (int t = 0; t < 4; ++t) D[t] = f32x4_t{v.at(t, 0), v.at(t, 1), v.at(t, 2), v.at(t, 3)};   // V, until R is formed
         __syncthreads();
         if (jc + 1 < c.nchunks) fetch(jc + 1);
 #pragma unroll
@@ -254,7 +263,7 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
 
     WalkTile<DK, PK> kh, qh, kd;
     WalkTile<64, PC> pt, tt;
-    f32x4_t dof[4];
+    TokenCols<TIn, DV> dof;
     float lam = 0.f, beta = 0.f;
     auto fetch = [&](long jc) {
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
@@ -266,7 +275,7 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
         tt.load(p.tmat + widx * 4096, tid);
         if (tid < DK) lam = p.lam[widx * DK + tid];
         if (tid < 64) beta = tid < len ? p.beta[(bos + tid) * H + c.h] : 0.f;
-        load_cols<TIn, DV>(dof, static_cast<const TIn*>(b.d_o), bos, len, H, c.h, col, lq);
+        dof.load(b.d_o, bos, len, H, c.h, col, lq);
     };
     if (c.nchunks > 0) fetch(c.nchunks - 1);
     for (long jc = c.nchunks - 1; jc >= 0; --jc) {
@@ -281,7 +290,7 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
         if (tid < 64) sm.beta[tid] = beta;
         f32x4_t dO[4], X[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) dO[t] = dof[t];
+        for (int t = 0; t < 4; ++t) dO[t] = f32x4_t{dof.at(t, 0), dof.at(t, 1), dof.at(t, 2), dof.at(t, 3)};
         __syncthreads();
         if (jc > 0) fetch(jc - 1);
 #pragma unroll
