@@ -54,31 +54,171 @@ __device__ __forceinline__ void buf_out(__amdgpu_buffer_rsrc_t r, int off, float
     else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
 }
 
-// A [64, W] fp32 matrix of the workspace on its way into LDS (row pitch P), 256 threads: 16-byte pieces in
-// registers, loaded a chunk ahead.
+// A [64, W] fp32 matrix of the workspace on its way into LDS (row pitch P), 256 threads: NV 16-byte pieces per thread,
+// held in registers between load and store.
 template <int W, int P>
 struct WalkTile {
     static constexpr int NV = 64 * W / 4 / 256;
     f32x4_t x[NV];
-    __device__ __forceinline__ void load(const float* src, int tid) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) x[i] = *reinterpret_cast<const f32x4_t*>(src + 4 * (tid + 256 * i));
+    __device__ __forceinline__ void load(const float* src, int i, int tid) {
+        x[i] = *reinterpret_cast<const f32x4_t*>(src + 4 * (tid + 256 * i));
     }
-    __device__ __forceinline__ void store(float* dst, int tid) const {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = 4 * (tid + 256 * i);
-            *reinterpret_cast<f32x4_t*>(&dst[(e / W) * P + e % W]) = x[i];
+    __device__ __forceinline__ void store(float* dst, int i, int tid) const {
+        const int e = 4 * (tid + 256 * i);
+        *reinterpret_cast<f32x4_t*>(&dst[(e / W) * P + e % W]) = x[i];
+    }
+};
+
+// A wave's 16 columns of a chunk's [len, H, DV] tokens: 16-byte pieces in registers as loaded (zeros past the end), then
+// through 4 KB of LDS of the wave's own into the layout of a right operand (lane (lq, l16): rows 16 t + 4 lq + m of
+// column l16, stored in that order, so that the reads are free of bank conflicts).
+template <typename TIn, int DV>
+struct TokenCols {
+    static constexpr int EB = (int)sizeof(TIn), PR = 16 * EB / 16, NV = 64 * PR / 64;   // pieces a row, pieces a lane
+    u32x4_t x[NV];
+    __device__ __forceinline__ void load(const void* src, long bos, int len, int H, int h, int col0, int i, int lane) {
+        const auto rs = make_rsrc(static_cast<const TIn*>(src) + (bos * H + h) * DV, (unsigned)((len - 1) * H * DV + DV) * EB);
+        const int n = lane + 64 * i, r = n / PR, c = n % PR;
+        x[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, (r * H * DV + col0) * EB + 16 * c, 0, 0);
+    }
+    __device__ __forceinline__ void store(float* own, int i, int lane) const {
+        const int n = lane + 64 * i, r = n / PR, c = n % PR;
+        float* dst = own + ((r >> 4) * 4 + (r & 3)) * 64 + ((r >> 2) & 3) * 16 + c * (16 / EB);
+        if constexpr (EB == 2) {
+            *reinterpret_cast<f32x4_t*>(dst) = f32x4_t{bf16_lo_half(x[i][0]), bf16_hi_half(x[i][0]), bf16_lo_half(x[i][1]), bf16_hi_half(x[i][1])};
+            *reinterpret_cast<f32x4_t*>(dst + 4) = f32x4_t{bf16_lo_half(x[i][2]), bf16_hi_half(x[i][2]), bf16_lo_half(x[i][3]), bf16_hi_half(x[i][3])};
+        } else {
+            *reinterpret_cast<u32x4_t*>(dst) = x[i];
         }
     }
+    static __device__ __forceinline__ void get(const float* own, f32x4_t (&v)[4], int lane) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) v[t][m] = own[(4 * t + m) * 64 + lane];
+    }
+};
+
+// Keeps the compiler from moving memory accesses across: without it, it reads the operands of whole unrolled sections
+// ahead and spills what it read.
+__device__ __forceinline__ void pin() { asm volatile("" ::: "memory"); }
+
+// Makes the compiler have x in a register at this point of the program.
+__device__ __forceinline__ void hold(float& x) { asm volatile("" : "+v"(x)); }
+
+// Operands of the walks, read from LDS ahead of their products (a wave has a SIMD to itself there, so a read that is waited
+// for right before its product costs its whole latency). Rows: 16-byte pieces of row 16 t + l16 of a [64, P] matrix, tile t
+// (and block j) each; cols: column c + l16 of the rows 16 t2 + 4 lq + s.
+template <int NJ>
+struct RowFrags {
+    f32x4_t a[4][NJ];
+    __device__ __forceinline__ void read(const float* m, int pitch, int c0, int l16, int lq) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[t][j] = *reinterpret_cast<const f32x4_t*>(&m[(16 * t + l16) * pitch + c0 + 16 * j + 4 * lq]);
+        pin();
+    }
+    // acc[t] += rows of tile t times b
+    __device__ __forceinline__ void mul(f32x4_t (&acc)[4], const f32x4_t (&b)[NJ]) const {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) acc[t] = mfma4(a[t][j][s], b[j][s], acc[t]);
+    }
+};
+template <int NJ>
+struct ColFrags {
+    f32x4_t a[4][NJ];
+    __device__ __forceinline__ void read(const float* m, int pitch, int c0, int l16, int lq) {
+#pragma unroll
+        for (int t2 = 0; t2 < 4; ++t2)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) a[t2][j][s] = m[(16 * t2 + 4 * lq + s) * pitch + c0 + 16 * j + l16];
+        pin();
+    }
+    // acc[j] += columns of block j times b, with step(0) .. step(15) in between: the memory instructions of the chunks to
+    // come, which the matrix core hides there
+    template <typename F>
+    __device__ __forceinline__ void mul(f32x4_t (&acc)[NJ], const f32x4_t (&b)[4], F step) const {
+#pragma unroll
+        for (int t2 = 0; t2 < 4; ++t2)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[j] = mfma4(a[t2][j][s], b[t2][s], acc[j]);
+                __builtin_amdgcn_sched_barrier(0);
+                step(4 * t2 + s);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+};
+// The wave's share of a product with a lower triangular [64, 64] matrix m (TRANS: with m^T): row tiles 0 and 3 for
+// hf = 0, 1 and 2 for hf = 1, five block products either way. d0, d1: the lower and the higher row tile.
+template <bool TRANS, int PC>
+struct TriFrags {
+    f32x4_t a[5];
+    // block of (row tile, contraction tile) number i: (0,0) (3,0) (3,1) (3,2) (3,3) or (1,0) (1,1) (2,0) (2,1) (2,2);
+    // transposed: (3,3) (0,0) (0,1) (0,2) (0,3) or (2,2) (2,3) (1,1) (1,2) (1,3)
+    template <int HF>
+    static constexpr int row(int i) {
+        return TRANS ? (HF == 0 ? (i == 0 ? 3 : 0) : (i < 2 ? 2 : 1)) : (HF == 0 ? (i == 0 ? 0 : 3) : (i < 2 ? 1 : 2));
+    }
+    template <int HF>
+    static constexpr int con(int i) {
+        return TRANS ? (HF == 0 ? (i == 0 ? 3 : i - 1) : (i < 2 ? 2 + i : i - 1)) : (HF == 0 ? (i == 0 ? 0 : i - 1) : (i < 2 ? i : i - 2));
+    }
+    template <int HF>
+    __device__ __forceinline__ void read_of(const float* m, int l16, int lq) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            const int t = row<HF>(i), t2 = con<HF>(i);
+            if constexpr (TRANS) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) a[i][s] = m[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16];
+            } else {
+                a[i] = *reinterpret_cast<const f32x4_t*>(&m[(16 * t + l16) * PC + 16 * t2 + 4 * lq]);
+            }
+        }
+        pin();
+    }
+    __device__ __forceinline__ void read(const float* m, int hf, int l16, int lq) {
+        if (hf == 0) read_of<0>(m, l16, lq);
+        else read_of<1>(m, l16, lq);
+    }
+    // The two row tiles of the product with x, each block's product on its own accumulator
+    template <int HF>
+    __device__ __forceinline__ void mul_of(const f32x4_t (&x)[4], f32x4_t& first, f32x4_t& second) const {
+        f32x4_t d[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) d[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 5; ++i) d[i] = mfma4(a[i][s], x[con<HF>(i)][s], d[i]);
+        if constexpr (HF == 0) first = d[0], second = (d[1] + d[2]) + (d[3] + d[4]);
+        else first = d[0] + d[1], second = (d[2] + d[3]) + d[4];
+    }
+    __device__ __forceinline__ void mul(const f32x4_t (&x)[4], int hf, f32x4_t& first, f32x4_t& second) const {
+        if (hf == 0) mul_of<0>(x, first, second);
+        else mul_of<1>(x, first, second);
+    }
+    static __device__ __forceinline__ int first_tile(int hf) { return TRANS ? (hf == 0 ? 3 : 2) : (hf == 0 ? 0 : 1); }
+    static __device__ __forceinline__ int second_tile(int hf) { return TRANS ? (hf == 0 ? 0 : 1) : (hf == 0 ? 3 : 2); }
 };
 
 // ------------------------------------------------------------------- the two walks
 // One work-group of four waves per (sequence, head, 32-column tile of d_v). Wave w has the 16 columns cg = w & 1 and the
 // half hf = w >> 1 of the d_k channels: S^T [dk/2, 16] in accumulator registers. Per chunk each wave forms its half of the
 // products over d_k for all 64 rows, the two halves are added through LDS, the triangular product (M, or T^T) is shared
-// by row tiles ({0, 3} and {1, 2}: five block products each), and each wave updates its own channels. The next
-// chunk's operands are in flight in registers meanwhile.
+// by row tiles ({0, 3} and {1, 2}: five block products each), and each wave updates its own channels. Every operand has
+// been read from LDS into registers by the first of the two exchanges, so the next chunk's are written over them, and the
+// loads of the chunk after it issued, between the products of the state update (a probe of an earlier form, which issued the
+// loads in one go, showed 3,000 of a chunk's 13,500 cycles in their issue and 1,200 in the LDS writes).
 template <int DK>
 struct alignas(16) KdaStateSmem {
     static constexpr int PK = DK + 4, PC = 68;
@@ -97,8 +237,11 @@ struct Chain {   // the chunks of the work-group's (sequence, head)
 template <int NTILE>
 __device__ __forceinline__ Chain chain_of(const ChunkProblem& p) {
     Chain c;
-    const long slot = blockIdx.x / NTILE;
-    c.tile = (int)(blockIdx.x % NTILE);
+    // Work-groups go to the eight XCDs in turn; the tiles of one pair read the same operators, so in every full group
+    // of eight pairs they are eight apart and share an XCD's L2.
+    const long b = blockIdx.x, full = (gridDim.x / (8 * NTILE)) * (8 * NTILE);
+    const long slot = b < full ? b / (8 * NTILE) * 8 + b % 8 : b / NTILE;
+    c.tile = (int)(b < full ? b / 8 % NTILE : b % NTILE);
     // packed sequences are taken longest first (the chunk table's order)
     const int n = p.cu_seqlens ? p.chunk_base[p.N + 1 + (int)(slot / p.H)] : (int)(slot / p.H);
     c.h = (int)(slot % p.H);
@@ -110,35 +253,14 @@ __device__ __forceinline__ Chain chain_of(const ChunkProblem& p) {
     return c;
 }
 
-// The rows 16 t + 4 lq + m of column `col` of a chunk's [len, H, DV] tokens, as loaded (zeros past the end): converted
-// where they are used, since a conversion at the load would wait for it.
-template <typename TIn, int DV>
-struct TokenCols {
-    uint32_t x[4][4];
-    __device__ __forceinline__ void load(const void* src, long bos, int len, int H, int h, int col, int lq) {
-        constexpr int EB = (int)sizeof(TIn);
-        const auto rs = make_rsrc(static_cast<const TIn*>(src) + (bos * H + h) * DV, (unsigned)((len - 1) * H * DV + DV) * EB);
-        const int o0 = (4 * lq * H * DV + col) * EB;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int o = o0 + (16 * t + m) * H * DV * EB;
-                if constexpr (EB == 2) x[t][m] = __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0);
-                else x[t][m] = __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
-            }
-    }
-    __device__ __forceinline__ float at(int t, int m) const { return __uint_as_float(sizeof(TIn) == 2 ? x[t][m] << 16 : x[t][m]); }
-};
-
 template <typename TIn, int DK, int DV>
 __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
     using SM = KdaStateSmem<DK>;
     constexpr int PK = SM::PK, PC = SM::PC, HK = DK / 2, NJ = HK / 16;
     __shared__ SM sm;
     const ChunkProblem& p = b.f;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, lq = lane >> 4;
-    const int cg = wave & 1, hf = wave >> 1;
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 1, hf = wave >> 1;
     const Chain c = chain_of<DV / 32>(p);
     const int H = p.H, col = 32 * c.tile + 16 * cg + l16;
 
@@ -152,81 +274,85 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
     WalkTile<64, PC> mt;
     TokenCols<TIn, DV> v;
     float lam = 0.f;
-    auto fetch = [&](long jc) {
+    float* own = reinterpret_cast<float*>(&sm.ex[wave][0][0]);
+    constexpr int NV = WalkTile<DK, PK>::NV;
+    auto load = [&](long jc, int i) {   // i = 0 .. 7: a share of the chunk's loads
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
-        kh.load(p.khat + widx * 64 * DK, tid);
-        kd.load(p.kdec + widx * 64 * DK, tid);
-        mt.load(static_cast<const float*>(p.mmat) + widx * 4096, tid);
-        if (tid < DK) lam = p.lam[widx * DK + tid];
-        v.load(p.v, bos, (int)min(64L, c.seos - bos), H, c.h, col, lq);
+        if (i < NV) {
+            kh.load(p.khat + widx * 64 * DK, i, tid);
+            kd.load(p.kdec + widx * 64 * DK, i, tid);
+        }
+        if (i < 4) mt.load(static_cast<const float*>(p.mmat) + widx * 4096, i, tid);
+        if (i == 4) lam = p.lam[widx * DK + tid % DK];
+        if (i >= 4 && i - 4 < v.NV) v.load(p.v, bos, (int)min(64L, c.seos - bos), H, c.h, 32 * c.tile + 16 * cg, i - 4, lane);
     };
-    if (c.nchunks > 0) fetch(0);
+    auto store = [&](int i) {           // and of its LDS writes
+        if (i < NV) {
+            kh.store(sm.Kh, i, tid);
+            kd.store(sm.Kd, i, tid);
+        }
+        if (i < 4) mt.store(sm.M, i, tid);
+        if (i == 4) sm.lam[tid % DK] = lam;
+        if (i >= 4 && i - 4 < v.NV) v.store(own, i - 4, lane);
+    };
+    if (c.nchunks > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load(0, i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) store(i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load(min(1L, c.nchunks - 1), i);
+    }
     for (long jc = 0; jc < c.nchunks; ++jc) {
         const long widx = (c.cbase + jc) * H + c.h;
-        __syncthreads();   // the previous chunk's operands are dead
-        kh.store(sm.Kh, tid);
-        kd.store(sm.Kd, tid);
-        mt.store(sm.M, tid);
-        if (tid < DK) sm.lam[tid] = lam;
         f32x4_t X[4], D[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) D[t] = f32x4_t{v.at(t, 0), v.at(t, 1), v.at(t, 2), v.at(t, 3)};   // V, until R is formed
-        __syncthreads();
-        if (jc + 1 < c.nchunks) fetch(jc + 1);
+        __syncthreads();   // the chunk's operands are in LDS
+        TokenCols<TIn, DV>::get(own, D, lane);   // V, until R is formed
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
             *reinterpret_cast<f32x4_t*>(p.states + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = ST[j];
         // this half of X = Kh S^T
+        {
+            RowFrags<NJ> f;
+            f.read(sm.Kh, PK, hf * HK, l16, lq);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const f32x4_t a = *reinterpret_cast<const f32x4_t*>(&sm.Kh[(16 * t + l16) * PK + hf * HK + 16 * j + 4 * lq]);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) X[t] = mfma4(a[s], ST[j][s], X[t]);
-            }
-            sm.ex[wave][t][lane] = X[t];
+            for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            f.mul(X, ST);
         }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) sm.ex[wave][t][lane] = X[t];
+        TriFrags<false, PC> m;
+        m.read(sm.M, hf, l16, lq);
+        ColFrags<NJ> kf;
+        kf.read(sm.Kd, PK, hf * HK, l16, lq);
+        f32x4_t lm[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) lm[j] = *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] = D[t] - (X[t] + sm.ex[wave ^ 2][t][lane]);   // R
         // D = M R on the wave's row tiles
+        {
+            f32x4_t d[2];
+            m.mul(X, hf, d[0], d[1]);
+            const int ta = m.first_tile(hf), tb = m.second_tile(hf);
+            sm.ex2[cg][ta][lane] = d[0];
+            sm.ex2[cg][tb][lane] = d[1];
+            float* dst = b.delta + (widx * 64 + 4 * lq) * DV + col;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            auto rows = [&](auto tc) {
-                constexpr int t = decltype(tc)::value;
-                f32x4_t d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int t2 = 0; t2 <= t; ++t2) {
-                    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(&sm.M[(16 * t + l16) * PC + 16 * t2 + 4 * lq]);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) d = mfma4(a[s], X[t2][s], d);
-                }
-                sm.ex2[cg][t][lane] = d;
-                float* dst = b.delta + (widx * 64 + 16 * t + 4 * lq) * DV + col;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) dst[m * DV] = d[m];
-            };
-            if (hf == 0) { if (i == 0) rows(std::integral_constant<int, 0>{}); else rows(std::integral_constant<int, 3>{}); }
-            else { if (i == 0) rows(std::integral_constant<int, 1>{}); else rows(std::integral_constant<int, 2>{}); }
+            for (int i = 0; i < 4; ++i) dst[(16 * ta + i) * DV] = d[0][i], dst[(16 * tb + i) * DV] = d[1][i];
         }
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < 4; ++t) D[t] = sm.ex2[cg][t][lane];
         // S^T <- Diag(lam) S^T + Kd^T D on the wave's channels
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            f32x4_t acc;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) acc[m] = ST[j][m] * sm.lam[hf * HK + 16 * j + 4 * lq + m];
-#pragma unroll
-            for (int t2 = 0; t2 < 4; ++t2)
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    acc = mfma4(sm.Kd[(16 * t2 + 4 * lq + s) * PK + hf * HK + 16 * j + l16], D[t2][s], acc);
-            ST[j] = acc;
-        }
+        for (int j = 0; j < NJ; ++j) ST[j] *= lm[j];
+        const long nxt = min(jc + 2, c.nchunks - 1);   // the last chunk again past the end
+        kf.mul(ST, D, [&](int i) {
+            if (i < 8) store(i);
+            else load(nxt, i - 8);
+        });
     }
 }
 
@@ -250,8 +376,8 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
     constexpr int PK = SM::PK, PC = SM::PC, HK = DK / 2, NJ = HK / 16;
     __shared__ SM sm;
     const ChunkProblem& p = b.f;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, lq = lane >> 4;
-    const int cg = wave & 1, hf = wave >> 1;
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 1, hf = wave >> 1;
     const Chain c = chain_of<DV / 32>(p);
     const int H = p.H, col = 32 * c.tile + 16 * cg + l16;
 
@@ -265,102 +391,121 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
     WalkTile<64, PC> pt, tt;
     TokenCols<TIn, DV> dof;
     float lam = 0.f, beta = 0.f;
-    auto fetch = [&](long jc) {
+    float* own = reinterpret_cast<float*>(&sm.ex[wave][0][0]);
+    constexpr int NV = WalkTile<DK, PK>::NV;
+    auto load = [&](long jc, int i) {   // i = 0 .. 7: a share of the chunk's loads
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
         const int len = (int)min(64L, c.seos - bos);
-        kh.load(p.khat + widx * 64 * DK, tid);
-        qh.load(p.qhat + widx * 64 * DK, tid);
-        kd.load(p.kdec + widx * 64 * DK, tid);
-        pt.load(static_cast<const float*>(p.pmat) + widx * 4096, tid);
-        tt.load(p.tmat + widx * 4096, tid);
-        if (tid < DK) lam = p.lam[widx * DK + tid];
-        if (tid < 64) beta = tid < len ? p.beta[(bos + tid) * H + c.h] : 0.f;
-        dof.load(b.d_o, bos, len, H, c.h, col, lq);
+        if (i < NV) {
+            kh.load(p.khat + widx * 64 * DK, i, tid);
+            qh.load(p.qhat + widx * 64 * DK, i, tid);
+            kd.load(p.kdec + widx * 64 * DK, i, tid);
+        }
+        if (i < 4) {
+            pt.load(static_cast<const float*>(p.pmat) + widx * 4096, i, tid);
+            tt.load(p.tmat + widx * 4096, i, tid);
+        }
+        if (i == 4) {
+            lam = p.lam[widx * DK + tid % DK];
+            const auto br = make_rsrc(p.beta + bos * H + c.h, (unsigned)(((len - 1) * H + 1) * 4));
+            beta = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(br, (tid & 63) * H * 4, 0, 0));
+        }
+        if (i >= 4 && i - 4 < dof.NV) dof.load(b.d_o, bos, len, H, c.h, 32 * c.tile + 16 * cg, i - 4, lane);
     };
-    if (c.nchunks > 0) fetch(c.nchunks - 1);
+    auto store = [&](int i) {           // and of its LDS writes
+        if (i < NV) {
+            kh.store(sm.Kh, i, tid);
+            qh.store(sm.Qh, i, tid);
+            kd.store(sm.Kd, i, tid);
+        }
+        if (i < 4) {
+            pt.store(sm.P, i, tid);
+            tt.store(sm.T, i, tid);
+        }
+        if (i == 4) {
+            sm.lam[tid % DK] = lam;
+            sm.beta[tid & 63] = beta;
+        }
+        if (i >= 4 && i - 4 < dof.NV) dof.store(own, i - 4, lane);
+    };
+    if (c.nchunks > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load(c.nchunks - 1, i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) store(i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load(max(0L, c.nchunks - 2), i);
+    }
     for (long jc = c.nchunks - 1; jc >= 0; --jc) {
         const long widx = (c.cbase + jc) * H + c.h;
-        __syncthreads();   // the previous chunk's operands are dead
-        kh.store(sm.Kh, tid);
-        qh.store(sm.Qh, tid);
-        kd.store(sm.Kd, tid);
-        pt.store(sm.P, tid);
-        tt.store(sm.T, tid);
-        if (tid < DK) sm.lam[tid] = lam;
-        if (tid < 64) sm.beta[tid] = beta;
         f32x4_t dO[4], X[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) dO[t] = f32x4_t{dof.at(t, 0), dof.at(t, 1), dof.at(t, 2), dof.at(t, 3)};
-        __syncthreads();
-        if (jc > 0) fetch(jc - 1);
+        __syncthreads();   // the chunk's operands are in LDS
+        TokenCols<TIn, DV>::get(own, dO, lane);
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
             *reinterpret_cast<f32x4_t*>(b.dstates + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = dST[j];
         // this wave's share of dD = Kd dS'^T + P^T dO: its half of the channels, and of P's rows (tiles {0, 3}, {1, 2})
+        {
+            RowFrags<NJ> f;
+            f.read(sm.Kd, PK, hf * HK, l16, lq);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const f32x4_t a = *reinterpret_cast<const f32x4_t*>(&sm.Kd[(16 * t + l16) * PK + hf * HK + 16 * j + 4 * lq]);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) X[t] = mfma4(a[s], dST[j][s], X[t]);
-            }
+            for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            f.mul(X, dST);
         }
         auto prow = [&](auto tc) {
             constexpr int t2 = decltype(tc)::value;
+            f32x4_t a[t2 + 1];
 #pragma unroll
             for (int t = 0; t <= t2; ++t)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) X[t] = mfma4(sm.P[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16], dO[t2][s], X[t]);
+                for (int s = 0; s < 4; ++s) a[t][s] = sm.P[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16];
+            pin();
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int t = 0; t <= t2; ++t) X[t] = mfma4(a[t][s], dO[t2][s], X[t]);
         };
         if (hf == 0) { prow(std::integral_constant<int, 0>{}); prow(std::integral_constant<int, 3>{}); }
         else { prow(std::integral_constant<int, 1>{}); prow(std::integral_constant<int, 2>{}); }
 #pragma unroll
         for (int t = 0; t < 4; ++t) sm.ex[wave][t][lane] = X[t];
         // dS'^T Diag(lam) + Qh^T dO on the wave's channels
+        {
+            ColFrags<NJ> f;
+            f.read(sm.Qh, PK, hf * HK, l16, lq);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) dST[j][m] *= sm.lam[hf * HK + 16 * j + 4 * lq + m];
-#pragma unroll
-            for (int t2 = 0; t2 < 4; ++t2)
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    dST[j] = mfma4(sm.Qh[(16 * t2 + 4 * lq + s) * PK + hf * HK + 16 * j + l16], dO[t2][s], dST[j]);
+            for (int j = 0; j < NJ; ++j) dST[j] *= *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
+            f.mul(dST, dO, [](int) {});
         }
+        TriFrags<true, PC> tf;
+        tf.read(sm.T, hf, l16, lq);
+        ColFrags<NJ> kf;
+        kf.read(sm.Kh, PK, hf * HK, l16, lq);
+        f32x4_t bt[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) bt[t] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * t + 4 * lq]);
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] += sm.ex[wave ^ 2][t][lane];   // dD
         // Y = T^T dD on the wave's row tiles
-        auto yrow = [&](auto tc) {
-            constexpr int t = decltype(tc)::value;
-            f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+        {
+            f32x4_t y[2];
+            tf.mul(X, hf, y[0], y[1]);
+            const int ta = tf.first_tile(hf), tb = tf.second_tile(hf);
+            sm.ex2[cg][ta][lane] = y[0];
+            sm.ex2[cg][tb][lane] = y[1];
+            float* dst = b.ymat + (widx * 64 + 4 * lq) * DV + col;
 #pragma unroll
-            for (int t2 = t; t2 < 4; ++t2)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) y = mfma4(sm.T[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16], X[t2][s], y);
-            sm.ex2[cg][t][lane] = y;
-            float* dst = b.ymat + (widx * 64 + 16 * t + 4 * lq) * DV + col;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) dst[m * DV] = y[m];
-        };
-        if (hf == 0) { yrow(std::integral_constant<int, 0>{}); yrow(std::integral_constant<int, 3>{}); }
-        else { yrow(std::integral_constant<int, 1>{}); yrow(std::integral_constant<int, 2>{}); }
+            for (int i = 0; i < 4; ++i) dst[(16 * ta + i) * DV] = y[0][i], dst[(16 * tb + i) * DV] = y[1][i];
+        }
         __syncthreads();
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {   // -dR
-            X[t] = sm.ex2[cg][t][lane];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) X[t][m] *= -sm.beta[16 * t + 4 * lq + m];
-        }
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int t2 = 0; t2 < 4; ++t2)
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    dST[j] = mfma4(sm.Kh[(16 * t2 + 4 * lq + s) * PK + hf * HK + 16 * j + l16], X[t2][s], dST[j]);
+        for (int t = 0; t < 4; ++t) X[t] = -(bt[t] * sm.ex2[cg][t][lane]);   // -dR
+        const long nxt = max(jc - 2, 0L);   // the first chunk again past the end
+        kf.mul(dST, X, [&](int i) {
+            if (i < 8) store(i);
+            else load(nxt, i - 8);
+        });
     }
     if (b.dh0) {
 #pragma unroll
@@ -387,13 +532,6 @@ struct alignas(16) KdaGradSmem {
     float yv[64];
     float part[NW][64];
 };
-
-// Keeps the compiler from moving memory accesses across: without it, it reads the operands of whole unrolled sections
-// ahead and spills what it read.
-__device__ __forceinline__ void pin() { asm volatile("" ::: "memory"); }
-
-// Makes the compiler have x in a register at this point of the program.
-__device__ __forceinline__ void hold(float& x) { asm volatile("" : "+v"(x)); }
 
 // Orders a wave's own LDS writes before its reads of what other lanes wrote.
 __device__ __forceinline__ void wave_lds_fence() {
