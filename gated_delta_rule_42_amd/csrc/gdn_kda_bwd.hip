@@ -106,55 +106,51 @@ __device__ __forceinline__ void pin() { asm volatile("" ::: "memory"); }
 // Makes the compiler have x in a register at this point of the program.
 __device__ __forceinline__ void hold(float& x) { asm volatile("" : "+v"(x)); }
 
-// Operands of the walks, read from LDS ahead of their products (a wave has a SIMD to itself there, so a read that is waited
-// for right before its product costs its whole latency). Rows: 16-byte pieces of row 16 t + l16 of a [64, P] matrix, tile t
-// (and block j) each; cols: column c + l16 of the rows 16 t2 + 4 lq + s.
-template <int NJ>
-struct RowFrags {
-    f32x4_t a[4][NJ];
-    __device__ __forceinline__ void read(const float* m, int pitch, int c0, int l16, int lq) {
+// Products of the walks. A wave has a SIMD to itself there, so whatever it waits for stands still: every product takes
+// step(0) .. step(15) between its matrix instructions, the memory instructions of what comes next, which the matrix core
+// hides. Rows: operands are 16-byte pieces of the rows 16 t + l16 of a [64, P] matrix (block j: 16 channels), read here
+// one block ahead. Cols: column c + l16 of the rows 16 t2 + 4 lq + s, read in the steps of an earlier product.
+template <int NJ, typename F>
+__device__ __forceinline__ void mul_rows(f32x4_t (&acc)[4], const float* m, int pitch, int c0, const f32x4_t (&b)[NJ], int l16, int lq, F step) {
+    f32x4_t a[NJ][4];
+    auto read = [&](int j) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int t = 0; t < 4; ++t) a[j][t] = *reinterpret_cast<const f32x4_t*>(&m[(16 * t + l16) * pitch + c0 + 16 * j + 4 * lq]);
+    };
+    read(0);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) a[t][j] = *reinterpret_cast<const f32x4_t*>(&m[(16 * t + l16) * pitch + c0 + 16 * j + 4 * lq]);
-        pin();
-    }
-    // acc[t] += rows of tile t times b
-    __device__ __forceinline__ void mul(f32x4_t (&acc)[4], const f32x4_t (&b)[NJ]) const {
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int s = 0; s < 4; ++s) {
+            if (s == 0 && j + 1 < NJ) read(j + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int t = 0; t < 4; ++t) acc[t] = mfma4(a[j][t][s], b[j][s], acc[t]);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) acc[t] = mfma4(a[t][j][s], b[j][s], acc[t]);
-    }
-};
+            for (int i = 0; i < 4 / NJ; ++i) step((4 * j + s) * (4 / NJ) + i);
+        }
+    __builtin_amdgcn_sched_barrier(0);
+}
 template <int NJ>
 struct ColFrags {
     f32x4_t a[4][NJ];
-    __device__ __forceinline__ void read(const float* m, int pitch, int c0, int l16, int lq) {
+    __device__ __forceinline__ void read(const float* m, int pitch, int c0, int i, int l16, int lq) {   // i = 0 .. 15
+        const int t2 = i / 4, s = i % 4;
 #pragma unroll
-        for (int t2 = 0; t2 < 4; ++t2)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) a[t2][j][s] = m[(16 * t2 + 4 * lq + s) * pitch + c0 + 16 * j + l16];
-        pin();
+        for (int j = 0; j < NJ; ++j) a[t2][j][s] = m[(16 * t2 + 4 * lq + s) * pitch + c0 + 16 * j + l16];
     }
-    // acc[j] += columns of block j times b, with step(0) .. step(15) in between: the memory instructions of the chunks to
-    // come, which the matrix core hides there
+    // acc[j] += columns of block j times b
     template <typename F>
     __device__ __forceinline__ void mul(f32x4_t (&acc)[NJ], const f32x4_t (&b)[4], F step) const {
 #pragma unroll
-        for (int t2 = 0; t2 < 4; ++t2)
+        for (int i = 0; i < 16; ++i) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) acc[j] = mfma4(a[t2][j][s], b[t2][s], acc[j]);
-                __builtin_amdgcn_sched_barrier(0);
-                step(4 * t2 + s);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int j = 0; j < NJ; ++j) acc[j] = mfma4(a[i / 4][j][i % 4], b[i / 4][i % 4], acc[j]);
+            __builtin_amdgcn_sched_barrier(0);
+            step(i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 };
 // The wave's share of a product with a lower triangular [64, 64] matrix m (TRANS: with m^T): row tiles 0 and 3 for
@@ -172,23 +168,14 @@ struct TriFrags {
     static constexpr int con(int i) {
         return TRANS ? (HF == 0 ? (i == 0 ? 3 : i - 1) : (i < 2 ? 2 + i : i - 1)) : (HF == 0 ? (i == 0 ? 0 : i - 1) : (i < 2 ? i : i - 2));
     }
-    template <int HF>
-    __device__ __forceinline__ void read_of(const float* m, int l16, int lq) {
+    __device__ __forceinline__ void read(const float* m, int hf, int i, int l16, int lq) {   // i = 0 .. 4
+        const int t = hf == 0 ? row<0>(i) : row<1>(i), t2 = hf == 0 ? con<0>(i) : con<1>(i);
+        if constexpr (TRANS) {
 #pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            const int t = row<HF>(i), t2 = con<HF>(i);
-            if constexpr (TRANS) {
-#pragma unroll
-                for (int s = 0; s < 4; ++s) a[i][s] = m[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16];
-            } else {
-                a[i] = *reinterpret_cast<const f32x4_t*>(&m[(16 * t + l16) * PC + 16 * t2 + 4 * lq]);
-            }
+            for (int s = 0; s < 4; ++s) a[i][s] = m[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16];
+        } else {
+            a[i] = *reinterpret_cast<const f32x4_t*>(&m[(16 * t + l16) * PC + 16 * t2 + 4 * lq]);
         }
-        pin();
-    }
-    __device__ __forceinline__ void read(const float* m, int hf, int l16, int lq) {
-        if (hf == 0) read_of<0>(m, l16, lq);
-        else read_of<1>(m, l16, lq);
     }
     // The two row tiles of the product with x, each block's product on its own accumulator
     template <int HF>
@@ -308,26 +295,23 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
         f32x4_t X[4], D[4];
         __syncthreads();   // the chunk's operands are in LDS
         TokenCols<TIn, DV>::get(own, D, lane);   // V, until R is formed
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            *reinterpret_cast<f32x4_t*>(p.states + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = ST[j];
         // this half of X = Kh S^T
-        {
-            RowFrags<NJ> f;
-            f.read(sm.Kh, PK, hf * HK, l16, lq);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            f.mul(X, ST);
-        }
+        for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        TriFrags<false, PC> m;
+        ColFrags<NJ> kf;
+        f32x4_t lm[NJ];
+        mul_rows<NJ>(X, sm.Kh, PK, hf * HK, ST, l16, lq, [&](int i) {
+            kf.read(sm.Kd, PK, hf * HK, i, l16, lq);
+            if (i < 5) m.read(sm.M, hf, i, l16, lq);
+            const int j = i / 4;
+            if (i % 4 == 0 && j < NJ) {
+                *reinterpret_cast<f32x4_t*>(p.states + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = ST[j];
+                lm[j] = *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
+            }
+        });
 #pragma unroll
         for (int t = 0; t < 4; ++t) sm.ex[wave][t][lane] = X[t];
-        TriFrags<false, PC> m;
-        m.read(sm.M, hf, l16, lq);
-        ColFrags<NJ> kf;
-        kf.read(sm.Kd, PK, hf * HK, l16, lq);
-        f32x4_t lm[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) lm[j] = *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] = D[t] - (X[t] + sm.ex[wave ^ 2][t][lane]);   // R
@@ -350,8 +334,8 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
         for (int j = 0; j < NJ; ++j) ST[j] *= lm[j];
         const long nxt = min(jc + 2, c.nchunks - 1);   // the last chunk again past the end
         kf.mul(ST, D, [&](int i) {
-            if (i < 8) store(i);
-            else load(nxt, i - 8);
+            if (i % 2 == 0) store(i / 2);
+            else load(nxt, i / 2);
         });
     }
 }
@@ -441,49 +425,35 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
         f32x4_t dO[4], X[4];
         __syncthreads();   // the chunk's operands are in LDS
         TokenCols<TIn, DV>::get(own, dO, lane);
+        // this wave's share of dD = Kd dS'^T + P^T dO: its half of the channels, and of the row tiles of P^T dO ({3, 0}, {2, 1})
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            *reinterpret_cast<f32x4_t*>(b.dstates + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = dST[j];
-        // this wave's share of dD = Kd dS'^T + P^T dO: its half of the channels, and of P's rows (tiles {0, 3}, {1, 2})
+        for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        ColFrags<NJ> qf, kf;
+        TriFrags<true, PC> pf, tf;
+        mul_rows<NJ>(X, sm.Kd, PK, hf * HK, dST, l16, lq, [&](int i) {
+            qf.read(sm.Qh, PK, hf * HK, i, l16, lq);
+            if (i < 5) pf.read(sm.P, hf, i, l16, lq);
+            const int j = i / 4;
+            if (i % 4 == 0 && j < NJ)
+                *reinterpret_cast<f32x4_t*>(b.dstates + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = dST[j];
+        });
         {
-            RowFrags<NJ> f;
-            f.read(sm.Kd, PK, hf * HK, l16, lq);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            f.mul(X, dST);
+            f32x4_t y[2];
+            pf.mul(dO, hf, y[0], y[1]);
+            if (hf == 0) X[3] += y[0], X[0] += y[1];
+            else X[2] += y[0], X[1] += y[1];
         }
-        auto prow = [&](auto tc) {
-            constexpr int t2 = decltype(tc)::value;
-            f32x4_t a[t2 + 1];
-#pragma unroll
-            for (int t = 0; t <= t2; ++t)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) a[t][s] = sm.P[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16];
-            pin();
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int t = 0; t <= t2; ++t) X[t] = mfma4(a[t][s], dO[t2][s], X[t]);
-        };
-        if (hf == 0) { prow(std::integral_constant<int, 0>{}); prow(std::integral_constant<int, 3>{}); }
-        else { prow(std::integral_constant<int, 1>{}); prow(std::integral_constant<int, 2>{}); }
 #pragma unroll
         for (int t = 0; t < 4; ++t) sm.ex[wave][t][lane] = X[t];
         // dS'^T Diag(lam) + Qh^T dO on the wave's channels
-        {
-            ColFrags<NJ> f;
-            f.read(sm.Qh, PK, hf * HK, l16, lq);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) dST[j] *= *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
-            f.mul(dST, dO, [](int) {});
-        }
-        TriFrags<true, PC> tf;
-        tf.read(sm.T, hf, l16, lq);
-        ColFrags<NJ> kf;
-        kf.read(sm.Kh, PK, hf * HK, l16, lq);
         f32x4_t bt[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) bt[t] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * t + 4 * lq]);
+        for (int j = 0; j < NJ; ++j) dST[j] *= *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
+        qf.mul(dST, dO, [&](int i) {
+            kf.read(sm.Kh, PK, hf * HK, i, l16, lq);
+            if (i < 5) tf.read(sm.T, hf, i, l16, lq);
+            if (i < 4) bt[i] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * i + 4 * lq]);
+        });
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] += sm.ex[wave ^ 2][t][lane];   // dD
@@ -503,8 +473,8 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
         for (int t = 0; t < 4; ++t) X[t] = -(bt[t] * sm.ex2[cg][t][lane]);   // -dR
         const long nxt = max(jc - 2, 0L);   // the first chunk again past the end
         kf.mul(dST, X, [&](int i) {
-            if (i < 8) store(i);
-            else load(nxt, i - 8);
+            if (i % 2 == 0) store(i / 2);
+            else load(nxt, i / 2);
         });
     }
     if (b.dh0) {
