@@ -31,12 +31,7 @@
 
 namespace gdn {
 
-// Four consecutive input elements as fp32.
-__device__ __forceinline__ float4 kb_in4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 kb_in4(const uint16_t* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(bf16_lo_half(w.x), bf16_hi_half(w.x), bf16_lo_half(w.y), bf16_hi_half(w.y));
-}
+// Four consecutive gradients, rounded to the output type.
 __device__ __forceinline__ void kb_out4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void kb_out4(uint16_t* p, float4 x) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
@@ -48,12 +43,6 @@ __device__ __forceinline__ float buf_in(__amdgpu_buffer_rsrc_t r, int off) {
     if constexpr (sizeof(TIn) == 2) return to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
     else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
 }
-template <typename TG>
-__device__ __forceinline__ void buf_out(__amdgpu_buffer_rsrc_t r, int off, float x) {
-    if constexpr (sizeof(TG) == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(x), r, off, 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
-}
-
 // A [64, W] fp32 matrix of the workspace on its way into LDS (row pitch P), 256 threads: NV 16-byte pieces per thread,
 // held in registers between load and store.
 template <int W, int P>
@@ -495,13 +484,26 @@ struct alignas(16) KdaGradSmem {
     union {
         struct { float D[64 * PV], Y[64 * PV], dO[64 * PV]; } in;
         float turn[NW][64 * PT];
+        float out[3][64 * 16 * NW];   // dq, dk, dg on their way out (see out_at)
     };
-    float dP[64 * PC];
+    float dP[64 * PC];                // see tri_at
     float dA[64 * PC];
     float beta[64];
     float yv[64];
     float part[NW][64];
 };
+
+// Element (r, i) of dP and dA. They are read by rows (pieces of one row), by columns (16 columns of the row s of all four
+// row blocks at once) and by diagonal blocks (a piece of the row s of all four), so the column blocks of row block b are
+// permuted by f(b), a permutation for which b ^ f(b) is one as well: either way the four blocks sit in different banks.
+template <int PC>
+__device__ __forceinline__ int tri_at(int r, int i) {
+    const int b = r >> 4, f = ((b << 1) ^ ((b >> 1) * 3)) & 3;
+    return r * PC + (i ^ (16 * f));
+}
+// Element (r, c) of an output tile: a wave writes 16 columns of four row blocks at once.
+template <int W>
+__device__ __forceinline__ int out_at(int r, int c) { return r * W + (c ^ (16 * ((r >> 4) & 3))); }
 
 // Orders a wave's own LDS writes before its reads of what other lanes wrote.
 __device__ __forceinline__ void wave_lds_fence() {
@@ -525,11 +527,39 @@ __global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     if (!locate_chunk(p, unit / H, bos, len)) return;   // packed: past the last chunk
     const int h = (int)(unit % H);
     {
-        // q, k, g of the lane's rows and channel, through resources that end at the chunk's last token
+        // D, Y, dO and V, then q, k, g of the lane's rows and channel, all issued before the first is used; inputs
+        // through resources that end at the chunk's last token
+        constexpr int NP = 64 * DV / 4 / NT;   // pieces of four per thread
+        constexpr int EB = (int)sizeof(TIn);
+        f32x4_t dpc[NP], ypc[NP];
+        u32x4_t gpc[NP], vpc[NP];
+        float bpc[NP];
+        const float bt = p.beta[(bos + min(tid & 63, len - 1)) * H + h];
+        {
+            const long vb = (bos * H + h) * DV;
+            const unsigned rows = (unsigned)((len - 1) * H * DV + DV);
+            const auto gr = make_rsrc(static_cast<const TIn*>(b.d_o) + vb, rows * EB);
+            const auto vr = make_rsrc(static_cast<const TIn*>(p.v) + vb, rows * EB);
+            const auto br = make_rsrc(p.beta + bos * H + h, (unsigned)(((len - 1) * H + 1) * 4));
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const int i = tid + NT * n, r = i / (DV / 4), cc = 4 * (i % (DV / 4)), o = (r * H * DV + cc) * EB;
+                dpc[n] = *reinterpret_cast<const f32x4_t*>(b.delta + (unit * 64 + r) * DV + cc);
+                ypc[n] = *reinterpret_cast<const f32x4_t*>(b.ymat + (unit * 64 + r) * DV + cc);
+                if constexpr (EB == 2) {
+                    const u32x2_t g2 = __builtin_amdgcn_raw_buffer_load_b64(gr, o, 0, 0), v2 = __builtin_amdgcn_raw_buffer_load_b64(vr, o, 0, 0);
+                    gpc[n] = u32x4_t{g2[0], g2[1], 0u, 0u};
+                    vpc[n] = u32x4_t{v2[0], v2[1], 0u, 0u};
+                } else {
+                    gpc[n] = __builtin_amdgcn_raw_buffer_load_b128(gr, o, 0, 0);
+                    vpc[n] = __builtin_amdgcn_raw_buffer_load_b128(vr, o, 0, 0);
+                }
+                bpc[n] = buf_in<float>(br, r * H * 4);
+            }
+        }
         float k[16], q[16], gm[16];
         const long base = (bos * H + h) * DK;
         {
-            constexpr int EB = (int)sizeof(TIn);
             const unsigned rows = (unsigned)((len - 1) * H * DK + DK);
             const auto kr = make_rsrc(static_cast<const TIn*>(p.k) + base, rows * EB);
             const auto qr = make_rsrc(static_cast<const TIn*>(p.q) + base, rows * EB);
@@ -540,31 +570,30 @@ __global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
                 const int o = o0 + r * H * DK;
                 k[r] = buf_in<TIn>(kr, o * EB);
                 q[r] = buf_in<TIn>(qr, o * EB);
-                gm[r] = fmaxf(buf_in<float>(gr, o * 4), kMinLogDecay);
+                gm[r] = buf_in<float>(gr, o * 4);
             }
         }
+        pin();
         // D, Y and dO into LDS; dV = beta Y and Y . V on the way (a row's DV / 4 threads are consecutive lanes)
-        if (tid < 64) sm.beta[tid] = tid < len ? p.beta[(bos + tid) * H + h] : 0.f;
-        for (int i = tid; i < 64 * DV / 4; i += NT) {
-            const int r = i / (DV / 4), cc = 4 * (i % (DV / 4));
-            const float4 d = *reinterpret_cast<const float4*>(b.delta + (unit * 64 + r) * DV + cc);
-            const float4 y = *reinterpret_cast<const float4*>(b.ymat + (unit * 64 + r) * DV + cc);
-            float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
-            float yv = 0.f;
-            if (r < len) {
-                const long o = ((bos + r) * H + h) * DV + cc;
-                const float bt = p.beta[(bos + r) * H + h];
-                g = kb_in4(static_cast<const TIn*>(b.d_o) + o);
-                const float4 v = kb_in4(static_cast<const TIn*>(p.v) + o);
-                yv = y.x * v.x + y.y * v.y + y.z * v.z + y.w * v.w;
-                kb_out4(static_cast<TG*>(b.dv) + o, make_float4(bt * y.x, bt * y.y, bt * y.z, bt * y.w));
-            }
-            *reinterpret_cast<float4*>(&sm.in.D[r * PV + cc]) = d;
-            *reinterpret_cast<float4*>(&sm.in.Y[r * PV + cc]) = y;
-            *reinterpret_cast<float4*>(&sm.in.dO[r * PV + cc]) = g;
-            yv = row16_sum(yv);
+        auto widen = [](u32x4_t x) {
+            if constexpr (EB == 2) return make_float4(bf16_lo_half(x[0]), bf16_hi_half(x[0]), bf16_lo_half(x[1]), bf16_hi_half(x[1]));
+            else return __builtin_bit_cast(float4, x);
+        };
+        if (tid < 64) sm.beta[tid] = tid < len ? bt : 0.f;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int i = tid + NT * n, r = i / (DV / 4), cc = 4 * (i % (DV / 4));
+            const f32x4_t y = ypc[n];
+            const float4 v = widen(vpc[n]);
+            *reinterpret_cast<f32x4_t*>(&sm.in.D[r * PV + cc]) = dpc[n];
+            *reinterpret_cast<f32x4_t*>(&sm.in.Y[r * PV + cc]) = y;
+            *reinterpret_cast<float4*>(&sm.in.dO[r * PV + cc]) = widen(gpc[n]);
+            float yv = row16_sum(y[0] * v.x + y[1] * v.y + y[2] * v.z + y[3] * v.w);
             if constexpr (DV == 128) yv += __shfl_xor(yv, 16, 64);
             if (cc == 0) sm.yv[r] = yv;
+            if (r < len)
+                kb_out4(static_cast<TG*>(b.dv) + ((bos + r) * H + h) * DV + cc,
+                        make_float4(bpc[n] * y[0], bpc[n] * y[1], bpc[n] * y[2], bpc[n] * y[3]));
         }
         __syncthreads();
 
@@ -586,7 +615,7 @@ __global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const int r = 16 * I + 4 * lq + m, i = 16 * J + l16;
-                out[r * PC + i] = (job & 1) ? (i < r ? -acc[m] : 0.f) : (i <= r ? acc[m] : 0.f);
+                out[tri_at<PC>(r, i)] = (job & 1) ? (i < r ? -acc[m] : 0.f) : (i <= r ? acc[m] : 0.f);
             }
         }
         // dO S, Y S and D dS' on the wave's channels; colsum(S dS')
@@ -629,6 +658,7 @@ __global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         float a[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
+            gm[r] = fmaxf(gm[r], kMinLogDecay);
             a[r] = __expf(gm[r]);
             if (r > 0) gm[r] += gm[r - 1];
         }
@@ -675,7 +705,7 @@ __global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
 #pragma unroll
             for (int s4 = 0; s4 < 4; ++s4) {
                 pin();
-                const int o = (16 * I + l16) * PC + 16 * lq + 4 * s4;
+                const int o = tri_at<PC>(16 * I + l16, 16 * lq + 4 * s4);
                 const f32x4_t vp = *reinterpret_cast<const f32x4_t*>(&sm.dP[o]);
                 const f32x4_t va = *reinterpret_cast<const f32x4_t*>(&sm.dA[o]);
 #pragma unroll
@@ -692,7 +722,7 @@ __global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
 #pragma unroll
             for (int s = 0; s < 16; ++s) {
                 if (s % 4 == 0) pin();
-                const int o = (16 * lq + s) * PC + 16 * J + l16;
+                const int o = tri_at<PC>(16 * lq + s, 16 * J + l16);
                 const float e = lq > J ? __expf(gm[s] - end[J]) : 0.f;
                 ad[J] = mfma4(sm.dP[o], q[s] * e, ad[J]);
                 ad[J] = mfma4(sm.dA[o], sm.beta[16 * lq + s] * k[s] * e, ad[J]);
@@ -711,8 +741,8 @@ __global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             pin();
-            const float* pr = &sm.dP[(16 * lq + r) * PC + 16 * lq];
-            const float* pa = &sm.dA[(16 * lq + r) * PC + 16 * lq];
+            const float* pr = &sm.dP[tri_at<PC>(16 * lq + r, 16 * lq)];
+            const float* pa = &sm.dA[tri_at<PC>(16 * lq + r, 16 * lq)];
             const float bk = sm.beta[16 * lq + r] * k[r];
             w[r] = 1.f;
 #pragma unroll
@@ -754,22 +784,25 @@ __global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         for (int r = 14; r >= 0; --r) w[r] += w[r + 1];
         const float b1 = __shfl(w[0], 16 + l16, 64), b2 = __shfl(w[0], 32 + l16, 64), b3 = __shfl(w[0], 48 + l16, 64);
         const float tail = kx + (lq < 3 ? b3 : 0.f) + (lq < 2 ? b2 : 0.f) + (lq < 1 ? b1 : 0.f);
-        {
-            constexpr int EB = (int)sizeof(TG);
-            const unsigned rows = (unsigned)((len - 1) * H * DK + DK);
-            const auto qr = make_rsrc(static_cast<TG*>(b.dq) + base, rows * EB);
-            const auto kr = make_rsrc(static_cast<TG*>(b.dk) + base, rows * EB);
-            const auto gr = make_rsrc(b.dg + base, rows * 4);
-            const int o0 = 16 * lq * H * DK + ch;
+        __syncthreads();   // every wave is done with its turning tile
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int o = o0 + r * H * DK;
-                buf_out<TG>(qr, o * EB, dq[r]);
-                buf_out<TG>(kr, o * EB, l[r]);
-                buf_out<float>(gr, o * 4, w[r] + tail);
-            }
+        for (int r = 0; r < 16; ++r) {
+            const int o = out_at<DK>(16 * lq + r, ch);
+            sm.out[0][o] = dq[r];
+            sm.out[1][o] = l[r];
+            sm.out[2][o] = w[r] + tail;
         }
         __syncthreads();
+#pragma unroll
+        for (int n = 0; n < 64 * DK / 4 / NT; ++n) {
+            const int i = tid + NT * n, r = i / (DK / 4), cc = 4 * (i % (DK / 4)), o = out_at<DK>(r, cc);
+            if (r < len) {
+                const long g = base + (long)r * H * DK + cc;
+                kb_out4(static_cast<TG*>(b.dq) + g, *reinterpret_cast<const float4*>(&sm.out[0][o]));
+                kb_out4(static_cast<TG*>(b.dk) + g, *reinterpret_cast<const float4*>(&sm.out[1][o]));
+                kb_out4(b.dg + g, *reinterpret_cast<const float4*>(&sm.out[2][o]));
+            }
+        }
         if (tid < len) {
             float s = sm.yv[tid];
 #pragma unroll
