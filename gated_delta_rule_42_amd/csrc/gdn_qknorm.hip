@@ -24,20 +24,33 @@ constexpr int kNormPasses = 4;   // rows per lane group
 
 enum { ROPE_NONE = 0, ROPE_HALF = 1, ROPE_PAIRS = 2 };
 
-// Eight consecutive channels as fp32.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[2 * e] = bf16_lo_half(w[e]);
-        x[2 * e + 1] = bf16_hi_half(w[e]);
+// Eight consecutive channels as they lie in memory, and as fp32: rows wait for their turn as loaded, which halves the
+// registers of bf16 rows in flight.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
     }
-}
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+template <> struct Raw8<uint16_t> {
+    uint4 a;
+    __device__ __forceinline__ void load(const uint16_t* p) { a = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = bf16_lo_half(w[e]);
+            x[2 * e + 1] = bf16_hi_half(w[e]);
+        }
+    }
+};
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
@@ -115,22 +128,27 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const float2* cs, int l, 
     }
 }
 
-// Row `row` of q or k: its tensor, its element offset with the tensor's strides, its token.
+// Row `row` of the call (at most 2^28 rows): its token, its head, whether that is one of the keys'.
 struct NormRow {
     bool ok, key;
-    int head;
-    long token;
+    int head, token;
 };
-__device__ __forceinline__ NormRow norm_row(const NormProblem& p, long row, long nrows) {
+__device__ __forceinline__ NormRow norm_row(const NormProblem& p, unsigned row, unsigned nrows) {
     NormRow r;
     r.ok = row < nrows;
-    const unsigned ht = p.hq + p.hk;
-    const long t = r.ok ? row / ht : 0;
+    const unsigned ht = p.hq + p.hk, t = r.ok ? row / ht : 0;
     const int h = r.ok ? (int)(row - t * ht) : 0;
     r.key = h >= p.hq;
     r.head = r.key ? h - p.hq : h;
-    r.token = t;
+    r.token = (int)t;
     return r;
+}
+// Element offsets of a row: in q and k, and in dense tensors.
+__device__ __forceinline__ long row_in(const NormProblem& p, const NormRow& r) {
+    return r.key ? r.token * p.k_token + r.head * p.k_head : r.token * p.q_token + r.head * p.q_head;
+}
+__device__ __forceinline__ long row_dense(const NormProblem& p, const NormRow& r) {
+    return ((long)r.token * (r.key ? p.hk : p.hq) + r.head) * p.d;
 }
 
 template <typename TX, typename TY, int G, int ROPE>
@@ -138,56 +156,49 @@ __global__ __launch_bounds__(kNormThreads) void qk_norm_fwd_kernel(NormProblem p
     using B = NormBlock<G>;
     __shared__ float2 cs[ROPE ? B::MAXTOK * B::PAIRS : 1];
     const int tid = threadIdx.x, l = tid % G, grp = tid / G;
-    const long nrows = p.tokens * (p.hq + p.hk), row0 = (long)blockIdx.x * B::RB;
+    const unsigned nrows = (unsigned)(p.tokens * (p.hq + p.hk)), row0 = blockIdx.x * B::RB;
     const bool lane_in = 8 * l < p.d;
 
-    float x[kNormPasses][8];
+    Raw8<TX> raw[kNormPasses];
     NormRow rw[kNormPasses];
 #pragma unroll
     for (int i = 0; i < kNormPasses; ++i) {
         rw[i] = norm_row(p, row0 + i * B::RPP + grp, nrows);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-        if (rw[i].ok && lane_in) {
-            const long o = rw[i].key ? rw[i].token * p.k_token + rw[i].head * p.k_head
-                                     : rw[i].token * p.q_token + rw[i].head * p.q_head;
-            load8(static_cast<const TX*>(rw[i].key ? p.k : p.q) + o + 8 * l, x[i]);
-        }
+        raw[i].zero();
+        if (rw[i].ok && lane_in) raw[i].load(static_cast<const TX*>(rw[i].key ? p.k : p.q) + row_in(p, rw[i]) + 8 * l);
     }
-    long tok0 = 0;
+    int tok0 = 0;
     if constexpr (ROPE != ROPE_NONE) {
-        const unsigned ht = p.hq + p.hk;
-        const long last = (row0 + B::RB < nrows ? row0 + B::RB : nrows) - 1;
-        tok0 = row0 / ht;
-        fill_angles<G>(p, cs, tok0, (int)(last / ht - tok0) + 1, tid);
+        const unsigned ht = p.hq + p.hk, last = min(row0 + B::RB, nrows) - 1;
+        tok0 = (int)(row0 / ht);
+        fill_angles<G>(p, cs, tok0, (int)(last / ht) - tok0 + 1, tid);
         __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < kNormPasses; ++i) {
-        float ss = 0.f;
+        float x[8], ss = 0.f;
+        raw[i].get(x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += x[i][e] * x[i][e];
+        for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
         ss = row_sum<G>(ss);
         const float r = 1.f / sqrtf(ss * p.inv_n + p.eps);
         const float* w = rw[i].key ? p.k_weight : p.q_weight;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] *= r;
+        for (int e = 0; e < 8; ++e) x[e] *= r;
         if (w && lane_in) {
+            Raw8<float> wr;
             float wv[8];
-            load8(w + 8 * l, wv);
+            wr.load(w + 8 * l);
+            wr.get(wv);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][e] *= wv[e];
+            for (int e = 0; e < 8; ++e) x[e] *= wv[e];
         }
         if constexpr (ROPE != ROPE_NONE)
-            rotate8<ROPE, false>(x[i], cs + (rw[i].ok ? (rw[i].token - tok0) : 0) * B::PAIRS, l, p.rot);
+            rotate8<ROPE, false>(x, cs + (rw[i].ok ? (rw[i].token - tok0) : 0) * B::PAIRS, l, p.rot);
         const float scale = rw[i].key ? 1.f : p.q_scale;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] *= scale;
-        if (rw[i].ok && lane_in) {
-            TY* out = rw[i].key ? static_cast<TY*>(p.k_out) + (rw[i].token * p.hk + rw[i].head) * p.d
-                                : static_cast<TY*>(p.q_out) + (rw[i].token * p.hq + rw[i].head) * p.d;
-            store8(out + 8 * l, x[i]);
-        }
+        for (int e = 0; e < 8; ++e) x[e] *= scale;
+        if (rw[i].ok && lane_in) store8(static_cast<TY*>(rw[i].key ? p.k_out : p.q_out) + row_dense(p, rw[i]) + 8 * l, x);
     }
 }
 
@@ -200,74 +211,77 @@ __global__ __launch_bounds__(kNormThreads) void qk_norm_bwd_kernel(NormProblem p
     __shared__ float2 cs[ROPE ? B::MAXTOK * B::PAIRS : 1];
     __shared__ float part[DW ? 4 * 2 * 8 * G : 1];
     const int tid = threadIdx.x, l = tid % G, grp = tid / G;
-    const long nrows = p.tokens * (p.hq + p.hk);
-    const long nblocks = (nrows + B::RB - 1) / B::RB;
+    const unsigned nrows = (unsigned)(p.tokens * (p.hq + p.hk)), nblocks = (nrows + B::RB - 1) / B::RB;
     const bool lane_in = 8 * l < p.d;
     float aq[8], ak[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
 
-    for (long blk = blockIdx.x; blk < nblocks; blk += gridDim.x) {
-        const long row0 = blk * B::RB;
-        float x[kNormPasses][8], g[kNormPasses][8];
+    for (unsigned blk = blockIdx.x; blk < nblocks; blk += gridDim.x) {
+        const unsigned row0 = blk * B::RB;
+        Raw8<TX> xr[kNormPasses];
+        Raw8<TY> gr[kNormPasses];
         NormRow rw[kNormPasses];
 #pragma unroll
         for (int i = 0; i < kNormPasses; ++i) {
             rw[i] = norm_row(p, row0 + i * B::RPP + grp, nrows);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][e] = g[i][e] = 0.f;
+            xr[i].zero();
+            gr[i].zero();
             if (rw[i].ok && lane_in) {
-                const long o = rw[i].key ? rw[i].token * p.k_token + rw[i].head * p.k_head
-                                         : rw[i].token * p.q_token + rw[i].head * p.q_head;
-                load8(static_cast<const TX*>(rw[i].key ? p.k : p.q) + o + 8 * l, x[i]);
-                const long od = rw[i].key ? (rw[i].token * p.hk + rw[i].head) * p.d : (rw[i].token * p.hq + rw[i].head) * p.d;
-                load8(static_cast<const TY*>(rw[i].key ? p.dk_in : p.dq_in) + od + 8 * l, g[i]);
+                xr[i].load(static_cast<const TX*>(rw[i].key ? p.k : p.q) + row_in(p, rw[i]) + 8 * l);
+                gr[i].load(static_cast<const TY*>(rw[i].key ? p.dk_in : p.dq_in) + row_dense(p, rw[i]) + 8 * l);
             }
         }
-        long tok0 = 0;
+        int tok0 = 0;
         if constexpr (ROPE != ROPE_NONE) {
-            const unsigned ht = p.hq + p.hk;
-            const long last = (row0 + B::RB < nrows ? row0 + B::RB : nrows) - 1;
-            tok0 = row0 / ht;
+            const unsigned ht = p.hq + p.hk, last = min(row0 + B::RB, nrows) - 1;
+            tok0 = (int)(row0 / ht);
             if (DW) __syncthreads();   // the previous block is done with the angles
-            fill_angles<G>(p, cs, tok0, (int)(last / ht - tok0) + 1, tid);
+            fill_angles<G>(p, cs, tok0, (int)(last / ht) - tok0 + 1, tid);
             __syncthreads();
         }
 #pragma unroll
         for (int i = 0; i < kNormPasses; ++i) {
+            float x[8], g[8];
+            xr[i].get(x);
+            gr[i].get(g);
             const float scale = rw[i].key ? 1.f : p.q_scale;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[i][e] *= scale;
+            for (int e = 0; e < 8; ++e) g[e] *= scale;
             if constexpr (ROPE != ROPE_NONE)
-                rotate8<ROPE, true>(g[i], cs + (rw[i].ok ? (rw[i].token - tok0) : 0) * B::PAIRS, l, p.rot);
+                rotate8<ROPE, true>(g, cs + (rw[i].ok ? (rw[i].token - tok0) : 0) * B::PAIRS, l, p.rot);
             float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss += x[i][e] * x[i][e];
+            for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
             ss = row_sum<G>(ss);
             const float r = 1.f / sqrtf(ss * p.inv_n + p.eps);
             const float* w = rw[i].key ? p.k_weight : p.q_weight;
             float c = 0.f, wv[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) wv[e] = 1.f;
-            if (w && lane_in) load8(w + 8 * l, wv);
+            if (w && lane_in) {
+                Raw8<float> wr;
+                wr.load(w + 8 * l);
+                wr.get(wv);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                x[i][e] *= r;
+                x[e] *= r;
                 if constexpr (DW) {   // rows past the end hold zeros
-                    const float t = x[i][e] * g[i][e];
+                    const float t = x[e] * g[e];
                     aq[e] += rw[i].key ? 0.f : t;
                     ak[e] += rw[i].key ? t : 0.f;
                 }
-                g[i][e] *= wv[e];
-                c += g[i][e] * x[i][e];
+                g[e] *= wv[e];
+                c += g[e] * x[e];
             }
             c = row_sum<G>(c) * p.inv_n;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[i][e] = r * (g[i][e] - x[i][e] * c);
+            for (int e = 0; e < 8; ++e) g[e] = r * (g[e] - x[e] * c);
             if (rw[i].ok && lane_in) {
                 const long o = rw[i].key ? rw[i].token * p.dk_token + rw[i].head * p.dk_head
                                          : rw[i].token * p.dq_token + rw[i].head * p.dq_head;
-                store8(static_cast<TX*>(rw[i].key ? p.dk_out : p.dq_out) + o + 8 * l, g[i]);
+                store8(static_cast<TX*>(rw[i].key ? p.dk_out : p.dq_out) + o + 8 * l, g);
             }
         }
     }

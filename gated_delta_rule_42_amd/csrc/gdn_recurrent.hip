@@ -21,11 +21,19 @@ __device__ __forceinline__ f32x4_t in4(const uint16_t* p) {
 
 // One work-group per (sequence, value head, tile of 16 RPG state rows): 16 groups of 16 lanes, RPG rows each. Lane l16
 // owns the columns 4 l16 + 0..3 of each 64-column half of a row, so that the state's loads and stores cover whole
-// 256-byte runs. The next token's operands are loaded while the current one is computed.
-template <typename TS, typename TO, int DK, int DV, int RPG, bool CW>
+// 256-byte runs. Where sequences have about one token each (RUNS false) its operands go straight to registers, which leaves
+// room for more waves. Longer runs take their tokens in blocks of TB through
+// LDS: the next block's loads are in flight while the current one is computed, and what all 16 groups need (the decay,
+// k . q) is computed once per work-group.
+template <typename TS, typename TO, int DK, int DV, int RPG, bool CW, bool RUNS>
 __global__ __launch_bounds__(256) void recurrent_kernel(RecurrentProblem p) {
-    constexpr int EPL = DK / 16, NH = EPL / 4;   // state columns per lane, in runs of four
+    constexpr int NH = DK / 64;                  // a lane's runs of four columns
     constexpr int TILES = DV / (16 * RPG);
+    constexpr int TB = 1024 / DK;                // tokens per block: four channels per thread
+    constexpr int NVB = TB * 16 * RPG / 256 > 0 ? TB * 16 * RPG / 256 : 1;   // value rows per thread and block
+    constexpr int LB = RUNS ? TB : 1;
+    __shared__ float sk[LB][DK], sq[LB][DK], sa[CW ? LB : 1][DK], sv[LB][16 * RPG];
+    __shared__ float4 sc[LB];                    // alpha (scalar gate), beta, k . q
     const int tid = threadIdx.x, l16 = tid & 15, grp = tid >> 4;
     const long unit = blockIdx.x / TILES;
     const int tile = (int)(blockIdx.x % TILES);
@@ -38,12 +46,13 @@ __global__ __launch_bounds__(256) void recurrent_kernel(RecurrentProblem p) {
     if (t0 >= t1) return;
     const int slot = p.slots[n];
     const int row0 = tile * 16 * RPG + grp;
+    const long otok = (long)p.HV * DV;
     TO* op = static_cast<TO*>(p.o) + (long)hv * DV + row0;
     if (slot < 0 || slot >= p.n_slots) {   // a padded entry: zeros for its tokens, no state touched
         if (l16 == 0)
             for (int t = t0; t < t1; ++t)
 #pragma unroll
-                for (int r = 0; r < RPG; ++r) op[(long)t * p.HV * DV + 16 * r] = from_f32<TO>(0.f);
+                for (int r = 0; r < RPG; ++r) op[t * otok + 16 * r] = from_f32<TO>(0.f);
         return;
     }
     const long srow = (long)hv * DV + row0;   // row within a slot
@@ -55,94 +64,154 @@ __global__ __launch_bounds__(256) void recurrent_kernel(RecurrentProblem p) {
 #pragma unroll
         for (int e = 0; e < NH; ++e)
             s[r][e] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(st + (long)16 * r * DK + 64 * e));
-
-    struct Token {
-        f32x4_t q[NH], k[NH], g[CW ? NH : 1];
-        float v[RPG], g1, beta;
-    };
-    auto load = [&](Token& x, int t) {
-        const TS* qp = static_cast<const TS*>(p.q) + t * p.q_token + h * DK + 4 * l16;
-        const TS* kp = static_cast<const TS*>(p.k) + t * p.k_token + h * DK + 4 * l16;
-        const TS* vp = static_cast<const TS*>(p.v) + t * p.v_token + hv * DV + row0;
-        const long gi = (long)t * p.HV + hv;
-#pragma unroll
-        for (int e = 0; e < NH; ++e) {
-            x.q[e] = in4(qp + 64 * e);
-            x.k[e] = in4(kp + 64 * e);
-            if constexpr (CW) x.g[e] = *reinterpret_cast<const f32x4_t*>(p.g + gi * DK + 64 * e + 4 * l16);
-        }
-        if constexpr (!CW) x.g1 = p.g[gi];
-        x.beta = p.beta[gi];
-#pragma unroll
-        for (int r = 0; r < RPG; ++r) x.v[r] = to_f32(vp[16 * r]);
-    };
-    Token cur, nxt;
-    load(cur, t0);
-    for (int t = t0; t < t1; ++t) {
-        if (t + 1 < t1) load(nxt, t + 1);
-        f32x4_t a[NH];
-        float kq = 0.f;
-#pragma unroll
-        for (int e = 0; e < NH; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[e][i] = CW ? __expf(cur.g[CW ? e : 0][i]) : 0.f;
-                kq += cur.k[e][i] * cur.q[e][i];
-            }
-        kq = row16_sum(kq);
-        const float a1 = CW ? 1.f : __expf(cur.g1);
-#pragma unroll
-        for (int r = 0; r < RPG; ++r) {
-            float sk = 0.f, sq = 0.f;
-#pragma unroll
-            for (int e = 0; e < NH; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[r][e][i] *= CW ? a[e][i] : a1;
-                    sk += s[r][e][i] * cur.k[e][i];
-                    sq += s[r][e][i] * cur.q[e][i];
-                }
-            sk = row16_sum(sk);
-            sq = row16_sum(sq);
-            const float c = cur.beta * (cur.v[r] - sk);
-#pragma unroll
-            for (int e = 0; e < NH; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[r][e][i] += c * cur.k[e][i];
-            if (l16 == 0) op[(long)t * p.HV * DV + 16 * r] = from_f32<TO>(sq + c * kq);
-        }
-        const int to = p.out_slots ? p.out_slots[t] : -1;
-        if (to >= 0 && to < p.n_slots) {
-            float* dst = p.states + (to * slot_size + srow) * DK + 4 * l16;
-#pragma unroll
-            for (int r = 0; r < RPG; ++r)
-#pragma unroll
-                for (int e = 0; e < NH; ++e)
-                    __builtin_nontemporal_store(s[r][e], reinterpret_cast<f32x4_t*>(dst + (long)16 * r * DK + 64 * e));
-        }
-        cur = nxt;
-    }
-    if (!p.out_slots) {
+    auto put = [&](float* dst) {
 #pragma unroll
         for (int r = 0; r < RPG; ++r)
 #pragma unroll
             for (int e = 0; e < NH; ++e)
-                __builtin_nontemporal_store(s[r][e], reinterpret_cast<f32x4_t*>(st + (long)16 * r * DK + 64 * e));
+                __builtin_nontemporal_store(s[r][e], reinterpret_cast<f32x4_t*>(dst + (long)16 * r * DK + 64 * e));
+    };
+    const TS* qp = static_cast<const TS*>(p.q) + h * DK;
+    const TS* kp = static_cast<const TS*>(p.k) + h * DK;
+    const TS* vp = static_cast<const TS*>(p.v) + (long)hv * DV + tile * 16 * RPG;
+
+    struct Token {
+        f32x4_t q[NH], k[NH], a[NH];   // a: the decay of the lane's columns
+        float v[RPG], beta, kq;
+    };
+    auto step = [&](const Token& x, int t) {
+#pragma unroll
+        for (int r = 0; r < RPG; ++r) {
+            float dk = 0.f, dq = 0.f;
+#pragma unroll
+            for (int e = 0; e < NH; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[r][e][i] *= x.a[e][i];
+                    dk += s[r][e][i] * x.k[e][i];
+                    dq += s[r][e][i] * x.q[e][i];
+                }
+            dk = row16_sum(dk);
+            dq = row16_sum(dq);
+            const float c = x.beta * (x.v[r] - dk);
+#pragma unroll
+            for (int e = 0; e < NH; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[r][e][i] += c * x.k[e][i];
+            if (l16 == 0) op[t * otok + 16 * r] = from_f32<TO>(dq + c * x.kq);
+        }
+        if (p.out_slots) {
+            const int to = p.out_slots[t];
+            if (to >= 0 && to < p.n_slots) put(p.states + (to * slot_size + srow) * DK + 4 * l16);
+        }
+    };
+
+    if constexpr (!RUNS) {
+        for (int t = t0; t < t1; ++t) {
+            Token x;
+            const long gi = (long)t * p.HV + hv;
+            x.kq = 0.f;
+#pragma unroll
+            for (int e = 0; e < NH; ++e) {
+                x.q[e] = in4(qp + t * p.q_token + 64 * e + 4 * l16);
+                x.k[e] = in4(kp + t * p.k_token + 64 * e + 4 * l16);
+                if constexpr (CW) x.a[e] = *reinterpret_cast<const f32x4_t*>(p.g + gi * DK + 64 * e + 4 * l16);
+            }
+            const float g1 = CW ? 0.f : p.g[gi];
+            x.beta = p.beta[gi];
+#pragma unroll
+            for (int r = 0; r < RPG; ++r) x.v[r] = to_f32(vp[t * p.v_token + grp + 16 * r]);
+            const float a1 = __expf(g1);
+#pragma unroll
+            for (int e = 0; e < NH; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x.a[e][i] = CW ? __expf(x.a[e][i]) : a1;
+                    x.kq += x.k[e][i] * x.q[e][i];
+                }
+            x.kq = row16_sum(x.kq);
+            step(x, t);
+        }
+    } else {
+        // thread's share of a block: four channels of token tid / (DK / 4), one or more values, a token's scalars;
+        // tokens past the run's end are the last one again (not used)
+        const int bt = tid / (DK / 4), bc = 4 * (tid % (DK / 4));
+        f32x4_t fq, fk, fa;
+        float fv[NVB], fg = 0.f, fb = 0.f;
+        auto fetch = [&](int t) {
+            const int tt = min(t + bt, t1 - 1);
+            const long gi = (long)tt * p.HV + hv;
+            fq = in4(qp + tt * p.q_token + bc);
+            fk = in4(kp + tt * p.k_token + bc);
+            if constexpr (CW) fa = *reinterpret_cast<const f32x4_t*>(p.g + gi * DK + bc);
+            else fg = p.g[gi];
+            fb = p.beta[gi];
+#pragma unroll
+            for (int i = 0; i < NVB; ++i) {
+                const int x = (tid + 256 * i) % (TB * 16 * RPG);
+                fv[i] = to_f32(vp[min(t + x / (16 * RPG), t1 - 1) * p.v_token + x % (16 * RPG)]);
+            }
+        };
+        fetch(t0);
+        for (int tb = t0; tb < t1; tb += TB) {
+            __syncthreads();   // the previous block is done with LDS
+            *reinterpret_cast<f32x4_t*>(&sk[bt][bc]) = fk;
+            *reinterpret_cast<f32x4_t*>(&sq[bt][bc]) = fq;
+            if constexpr (CW)
+                *reinterpret_cast<f32x4_t*>(&sa[bt][bc]) = f32x4_t{__expf(fa[0]), __expf(fa[1]), __expf(fa[2]), __expf(fa[3])};
+            float kq = row16_sum(fk[0] * fq[0] + fk[1] * fq[1] + fk[2] * fq[2] + fk[3] * fq[3]);
+            if constexpr (DK == 128) kq += __shfl_xor(kq, 16, 64);
+            if (bc == 0) sc[bt] = make_float4(__expf(fg), fb, kq, 0.f);
+#pragma unroll
+            for (int i = 0; i < NVB; ++i) {
+                const int x = (tid + 256 * i) % (TB * 16 * RPG);   // threads past the block write a value again
+                sv[x / (16 * RPG)][x % (16 * RPG)] = fv[i];
+            }
+            __syncthreads();
+            if (tb + TB < t1) fetch(tb + TB);
+            auto get = [&](Token& x, int i) {
+                const float4 c = sc[i];
+#pragma unroll
+                for (int e = 0; e < NH; ++e) {
+                    x.k[e] = *reinterpret_cast<const f32x4_t*>(&sk[i][64 * e + 4 * l16]);
+                    x.q[e] = *reinterpret_cast<const f32x4_t*>(&sq[i][64 * e + 4 * l16]);
+                    if constexpr (CW) x.a[e] = *reinterpret_cast<const f32x4_t*>(&sa[i][64 * e + 4 * l16]);
+                    else x.a[e] = f32x4_t{c.x, c.x, c.x, c.x};
+                }
+                x.beta = c.y;
+                x.kq = c.z;
+#pragma unroll
+                for (int r = 0; r < RPG; ++r) x.v[r] = sv[i][grp + 16 * r];
+            };
+            const int nt = min(TB, t1 - tb);
+            Token x, y;
+            get(x, 0);
+            for (int i = 0; i < nt; i += 2) {
+                get(y, min(i + 1, TB - 1));
+                step(x, tb + i);
+                if (i + 1 < nt) {
+                    get(x, min(i + 2, TB - 1));
+                    step(y, tb + i + 1);
+                }
+            }
+        }
     }
+    if (!p.out_slots) put(st);
 }
 
-template <typename TS, typename TO, int DK, int DV, int RPG>
+template <typename TS, typename TO, int DK, int DV, int RPG, bool RUNS>
 static hipError_t recurrent_gate(const RecurrentProblem& p, hipStream_t s) {
     const dim3 grid((unsigned)((long)p.N * p.HV * (DV / (16 * RPG))));
-    return p.channel_gate ? launch(recurrent_kernel<TS, TO, DK, DV, RPG, true>, grid, dim3(256), s, p)
-                          : launch(recurrent_kernel<TS, TO, DK, DV, RPG, false>, grid, dim3(256), s, p);
+    return p.channel_gate ? launch(recurrent_kernel<TS, TO, DK, DV, RPG, true, RUNS>, grid, dim3(256), s, p)
+                          : launch(recurrent_kernel<TS, TO, DK, DV, RPG, false, RUNS>, grid, dim3(256), s, p);
 }
 
 template <typename TS, typename TO, int DK, int DV>
 static hipError_t recurrent_rows(const RecurrentProblem& p, hipStream_t s) {
-    const long units = (long)p.N * p.HV;
-    if (units * (DV / 64) >= 2048) return recurrent_gate<TS, TO, DK, DV, 4>(p, s);
-    return recurrent_gate<TS, TO, DK, DV, 1>(p, s);
+    const bool runs = p.T > p.N + p.N / 4;
+    const bool wide = (long)p.N * p.HV * (DV / 64) >= 2048;
+    if (runs) return wide ? recurrent_gate<TS, TO, DK, DV, 4, true>(p, s) : recurrent_gate<TS, TO, DK, DV, 1, true>(p, s);
+    return wide ? recurrent_gate<TS, TO, DK, DV, 4, false>(p, s) : recurrent_gate<TS, TO, DK, DV, 1, false>(p, s);
 }
 
 template <typename TS, typename TO>
