@@ -206,12 +206,19 @@ static hipError_t recurrent_gate(const RecurrentProblem& p, hipStream_t s) {
                           : launch(recurrent_kernel<TS, TO, DK, DV, RPG, false, RUNS>, grid, dim3(256), s, p);
 }
 
+// One row per group streams single tokens fastest at every size (256 sequences x 32 heads of 128 x 128: 179 us, 5.9 TB/s,
+// against 185 with two and 196 with four rows; 32 sequences: 24.7, 25.1, 25.4). Runs are bound by vector instructions once
+// there are enough of them; more rows then share a token's operands. Work-groups of one row per group: 1,024 (4 runs of 16
+// tokens, 32 heads) 10.0 us with one row, 10.8 with two; 16,384 (64 runs of 8) 69 with one, 65 with two, 68 with four;
+// 65,536 (256 runs of 4, channel-wise) 237, 210, 190.
 template <typename TS, typename TO, int DK, int DV>
 static hipError_t recurrent_rows(const RecurrentProblem& p, hipStream_t s) {
     const bool runs = p.T > p.N + p.N / 4;
-    const bool wide = (long)p.N * p.HV * (DV / 64) >= 2048;
-    if (runs) return wide ? recurrent_gate<TS, TO, DK, DV, 4, true>(p, s) : recurrent_gate<TS, TO, DK, DV, 1, true>(p, s);
-    return wide ? recurrent_gate<TS, TO, DK, DV, 4, false>(p, s) : recurrent_gate<TS, TO, DK, DV, 1, false>(p, s);
+    const long groups = (long)p.N * p.HV * (DV / 16);
+    if (!runs) return recurrent_gate<TS, TO, DK, DV, 1, false>(p, s);
+    if (groups >= 32768) return recurrent_gate<TS, TO, DK, DV, 4, true>(p, s);
+    if (groups >= 8192) return recurrent_gate<TS, TO, DK, DV, 2, true>(p, s);
+    return recurrent_gate<TS, TO, DK, DV, 1, true>(p, s);
 }
 
 template <typename TS, typename TO>
