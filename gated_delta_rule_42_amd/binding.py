@@ -380,6 +380,10 @@ def _same_gpu(device, **ts):
             raise ValueError(f"gdn: {name} is on {t.device}, expected {device}")
 
 
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _dense(**ts):
     for name, t in ts.items():
         if t is not None and not t.is_contiguous():
@@ -470,8 +474,8 @@ def gdn_recurrent_fwd(q, k, v, g, beta, states, slots, cu_seqlens=None, out_slot
     if o is None:
         o = torch.empty((T, HV, dv), dtype=o_dtype, device=q.device)
         made = (o,)
-    _call("gdn_recurrent_fwd", q.device, stream, made, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(states),
-          _ptr(slots), _ptr(cu_seqlens), _ptr(out_slots), _ptr(o), T, N, H, HV, dk, dv, states.shape[0], *strides,
+    _call("gdn_recurrent_fwd", q.device, stream, made, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(states),
+          _adr(slots), _adr(cu_seqlens), _adr(out_slots), _adr(o), T, N, H, HV, dk, dv, states.shape[0], *strides,
           int(channels), _DTYPE.get(q.dtype, -1), _DTYPE.get(o.dtype, -1))
     return o
 
@@ -534,8 +538,8 @@ def gdn_qk_norm_fwd(q, k, q_weight=None, k_weight=None, *, positions=None, inv_f
         made.append(k_out)
     _same_gpu(q.device, q_out=q_out, k_out=k_out)
     _dense(q_out=q_out, k_out=k_out)
-    _call("gdn_qk_norm_fwd", q.device, stream, made, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-          _ptr(inv_freq), _ptr(q_out), _ptr(k_out), tokens, hq, hk, d, *qs, *ks, _NORM[norm], eps, rot, _ROPE[layout],
+    _call("gdn_qk_norm_fwd", q.device, stream, made, _adr(q), _adr(k), _adr(q_weight), _adr(k_weight), _adr(positions),
+          _adr(inv_freq), _adr(q_out), _adr(k_out), tokens, hq, hk, d, *qs, *ks, _NORM[norm], eps, rot, _ROPE[layout],
           q_scale, rope_scale, _DTYPE.get(q.dtype, -1), _DTYPE.get(od, -1))
     return q_out, k_out
 
@@ -577,10 +581,10 @@ def gdn_qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, *, posit
     _same_gpu(q.device, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk, workspace=workspace)
     _dense(dq_out=dq_out, dk_out=dk_out, workspace=workspace)
     strides = [s for t, name in ((q, "q"), (k, "k"), (dq, "dq"), (dk, "dk")) for s in _row_strides(t, name)]
-    _call("gdn_qk_norm_bwd", q.device, stream, made, _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight),
-          _ptr(k_weight), _ptr(positions), _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), tokens, hq, hk, d,
+    _call("gdn_qk_norm_bwd", q.device, stream, made, _adr(q), _adr(k), _adr(dq_out), _adr(dk_out), _adr(q_weight),
+          _adr(k_weight), _adr(positions), _adr(inv_freq), _adr(dq), _adr(dk), _adr(dqw), _adr(dkw), tokens, hq, hk, d,
           *strides, _NORM[norm], eps, rot, _ROPE[layout], q_scale, rope_scale, _DTYPE.get(q.dtype, -1),
-          _DTYPE.get(dq_out.dtype, -1), _ptr(workspace),
+          _DTYPE.get(dq_out.dtype, -1), _adr(workspace),
           workspace.numel() * workspace.element_size() if workspace is not None else 0)
     return dq, dk, dqw, dkw
 
@@ -611,8 +615,8 @@ def gdn_kda_chunk_bwd(q, k, v, g, beta, do, h0=None, dhT=None, cu_seqlens=None, 
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         made.append(workspace)
-    _call("gdn_kda_chunk_bwd", dev, stream, made, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(do),
-          _ptr(dhT), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dg), _ptr(db), _ptr(dh0), _ptr(cu_seqlens), chunk, B, T, H, dk,
-          dv, N, _DTYPE.get(q.dtype, -1), _DTYPE.get(gd, -1), _ptr(workspace),
+    _call("gdn_kda_chunk_bwd", dev, stream, made, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(do),
+          _adr(dhT), _adr(dq), _adr(dk_), _adr(dv_), _adr(dg), _adr(db), _adr(dh0), _adr(cu_seqlens), chunk, B, T, H, dk,
+          dv, N, _DTYPE.get(q.dtype, -1), _DTYPE.get(gd, -1), _adr(workspace),
           workspace.numel() * workspace.element_size() if workspace is not None else 0)
     return dq, dk_, dv_, dg, db, dh0

@@ -414,8 +414,8 @@ GDN_EXPORT int gdn_kda_chunk_bwd(const void* q, const void* k, const void* v, co
         if (x && !aligned(x, 4)) return GDN_ERR_ALIGN;
     const gdn::KdaBwdLayout w = gdn::kda_bwd_workspace_layout(B, T, H, dk, dv, N, cu_seqlens != nullptr);
     if (w.fwd.nc_bound * H > 0x7fffffffL) return GDN_ERR_SHAPE;
-    // the walks: a work-group of 256 threads per (sequence, head, 32 columns), fewer than 2^32 threads in all
-    if ((long long)N * H >= 1 << 21) return GDN_ERR_SHAPE;
+    // work-groups of 256 threads per (sequence, head, 32 columns) and (chunk, head, 64 channels), fewer than 2^32 threads
+    if ((long long)N * H >= 1 << 21 || (long long)w.fwd.nc_bound * H >= 1 << 23) return GDN_ERR_SHAPE;
     if (w.total > 0 && (!workspace || workspace_bytes < w.total)) return GDN_ERR_WORKSPACE;
     if (workspace && !aligned(workspace, 256)) return GDN_ERR_ALIGN;
     char* base = static_cast<char*>(workspace);
@@ -541,7 +541,7 @@ int check_norm(const void* q, const void* k, const float* q_weight, const float*
     if (rot < 0 || rot > d || rot % (rope == GDN_ROPE_HALF ? 16 : 2)) return GDN_ERR_UNSUPPORTED;
     if (tokens < 0 || hq < 1 || hk < 1 || hq > 32768 || hk > 32768) return GDN_ERR_SHAPE;
     if (!(eps > 0.f)) return GDN_ERR_SHAPE;
-    // work-groups of 256 threads on 32 rows or more, fewer than 2^32 threads in all
+    // rows are counted in 32 bits, and a large call's work-groups of 256 threads take 32 rows or more: fewer than 2^32 threads
     if ((long long)tokens * (hq + hk) > (1LL << 28)) return GDN_ERR_SHAPE;
     const int64_t strides[] = {q_token, q_head, k_token, k_head};
     for (int64_t x : strides)

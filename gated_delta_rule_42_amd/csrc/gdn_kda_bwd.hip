@@ -414,6 +414,10 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
         f32x4_t dO[4], X[4];
         __syncthreads();   // the chunk's operands are in LDS
         TokenCols<TIn, DV>::get(own, dO, lane);
+        if constexpr (DK == 128) {   // the chunk gradients add their halves to it
+            const int len = (int)min(64L, c.seos - (c.sbos + jc * 64));
+            if (c.tile == 0 && tid < len) b.dbeta[(c.sbos + jc * 64 + tid) * H + c.h] = 0.f;
+        }
         // this wave's share of dD = Kd dS'^T + P^T dO: its half of the channels, and of the row tiles of P^T dO ({3, 0}, {2, 1})
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -474,23 +478,25 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
 }
 
 // ------------------------------------------------------------------- gradients of each chunk
-// One work-group per (chunk, head), a wave per 16 channels (c0 = 16 wave). Two register layouts of a wave's
-// [64 rows, 16 channels]: the accumulator layout (rows 16 t + 4 lq + m) of the products, and the block layout (lane
-// (lq, l16) has rows 16 lq .. 16 lq + 15 of channel c0 + l16), in which gamma is scanned, the pairs inside a block are
-// summed and the gradients are formed. An accumulator goes to the block layout through a private LDS tile.
-template <int DV, int NW>
+// One work-group of four waves per (chunk, head, 64 of the d_k channels), a wave per 16 channels; two work-groups fit a CU, so that
+// one's loads and vector work hide behind the other's products (one of eight waves for all 128 channels, alone on its CU:
+// 395 us for the training shape, of which the matrix cores were busy for 146). D, Y and dO pass through LDS in
+// slices of 32 columns, the next one's loads in flight. Two register layouts of a wave's [64 rows, 16 channels]: the accumulator layout
+// (rows 16 t + 4 lq + m) of the products, and the block layout (lane (lq, l16) has rows 16 lq .. 16 lq + 15 of its
+// channel), in which gamma is scanned, the pairs inside a block are summed and the gradients are formed. An accumulator
+// goes to the block layout through a private LDS tile.
 struct alignas(16) KdaGradSmem {
-    static constexpr int PV = DV + 4, PC = 68, PT = 17;
+    static constexpr int PV = 36, PC = 68, PT = 17;
     union {
         struct { float D[64 * PV], Y[64 * PV], dO[64 * PV]; } in;
-        float turn[NW][64 * PT];
-        float out[3][64 * 16 * NW];   // dq, dk, dg on their way out (see out_at)
+        float turn[4][64 * PT];
+        float out[2][64 * 64];        // gradients on their way out (see out_at)
     };
     float dP[64 * PC];                // see tri_at
     float dA[64 * PC];
     float beta[64];
     float yv[64];
-    float part[NW][64];
+    float part[4][64];
 };
 
 // Element (r, i) of dP and dA. They are read by rows (pieces of one row), by columns (16 columns of the row s of all four
@@ -513,302 +519,332 @@ __device__ __forceinline__ void wave_lds_fence() {
 }
 
 template <typename TIn, typename TG, int DK, int DV>
-__global__ __launch_bounds__(DK * 4) void kda_bwd_grad_kernel(KdaBwdProblem b) {
-    constexpr int NW = DK / 16, NT = 64 * NW;
-    using SM = KdaGradSmem<DV, NW>;
-    constexpr int PV = SM::PV, PC = SM::PC, PT = SM::PT, NU = DV / 16;
+__global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
+    using SM = KdaGradSmem;
+    constexpr int PV = SM::PV, PC = SM::PC, PT = SM::PT, NH = DK / 64, NS = DV / 32, EB = (int)sizeof(TIn);
     __shared__ SM sm;
     const ChunkProblem& p = b.f;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, lq = lane >> 4;
-    const int H = p.H, ch = 16 * wave + l16;
-    const long unit = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int H = p.H;
+    // the channel halves of a unit read the same D, Y, dO: eight work-groups apart, on one XCD (see chain_of)
+    const long blk = blockIdx.x, full = (gridDim.x / (8 * NH)) * (8 * NH);
+    const long unit = blk < full ? blk / (8 * NH) * 8 + blk % 8 : blk / NH;
+    const int half = (int)(blk < full ? blk / 8 % NH : blk % NH);
+    const int c0 = 64 * half, ch = c0 + 16 * wave + l16;
     long bos;
     int len;
     if (!locate_chunk(p, unit / H, bos, len)) return;   // packed: past the last chunk
     const int h = (int)(unit % H);
+
+    // a slice's pieces of four columns (two per thread), raw; inputs through resources that end at the chunk's last token
+    const long vb = (bos * H + h) * DV;
+    const unsigned vrows = (unsigned)((len - 1) * H * DV + DV);
+    const auto gres = make_rsrc(static_cast<const TIn*>(b.d_o) + vb, vrows * EB);
+    const auto vres = make_rsrc(static_cast<const TIn*>(p.v) + vb, vrows * EB);
+    f32x4_t dpc[2], ypc[2];
+    u32x4_t gpc[2], vpc[2];
+    float sn[8], dn[8];   // the lane's rows 32 sl + 16 u + 4 lq + e of S and dS'
+    const float* sp = p.states + unit * DV * DK + ch;
+    const float* dp = b.dstates + unit * DV * DK + ch;
+    auto piece = [](__amdgpu_buffer_rsrc_t r, int o) {
+        if constexpr (EB == 2) {
+            const u32x2_t x = __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, 0);
+            return u32x4_t{x[0], x[1], 0u, 0u};
+        } else {
+            return __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0);
+        }
+    };
+    auto load = [&](int sl) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int i = tid + 256 * n, r = i / 8, cc = 32 * sl + 4 * (i % 8);
+            dpc[n] = *reinterpret_cast<const f32x4_t*>(b.delta + (unit * 64 + r) * DV + cc);
+            ypc[n] = *reinterpret_cast<const f32x4_t*>(b.ymat + (unit * 64 + r) * DV + cc);
+            gpc[n] = piece(gres, (r * H * DV + cc) * EB);
+            vpc[n] = piece(vres, (r * H * DV + cc) * EB);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sn[4 * u + e] = sp[(32 * sl + 16 * u + 4 * lq + e) * DK];
+                dn[4 * u + e] = dp[(32 * sl + 16 * u + 4 * lq + e) * DK];
+            }
+    };
+    load(0);
+    // k, q, g of the lane's rows and channel
+    float k[16], q[16], gm[16];
+    const long base = (bos * H + h) * DK;
     {
-        // D, Y, dO and V, then q, k, g of the lane's rows and channel, all issued before the first is used; inputs
-        // through resources that end at the chunk's last token
-        constexpr int NP = 64 * DV / 4 / NT;   // pieces of four per thread
-        constexpr int EB = (int)sizeof(TIn);
-        f32x4_t dpc[NP], ypc[NP];
-        u32x4_t gpc[NP], vpc[NP];
-        float bpc[NP];
-        const float bt = p.beta[(bos + min(tid & 63, len - 1)) * H + h];
-        {
-            const long vb = (bos * H + h) * DV;
-            const unsigned rows = (unsigned)((len - 1) * H * DV + DV);
-            const auto gr = make_rsrc(static_cast<const TIn*>(b.d_o) + vb, rows * EB);
-            const auto vr = make_rsrc(static_cast<const TIn*>(p.v) + vb, rows * EB);
-            const auto br = make_rsrc(p.beta + bos * H + h, (unsigned)(((len - 1) * H + 1) * 4));
+        const unsigned rows = (unsigned)((len - 1) * H * DK + DK);
+        const auto kr = make_rsrc(static_cast<const TIn*>(p.k) + base, rows * EB);
+        const auto qr = make_rsrc(static_cast<const TIn*>(p.q) + base, rows * EB);
+        const auto gr = make_rsrc(p.g + base, rows * 4);
+        const int o0 = 16 * lq * H * DK + ch;
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                const int i = tid + NT * n, r = i / (DV / 4), cc = 4 * (i % (DV / 4)), o = (r * H * DV + cc) * EB;
-                dpc[n] = *reinterpret_cast<const f32x4_t*>(b.delta + (unit * 64 + r) * DV + cc);
-                ypc[n] = *reinterpret_cast<const f32x4_t*>(b.ymat + (unit * 64 + r) * DV + cc);
-                if constexpr (EB == 2) {
-                    const u32x2_t g2 = __builtin_amdgcn_raw_buffer_load_b64(gr, o, 0, 0), v2 = __builtin_amdgcn_raw_buffer_load_b64(vr, o, 0, 0);
-                    gpc[n] = u32x4_t{g2[0], g2[1], 0u, 0u};
-                    vpc[n] = u32x4_t{v2[0], v2[1], 0u, 0u};
-                } else {
-                    gpc[n] = __builtin_amdgcn_raw_buffer_load_b128(gr, o, 0, 0);
-                    vpc[n] = __builtin_amdgcn_raw_buffer_load_b128(vr, o, 0, 0);
-                }
-                bpc[n] = buf_in<float>(br, r * H * 4);
-            }
+        for (int r = 0; r < 16; ++r) {
+            const int o = o0 + r * H * DK;
+            k[r] = buf_in<TIn>(kr, o * EB);
+            q[r] = buf_in<TIn>(qr, o * EB);
+            gm[r] = buf_in<float>(gr, o * 4);
         }
-        float k[16], q[16], gm[16];
-        const long base = (bos * H + h) * DK;
-        {
-            const unsigned rows = (unsigned)((len - 1) * H * DK + DK);
-            const auto kr = make_rsrc(static_cast<const TIn*>(p.k) + base, rows * EB);
-            const auto qr = make_rsrc(static_cast<const TIn*>(p.q) + base, rows * EB);
-            const auto gr = make_rsrc(p.g + base, rows * 4);
-            const int o0 = 16 * lq * H * DK + ch;
+    }
+    float bt[2];   // beta of the thread's two piece rows
+    {
+        const auto br = make_rsrc(p.beta + bos * H + h, (unsigned)(((len - 1) * H + 1) * 4));
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int o = o0 + r * H * DK;
-                k[r] = buf_in<TIn>(kr, o * EB);
-                q[r] = buf_in<TIn>(qr, o * EB);
-                gm[r] = buf_in<float>(gr, o * 4);
-            }
-        }
-        pin();
-        // D, Y and dO into LDS; dV = beta Y and Y . V on the way (a row's DV / 4 threads are consecutive lanes)
-        auto widen = [](u32x4_t x) {
-            if constexpr (EB == 2) return make_float4(bf16_lo_half(x[0]), bf16_hi_half(x[0]), bf16_lo_half(x[1]), bf16_hi_half(x[1]));
-            else return __builtin_bit_cast(float4, x);
-        };
-        if (tid < 64) sm.beta[tid] = tid < len ? bt : 0.f;
+        for (int n = 0; n < 2; ++n) bt[n] = buf_in<float>(br, ((tid + 256 * n) / 8) * H * 4);
+        if (tid % 8 == 0) sm.beta[tid / 8] = bt[0], sm.beta[tid / 8 + 32] = bt[1];
+    }
+    auto widen = [](u32x4_t x) {
+        if constexpr (EB == 2) return f32x4_t{bf16_lo_half(x[0]), bf16_hi_half(x[0]), bf16_lo_half(x[1]), bf16_hi_half(x[1])};
+        else return __builtin_bit_cast(f32x4_t, x);
+    };
+
+    // dP = dO D^T and dA = -Y D^T (job w + 4 n: lower tile number job / 2, of dP or dA), dO S, Y S and D dS' on the
+    // wave's channels, colsum(S dS'), Y . V, all summed slice by slice; dV = beta Y on the way
+    f32x4_t aq[4], ay[4], ad[4], tri[5];
+    float sds = 0.f, yv[2] = {0.f, 0.f};
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            const int i = tid + NT * n, r = i / (DV / 4), cc = 4 * (i % (DV / 4));
-            const f32x4_t y = ypc[n];
-            const float4 v = widen(vpc[n]);
+    for (int t = 0; t < 4; ++t) aq[t] = ay[t] = ad[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < 5; ++n) tri[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto tile_row = [](int tile) { return tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3; };
+#pragma unroll 1
+    for (int sl = 0; sl < NS; ++sl) {
+        __syncthreads();   // the previous slice is dead
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int i = tid + 256 * n, r = i / 8, cc = 4 * (i % 8);
+            const f32x4_t y = ypc[n], v = widen(vpc[n]);
             *reinterpret_cast<f32x4_t*>(&sm.in.D[r * PV + cc]) = dpc[n];
             *reinterpret_cast<f32x4_t*>(&sm.in.Y[r * PV + cc]) = y;
-            *reinterpret_cast<float4*>(&sm.in.dO[r * PV + cc]) = widen(gpc[n]);
-            float yv = row16_sum(y[0] * v.x + y[1] * v.y + y[2] * v.z + y[3] * v.w);
-            if constexpr (DV == 128) yv += __shfl_xor(yv, 16, 64);
-            if (cc == 0) sm.yv[r] = yv;
-            if (r < len)
-                kb_out4(static_cast<TG*>(b.dv) + ((bos + r) * H + h) * DV + cc,
-                        make_float4(bpc[n] * y[0], bpc[n] * y[1], bpc[n] * y[2], bpc[n] * y[3]));
+            *reinterpret_cast<f32x4_t*>(&sm.in.dO[r * PV + cc]) = widen(gpc[n]);
+            yv[n] += y[0] * v[0] + y[1] * v[1] + y[2] * v[2] + y[3] * v[3];
+            if (half == 0 && r < len)
+                kb_out4(static_cast<TG*>(b.dv) + vb + (long)r * H * DV + 32 * sl + cc,
+                        make_float4(bt[n] * y[0], bt[n] * y[1], bt[n] * y[2], bt[n] * y[3]));
         }
+        float s[8], d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = sn[i], d[i] = dn[i], sds += s[i] * d[i];
         __syncthreads();
-
-        // dP and dA tile by tile (the ten lower tiles of each; zeros above)
-        for (int job = wave; job < 32; job += NW) {
-            const int I = job >> 3, J = (job >> 1) & 3;
-            const float* L = (job & 1) ? sm.in.Y : sm.in.dO;
-            float* out = (job & 1) ? sm.dA : sm.dP;
-            f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-            if (J <= I) {
+        load(min(sl + 1, NS - 1));   // the last slice again at the end
 #pragma unroll
-                for (int u = 0; u < NU; ++u) {
-                    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&L[(16 * I + l16) * PV + 16 * u + 4 * lq]);
-                    const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&sm.in.D[(16 * J + l16) * PV + 16 * u + 4 * lq]);
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc = mfma4(x[e], y[e], acc);
-                }
+            for (int n = 0; n < 5; ++n) {
+                const int job = wave + 4 * n, tile = job >> 1, I = tile_row(tile), J = tile - I * (I + 1) / 2;
+                const float* L = (job & 1) ? sm.in.Y : sm.in.dO;
+                const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&L[(16 * I + l16) * PV + 16 * u + 4 * lq]);
+                const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&sm.in.D[(16 * J + l16) * PV + 16 * u + 4 * lq]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tri[n] = mfma4(x[e], y[e], tri[n]);
             }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int r = 16 * I + 4 * lq + m, i = 16 * J + l16;
-                out[tri_at<PC>(r, i)] = (job & 1) ? (i < r ? -acc[m] : 0.f) : (i <= r ? acc[m] : 0.f);
-            }
-        }
-        // dO S, Y S and D dS' on the wave's channels; colsum(S dS')
-        f32x4_t aq[4], ay[4], ad[4];
-        float sds = 0.f;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) aq[t] = ay[t] = ad[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        {
-            const float* sp = p.states + unit * DV * DK + ch;
-            const float* dp = b.dstates + unit * DV * DK + ch;
-#pragma unroll 2
-            for (int u = 0; u < NU; ++u) {
-                float s[4], d[4];
+            for (int t = 0; t < 4; ++t) {
+                const int a = (16 * t + l16) * PV + 16 * u + 4 * lq;
+                const f32x4_t o = *reinterpret_cast<const f32x4_t*>(&sm.in.dO[a]);
+                const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&sm.in.Y[a]);
+                const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sm.in.D[a]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[e] = sp[(16 * u + 4 * lq + e) * DK];
-                    d[e] = dp[(16 * u + 4 * lq + e) * DK];
-                    sds += s[e] * d[e];
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int a = (16 * t + l16) * PV + 16 * u + 4 * lq;
-                    const f32x4_t o = *reinterpret_cast<const f32x4_t*>(&sm.in.dO[a]);
-                    const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&sm.in.Y[a]);
-                    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sm.in.D[a]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        aq[t] = mfma4(o[e], s[e], aq[t]);
-                        ay[t] = mfma4(y[e], s[e], ay[t]);
-                        ad[t] = mfma4(x[e], d[e], ad[t]);
-                    }
+                    aq[t] = mfma4(o[e], s[4 * u + e], aq[t]);
+                    ay[t] = mfma4(y[e], s[4 * u + e], ay[t]);
+                    ad[t] = mfma4(x[e], d[4 * u + e], ad[t]);
                 }
             }
-            sds += __shfl_xor(sds, 16, 64);
-            sds += __shfl_xor(sds, 32, 64);
         }
-        __syncthreads();   // dP and dA are whole; D, Y, dO are dead
-
-        // gamma of the lane's rows; a[r] = e^{g_r}, the decay from the row above
-        float a[16];
+    }
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            gm[r] = fmaxf(gm[r], kMinLogDecay);
-            a[r] = __expf(gm[r]);
-            if (r > 0) gm[r] += gm[r - 1];
+    for (int n = 0; n < 5; ++n) {
+        const int job = wave + 4 * n, tile = job >> 1, I = tile_row(tile), J = tile - I * (I + 1) / 2;
+        float* out = (job & 1) ? sm.dA : sm.dP;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int r = 16 * I + 4 * lq + m, i = 16 * J + l16;
+            out[tri_at<PC>(r, i)] = (job & 1) ? (i < r ? -tri[n][m] : 0.f) : (i <= r ? tri[n][m] : 0.f);
         }
-        {
-            const float t0 = __shfl(gm[15], l16, 64), t1 = __shfl(gm[15], 16 + l16, 64), t2 = __shfl(gm[15], 32 + l16, 64);
-            const float pre = (lq > 0 ? t0 : 0.f) + (lq > 1 ? t1 : 0.f) + (lq > 2 ? t2 : 0.f);
+    }
+    // zeros in the upper tiles (I, J) = (0, 1), (0, 2), (0, 3), (1, 2), (1, 3), (2, 3)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) gm[r] += pre;
-        }
-        float end[4];   // gamma at the last row of each block
+    for (int n = 0; n < 3; ++n) {
+        const int job = wave + 4 * n, tile = job >> 1, I = tile < 3 ? 0 : tile < 5 ? 1 : 2, J = tile < 3 ? tile + 1 : tile < 5 ? tile - 1 : 3;
+        float* out = (job & 1) ? sm.dA : sm.dP;
 #pragma unroll
-        for (int B = 0; B < 4; ++B) end[B] = __shfl(gm[15], 16 * B + l16, 64);
+        for (int m = 0; m < 4; ++m) out[tri_at<PC>(16 * I + 4 * lq + m, 16 * J + l16)] = 0.f;
+    }
+    sds += __shfl_xor(sds, 16, 64);
+    sds += __shfl_xor(sds, 32, 64);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {   // a row's eight pieces are consecutive lanes
+        float x = yv[n];
+        x += dpp_f32<0xB1>(x);
+        x += dpp_f32<0x4E>(x);
+        x += dpp_f32<0x141>(x);
+        if (tid % 8 == 0) sm.yv[tid / 8 + 32 * n] = x;
+    }
+    __syncthreads();   // dP and dA are whole; D, Y, dO are dead
 
-        float* turn = sm.turn[wave];
-        auto to_block = [&](const f32x4_t (&x)[4], float (&y)[16]) {
-            wave_lds_fence();
+    // gamma of the lane's rows; a[r] = e^{g_r}, the decay from the row above
+    float a[16];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+    for (int r = 0; r < 16; ++r) {
+        gm[r] = fmaxf(gm[r], kMinLogDecay);
+        a[r] = __expf(gm[r]);
+        if (r > 0) gm[r] += gm[r - 1];
+    }
+    {
+        const float t0 = __shfl(gm[15], l16, 64), t1 = __shfl(gm[15], 16 + l16, 64), t2 = __shfl(gm[15], 32 + l16, 64);
+        const float pre = (lq > 0 ? t0 : 0.f) + (lq > 1 ? t1 : 0.f) + (lq > 2 ? t2 : 0.f);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) turn[(16 * t + 4 * lq + m) * PT + l16] = x[t][m];
-            wave_lds_fence();
+        for (int r = 0; r < 16; ++r) gm[r] += pre;
+    }
+    float end[4];   // gamma at the last row of each block
 #pragma unroll
-            for (int r = 0; r < 16; ++r) y[r] = turn[(16 * lq + r) * PT + l16];
-        };
-        const float ref = lq == 0 ? 0.f : lq == 1 ? end[0] : lq == 2 ? end[1] : end[2];   // gamma before the lane's block
-        const float own = gm[15];
-        float dq[16], l[16], x[16], ar[16], w[16];
-        to_block(aq, w);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) dq[r] = __expf(gm[r]) * w[r];
-        to_block(ay, w);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) l[r] = -__expf(gm[r]) * w[r];
-        to_block(ad, w);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = __expf(end[3] - gm[r]) * w[r];
+    for (int B = 0; B < 4; ++B) end[B] = __shfl(gm[15], 16 * B + l16, 64);
 
-        // pairs of different blocks. Rows of block I against all rows before it, through gamma at the row before
-        // block I: step s takes row s of every block (lane lq its own), blocks I and later as zeros.
+    float* turn = sm.turn[wave];
+    auto to_block = [&](const f32x4_t (&x)[4], float (&y)[16]) {
+        wave_lds_fence();
 #pragma unroll
-        for (int t = 0; t < 4; ++t) aq[t] = ay[t] = ad[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int I = 1; I < 4; ++I)
+            for (int m = 0; m < 4; ++m) turn[(16 * t + 4 * lq + m) * PT + l16] = x[t][m];
+        wave_lds_fence();
 #pragma unroll
-            for (int s4 = 0; s4 < 4; ++s4) {
-                pin();
-                const int o = tri_at<PC>(16 * I + l16, 16 * lq + 4 * s4);
-                const f32x4_t vp = *reinterpret_cast<const f32x4_t*>(&sm.dP[o]);
-                const f32x4_t va = *reinterpret_cast<const f32x4_t*>(&sm.dA[o]);
+        for (int r = 0; r < 16; ++r) y[r] = turn[(16 * lq + r) * PT + l16];
+    };
+    const float ref = lq == 0 ? 0.f : lq == 1 ? end[0] : lq == 2 ? end[1] : end[2];   // gamma before the lane's block
+    const float own = gm[15];
+    float dq[16], l[16], x[16], ar[16], w[16];
+    to_block(aq, w);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int s = 4 * s4 + e;
-                    const float kb = lq < I ? k[s] * __expf(end[I - 1] - gm[s]) : 0.f;
-                    aq[I] = mfma4(vp[e], kb, aq[I]);
-                    ay[I] = mfma4(va[e], kb, ay[I]);
-                }
-            }
-        // Columns of block J against all rows behind it, through gamma at the block's last row.
+    for (int r = 0; r < 16; ++r) dq[r] = __expf(gm[r]) * w[r];
+    to_block(ay, w);
 #pragma unroll
-        for (int J = 0; J < 3; ++J)
+    for (int r = 0; r < 16; ++r) l[r] = -__expf(gm[r]) * w[r];
+    to_block(ad, w);
 #pragma unroll
-            for (int s = 0; s < 16; ++s) {
-                if (s % 4 == 0) pin();
-                const int o = tri_at<PC>(16 * lq + s, 16 * J + l16);
-                const float e = lq > J ? __expf(gm[s] - end[J]) : 0.f;
-                ad[J] = mfma4(sm.dP[o], q[s] * e, ad[J]);
-                ad[J] = mfma4(sm.dA[o], sm.beta[16 * lq + s] * k[s] * e, ad[J]);
-            }
-        to_block(aq, w);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) dq[r] += __expf(gm[r] - ref) * w[r];
-        to_block(ay, w);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) l[r] += __expf(gm[r] - ref) * w[r];
-        to_block(ad, w);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) ar[r] = __expf(own - gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) x[r] = __expf(end[3] - gm[r]) * w[r];
 
-        // pairs inside the lane's block: w[i] holds e^{gamma_r - gamma_i}, decayed row by row
+    // pairs of different blocks. Rows of block I against all rows before it, through gamma at the row before
+    // block I: step s takes row s of every block (lane lq its own), blocks I and later as zeros.
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+    for (int t = 0; t < 4; ++t) aq[t] = ay[t] = ad[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int I = 1; I < 4; ++I)
+#pragma unroll
+        for (int s4 = 0; s4 < 4; ++s4) {
             pin();
-            const float* pr = &sm.dP[tri_at<PC>(16 * lq + r, 16 * lq)];
-            const float* pa = &sm.dA[tri_at<PC>(16 * lq + r, 16 * lq)];
-            const float bk = sm.beta[16 * lq + r] * k[r];
-            w[r] = 1.f;
+            const int o = tri_at<PC>(16 * I + l16, 16 * lq + 4 * s4);
+            const f32x4_t vp = *reinterpret_cast<const f32x4_t*>(&sm.dP[o]);
+            const f32x4_t va = *reinterpret_cast<const f32x4_t*>(&sm.dA[o]);
 #pragma unroll
-            for (int i4 = 0; i4 <= r / 4; ++i4) {
-                const f32x4_t vp = *reinterpret_cast<const f32x4_t*>(pr + 4 * i4);
-                const f32x4_t va = *reinterpret_cast<const f32x4_t*>(pa + 4 * i4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 4 * i4 + e;
-                    if (i > r) continue;
-                    if (i < r) w[i] *= a[r];
-                    const float ke = w[i] * k[i];
-                    dq[r] += vp[e] * ke;
-                    if (i < r) l[r] += va[e] * ke;
-                    ar[i] += (i < r ? vp[e] * q[r] + va[e] * bk : vp[e] * q[r]) * w[i];
-                }
-            }
-            // the row's sums are formed here, not at their use at the end
-            hold(dq[r]);
-            hold(l[r]);
-#pragma unroll
-            for (int i = 0; i <= r; ++i) hold(ar[i]);
-        }
-        // gradients
-        float kx = 0.f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const float bl = sm.beta[16 * lq + r] * l[r];
-            kx += k[r] * x[r];
-            w[r] = q[r] * dq[r] + k[r] * (bl - x[r] - ar[r]);
-            const float db = row16_sum(k[r] * l[r]);
-            if (l16 == 0) sm.part[wave][16 * lq + r] = db;
-            l[r] = bl + x[r] + ar[r];   // dk
-        }
-        kx += __shfl_xor(kx, 16, 64);
-        kx += __shfl_xor(kx, 32, 64);
-        kx += __expf(end[3]) * sds;
-#pragma unroll
-        for (int r = 14; r >= 0; --r) w[r] += w[r + 1];
-        const float b1 = __shfl(w[0], 16 + l16, 64), b2 = __shfl(w[0], 32 + l16, 64), b3 = __shfl(w[0], 48 + l16, 64);
-        const float tail = kx + (lq < 3 ? b3 : 0.f) + (lq < 2 ? b2 : 0.f) + (lq < 1 ? b1 : 0.f);
-        __syncthreads();   // every wave is done with its turning tile
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int o = out_at<DK>(16 * lq + r, ch);
-            sm.out[0][o] = dq[r];
-            sm.out[1][o] = l[r];
-            sm.out[2][o] = w[r] + tail;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < 64 * DK / 4 / NT; ++n) {
-            const int i = tid + NT * n, r = i / (DK / 4), cc = 4 * (i % (DK / 4)), o = out_at<DK>(r, cc);
-            if (r < len) {
-                const long g = base + (long)r * H * DK + cc;
-                kb_out4(static_cast<TG*>(b.dq) + g, *reinterpret_cast<const float4*>(&sm.out[0][o]));
-                kb_out4(static_cast<TG*>(b.dk) + g, *reinterpret_cast<const float4*>(&sm.out[1][o]));
-                kb_out4(b.dg + g, *reinterpret_cast<const float4*>(&sm.out[2][o]));
+            for (int e = 0; e < 4; ++e) {
+                const int s = 4 * s4 + e;
+                const float kb = lq < I ? k[s] * __expf(end[I - 1] - gm[s]) : 0.f;
+                aq[I] = mfma4(vp[e], kb, aq[I]);
+                ay[I] = mfma4(va[e], kb, ay[I]);
             }
         }
-        if (tid < len) {
-            float s = sm.yv[tid];
+    // Columns of block J against all rows behind it, through gamma at the block's last row.
 #pragma unroll
-            for (int i = 0; i < NW; ++i) s += sm.part[i][tid];
-            b.dbeta[(bos + tid) * H + h] = s;
+    for (int J = 0; J < 3; ++J)
+#pragma unroll
+        for (int s = 0; s < 16; ++s) {
+            if (s % 4 == 0) pin();
+            const int o = tri_at<PC>(16 * lq + s, 16 * J + l16);
+            const float e = lq > J ? __expf(gm[s] - end[J]) : 0.f;
+            ad[J] = mfma4(sm.dP[o], q[s] * e, ad[J]);
+            ad[J] = mfma4(sm.dA[o], sm.beta[16 * lq + s] * k[s] * e, ad[J]);
         }
+    to_block(aq, w);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) dq[r] += __expf(gm[r] - ref) * w[r];
+    to_block(ay, w);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) l[r] += __expf(gm[r] - ref) * w[r];
+    to_block(ad, w);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) ar[r] = __expf(own - gm[r]) * w[r];
+
+    // pairs inside the lane's block: w[i] holds e^{gamma_r - gamma_i}, decayed row by row
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        pin();
+        const float* pr = &sm.dP[tri_at<PC>(16 * lq + r, 16 * lq)];
+        const float* pa = &sm.dA[tri_at<PC>(16 * lq + r, 16 * lq)];
+        const float bk = sm.beta[16 * lq + r] * k[r];
+        w[r] = 1.f;
+#pragma unroll
+        for (int i4 = 0; i4 <= r / 4; ++i4) {
+            const f32x4_t vp = *reinterpret_cast<const f32x4_t*>(pr + 4 * i4);
+            const f32x4_t va = *reinterpret_cast<const f32x4_t*>(pa + 4 * i4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * i4 + e;
+                if (i > r) continue;
+                if (i < r) w[i] *= a[r];
+                const float ke = w[i] * k[i];
+                dq[r] += vp[e] * ke;
+                if (i < r) l[r] += va[e] * ke;
+                ar[i] += (i < r ? vp[e] * q[r] + va[e] * bk : vp[e] * q[r]) * w[i];
+            }
+        }
+        // the row's sums are formed here, not at their use at the end
+        hold(dq[r]);
+        hold(l[r]);
+#pragma unroll
+        for (int i = 0; i <= r; ++i) hold(ar[i]);
+    }
+    // gradients
+    float kx = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const float bl = sm.beta[16 * lq + r] * l[r];
+        kx += k[r] * x[r];
+        w[r] = q[r] * dq[r] + k[r] * (bl - x[r] - ar[r]);
+        const float db = row16_sum(k[r] * l[r]);
+        if (l16 == 0) sm.part[wave][16 * lq + r] = db;
+        l[r] = bl + x[r] + ar[r];   // dk
+    }
+    kx += __shfl_xor(kx, 16, 64);
+    kx += __shfl_xor(kx, 32, 64);
+    kx += __expf(end[3]) * sds;
+#pragma unroll
+    for (int r = 14; r >= 0; --r) w[r] += w[r + 1];
+    const float b1 = __shfl(w[0], 16 + l16, 64), b2 = __shfl(w[0], 32 + l16, 64), b3 = __shfl(w[0], 48 + l16, 64);
+    const float tail = kx + (lq < 3 ? b3 : 0.f) + (lq < 2 ? b2 : 0.f) + (lq < 1 ? b1 : 0.f);
+    __syncthreads();   // every wave is done with its turning tile
+    auto store_rows = [&](const float* tile, auto* dst) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int i = tid + 256 * n, r = i / 16, cc = 4 * (i % 16);
+            if (r < len) kb_out4(dst + base + (long)r * H * DK + c0 + cc, *reinterpret_cast<const float4*>(&tile[out_at<64>(r, cc)]));
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int o = out_at<64>(16 * lq + r, 16 * wave + l16);
+        sm.out[0][o] = dq[r];
+        sm.out[1][o] = l[r];
+    }
+    __syncthreads();
+    store_rows(sm.out[0], static_cast<TG*>(b.dq));
+    store_rows(sm.out[1], static_cast<TG*>(b.dk));
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 16; ++r) sm.out[0][out_at<64>(16 * lq + r, 16 * wave + l16)] = w[r] + tail;
+    __syncthreads();
+    store_rows(sm.out[0], b.dg);
+    if (tid < len) {
+        float s = (half == 0 ? sm.yv[tid] : 0.f) + (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]);
+        float* dst = b.dbeta + (bos + tid) * H + h;
+        // two halves add to the zero that the reverse walk left: one addition each, whose order does not matter
+        if constexpr (NH == 1) *dst = s;
+        else unsafeAtomicAdd(dst, s);
     }
 }
 
@@ -836,9 +872,9 @@ static hipError_t kda_bwd_launch(const KdaBwdProblem& b, hipStream_t s) {
     hipError_t e = launch(kda_bwd_states_kernel<TIn, DK, DV>, walks, dim3(256), s, b);
     if (e == hipSuccess) e = launch(kda_bwd_reverse_kernel<TIn, DK, DV>, walks, dim3(256), s, b);
     if (e != hipSuccess || units == 0) return e;
-    const dim3 grid((unsigned)units);
-    return b.grad_bf16 ? launch(kda_bwd_grad_kernel<TIn, uint16_t, DK, DV>, grid, dim3(DK * 4), s, b)
-                       : launch(kda_bwd_grad_kernel<TIn, float, DK, DV>, grid, dim3(DK * 4), s, b);
+    const dim3 grid((unsigned)(units * (DK / 64)));
+    return b.grad_bf16 ? launch(kda_bwd_grad_kernel<TIn, uint16_t, DK, DV>, grid, dim3(256), s, b)
+                       : launch(kda_bwd_grad_kernel<TIn, float, DK, DV>, grid, dim3(256), s, b);
 }
 
 template <typename TIn>

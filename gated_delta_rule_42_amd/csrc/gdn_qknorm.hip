@@ -10,7 +10,7 @@
 // anyway. Sums are fp32.
 //
 // A row takes G lanes of 8 channels (G = 8, 16 or 32 by d), so every load and store is 16 bytes wide and the row's
-// sums are G-lane butterflies. A work-group takes a run of kPasses * 256 / G consecutive rows, whatever heads they
+// sums are G-lane butterflies. A work-group takes a run of NP * 256 / G consecutive rows, whatever heads they
 // are, with all of its loads issued before the first row is used. The angles of the few tokens these rows belong to are computed
 // once per work-group, in fp64 revolutions (a position of a million times a frequency near 1 has lost 5 of its
 // digits in fp32), reduced to half a revolution, and their cosines and sines kept in LDS for all heads.
@@ -20,7 +20,9 @@
 namespace gdn {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormPasses = 4;   // rows per lane group
+// NP rows per lane group: four where there are enough of them to fill the device many times over, else one, which spreads
+// a small call over more work-groups. 64 tokens x 32 heads of 128: 3.6 us with one, 5.3 with four; 32768 x 36 heads of 64,
+// rotated: 69 us with one, 57 with four.
 
 enum { ROPE_NONE = 0, ROPE_HALF = 1, ROPE_PAIRS = 2 };
 
@@ -51,13 +53,21 @@ template <> struct Raw8<uint16_t> {
         }
     }
 };
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+// NT: past the caches, for outputs larger than the L2 (the 32768-token call above: 57 us against 61).
+template <bool NT, typename T>
+__device__ __forceinline__ void store_piece(void* p, const T& x) {
+    if constexpr (NT) __builtin_nontemporal_store(x, static_cast<T*>(p));
+    else *static_cast<T*>(p) = x;
 }
+template <bool NT>
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    store_piece<NT>(p, f32x4_t{x[0], x[1], x[2], x[3]});
+    store_piece<NT>(p + 4, f32x4_t{x[4], x[5], x[6], x[7]});
+}
+template <bool NT>
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    store_piece<NT>(p, u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                               pack_bf16x2(x[6], x[7])});
 }
 
 // Sum over the G lanes of a row, in every lane.
@@ -73,15 +83,15 @@ __device__ __forceinline__ float row_sum(float x) {
 
 // The rows of a work-group and their angles. A block of RB consecutive rows (row = token * (Hq + Hk) + head, queries
 // first) touches at most RB / 2 + 2 tokens, since a token has two rows at least.
-template <int G>
+template <int G, int NP>
 struct NormBlock {
     static constexpr int RPP = kNormThreads / G;         // rows per pass
-    static constexpr int RB = RPP * kNormPasses;
+    static constexpr int RB = RPP * NP;
     static constexpr int MAXTOK = RB / 2 + 2;
     static constexpr int PAIRS = 4 * G;                  // rotated pairs of a row at most
 };
 
-template <int G>
+template <int PAIRS>
 __device__ __forceinline__ void fill_angles(const NormProblem& p, float2* cs, long tok0, int ntok, int tid) {
     const int half = p.rot / 2;
     for (int i = tid; i < ntok * half; i += kNormThreads) {
@@ -90,7 +100,7 @@ __device__ __forceinline__ void fill_angles(const NormProblem& p, float2* cs, lo
         u -= rint(u);
         float s, c;
         sincospif(2.f * (float)u, &s, &c);
-        cs[t * NormBlock<G>::PAIRS + j] = make_float2(c * p.rope_scale, s * p.rope_scale);
+        cs[t * PAIRS + j] = make_float2(c * p.rope_scale, s * p.rope_scale);
     }
 }
 
@@ -151,18 +161,18 @@ __device__ __forceinline__ long row_dense(const NormProblem& p, const NormRow& r
     return ((long)r.token * (r.key ? p.hk : p.hq) + r.head) * p.d;
 }
 
-template <typename TX, typename TY, int G, int ROPE>
+template <typename TX, typename TY, int G, int ROPE, int NP>
 __global__ __launch_bounds__(kNormThreads) void qk_norm_fwd_kernel(NormProblem p) {
-    using B = NormBlock<G>;
+    using B = NormBlock<G, NP>;
     __shared__ float2 cs[ROPE ? B::MAXTOK * B::PAIRS : 1];
     const int tid = threadIdx.x, l = tid % G, grp = tid / G;
     const unsigned nrows = (unsigned)(p.tokens * (p.hq + p.hk)), row0 = blockIdx.x * B::RB;
     const bool lane_in = 8 * l < p.d;
 
-    Raw8<TX> raw[kNormPasses];
-    NormRow rw[kNormPasses];
+    Raw8<TX> raw[NP];
+    NormRow rw[NP];
 #pragma unroll
-    for (int i = 0; i < kNormPasses; ++i) {
+    for (int i = 0; i < NP; ++i) {
         rw[i] = norm_row(p, row0 + i * B::RPP + grp, nrows);
         raw[i].zero();
         if (rw[i].ok && lane_in) raw[i].load(static_cast<const TX*>(rw[i].key ? p.k : p.q) + row_in(p, rw[i]) + 8 * l);
@@ -171,11 +181,11 @@ __global__ __launch_bounds__(kNormThreads) void qk_norm_fwd_kernel(NormProblem p
     if constexpr (ROPE != ROPE_NONE) {
         const unsigned ht = p.hq + p.hk, last = min(row0 + B::RB, nrows) - 1;
         tok0 = (int)(row0 / ht);
-        fill_angles<G>(p, cs, tok0, (int)(last / ht) - tok0 + 1, tid);
+        fill_angles<B::PAIRS>(p, cs, tok0, (int)(last / ht) - tok0 + 1, tid);
         __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < kNormPasses; ++i) {
+    for (int i = 0; i < NP; ++i) {
         float x[8], ss = 0.f;
         raw[i].get(x);
 #pragma unroll
@@ -198,16 +208,16 @@ __global__ __launch_bounds__(kNormThreads) void qk_norm_fwd_kernel(NormProblem p
         const float scale = rw[i].key ? 1.f : p.q_scale;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= scale;
-        if (rw[i].ok && lane_in) store8(static_cast<TY*>(rw[i].key ? p.k_out : p.q_out) + row_dense(p, rw[i]) + 8 * l, x);
+        if (rw[i].ok && lane_in) store8<(NP > 1)>(static_cast<TY*>(rw[i].key ? p.k_out : p.q_out) + row_dense(p, rw[i]) + 8 * l, x);
     }
 }
 
 // DW: the weights' gradients too. The grid is then at most kNormGradBlocks work-groups, each of which walks its blocks
 // of rows in a fixed order, sums its rows' contributions in registers, then over its lane groups in LDS, and writes
 // one partial row [2, d] (q, k); norm_weight_grad_kernel adds those. No atomics: the same inputs give the same bits.
-template <typename TX, typename TY, int G, int ROPE, bool DW>
+template <typename TX, typename TY, int G, int ROPE, int NP, bool DW>
 __global__ __launch_bounds__(kNormThreads) void qk_norm_bwd_kernel(NormProblem p) {
-    using B = NormBlock<G>;
+    using B = NormBlock<G, NP>;
     __shared__ float2 cs[ROPE ? B::MAXTOK * B::PAIRS : 1];
     __shared__ float part[DW ? 4 * 2 * 8 * G : 1];
     const int tid = threadIdx.x, l = tid % G, grp = tid / G;
@@ -219,11 +229,11 @@ __global__ __launch_bounds__(kNormThreads) void qk_norm_bwd_kernel(NormProblem p
 
     for (unsigned blk = blockIdx.x; blk < nblocks; blk += gridDim.x) {
         const unsigned row0 = blk * B::RB;
-        Raw8<TX> xr[kNormPasses];
-        Raw8<TY> gr[kNormPasses];
-        NormRow rw[kNormPasses];
+        Raw8<TX> xr[NP];
+        Raw8<TY> gr[NP];
+        NormRow rw[NP];
 #pragma unroll
-        for (int i = 0; i < kNormPasses; ++i) {
+        for (int i = 0; i < NP; ++i) {
             rw[i] = norm_row(p, row0 + i * B::RPP + grp, nrows);
             xr[i].zero();
             gr[i].zero();
@@ -237,11 +247,11 @@ __global__ __launch_bounds__(kNormThreads) void qk_norm_bwd_kernel(NormProblem p
             const unsigned ht = p.hq + p.hk, last = min(row0 + B::RB, nrows) - 1;
             tok0 = (int)(row0 / ht);
             if (DW) __syncthreads();   // the previous block is done with the angles
-            fill_angles<G>(p, cs, tok0, (int)(last / ht) - tok0 + 1, tid);
+            fill_angles<B::PAIRS>(p, cs, tok0, (int)(last / ht) - tok0 + 1, tid);
             __syncthreads();
         }
 #pragma unroll
-        for (int i = 0; i < kNormPasses; ++i) {
+        for (int i = 0; i < NP; ++i) {
             float x[8], g[8];
             xr[i].get(x);
             gr[i].get(g);
@@ -281,7 +291,7 @@ __global__ __launch_bounds__(kNormThreads) void qk_norm_bwd_kernel(NormProblem p
             if (rw[i].ok && lane_in) {
                 const long o = rw[i].key ? rw[i].token * p.dk_token + rw[i].head * p.dk_head
                                          : rw[i].token * p.dq_token + rw[i].head * p.dq_head;
-                store8(static_cast<TX*>(rw[i].key ? p.dk_out : p.dq_out) + o + 8 * l, g);
+                store8<(NP > 1)>(static_cast<TX*>(rw[i].key ? p.dk_out : p.dq_out) + o + 8 * l, g);
             }
         }
     }
@@ -319,7 +329,15 @@ __global__ __launch_bounds__(1024) void norm_weight_grad_kernel(const float* par
     __shared__ float sum[64][17];
     const int lc = threadIdx.x & 15, lr = threadIdx.x >> 4, c = blockIdx.x * 16 + lc;
     float a = 0.f;
-    for (int i = lr; i < nparts; i += 64) a += partial[(long)i * 2 * d + c];
+    // kNormGradBlocks / 64 = 16 rows a lane at most, loaded together
+    float x[kNormGradBlocks / 64];
+#pragma unroll
+    for (int j = 0; j < kNormGradBlocks / 64; ++j) {
+        const int i = lr + 64 * j;
+        x[j] = i < nparts ? partial[(long)i * 2 * d + c] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kNormGradBlocks / 64; ++j) a += x[j];
     sum[lr][lc] = a;
     __syncthreads();
 #pragma unroll
@@ -333,21 +351,21 @@ __global__ __launch_bounds__(1024) void norm_weight_grad_kernel(const float* par
     }
 }
 
-template <typename TX, typename TY, int G, int ROPE>
+template <typename TX, typename TY, int G, int ROPE, int NP>
 static hipError_t norm_launch(const NormProblem& p, hipStream_t s) {
     const long nrows = p.tokens * (p.hq + p.hk);
-    const long nblocks = (nrows + NormBlock<G>::RB - 1) / NormBlock<G>::RB;
+    const long nblocks = (nrows + NormBlock<G, NP>::RB - 1) / NormBlock<G, NP>::RB;
     if (!p.backward) {
         if (nblocks == 0) return hipSuccess;
-        return launch(qk_norm_fwd_kernel<TX, TY, G, ROPE>, dim3((unsigned)nblocks), dim3(kNormThreads), s, p);
+        return launch(qk_norm_fwd_kernel<TX, TY, G, ROPE, NP>, dim3((unsigned)nblocks), dim3(kNormThreads), s, p);
     }
     if (!p.dqw && !p.dkw) {
         if (nblocks == 0) return hipSuccess;
-        return launch(qk_norm_bwd_kernel<TX, TY, G, ROPE, false>, dim3((unsigned)nblocks), dim3(kNormThreads), s, p);
+        return launch(qk_norm_bwd_kernel<TX, TY, G, ROPE, NP, false>, dim3((unsigned)nblocks), dim3(kNormThreads), s, p);
     }
     const int parts = norm_grad_blocks(nrows);
     if (nblocks > 0) {
-        const hipError_t e = launch(qk_norm_bwd_kernel<TX, TY, G, ROPE, true>, dim3((unsigned)parts), dim3(kNormThreads), s, p);
+        const hipError_t e = launch(qk_norm_bwd_kernel<TX, TY, G, ROPE, NP, true>, dim3((unsigned)parts), dim3(kNormThreads), s, p);
         if (e != hipSuccess) return e;
     }
     return launch(norm_weight_grad_kernel, dim3((unsigned)(p.d / 8)), dim3(1024), s, (const float*)p.partial, parts, p.d, p.dqw, p.dkw);
@@ -355,8 +373,11 @@ static hipError_t norm_launch(const NormProblem& p, hipStream_t s) {
 
 template <typename TX, typename TY, int G>
 static hipError_t norm_rope(const NormProblem& p, hipStream_t s) {
-    if (p.rot == 0) return norm_launch<TX, TY, G, ROPE_NONE>(p, s);
-    return p.interleaved ? norm_launch<TX, TY, G, ROPE_PAIRS>(p, s) : norm_launch<TX, TY, G, ROPE_HALF>(p, s);
+    const bool large = p.tokens * (p.hq + p.hk) >= 2048 * NormBlock<G, 1>::RB;
+    if (p.rot == 0) return large ? norm_launch<TX, TY, G, ROPE_NONE, 4>(p, s) : norm_launch<TX, TY, G, ROPE_NONE, 1>(p, s);
+    if (p.interleaved)
+        return large ? norm_launch<TX, TY, G, ROPE_PAIRS, 4>(p, s) : norm_launch<TX, TY, G, ROPE_PAIRS, 1>(p, s);
+    return large ? norm_launch<TX, TY, G, ROPE_HALF, 4>(p, s) : norm_launch<TX, TY, G, ROPE_HALF, 1>(p, s);
 }
 
 template <typename TX, typename TY>
@@ -367,7 +388,7 @@ static hipError_t norm_dispatch(const NormProblem& p, hipStream_t s) {
 }
 
 // Work-groups (and partial rows) of the backward pass with weight gradients: enough to fill the device several times
-// over, but no more than there are blocks of rows (counted at the smallest block, 32 rows).
+// over, but no more than there are blocks of rows (counted at 32 rows each).
 int norm_grad_blocks(long nrows) {
     const long blocks = (nrows + 31) / 32;
     return (int)(blocks < kNormGradBlocks ? blocks : kNormGradBlocks);

@@ -192,6 +192,11 @@ CASES = [
     (100, 2, 2, 72, "bf16", 6, "interleaved", "l2", True, 2 ** 30),
     (515, 16, 4, 128, "bf16", 64, "interleaved", "rms", True, 100000),
     (515, 6, 2, 192, "f32", 0, "half", "l2", True, 0),
+    # enough rows for four per lane group
+    (1101, 24, 8, 128, "bf16", 64, "half", "rms", True, 3000),
+    (2050, 30, 3, 64, "bf16", 32, "interleaved", "l2", True, 100),
+    (553, 29, 1, 256, "f32", 0, "half", "rms", True, 0),
+    (1111, 29, 1, 96, "f32", 96, "half", "l2", True, 0),
 ]
 
 
