@@ -485,10 +485,17 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
 // (rows 16 t + 4 lq + m) of the products, and the block layout (lane (lq, l16) has rows 16 lq .. 16 lq + 15 of its
 // channel), in which gamma is scanned, the pairs inside a block are summed and the gradients are formed. An accumulator
 // goes to the block layout through a private LDS tile.
+//
+// The products over d_v (dO D^T, Y D^T, dO S, Y S, D dS') run on the bf16 matrix core at fp32's accuracy: an fp32 operand
+// is split into three bf16 planes, x = x0 + x1 + x2 (24 significant bits), and a product takes the six plane products down to
+// 2^-24 of it: 00, 01, 10, 11, 02, 20 (a bf16 dO is one plane by itself and takes three). Six 16x16x32 products are 96
+// cycles where the fp32 core takes 256.
+constexpr int kPlane = 64 * 32;   // elements of one plane of a slice (see plane_at)
+template <int OP>                 // planes of dO: 1 (bf16 inputs) or 3
 struct alignas(16) KdaGradSmem {
-    static constexpr int PV = 36, PC = 68, PT = 17;
+    static constexpr int PC = 68, PT = 17;
     union {
-        struct { float D[64 * PV], Y[64 * PV], dO[64 * PV]; } in;
+        struct { uint16_t D[3][kPlane], Y[3][kPlane], dO[OP][kPlane]; } in;
         float turn[4][64 * PT];
         float out[2][64 * 64];        // gradients on their way out (see out_at)
     };
@@ -498,6 +505,48 @@ struct alignas(16) KdaGradSmem {
     float yv[64];
     float part[4][64];
 };
+
+// Element (r, c) of a plane, c a multiple of four: rows of 64 bytes whose 16-byte pieces are permuted so that 16 rows'
+// pieces of one column fall into different banks.
+__device__ __forceinline__ int plane_at(int r, int c) { return r * 32 + (((c >> 3) ^ ((r >> 2) & 3)) << 3) + (c & 4); }
+// Pairs of fp32 values (a, b) as three bf16 planes: in w[0], w[1], w[2] the pair's roundings and those of the two remainders.
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[3]) {
+    w[0] = pack_bf16x2(a, b);
+    a -= bf16_lo_half(w[0]);
+    b -= bf16_hi_half(w[0]);
+    w[1] = pack_bf16x2(a, b);
+    w[2] = pack_bf16x2(a - bf16_lo_half(w[1]), b - bf16_hi_half(w[1]));
+}
+template <int NP>
+struct Planes { uint4 w[NP]; };   // eight values of each plane
+__device__ __forceinline__ Planes<3> split8(const float (&x)[8]) {
+    uint32_t a[3], b[3], c[3], d[3];
+    split_pair(x[0], x[1], a);
+    split_pair(x[2], x[3], b);
+    split_pair(x[4], x[5], c);
+    split_pair(x[6], x[7], d);
+    Planes<3> r;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) r.w[i] = make_uint4(a[i], b[i], c[i], d[i]);
+    return r;
+}
+template <int NP>
+__device__ __forceinline__ Planes<NP> read_planes(const uint16_t (*m)[kPlane], int r, int c) {
+    Planes<NP> x;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) x.w[i] = *reinterpret_cast<const uint4*>(&m[i][plane_at(r, c)]);
+    return x;
+}
+// acc += x y to fp32's accuracy, the smallest products first
+template <int NX>
+__device__ __forceinline__ void mul_planes(f32x4_t& acc, const Planes<NX>& x, const Planes<3>& y) {
+    if constexpr (NX == 3) acc = mfma_bf16(x.w[2], y.w[0], acc);
+    acc = mfma_bf16(x.w[0], y.w[2], acc);
+    if constexpr (NX == 3) acc = mfma_bf16(x.w[1], y.w[1], acc);
+    if constexpr (NX == 3) acc = mfma_bf16(x.w[1], y.w[0], acc);
+    acc = mfma_bf16(x.w[0], y.w[1], acc);
+    acc = mfma_bf16(x.w[0], y.w[0], acc);
+}
 
 // Element (r, i) of dP and dA. They are read by rows (pieces of one row), by columns (16 columns of the row s of all four
 // row blocks at once) and by diagonal blocks (a piece of the row s of all four), so the column blocks of row block b are
@@ -520,8 +569,9 @@ __device__ __forceinline__ void wave_lds_fence() {
 
 template <typename TIn, typename TG, int DK, int DV>
 __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
-    using SM = KdaGradSmem;
-    constexpr int PV = SM::PV, PC = SM::PC, PT = SM::PT, NH = DK / 64, NS = DV / 32, EB = (int)sizeof(TIn);
+    constexpr int NH = DK / 64, NS = DV / 32, EB = (int)sizeof(TIn), OP = EB == 2 ? 1 : 3;
+    using SM = KdaGradSmem<OP>;
+    constexpr int PC = SM::PC, PT = SM::PT;
     __shared__ SM sm;
     const ChunkProblem& p = b.f;
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
@@ -544,7 +594,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     const auto vres = make_rsrc(static_cast<const TIn*>(p.v) + vb, vrows * EB);
     f32x4_t dpc[2], ypc[2];
     u32x4_t gpc[2], vpc[2];
-    float sn[8], dn[8];   // the lane's rows 32 sl + 16 u + 4 lq + e of S and dS'
+    float sn[8], dn[8];   // the lane's rows 32 sl + 8 lq + e of S and dS'
     const float* sp = p.states + unit * DV * DK + ch;
     const float* dp = b.dstates + unit * DV * DK + ch;
     auto piece = [](__amdgpu_buffer_rsrc_t r, int o) {
@@ -565,12 +615,10 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
             vpc[n] = piece(vres, (r * H * DV + cc) * EB);
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sn[4 * u + e] = sp[(32 * sl + 16 * u + 4 * lq + e) * DK];
-                dn[4 * u + e] = dp[(32 * sl + 16 * u + 4 * lq + e) * DK];
-            }
+        for (int e = 0; e < 8; ++e) {
+            sn[e] = sp[(32 * sl + 8 * lq + e) * DK];
+            dn[e] = dp[(32 * sl + 8 * lq + e) * DK];
+        }
     };
     load(0);
     // k, q, g of the lane's rows and channel
@@ -602,7 +650,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         else return __builtin_bit_cast(f32x4_t, x);
     };
 
-    // dP = dO D^T and dA = -Y D^T (job w + 4 n: lower tile number job / 2, of dP or dA), dO S, Y S and D dS' on the
+    // dP = dO D^T and dA = -Y D^T (job w + 4 n: lower tile number job / 2, of dP or dA in turn), dO S, Y S and D dS' on the
     // wave's channels, colsum(S dS'), Y . V, all summed slice by slice; dV = beta Y on the way
     f32x4_t aq[4], ay[4], ad[4], tri[5];
     float sds = 0.f, yv[2] = {0.f, 0.f};
@@ -611,6 +659,14 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
 #pragma unroll
     for (int n = 0; n < 5; ++n) tri[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     auto tile_row = [](int tile) { return tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3; };
+    auto of_a = [](int job) { return (job ^ (job >> 2)) & 1; };   // a wave's jobs alternate: dA takes twice dP's products
+    auto put = [](uint16_t (*m)[kPlane], int at, const f32x4_t& x) {
+        uint32_t a[3], c[3];
+        split_pair(x[0], x[1], a);
+        split_pair(x[2], x[3], c);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(&m[i][at]) = make_uint2(a[i], c[i]);
+    };
 #pragma unroll 1
     for (int sl = 0; sl < NS; ++sl) {
         __syncthreads();   // the previous slice is dead
@@ -618,53 +674,43 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         for (int n = 0; n < 2; ++n) {
             const int i = tid + 256 * n, r = i / 8, cc = 4 * (i % 8);
             const f32x4_t y = ypc[n], v = widen(vpc[n]);
-            *reinterpret_cast<f32x4_t*>(&sm.in.D[r * PV + cc]) = dpc[n];
-            *reinterpret_cast<f32x4_t*>(&sm.in.Y[r * PV + cc]) = y;
-            *reinterpret_cast<f32x4_t*>(&sm.in.dO[r * PV + cc]) = widen(gpc[n]);
+            const int at = plane_at(r, cc);
+            put(sm.in.D, at, dpc[n]);
+            put(sm.in.Y, at, y);
+            if constexpr (OP == 1) *reinterpret_cast<uint2*>(&sm.in.dO[0][at]) = make_uint2(gpc[n][0], gpc[n][1]);
+            else put(sm.in.dO, at, widen(gpc[n]));
             yv[n] += y[0] * v[0] + y[1] * v[1] + y[2] * v[2] + y[3] * v[3];
             if (half == 0 && r < len)
                 kb_out4(static_cast<TG*>(b.dv) + vb + (long)r * H * DV + 32 * sl + cc,
                         make_float4(bt[n] * y[0], bt[n] * y[1], bt[n] * y[2], bt[n] * y[3]));
         }
-        float s[8], d[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = sn[i], d[i] = dn[i], sds += s[i] * d[i];
+        for (int i = 0; i < 8; ++i) sds += sn[i] * dn[i];
+        const Planes<3> s = split8(sn), d = split8(dn);
         __syncthreads();
         load(min(sl + 1, NS - 1));   // the last slice again at the end
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int n = 0; n < 5; ++n) {
+            const int job = wave + 4 * n, tile = job >> 1, I = tile_row(tile), J = tile - I * (I + 1) / 2;
+            const Planes<3> y = read_planes<3>(sm.in.D, 16 * J + l16, 8 * lq);
+            if (of_a(job)) mul_planes<3>(tri[n], read_planes<3>(sm.in.Y, 16 * I + l16, 8 * lq), y);
+            else mul_planes<OP>(tri[n], read_planes<OP>(sm.in.dO, 16 * I + l16, 8 * lq), y);
+        }
 #pragma unroll
-            for (int n = 0; n < 5; ++n) {
-                const int job = wave + 4 * n, tile = job >> 1, I = tile_row(tile), J = tile - I * (I + 1) / 2;
-                const float* L = (job & 1) ? sm.in.Y : sm.in.dO;
-                const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&L[(16 * I + l16) * PV + 16 * u + 4 * lq]);
-                const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&sm.in.D[(16 * J + l16) * PV + 16 * u + 4 * lq]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) tri[n] = mfma4(x[e], y[e], tri[n]);
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int a = (16 * t + l16) * PV + 16 * u + 4 * lq;
-                const f32x4_t o = *reinterpret_cast<const f32x4_t*>(&sm.in.dO[a]);
-                const f32x4_t y = *reinterpret_cast<const f32x4_t*>(&sm.in.Y[a]);
-                const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sm.in.D[a]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    aq[t] = mfma4(o[e], s[4 * u + e], aq[t]);
-                    ay[t] = mfma4(y[e], s[4 * u + e], ay[t]);
-                    ad[t] = mfma4(x[e], d[4 * u + e], ad[t]);
-                }
-            }
+        for (int t = 0; t < 4; ++t) {
+            mul_planes<OP>(aq[t], read_planes<OP>(sm.in.dO, 16 * t + l16, 8 * lq), s);
+            mul_planes<3>(ay[t], read_planes<3>(sm.in.Y, 16 * t + l16, 8 * lq), s);
+            mul_planes<3>(ad[t], read_planes<3>(sm.in.D, 16 * t + l16, 8 * lq), d);
         }
     }
 #pragma unroll
     for (int n = 0; n < 5; ++n) {
         const int job = wave + 4 * n, tile = job >> 1, I = tile_row(tile), J = tile - I * (I + 1) / 2;
-        float* out = (job & 1) ? sm.dA : sm.dP;
+        float* out = of_a(job) ? sm.dA : sm.dP;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const int r = 16 * I + 4 * lq + m, i = 16 * J + l16;
-            out[tri_at<PC>(r, i)] = (job & 1) ? (i < r ? -tri[n][m] : 0.f) : (i <= r ? tri[n][m] : 0.f);
+            out[tri_at<PC>(r, i)] = of_a(job) ? (i < r ? -tri[n][m] : 0.f) : (i <= r ? tri[n][m] : 0.f);
         }
     }
     // zeros in the upper tiles (I, J) = (0, 1), (0, 2), (0, 3), (1, 2), (1, 3), (2, 3)
