@@ -493,10 +493,10 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
 constexpr int kPlane = 64 * 32;   // elements of one plane of a slice (see plane_at)
 template <int OP>                 // planes of dO: 1 (bf16 inputs) or 3
 struct alignas(16) KdaGradSmem {
-    static constexpr int PC = 68, PT = 17;
+    static constexpr int PC = 68;
     union {
         struct { uint16_t D[3][kPlane], Y[3][kPlane], dO[OP][kPlane]; } in;
-        float turn[4][64 * PT];
+        float turn[4][64 * 16];
         float out[2][64 * 64];        // gradients on their way out (see out_at)
     };
     float dP[64 * PC];                // see tri_at
@@ -506,9 +506,10 @@ struct alignas(16) KdaGradSmem {
     float part[4][64];
 };
 
-// Element (r, c) of a plane, c a multiple of four: rows of 64 bytes whose 16-byte pieces are permuted so that 16 rows'
-// pieces of one column fall into different banks.
-__device__ __forceinline__ int plane_at(int r, int c) { return r * 32 + (((c >> 3) ^ ((r >> 2) & 3)) << 3) + (c & 4); }
+// Element (r, c) of a plane, c a multiple of four: rows of 64 bytes whose 16-byte pieces are permuted. A 16-byte LDS read
+// serves lanes 0-3, 12-15, 20-27 together, then 4-11, 16-19, 28-31 (and the same of the upper half): rows 0-3 and 12-15
+// of one piece with rows 4-11 of the next. With rows 8-15 of each 16 flipped by 3 these fall into different banks.
+__device__ __forceinline__ int plane_at(int r, int c) { return r * 32 + (((c >> 3) ^ ((r >> 3) & 1) * 3) << 3) + (c & 4); }
 // Pairs of fp32 values (a, b) as three bf16 planes: in w[0], w[1], w[2] the pair's roundings and those of the two remainders.
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[3]) {
     w[0] = pack_bf16x2(a, b);
@@ -556,6 +557,11 @@ __device__ __forceinline__ int tri_at(int r, int i) {
     const int b = r >> 4, f = ((b << 1) ^ ((b >> 1) * 3)) & 3;
     return r * PC + (i ^ (16 * f));
 }
+// Row r of a turning tile [64, 16]: written four rows 4 lq + m at a time and read four rows 16 lq + r at a time, so both
+// pick the 16 banks of a row.
+__device__ __forceinline__ int turn_at(int r) { return ((r & ~3) | ((r ^ (r >> 2) ^ (r >> 4)) & 3)) * 16; }
+// 2^x (0 below fp32's range).
+__device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
 // Element (r, c) of an output tile: a wave writes 16 columns of four row blocks at once.
 template <int W>
 __device__ __forceinline__ int out_at(int r, int c) { return r * W + (c ^ (16 * ((r >> 4) & 3))); }
@@ -571,7 +577,7 @@ template <typename TIn, typename TG, int DK, int DV>
 __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     constexpr int NH = DK / 64, NS = DV / 32, EB = (int)sizeof(TIn), OP = EB == 2 ? 1 : 3;
     using SM = KdaGradSmem<OP>;
-    constexpr int PC = SM::PC, PT = SM::PT;
+    constexpr int PC = SM::PC;
     __shared__ SM sm;
     const ChunkProblem& p = b.f;
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
@@ -733,12 +739,12 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     }
     __syncthreads();   // dP and dA are whole; D, Y, dO are dead
 
-    // gamma of the lane's rows; a[r] = e^{g_r}, the decay from the row above
+    // gamma of the lane's rows, in units of log 2 (2^x is one instruction); a[r] = e^{g_r}, the decay from the row above
     float a[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        gm[r] = fmaxf(gm[r], kMinLogDecay);
-        a[r] = __expf(gm[r]);
+        gm[r] = fmaxf(gm[r], kMinLogDecay) * 1.44269504f;
+        a[r] = exp2_raw(gm[r]);
         if (r > 0) gm[r] += gm[r - 1];
     }
     {
@@ -751,29 +757,30 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
 #pragma unroll
     for (int B = 0; B < 4; ++B) end[B] = __shfl(gm[15], 16 * B + l16, 64);
 
+    constexpr float kNone = -1000.f;   // 2^kNone = 0: rows that a product leaves out
     float* turn = sm.turn[wave];
     auto to_block = [&](const f32x4_t (&x)[4], float (&y)[16]) {
         wave_lds_fence();
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) turn[(16 * t + 4 * lq + m) * PT + l16] = x[t][m];
+            for (int m = 0; m < 4; ++m) turn[turn_at(16 * t + 4 * lq + m) + l16] = x[t][m];
         wave_lds_fence();
 #pragma unroll
-        for (int r = 0; r < 16; ++r) y[r] = turn[(16 * lq + r) * PT + l16];
+        for (int r = 0; r < 16; ++r) y[r] = turn[turn_at(16 * lq + r) + l16];
     };
     const float ref = lq == 0 ? 0.f : lq == 1 ? end[0] : lq == 2 ? end[1] : end[2];   // gamma before the lane's block
     const float own = gm[15];
     float dq[16], l[16], x[16], ar[16], w[16];
     to_block(aq, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) dq[r] = __expf(gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) dq[r] = exp2_raw(gm[r]) * w[r];
     to_block(ay, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) l[r] = -__expf(gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) l[r] = -exp2_raw(gm[r]) * w[r];
     to_block(ad, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) x[r] = __expf(end[3] - gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) x[r] = exp2_raw(end[3] - gm[r]) * w[r];
 
     // pairs of different blocks. Rows of block I against all rows before it, through gamma at the row before
     // block I: step s takes row s of every block (lane lq its own), blocks I and later as zeros.
@@ -790,7 +797,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int s = 4 * s4 + e;
-                const float kb = lq < I ? k[s] * __expf(end[I - 1] - gm[s]) : 0.f;
+                const float kb = k[s] * exp2_raw(lq < I ? end[I - 1] - gm[s] : kNone);
                 aq[I] = mfma4(vp[e], kb, aq[I]);
                 ay[I] = mfma4(va[e], kb, ay[I]);
             }
@@ -802,19 +809,19 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         for (int s = 0; s < 16; ++s) {
             if (s % 4 == 0) pin();
             const int o = tri_at<PC>(16 * lq + s, 16 * J + l16);
-            const float e = lq > J ? __expf(gm[s] - end[J]) : 0.f;
+            const float e = exp2_raw(lq > J ? gm[s] - end[J] : kNone);
             ad[J] = mfma4(sm.dP[o], q[s] * e, ad[J]);
             ad[J] = mfma4(sm.dA[o], sm.beta[16 * lq + s] * k[s] * e, ad[J]);
         }
     to_block(aq, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) dq[r] += __expf(gm[r] - ref) * w[r];
+    for (int r = 0; r < 16; ++r) dq[r] += exp2_raw(gm[r] - ref) * w[r];
     to_block(ay, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) l[r] += __expf(gm[r] - ref) * w[r];
+    for (int r = 0; r < 16; ++r) l[r] += exp2_raw(gm[r] - ref) * w[r];
     to_block(ad, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) ar[r] = __expf(own - gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) ar[r] = exp2_raw(own - gm[r]) * w[r];
 
     // pairs inside the lane's block: w[i] holds e^{gamma_r - gamma_i}, decayed row by row
 #pragma unroll
@@ -858,7 +865,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     }
     kx += __shfl_xor(kx, 16, 64);
     kx += __shfl_xor(kx, 32, 64);
-    kx += __expf(end[3]) * sds;
+    kx += exp2_raw(end[3]) * sds;
 #pragma unroll
     for (int r = 14; r >= 0; --r) w[r] += w[r + 1];
     const float b1 = __shfl(w[0], 16 + l16, 64), b2 = __shfl(w[0], 32 + l16, 64), b3 = __shfl(w[0], 48 + l16, 64);
