@@ -191,10 +191,13 @@ struct TriFrags {
 // One work-group of four waves per (sequence, head, 32-column tile of d_v). Wave w has the 16 columns cg = w & 1 and the
 // half hf = w >> 1 of the d_k channels: S^T [dk/2, 16] in accumulator registers. Per chunk each wave forms its half of the
 // products over d_k for all 64 rows, the two halves are added through LDS, the triangular product (M, or T^T) is shared
-// by row tiles ({0, 3} and {1, 2}: five block products each), and each wave updates its own channels. Every operand has
-// been read from LDS into registers by the first of the two exchanges, so the next chunk's are written over them, and the
-// loads of the chunk after it issued, between the products of the state update (a probe of an earlier form, which issued the
-// loads in one go, showed 3,000 of a chunk's 13,500 cycles in their issue and 1,200 in the LDS writes).
+// by row tiles ({0, 3} and {1, 2}: five block products each), and each wave updates its own channels. The next
+// chunk's operands are loaded into registers between the products before the first exchange; by then every operand
+// has been read from LDS, so they are written over it between the products of the state update (a probe of an earlier form,
+// which issued the loads in one go, showed 3,000 of a chunk's 13,500 cycles in their issue and 1,200 in the LDS writes).
+constexpr int kEarlyS = 4;              // shares of the loads issued in the state update, the rest in the next chunk's X
+constexpr int kEarlyR = 4, kMidR = 2;   // the reverse walk's, and those in its Kd dS'^T; the rest in Qh^T dO
+
 template <int DK>
 struct alignas(16) KdaStateSmem {
     static constexpr int PK = DK + 4, PC = 68;
@@ -277,7 +280,7 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) store(i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load(min(1L, c.nchunks - 1), i);
+        for (int i = 0; i < kEarlyS; ++i) load(min(1L, c.nchunks - 1), i);
     }
     for (long jc = 0; jc < c.nchunks; ++jc) {
         const long widx = (c.cbase + jc) * H + c.h;
@@ -290,7 +293,10 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
         TriFrags<false, PC> m;
         ColFrags<NJ> kf;
         f32x4_t lm[NJ];
+        const long nxt = min(jc + 1, c.nchunks - 1), nxt2 = min(jc + 2, c.nchunks - 1);   // the last chunk again at the end
         mul_rows<NJ>(X, sm.Kh, PK, hf * HK, ST, l16, lq, [&](int i) {
+            if (i % 4 == 1 && kEarlyS + i / 4 < 8) load(nxt, kEarlyS + i / 4);
+            if (i % 4 == 3 && kEarlyS + 4 + i / 4 < 8) load(nxt, kEarlyS + 4 + i / 4);
             kf.read(sm.Kd, PK, hf * HK, i, l16, lq);
             if (i < 5) m.read(sm.M, hf, i, l16, lq);
             const int j = i / 4;
@@ -321,10 +327,9 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
         // S^T <- Diag(lam) S^T + Kd^T D on the wave's channels
 #pragma unroll
         for (int j = 0; j < NJ; ++j) ST[j] *= lm[j];
-        const long nxt = min(jc + 2, c.nchunks - 1);   // the last chunk again past the end
         kf.mul(ST, D, [&](int i) {
             if (i % 2 == 0) store(i / 2);
-            else load(nxt, i / 2);
+            else if (i / 2 < kEarlyS) load(nxt2, i / 2);
         });
     }
 }
@@ -407,7 +412,7 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) store(i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load(max(0L, c.nchunks - 2), i);
+        for (int i = 0; i < kEarlyR; ++i) load(max(0L, c.nchunks - 2), i);
     }
     for (long jc = c.nchunks - 1; jc >= 0; --jc) {
         const long widx = (c.cbase + jc) * H + c.h;
@@ -423,7 +428,9 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
         for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         ColFrags<NJ> qf, kf;
         TriFrags<true, PC> pf, tf;
+        const long nxt = max(jc - 1, 0L), nxt2 = max(jc - 2, 0L);   // the first chunk again at the end
         mul_rows<NJ>(X, sm.Kd, PK, hf * HK, dST, l16, lq, [&](int i) {
+            if (i % 4 == 1 && i / 4 < kMidR) load(nxt, kEarlyR + i / 4);
             qf.read(sm.Qh, PK, hf * HK, i, l16, lq);
             if (i < 5) pf.read(sm.P, hf, i, l16, lq);
             const int j = i / 4;
@@ -443,6 +450,7 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) dST[j] *= *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
         qf.mul(dST, dO, [&](int i) {
+            if (i % 4 == 1 && kEarlyR + kMidR + i / 4 < 8) load(nxt, kEarlyR + kMidR + i / 4);
             kf.read(sm.Kh, PK, hf * HK, i, l16, lq);
             if (i < 5) tf.read(sm.T, hf, i, l16, lq);
             if (i < 4) bt[i] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * i + 4 * lq]);
@@ -464,10 +472,9 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] = -(bt[t] * sm.ex2[cg][t][lane]);   // -dR
-        const long nxt = max(jc - 2, 0L);   // the first chunk again past the end
         kf.mul(dST, X, [&](int i) {
             if (i % 2 == 0) store(i / 2);
-            else load(nxt, i / 2);
+            else if (i / 2 < kEarlyR) load(nxt2, i / 2);
         });
     }
     if (b.dh0) {
