@@ -414,7 +414,8 @@ GDN_EXPORT int gdn_kda_chunk_bwd(const void* q, const void* k, const void* v, co
         if (x && !aligned(x, 4)) return GDN_ERR_ALIGN;
     const gdn::KdaBwdLayout w = gdn::kda_bwd_workspace_layout(B, T, H, dk, dv, N, cu_seqlens != nullptr);
     if (w.fwd.nc_bound * H > 0x7fffffffL) return GDN_ERR_SHAPE;
-    // work-groups of 256 threads per (sequence, head, 32 columns) and (chunk, head, 64 channels), fewer than 2^32 threads
+    // two work-groups of 512 threads per (sequence, head, 64 columns), one of 256 per (chunk, head, 64 channels): fewer than
+    // 2^32 threads each
     if ((long long)N * H >= 1 << 21 || (long long)w.fwd.nc_bound * H >= 1 << 23) return GDN_ERR_SHAPE;
     if (w.total > 0 && (!workspace || workspace_bytes < w.total)) return GDN_ERR_WORKSPACE;
     if (workspace && !aligned(workspace, 256)) return GDN_ERR_ALIGN;

@@ -18,8 +18,8 @@
 //     dg = the reverse cumulative sum of dgamma in the chunk + that.
 // (dbeta needs no second look at A: sum_i dA[r,i] G[r,i] = k_r . al_r, and Y_r . R_r = Y_r . V_r - (Y S)_r . Kh_r.)
 //
-// Four kernels: the forward pass's stage 1 with fp32 operators (which also keeps T); a walk over the chunks of each sequence
-// that keeps the state entering each chunk and D; the reverse walk that keeps dS' and Y; and one that takes
+// Three kernels: the forward pass's stage 1 with fp32 operators (which also keeps T); the two walks over the chunks of each
+// sequence, forwards for the state entering each chunk and D, backwards for dS' and Y; and one that takes
 // every chunk by itself. All arithmetic is fp32 for both input types (fp32 matrix core, 16x16x4): dg is a reverse cumulative
 // sum of differences, so rounding any product operand to 16 bits would show in it many times over.
 // No e^{-gamma} is formed: a product over rows of different 16-row blocks is factored through gamma at the block
@@ -43,18 +43,67 @@ __device__ __forceinline__ float buf_in(__amdgpu_buffer_rsrc_t r, int off) {
     if constexpr (sizeof(TIn) == 2) return to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
     else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
 }
-// A [64, W] fp32 matrix of the workspace on its way into LDS (row pitch P), 256 threads: NV 16-byte pieces per thread,
-// held in registers between load and store.
-template <int W, int P>
+// Keeps the compiler from moving memory accesses across: without it, it reads the operands of whole unrolled sections
+// ahead and spills what it read.
+__device__ __forceinline__ void pin() { asm volatile("" ::: "memory"); }
+
+// Makes the compiler have x in a register at this point of the program.
+__device__ __forceinline__ void hold(float& x) { asm volatile("" : "+v"(x)); }
+
+// ------------------------------------------------------------------- the two walks
+// The state walk (S entering each chunk, D) and the reverse walk (dS' leaving each chunk, Y) do not need each other and
+// run side by side in one launch. One work-group of eight waves per walk, (sequence, head) and tile of 64 columns of d_v (one
+// tile of 32 columns on four waves each, one walk after the other, moved twice the operands through the L2, which bound them:
+// 357 us for the training shape). Wave w has the 16 columns cg = w & 3 and the half hf = w >> 2 of the d_k channels: S^T [dk/2,
+// 16] in accumulator registers. Per chunk each wave forms its half of the products over d_k for all 64 rows, the two halves
+// are added through LDS, the triangular product (M, or T^T) is shared by row tiles ({0, 3} and {1, 2}: five block
+// products each), and each wave updates its own channels. Operators go global -> registers -> LDS a chunk ahead, all of
+// these memory instructions placed between the products, whose steps hide them.
+constexpr int kWalkThreads = 512;
+constexpr int kWalkPitch = 4;   // pad of an operator row in LDS (floats)
+
+// A [64, W] fp32 operator on its way into LDS (row pitch W + kWalkPitch): NV 16-byte pieces per thread, held in registers
+// between load and store.
+template <int W>
 struct WalkTile {
-    static constexpr int NV = 64 * W / 4 / 256;
+    static constexpr int NV = 64 * W / 4 / kWalkThreads;
     f32x4_t x[NV];
     __device__ __forceinline__ void load(const float* src, int i, int tid) {
-        x[i] = *reinterpret_cast<const f32x4_t*>(src + 4 * (tid + 256 * i));
+        x[i] = *reinterpret_cast<const f32x4_t*>(src + 4 * (tid + kWalkThreads * i));
     }
     __device__ __forceinline__ void store(float* dst, int i, int tid) const {
-        const int e = 4 * (tid + 256 * i);
-        *reinterpret_cast<f32x4_t*>(&dst[(e / W) * P + e % W]) = x[i];
+        const int e = 4 * (tid + kWalkThreads * i);
+        *reinterpret_cast<f32x4_t*>(&dst[(e / W) * (W + kWalkPitch) + e % W]) = x[i];
+    }
+};
+
+// Lower triangular [64, 64] matrices keep only their ten lower 16x16 tiles in LDS, tile (I, J) at I (I + 1) / 2 + J, its
+// rows permuted so that the four rows 4 lq + s of a column read are in different banks.
+constexpr int kTriFloats = 10 * 256;
+__device__ __forceinline__ int tri_tile(int I, int J) { return (I * (I + 1) / 2 + J) * 256; }
+__device__ __forceinline__ int tri_row(int r) { return ((r & ~3) | ((r ^ (r >> 2)) & 3)) * 16; }
+// NM such matrices on their way into LDS, one after the other: 640 pieces each.
+template <int NM>
+struct WalkTri {
+    static constexpr int NP = 640 * NM, NV = (NP + kWalkThreads - 1) / kWalkThreads;
+    f32x4_t x[NV];
+    static __device__ __forceinline__ void place(int i, int tid, int& m, int& I, int& J, int& r, int& c) {
+        const int n = min(tid + kWalkThreads * i, NP - 1), tile = n % 640 / 64;
+        m = n / 640;
+        I = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
+        J = tile - I * (I + 1) / 2;
+        r = n % 64 / 4;
+        c = 4 * (n % 4);
+    }
+    __device__ __forceinline__ void load(const float* a, const float* b, int i, int tid) {
+        int m, I, J, r, c;
+        place(i, tid, m, I, J, r, c);
+        x[i] = *reinterpret_cast<const f32x4_t*>((m ? b : a) + (16 * I + r) * 64 + 16 * J + c);
+    }
+    __device__ __forceinline__ void store(float* dst, int i, int tid) const {   // threads past the end write the last piece again
+        int m, I, J, r, c;
+        place(i, tid, m, I, J, r, c);
+        *reinterpret_cast<f32x4_t*>(&dst[m * kTriFloats + tri_tile(I, J) + tri_row(r) + c]) = x[i];
     }
 };
 
@@ -88,23 +137,14 @@ struct TokenCols {
     }
 };
 
-// Keeps the compiler from moving memory accesses across: without it, it reads the operands of whole unrolled sections
-// ahead and spills what it read.
-__device__ __forceinline__ void pin() { asm volatile("" ::: "memory"); }
-
-// Makes the compiler have x in a register at this point of the program.
-__device__ __forceinline__ void hold(float& x) { asm volatile("" : "+v"(x)); }
-
-// Products of the walks. A wave has a SIMD to itself there, so whatever it waits for stands still: every product takes
-// step(0) .. step(15) between its matrix instructions, the memory instructions of what comes next, which the matrix core
-// hides. Rows: operands are 16-byte pieces of the rows 16 t + l16 of a [64, P] matrix (block j: 16 channels), read here
-// one block ahead. Cols: column c + l16 of the rows 16 t2 + 4 lq + s, read in the steps of an earlier product.
+// acc[t] += the wave's channels (from c0) of the rows of tile t of m [64, P] times b, operands read one block of 16
+// channels ahead; step(0) .. step(15) run between the products.
 template <int NJ, typename F>
 __device__ __forceinline__ void mul_rows(f32x4_t (&acc)[4], const float* m, int pitch, int c0, const f32x4_t (&b)[NJ], int l16, int lq, F step) {
-    f32x4_t a[NJ][4];
+    f32x4_t a[2][4];
     auto read = [&](int j) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) a[j][t] = *reinterpret_cast<const f32x4_t*>(&m[(16 * t + l16) * pitch + c0 + 16 * j + 4 * lq]);
+        for (int t = 0; t < 4; ++t) a[j & 1][t] = *reinterpret_cast<const f32x4_t*>(&m[(16 * t + l16) * pitch + c0 + 16 * j + 4 * lq]);
     };
     read(0);
 #pragma unroll
@@ -114,37 +154,37 @@ __device__ __forceinline__ void mul_rows(f32x4_t (&acc)[4], const float* m, int 
             if (s == 0 && j + 1 < NJ) read(j + 1);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) acc[t] = mfma4(a[j][t][s], b[j][s], acc[t]);
+            for (int t = 0; t < 4; ++t) acc[t] = mfma4(a[j & 1][t][s], b[j][s], acc[t]);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 4 / NJ; ++i) step((4 * j + s) * (4 / NJ) + i);
         }
     __builtin_amdgcn_sched_barrier(0);
 }
-template <int NJ>
-struct ColFrags {
-    f32x4_t a[4][NJ];
-    __device__ __forceinline__ void read(const float* m, int pitch, int c0, int i, int l16, int lq) {   // i = 0 .. 15
-        const int t2 = i / 4, s = i % 4;
+// acc[j] += m^T (its columns c0 + 16 j + l16) times b over the 64 rows, operands read two steps ahead.
+template <int NJ, typename F>
+__device__ __forceinline__ void mul_cols(f32x4_t (&acc)[NJ], const float* m, int pitch, int c0, const f32x4_t (&b)[4], int l16, int lq, F step) {
+    float a[4][NJ];
+    auto read = [&](int i) {   // row 16 (i / 4) + 4 lq + i % 4
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) a[t2][j][s] = m[(16 * t2 + 4 * lq + s) * pitch + c0 + 16 * j + l16];
+        for (int j = 0; j < NJ; ++j) a[i & 3][j] = m[(16 * (i / 4) + 4 * lq + i % 4) * pitch + c0 + 16 * j + l16];
+    };
+    read(0);
+    read(1);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (i + 2 < 16) read(i + 2);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[j] = mfma4(a[i & 3][j], b[i / 4][i % 4], acc[j]);
+        __builtin_amdgcn_sched_barrier(0);
+        step(i);
     }
-    // acc[j] += columns of block j times b
-    template <typename F>
-    __device__ __forceinline__ void mul(f32x4_t (&acc)[NJ], const f32x4_t (&b)[4], F step) const {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[j] = mfma4(a[i / 4][j][i % 4], b[i / 4][i % 4], acc[j]);
-            __builtin_amdgcn_sched_barrier(0);
-            step(i);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-};
-// The wave's share of a product with a lower triangular [64, 64] matrix m (TRANS: with m^T): row tiles 0 and 3 for
-// hf = 0, 1 and 2 for hf = 1, five block products either way. d0, d1: the lower and the higher row tile.
-template <bool TRANS, int PC>
+    __builtin_amdgcn_sched_barrier(0);
+}
+// The wave's share of a product with a lower triangular matrix m (TRANS: with m^T): row tiles 0 and 3 for hf = 0, 1 and 2
+// for hf = 1, five block products either way.
+template <bool TRANS>
 struct TriFrags {
     f32x4_t a[5];
     // block of (row tile, contraction tile) number i: (0,0) (3,0) (3,1) (3,2) (3,3) or (1,0) (1,1) (2,0) (2,1) (2,2);
@@ -161,9 +201,9 @@ struct TriFrags {
         const int t = hf == 0 ? row<0>(i) : row<1>(i), t2 = hf == 0 ? con<0>(i) : con<1>(i);
         if constexpr (TRANS) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) a[i][s] = m[(16 * t2 + 4 * lq + s) * PC + 16 * t + l16];
+            for (int s = 0; s < 4; ++s) a[i][s] = m[tri_tile(t2, t) + tri_row(4 * lq + s) + l16];
         } else {
-            a[i] = *reinterpret_cast<const f32x4_t*>(&m[(16 * t + l16) * PC + 16 * t2 + 4 * lq]);
+            a[i] = *reinterpret_cast<const f32x4_t*>(&m[tri_tile(t, t2) + tri_row(l16) + 4 * lq]);
         }
     }
     // The two row tiles of the product with x, each block's product on its own accumulator
@@ -187,26 +227,27 @@ struct TriFrags {
     static __device__ __forceinline__ int second_tile(int hf) { return TRANS ? (hf == 0 ? 0 : 1) : (hf == 0 ? 3 : 2); }
 };
 
-// ------------------------------------------------------------------- the two walks
-// One work-group of four waves per (sequence, head, 32-column tile of d_v). Wave w has the 16 columns cg = w & 1 and the
-// half hf = w >> 1 of the d_k channels: S^T [dk/2, 16] in accumulator registers. Per chunk each wave forms its half of the
-// products over d_k for all 64 rows, the two halves are added through LDS, the triangular product (M, or T^T) is shared
-// by row tiles ({0, 3} and {1, 2}: five block products each), and each wave updates its own channels. The next
-// chunk's operands are loaded into registers between the products before the first exchange; by then every operand
-// has been read from LDS, so they are written over it between the products of the state update (a probe of an earlier form,
-// which issued the loads in one go, showed 3,000 of a chunk's 13,500 cycles in their issue and 1,200 in the LDS writes).
-constexpr int kEarlyS = 4;              // shares of the loads issued in the state update, the rest in the next chunk's X
-constexpr int kEarlyR = 4, kMidR = 2;   // the reverse walk's, and those in its Kd dS'^T; the rest in Qh^T dO
-
 template <int DK>
 struct alignas(16) KdaStateSmem {
-    static constexpr int PK = DK + 4, PC = 68;
-    float Kh[64 * PK];
-    float Kd[64 * PK];
-    float M[64 * PC];
+    float Kh[64 * (DK + kWalkPitch)];
+    float Kd[64 * (DK + kWalkPitch)];
+    float M[kTriFloats];
     float lam[DK];
-    f32x4_t ex[4][4][64];    // each wave's partial products, row tile by row tile
-    f32x4_t ex2[2][4][64];   // the triangular product, per column group
+    f32x4_t ex[8][4][64];    // each wave's partial products, row tile by row tile
+    f32x4_t ex2[4][4][64];   // the triangular product, per column group
+};
+template <int DK>
+struct alignas(16) KdaRevSmem {
+    float Kd[64 * (DK + kWalkPitch)];
+    union {
+        float Qh[64 * (DK + kWalkPitch)];
+        f32x4_t ex2[4][4][64];
+    };
+    float Kh[64 * (DK + kWalkPitch)];
+    float PT[2 * kTriFloats];   // P, then T
+    float lam[DK];
+    float beta[64];
+    f32x4_t ex[8][4][64];
 };
 
 struct Chain {   // the chunks of the work-group's (sequence, head)
@@ -214,11 +255,11 @@ struct Chain {   // the chunks of the work-group's (sequence, head)
     int h, tile;
 };
 template <int NTILE>
-__device__ __forceinline__ Chain chain_of(const ChunkProblem& p) {
+__device__ __forceinline__ Chain chain_of(const ChunkProblem& p, long b, long nb) {
     Chain c;
     // Work-groups go to the eight XCDs in turn; the tiles of one pair read the same operators, so in every full group
     // of eight pairs they are eight apart and share an XCD's L2.
-    const long b = blockIdx.x, full = (gridDim.x / (8 * NTILE)) * (8 * NTILE);
+    const long full = nb / (8 * NTILE) * (8 * NTILE);
     const long slot = b < full ? b / (8 * NTILE) * 8 + b % 8 : b / NTILE;
     c.tile = (int)(b < full ? b / 8 % NTILE : b % NTILE);
     // packed sequences are taken longest first (the chunk table's order)
@@ -232,84 +273,81 @@ __device__ __forceinline__ Chain chain_of(const ChunkProblem& p) {
     return c;
 }
 
+// Barriers of a chunk: (1) its first operators are in LDS; (2) all partial products are exchanged, and the rest of the
+// operators are in; (3) the triangular product is exchanged.
 template <typename TIn, int DK, int DV>
-__global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
-    using SM = KdaStateSmem<DK>;
-    constexpr int PK = SM::PK, PC = SM::PC, HK = DK / 2, NJ = HK / 16;
-    __shared__ SM sm;
+__device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem<DK>& sm, const Chain& c, int tid) {
+    constexpr int PK = DK + kWalkPitch, HK = DK / 2, NJ = HK / 16, NV = WalkTile<DK>::NV;
     const ChunkProblem& p = b.f;
-    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 1, hf = wave >> 1;
-    const Chain c = chain_of<DV / 32>(p);
-    const int H = p.H, col = 32 * c.tile + 16 * cg + l16;
+    const int lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 3, hf = wave >> 2;
+    const int H = p.H, col0 = 64 * c.tile + 16 * cg, col = col0 + l16;
 
     f32x4_t ST[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
         ST[j] = p.h0 ? *reinterpret_cast<const f32x4_t*>(p.h0 + (c.pair * DV + col) * DK + hf * HK + 16 * j + 4 * lq)
                      : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (c.nchunks == 0) return;
 
-    WalkTile<DK, PK> kh, kd;
-    WalkTile<64, PC> mt;
+    WalkTile<DK> kh, kd;
+    WalkTri<1> mt;
     TokenCols<TIn, DV> v;
     float lam = 0.f;
     float* own = reinterpret_cast<float*>(&sm.ex[wave][0][0]);
-    constexpr int NV = WalkTile<DK, PK>::NV;
-    auto load = [&](long jc, int i) {   // i = 0 .. 7: a share of the chunk's loads
+    // the chunk's first operators (Kh, V) and the rest (Kd, M, lam), each in up to eight shares
+    auto load1 = [&](long jc, int i) {
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
-        if (i < NV) {
-            kh.load(p.khat + widx * 64 * DK, i, tid);
-            kd.load(p.kdec + widx * 64 * DK, i, tid);
-        }
-        if (i < 4) mt.load(static_cast<const float*>(p.mmat) + widx * 4096, i, tid);
-        if (i == 4) lam = p.lam[widx * DK + tid % DK];
-        if (i >= 4 && i - 4 < v.NV) v.load(p.v, bos, (int)min(64L, c.seos - bos), H, c.h, 32 * c.tile + 16 * cg, i - 4, lane);
+        if (i < NV) kh.load(p.khat + widx * 64 * DK, i, tid);
+        if (i >= 4 && i - 4 < v.NV) v.load(p.v, bos, (int)min(64L, c.seos - bos), H, c.h, col0, i - 4, lane);
     };
-    auto store = [&](int i) {           // and of its LDS writes
-        if (i < NV) {
-            kh.store(sm.Kh, i, tid);
-            kd.store(sm.Kd, i, tid);
-        }
-        if (i < 4) mt.store(sm.M, i, tid);
-        if (i == 4) sm.lam[tid % DK] = lam;
+    auto store1 = [&](int i) {
+        if (i < NV) kh.store(sm.Kh, i, tid);
         if (i >= 4 && i - 4 < v.NV) v.store(own, i - 4, lane);
     };
-    if (c.nchunks > 0) {
+    auto load2 = [&](long jc, int i) {
+        const long widx = (c.cbase + jc) * H + c.h;
+        if (i < NV) kd.load(p.kdec + widx * 64 * DK, i, tid);
+        if (i >= 4 && i - 4 < mt.NV) mt.load(static_cast<const float*>(p.mmat) + widx * 4096, nullptr, i - 4, tid);
+        if (i == 7) lam = p.lam[widx * DK + tid % DK];
+    };
+    auto store2 = [&](int i) {
+        if (i < NV) kd.store(sm.Kd, i, tid);
+        if (i >= 4 && i - 4 < mt.NV) mt.store(sm.M, i - 4, tid);
+        if (i == 7) sm.lam[tid % DK] = lam;
+    };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load(0, i);
+    for (int i = 0; i < 8; ++i) load1(0, i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) store(i);
+    for (int i = 0; i < 8; ++i) load2(0, i);
 #pragma unroll
-        for (int i = 0; i < kEarlyS; ++i) load(min(1L, c.nchunks - 1), i);
-    }
+    for (int i = 0; i < 8; ++i) store1(i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load1(min(1L, c.nchunks - 1), i);
+
     for (long jc = 0; jc < c.nchunks; ++jc) {
         const long widx = (c.cbase + jc) * H + c.h;
+        const long nxt = min(jc + 1, c.nchunks - 1), nxt2 = min(jc + 2, c.nchunks - 1);   // the last chunk again at the end
         f32x4_t X[4], D[4];
-        __syncthreads();   // the chunk's operands are in LDS
+        __syncthreads();   // (1)
         TokenCols<TIn, DV>::get(own, D, lane);   // V, until R is formed
         // this half of X = Kh S^T
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        TriFrags<false, PC> m;
-        ColFrags<NJ> kf;
-        f32x4_t lm[NJ];
-        const long nxt = min(jc + 1, c.nchunks - 1), nxt2 = min(jc + 2, c.nchunks - 1);   // the last chunk again at the end
         mul_rows<NJ>(X, sm.Kh, PK, hf * HK, ST, l16, lq, [&](int i) {
-            if (i % 4 == 1 && kEarlyS + i / 4 < 8) load(nxt, kEarlyS + i / 4);
-            if (i % 4 == 3 && kEarlyS + 4 + i / 4 < 8) load(nxt, kEarlyS + 4 + i / 4);
-            kf.read(sm.Kd, PK, hf * HK, i, l16, lq);
-            if (i < 5) m.read(sm.M, hf, i, l16, lq);
+            if (i % 2 == 0) store2(i / 2);
             const int j = i / 4;
-            if (i % 4 == 0 && j < NJ) {
+            if (i % 4 == 1 && j < NJ)
                 *reinterpret_cast<f32x4_t*>(p.states + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = ST[j];
-                lm[j] = *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
-            }
         });
 #pragma unroll
         for (int t = 0; t < 4; ++t) sm.ex[wave][t][lane] = X[t];
-        __syncthreads();
+        __syncthreads();   // (2)
+        TriFrags<false> m;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) X[t] = D[t] - (X[t] + sm.ex[wave ^ 2][t][lane]);   // R
+        for (int i = 0; i < 5; ++i) m.read(sm.M, hf, i, l16, lq);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) X[t] = D[t] - (X[t] + sm.ex[wave ^ 4][t][lane]);   // R
         // D = M R on the wave's row tiles
         {
             f32x4_t d[2];
@@ -321,103 +359,95 @@ __global__ __launch_bounds__(256) void kda_bwd_states_kernel(KdaBwdProblem b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[(16 * ta + i) * DV] = d[0][i], dst[(16 * tb + i) * DV] = d[1][i];
         }
-        __syncthreads();
+        f32x4_t lm[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) lm[j] = *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
+        __syncthreads();   // (3)
 #pragma unroll
         for (int t = 0; t < 4; ++t) D[t] = sm.ex2[cg][t][lane];
         // S^T <- Diag(lam) S^T + Kd^T D on the wave's channels
 #pragma unroll
         for (int j = 0; j < NJ; ++j) ST[j] *= lm[j];
-        kf.mul(ST, D, [&](int i) {
-            if (i % 2 == 0) store(i / 2);
-            else if (i / 2 < kEarlyS) load(nxt2, i / 2);
+        mul_cols<NJ>(ST, sm.Kd, PK, hf * HK, D, l16, lq, [&](int i) {
+            if (i % 2 == 0) store1(i / 2), load2(nxt, i / 2);
+            else load1(nxt2, i / 2);
         });
     }
 }
 
-template <int DK>
-struct alignas(16) KdaRevSmem {
-    static constexpr int PK = DK + 4, PC = 68;
-    float Kh[64 * PK];
-    float Qh[64 * PK];
-    float Kd[64 * PK];
-    float P[64 * PC];
-    float T[64 * PC];
-    float lam[DK];
-    float beta[64];
-    f32x4_t ex[4][4][64];
-    f32x4_t ex2[2][4][64];
-};
-
+// Barriers of a chunk: (1) Kd, P, T and dO are in LDS; (2) all partial products are exchanged, and Qh, Kh, lam and beta
+// are in; (3) Qh is dead; (4) the triangular product is exchanged (over Qh).
 template <typename TIn, int DK, int DV>
-__global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
-    using SM = KdaRevSmem<DK>;
-    constexpr int PK = SM::PK, PC = SM::PC, HK = DK / 2, NJ = HK / 16;
-    __shared__ SM sm;
+__device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK>& sm, const Chain& c, int tid) {
+    constexpr int PK = DK + kWalkPitch, HK = DK / 2, NJ = HK / 16, NV = WalkTile<DK>::NV;
     const ChunkProblem& p = b.f;
-    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 1, hf = wave >> 1;
-    const Chain c = chain_of<DV / 32>(p);
-    const int H = p.H, col = 32 * c.tile + 16 * cg + l16;
+    const int lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 3, hf = wave >> 2;
+    const int H = p.H, col0 = 64 * c.tile + 16 * cg, col = col0 + l16;
 
     f32x4_t dST[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
         dST[j] = b.dhT ? *reinterpret_cast<const f32x4_t*>(b.dhT + (c.pair * DV + col) * DK + hf * HK + 16 * j + 4 * lq)
                        : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto finish = [&]() {
+        if (b.dh0) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                *reinterpret_cast<f32x4_t*>(b.dh0 + (c.pair * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = dST[j];
+        }
+    };
+    if (c.nchunks == 0) return finish();
 
-    WalkTile<DK, PK> kh, qh, kd;
-    WalkTile<64, PC> pt, tt;
+    WalkTile<DK> kh, qh, kd;
+    WalkTri<2> pt;
     TokenCols<TIn, DV> dof;
     float lam = 0.f, beta = 0.f;
     float* own = reinterpret_cast<float*>(&sm.ex[wave][0][0]);
-    constexpr int NV = WalkTile<DK, PK>::NV;
-    auto load = [&](long jc, int i) {   // i = 0 .. 7: a share of the chunk's loads
+    auto load1 = [&](long jc, int i) {   // Kd, P, T, dO
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
-        const int len = (int)min(64L, c.seos - bos);
-        if (i < NV) {
-            kh.load(p.khat + widx * 64 * DK, i, tid);
-            qh.load(p.qhat + widx * 64 * DK, i, tid);
-            kd.load(p.kdec + widx * 64 * DK, i, tid);
-        }
-        if (i < 4) {
-            pt.load(static_cast<const float*>(p.pmat) + widx * 4096, i, tid);
-            tt.load(p.tmat + widx * 4096, i, tid);
-        }
-        if (i == 4) {
+        if (i < NV) kd.load(p.kdec + widx * 64 * DK, i, tid);
+        if (i >= 4 && i - 4 < pt.NV) pt.load(static_cast<const float*>(p.pmat) + widx * 4096, p.tmat + widx * 4096, i - 4, tid);
+        if (i < dof.NV) dof.load(b.d_o, bos, (int)min(64L, c.seos - bos), H, c.h, col0, i, lane);
+    };
+    auto store1 = [&](int i) {
+        if (i < NV) kd.store(sm.Kd, i, tid);
+        if (i >= 4 && i - 4 < pt.NV) pt.store(sm.PT, i - 4, tid);
+        if (i < dof.NV) dof.store(own, i, lane);
+    };
+    auto load2 = [&](long jc, int i) {   // Qh, Kh, lam, beta
+        const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
+        if (i < NV) qh.load(p.qhat + widx * 64 * DK, i, tid);
+        if (i >= 4 && i - 4 < NV) kh.load(p.khat + widx * 64 * DK, i - 4, tid);
+        if (i == 7) {
+            const int len = (int)min(64L, c.seos - bos);
             lam = p.lam[widx * DK + tid % DK];
             const auto br = make_rsrc(p.beta + bos * H + c.h, (unsigned)(((len - 1) * H + 1) * 4));
             beta = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(br, (tid & 63) * H * 4, 0, 0));
         }
-        if (i >= 4 && i - 4 < dof.NV) dof.load(b.d_o, bos, len, H, c.h, 32 * c.tile + 16 * cg, i - 4, lane);
     };
-    auto store = [&](int i) {           // and of its LDS writes
-        if (i < NV) {
-            kh.store(sm.Kh, i, tid);
-            qh.store(sm.Qh, i, tid);
-            kd.store(sm.Kd, i, tid);
-        }
-        if (i < 4) {
-            pt.store(sm.P, i, tid);
-            tt.store(sm.T, i, tid);
-        }
-        if (i == 4) {
+    auto store2 = [&](int i) {
+        if (i < NV) qh.store(sm.Qh, i, tid);
+        if (i >= 4 && i - 4 < NV) kh.store(sm.Kh, i - 4, tid);
+        if (i == 7) {
             sm.lam[tid % DK] = lam;
             sm.beta[tid & 63] = beta;
         }
-        if (i >= 4 && i - 4 < dof.NV) dof.store(own, i - 4, lane);
     };
-    if (c.nchunks > 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load(c.nchunks - 1, i);
+    for (int i = 0; i < 8; ++i) load1(c.nchunks - 1, i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) store(i);
+    for (int i = 0; i < 8; ++i) load2(c.nchunks - 1, i);
 #pragma unroll
-        for (int i = 0; i < kEarlyR; ++i) load(max(0L, c.nchunks - 2), i);
-    }
+    for (int i = 0; i < 8; ++i) store1(i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load1(max(c.nchunks - 2, 0L), i);
+
     for (long jc = c.nchunks - 1; jc >= 0; --jc) {
         const long widx = (c.cbase + jc) * H + c.h;
+        const long nxt = max(jc - 1, 0L), nxt2 = max(jc - 2, 0L);   // the first chunk again at the end
         f32x4_t dO[4], X[4];
-        __syncthreads();   // the chunk's operands are in LDS
+        __syncthreads();   // (1)
         TokenCols<TIn, DV>::get(own, dO, lane);
         if constexpr (DK == 128) {   // the chunk gradients add their halves to it
             const int len = (int)min(64L, c.seos - (c.sbos + jc * 64));
@@ -426,15 +456,12 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
         // this wave's share of dD = Kd dS'^T + P^T dO: its half of the channels, and of the row tiles of P^T dO ({3, 0}, {2, 1})
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        ColFrags<NJ> qf, kf;
-        TriFrags<true, PC> pf, tf;
-        const long nxt = max(jc - 1, 0L), nxt2 = max(jc - 2, 0L);   // the first chunk again at the end
+        TriFrags<true> pf;
         mul_rows<NJ>(X, sm.Kd, PK, hf * HK, dST, l16, lq, [&](int i) {
-            if (i % 4 == 1 && i / 4 < kMidR) load(nxt, kEarlyR + i / 4);
-            qf.read(sm.Qh, PK, hf * HK, i, l16, lq);
-            if (i < 5) pf.read(sm.P, hf, i, l16, lq);
+            if (i % 2 == 0) store2(i / 2);
+            if (i >= 11) pf.read(sm.PT, hf, i - 11, l16, lq);
             const int j = i / 4;
-            if (i % 4 == 0 && j < NJ)
+            if (i % 4 == 1 && j < NJ)
                 *reinterpret_cast<f32x4_t*>(b.dstates + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = dST[j];
         });
         {
@@ -445,19 +472,17 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) sm.ex[wave][t][lane] = X[t];
+        __syncthreads();   // (2)
         // dS'^T Diag(lam) + Qh^T dO on the wave's channels
-        f32x4_t bt[4];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) dST[j] *= *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
-        qf.mul(dST, dO, [&](int i) {
-            if (i % 4 == 1 && kEarlyR + kMidR + i / 4 < 8) load(nxt, kEarlyR + kMidR + i / 4);
-            kf.read(sm.Kh, PK, hf * HK, i, l16, lq);
-            if (i < 5) tf.read(sm.T, hf, i, l16, lq);
-            if (i < 4) bt[i] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * i + 4 * lq]);
+        TriFrags<true> tf;
+        mul_cols<NJ>(dST, sm.Qh, PK, hf * HK, dO, l16, lq, [&](int i) {
+            if (i % 2 == 0) load2(nxt, i / 2);
+            if (i < 4) X[i] += sm.ex[wave ^ 4][i][lane];   // dD
+            if (i >= 11) tf.read(sm.PT + kTriFloats, hf, i - 11, l16, lq);
         });
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < 4; ++t) X[t] += sm.ex[wave ^ 2][t][lane];   // dD
+        __syncthreads();   // (3)
         // Y = T^T dD on the wave's row tiles
         {
             f32x4_t y[2];
@@ -469,19 +494,29 @@ __global__ __launch_bounds__(256) void kda_bwd_reverse_kernel(KdaBwdProblem b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[(16 * ta + i) * DV] = y[0][i], dst[(16 * tb + i) * DV] = y[1][i];
         }
-        __syncthreads();
+        __syncthreads();   // (4)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) X[t] = -(bt[t] * sm.ex2[cg][t][lane]);   // -dR
-        kf.mul(dST, X, [&](int i) {
-            if (i % 2 == 0) store(i / 2);
-            else if (i / 2 < kEarlyR) load(nxt2, i / 2);
+        for (int t = 0; t < 4; ++t)   // -dR
+            X[t] = -(*reinterpret_cast<const f32x4_t*>(&sm.beta[16 * t + 4 * lq]) * sm.ex2[cg][t][lane]);
+        mul_cols<NJ>(dST, sm.Kh, PK, hf * HK, X, l16, lq, [&](int i) {
+            if (i % 2 == 0) store1(i / 2);
+            else load1(nxt2, i / 2);
         });
     }
-    if (b.dh0) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            *reinterpret_cast<f32x4_t*>(b.dh0 + (c.pair * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = dST[j];
-    }
+    finish();
+}
+
+// The reverse walks are the longer ones and come first.
+template <typename TIn, int DK, int DV>
+__global__ __launch_bounds__(kWalkThreads) void kda_bwd_walk_kernel(KdaBwdProblem b) {
+    __shared__ union Smem {
+        __device__ Smem() {}
+        KdaRevSmem<DK> back;
+        KdaStateSmem<DK> states;
+    } sm;
+    const long half = gridDim.x / 2;
+    if (blockIdx.x < half) walk_back<TIn, DK, DV>(b, sm.back, chain_of<DV / 64>(b.f, blockIdx.x, half), threadIdx.x);
+    else walk_states<TIn, DK, DV>(b, sm.states, chain_of<DV / 64>(b.f, blockIdx.x - half, half), threadIdx.x);
 }
 
 // ------------------------------------------------------------------- gradients of each chunk
@@ -928,9 +963,8 @@ static hipError_t kda_bwd_launch(const KdaBwdProblem& b, hipStream_t s) {
     const ChunkProblem& p = b.f;
     const long pairs = (long)p.N * p.H, units = p.nc_bound * p.H;
     if (pairs == 0) return hipSuccess;
-    const dim3 walks((unsigned)(pairs * (DV / 32)));
-    hipError_t e = launch(kda_bwd_states_kernel<TIn, DK, DV>, walks, dim3(256), s, b);
-    if (e == hipSuccess) e = launch(kda_bwd_reverse_kernel<TIn, DK, DV>, walks, dim3(256), s, b);
+    const dim3 walks((unsigned)(2 * pairs * (DV / 64)));
+    const hipError_t e = launch(kda_bwd_walk_kernel<TIn, DK, DV>, walks, dim3(kWalkThreads), s, b);
     if (e != hipSuccess || units == 0) return e;
     const dim3 grid((unsigned)(units * (DK / 64)));
     return b.grad_bf16 ? launch(kda_bwd_grad_kernel<TIn, uint16_t, DK, DV>, grid, dim3(256), s, b)
