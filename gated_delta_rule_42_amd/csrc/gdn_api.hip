@@ -430,13 +430,12 @@ GDN_EXPORT int gdn_kda_chunk_bwd(const void* q, const void* k, const void* v, co
     P.nc_per_seq = (T + 63) / 64;
     P.chunk_base = cu_seqlens ? reinterpret_cast<int32_t*>(base + w.fwd.off_base) : nullptr;
     if (w.fwd.nc_bound > 0) {
-        P.mmat = base + w.fwd.off_m;
+        P.tmat = reinterpret_cast<float*>(base + w.fwd.off_m);   // T in the place of Mmat
         P.pmat = base + w.fwd.off_p;
         P.khat = reinterpret_cast<float*>(base + w.fwd.off_kh);
         P.qhat = reinterpret_cast<float*>(base + w.fwd.off_qh);
         P.kdec = reinterpret_cast<float*>(base + w.fwd.off_kd);
         P.lam = reinterpret_cast<float*>(base + w.fwd.off_lam);
-        P.tmat = reinterpret_cast<float*>(base + w.off_t);
         P.states = reinterpret_cast<float*>(base + w.off_states);
         b.dstates = reinterpret_cast<float*>(base + w.off_dstates);
         b.delta = reinterpret_cast<float*>(base + w.off_delta);

@@ -193,7 +193,8 @@ hipError_t launch_kda_chunk_fwd(const ChunkProblem& p, hipStream_t s);
 // The log decay that the backward pass takes for any smaller one: e^-104 is below half of fp32's smallest number.
 constexpr float kMinLogDecay = -104.f;
 
-// The channel-wise stage 1 with fp32 operators and products for either input type, and T into p.tmat.
+// The channel-wise stage 1 with fp32 operators and products for either input type; T into p.tmat instead of Mmat, and of T
+// and P the lower 16x16 tiles only.
 hipError_t launch_kda_prepare_f32(const ChunkProblem& p, hipStream_t s);
 
 // Backward pass of the channel-wise rule (gdn_kda_bwd.hip). `f`: the forward problem with the fp32 regions of stage 1, tmat
@@ -215,7 +216,7 @@ struct KdaBwdProblem {
 };
 struct KdaBwdLayout {
     KdaLayout fwd;
-    size_t off_t, off_states, off_dstates, off_delta, off_y, total;
+    size_t off_states, off_dstates, off_delta, off_y, total;
 };
 KdaBwdLayout kda_bwd_workspace_layout(int B, int T, int H, int dk, int dv, int N, int varlen);
 hipError_t launch_kda_chunk_bwd(const KdaBwdProblem& p, hipStream_t s);

@@ -469,7 +469,7 @@ struct KdaPrepStage {
 // decoupled gates (DEC) the erased read runs along E * K, so A's left operand is E * K (held
 // in the Q buffer until A is formed, then Q is moved there from its raw copy in P), Kh is
 // E * K * e^gamma, V is scaled by the write gate in stage 2 and Mmat is T itself.
-// F32OP: fp32 operators and fp32 products for either input type (the backward pass, which also takes T itself).
+// F32OP: fp32 operators and fp32 products for either input type (the backward pass, which takes T in place of Mmat).
 template <typename TIn, int DK, bool DEC, bool F32OP = sizeof(TIn) == 4>
 __global__ __launch_bounds__(kKdaPrepThreads) void kda_prepare_kernel(ChunkProblem p) {
     using SM = KdaPrepSmem<DK>;
@@ -580,18 +580,21 @@ __global__ __launch_bounds__(kKdaPrepThreads) void kda_prepare_kernel(ChunkProbl
 #pragma unroll
             for (int q4 = 0; q4 < NE / 4; ++q4) {
                 const int o = IMG ? img_off<64>(r, c0 + 4 * q4) : r * 64 + c0 + 4 * q4;
+                if constexpr (F32OP && !DEC) {
+                    if (p.tmat) {   // backward pass: T and P, their lower 16x16 tiles only
+                        if ((c0 >> 4) <= (r >> 4)) {
+                            const float* t4 = &sm.T[r * PF + c0 + 4 * q4];
+                            *reinterpret_cast<float4*>(p.tmat + widx * 4096 + o) = make_float4(t4[0], t4[1], t4[2], t4[3]);
+                            put4(static_cast<TM*>(p.pmat) + widx * 4096 + o,
+                                 make_float4(pv[4 * q4], pv[4 * q4 + 1], pv[4 * q4 + 2], pv[4 * q4 + 3]));
+                        }
+                        continue;
+                    }
+                }
                 put4(static_cast<TM*>(p.mmat) + widx * 4096 + o,
                      make_float4(mv[4 * q4], mv[4 * q4 + 1], mv[4 * q4 + 2], mv[4 * q4 + 3]));
                 put4(static_cast<TM*>(p.pmat) + widx * 4096 + o,
                      make_float4(pv[4 * q4], pv[4 * q4 + 1], pv[4 * q4 + 2], pv[4 * q4 + 3]));
-                if constexpr (F32OP && !DEC) {
-                    if (p.tmat) {   // backward pass: T, its upper blocks zero like Mmat's
-                        const bool in = (c0 >> 4) <= (r >> 4);
-                        const float* t4 = &sm.T[r * PF + c0 + 4 * q4];
-                        *reinterpret_cast<float4*>(p.tmat + widx * 4096 + o) =
-                            in ? make_float4(t4[0], t4[1], t4[2], t4[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                }
             }
         }
         unit = nxt; ok = nok; bos = nbos; len = nlen;

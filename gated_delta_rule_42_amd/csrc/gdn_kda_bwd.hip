@@ -18,7 +18,7 @@
 //     dg = the reverse cumulative sum of dgamma in the chunk + that.
 // (dbeta needs no second look at A: sum_i dA[r,i] G[r,i] = k_r . al_r, and Y_r . R_r = Y_r . V_r - (Y S)_r . Kh_r.)
 //
-// Three kernels: the forward pass's stage 1 with fp32 operators (which also keeps T); the two walks over the chunks of each
+// Three kernels: the forward pass's stage 1 with fp32 operators (and T in place of M); the two walks over the chunks of each
 // sequence, forwards for the state entering each chunk and D, backwards for dS' and Y; and one that takes
 // every chunk by itself. All arithmetic is fp32 for both input types (fp32 matrix core, 16x16x4): dg is a reverse cumulative
 // sum of differences, so rounding any product operand to 16 bits would show in it many times over.
@@ -56,7 +56,7 @@ __device__ __forceinline__ void hold(float& x) { asm volatile("" : "+v"(x)); }
 // tile of 32 columns on four waves each, one walk after the other, moved twice the operands through the L2, which bound them:
 // 357 us for the training shape). Wave w has the 16 columns cg = w & 3 and the half hf = w >> 2 of the d_k channels: S^T [dk/2,
 // 16] in accumulator registers. Per chunk each wave forms its half of the products over d_k for all 64 rows, the two halves
-// are added through LDS, the triangular product (M, or T^T) is shared by row tiles ({0, 3} and {1, 2}: five block
+// are added through LDS, the triangular product (with T or T^T) is shared by row tiles ({0, 3} and {1, 2}: five block
 // products each), and each wave updates its own channels. Operators go global -> registers -> LDS a chunk ahead, all of
 // these memory instructions placed between the products, whose steps hide them.
 constexpr int kWalkThreads = 512;
@@ -231,8 +231,9 @@ template <int DK>
 struct alignas(16) KdaStateSmem {
     float Kh[64 * (DK + kWalkPitch)];
     float Kd[64 * (DK + kWalkPitch)];
-    float M[kTriFloats];
+    float T[kTriFloats];
     float lam[DK];
+    float beta[64];
     f32x4_t ex[8][4][64];    // each wave's partial products, row tile by row tile
     f32x4_t ex2[4][4][64];   // the triangular product, per column group
 };
@@ -291,11 +292,11 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
     if (c.nchunks == 0) return;
 
     WalkTile<DK> kh, kd;
-    WalkTri<1> mt;
+    WalkTri<1> tt;
     TokenCols<TIn, DV> v;
-    float lam = 0.f;
+    float lam = 0.f, beta = 0.f;
     float* own = reinterpret_cast<float*>(&sm.ex[wave][0][0]);
-    // the chunk's first operators (Kh, V) and the rest (Kd, M, lam), each in up to eight shares
+    // the chunk's first operators (Kh, V) and the rest (Kd, T, lam, beta), each in up to eight shares
     auto load1 = [&](long jc, int i) {
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
         if (i < NV) kh.load(p.khat + widx * 64 * DK, i, tid);
@@ -308,13 +309,21 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
     auto load2 = [&](long jc, int i) {
         const long widx = (c.cbase + jc) * H + c.h;
         if (i < NV) kd.load(p.kdec + widx * 64 * DK, i, tid);
-        if (i >= 4 && i - 4 < mt.NV) mt.load(static_cast<const float*>(p.mmat) + widx * 4096, nullptr, i - 4, tid);
-        if (i == 7) lam = p.lam[widx * DK + tid % DK];
+        if (i >= 4 && i - 4 < tt.NV) tt.load(p.tmat + widx * 4096, nullptr, i - 4, tid);
+        if (i == 7) {
+            const long bos = c.sbos + jc * 64;
+            const auto br = make_rsrc(p.beta + bos * H + c.h, (unsigned)((((int)min(64L, c.seos - bos) - 1) * H + 1) * 4));
+            lam = p.lam[widx * DK + tid % DK];
+            beta = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(br, (tid & 63) * H * 4, 0, 0));
+        }
     };
     auto store2 = [&](int i) {
         if (i < NV) kd.store(sm.Kd, i, tid);
-        if (i >= 4 && i - 4 < mt.NV) mt.store(sm.M, i - 4, tid);
-        if (i == 7) sm.lam[tid % DK] = lam;
+        if (i >= 4 && i - 4 < tt.NV) tt.store(sm.T, i - 4, tid);
+        if (i == 7) {
+            sm.lam[tid % DK] = lam;
+            sm.beta[tid & 63] = beta;
+        }
     };
 #pragma unroll
     for (int i = 0; i < 8; ++i) load1(0, i);
@@ -345,10 +354,11 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
         __syncthreads();   // (2)
         TriFrags<false> m;
 #pragma unroll
-        for (int i = 0; i < 5; ++i) m.read(sm.M, hf, i, l16, lq);
+        for (int i = 0; i < 5; ++i) m.read(sm.T, hf, i, l16, lq);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) X[t] = D[t] - (X[t] + sm.ex[wave ^ 4][t][lane]);   // R
-        // D = M R on the wave's row tiles
+        for (int t = 0; t < 4; ++t)   // beta R
+            X[t] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * t + 4 * lq]) * (D[t] - (X[t] + sm.ex[wave ^ 4][t][lane]));
+        // D = T beta R on the wave's row tiles
         {
             f32x4_t d[2];
             m.mul(X, hf, d[0], d[1]);
@@ -669,23 +679,6 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         }
     };
     load(0);
-    // k, q, g of the lane's rows and channel
-    float k[16], q[16], gm[16];
-    const long base = (bos * H + h) * DK;
-    {
-        const unsigned rows = (unsigned)((len - 1) * H * DK + DK);
-        const auto kr = make_rsrc(static_cast<const TIn*>(p.k) + base, rows * EB);
-        const auto qr = make_rsrc(static_cast<const TIn*>(p.q) + base, rows * EB);
-        const auto gr = make_rsrc(p.g + base, rows * 4);
-        const int o0 = 16 * lq * H * DK + ch;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int o = o0 + r * H * DK;
-            k[r] = buf_in<TIn>(kr, o * EB);
-            q[r] = buf_in<TIn>(qr, o * EB);
-            gm[r] = buf_in<float>(gr, o * 4);
-        }
-    }
     float bt[2];   // beta of the thread's two piece rows
     {
         const auto br = make_rsrc(p.beta + bos * H + h, (unsigned)(((len - 1) * H + 1) * 4));
@@ -749,6 +742,24 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
             mul_planes<OP>(aq[t], read_planes<OP>(sm.in.dO, 16 * t + l16, 8 * lq), s);
             mul_planes<3>(ay[t], read_planes<3>(sm.in.Y, 16 * t + l16, 8 * lq), s);
             mul_planes<3>(ad[t], read_planes<3>(sm.in.D, 16 * t + l16, 8 * lq), d);
+        }
+    }
+    pin();
+    // k, q, g of the lane's rows and channel: only now, their registers are the slices' until here
+    float k[16], q[16], gm[16];
+    const long base = (bos * H + h) * DK;
+    {
+        const unsigned rows = (unsigned)((len - 1) * H * DK + DK);
+        const auto kr = make_rsrc(static_cast<const TIn*>(p.k) + base, rows * EB);
+        const auto qr = make_rsrc(static_cast<const TIn*>(p.q) + base, rows * EB);
+        const auto gr = make_rsrc(p.g + base, rows * 4);
+        const int o0 = 16 * lq * H * DK + ch;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int o = o0 + r * H * DK;
+            k[r] = buf_in<TIn>(kr, o * EB);
+            q[r] = buf_in<TIn>(qr, o * EB);
+            gm[r] = buf_in<float>(gr, o * 4);
         }
     }
 #pragma unroll
@@ -949,8 +960,7 @@ KdaBwdLayout kda_bwd_workspace_layout(int B, int T, int H, int dk, int dv, int N
     KdaBwdLayout w{};
     w.fwd = kda_workspace_layout(B, T, H, dk, N, varlen, 4);
     const size_t units = (size_t)w.fwd.nc_bound * H;
-    w.off_t = al(w.fwd.total);
-    w.off_states = al(w.off_t + units * 4096 * 4);
+    w.off_states = al(w.fwd.total);
     w.off_dstates = al(w.off_states + units * dv * dk * 4);
     w.off_delta = al(w.off_dstates + units * dv * dk * 4);
     w.off_y = al(w.off_delta + units * 64 * dv * 4);

@@ -333,11 +333,13 @@ int gdn_kda_chunk_fwd(const void *q, const void *k, const void *v, const float *
  * Backward pass of gdn_kda_chunk_fwd: arguments as in gdn_chunk_bwd except
  *   g_log_alpha, dg [B, T, H, dk] fp32 (16-byte aligned)
  *   workspace   at least gdn_kda_chunk_bwd_workspace_bytes(...) bytes: the regions of
- *               gdn_kda_chunk_fwd_workspace_bytes for fp32 inputs, then fp32 T [nc, H, 64, 64], the
- *               states entering each chunk [nc, H, dv, dk], the gradients reaching the state behind
- *               each chunk (same), Delta [nc, H, 64, dv] and T^T dDelta (same)
- * and N * H < 2^21. All arithmetic is fp32 for both input types (products on the fp32 matrix core);
- * bf16 gradients are the fp32 results rounded to nearest even. dg and dbeta of a token depend on its own
+ *               gdn_kda_chunk_fwd_workspace_bytes for fp32 inputs (T = (I + A)^{-1} in place of Mmat; of T
+ *               and P only the lower 16x16 tiles are written), then fp32 the states entering each
+ *               chunk [nc, H, dv, dk], the gradients reaching the state behind each chunk (same),
+ *               Delta [nc, H, 64, dv] and T^T dDelta (same)
+ * and N * H < 2^21, nc * H < 2^23. All arithmetic is to fp32's accuracy for both input types (products on the
+ * fp32 matrix core, or on the bf16 one with operands split into three bf16 parts); g below -104 (e^g = 0 in
+ * fp32) is taken as -104. bf16 gradients are the fp32 results rounded to nearest even. dg and dbeta of a token depend on its own
  * sequence only; rows of the outputs that no sequence covers are not written.
  */
 size_t gdn_kda_chunk_bwd_workspace_bytes(int B, int T, int H, int dk, int dv, int N, int varlen,

@@ -70,7 +70,7 @@ def test_workspace_matches_its_regions():
         nc = (T + 63 * N) // 64 if var else B * ((T + 63) // 64)
         al = lambda x: (x + 255) // 256 * 256  # noqa: E731
         u, w = nc * H, gb.gdn_kda_chunk_fwd_workspace_bytes(B, T, H, dk, dv, N, var, dtype=torch.float32)
-        for n in (u * 4096, u * dv * dk, u * dv * dk, u * 64 * dv, u * 64 * dv):
+        for n in (u * dv * dk, u * dv * dk, u * 64 * dv, u * 64 * dv):
             w = al(w) + 4 * n
         assert f(B, T, H, dk, dv, N, var) == w
 
