@@ -824,7 +824,8 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     };
     const float ref = lq == 0 ? 0.f : lq == 1 ? end[0] : lq == 2 ? end[1] : end[2];   // gamma before the lane's block
     const float own = gm[15];
-    float dq[16], l[16], x[16], ar[16], w[16];
+    float dq[16], l[16], ar[16], w[16];   // ar: with e^{gamma_last - gamma} (D dS') of the row in it
+    float kx = 0.f;
     to_block(aq, w);
 #pragma unroll
     for (int r = 0; r < 16; ++r) dq[r] = exp2_raw(gm[r]) * w[r];
@@ -833,7 +834,10 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     for (int r = 0; r < 16; ++r) l[r] = -exp2_raw(gm[r]) * w[r];
     to_block(ad, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) x[r] = exp2_raw(end[3] - gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) {
+        ar[r] = exp2_raw(end[3] - gm[r]) * w[r];
+        kx += k[r] * ar[r];
+    }
 
     // pairs of different blocks. Rows of block I against all rows before it, through gamma at the row before
     // block I: step s takes row s of every block (lane lq its own), blocks I and later as zeros.
@@ -874,7 +878,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     for (int r = 0; r < 16; ++r) l[r] += exp2_raw(gm[r] - ref) * w[r];
     to_block(ad, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) ar[r] = exp2_raw(own - gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) ar[r] += exp2_raw(own - gm[r]) * w[r];
 
     // pairs inside the lane's block: w[i] holds e^{gamma_r - gamma_i}, decayed row by row
 #pragma unroll
@@ -906,15 +910,13 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         for (int i = 0; i <= r; ++i) hold(ar[i]);
     }
     // gradients
-    float kx = 0.f;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
         const float bl = sm.beta[16 * lq + r] * l[r];
-        kx += k[r] * x[r];
-        w[r] = q[r] * dq[r] + k[r] * (bl - x[r] - ar[r]);
+        w[r] = q[r] * dq[r] + k[r] * (bl - ar[r]);
         const float db = row16_sum(k[r] * l[r]);
         if (l16 == 0) sm.part[wave][16 * lq + r] = db;
-        l[r] = bl + x[r] + ar[r];   // dk
+        l[r] = bl + ar[r];   // dk
     }
     kx += __shfl_xor(kx, 16, 64);
     kx += __shfl_xor(kx, 32, 64);
