@@ -590,15 +590,11 @@ __device__ __forceinline__ Planes<NP> read_planes(const uint16_t (*m)[kPlane], i
     for (int i = 0; i < NP; ++i) x.w[i] = *reinterpret_cast<const uint4*>(&m[i][plane_at(r, c)]);
     return x;
 }
-// acc += x y to fp32's accuracy, the smallest products first
+// Product i = 0 .. 5 of acc += x y at fp32's accuracy, the smallest first (x of one plane has three of them).
 template <int NX>
-__device__ __forceinline__ void mul_planes(f32x4_t& acc, const Planes<NX>& x, const Planes<3>& y) {
-    if constexpr (NX == 3) acc = mfma_bf16(x.w[2], y.w[0], acc);
-    acc = mfma_bf16(x.w[0], y.w[2], acc);
-    if constexpr (NX == 3) acc = mfma_bf16(x.w[1], y.w[1], acc);
-    if constexpr (NX == 3) acc = mfma_bf16(x.w[1], y.w[0], acc);
-    acc = mfma_bf16(x.w[0], y.w[1], acc);
-    acc = mfma_bf16(x.w[0], y.w[0], acc);
+__device__ __forceinline__ void mul_plane(f32x4_t& acc, const Planes<NX>& x, const Planes<3>& y, int i) {
+    constexpr int px[6] = {2, 0, 1, 1, 0, 0}, py[6] = {0, 2, 1, 0, 1, 0};
+    if (px[i] < NX) acc = mfma_bf16(x.w[px[i] < NX ? px[i] : 0], y.w[py[i]], acc);
 }
 
 // Element (r, i) of dP and dA. They are read by rows (pieces of one row), by columns (16 columns of the row s of all four
@@ -700,7 +696,38 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
 #pragma unroll
     for (int n = 0; n < 5; ++n) tri[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     auto tile_row = [](int tile) { return tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3; };
-    auto of_a = [](int job) { return (job ^ (job >> 2)) & 1; };   // a wave's jobs alternate: dA takes twice dP's products
+    // a wave's jobs alternate between dP and dA, since dA takes twice dP's products: job w + 4 n is one of dA where
+    // w + n is odd
+    auto tri_jobs = [&](auto parity) {
+#pragma unroll
+        for (int n = 0; n < 5; ++n) {
+            constexpr int par = decltype(parity)::value;
+            const int tile = (wave + 4 * n) >> 1, I = tile_row(tile), J = tile - I * (I + 1) / 2;
+            const auto y = read_planes<3>(sm.in.D, 16 * J + l16, 8 * lq);
+            if ((par + n) & 1) {
+                const auto x = read_planes<3>(sm.in.Y, 16 * I + l16, 8 * lq);
+#pragma unroll
+                for (int i = 0; i < 6; ++i) mul_plane<3>(tri[n], x, y, i);
+            } else {
+                const auto x = read_planes<OP>(sm.in.dO, 16 * I + l16, 8 * lq);
+#pragma unroll
+                for (int i = 0; i < 6; ++i) mul_plane<OP>(tri[n], x, y, i);
+            }
+        }
+    };
+    auto tri_store = [&](auto parity) {
+#pragma unroll
+        for (int n = 0; n < 5; ++n) {
+            constexpr int par = decltype(parity)::value;
+            const int tile = (wave + 4 * n) >> 1, I = tile_row(tile), J = tile - I * (I + 1) / 2;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int r = 16 * I + 4 * lq + m, i = 16 * J + l16;
+                if ((par + n) & 1) sm.dA[tri_at<PC>(r, i)] = i < r ? -tri[n][m] : 0.f;
+                else sm.dP[tri_at<PC>(r, i)] = i <= r ? tri[n][m] : 0.f;
+            }
+        }
+    };
     auto put = [](uint16_t (*m)[kPlane], int at, const f32x4_t& x) {
         uint32_t a[3], c[3];
         split_pair(x[0], x[1], a);
@@ -730,18 +757,18 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         const Planes<3> s = split8(sn), d = split8(dn);
         __syncthreads();
         load(min(sl + 1, NS - 1));   // the last slice again at the end
-#pragma unroll
-        for (int n = 0; n < 5; ++n) {
-            const int job = wave + 4 * n, tile = job >> 1, I = tile_row(tile), J = tile - I * (I + 1) / 2;
-            const Planes<3> y = read_planes<3>(sm.in.D, 16 * J + l16, 8 * lq);
-            if (of_a(job)) mul_planes<3>(tri[n], read_planes<3>(sm.in.Y, 16 * I + l16, 8 * lq), y);
-            else mul_planes<OP>(tri[n], read_planes<OP>(sm.in.dO, 16 * I + l16, 8 * lq), y);
-        }
+        if (wave & 1) tri_jobs(std::integral_constant<int, 1>{});
+        else tri_jobs(std::integral_constant<int, 0>{});
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            mul_planes<OP>(aq[t], read_planes<OP>(sm.in.dO, 16 * t + l16, 8 * lq), s);
-            mul_planes<3>(ay[t], read_planes<3>(sm.in.Y, 16 * t + l16, 8 * lq), s);
-            mul_planes<3>(ad[t], read_planes<3>(sm.in.D, 16 * t + l16, 8 * lq), d);
+            const auto o = read_planes<OP>(sm.in.dO, 16 * t + l16, 8 * lq);
+            const auto y = read_planes<3>(sm.in.Y, 16 * t + l16, 8 * lq), x = read_planes<3>(sm.in.D, 16 * t + l16, 8 * lq);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {   // three chains of products side by side
+                mul_plane<3>(ay[t], y, s, i);
+                mul_plane<3>(ad[t], x, d, i);
+                mul_plane<OP>(aq[t], o, s, i);
+            }
         }
     }
     pin();
@@ -762,16 +789,8 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
             gm[r] = buf_in<float>(gr, o * 4);
         }
     }
-#pragma unroll
-    for (int n = 0; n < 5; ++n) {
-        const int job = wave + 4 * n, tile = job >> 1, I = tile_row(tile), J = tile - I * (I + 1) / 2;
-        float* out = of_a(job) ? sm.dA : sm.dP;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int r = 16 * I + 4 * lq + m, i = 16 * J + l16;
-            out[tri_at<PC>(r, i)] = of_a(job) ? (i < r ? -tri[n][m] : 0.f) : (i <= r ? tri[n][m] : 0.f);
-        }
-    }
+    if (wave & 1) tri_store(std::integral_constant<int, 1>{});
+    else tri_store(std::integral_constant<int, 0>{});
     // zeros in the upper tiles (I, J) = (0, 1), (0, 2), (0, 3), (1, 2), (1, 3), (2, 3)
 #pragma unroll
     for (int n = 0; n < 3; ++n) {
