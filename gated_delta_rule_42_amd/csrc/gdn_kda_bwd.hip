@@ -52,27 +52,25 @@ __device__ __forceinline__ void hold(float& x) { asm volatile("" : "+v"(x)); }
 
 // ------------------------------------------------------------------- the two walks
 // The state walk (S entering each chunk, D) and the reverse walk (dS' leaving each chunk, Y) do not need each other and
-// run side by side in one launch. One work-group of eight waves per walk, (sequence, head) and tile of 64 columns of d_v (one
-// tile of 32 columns on four waves each, one walk after the other, moved twice the operands through the L2, which bound them:
-// 357 us for the training shape). Wave w has the 16 columns cg = w & 3 and the half hf = w >> 2 of the d_k channels: S^T [dk/2,
-// 16] in accumulator registers. Per chunk each wave forms its half of the products over d_k for all 64 rows, the two halves
+// run side by side in one launch (one after the other, on tiles of 32 columns: 357 us for the training shape, against 320).
+// One work-group per walk, (sequence, head) and tile of 16 NCG columns of d_v (NCG 2 or 4, see kNarrowWalks), 2 NCG waves. Wave
+// w has the 16 columns cg = w % NCG and the half hf = w / NCG of the d_k channels: S^T [dk/2, 16] in accumulator registers. Per chunk each wave forms its half of the products over d_k for all 64 rows, the two halves
 // are added through LDS, the triangular product (with T or T^T) is shared by row tiles ({0, 3} and {1, 2}: five block
 // products each), and each wave updates its own channels. Operators go global -> registers -> LDS a chunk ahead, all of
 // these memory instructions placed between the products, whose steps hide them.
-constexpr int kWalkThreads = 512;
 constexpr int kWalkPitch = 4;   // pad of an operator row in LDS (floats)
 
 // A [64, W] fp32 operator on its way into LDS (row pitch W + kWalkPitch): NV 16-byte pieces per thread, held in registers
 // between load and store.
-template <int W>
+template <int W, int NT>
 struct WalkTile {
-    static constexpr int NV = 64 * W / 4 / kWalkThreads;
+    static constexpr int NV = 64 * W / 4 / NT;
     f32x4_t x[NV];
     __device__ __forceinline__ void load(const float* src, int i, int tid) {
-        x[i] = *reinterpret_cast<const f32x4_t*>(src + 4 * (tid + kWalkThreads * i));
+        x[i] = *reinterpret_cast<const f32x4_t*>(src + 4 * (tid + NT * i));
     }
     __device__ __forceinline__ void store(float* dst, int i, int tid) const {
-        const int e = 4 * (tid + kWalkThreads * i);
+        const int e = 4 * (tid + NT * i);
         *reinterpret_cast<f32x4_t*>(&dst[(e / W) * (W + kWalkPitch) + e % W]) = x[i];
     }
 };
@@ -83,12 +81,12 @@ constexpr int kTriFloats = 10 * 256;
 __device__ __forceinline__ int tri_tile(int I, int J) { return (I * (I + 1) / 2 + J) * 256; }
 __device__ __forceinline__ int tri_row(int r) { return ((r & ~3) | ((r ^ (r >> 2)) & 3)) * 16; }
 // NM such matrices on their way into LDS, one after the other: 640 pieces each.
-template <int NM>
+template <int NM, int NT>
 struct WalkTri {
-    static constexpr int NP = 640 * NM, NV = (NP + kWalkThreads - 1) / kWalkThreads;
+    static constexpr int NP = 640 * NM, NV = (NP + NT - 1) / NT;
     f32x4_t x[NV];
     static __device__ __forceinline__ void place(int i, int tid, int& m, int& I, int& J, int& r, int& c) {
-        const int n = min(tid + kWalkThreads * i, NP - 1), tile = n % 640 / 64;
+        const int n = min(tid + NT * i, NP - 1), tile = n % 640 / 64;
         m = n / 640;
         I = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
         J = tile - I * (I + 1) / 2;
@@ -106,6 +104,13 @@ struct WalkTri {
         *reinterpret_cast<f32x4_t*>(&dst[m * kTriFloats + tri_tile(I, J) + tri_row(r) + c]) = x[i];
     }
 };
+
+// The pieces j of NV that the i-th of eight shares has.
+template <int NV, typename F>
+__device__ __forceinline__ void share(int i, F f) {
+#pragma unroll
+    for (int j = i * NV / 8; j < (i + 1) * NV / 8; ++j) f(j);
+}
 
 // A wave's 16 columns of a chunk's [len, H, DV] tokens: 16-byte pieces in registers as loaded (zeros past the end), then
 // through 4 KB of LDS of the wave's own into the layout of a right operand (lane (lq, l16): rows 16 t + 4 lq + m of
@@ -227,28 +232,28 @@ struct TriFrags {
     static __device__ __forceinline__ int second_tile(int hf) { return TRANS ? (hf == 0 ? 0 : 1) : (hf == 0 ? 3 : 2); }
 };
 
-template <int DK>
+template <int DK, int NCG>
 struct alignas(16) KdaStateSmem {
     float Kh[64 * (DK + kWalkPitch)];
     float Kd[64 * (DK + kWalkPitch)];
     float T[kTriFloats];
     float lam[DK];
     float beta[64];
-    f32x4_t ex[8][4][64];    // each wave's partial products, row tile by row tile
-    f32x4_t ex2[4][4][64];   // the triangular product, per column group
+    f32x4_t ex[2 * NCG][4][64];    // each wave's partial products, row tile by row tile
+    f32x4_t ex2[NCG][4][64];   // the triangular product, per column group
 };
-template <int DK>
+template <int DK, int NCG>
 struct alignas(16) KdaRevSmem {
     float Kd[64 * (DK + kWalkPitch)];
     union {
         float Qh[64 * (DK + kWalkPitch)];
-        f32x4_t ex2[4][4][64];
+        f32x4_t ex2[NCG][4][64];
     };
     float Kh[64 * (DK + kWalkPitch)];
     float PT[2 * kTriFloats];   // P, then T
     float lam[DK];
     float beta[64];
-    f32x4_t ex[8][4][64];
+    f32x4_t ex[2 * NCG][4][64];
 };
 
 struct Chain {   // the chunks of the work-group's (sequence, head)
@@ -276,13 +281,13 @@ __device__ __forceinline__ Chain chain_of(const ChunkProblem& p, long b, long nb
 
 // Barriers of a chunk: (1) its first operators are in LDS; (2) all partial products are exchanged, and the rest of the
 // operators are in; (3) the triangular product is exchanged.
-template <typename TIn, int DK, int DV>
-__device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem<DK>& sm, const Chain& c, int tid) {
-    constexpr int PK = DK + kWalkPitch, HK = DK / 2, NJ = HK / 16, NV = WalkTile<DK>::NV;
+template <typename TIn, int DK, int DV, int NCG>
+__device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem<DK, NCG>& sm, const Chain& c, int tid) {
+    constexpr int PK = DK + kWalkPitch, HK = DK / 2, NJ = HK / 16, NT = 128 * NCG, NV = WalkTile<DK, NT>::NV;
     const ChunkProblem& p = b.f;
     const int lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 3, hf = wave >> 2;
-    const int H = p.H, col0 = 64 * c.tile + 16 * cg, col = col0 + l16;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave % NCG, hf = wave / NCG;
+    const int H = p.H, col0 = 16 * NCG * c.tile + 16 * cg, col = col0 + l16;
 
     f32x4_t ST[NJ];
 #pragma unroll
@@ -291,25 +296,25 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
                      : f32x4_t{0.f, 0.f, 0.f, 0.f};
     if (c.nchunks == 0) return;
 
-    WalkTile<DK> kh, kd;
-    WalkTri<1> tt;
+    WalkTile<DK, NT> kh, kd;
+    WalkTri<1, NT> tt;
     TokenCols<TIn, DV> v;
     float lam = 0.f, beta = 0.f;
     float* own = reinterpret_cast<float*>(&sm.ex[wave][0][0]);
     // the chunk's first operators (Kh, V) and the rest (Kd, T, lam, beta), each in up to eight shares
     auto load1 = [&](long jc, int i) {
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
-        if (i < NV) kh.load(p.khat + widx * 64 * DK, i, tid);
-        if (i >= 4 && i - 4 < v.NV) v.load(p.v, bos, (int)min(64L, c.seos - bos), H, c.h, col0, i - 4, lane);
+        share<NV>(i, [&](int j) { kh.load(p.khat + widx * 64 * DK, j, tid); });
+        share<v.NV>(i, [&](int j) { v.load(p.v, bos, (int)min(64L, c.seos - bos), H, c.h, col0, j, lane); });
     };
     auto store1 = [&](int i) {
-        if (i < NV) kh.store(sm.Kh, i, tid);
-        if (i >= 4 && i - 4 < v.NV) v.store(own, i - 4, lane);
+        share<NV>(i, [&](int j) { kh.store(sm.Kh, j, tid); });
+        share<v.NV>(i, [&](int j) { v.store(own, j, lane); });
     };
     auto load2 = [&](long jc, int i) {
         const long widx = (c.cbase + jc) * H + c.h;
-        if (i < NV) kd.load(p.kdec + widx * 64 * DK, i, tid);
-        if (i >= 4 && i - 4 < tt.NV) tt.load(p.tmat + widx * 4096, nullptr, i - 4, tid);
+        share<NV>(i, [&](int j) { kd.load(p.kdec + widx * 64 * DK, j, tid); });
+        share<tt.NV>(i, [&](int j) { tt.load(p.tmat + widx * 4096, nullptr, j, tid); });
         if (i == 7) {
             const long bos = c.sbos + jc * 64;
             const auto br = make_rsrc(p.beta + bos * H + c.h, (unsigned)((((int)min(64L, c.seos - bos) - 1) * H + 1) * 4));
@@ -318,8 +323,8 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
         }
     };
     auto store2 = [&](int i) {
-        if (i < NV) kd.store(sm.Kd, i, tid);
-        if (i >= 4 && i - 4 < tt.NV) tt.store(sm.T, i - 4, tid);
+        share<NV>(i, [&](int j) { kd.store(sm.Kd, j, tid); });
+        share<tt.NV>(i, [&](int j) { tt.store(sm.T, j, tid); });
         if (i == 7) {
             sm.lam[tid % DK] = lam;
             sm.beta[tid & 63] = beta;
@@ -357,7 +362,7 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
         for (int i = 0; i < 5; ++i) m.read(sm.T, hf, i, l16, lq);
 #pragma unroll
         for (int t = 0; t < 4; ++t)   // beta R
-            X[t] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * t + 4 * lq]) * (D[t] - (X[t] + sm.ex[wave ^ 4][t][lane]));
+            X[t] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * t + 4 * lq]) * (D[t] - (X[t] + sm.ex[wave ^ NCG][t][lane]));
         // D = T beta R on the wave's row tiles
         {
             f32x4_t d[2];
@@ -387,13 +392,13 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
 
 // Barriers of a chunk: (1) Kd, P, T and dO are in LDS; (2) all partial products are exchanged, and Qh, Kh, lam and beta
 // are in; (3) Qh is dead; (4) the triangular product is exchanged (over Qh).
-template <typename TIn, int DK, int DV>
-__device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK>& sm, const Chain& c, int tid) {
-    constexpr int PK = DK + kWalkPitch, HK = DK / 2, NJ = HK / 16, NV = WalkTile<DK>::NV;
+template <typename TIn, int DK, int DV, int NCG>
+__device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK, NCG>& sm, const Chain& c, int tid) {
+    constexpr int PK = DK + kWalkPitch, HK = DK / 2, NJ = HK / 16, NT = 128 * NCG, NV = WalkTile<DK, NT>::NV;
     const ChunkProblem& p = b.f;
     const int lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 3, hf = wave >> 2;
-    const int H = p.H, col0 = 64 * c.tile + 16 * cg, col = col0 + l16;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave % NCG, hf = wave / NCG;
+    const int H = p.H, col0 = 16 * NCG * c.tile + 16 * cg, col = col0 + l16;
 
     f32x4_t dST[NJ];
 #pragma unroll
@@ -409,26 +414,28 @@ __device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK>
     };
     if (c.nchunks == 0) return finish();
 
-    WalkTile<DK> kh, qh, kd;
-    WalkTri<2> pt;
+    WalkTile<DK, NT> kh, qh, kd;
+    WalkTri<2, NT> pt;
     TokenCols<TIn, DV> dof;
     float lam = 0.f, beta = 0.f;
     float* own = reinterpret_cast<float*>(&sm.ex[wave][0][0]);
     auto load1 = [&](long jc, int i) {   // Kd, P, T, dO
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
-        if (i < NV) kd.load(p.kdec + widx * 64 * DK, i, tid);
-        if (i >= 4 && i - 4 < pt.NV) pt.load(static_cast<const float*>(p.pmat) + widx * 4096, p.tmat + widx * 4096, i - 4, tid);
-        if (i < dof.NV) dof.load(b.d_o, bos, (int)min(64L, c.seos - bos), H, c.h, col0, i, lane);
+        share<NV>(i, [&](int j) { kd.load(p.kdec + widx * 64 * DK, j, tid); });
+        share<pt.NV>(i, [&](int j) { pt.load(static_cast<const float*>(p.pmat) + widx * 4096, p.tmat + widx * 4096, j, tid); });
+        share<dof.NV>(i, [&](int j) { dof.load(b.d_o, bos, (int)min(64L, c.seos - bos), H, c.h, col0, j, lane); });
     };
     auto store1 = [&](int i) {
-        if (i < NV) kd.store(sm.Kd, i, tid);
-        if (i >= 4 && i - 4 < pt.NV) pt.store(sm.PT, i - 4, tid);
-        if (i < dof.NV) dof.store(own, i, lane);
+        share<NV>(i, [&](int j) { kd.store(sm.Kd, j, tid); });
+        share<pt.NV>(i, [&](int j) { pt.store(sm.PT, j, tid); });
+        share<dof.NV>(i, [&](int j) { dof.store(own, j, lane); });
     };
     auto load2 = [&](long jc, int i) {   // Qh, Kh, lam, beta
         const long widx = (c.cbase + jc) * H + c.h, bos = c.sbos + jc * 64;
-        if (i < NV) qh.load(p.qhat + widx * 64 * DK, i, tid);
-        if (i >= 4 && i - 4 < NV) kh.load(p.khat + widx * 64 * DK, i - 4, tid);
+        share<NV>(i, [&](int j) {
+            qh.load(p.qhat + widx * 64 * DK, j, tid);
+            kh.load(p.khat + widx * 64 * DK, j, tid);
+        });
         if (i == 7) {
             const int len = (int)min(64L, c.seos - bos);
             lam = p.lam[widx * DK + tid % DK];
@@ -437,8 +444,10 @@ __device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK>
         }
     };
     auto store2 = [&](int i) {
-        if (i < NV) qh.store(sm.Qh, i, tid);
-        if (i >= 4 && i - 4 < NV) kh.store(sm.Kh, i - 4, tid);
+        share<NV>(i, [&](int j) {
+            qh.store(sm.Qh, j, tid);
+            kh.store(sm.Kh, j, tid);
+        });
         if (i == 7) {
             sm.lam[tid % DK] = lam;
             sm.beta[tid & 63] = beta;
@@ -489,7 +498,7 @@ __device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK>
         TriFrags<true> tf;
         mul_cols<NJ>(dST, sm.Qh, PK, hf * HK, dO, l16, lq, [&](int i) {
             if (i % 2 == 0) load2(nxt, i / 2);
-            if (i < 4) X[i] += sm.ex[wave ^ 4][i][lane];   // dD
+            if (i < 4) X[i] += sm.ex[wave ^ NCG][i][lane];   // dD
             if (i >= 11) tf.read(sm.PT + kTriFloats, hf, i - 11, l16, lq);
         });
         __syncthreads();   // (3)
@@ -517,16 +526,17 @@ __device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK>
 }
 
 // The reverse walks are the longer ones and come first.
-template <typename TIn, int DK, int DV>
-__global__ __launch_bounds__(kWalkThreads) void kda_bwd_walk_kernel(KdaBwdProblem b) {
+template <typename TIn, int DK, int DV, int NCG>
+__global__ __launch_bounds__(128 * NCG) void kda_bwd_walk_kernel(KdaBwdProblem b) {
     __shared__ union Smem {
         __device__ Smem() {}
-        KdaRevSmem<DK> back;
-        KdaStateSmem<DK> states;
+        KdaRevSmem<DK, NCG> back;
+        KdaStateSmem<DK, NCG> states;
     } sm;
+    constexpr int TILES = DV / (16 * NCG);
     const long half = gridDim.x / 2;
-    if (blockIdx.x < half) walk_back<TIn, DK, DV>(b, sm.back, chain_of<DV / 64>(b.f, blockIdx.x, half), threadIdx.x);
-    else walk_states<TIn, DK, DV>(b, sm.states, chain_of<DV / 64>(b.f, blockIdx.x - half, half), threadIdx.x);
+    if (blockIdx.x < half) walk_back<TIn, DK, DV, NCG>(b, sm.back, chain_of<TILES>(b.f, blockIdx.x, half), threadIdx.x);
+    else walk_states<TIn, DK, DV, NCG>(b, sm.states, chain_of<TILES>(b.f, blockIdx.x - half, half), threadIdx.x);
 }
 
 // ------------------------------------------------------------------- gradients of each chunk
@@ -989,13 +999,20 @@ KdaBwdLayout kda_bwd_workspace_layout(int B, int T, int H, int dk, int dv, int N
     return w;
 }
 
+// Work-groups of 32 columns (four waves, a SIMD each) step a chunk in about 6 us, those of 64 columns (eight waves) in about 10,
+// moving half the operators per column. As long as all narrow ones run at once, they win (16 pairs x 64 chunks: 557 us
+// the whole pass against 757; 32 x 32: 410, 495; at 64 x 32 wide ones do: 753, 715). Packed sequences mostly differ in length,
+// so the longest one's time counts up to twice as many (64 pairs, 64 .. 1600 tokens: 300 us narrow, 370 wide).
+constexpr long kNarrowWalks = 256;
+
 template <typename TIn, int DK, int DV>
 static hipError_t kda_bwd_launch(const KdaBwdProblem& b, hipStream_t s) {
     const ChunkProblem& p = b.f;
     const long pairs = (long)p.N * p.H, units = p.nc_bound * p.H;
     if (pairs == 0) return hipSuccess;
-    const dim3 walks((unsigned)(2 * pairs * (DV / 64)));
-    const hipError_t e = launch(kda_bwd_walk_kernel<TIn, DK, DV>, walks, dim3(kWalkThreads), s, b);
+    const bool narrow = 2 * pairs * (DV / 32) <= (p.cu_seqlens ? 2 : 1) * kNarrowWalks;
+    const hipError_t e = narrow ? launch(kda_bwd_walk_kernel<TIn, DK, DV, 2>, dim3((unsigned)(2 * pairs * (DV / 32))), dim3(256), s, b)
+                                : launch(kda_bwd_walk_kernel<TIn, DK, DV, 4>, dim3((unsigned)(2 * pairs * (DV / 64))), dim3(512), s, b);
     if (e != hipSuccess || units == 0) return e;
     const dim3 grid((unsigned)(units * (DK / 64)));
     return b.grad_bf16 ? launch(kda_bwd_grad_kernel<TIn, uint16_t, DK, DV>, grid, dim3(256), s, b)

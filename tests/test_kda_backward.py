@@ -144,6 +144,16 @@ def test_small(B, T, H, dk, dv, dtype, h0, dhT, gs):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H,dk,dv,dtype,packed", [
+    (100, 66, 64, 64, "f32", False), (130, 34, 64, 128, "bf16", False), (130, 67, 128, 64, "bf16", False),
+    (150, 33, 128, 128, "f32", False), (0, 70, 128, 128, "bf16", True)])
+def test_many_heads(T, H, dk, dv, dtype, packed):
+    """Enough (sequence, head) pairs for work-groups of 64 columns; not multiples of eight."""
+    x = make(71, 1, T, H, dk, dv, dtype, True, 0.1, lengths=[65, 40] if packed else None)
+    check(x, SY.make_cotangents(x, 72), heads=[0, H // 2, H - 1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,dk,dv", [("f32", 128, 128), ("bf16", 128, 128), ("bf16", 64, 128)])
 def test_packed(dtype, dk, dv):
     """Packed sequences, some of them empty (their dh0 is dhT), single tokens, ends inside and at chunk borders."""
