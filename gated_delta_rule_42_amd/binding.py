@@ -390,14 +390,18 @@ def _dense(**ts):
             raise ValueError(f"gdn: {name} must be contiguous")
 
 
-def _call(name, device, stream, made, *args):
-    """Run an entry point on `stream` (default: the current one of `device`) with `device` current. `made`: tensors
-    allocated by this call; on a stream of the caller's choice the allocator is told that they are in use there."""
+def _new(shape, dtype, device, stream):
+    """An output or workspace of a call on `stream`, from that stream's share of the allocator: memory that is still in
+    use on another stream is never handed out for it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call(name, device, stream, *args):
+    """Run an entry point on `stream` (default: the current one of `device`) with `device` current."""
     fn = getattr(lib(), name)
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
     if torch.cuda.current_device() == device.index:
         st = fn(*args, _stream(device, stream))
     else:
@@ -470,11 +474,9 @@ def gdn_recurrent_fwd(q, k, v, g, beta, states, slots, cu_seqlens=None, out_slot
         if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
             raise ValueError(f"gdn: the heads of {name} must follow each other densely within a token")
         strides.append(t.stride(0) if t.shape[0] > 1 else 0)
-    made = ()
     if o is None:
-        o = torch.empty((T, HV, dv), dtype=o_dtype, device=q.device)
-        made = (o,)
-    _call("gdn_recurrent_fwd", q.device, stream, made, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(states),
+        o = _new((T, HV, dv), o_dtype, q.device, stream)
+    _call("gdn_recurrent_fwd", q.device, stream, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(states),
           _adr(slots), _adr(cu_seqlens), _adr(out_slots), _adr(o), T, N, H, HV, dk, dv, states.shape[0], *strides,
           int(channels), _DTYPE.get(q.dtype, -1), _DTYPE.get(o.dtype, -1))
     return o
@@ -523,7 +525,6 @@ def gdn_qk_norm_fwd(q, k, q_weight=None, k_weight=None, *, positions=None, inv_f
     (default the dtype of q; fp32 is allowed for bf16 inputs)."""
     tokens, hq, hk, d, rot = _check_norm_args(q, k, q_weight, k_weight, positions, inv_freq, norm, layout)
     qs, ks = _row_strides(q, "q"), _row_strides(k, "k")
-    made = []
     for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
         _expect(t, name, like.shape, _IN)
     if q_out is not None and k_out is not None and q_out.dtype != k_out.dtype:
@@ -531,14 +532,12 @@ def gdn_qk_norm_fwd(q, k, q_weight=None, k_weight=None, *, positions=None, inv_f
     given = q_out if q_out is not None else k_out
     od = given.dtype if given is not None else (out_dtype or q.dtype)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=od, device=q.device)
-        made.append(q_out)
+        q_out = _new(q.shape, od, q.device, stream)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=od, device=q.device)
-        made.append(k_out)
+        k_out = _new(k.shape, od, q.device, stream)
     _same_gpu(q.device, q_out=q_out, k_out=k_out)
     _dense(q_out=q_out, k_out=k_out)
-    _call("gdn_qk_norm_fwd", q.device, stream, made, _adr(q), _adr(k), _adr(q_weight), _adr(k_weight), _adr(positions),
+    _call("gdn_qk_norm_fwd", q.device, stream, _adr(q), _adr(k), _adr(q_weight), _adr(k_weight), _adr(positions),
           _adr(inv_freq), _adr(q_out), _adr(k_out), tokens, hq, hk, d, *qs, *ks, _NORM[norm], eps, rot, _ROPE[layout],
           q_scale, rope_scale, _DTYPE.get(q.dtype, -1), _DTYPE.get(od, -1))
     return q_out, k_out
@@ -560,28 +559,23 @@ def gdn_qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, *, posit
     _expect(dk_out, "dk_out", k.shape, (dq_out.dtype,))
     _expect(dq, "dq", q.shape, (q.dtype,))
     _expect(dk, "dk", k.shape, (q.dtype,))
-    made = []
     if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        made.append(dq)
+        dq = _new(q.shape, q.dtype, q.device, stream)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        made.append(dk)
+        dk = _new(k.shape, q.dtype, q.device, stream)
     dqw = dkw = None
     if need_dw or (need_dw is None and q_weight is not None):
-        dqw = torch.empty(d, dtype=torch.float32, device=q.device)
+        dqw = _new(d, torch.float32, q.device, stream)
     if need_dw or (need_dw is None and k_weight is not None):
-        dkw = torch.empty(d, dtype=torch.float32, device=q.device)
-    made += [dqw, dkw]
+        dkw = _new(d, torch.float32, q.device, stream)
     if dqw is not None or dkw is not None:
         need = gdn_qk_norm_bwd_workspace_bytes(tokens, hq, hk, d)
         if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            made.append(workspace)
+            workspace = _new(need, torch.uint8, q.device, stream)
     _same_gpu(q.device, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk, workspace=workspace)
     _dense(dq_out=dq_out, dk_out=dk_out, workspace=workspace)
     strides = [s for t, name in ((q, "q"), (k, "k"), (dq, "dq"), (dk, "dk")) for s in _row_strides(t, name)]
-    _call("gdn_qk_norm_bwd", q.device, stream, made, _adr(q), _adr(k), _adr(dq_out), _adr(dk_out), _adr(q_weight),
+    _call("gdn_qk_norm_bwd", q.device, stream, _adr(q), _adr(k), _adr(dq_out), _adr(dk_out), _adr(q_weight),
           _adr(k_weight), _adr(positions), _adr(inv_freq), _adr(dq), _adr(dk), _adr(dqw), _adr(dkw), tokens, hq, hk, d,
           *strides, _NORM[norm], eps, rot, _ROPE[layout], q_scale, rope_scale, _DTYPE.get(q.dtype, -1),
           _DTYPE.get(dq_out.dtype, -1), _adr(workspace),
@@ -604,18 +598,16 @@ def gdn_kda_chunk_bwd(q, k, v, g, beta, do, h0=None, dhT=None, cu_seqlens=None, 
     _same_gpu(dev, k=k, v=v, g=g, beta=beta, do=do, h0=h0, dhT=dhT, cu_seqlens=cu_seqlens, workspace=workspace)
     _dense(q=q, k=k, v=v, g=g, beta=beta, do=do, h0=h0, dhT=dhT, cu_seqlens=cu_seqlens, workspace=workspace)
     gd = grad_dtype or q.dtype
-    dq = torch.empty(q.shape, dtype=gd, device=dev)
-    dk_ = torch.empty(k.shape, dtype=gd, device=dev)
-    dv_ = torch.empty(v.shape, dtype=gd, device=dev)
-    dg = torch.empty(g.shape, dtype=torch.float32, device=dev)
-    db = torch.empty((B, T, H), dtype=torch.float32, device=dev)
-    dh0 = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev) if need_dh0 else None
-    made = [dq, dk_, dv_, dg, db, dh0]
+    dq = _new(q.shape, gd, dev, stream)
+    dk_ = _new(k.shape, gd, dev, stream)
+    dv_ = _new(v.shape, gd, dev, stream)
+    dg = _new(g.shape, torch.float32, dev, stream)
+    db = _new((B, T, H), torch.float32, dev, stream)
+    dh0 = _new((N, H, dv, dk), torch.float32, dev, stream) if need_dh0 else None
     need = gdn_kda_chunk_bwd_workspace_bytes(B, T, H, dk, dv, N, cu_seqlens is not None, chunk, q.dtype)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        made.append(workspace)
-    _call("gdn_kda_chunk_bwd", dev, stream, made, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(do),
+        workspace = _new(need, torch.uint8, dev, stream)
+    _call("gdn_kda_chunk_bwd", dev, stream, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(do),
           _adr(dhT), _adr(dq), _adr(dk_), _adr(dv_), _adr(dg), _adr(db), _adr(dh0), _adr(cu_seqlens), chunk, B, T, H, dk,
           dv, N, _DTYPE.get(q.dtype, -1), _DTYPE.get(gd, -1), _adr(workspace),
           workspace.numel() * workspace.element_size() if workspace is not None else 0)

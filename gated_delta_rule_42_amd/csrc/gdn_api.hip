@@ -48,15 +48,16 @@ FwdLayout fwd_layout(int B, int T, int H, int dk, int dv, int N, int varlen, int
 
 // GDN_CHECK=1 in the environment: copy cu_seqlens to the host (this synchronises `stream`) and
 // reject offsets that break 0 = cu[0] <= cu[1] <= ... <= cu[N] = T. A debugging aid: without it
-// the offsets are a precondition that the kernels only clamp into [0, T].
-int debug_check_offsets(const int32_t* cu, int N, int T, hipStream_t s) {
+// the offsets are a precondition that the kernels only clamp into [0, T]. padded: tokens behind the last sequence
+// are allowed (cu[N] <= T).
+int debug_check_offsets(const int32_t* cu, int N, int T, hipStream_t s, bool padded = false) {
     const char* env = std::getenv("GDN_CHECK");
     if (!cu || !env || std::strcmp(env, "1") != 0) return GDN_OK;
     std::vector<int32_t> h((size_t)N + 1);
     if (hipMemcpyAsync(h.data(), cu, h.size() * sizeof(int32_t), hipMemcpyDeviceToHost, s) != hipSuccess ||
         hipStreamSynchronize(s) != hipSuccess)
         return GDN_ERR_HIP;
-    if (h[0] != 0 || h[(size_t)N] != T) return GDN_ERR_SHAPE;
+    if (h[0] != 0 || (padded ? h[(size_t)N] > T : h[(size_t)N] != T)) return GDN_ERR_SHAPE;
     for (int i = 0; i < N; ++i)
         if (h[(size_t)i + 1] < h[(size_t)i]) return GDN_ERR_SHAPE;
     return GDN_OK;
@@ -514,7 +515,7 @@ GDN_EXPORT int gdn_recurrent_fwd(const void* q, const void* k, const void* v, co
     const int per16 = dtype == GDN_BF16 ? 8 : 4;   // elements of 16 bytes
     if (q_stride % per16 || k_stride % per16 || v_stride % per16) return GDN_ERR_ALIGN;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int chk = debug_check_offsets(cu_seqlens, N, T, s);
+    const int chk = debug_check_offsets(cu_seqlens, N, T, s, true);
     if (chk != GDN_OK) return chk;
     gdn::RecurrentProblem p{};
     p.q = q; p.k = k; p.v = v; p.g = g_log_alpha; p.beta = beta; p.states = states;

@@ -981,7 +981,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         float* dst = b.dbeta + (bos + tid) * H + h;
         // two halves add to the zero that the reverse walk left: one addition each, whose order does not matter
         if constexpr (NH == 1) *dst = s;
-        else unsafeAtomicAdd(dst, s);
+        else atomicAdd(dst, s);
     }
 }
 

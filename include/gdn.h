@@ -40,7 +40,7 @@
  *    during execution surface at the caller's next synchronisation.
  *  - GDN_CHECK=1 in the environment (a debugging aid): every entry point that takes
  *    cu_seqlens first copies it to the host, which synchronises `stream`, and returns
- *    GDN_ERR_SHAPE unless 0 = cu[0] <= cu[1] <= ... <= cu[N] = T.
+ *    GDN_ERR_SHAPE unless 0 = cu[0] <= cu[1] <= ... <= cu[N] = T (gdn_recurrent_fwd: <= T).
  *  - GDN_SEGMENT_CHUNKS=L in the environment (for tests and tuning) fixes the segment length
  *    of the long-chain split of the bf16 forward pass to L chunks; 0 turns the split off.
  *    Without it the split is chosen from the shape (see gdn_chunk_fwd_workspace_bytes). The

@@ -302,3 +302,21 @@ def test_repeats_streams_and_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, held))
         assert all(torch.equal(a, b) for a, b in zip(want, both()))
+
+
+@pytest.mark.gpu
+def test_strides_past_32_bits():
+    """Rows whose elements start past 2^31 (views with a huge token stride into a 4.6 GB buffer), both directions."""
+    x = make(31, 3, 2, 1, 64, "bf16", 64, True, 100, fused=False)
+    t = {n: v.cuda() for n, v in x.items()}
+    big = torch.zeros(2300000000, dtype=torch.bfloat16, device="cuda")
+    step = 1149999872
+    q, k = big.as_strided((3, 2, 64), (step, 64, 1)), big.as_strided((3, 1, 64), (step, 64, 1), 128)
+    q.copy_(t["q"])
+    k.copy_(t["k"])
+    kw = dict(positions=t["pos"], inv_freq=t["freq"])
+    assert all(torch.equal(a, b) for a, b in zip(gb.gdn_qk_norm_fwd(q, k, t["qw"], t["kw"], **kw),
+                                                 gb.gdn_qk_norm_fwd(t["q"], t["k"], t["qw"], t["kw"], **kw)))
+    want = gb.gdn_qk_norm_bwd(t["q"], t["k"], t["dq"], t["dk"], t["qw"], t["kw"], **kw)
+    got = gb.gdn_qk_norm_bwd(q, k, t["dq"], t["dk"], t["qw"], t["kw"], dq=q, dk=k, **kw)   # over the inputs
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -225,3 +225,35 @@ def test_graph_replay_streams_and_repeats():
     got = gb.gdn_recurrent_fwd(*args, states, slots, d["cu"], stream=side)
     side.synchronize()
     assert torch.equal(got, outs[0])
+
+
+@pytest.mark.gpu
+def test_pool_past_32_bits():
+    """A slot whose elements start past 2^31 (a pool of 8.8 GB)."""
+    x = make(21, [2, 1], 16, 32, 128, 128, "bf16", False, 3)
+    d = {n: t.cuda() for n, t in x.items()}
+    pool = torch.zeros(4200, 32, 128, 128, device="cuda")
+    slots, out = [4199, 4100], [4150, -1, 4198]
+    pool[slots] = d["states"][:2]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    o = gb.gdn_recurrent_fwd(*args, pool, torch.tensor(slots, **i32), d["cu"], torch.tensor(out, **i32))
+    o_ref, s_ref = PO.run(x["q"], x["k"], x["v"], x["g"], x["beta"], x["states"], [0, 1], x["cu"], [0, -1, 1])
+    assert np.abs(o.cpu().double().numpy() - o_ref).max() <= 1e-4 * np.abs(o_ref).max()
+    for slot, ref in ((4150, 0), (4198, 1)):
+        assert np.abs(pool[slot].cpu().double().numpy() - s_ref[ref]).max() <= 1e-4 * np.abs(s_ref[ref]).max()
+    assert torch.equal(pool[4199], d["states"][0]) and float(pool[:4100].abs().max()) == 0.0
+
+
+@pytest.mark.gpu
+def test_debug_check_allows_padding(monkeypatch):
+    """GDN_CHECK=1 accepts tokens behind the last sequence and refuses falling offsets."""
+    x = make(22, [2, 1], 1, 1, 64, 64, "f32", False, 3, extra=2)
+    d = {n: t.cuda() for n, t in x.items()}
+    monkeypatch.setenv("GDN_CHECK", "1")
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    slots = d["order"][:2].contiguous()
+    gb.gdn_recurrent_fwd(*args, d["states"], slots, d["cu"])
+    for cu in ([0, 3, 2], [0, 2, 6], [1, 2, 3]):
+        with pytest.raises(gb.GDNError):
+            gb.gdn_recurrent_fwd(*args, d["states"], slots, torch.tensor(cu, dtype=torch.int32, device="cuda"))
