@@ -102,7 +102,7 @@ def _expect(t, name, shape, dtypes):
     of bounds on the device."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"gdn: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
         names = " or ".join(str(d).replace("torch.", "") for d in dtypes)
@@ -375,8 +375,9 @@ def _same_gpu(device, **ts):
     """Raise ValueError unless every given tensor is on this GPU (any strides)."""
     if device.type != "cuda":
         raise ValueError("gdn: every tensor must be on a GPU")
+    index = device.index
     for name, t in ts.items():
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"gdn: {name} is on {t.device}, expected {device}")
 
 
@@ -390,6 +391,11 @@ def _dense(**ts):
             raise ValueError(f"gdn: {name} must be contiguous")
 
 
+# the current stream's handle without the Stream object around it, where this torch has it: a call's checks and marshalling
+# are a third of a small call's time
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _new(shape, dtype, device, stream):
     """An output or workspace of a call on `stream`, from that stream's share of the allocator: memory that is still in
     use on another stream is never handed out for it."""
@@ -401,13 +407,20 @@ def _new(shape, dtype, device, stream):
 
 def _call(name, device, stream, *args):
     """Run an entry point on `stream` (default: the current one of `device`) with `device` current."""
-    fn = getattr(lib(), name)
+    fn = getattr(_lib or lib(), name)
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = torch.cuda.current_stream(device).cuda_stream
     if torch.cuda.current_device() == device.index:
-        st = fn(*args, _stream(device, stream))
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, _stream(device, stream))
-    _check(st, name)
+            st = fn(*args, handle)
+    if st != 0:
+        _check(st, name)
 
 
 def _token_stride(t, name, tail):
@@ -429,9 +442,13 @@ def _token_stride(t, name, tail):
 
 def _row_strides(t, name):
     """Token and head strides of t [..., heads, d] with contiguous channels."""
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"gdn: the last dimension of {name} must be contiguous")
-    return (_token_stride(t, name, 2) if t.numel() else 0), (t.stride(-2) if t.shape[-2] > 1 else 0)
+    head = strides[-2] if shape[-2] > 1 else 0
+    if len(shape) == 3:
+        return (strides[0] if shape[0] > 1 else 0), head
+    return (_token_stride(t, name, 2) if t.numel() else 0), head
 
 
 def gdn_recurrent_fwd(q, k, v, g, beta, states, slots, cu_seqlens=None, out_slots=None, o=None, *,
@@ -487,13 +504,14 @@ _ROPE = {"half": 0, "interleaved": 1}
 
 
 def _check_norm_args(q, k, q_weight, k_weight, positions, inv_freq, norm, layout):
-    if q.dim() < 3 or q.dtype not in _IN:
-        raise ValueError(f"gdn: q must be [..., heads, d] float32 or bfloat16, got {tuple(q.shape)} {q.dtype}")
-    lead, hq, d = q.shape[:-2], q.shape[-2], q.shape[-1]
-    if k.dim() != q.dim():
-        raise ValueError(f"gdn: k has shape {tuple(k.shape)}, expected {tuple(lead)} + (heads, {d})")
-    hk = k.shape[-2]
-    _expect(k, "k", (*lead, hk, d), (q.dtype,))
+    qs, ks, dtype = q.shape, k.shape, q.dtype
+    if len(qs) < 3 or dtype not in _IN:
+        raise ValueError(f"gdn: q must be [..., heads, d] float32 or bfloat16, got {tuple(qs)} {dtype}")
+    lead, hq, d = qs[:-2], qs[-2], qs[-1]
+    if len(ks) != len(qs):
+        raise ValueError(f"gdn: k has shape {tuple(ks)}, expected {tuple(lead)} + (heads, {d})")
+    hk = ks[-2]
+    _expect(k, "k", (*lead, hk, d), (dtype,))
     if norm not in _NORM:
         raise ValueError(f"gdn: norm must be one of {sorted(_NORM)}, got {norm!r}")
     if layout not in _ROPE:
