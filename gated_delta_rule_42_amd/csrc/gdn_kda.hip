@@ -221,6 +221,8 @@ __device__ __forceinline__ void gram_rows_of(const KdaPrepSmem<DK>& sm, const fl
         // fp32 products: lane (l16, lq) takes channels 16 u + 4 lq + e, e = 0..3, in product (u, e),
         // so its operands arrive as 16-byte reads
         constexpr int J0 = 0;
+        // (two iterations at a time: with all four unrolled stage 1 of the backward pass took 122 us at B4 H16 T2048 d128, so 110)
+#pragma unroll 2
         for (int u = HF * DK / 32; u < (HF + 1) * DK / 32; ++u) {
             const int c = 16 * u + 4 * lq;
             const f32x4_t gref = *reinterpret_cast<const f32x4_t*>(&sm.G[16 * I * PK + c]);
@@ -264,15 +266,26 @@ __device__ __forceinline__ void gram_rows_of(const KdaPrepSmem<DK>& sm, const fl
     }
     __syncthreads();  // the first half's sums are in O1, O2
     if constexpr (HF == 0) return;
+    // all of the first half's sums are read before the first one is written: one LDS latency, not one per entry
+    f32x4_t h1[I + 1], h2[I + 1];
+#pragma unroll
+    for (int J = 0; J <= I; ++J) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int o = (16 * I + 4 * lq + m) * PF + 16 * J + l16;
+            h1[J][m] = O1[o];
+            if constexpr (TWO) h2[J][m] = O2[o];
+        }
+    }
 #pragma unroll
     for (int J = 0; J <= I; ++J) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const int r = 16 * I + 4 * lq + m, i = 16 * J + l16;
             const bool k1 = J < I || (strict1 ? i < r : i <= r), k2 = J < I || i <= r;
-            if (k1) O1[r * PF + i] += (rs1 ? rs1[r] : 1.f) * a1[J][m];
+            if (k1) O1[r * PF + i] = h1[J][m] + (rs1 ? rs1[r] : 1.f) * a1[J][m];
             if constexpr (TWO)
-                if (k2) O2[r * PF + i] += a2[J][m];
+                if (k2) O2[r * PF + i] = h2[J][m] + a2[J][m];
         }
     }
     // channels left out of the diagonal block's product: exact sums over them (each lane adds to
