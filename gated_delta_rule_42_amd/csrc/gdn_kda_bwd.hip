@@ -872,33 +872,55 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     // block I: step s takes row s of every block (lane lq its own), blocks I and later as zeros.
 #pragma unroll
     for (int t = 0; t < 4; ++t) aq[t] = ay[t] = ad[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    {
+        f32x4_t vp[2], va[2];   // this step's operands and the next one's: step n has block I = 1 + n / 4, rows 4 (n % 4) ..
+        auto read = [&](int n) {
+            const int o = tri_at<PC>(16 * (1 + n / 4) + l16, 16 * lq + 4 * (n % 4));
+            vp[n & 1] = *reinterpret_cast<const f32x4_t*>(&sm.dP[o]);
+            va[n & 1] = *reinterpret_cast<const f32x4_t*>(&sm.dA[o]);
+        };
+        read(0);
 #pragma unroll
-    for (int I = 1; I < 4; ++I)
-#pragma unroll
-        for (int s4 = 0; s4 < 4; ++s4) {
+        for (int n = 0; n < 12; ++n) {
+            if (n + 1 < 12) read(n + 1);
             pin();
-            const int o = tri_at<PC>(16 * I + l16, 16 * lq + 4 * s4);
-            const f32x4_t vp = *reinterpret_cast<const f32x4_t*>(&sm.dP[o]);
-            const f32x4_t va = *reinterpret_cast<const f32x4_t*>(&sm.dA[o]);
+            const int I = 1 + n / 4;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int s = 4 * s4 + e;
+                const int s = 4 * (n % 4) + e;
                 const float kb = k[s] * exp2_raw(lq < I ? end[I - 1] - gm[s] : kNone);
-                aq[I] = mfma4(vp[e], kb, aq[I]);
-                ay[I] = mfma4(va[e], kb, ay[I]);
+                aq[I] = mfma4(vp[n & 1][e], kb, aq[I]);
+                ay[I] = mfma4(va[n & 1][e], kb, ay[I]);
             }
         }
+    }
     // Columns of block J against all rows behind it, through gamma at the block's last row.
+    {
+        f32x4_t vp[2], va[2], bt4[2];   // step n has block J = n / 4, rows 4 (n % 4) .. of every block
+        auto read = [&](int n) {
 #pragma unroll
-    for (int J = 0; J < 3; ++J)
+            for (int e = 0; e < 4; ++e) {
+                const int o = tri_at<PC>(16 * lq + 4 * (n % 4) + e, 16 * (n / 4) + l16);
+                vp[n & 1][e] = sm.dP[o];
+                va[n & 1][e] = sm.dA[o];
+            }
+            bt4[n & 1] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * lq + 4 * (n % 4)]);
+        };
+        read(0);
 #pragma unroll
-        for (int s = 0; s < 16; ++s) {
-            if (s % 4 == 0) pin();
-            const int o = tri_at<PC>(16 * lq + s, 16 * J + l16);
-            const float e = exp2_raw(lq > J ? gm[s] - end[J] : kNone);
-            ad[J] = mfma4(sm.dP[o], q[s] * e, ad[J]);
-            ad[J] = mfma4(sm.dA[o], sm.beta[16 * lq + s] * k[s] * e, ad[J]);
+        for (int n = 0; n < 12; ++n) {
+            if (n + 1 < 12) read(n + 1);
+            pin();
+            const int J = n / 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int s = 4 * (n % 4) + i;
+                const float e = exp2_raw(lq > J ? gm[s] - end[J] : kNone);
+                ad[J] = mfma4(vp[n & 1][i], q[s] * e, ad[J]);
+                ad[J] = mfma4(va[n & 1][i], bt4[n & 1][i] * k[s] * e, ad[J]);
+            }
         }
+    }
     to_block(aq, w);
 #pragma unroll
     for (int r = 0; r < 16; ++r) dq[r] += exp2_raw(gm[r] - ref) * w[r];
@@ -910,27 +932,30 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     for (int r = 0; r < 16; ++r) ar[r] += exp2_raw(own - gm[r]) * w[r];
 
     // pairs inside the lane's block: w[i] holds e^{gamma_r - gamma_i}, decayed row by row
+    f32x4_t vp[2][4], va[2][4];   // rows r and r + 1 of the lane's diagonal blocks
+    auto read = [&](int r) {
+        const int o = tri_at<PC>(16 * lq + r, 16 * lq);
+#pragma unroll
+        for (int i4 = 0; i4 <= r / 4; ++i4) {
+            vp[r & 1][i4] = *reinterpret_cast<const f32x4_t*>(&sm.dP[o + 4 * i4]);
+            va[r & 1][i4] = *reinterpret_cast<const f32x4_t*>(&sm.dA[o + 4 * i4]);
+        }
+    };
+    read(0);
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
+        if (r + 1 < 16) read(r + 1);
         pin();
-        const float* pr = &sm.dP[tri_at<PC>(16 * lq + r, 16 * lq)];
-        const float* pa = &sm.dA[tri_at<PC>(16 * lq + r, 16 * lq)];
         const float bk = sm.beta[16 * lq + r] * k[r];
         w[r] = 1.f;
 #pragma unroll
-        for (int i4 = 0; i4 <= r / 4; ++i4) {
-            const f32x4_t vp = *reinterpret_cast<const f32x4_t*>(pr + 4 * i4);
-            const f32x4_t va = *reinterpret_cast<const f32x4_t*>(pa + 4 * i4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 4 * i4 + e;
-                if (i > r) continue;
-                if (i < r) w[i] *= a[r];
-                const float ke = w[i] * k[i];
-                dq[r] += vp[e] * ke;
-                if (i < r) l[r] += va[e] * ke;
-                ar[i] += (i < r ? vp[e] * q[r] + va[e] * bk : vp[e] * q[r]) * w[i];
-            }
+        for (int i = 0; i <= r; ++i) {
+            const float p1 = vp[r & 1][i / 4][i % 4], p2 = va[r & 1][i / 4][i % 4];
+            if (i < r) w[i] *= a[r];
+            const float ke = w[i] * k[i];
+            dq[r] += p1 * ke;
+            if (i < r) l[r] += p2 * ke;
+            ar[i] += (i < r ? p1 * q[r] + p2 * bk : p1 * q[r]) * w[i];
         }
         // the row's sums are formed here, not at their use at the end
         hold(dq[r]);
