@@ -124,9 +124,9 @@ GDN_EXPORT const char* gdn_status_string(int status) {
         case GDN_ERR_NULL: return "a required pointer is NULL";
         case GDN_ERR_SHAPE: return "a size is out of range or inconsistent";
         case GDN_ERR_DTYPE: return "unknown dtype code";
-        case GDN_ERR_ALIGN: return "a pointer is misaligned (q/k/v/o/states 16 B, gates 4 B, workspace 256 B)";
-        case GDN_ERR_UNSUPPORTED: return "unsupported chunk size or head dimension (chunk 64; d_k, d_v in {64, 128})";
-        case GDN_ERR_WORKSPACE: return "workspace missing or smaller than gdn_chunk_fwd_workspace_bytes()";
+        case GDN_ERR_ALIGN: return "a pointer or stride is misaligned (q/k/v/o/states 16 B, gates 4 B, workspace 256 B)";
+        case GDN_ERR_UNSUPPORTED: return "unsupported chunk size, head dimension, norm or rotation (chunk 64; d_k, d_v in {64, 128})";
+        case GDN_ERR_WORKSPACE: return "workspace missing or smaller than the entry point's ..._workspace_bytes()";
         case GDN_ERR_HIP: return "a HIP launch failed";
         default: return "unknown status";
     }

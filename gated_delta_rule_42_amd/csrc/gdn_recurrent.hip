@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256) void recurrent_kernel(RecurrentProblem p) {
     constexpr int TB = 1024 / DK;                // tokens per block: four channels per thread
     constexpr int NVB = TB * 16 * RPG / 256 > 0 ? TB * 16 * RPG / 256 : 1;   // value rows per thread and block
     constexpr int LB = RUNS ? TB : 1;
-    __shared__ float sk[LB][DK], sq[LB][DK], sa[CW ? LB : 1][DK], sv[LB][16 * RPG];
+    __shared__ alignas(16) float sk[LB][DK], sq[LB][DK], sa[CW ? LB : 1][DK], sv[LB][16 * RPG];
     __shared__ float4 sc[LB];                    // alpha (scalar gate), beta, k . q
     const int tid = threadIdx.x, l16 = tid & 15, grp = tid >> 4;
     const long unit = blockIdx.x / TILES;

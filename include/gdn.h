@@ -67,7 +67,7 @@ typedef enum {
     GDN_ERR_SHAPE = -2,       /* a size is out of range or inconsistent */
     GDN_ERR_DTYPE = -3,       /* unknown dtype code */
     GDN_ERR_ALIGN = -4,       /* a pointer is misaligned */
-    GDN_ERR_UNSUPPORTED = -5, /* chunk size or head dimension not built */
+    GDN_ERR_UNSUPPORTED = -5, /* chunk size, head dimension, norm or rotation not built */
     GDN_ERR_WORKSPACE = -6,   /* workspace missing or smaller than required */
     GDN_ERR_HIP = -7          /* a HIP launch reported an error */
 } gdn_status;
@@ -435,7 +435,8 @@ int gdn_recurrent_fwd(const void *q, const void *k, const void *v, const float *
  *               strides in elements (views of a fused projection need no copy)
  *   q_weight, k_weight  fp32 [d] (16-byte aligned) or NULL (ones)
  *   positions   int32 [tokens], inv_freq fp32 [rot / 2]; not used when rot = 0
- *   q_out, k_out  dense [tokens, hq, d], [tokens, hk, d] out_dtype (GDN_BF16 only for bf16 inputs)
+ *   q_out, k_out  dense [tokens, hq, d], [tokens, hk, d] out_dtype (GDN_BF16 only for bf16 inputs);
+ *               may be q, k themselves where those are dense and of that type, other overlaps are undefined
  *   d           a multiple of 8, 8 .. 256; rot 0 .. d, a multiple of 2 (half layout: of 16)
  *   eps > 0; hq, hk >= 1; tokens * (hq + hk) <= 2^28
  * Pointers and strides are multiples of 16 bytes. A row of zeros gives zeros. Sums of squares are
