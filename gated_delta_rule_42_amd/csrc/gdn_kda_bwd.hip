@@ -53,11 +53,12 @@ __device__ __forceinline__ void hold(float& x) { asm volatile("" : "+v"(x)); }
 // ------------------------------------------------------------------- the two walks
 // The state walk (S entering each chunk, D) and the reverse walk (dS' leaving each chunk, Y) do not need each other and
 // run side by side in one launch (one after the other, on tiles of 32 columns: 357 us for the training shape, against 320).
-// One work-group per walk, (sequence, head) and tile of 16 NCG columns of d_v (NCG 2 or 4, see kNarrowWalks), 2 NCG waves. Wave
-// w has the 16 columns cg = w % NCG and the half hf = w / NCG of the d_k channels: S^T [dk/2, 16] in accumulator registers. Per chunk each wave forms its half of the products over d_k for all 64 rows, the two halves
-// are added through LDS, the triangular product (with T or T^T) is shared by row tiles ({0, 3} and {1, 2}: five block
-// products each), and each wave updates its own channels. Operators go global -> registers -> LDS a chunk ahead, all of
-// these memory instructions placed between the products, whose steps hide them.
+// One work-group per walk, (sequence, head) and tile of 16 NCG columns of d_v, NHF NCG waves (NCG x NHF is 1 x 4, 2 x 2 or
+// 4 x 2, see kNarrowWalks). Wave w has the 16 columns cg = w % NCG and the part hf = w / NCG of the d_k channels:
+// S^T [dk/NHF, 16] in accumulator registers. Per chunk each wave forms its part of the products over d_k for all 64 rows,
+// the parts are added through LDS, the triangular product (with T or T^T) is shared by row tiles (see TriFrags), and each
+// wave updates its own channels. Operators go global -> registers -> LDS a chunk ahead, all of these memory instructions
+// placed between the products, whose steps hide them.
 constexpr int kWalkPitch = 4;   // pad of an operator row in LDS (floats)
 
 // A [64, W] fp32 operator on its way into LDS (row pitch W + kWalkPitch): NV 16-byte pieces per thread, held in registers
@@ -187,12 +188,13 @@ __device__ __forceinline__ void mul_cols(f32x4_t (&acc)[NJ], const float* m, int
     }
     __builtin_amdgcn_sched_barrier(0);
 }
-// The wave's share of a product with a lower triangular matrix m (TRANS: with m^T): row tiles 0 and 3 for hf = 0, 1 and 2
-// for hf = 1, five block products either way.
-template <bool TRANS>
+// The wave's share of a product with a lower triangular matrix m (TRANS: with m^T). NHF = 2: row tiles 0 and 3 for
+// hf = 0, 1 and 2 for hf = 1, five block products either way. NHF = 4: row tile hf.
+template <bool TRANS, int NHF>
 struct TriFrags {
-    f32x4_t a[5];
-    // block of (row tile, contraction tile) number i: (0,0) (3,0) (3,1) (3,2) (3,3) or (1,0) (1,1) (2,0) (2,1) (2,2);
+    static constexpr int NB = NHF == 2 ? 5 : 4;
+    f32x4_t a[NB];
+    // NHF = 2, block of (row tile, contraction tile) number i: (0,0) (3,0) (3,1) (3,2) (3,3) or (1,0) (1,1) (2,0) (2,1) (2,2);
     // transposed: (3,3) (0,0) (0,1) (0,2) (0,3) or (2,2) (2,3) (1,1) (1,2) (1,3)
     template <int HF>
     static constexpr int row(int i) {
@@ -202,8 +204,15 @@ struct TriFrags {
     static constexpr int con(int i) {
         return TRANS ? (HF == 0 ? (i == 0 ? 3 : i - 1) : (i < 2 ? 2 + i : i - 1)) : (HF == 0 ? (i == 0 ? 0 : i - 1) : (i < 2 ? i : i - 2));
     }
-    __device__ __forceinline__ void read(const float* m, int hf, int i, int l16, int lq) {   // i = 0 .. 4
-        const int t = hf == 0 ? row<0>(i) : row<1>(i), t2 = hf == 0 ? con<0>(i) : con<1>(i);
+    __device__ __forceinline__ void read(const float* m, int hf, int i, int l16, int lq) {   // i = 0 .. NB - 1
+        int t = hf, t2 = i;
+        if constexpr (NHF == 2) {
+            t = hf == 0 ? row<0>(i) : row<1>(i);
+            t2 = hf == 0 ? con<0>(i) : con<1>(i);
+        } else if (TRANS ? t2 < t : t2 > t) {   // a block of zeros
+            a[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            return;
+        }
         if constexpr (TRANS) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) a[i][s] = m[tri_tile(t2, t) + tri_row(4 * lq + s) + l16];
@@ -211,38 +220,43 @@ struct TriFrags {
             a[i] = *reinterpret_cast<const f32x4_t*>(&m[tri_tile(t, t2) + tri_row(l16) + 4 * lq]);
         }
     }
-    // The two row tiles of the product with x, each block's product on its own accumulator
+    // The wave's row tiles of the product with x (NHF = 4: the first only), each block's product on its own accumulator
     template <int HF>
-    __device__ __forceinline__ void mul_of(const f32x4_t (&x)[4], f32x4_t& first, f32x4_t& second) const {
-        f32x4_t d[5];
+    __device__ __forceinline__ void mul_of(const f32x4_t (&x)[4], f32x4_t (&y)[2]) const {
+        f32x4_t d[NB];
 #pragma unroll
-        for (int i = 0; i < 5; ++i) d[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < NB; ++i) d[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int i = 0; i < 5; ++i) d[i] = mfma4(a[i][s], x[con<HF>(i)][s], d[i]);
-        if constexpr (HF == 0) first = d[0], second = (d[1] + d[2]) + (d[3] + d[4]);
-        else first = d[0] + d[1], second = (d[2] + d[3]) + d[4];
+            for (int i = 0; i < NB; ++i) d[i] = mfma4(a[i][s], x[NHF == 2 ? con<HF>(i) : i][s], d[i]);
+        if constexpr (NHF == 4) y[0] = (d[0] + d[1]) + (d[2] + d[3]);
+        else if constexpr (HF == 0) y[0] = d[0], y[1] = (d[1] + d[2]) + (d[3] + d[4]);
+        else y[0] = d[0] + d[1], y[1] = (d[2] + d[3]) + d[4];
     }
-    __device__ __forceinline__ void mul(const f32x4_t (&x)[4], int hf, f32x4_t& first, f32x4_t& second) const {
-        if (hf == 0) mul_of<0>(x, first, second);
-        else mul_of<1>(x, first, second);
+    __device__ __forceinline__ void mul(const f32x4_t (&x)[4], int hf, f32x4_t (&y)[2]) const {
+        if (NHF == 4 || hf == 0) mul_of<0>(x, y);
+        else mul_of<1>(x, y);
     }
-    static __device__ __forceinline__ int first_tile(int hf) { return TRANS ? (hf == 0 ? 3 : 2) : (hf == 0 ? 0 : 1); }
-    static __device__ __forceinline__ int second_tile(int hf) { return TRANS ? (hf == 0 ? 0 : 1) : (hf == 0 ? 3 : 2); }
+    static constexpr int TILES = NHF == 2 ? 2 : 1;
+    static __device__ __forceinline__ int tile(int hf, int k) {   // row tile of y[k]
+        if (NHF == 4) return hf;
+        if (TRANS) return hf == 0 ? (k ? 0 : 3) : (k ? 1 : 2);
+        return hf == 0 ? (k ? 3 : 0) : (k ? 2 : 1);
+    }
 };
 
-template <int DK, int NCG>
+template <int DK, int NCG, int NHF>
 struct alignas(16) KdaStateSmem {
     float Kh[64 * (DK + kWalkPitch)];
     float Kd[64 * (DK + kWalkPitch)];
     float T[kTriFloats];
     float lam[DK];
     float beta[64];
-    f32x4_t ex[2 * NCG][4][64];    // each wave's partial products, row tile by row tile
+    f32x4_t ex[NHF * NCG][4][64];    // each wave's partial products, row tile by row tile
     f32x4_t ex2[NCG][4][64];   // the triangular product, per column group
 };
-template <int DK, int NCG>
+template <int DK, int NCG, int NHF>
 struct alignas(16) KdaRevSmem {
     float Kd[64 * (DK + kWalkPitch)];
     union {
@@ -253,8 +267,16 @@ struct alignas(16) KdaRevSmem {
     float PT[2 * kTriFloats];   // P, then T
     float lam[DK];
     float beta[64];
-    f32x4_t ex[2 * NCG][4][64];
+    f32x4_t ex[NHF * NCG][4][64];
 };
+
+// The sum of the NHF partial products of row tile t, the same in every wave.
+template <int NCG, int NHF, typename SM>
+__device__ __forceinline__ f32x4_t join(const SM& sm, int cg, int t, int lane) {
+    const f32x4_t x = sm.ex[cg][t][lane] + sm.ex[cg + NCG][t][lane];
+    if constexpr (NHF == 2) return x;
+    else return x + (sm.ex[cg + 2 * NCG][t][lane] + sm.ex[cg + 3 * NCG][t][lane]);
+}
 
 struct Chain {   // the chunks of the work-group's (sequence, head)
     long pair, sbos, seos, cbase, nchunks;
@@ -281,9 +303,9 @@ __device__ __forceinline__ Chain chain_of(const ChunkProblem& p, long b, long nb
 
 // Barriers of a chunk: (1) its first operators are in LDS; (2) all partial products are exchanged, and the rest of the
 // operators are in; (3) the triangular product is exchanged.
-template <typename TIn, int DK, int DV, int NCG>
-__device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem<DK, NCG>& sm, const Chain& c, int tid) {
-    constexpr int PK = DK + kWalkPitch, HK = DK / 2, NJ = HK / 16, NT = 128 * NCG, NV = WalkTile<DK, NT>::NV;
+template <typename TIn, int DK, int DV, int NCG, int NHF>
+__device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem<DK, NCG, NHF>& sm, const Chain& c, int tid) {
+    constexpr int PK = DK + kWalkPitch, HK = DK / NHF, NJ = HK / 16, NT = 64 * NHF * NCG, NV = WalkTile<DK, NT>::NV;
     const ChunkProblem& p = b.f;
     const int lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave % NCG, hf = wave / NCG;
@@ -345,7 +367,7 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
         f32x4_t X[4], D[4];
         __syncthreads();   // (1)
         TokenCols<TIn, DV>::get(own, D, lane);   // V, until R is formed
-        // this half of X = Kh S^T
+        // this part of X = Kh S^T
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         mul_rows<NJ>(X, sm.Kh, PK, hf * HK, ST, l16, lq, [&](int i) {
@@ -357,22 +379,24 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
 #pragma unroll
         for (int t = 0; t < 4; ++t) sm.ex[wave][t][lane] = X[t];
         __syncthreads();   // (2)
-        TriFrags<false> m;
+        TriFrags<false, NHF> m;
 #pragma unroll
-        for (int i = 0; i < 5; ++i) m.read(sm.T, hf, i, l16, lq);
+        for (int i = 0; i < m.NB; ++i) m.read(sm.T, hf, i, l16, lq);
 #pragma unroll
         for (int t = 0; t < 4; ++t)   // beta R
-            X[t] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * t + 4 * lq]) * (D[t] - (X[t] + sm.ex[wave ^ NCG][t][lane]));
+            X[t] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * t + 4 * lq]) * (D[t] - join<NCG, NHF>(sm, cg, t, lane));
         // D = T beta R on the wave's row tiles
         {
             f32x4_t d[2];
-            m.mul(X, hf, d[0], d[1]);
-            const int ta = m.first_tile(hf), tb = m.second_tile(hf);
-            sm.ex2[cg][ta][lane] = d[0];
-            sm.ex2[cg][tb][lane] = d[1];
+            m.mul(X, hf, d);
             float* dst = b.delta + (widx * 64 + 4 * lq) * DV + col;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[(16 * ta + i) * DV] = d[0][i], dst[(16 * tb + i) * DV] = d[1][i];
+            for (int k = 0; k < m.TILES; ++k) {
+                const int t = m.tile(hf, k);
+                sm.ex2[cg][t][lane] = d[k];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dst[(16 * t + i) * DV] = d[k][i];
+            }
         }
         f32x4_t lm[NJ];
 #pragma unroll
@@ -392,9 +416,9 @@ __device__ __forceinline__ void walk_states(const KdaBwdProblem& b, KdaStateSmem
 
 // Barriers of a chunk: (1) Kd, P, T and dO are in LDS; (2) all partial products are exchanged, and Qh, Kh, lam and beta
 // are in; (3) Qh is dead; (4) the triangular product is exchanged (over Qh).
-template <typename TIn, int DK, int DV, int NCG>
-__device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK, NCG>& sm, const Chain& c, int tid) {
-    constexpr int PK = DK + kWalkPitch, HK = DK / 2, NJ = HK / 16, NT = 128 * NCG, NV = WalkTile<DK, NT>::NV;
+template <typename TIn, int DK, int DV, int NCG, int NHF>
+__device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK, NCG, NHF>& sm, const Chain& c, int tid) {
+    constexpr int PK = DK + kWalkPitch, HK = DK / NHF, NJ = HK / 16, NT = 64 * NHF * NCG, NV = WalkTile<DK, NT>::NV;
     const ChunkProblem& p = b.f;
     const int lane = tid & 63, l16 = lane & 15, lq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave % NCG, hf = wave / NCG;
@@ -472,22 +496,25 @@ __device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK,
             const int len = (int)min(64L, c.seos - (c.sbos + jc * 64));
             if (c.tile == 0 && tid < len) b.dbeta[(c.sbos + jc * 64 + tid) * H + c.h] = 0.f;
         }
-        // this wave's share of dD = Kd dS'^T + P^T dO: its half of the channels, and of the row tiles of P^T dO ({3, 0}, {2, 1})
+        // this wave's share of dD = Kd dS'^T + P^T dO: its part of the channels, and of the row tiles of P^T dO
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        TriFrags<true> pf;
+        TriFrags<true, NHF> pf;
         mul_rows<NJ>(X, sm.Kd, PK, hf * HK, dST, l16, lq, [&](int i) {
             if (i % 2 == 0) store2(i / 2);
-            if (i >= 11) pf.read(sm.PT, hf, i - 11, l16, lq);
+            if (i >= 16 - pf.NB) pf.read(sm.PT, hf, i - (16 - pf.NB), l16, lq);
             const int j = i / 4;
             if (i % 4 == 1 && j < NJ)
                 *reinterpret_cast<f32x4_t*>(b.dstates + (widx * DV + col) * DK + hf * HK + 16 * j + 4 * lq) = dST[j];
         });
         {
             f32x4_t y[2];
-            pf.mul(dO, hf, y[0], y[1]);
-            if (hf == 0) X[3] += y[0], X[0] += y[1];
-            else X[2] += y[0], X[1] += y[1];
+            pf.mul(dO, hf, y);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int k = 0; k < pf.TILES; ++k)
+                    if (pf.tile(hf, k) == t) X[t] += y[k];
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) sm.ex[wave][t][lane] = X[t];
@@ -495,23 +522,25 @@ __device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK,
         // dS'^T Diag(lam) + Qh^T dO on the wave's channels
 #pragma unroll
         for (int j = 0; j < NJ; ++j) dST[j] *= *reinterpret_cast<const f32x4_t*>(&sm.lam[hf * HK + 16 * j + 4 * lq]);
-        TriFrags<true> tf;
+        TriFrags<true, NHF> tf;
         mul_cols<NJ>(dST, sm.Qh, PK, hf * HK, dO, l16, lq, [&](int i) {
             if (i % 2 == 0) load2(nxt, i / 2);
-            if (i < 4) X[i] += sm.ex[wave ^ NCG][i][lane];   // dD
-            if (i >= 11) tf.read(sm.PT + kTriFloats, hf, i - 11, l16, lq);
+            if (i < 4) X[i] = join<NCG, NHF>(sm, cg, i, lane);   // dD
+            if (i >= 16 - tf.NB) tf.read(sm.PT + kTriFloats, hf, i - (16 - tf.NB), l16, lq);
         });
         __syncthreads();   // (3)
         // Y = T^T dD on the wave's row tiles
         {
             f32x4_t y[2];
-            tf.mul(X, hf, y[0], y[1]);
-            const int ta = tf.first_tile(hf), tb = tf.second_tile(hf);
-            sm.ex2[cg][ta][lane] = y[0];
-            sm.ex2[cg][tb][lane] = y[1];
+            tf.mul(X, hf, y);
             float* dst = b.ymat + (widx * 64 + 4 * lq) * DV + col;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[(16 * ta + i) * DV] = y[0][i], dst[(16 * tb + i) * DV] = y[1][i];
+            for (int k = 0; k < tf.TILES; ++k) {
+                const int t = tf.tile(hf, k);
+                sm.ex2[cg][t][lane] = y[k];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dst[(16 * t + i) * DV] = y[k][i];
+            }
         }
         __syncthreads();   // (4)
 #pragma unroll
@@ -526,17 +555,17 @@ __device__ __forceinline__ void walk_back(const KdaBwdProblem& b, KdaRevSmem<DK,
 }
 
 // The reverse walks are the longer ones and come first.
-template <typename TIn, int DK, int DV, int NCG>
-__global__ __launch_bounds__(128 * NCG) void kda_bwd_walk_kernel(KdaBwdProblem b) {
+template <typename TIn, int DK, int DV, int NCG, int NHF>
+__global__ __launch_bounds__(64 * NHF * NCG) void kda_bwd_walk_kernel(KdaBwdProblem b) {
     __shared__ union Smem {
         __device__ Smem() {}
-        KdaRevSmem<DK, NCG> back;
-        KdaStateSmem<DK, NCG> states;
+        KdaRevSmem<DK, NCG, NHF> back;
+        KdaStateSmem<DK, NCG, NHF> states;
     } sm;
     constexpr int TILES = DV / (16 * NCG);
     const long half = gridDim.x / 2;
-    if (blockIdx.x < half) walk_back<TIn, DK, DV, NCG>(b, sm.back, chain_of<TILES>(b.f, blockIdx.x, half), threadIdx.x);
-    else walk_states<TIn, DK, DV, NCG>(b, sm.states, chain_of<TILES>(b.f, blockIdx.x - half, half), threadIdx.x);
+    if (blockIdx.x < half) walk_back<TIn, DK, DV, NCG, NHF>(b, sm.back, chain_of<TILES>(b.f, blockIdx.x, half), threadIdx.x);
+    else walk_states<TIn, DK, DV, NCG, NHF>(b, sm.states, chain_of<TILES>(b.f, blockIdx.x - half, half), threadIdx.x);
 }
 
 // ------------------------------------------------------------------- gradients of each chunk
@@ -1024,20 +1053,31 @@ KdaBwdLayout kda_bwd_workspace_layout(int B, int T, int H, int dk, int dv, int N
     return w;
 }
 
-// Work-groups of 32 columns (four waves, a SIMD each) step a chunk in about 6 us, those of 64 columns (eight waves) in about 10,
-// moving half the operators per column. As long as all narrow ones run at once, they win (16 pairs x 64 chunks: 557 us
-// the whole pass against 757; 32 x 32: 410, 495; at 64 x 32 wide ones do: 753, 715). Packed sequences mostly differ in length,
-// so the longest one's time counts up to twice as many (64 pairs, 64 .. 1600 tokens: 300 us narrow, 370 wide).
-constexpr long kNarrowWalks = 256;
+// The rule by the number of work-groups of 32 columns. Those (2 x 2 waves, a SIMD each) step a chunk in about 6 us, those of
+// 64 columns (4 x 2 waves) in about 10, moving half the operators per column, those of 16 (1 x 4 waves) in about 5, moving
+// twice as many. The narrower ones win as long as all of them run at once. The whole pass, dk = dv = 128, bf16:
+//   pairs x chunks   16 columns   32    64
+//    4 x 64             323      398
+//   16 x 64             488      553   757
+//   18 x 64             665      578
+//   32 x 32                      410   495
+//   64 x 32                      753   715
+// Packed sequences mostly differ in length, so the longest one's time counts up to twice as many of 32 columns (64 pairs,
+// 64 .. 1600 tokens: 300 us, with 64 columns 370); those of 16 keep their limit (16 pairs: 199 us against 225, 32: 242, 230).
+constexpr long kShortWalks = 128, kNarrowWalks = 256;
 
 template <typename TIn, int DK, int DV>
 static hipError_t kda_bwd_launch(const KdaBwdProblem& b, hipStream_t s) {
     const ChunkProblem& p = b.f;
     const long pairs = (long)p.N * p.H, units = p.nc_bound * p.H;
     if (pairs == 0) return hipSuccess;
-    const bool narrow = 2 * pairs * (DV / 32) <= (p.cu_seqlens ? 2 : 1) * kNarrowWalks;
-    const hipError_t e = narrow ? launch(kda_bwd_walk_kernel<TIn, DK, DV, 2>, dim3((unsigned)(2 * pairs * (DV / 32))), dim3(256), s, b)
-                                : launch(kda_bwd_walk_kernel<TIn, DK, DV, 4>, dim3((unsigned)(2 * pairs * (DV / 64))), dim3(512), s, b);
+    auto walk = [&](auto kern, int columns, int threads) {
+        return launch(kern, dim3((unsigned)(2 * pairs * (DV / columns))), dim3(threads), s, b);
+    };
+    const long groups = 2 * pairs * (DV / 32);   // work-groups of 32 columns
+    const hipError_t e = groups <= kShortWalks ? walk(kda_bwd_walk_kernel<TIn, DK, DV, 1, 4>, 16, 256)
+                         : groups <= (p.cu_seqlens ? 2 : 1) * kNarrowWalks ? walk(kda_bwd_walk_kernel<TIn, DK, DV, 2, 2>, 32, 256)
+                                                                         : walk(kda_bwd_walk_kernel<TIn, DK, DV, 4, 2>, 64, 512);
     if (e != hipSuccess || units == 0) return e;
     const dim3 grid((unsigned)(units * (DK / 64)));
     return b.grad_bf16 ? launch(kda_bwd_grad_kernel<TIn, uint16_t, DK, DV>, grid, dim3(256), s, b)

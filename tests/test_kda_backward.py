@@ -154,6 +154,16 @@ def test_many_heads(T, H, dk, dv, dtype, packed):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H,dk,dv,dtype,packed", [
+    (130, 17, 64, 128, "f32", False), (150, 32, 128, 128, "bf16", False), (100, 35, 64, 64, "bf16", False),
+    (130, 33, 128, 64, "f32", False), (0, 30, 128, 128, "bf16", True)])
+def test_middling_heads(T, H, dk, dv, dtype, packed):
+    """(sequence, head) pairs for work-groups of 32 columns."""
+    x = make(73, 1, T, H, dk, dv, dtype, True, 0.1, lengths=[65, 40] if packed else None)
+    check(x, SY.make_cotangents(x, 74), heads=[0, H // 2, H - 1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,dk,dv", [("f32", 128, 128), ("bf16", 128, 128), ("bf16", 64, 128)])
 def test_packed(dtype, dk, dv):
     """Packed sequences, some of them empty (their dh0 is dhT), single tokens, ends inside and at chunk borders."""
