@@ -15,6 +15,7 @@
 //     dq = e^gamma (dO S) + aq,   l = al - e^gamma (Y S),   x = e^{gamma_last - gamma} (D dS')
 //     dk = beta l + x + ar,   dbeta_r = Y_r . V_r + k_r . l_r
 //     dgamma = q dq + k (beta l - x - ar),   and into every row of dg: sum_r k x + lam colsum(S dS')
+//     (the pairs i = r of dq and ar cancel in dgamma and are left out there),
 //     dg = the reverse cumulative sum of dgamma in the chunk + that.
 // (dbeta needs no second look at A: sum_i dA[r,i] G[r,i] = k_r . al_r, and Y_r . R_r = Y_r . V_r - (Y S)_r . Kh_r.)
 //
@@ -965,7 +966,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     auto read = [&](int r) {
         const int o = tri_at<PC>(16 * lq + r, 16 * lq);
 #pragma unroll
-        for (int i4 = 0; i4 <= r / 4; ++i4) {
+        for (int i4 = 0; 4 * i4 < r; ++i4) {
             vp[r & 1][i4] = *reinterpret_cast<const f32x4_t*>(&sm.dP[o + 4 * i4]);
             va[r & 1][i4] = *reinterpret_cast<const f32x4_t*>(&sm.dA[o + 4 * i4]);
         }
@@ -978,28 +979,30 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
         const float bk = sm.beta[16 * lq + r] * k[r];
         w[r] = 1.f;
 #pragma unroll
-        for (int i = 0; i <= r; ++i) {
+        for (int i = 0; i < r; ++i) {
             const float p1 = vp[r & 1][i / 4][i % 4], p2 = va[r & 1][i / 4][i % 4];
-            if (i < r) w[i] *= a[r];
+            w[i] *= a[r];
             const float ke = w[i] * k[i];
             dq[r] += p1 * ke;
-            if (i < r) l[r] += p2 * ke;
-            ar[i] += (i < r ? p1 * q[r] + p2 * bk : p1 * q[r]) * w[i];
+            l[r] += p2 * ke;
+            ar[i] += (p1 * q[r] + p2 * bk) * w[i];
         }
         // the row's sums are formed here, not at their use at the end
         hold(dq[r]);
         hold(l[r]);
 #pragma unroll
-        for (int i = 0; i <= r; ++i) hold(ar[i]);
+        for (int i = 0; i < r; ++i) hold(ar[i]);
     }
-    // gradients
+    // gradients; a token's pair with itself has no decay, so it stays out of w (its two parts there would cancel)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
         const float bl = sm.beta[16 * lq + r] * l[r];
         w[r] = q[r] * dq[r] + k[r] * (bl - ar[r]);
         const float db = row16_sum(k[r] * l[r]);
         if (l16 == 0) sm.part[wave][16 * lq + r] = db;
-        l[r] = bl + ar[r];   // dk
+        const float own_pair = sm.dP[tri_at<PC>(16 * lq + r, 16 * lq + r)];
+        dq[r] += own_pair * k[r];
+        l[r] = bl + ar[r] + own_pair * q[r];   // dk
     }
     kx += __shfl_xor(kx, 16, 64);
     kx += __shfl_xor(kx, 32, 64);

@@ -176,6 +176,16 @@ def test_packed(dtype, dk, dv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,dk,dhT", [("f32", 64, False), ("bf16", 128, False), ("bf16", 128, True)])
+def test_single_tokens_from_nothing(dtype, dk, dhT):
+    """A first token's decay acts on a state of zeros, so its gradient is zero, not the rounding of terms that cancel."""
+    x = make(51, 1, 0, 3, dk, 64, dtype, False, 0.5, lengths=[1, 0, 1, 1])
+    cot = SY.make_cotangents(x, 52, dhT=dhT)
+    check(x, cot)
+    assert not gpu_bwd(x, cot)[3].any()
+
+
+@pytest.mark.gpu
 def test_beta_to_2_and_mixed_decays():
     """Erasing strengths beyond 1, and channels of very different decays side by side (one of them stepwise)."""
     x = make(43, 1, 200, 2, 128, 128, "bf16", True, 0.01, beta_scale=2.0)
