@@ -385,10 +385,17 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
-def _dense(**ts):
+def _dense_on(device, **ts):
+    """_same_gpu, and every given tensor contiguous."""
+    if device.type != "cuda":
+        raise ValueError("gdn: every tensor must be on a GPU")
+    index = device.index
     for name, t in ts.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"gdn: {name} must be contiguous")
+        if t is not None:
+            if t.get_device() != index:
+                raise ValueError(f"gdn: {name} is on {t.device}, expected {device}")
+            if not t.is_contiguous():
+                raise ValueError(f"gdn: {name} must be contiguous")
 
 
 # the current stream's handle without the Stream object around it, where this torch has it: a call's checks and marshalling
@@ -399,10 +406,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _new(shape, dtype, device, stream):
     """An output or workspace of a call on `stream`, from that stream's share of the allocator: memory that is still in
     use on another stream is never handed out for it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+    if stream is None:   # the sizes one by one: 1.3 us where a shape object takes 2.1
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _call(name, device, stream, *args):
@@ -483,17 +490,18 @@ def gdn_recurrent_fwd(q, k, v, g, beta, states, slots, cu_seqlens=None, out_slot
     _expect(cu_seqlens, "cu_seqlens", (N + 1,), (torch.int32,))
     _expect(out_slots, "out_slots", (T,), (torch.int32,))
     _expect(o, "o", (T, HV, dv), _IN)
-    _same_gpu(q.device, k=k, v=v, g=g, beta=beta, states=states, slots=slots, cu_seqlens=cu_seqlens,
-              out_slots=out_slots, o=o)
-    _dense(g=g, beta=beta, states=states, slots=slots, cu_seqlens=cu_seqlens, out_slots=out_slots, o=o)
+    dev = q.device
+    _same_gpu(dev, k=k, v=v)
+    _dense_on(dev, g=g, beta=beta, states=states, slots=slots, cu_seqlens=cu_seqlens, out_slots=out_slots, o=o)
     strides = []
-    for name, t, d in (("q", q, dk), ("k", k, dk), ("v", v, dv)):
-        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+    for name, t, heads, d in (("q", q, H, dk), ("k", k, H, dk), ("v", v, HV, dv)):
+        step = t.stride()
+        if T and (step[2] != 1 or (heads > 1 and step[1] != d)):
             raise ValueError(f"gdn: the heads of {name} must follow each other densely within a token")
-        strides.append(t.stride(0) if t.shape[0] > 1 else 0)
+        strides.append(step[0] if T > 1 else 0)
     if o is None:
-        o = _new((T, HV, dv), o_dtype, q.device, stream)
-    _call("gdn_recurrent_fwd", q.device, stream, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(states),
+        o = _new((T, HV, dv), o_dtype, dev, stream)
+    _call("gdn_recurrent_fwd", dev, stream, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(states),
           _adr(slots), _adr(cu_seqlens), _adr(out_slots), _adr(o), T, N, H, HV, dk, dv, states.shape[0], *strides,
           int(channels), _DTYPE.get(q.dtype, -1), _DTYPE.get(o.dtype, -1))
     return o
@@ -526,8 +534,9 @@ def _check_norm_args(q, k, q_weight, k_weight, positions, inv_freq, norm, layout
             raise ValueError("gdn: inv_freq must be a 1-D float32 tensor of rot / 2 frequencies")
         rot = 2 * inv_freq.numel()
         _expect(positions, "positions", lead, (torch.int32,))
-    _same_gpu(q.device, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq)
-    _dense(q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq)
+    dev = q.device
+    _same_gpu(dev, k=k)
+    _dense_on(dev, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq)
     tokens = 1
     for n in lead:
         tokens *= n
@@ -543,19 +552,19 @@ def gdn_qk_norm_fwd(q, k, q_weight=None, k_weight=None, *, positions=None, inv_f
     (default the dtype of q; fp32 is allowed for bf16 inputs)."""
     tokens, hq, hk, d, rot = _check_norm_args(q, k, q_weight, k_weight, positions, inv_freq, norm, layout)
     qs, ks = _row_strides(q, "q"), _row_strides(k, "k")
-    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        _expect(t, name, like.shape, _IN)
-    if q_out is not None and k_out is not None and q_out.dtype != k_out.dtype:
-        raise ValueError("gdn: q_out and k_out must have one dtype")
-    given = q_out if q_out is not None else k_out
-    od = given.dtype if given is not None else (out_dtype or q.dtype)
+    dev, od = q.device, out_dtype or q.dtype
+    if q_out is not None or k_out is not None:
+        _expect(q_out, "q_out", q.shape, _IN)
+        _expect(k_out, "k_out", k.shape, _IN)
+        if q_out is not None and k_out is not None and q_out.dtype != k_out.dtype:
+            raise ValueError("gdn: q_out and k_out must have one dtype")
+        _dense_on(dev, q_out=q_out, k_out=k_out)
+        od = (k_out if q_out is None else q_out).dtype
     if q_out is None:
-        q_out = _new(q.shape, od, q.device, stream)
+        q_out = _new(q.shape, od, dev, stream)
     if k_out is None:
-        k_out = _new(k.shape, od, q.device, stream)
-    _same_gpu(q.device, q_out=q_out, k_out=k_out)
-    _dense(q_out=q_out, k_out=k_out)
-    _call("gdn_qk_norm_fwd", q.device, stream, _adr(q), _adr(k), _adr(q_weight), _adr(k_weight), _adr(positions),
+        k_out = _new(k.shape, od, dev, stream)
+    _call("gdn_qk_norm_fwd", dev, stream, _adr(q), _adr(k), _adr(q_weight), _adr(k_weight), _adr(positions),
           _adr(inv_freq), _adr(q_out), _adr(k_out), tokens, hq, hk, d, *qs, *ks, _NORM[norm], eps, rot, _ROPE[layout],
           q_scale, rope_scale, _DTYPE.get(q.dtype, -1), _DTYPE.get(od, -1))
     return q_out, k_out
@@ -577,23 +586,24 @@ def gdn_qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, *, posit
     _expect(dk_out, "dk_out", k.shape, (dq_out.dtype,))
     _expect(dq, "dq", q.shape, (q.dtype,))
     _expect(dk, "dk", k.shape, (q.dtype,))
+    dev = q.device
+    _same_gpu(dev, dq=dq, dk=dk)
+    _dense_on(dev, dq_out=dq_out, dk_out=dk_out, workspace=workspace)
     if dq is None:
-        dq = _new(q.shape, q.dtype, q.device, stream)
+        dq = _new(q.shape, q.dtype, dev, stream)
     if dk is None:
-        dk = _new(k.shape, q.dtype, q.device, stream)
+        dk = _new(k.shape, q.dtype, dev, stream)
     dqw = dkw = None
     if need_dw or (need_dw is None and q_weight is not None):
-        dqw = _new(d, torch.float32, q.device, stream)
+        dqw = _new((d,), torch.float32, dev, stream)
     if need_dw or (need_dw is None and k_weight is not None):
-        dkw = _new(d, torch.float32, q.device, stream)
+        dkw = _new((d,), torch.float32, dev, stream)
     if dqw is not None or dkw is not None:
         need = gdn_qk_norm_bwd_workspace_bytes(tokens, hq, hk, d)
         if workspace is None and need:
-            workspace = _new(need, torch.uint8, q.device, stream)
-    _same_gpu(q.device, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk, workspace=workspace)
-    _dense(dq_out=dq_out, dk_out=dk_out, workspace=workspace)
+            workspace = _new((need,), torch.uint8, dev, stream)
     strides = [s for t, name in ((q, "q"), (k, "k"), (dq, "dq"), (dk, "dk")) for s in _row_strides(t, name)]
-    _call("gdn_qk_norm_bwd", q.device, stream, _adr(q), _adr(k), _adr(dq_out), _adr(dk_out), _adr(q_weight),
+    _call("gdn_qk_norm_bwd", dev, stream, _adr(q), _adr(k), _adr(dq_out), _adr(dk_out), _adr(q_weight),
           _adr(k_weight), _adr(positions), _adr(inv_freq), _adr(dq), _adr(dk), _adr(dqw), _adr(dkw), tokens, hq, hk, d,
           *strides, _NORM[norm], eps, rot, _ROPE[layout], q_scale, rope_scale, _DTYPE.get(q.dtype, -1),
           _DTYPE.get(dq_out.dtype, -1), _adr(workspace),
@@ -613,8 +623,7 @@ def gdn_kda_chunk_bwd(q, k, v, g, beta, do, h0=None, dhT=None, cu_seqlens=None, 
     B, T, H, dk, dv, N = _check_chunk_args(q, k, v, g, beta, h0, cu_seqlens, hT=dhT, g_channels=True)
     _expect(do, "do", (B, T, H, dv), (q.dtype,))
     dev = q.device
-    _same_gpu(dev, k=k, v=v, g=g, beta=beta, do=do, h0=h0, dhT=dhT, cu_seqlens=cu_seqlens, workspace=workspace)
-    _dense(q=q, k=k, v=v, g=g, beta=beta, do=do, h0=h0, dhT=dhT, cu_seqlens=cu_seqlens, workspace=workspace)
+    _dense_on(dev, q=q, k=k, v=v, g=g, beta=beta, do=do, h0=h0, dhT=dhT, cu_seqlens=cu_seqlens, workspace=workspace)
     gd = grad_dtype or q.dtype
     dq = _new(q.shape, gd, dev, stream)
     dk_ = _new(k.shape, gd, dev, stream)
@@ -624,7 +633,7 @@ def gdn_kda_chunk_bwd(q, k, v, g, beta, do, h0=None, dhT=None, cu_seqlens=None, 
     dh0 = _new((N, H, dv, dk), torch.float32, dev, stream) if need_dh0 else None
     need = gdn_kda_chunk_bwd_workspace_bytes(B, T, H, dk, dv, N, cu_seqlens is not None, chunk, q.dtype)
     if workspace is None and need:
-        workspace = _new(need, torch.uint8, dev, stream)
+        workspace = _new((need,), torch.uint8, dev, stream)
     _call("gdn_kda_chunk_bwd", dev, stream, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(do),
           _adr(dhT), _adr(dq), _adr(dk_), _adr(dv_), _adr(dg), _adr(db), _adr(dh0), _adr(cu_seqlens), chunk, B, T, H, dk,
           dv, N, _DTYPE.get(q.dtype, -1), _DTYPE.get(gd, -1), _adr(workspace),
