@@ -566,6 +566,23 @@ int check_norm(const void* q, const void* k, const float* q_weight, const float*
     p->eps = eps; p->q_scale = q_scale; p->rope_scale = rope_scale;
     return GDN_OK;
 }
+
+// Whether two of the rows [d] that start at token * token_stride + head * head_stride share an element (strides >= 0; one of 0
+// is how an expanded tensor looks).
+bool rows_overlap(int tokens, int heads, int d, int64_t token_stride, int64_t head_stride) {
+    if ((tokens > 1 && token_stride < d) || (heads > 1 && head_stride < d)) return true;
+    if (tokens <= 1 || heads <= 1) return false;
+    using wide = __int128;   // a multiple of a stride can leave 64 bits
+    const wide ts = token_stride, hs = head_stride;
+    if (ts >= (heads - 1) * hs + d || hs >= (tokens - 1) * ts + d) return false;   // one dimension within the other
+    // interleaved: head h's first row against the rows of head 0 that start before and behind it (every other pair of rows is such
+    // a pair shifted, or further apart)
+    for (int h = 1; h < heads; ++h) {
+        const wide t = h * hs / ts, behind = h * hs - t * ts;
+        if ((t < tokens && behind < d) || (t + 1 < tokens && ts - behind < d)) return true;
+    }
+    return false;
+}
 }  // namespace
 
 GDN_EXPORT int gdn_qk_norm_fwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
@@ -607,9 +624,8 @@ GDN_EXPORT int gdn_qk_norm_bwd(const void* q, const void* k, const void* dq_out,
     const int64_t strides[] = {dq_token_stride, dq_head_stride, dk_token_stride, dk_head_stride};
     for (int64_t x : strides)
         if (x < 0) return GDN_ERR_SHAPE;
-    // rows of an output must not lie over each other (a stride of 0 is how an expanded tensor looks)
-    if ((tokens > 1 && (dq_token_stride < d || dk_token_stride < d)) || (hq > 1 && dq_head_stride < d) ||
-        (hk > 1 && dk_head_stride < d))
+    // rows of an output must not lie over each other: two work-groups would write the same elements
+    if (rows_overlap(tokens, hq, d, dq_token_stride, dq_head_stride) || rows_overlap(tokens, hk, d, dk_token_stride, dk_head_stride))
         return GDN_ERR_SHAPE;
     if (tokens > 0 && (!dq_out || !dk_out || !dq || !dk)) return GDN_ERR_NULL;
     const void* al16[] = {dq_out, dk_out, dq, dk};

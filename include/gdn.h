@@ -438,7 +438,7 @@ int gdn_recurrent_fwd(const void *q, const void *k, const void *v, const float *
  *   q_out, k_out  dense [tokens, hq, d], [tokens, hk, d] out_dtype (GDN_BF16 only for bf16 inputs);
  *               may be q, k themselves where those are dense and of that type, other overlaps are undefined
  *   d           a multiple of 8, 8 .. 256; rot 0 .. d, a multiple of 2 (half layout: of 16)
- *   eps > 0; hq, hk >= 1; tokens * (hq + hk) <= 2^28
+ *   eps > 0; hq, hk in 1 .. 32768; tokens * (hq + hk) <= 2^28
  * Pointers and strides are multiples of 16 bytes. A row of zeros gives zeros. Sums of squares are
  * fp32: rows of magnitudes above about 1e18 overflow.
  */
@@ -457,7 +457,8 @@ int gdn_qk_norm_fwd(const void *q, const void *k, const float *q_weight, const f
  * also for weights of NULL). The weights' gradients are sums over all tokens and heads in a fixed order and take
  * a workspace of gdn_qk_norm_bwd_workspace_bytes(...) bytes, 256-byte aligned (fp32 [work-groups, 2, d]); without them none is used. The
  * other arguments are the forward call's. dq and dk may be q and k themselves (with their strides) or
- * dense over dq_out, dk_out where the types agree; other overlaps are undefined.
+ * dense over dq_out, dk_out where the types agree; strides that lay rows of dq (or of dk) over each other are
+ * refused (GDN_ERR_SHAPE), other overlaps are undefined.
  */
 size_t gdn_qk_norm_bwd_workspace_bytes(int tokens, int hq, int hk, int d);
 int gdn_qk_norm_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out,

@@ -320,3 +320,36 @@ def test_strides_past_32_bits():
     want = gb.gdn_qk_norm_bwd(t["q"], t["k"], t["dq"], t["dk"], t["qw"], t["kw"], **kw)
     got = gb.gdn_qk_norm_bwd(q, k, t["dq"], t["dk"], t["qw"], t["kw"], dq=q, dk=k, **kw)   # over the inputs
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dqt=64, dqh=64), dict(dkt=64, dkh=64),            # row (1, 0) is row (0, 1)
+    dict(dqt=128, dqh=136), dict(dkt=192, dkh=136),        # rows that share some channels
+    dict(tokens=4, hq=9, dqt=192, dqh=72),                 # ... those of tokens and heads that are not neighbours
+    dict(tokens=2, hq=2, dqt=1 << 61, dqh=(1 << 61) + 8),  # strides whose multiples leave 64 bits
+    dict(tokens=4, hq=3, dqt=1 << 62, dqh=1 << 62),
+])
+def test_bwd_refuses_gradient_rows_that_overlap(kw):
+    """Two work-groups would write the same elements."""
+    assert c_bwd(**kw) == -2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,heads,step", [
+    (7, 5, (64, 448)),       # heads outside
+    (7, 5, (320, 64)),       # tokens outside
+    (3, 3, (192, 128)),      # rows of heads between the tokens' rows: starts 0 2 4, 3 5 7, 6 8 10 of 64
+    (1, 5, (0, 64)), (5, 1, (64, 0)),
+])
+def test_gradients_into_any_order_of_rows(tokens, heads, step):
+    """Rows of tokens and heads in either order or interleaved, as long as none lies over another."""
+    x = make(33, tokens, heads, heads, 64, "bf16", 0, False, fused=False)
+    t = {n: None if v is None else v.cuda() for n, v in x.items()}
+    want = gb.gdn_qk_norm_bwd(t["q"], t["k"], t["dq"], t["dk"])
+    into = [torch.full((64 * 64,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    views = [a.as_strided((tokens, heads, 64), (*step, 1)) for a in into]
+    gb.gdn_qk_norm_bwd(t["q"], t["k"], t["dq"], t["dk"], dq=views[0], dk=views[1])
+    for a, v, w in zip(into, views, want):
+        assert torch.equal(v, w)
+        v.fill_(7.0)
+        assert (a == 7).all()   # nothing beside the rows was written
