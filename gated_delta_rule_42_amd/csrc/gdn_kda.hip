@@ -531,7 +531,7 @@ __global__ __launch_bounds__(kKdaPrepThreads) void kda_prepare_kernel(ChunkProbl
 #pragma unroll
                 for (int it = 0; it < KdaPrepStage<TIn, DK, DEC>::NP; ++it)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) stage.g[it][e] = fmaxf(stage.g[it][e], kMinLogDecay);
+                    for (int e = 0; e < 4; ++e) stage.g[it][e] = clamp_log_decay(stage.g[it][e]);
             }
         }
         stage.store(sm, opaque(tid));

@@ -855,7 +855,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     float a[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        gm[r] = fmaxf(gm[r], kMinLogDecay) * 1.44269504f;
+        gm[r] = clamp_log_decay(gm[r]) * 1.44269504f;
         a[r] = exp2_raw(gm[r]);
         if (r > 0) gm[r] += gm[r - 1];
     }

@@ -272,3 +272,23 @@ def test_empty_problem():
     h = torch.randn(1, 2, 64, 64, device="cuda")
     out = gb.gdn_kda_chunk_bwd(z, z, z, z, z[..., 0].contiguous(), z, None, h)
     assert torch.equal(out[5], h) and out[0].numel() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,dk", [("f32", 128), ("f32", 64), ("bf16", 128), ("bf16", 64)])
+def test_nan_gate_shows(dtype, dk):
+    """A NaN gate reaches the gradients of its own sequence and head, as it reaches the forward pass's outputs, and no others."""
+    x = make(85, 1, 0, 2, dk, 64, dtype, True, 0.1, lengths=[70, 90])
+    cot = SY.make_cotangents(x, 86)
+    want = gpu_bwd(x, cot)
+    x["g"][0, 100, 1, 7] = float("nan")   # token 30 of the second sequence
+    got = gpu_bwd(x, cot)
+    assert torch.isnan(got[3][0, 100, 1, 7]) and torch.isnan(got[5][1, 1, :, 7]).all()
+    for n in (0, 1, 4):   # dq, dk, dbeta of the token and of those behind it in its chunk, whose states are NaN
+        rows = got[n][0, 100:134, 1]
+        assert torch.isnan(rows).all(), NAMES[n]
+    for n, (a, b) in enumerate(zip(want, got)):
+        if n == 5:
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1, 0], b[1, 0])
+        else:
+            assert torch.equal(a[:, :70], b[:, :70]) and torch.equal(a[:, :, 0], b[:, :, 0])
