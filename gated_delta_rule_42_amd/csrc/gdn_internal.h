@@ -190,11 +190,6 @@ struct KdaLayout {
 KdaLayout kda_workspace_layout(int B, int T, int H, int dk, int N, int varlen, int elem);
 hipError_t launch_kda_chunk_fwd(const ChunkProblem& p, hipStream_t s);
 
-// The log decay that the backward pass takes for any smaller one: e^-104 is below half of fp32's smallest number.
-constexpr float kMinLogDecay = -104.f;
-// (not fmaxf, which would take it for a NaN too: a NaN gate has to show in the gradients)
-inline __host__ __device__ float clamp_log_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }
-
 // The channel-wise stage 1 with fp32 operators and products for either input type; T into p.tmat instead of Mmat, and of T
 // and P the lower 16x16 tiles only.
 hipError_t launch_kda_prepare_f32(const ChunkProblem& p, hipStream_t s);

@@ -62,10 +62,12 @@ struct alignas(16) KdaPrepSmem {
     static constexpr int PK = DK + 4, PF = 68;
     float K[64 * PK];
     float Q[64 * PK];
-    float G[64 * PK];   // g, then gamma (in-chunk inclusive cumulative sum, per channel)
-    float A[64 * PF];
-    float T[64 * PF];   // before the Gram products: per row block of the gamma scan, the
-                        // block's sum of g per channel; during them, their scratch
+    // fp32 operators: suf(r) = the sum of g behind row r to the end of its block of 16, per channel, for rows 0 .. 48
+    static constexpr int SUF = 49 * PK;
+    float G[64 * PK];   // gamma (in-chunk inclusive cumulative sum, per channel); fp32 operators: g itself
+    float A[64 * PF];   // fp32 operators, before the Gram products: the scan's sums (see T)
+    float T[SUF > 64 * PF ? SUF : 64 * PF];   // before the Gram products: per row block of the gamma scan, the
+                        // block's sum of g per channel; during them, their scratch or suf
     float P[64 * PF];   // with decoupled gates, until A is formed: the raw Q tile
     float beta[64];
 };
@@ -85,6 +87,8 @@ constexpr int kKdaPrepThreads = 512;
 // diagonal block, grows with the channel's decay over the block's rows. A channel whose decay
 // over the block exceeds e^kMaxRange is left out of the diagonal block's product and summed
 // there exactly instead (one exponent per term), so no factor exceeds e^kMaxRange.
+// The exponents of the fp32 products are sums of exactly the g's between the two rows, never
+// differences of a sum over the chunk, which among tokens of g = -104 has lost 2e-4 (its ulp).
 //
 // F16 (bf16 inputs): the blocks below the diagonal block (J < I) go to the fp16 matrix core
 // instead, factored through the last row of column block J: the left factor
@@ -152,6 +156,7 @@ __device__ __forceinline__ void gram_rows_of(const KdaPrepSmem<DK>& sm, const fl
                                              KdaOffdiag<DK> od, int lane) {
     constexpr int PK = KdaPrepSmem<DK>::PK, PF = KdaPrepSmem<DK>::PF;
     const int l16 = lane & 15, lq = lane >> 4;
+    const float* suf = sm.T;   // fp32 products
     f32x4_t a1[4], a2[4];
 #pragma unroll
     for (int J = 0; J < 4; ++J) a1[J] = a2[J] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -225,26 +230,41 @@ __device__ __forceinline__ void gram_rows_of(const KdaPrepSmem<DK>& sm, const fl
 #pragma unroll 2
         for (int u = HF * DK / 32; u < (HF + 1) * DK / 32; ++u) {
             const int c = 16 * u + 4 * lq;
-            const f32x4_t gref = *reinterpret_cast<const f32x4_t*>(&sm.G[16 * I * PK + c]);
-            const f32x4_t glast = *reinterpret_cast<const f32x4_t*>(&sm.G[(16 * I + 15) * PK + c]);
-            const f32x4_t grow = *reinterpret_cast<const f32x4_t*>(&sm.G[(16 * I + l16) * PK + c]);
-            const f32x4_t l1 = *reinterpret_cast<const f32x4_t*>(&L1[(16 * I + l16) * PK + c]);
+            const auto at = [&](const float* m, int row) { return *reinterpret_cast<const f32x4_t*>(&m[row * PK + c]); };
+            const f32x4_t l1 = at(L1, 16 * I + l16), tot = at(suf, 16 * I);   // tot: of the block's rows behind its first
             f32x4_t l2 = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            if constexpr (TWO) l2 = *reinterpret_cast<const f32x4_t*>(&L2[(16 * I + l16) * PK + c]);
-            f32x4_t kj[I + 1], gj[I + 1];
+            if constexpr (TWO) l2 = at(L2, 16 * I + l16);
+            f32x4_t pre = at(sm.G, 16 * I + l16);   // gamma_r - gamma_ref: summed over the lanes, without the first row
+            f32x4_t kj[I + 1], sj[I + 1];           // sj: gamma_ref - gamma_i
     #pragma unroll
             for (int J = J0; J <= I; ++J) {
-                kj[J] = *reinterpret_cast<const f32x4_t*>(&sm.K[(16 * J + l16) * PK + c]);
-                gj[J] = *reinterpret_cast<const f32x4_t*>(&sm.G[(16 * J + l16) * PK + c]);
+                kj[J] = at(sm.K, 16 * J + l16);
+                if (J < I) sj[J] = at(suf, 16 * J + l16);
+            }
+            f32x4_t gap = at(sm.G, 16 * I);         // from behind block J through row 16 I
+    #pragma unroll
+            for (int J = I - 1; J >= J0; --J) {
+                sj[J] += gap;
+                if (J > 0) gap += at(sm.G, 16 * J) + at(suf, 16 * J);
             }
     #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const bool fits = gref[e] - glast[e] <= kMaxRange;
-                const float el = __expf(grow[e] - gref[e]);
+                float x = l16 == 0 ? 0.f : pre[e];
+                x += dpp_f32<0x111>(x);   // row_shr 1, 2, 4, 8 (0 from before the first lane)
+                x += dpp_f32<0x112>(x);
+                x += dpp_f32<0x114>(x);
+                x += dpp_f32<0x118>(x);
+                pre[e] = x;
+                sj[I][e] = -x;
+            }
+    #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool fits = -tot[e] <= kMaxRange;
+                const float el = __expf(pre[e]);
                 const float x1 = l1[e] * el, x2 = l2[e] * el;
     #pragma unroll
                 for (int J = J0; J <= I; ++J) {
-                    const float b = kj[J][e] * __expf(gref[e] - gj[J][e]);
+                    const float b = kj[J][e] * __expf(sj[J][e]);
                     const float bb = (J < I || fits) ? b : 0.f;
                     a1[J] = mfma4(x1, bb, a1[J]);
                     if constexpr (TWO) a2[J] = mfma4(x2, bb, a2[J]);
@@ -289,23 +309,55 @@ __device__ __forceinline__ void gram_rows_of(const KdaPrepSmem<DK>& sm, const fl
         }
     }
     // channels left out of the diagonal block's product: exact sums over them (each lane adds to
-    // the entries it added to above)
+    // the entries it added to above; fp32: once, after the last channel)
+    float d1[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f};
     for (int c0 = 0; c0 < DK; c0 += 64) {
         const int ch = c0 + lane;
-        const bool out = ch < DK && sm.G[16 * I * PK + ch] - sm.G[(16 * I + 15) * PK + ch] > kMaxRange;
+        bool out;
+        if constexpr (F16) out = ch < DK && sm.G[16 * I * PK + ch] - sm.G[(16 * I + 15) * PK + ch] > kMaxRange;
+        else out = ch < DK && !(-suf[16 * I * PK + ch] <= kMaxRange);
         unsigned long long bits = __ballot(out);
         while (bits) {
             const int c = c0 + __builtin_ctzll(bits);
             bits &= bits - 1;
+            if constexpr (F16) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int r = 16 * I + 4 * lq + m, i = 16 * I + l16;
-                if (i <= r) {
-                    const float e = __expf(sm.G[r * PK + c] - sm.G[i * PK + c]) * sm.K[i * PK + c];
-                    if (strict1 ? i < r : true) O1[r * PF + i] += (rs1 ? rs1[r] : 1.f) * L1[r * PK + c] * e;
-                    if constexpr (TWO) O2[r * PF + i] += L2[r * PK + c] * e;
+                for (int m = 0; m < 4; ++m) {
+                    const int r = 16 * I + 4 * lq + m, i = 16 * I + l16;
+                    if (i <= r) {
+                        const float e = __expf(sm.G[r * PK + c] - sm.G[i * PK + c]) * sm.K[i * PK + c];
+                        if (strict1 ? i < r : true) O1[r * PF + i] += (rs1 ? rs1[r] : 1.f) * L1[r * PK + c] * e;
+                        if constexpr (TWO) O2[r * PF + i] += L2[r * PK + c] * e;
+                    }
+                }
+            } else {
+                // the sum of g over rows i + 1 .. r, by the quads of rows that i and r lie in and those between
+                const float* g = &sm.G[16 * I * PK + c];
+                const int qi = l16 >> 2, ii = l16 & 3;
+                const float* gc = g + 4 * qi * PK;
+                const float m1 = (g[4 * PK] + g[5 * PK]) + (g[6 * PK] + g[7 * PK]), m2 = (g[8 * PK] + g[9 * PK]) + (g[10 * PK] + g[11 * PK]);
+                float x = (ii < 3 ? gc[3 * PK] : 0.f) + (ii < 2 ? gc[2 * PK] : 0.f) + (ii < 1 ? gc[PK] : 0.f);
+                x += (qi < 1 && lq > 1 ? m1 : 0.f) + (qi < 2 && lq > 2 ? m2 : 0.f);
+                if (qi >= lq) x = 0.f;
+                const float ki = sm.K[(16 * I + l16) * PK + c];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int r = 16 * I + 4 * lq + m;
+                    x += qi < lq || m > ii ? g[(4 * lq + m) * PK] : 0.f;
+                    const float e = __expf(x) * ki;
+                    d1[m] += L1[r * PK + c] * e;
+                    if constexpr (TWO) d2[m] += L2[r * PK + c] * e;
                 }
             }
+        }
+    }
+    if constexpr (!F16) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int r = 16 * I + 4 * lq + m, i = 16 * I + l16;
+            if (strict1 ? i < r : i <= r) O1[r * PF + i] += (rs1 ? rs1[r] : 1.f) * d1[m];
+            if constexpr (TWO)
+                if (i <= r) O2[r * PF + i] += d2[m];
         }
     }
 }
@@ -355,9 +407,10 @@ struct KdaPrepStage {
     // with decoupled gates Q is staged too when its raw tile fits in the P buffer (all shapes
     // but fp32 d_k = 128, which loads it when needed)
     static constexpr bool QPRE = !DEC || 64 * DK * EB <= (int)sizeof(KdaPrepSmem<DK>::P);
-    static_assert(RB * DK <= (int)sizeof(KdaPrepSmem<DK>::T) / 4, "the scan's block sums fit in T");
+    static_assert(RB * DK <= (int)sizeof(KdaPrepSmem<DK>::A) / 4, "the scan's block sums fit in A and T");
     u32x4_t k[NP], q[NP];                         // raw groups (bf16: the low 8 bytes)
     f32x4_t g[NP], e[NP];
+    f32x4_t eg[NP];                               // fp32 operators with decoupled gates: e^gamma, for Qh
     float beta;
 
     __device__ __forceinline__ static u32x4_t raw4(__amdgpu_buffer_rsrc_t r, int off) {
@@ -398,9 +451,11 @@ struct KdaPrepStage {
 
     // K and (Q, or E * K with decoupled gates) into LDS as fp32, and with decoupled gates the raw
     // Q tile into P ([64, DK] row-major input elements); g scanned down the thread's rows in
-    // registers, the row block's sum into T
+    // registers, the row block's sum into T (fp32 operators, IMG false: g itself into G, the sum into A)
+    template <bool IMG>
     __device__ __forceinline__ void store(KdaPrepSmem<DK>& sm, int tid) {
         constexpr int PK = KdaPrepSmem<DK>::PK;
+        f32x4_t sum = g[0];
 #pragma unroll
         for (int it = 0; it < NP; ++it) {
             const int r = NP * (tid / NG) + it, cc = 4 * (tid % NG);
@@ -414,9 +469,11 @@ struct KdaPrepStage {
                 if constexpr (EB == 2) *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{q[it][0], q[it][1]};
                 else *reinterpret_cast<u32x4_t*>(dst) = q[it];
             }
-            if (it > 0) g[it] += g[it - 1];
+            if (it > 0) sum += g[it];
+            if constexpr (IMG) g[it] = sum;
+            else *reinterpret_cast<f32x4_t*>(&sm.G[r * PK + cc]) = g[it];
         }
-        *reinterpret_cast<f32x4_t*>(&sm.T[(tid / NG) * DK + 4 * (tid % NG)]) = g[NP - 1];
+        *reinterpret_cast<f32x4_t*>(&(IMG ? sm.T : sm.A)[(tid / NG) * DK + 4 * (tid % NG)]) = sum;
         if (tid < 64) sm.beta[tid] = beta;
     }
     // with decoupled gates: the raw Q tile in P to fp32 in Q (rows past the chunk's end are zero,
@@ -441,28 +498,62 @@ struct KdaPrepStage {
     // straight from registers: Kh (E * K * e^gamma with decoupled gates), Qh (not with
     // decoupled gates, whose Q is loaded later), Kd and lam, at element offset widx * 64 * DK +
     // (IMG ? the image offset : row-major). Between a barrier after store and one before gamma
-    // is read.
+    // is read. fp32 operators (IMG false): gamma_last - gamma is summed by itself, from the rows behind, and
+    // the part of it inside the row's block of 16 goes to LDS (suf) in place of gamma.
     template <bool IMG, typename TM>
     __device__ __forceinline__ void finish_scan(KdaPrepSmem<DK>& sm, int tid, TM* khat, TM* qhat, TM* kdec,
-                                                float* lam, long widx) const {
+                                                float* lam, long widx) {
         constexpr int PK = KdaPrepSmem<DK>::PK;
         const int rb = tid / NG, cc = 4 * (tid % NG);
-        f32x4_t pre = {0.f, 0.f, 0.f, 0.f}, last = pre;   // rows above the block; gamma_last
-        for (int b = 0; b < RB; ++b) {
-            if (b == rb) pre = last;
-            last += *reinterpret_cast<const f32x4_t*>(&sm.T[b * DK + cc]);
+        f32x4_t pre = {0.f, 0.f, 0.f, 0.f}, last = pre;   // rows above the thread's; gamma_last
+        f32x4_t rest[NP], behind = pre;                   // fp32: behind each row in its block of 16; behind that block
+        if constexpr (IMG) {
+            for (int b = 0; b < RB; ++b) {
+                if (b == rb) pre = last;
+                last += *reinterpret_cast<const f32x4_t*>(&sm.T[b * DK + cc]);
+            }
+        } else {
+            constexpr int GB = 16 / NP;   // threads down a block of 16 rows
+            f32x4_t head = pre, tail = pre;
+#pragma unroll
+            for (int B = 0; B < 4; ++B) {
+                f32x4_t tot = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < GB; ++j) tot += *reinterpret_cast<const f32x4_t*>(&sm.A[(B * GB + j) * DK + cc]);
+                if (B < rb / GB) pre += tot;
+                if (B > rb / GB) behind += tot;
+                last += tot;
+            }
+#pragma unroll
+            for (int j = 0; j < GB; ++j) {
+                const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sm.A[(rb / GB * GB + j) * DK + cc]);
+                if (j < rb % GB) head += x;
+                if (j > rb % GB) tail += x;
+            }
+            pre += head;
+            rest[NP - 1] = tail;
+#pragma unroll
+            for (int it = NP - 2; it >= 0; --it) rest[it] = rest[it + 1] + g[it + 1];
         }
 #pragma unroll
         for (int it = 0; it < NP; ++it) {
             const int r = NP * rb + it;
-            const f32x4_t gm = g[it] + pre;
-            *reinterpret_cast<f32x4_t*>(&sm.G[r * PK + cc]) = gm;
+            f32x4_t gm, gd;   // gamma, gamma_last - gamma
+            if constexpr (IMG) {
+                gm = g[it] + pre;
+                gd = last - gm;
+                *reinterpret_cast<f32x4_t*>(&sm.G[r * PK + cc]) = gm;
+            } else {
+                gm = pre += g[it];
+                gd = rest[it] + behind;
+                if (r <= 48) *reinterpret_cast<f32x4_t*>(&sm.T[r * PK + cc]) = rest[it];
+            }
             const float4 kv = widen(k[it]);
             const float4 x = DEC ? make_float4(e[it][0] * kv.x, e[it][1] * kv.y, e[it][2] * kv.z, e[it][3] * kv.w)
                                  : widen(q[it]);
             const float4 eg = make_float4(__expf(gm[0]), __expf(gm[1]), __expf(gm[2]), __expf(gm[3]));
-            const float4 ed = make_float4(__expf(last[0] - gm[0]), __expf(last[1] - gm[1]), __expf(last[2] - gm[2]),
-                                          __expf(last[3] - gm[3]));
+            const float4 ed = make_float4(__expf(gd[0]), __expf(gd[1]), __expf(gd[2]), __expf(gd[3]));
+            if constexpr (DEC && !IMG) this->eg[it] = f32x4_t{eg.x, eg.y, eg.z, eg.w};
             const long o = widx * 64 * DK + (IMG ? img_off<DK>(r, cc) : r * DK + cc);
             const float4 xs = make_float4(x.x * eg.x, x.y * eg.y, x.z * eg.z, x.w * eg.w);
             put4(khat + o, DEC ? xs : make_float4(kv.x * eg.x, kv.y * eg.y, kv.z * eg.z, kv.w * eg.w));
@@ -524,19 +615,9 @@ __global__ __launch_bounds__(kKdaPrepThreads) void kda_prepare_kernel(ChunkProbl
         // of one phase are formed there instead of being hoisted out of the unit loop and held
         // (or spilled) through the others.
         __syncthreads();  // the previous unit is done with LDS
-        if constexpr (F32OP && !DEC) {
-            // backward pass: e^g is 0 in fp32 from kMinLogDecay down, and a smaller g would only cost the
-            // differences of gamma behind it their digits
-            if (p.tmat) {
-#pragma unroll
-                for (int it = 0; it < KdaPrepStage<TIn, DK, DEC>::NP; ++it)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) stage.g[it][e] = clamp_log_decay(stage.g[it][e]);
-            }
-        }
-        stage.store(sm, opaque(tid));
+        stage.template store<IMG>(sm, opaque(tid));
         __syncthreads();
-        // gamma (rows past the chunk's end add 0) and Kh, Qh, Kd, lam to the workspace
+        // gamma, or suf (rows past the chunk's end add 0), and Kh, Qh, Kd, lam to the workspace
         stage.template finish_scan<IMG>(sm, opaque(tid), khat, qhat, kdec, p.lam, widx);
         __syncthreads();
         // the next unit's loads, issued past the barrier so that no wave waits there for another
@@ -546,6 +627,17 @@ __global__ __launch_bounds__(kKdaPrepThreads) void kda_prepare_kernel(ChunkProbl
 
         // -- Qh with decoupled gates (Q is loaded after A is formed)
         auto write_qhat = [&]() {
+            if constexpr (!IMG) {   // the rows that the thread scanned
+                using ST = KdaPrepStage<TIn, DK, DEC>;
+                const int t = opaque(tid), cc = 4 * (t % ST::NG);
+#pragma unroll
+                for (int it = 0; it < ST::NP; ++it) {
+                    const int r = ST::NP * (t / ST::NG) + it;
+                    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sm.Q[r * PK + cc]) * stage.eg[it];
+                    put4(qhat + widx * 64 * DK + r * DK + cc, make_float4(x[0], x[1], x[2], x[3]));
+                }
+                return;
+            }
             for (int i = opaque(tid); i < 64 * DK / 4; i += kKdaPrepThreads) {
                 const int r = i / (DK / 4), cc = 4 * (i % (DK / 4));
                 const float4 g = *reinterpret_cast<const float4*>(&sm.G[r * PK + cc]);

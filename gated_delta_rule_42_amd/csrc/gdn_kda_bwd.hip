@@ -23,8 +23,9 @@
 // sequence, forwards for the state entering each chunk and D, backwards for dS' and Y; and one that takes
 // every chunk by itself. All arithmetic is fp32 for both input types (fp32 matrix core, 16x16x4): dg is a reverse cumulative
 // sum of differences, so rounding any product operand to 16 bits would show in it many times over.
-// No e^{-gamma} is formed: a product over rows of different 16-row blocks is factored through gamma at the block
-// boundary between them (both factors at most 1), and a pair inside a block takes its own decay.
+// No e^{-gamma} is formed: a product over rows of different 16-row blocks is factored through the block
+// boundary between them (both factors at most 1), and a pair inside a block takes its own decay. No e^{gamma_r - gamma_i} is
+// formed from the two gammas either: see the decays in the chunk kernel.
 #include "gdn_device.h"
 #include "gdn_internal.h"
 
@@ -575,7 +576,7 @@ __global__ __launch_bounds__(64 * NHF * NCG) void kda_bwd_walk_kernel(KdaBwdProb
 // 395 us for the training shape, of which the matrix cores were busy for 146). D, Y and dO pass through LDS in
 // slices of 32 columns, the next one's loads in flight. Two register layouts of a wave's [64 rows, 16 channels]: the accumulator layout
 // (rows 16 t + 4 lq + m) of the products, and the block layout (lane (lq, l16) has rows 16 lq .. 16 lq + 15 of its
-// channel), in which gamma is scanned, the pairs inside a block are summed and the gradients are formed. An accumulator
+// channel), in which the decays are formed, the pairs inside a block are summed and the gradients are formed. An accumulator
 // goes to the block layout through a private LDS tile.
 //
 // The products over d_v (dO D^T, Y D^T, dO S, Y S, D dS') run on the bf16 matrix core at fp32's accuracy: an fp32 operand
@@ -851,25 +852,35 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     }
     __syncthreads();   // dP and dA are whole; D, Y, dO are dead
 
-    // gamma of the lane's rows, in units of log 2 (2^x is one instruction); a[r] = e^{g_r}, the decay from the row above
-    float a[16];
+    // Decays as products of the tokens' own, a[r] = e^{g_r}, each factor at most 1, so that what passes between two tokens never
+    // depends on the decays outside of them (differences of gamma summed over the chunk cost 2e-4 of dq among tokens
+    // of g = -104, whose sums run into thousands). es holds one of two runs of them within the lane's block, formed anew for
+    // each use (registers): from before the block through row r, or from behind row r through the block's end.
+    float a[16], es[16];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        gm[r] = clamp_log_decay(gm[r]) * 1.44269504f;
-        a[r] = exp2_raw(gm[r]);
-        if (r > 0) gm[r] += gm[r - 1];
-    }
-    {
-        const float t0 = __shfl(gm[15], l16, 64), t1 = __shfl(gm[15], 16 + l16, 64), t2 = __shfl(gm[15], 32 + l16, 64);
-        const float pre = (lq > 0 ? t0 : 0.f) + (lq > 1 ? t1 : 0.f) + (lq > 2 ? t2 : 0.f);
+    for (int r = 0; r < 16; ++r) a[r] = exp2_raw(gm[r] * 1.44269504f);   // 2^x is one instruction
+    auto through = [&]() {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) gm[r] += pre;
-    }
-    float end[4];   // gamma at the last row of each block
+        for (int r = 0; r < 16; ++r) {
+            hold(a[r]);
+            es[r] = r > 0 ? es[r > 0 ? r - 1 : 0] * a[r] : a[r];
+        }
+    };
+    auto behind = [&]() {
+        es[15] = 1.f;
 #pragma unroll
-    for (int B = 0; B < 4; ++B) end[B] = __shfl(gm[15], 16 * B + l16, 64);
+        for (int r = 14; r >= 0; --r) {
+            hold(a[r + 1]);
+            es[r] = es[r + 1] * a[r + 1];
+        }
+    };
+    through();
+    // decays over whole blocks
+    const float t0 = __shfl(es[15], l16, 64), t1 = __shfl(es[15], 16 + l16, 64), t2 = __shfl(es[15], 32 + l16, 64),
+                t3 = __shfl(es[15], 48 + l16, 64);
+    const float above = (lq > 0 ? t0 : 1.f) * (lq > 1 ? t1 : 1.f) * (lq > 2 ? t2 : 1.f);    // the blocks before the lane's
+    const float below = (lq < 3 ? t3 : 1.f) * (lq < 2 ? t2 : 1.f) * (lq < 1 ? t1 : 1.f);    // and behind it
 
-    constexpr float kNone = -1000.f;   // 2^kNone = 0: rows that a product leaves out
     float* turn = sm.turn[wave];
     auto to_block = [&](const f32x4_t (&x)[4], float (&y)[16]) {
         wave_lds_fence();
@@ -881,24 +892,24 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) y[r] = turn[turn_at(16 * lq + r) + l16];
     };
-    const float ref = lq == 0 ? 0.f : lq == 1 ? end[0] : lq == 2 ? end[1] : end[2];   // gamma before the lane's block
-    const float own = gm[15];
     float dq[16], l[16], ar[16], w[16];   // ar: with e^{gamma_last - gamma} (D dS') of the row in it
-    float kx = 0.f;
+    float kx = lq == 0 ? t0 * t1 * t2 * t3 * sds : 0.f;   // summed over the four blocks at the end
+    hold(kx);   // formed here, not there
     to_block(aq, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) dq[r] = exp2_raw(gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) dq[r] = above * es[r] * w[r];
     to_block(ay, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) l[r] = -exp2_raw(gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) l[r] = -(above * es[r]) * w[r];
     to_block(ad, w);
+    behind();
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        ar[r] = exp2_raw(end[3] - gm[r]) * w[r];
+        ar[r] = es[r] * below * w[r];
         kx += k[r] * ar[r];
     }
 
-    // pairs of different blocks. Rows of block I against all rows before it, through gamma at the row before
+    // pairs of different blocks. Rows of block I against all rows before it, through the border before
     // block I: step s takes row s of every block (lane lq its own), blocks I and later as zeros.
 #pragma unroll
     for (int t = 0; t < 4; ++t) aq[t] = ay[t] = ad[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -910,42 +921,47 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
             va[n & 1] = *reinterpret_cast<const f32x4_t*>(&sm.dA[o]);
         };
         read(0);
+        float gap = 0.f;   // the decay over the blocks between the lane's and block I; 0 for the block itself and those behind it
 #pragma unroll
         for (int n = 0; n < 12; ++n) {
             if (n + 1 < 12) read(n + 1);
             pin();
             const int I = 1 + n / 4;
+            if (n % 4 == 0) gap = lq == I - 1 ? 1.f : gap * (I == 2 ? t1 : t2);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int s = 4 * (n % 4) + e;
-                const float kb = k[s] * exp2_raw(lq < I ? end[I - 1] - gm[s] : kNone);
+                const float kb = k[s] * (es[s] * gap);
                 aq[I] = mfma4(vp[n & 1][e], kb, aq[I]);
                 ay[I] = mfma4(va[n & 1][e], kb, ay[I]);
             }
         }
     }
-    // Columns of block J against all rows behind it, through gamma at the block's last row.
+    // Columns of block J against all rows behind it, through the border behind block J.
+    through();
     {
-        f32x4_t vp[2], va[2], bt4[2];   // step n has block J = n / 4, rows 4 (n % 4) .. of every block
+        f32x4_t vp[2], va[2], bt4[2];   // step n has block J = 2 - n / 4, rows 4 (n % 4) .. of every block
         auto read = [&](int n) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int o = tri_at<PC>(16 * lq + 4 * (n % 4) + e, 16 * (n / 4) + l16);
+                const int o = tri_at<PC>(16 * lq + 4 * (n % 4) + e, 16 * (2 - n / 4) + l16);
                 vp[n & 1][e] = sm.dP[o];
                 va[n & 1][e] = sm.dA[o];
             }
             bt4[n & 1] = *reinterpret_cast<const f32x4_t*>(&sm.beta[16 * lq + 4 * (n % 4)]);
         };
         read(0);
+        float gap = 0.f;   // over the blocks between block J and the lane's
 #pragma unroll
         for (int n = 0; n < 12; ++n) {
             if (n + 1 < 12) read(n + 1);
             pin();
-            const int J = n / 4;
+            const int J = 2 - n / 4;
+            if (n % 4 == 0) gap = lq == J + 1 ? 1.f : gap * (J == 1 ? t2 : t1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int s = 4 * (n % 4) + i;
-                const float e = exp2_raw(lq > J ? gm[s] - end[J] : kNone);
+                const float e = es[s] * gap;
                 ad[J] = mfma4(vp[n & 1][i], q[s] * e, ad[J]);
                 ad[J] = mfma4(va[n & 1][i], bt4[n & 1][i] * k[s] * e, ad[J]);
             }
@@ -953,13 +969,14 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     }
     to_block(aq, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) dq[r] += exp2_raw(gm[r] - ref) * w[r];
+    for (int r = 0; r < 16; ++r) dq[r] += es[r] * w[r];
     to_block(ay, w);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) l[r] += exp2_raw(gm[r] - ref) * w[r];
+    for (int r = 0; r < 16; ++r) l[r] += es[r] * w[r];
     to_block(ad, w);
+    behind();
 #pragma unroll
-    for (int r = 0; r < 16; ++r) ar[r] += exp2_raw(own - gm[r]) * w[r];
+    for (int r = 0; r < 16; ++r) ar[r] += es[r] * w[r];
 
     // pairs inside the lane's block: w[i] holds e^{gamma_r - gamma_i}, decayed row by row
     f32x4_t vp[2][4], va[2][4];   // rows r and r + 1 of the lane's diagonal blocks
@@ -1006,7 +1023,6 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
     }
     kx += __shfl_xor(kx, 16, 64);
     kx += __shfl_xor(kx, 32, 64);
-    kx += exp2_raw(end[3]) * sds;
 #pragma unroll
     for (int r = 14; r >= 0; --r) w[r] += w[r + 1];
     const float b1 = __shfl(w[0], 16 + l16, 64), b2 = __shfl(w[0], 32 + l16, 64), b3 = __shfl(w[0], 48 + l16, 64);

@@ -79,3 +79,15 @@ def test_decoupled_decode(dtype):
         eo, es = err(to_np(o), o_ref, dtype), err(to_np(st), S_ref, dtype)
         print(f"[gpu] decoupled_decode step {s} {dtype}: err(o)={eo:.2e} err(state)={es:.2e}", flush=True)
         assert eo <= tol(dtype) and es <= tol(dtype)
+
+
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("rows,g", [(range(0, 40), -104.0), (range(0, 64, 21), -1e4), (range(1, 64, 9), float("-inf"))])
+def test_decoupled_f32_mild_tokens_among_strong_ones(rows, g, dk):
+    """What passes between two tokens depends on the decays between them alone, however large the sum before them is."""
+    w = SY.Workload(99, "dc_strong", H=2, dk=dk, dv=64, dtype="f32", B=1, T=150)
+    x = dc_inputs(SY.make_forward_inputs(w, seed=75, h0=True), 76)
+    x["g"] = -0.02 * torch.rand(x["g"].shape, generator=torch.Generator().manual_seed(77))
+    for r in rows:
+        x["g"][:, r::64] = g
+    check_dc(x)

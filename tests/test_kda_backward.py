@@ -292,3 +292,24 @@ def test_nan_gate_shows(dtype, dk):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1, 0], b[1, 0])
         else:
             assert torch.equal(a[:, :70], b[:, :70]) and torch.equal(a[:, :, 0], b[:, :, 0])
+
+
+STRONG = [   # the tokens of every chunk of 64 that decay strongly, and their log decay; the others' is between -0.02 and 0
+    (range(0, 32), -20.0), (range(0, 48), -60.0), (range(0, 32), -104.0), (range(0, 40), -104.0),   # up to a block border, into a block
+    ([r for r in range(64) if r % 16 < 12], -104.0),           # the first twelve of every block of 16
+    ([r for r in range(64) if not 5 <= r % 16 < 11], -90.0),   # both ends of every block
+    (range(3, 64, 8), -104.0), (range(0, 64, 21), -1e4), (range(1, 64, 9), float("-inf")),   # resets
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,dk,dv", [("f32", 128, 64), ("bf16", 128, 128), ("bf16", 64, 64)])
+@pytest.mark.parametrize("rows,g", STRONG)
+def test_mild_tokens_among_strong_ones(rows, g, dtype, dk, dv):
+    """What passes between two tokens depends on the decays between them alone, however large the sum before them is."""
+    x = make(81, 1, 150, 2, dk, dv, dtype, True, 0.01)
+    gen = torch.Generator().manual_seed(82)
+    x["g"] = -0.02 * torch.rand(x["g"].shape, generator=gen)
+    for r in rows:
+        x["g"][:, r::64] = g
+    check(x, SY.make_cotangents(x, 83))

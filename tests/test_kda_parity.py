@@ -99,3 +99,21 @@ def test_kda_decode(dtype):
         eo, es = err(to_np(o), o_ref, dtype), err(to_np(st), S_ref, dtype)
         print(f"[gpu] kda_decode step {s} {dtype}: err(o)={eo:.2e} err(state)={es:.2e}", flush=True)
         assert eo <= tol(dtype) and es <= tol(dtype)
+
+
+STRONG = [   # the tokens of every chunk of 64 that decay strongly, and their log decay; the others' is between -0.02 and 0
+    (range(0, 48), -60.0), (range(0, 40), -104.0), ([r for r in range(64) if not 5 <= r % 16 < 11], -90.0),
+    (range(0, 64, 21), -1e4), (range(1, 64, 9), float("-inf")),
+]
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 64)])
+@pytest.mark.parametrize("rows,g", STRONG)
+def test_kda_f32_mild_tokens_among_strong_ones(rows, g, dk, dv):
+    """What passes between two tokens depends on the decays between them alone, however large the sum before them is."""
+    w = SY.Workload(99, "kda_strong", H=2, dk=dk, dv=dv, dtype="f32", B=1, T=150)
+    x = SY.channel_gates(SY.make_forward_inputs(w, seed=55, h0=True), 56)
+    x["g"] = -0.02 * torch.rand(x["g"].shape, generator=torch.Generator().manual_seed(57))
+    for r in rows:
+        x["g"][:, r::64] = g
+    check_kda(x)
