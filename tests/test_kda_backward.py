@@ -313,3 +313,45 @@ def test_mild_tokens_among_strong_ones(rows, g, dtype, dk, dv):
     for r in rows:
         x["g"][:, r::64] = g
     check(x, SY.make_cotangents(x, 83))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [16, 31, 48])
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dtype,dk,dv", [(t, dk, dv) for t in ("f32", "bf16") for dk in (64, 128) for dv in (64, 128)])
+def test_part_of_a_chunk_in_every_instance(dtype, dk, dv, grad, T):
+    """Chunks that end at or inside a block of 16 rows, through every instance of the chunk kernel; each of those keeps many sums in
+    registers, and a build that spilled hundreds of them once had the last rows of such a chunk wrong."""
+    if grad == torch.bfloat16 and dtype == "f32":
+        with pytest.raises(gb.GDNError):
+            gb.gdn_kda_chunk_bwd(*(torch.zeros(1, T, 1, d, device="cuda") for d in (dk, dk, dv, dk)), torch.zeros(1, T, 1, device="cuda"),
+                                 torch.zeros(1, T, 1, dv, device="cuda"), grad_dtype=grad)
+        return
+    x = make(91 + T, 1, T, 2, dk, dv, dtype, True, 0.1)
+    cot = SY.make_cotangents(x, 92)
+    check(x, cot)
+    a, b = gpu_bwd(x, cot, grad_dtype=torch.float32), gpu_bwd(x, cot, grad_dtype=grad)
+    assert all(torch.equal(p.to(q.dtype), q) for p, q in zip(a, b))
+
+
+@pytest.mark.gpu
+def test_gradients_match_differences_below_zero_gates():
+    """As test_gradients_match_differences_of_the_forward_pass, along the gates alone, from -0.05 - 0.1 softplus: a step of 1e-2
+    times 0.3 |e|, |e| < 5, stays below zero on both sides. The same bound on the difference."""
+    x = make(57, 1, 130, 1, 64, 64, "f32", True, 0.1)
+    x["g"] = x["g"] - 0.05
+    cot = SY.make_cotangents(x, 58)
+    dg = gpu_bwd(x, cot)[3]
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "g", "beta", "h0")}
+    do, dhT = cot["do"].cuda().double(), cot["dhT"].cuda().double()
+
+    def loss(g):
+        assert float(g.max()) < 0
+        o, hT = gb.gdn_kda_chunk_fwd(d["q"], d["k"], d["v"], g, d["beta"], d["h0"])
+        return float((o.double() * do).sum() + (hT.double() * dhT).sum())
+
+    e = -0.3 * torch.randn(d["g"].shape, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").abs()
+    h = 1e-2
+    along, diff = float((dg.double() * e.double()).sum()), (loss(d["g"] + h * e) - loss(d["g"] - h * e)) / (2 * h)
+    print(along, diff, flush=True)
+    assert abs(along - diff) <= 0.02 * max(10.0, abs(along))

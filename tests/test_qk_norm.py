@@ -353,3 +353,25 @@ def test_gradients_into_any_order_of_rows(tokens, heads, step):
         assert torch.equal(v, w)
         v.fill_(7.0)
         assert (a == 7).all()   # nothing beside the rows was written
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nan_and_infinite_rows_stay_by_themselves(dtype):
+    """A row with a NaN or an infinity spoils itself and, through a sum over rows, the weights' gradients, and nothing else."""
+    x = make(35, 40, 4, 2, 128, dtype, 64, True, 100, fused=False)
+    t = {n: v.cuda() for n, v in x.items()}
+    kw = dict(positions=t["pos"], inv_freq=t["freq"], norm="rms")
+    both = lambda: (*gb.gdn_qk_norm_fwd(t["q"], t["k"], t["qw"], t["kw"], **kw),  # noqa: E731
+                    *gb.gdn_qk_norm_bwd(t["q"], t["k"], t["dq"], t["dk"], t["qw"], t["kw"], **kw))
+    want = both()
+    t["q"][3, 1, 5] = float("nan")
+    t["q"][17, 2, 90] = float("inf")
+    t["dk"][9, 0, 3] = float("nan")
+    got = both()
+    bad_q, bad_k = torch.zeros(40, 4, dtype=torch.bool, device="cuda"), torch.zeros(40, 2, dtype=torch.bool, device="cuda")
+    bad_q[3, 1] = bad_q[17, 2] = bad_k[9, 0] = True
+    assert torch.equal(got[0][~bad_q], want[0][~bad_q]) and torch.equal(got[1], want[1])
+    assert torch.equal(got[2][~bad_q], want[2][~bad_q]) and torch.equal(got[3][~bad_k], want[3][~bad_k])
+    assert torch.isnan(got[0][3, 1]).all() and torch.isnan(got[0][17, 2, 90]) and torch.isnan(got[2][3, 1]).all()
+    assert torch.isnan(got[3][9, 0]).all() and torch.isnan(got[4][5]) and torch.isnan(got[5]).any()

@@ -257,3 +257,72 @@ def test_debug_check_allows_padding(monkeypatch):
     for cu in ([0, 3, 2], [0, 2, 6], [1, 2, 3]):
         with pytest.raises(gb.GDNError):
             gb.gdn_recurrent_fwd(*args, d["states"], slots, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+
+
+UNEVEN = [   # few more tokens than sequences: runs of several tokens on the single-token kernel
+    ([1] * 30 + [9, 0] + [1] * 8, 2, 4, 128, 128, "bf16", False),
+    ([1] * 5 + [4] + [1] * 25 + [2, 1, 3], 1, 3, 64, 128, "f32", True),
+    ([1] * 80 + [17], 2, 2, 128, 64, "f32", False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,H,HV,dk,dv,dtype,channels", UNEVEN)
+@pytest.mark.parametrize("mode", ["last", "every", "padded"])
+def test_single_tokens_beside_a_run(lens, H, HV, dk, dv, dtype, channels, mode):
+    assert sum(lens) + 2 <= len(lens) + len(lens) // 4   # (two rows behind the last sequence)
+    test_against_oracle(lens, H, HV, dk, dv, dtype, channels, mode)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,H,HV,dk,dv,dtype,channels", [
+    (128, 8, 32, 128, 128, "bf16", False), (128, 16, 32, 64, 128, "f32", True),       # four rows per lane group
+    (129, 16, 64, 64, 64, "bf16", True), (130, 16, 64, 128, 64, "f32", False),
+    (33, 8, 32, 128, 128, "f32", True), (70, 4, 32, 64, 64, "bf16", False)])          # two
+def test_many_runs(N, H, HV, dk, dv, dtype, channels):
+    """Batches for which a lane group takes several state rows."""
+    print(f"[gpu] recurrent N={N} H={H} HV={HV} {dk}x{dv} {dtype} channels={channels}", flush=True)
+    lens = [(2, 1, 3, 0, 4)[n % 5] for n in range(N)]
+    x = make(N + dk, lens, H, HV, dk, dv, dtype, channels, N + 2)
+    d = {n: t.cuda() for n, t in x.items()}
+    slots = d["order"][:N].contiguous()
+    args = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    a, b = d["states"].clone(), d["states"].clone()
+    o = gb.gdn_recurrent_fwd(*args, a, slots, d["cu"])
+    check(o, a, *PO.run(*(x[n] for n in ("q", "k", "v", "g", "beta", "states")), slots.cpu(), x["cu"]))
+    own = torch.full((sum(lens),), -1, dtype=torch.int32, device="cuda")   # the last token's state to the sequence's own slot
+    for n in range(N):
+        if lens[n]:
+            own[int(x["cu"][n + 1]) - 1] = slots[n]
+    assert torch.equal(gb.gdn_recurrent_fwd(*args, b, slots, d["cu"], own), o) and torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[1, 1, 1, 1], [5, 20, 3, 2]])
+@pytest.mark.parametrize("channels", [False, True])
+def test_nan_and_infinite_gates(lens, channels):
+    """A gate of -infinity forgets the state; NaN stays with its sequence and head; a padded entry reads nothing."""
+    x = make(14, lens, 2, 4, 128, 128, "f32", channels, 6)
+    cu = x["cu"].tolist()
+    d = {n: t.cuda() for n, t in x.items()}
+    slots = d["order"][:4].contiguous()
+    run = lambda states, sl: gb.gdn_recurrent_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], states, sl, d["cu"])  # noqa: E731
+    s0 = d["states"].clone()
+    want = run(s0, slots)
+    d["g"][cu[0]] = float("-inf")
+    a, b = d["states"].clone(), d["states"].clone()
+    b[slots[0].item()] = 0
+    oa, ob = run(a, slots), run(b, slots)
+    assert torch.equal(oa, ob) and torch.equal(a, b) and torch.isfinite(oa).all()
+    d["v"][cu[1], 1] = float("nan")   # one value head of sequence 1
+    for t in (d["q"], d["k"], d["v"], d["g"], d["beta"]):
+        t[cu[2]:cu[3]] = float("nan")   # all of sequence 2
+    slots[2] = -1
+    c = d["states"].clone()
+    oc = run(c, slots)
+    assert torch.isnan(oc[cu[1]:cu[2], 1]).all() and torch.isnan(c[slots[1].item(), 1]).all()
+    assert (oc[cu[2]:cu[3]] == 0).all()
+    others = [0, 2, 3]
+    assert torch.equal(oc[cu[1]:cu[2]][:, others], want[cu[1]:cu[2]][:, others])
+    assert torch.equal(c[slots[1].item()][others], s0[slots[1].item()][others])
+    assert torch.equal(oc[cu[3]:], want[cu[3]:]) and torch.equal(oc[:cu[1]], oa[:cu[1]])
