@@ -226,7 +226,7 @@ __device__ __forceinline__ void gram_rows_of(const KdaPrepSmem<DK>& sm, const fl
         // fp32 products: lane (l16, lq) takes channels 16 u + 4 lq + e, e = 0..3, in product (u, e),
         // so its operands arrive as 16-byte reads
         constexpr int J0 = 0;
-        // (two iterations at a time: with all four unrolled stage 1 of the backward pass took 122 us at B4 H16 T2048 d128, so 110)
+        // (two iterations at a time: with all four unrolled the backward pass takes 680 us at B4 H16 T2048 d128, so 673)
 #pragma unroll 2
         for (int u = HF * DK / 32; u < (HF + 1) * DK / 32; ++u) {
             const int c = 16 * u + 4 * lq;

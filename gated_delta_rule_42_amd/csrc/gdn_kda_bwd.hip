@@ -1004,7 +1004,9 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grad_kernel(KdaBwdProblem b) {
             l[r] += p2 * ke;
             ar[i] += (p1 * q[r] + p2 * bk) * w[i];
         }
-        // the row's sums are formed here, not at their use at the end
+        // The row's sums are formed here, not at their use at the end. Without this the compiler moved all of them there and
+        // spilled some 800 registers, and that build had the sums of rows 14 and 15 wrong for a chunk of 16 tokens, the same on
+        // every run, for a reason that was not found.
         hold(dq[r]);
         hold(l[r]);
 #pragma unroll
@@ -1076,13 +1078,13 @@ KdaBwdLayout kda_bwd_workspace_layout(int B, int T, int H, int dk, int dv, int N
 // 64 columns (4 x 2 waves) in about 10, moving half the operators per column, those of 16 (1 x 4 waves) in about 5, moving
 // twice as many. The narrower ones win as long as all of them run at once. The whole pass, dk = dv = 128, bf16:
 //   pairs x chunks   16 columns   32    64
-//    4 x 64             323      398
-//   16 x 64             488      553   757
-//   18 x 64             665      578
-//   32 x 32                      410   495
-//   64 x 32                      753   715
+//    4 x 64             322      398   596
+//   16 x 64             470      542   740
+//   18 x 64             659      570   768
+//   32 x 32             454      381   476
+//   64 x 32             910      714   667
 // Packed sequences mostly differ in length, so the longest one's time counts up to twice as many of 32 columns (64 pairs,
-// 64 .. 1600 tokens: 300 us, with 64 columns 370); those of 16 keep their limit (16 pairs: 199 us against 225, 32: 242, 230).
+// 331 .. 1345 tokens: 393 us, with 64 columns 406); those of 16 keep their limit (16 pairs: 157 us against 183, 32: 245, 231).
 constexpr long kShortWalks = 128, kNarrowWalks = 256;
 
 template <typename TIn, int DK, int DV>

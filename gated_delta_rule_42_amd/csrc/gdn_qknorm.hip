@@ -53,7 +53,8 @@ template <> struct Raw8<uint16_t> {
         }
     }
 };
-// NT: past the caches, for outputs larger than the L2 (the 32768-token call above: 57 us against 61).
+// NT: past the caches, in the calls of many rows (NP = 4), whose outputs mostly exceed the L2 (the 32768-token call above: 57 us
+// against 61). The rule counts rows, not bytes: very short rows go past the caches too.
 template <bool NT, typename T>
 __device__ __forceinline__ void store_piece(void* p, const T& x) {
     if constexpr (NT) __builtin_nontemporal_store(x, static_cast<T*>(p));

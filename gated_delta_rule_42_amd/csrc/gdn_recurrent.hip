@@ -211,6 +211,11 @@ static hipError_t recurrent_gate(const RecurrentProblem& p, hipStream_t s) {
 // there are enough of them; more rows then share a token's operands. Work-groups of one row per group: 1,024 (4 runs of 16
 // tokens, 32 heads) 10.0 us with one row, 10.8 with two; 16,384 (64 runs of 8) 69 with one, 65 with two, 68 with four;
 // 65,536 (256 runs of 4, channel-wise) 237, 210, 190.
+// Whether there are runs is judged by the call's average, more than 1.25 tokens a sequence, since the host does not see
+// the lengths. In mixed calls that costs something on either side of the border. 255 single tokens beside one run of
+// 64, 32 heads of 128 x 128: 197 us on the single-token kernel (the single tokens alone 166, the run alone 18), and with
+// 66, on the other one, 228; 4 heads: 42 and 44 (23 and 18). Rows behind the last sequence count as tokens: 256 single tokens
+// with 256 such rows 191.
 template <typename TS, typename TO, int DK, int DV>
 static hipError_t recurrent_rows(const RecurrentProblem& p, hipStream_t s) {
     const bool runs = p.T > p.N + p.N / 4;

@@ -336,12 +336,14 @@ int gdn_kda_chunk_fwd(const void *q, const void *k, const void *v, const float *
  *               gdn_kda_chunk_fwd_workspace_bytes for fp32 inputs (T = (I + A)^{-1} in place of Mmat; of T
  *               and P only the lower 16x16 tiles are written), then fp32 the states entering each
  *               chunk [nc, H, dv, dk], the gradients reaching the state behind each chunk (same),
- *               Delta [nc, H, 64, dv] and T^T dDelta (same)
+ *               Delta [nc, H, 64, dv] and T^T dDelta (same). With dk = dv = 128 that is 328,192 bytes per chunk and
+ *               head: 0.67 GB at B4 H16 T2048, 2.69 GB at B1 H16 T32768
  * and N * H < 2^21, nc * H < 2^23. All arithmetic is to fp32's accuracy for both input types (products on the
  * fp32 matrix core, or on the bf16 one with operands split into three bf16 parts), whatever decays stand before and
- * behind a token; g of -infinity resets a state (gdn_kda_chunk_fwd takes a finite one for bf16 inputs). bf16 gradients are the fp32 results rounded to nearest even. A NaN
- * or an infinity in any other operand makes gradients of its sequence and head NaN. dg and dbeta of a token depend on its own
- * sequence only; rows of the outputs that no sequence covers are not written.
+ * behind a token; g of -infinity resets a state (gdn_kda_chunk_fwd takes a finite one for bf16 inputs). bf16
+ * gradients are the fp32 results rounded to nearest even. A NaN or an infinity in any other operand makes gradients
+ * of its sequence and head NaN. dg and dbeta of a token depend on its own sequence only; rows of the outputs that no
+ * sequence covers are not written.
  */
 size_t gdn_kda_chunk_bwd_workspace_bytes(int B, int T, int H, int dk, int dv, int N, int varlen,
                                          int chunk, int dtype);
@@ -391,7 +393,10 @@ int gdn_decoupled_decode_step(const void *q, const void *k, const void *v, const
  * pool, token by token (the recurrence at the top of this file; with channel_gate the
  * channel-wise decay of gdn_kda_chunk_fwd). One call takes a batch of single new tokens, of draft
  * tokens to be verified, or of short prompts, in any mix of lengths; for prompts of some
- * hundred tokens and more the chunked entry points are faster.
+ * hundred tokens and more the chunked entry points are faster. The lengths are known on the
+ * device only, so the kernel is chosen from T / N: a call of many single tokens beside a few
+ * longer runs can take longer than two calls, one of each kind, and rows behind the last
+ * sequence count as tokens.
  *
  *   q, k        [T, H, dk]  dtype; token t starts at element t * q_stride (k_stride), its heads
  *               follow each other densely
