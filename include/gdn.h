@@ -341,9 +341,9 @@ int gdn_kda_chunk_fwd(const void *q, const void *k, const void *v, const float *
  * and N * H < 2^21, nc * H < 2^23. All arithmetic is to fp32's accuracy for both input types (products on the
  * fp32 matrix core, or on the bf16 one with operands split into three bf16 parts), whatever decays stand before and
  * behind a token; g of -infinity resets a state (gdn_kda_chunk_fwd takes a finite one for bf16 inputs). bf16
- * gradients are the fp32 results rounded to nearest even. A NaN or an infinity in any other operand makes gradients
- * of its sequence and head NaN. dg and dbeta of a token depend on its own sequence only; rows of the outputs that no
- * sequence covers are not written.
+ * gradients are the fp32 results rounded to nearest even. A NaN in any operand, or an infinity in one other than g,
+ * makes gradients of its sequence and head NaN. dg and dbeta of a token depend on its own sequence only; rows of the
+ * outputs that no sequence covers are not written.
  */
 size_t gdn_kda_chunk_bwd_workspace_bytes(int B, int T, int H, int dk, int dv, int N, int varlen,
                                          int chunk, int dtype);
