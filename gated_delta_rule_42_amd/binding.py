@@ -43,6 +43,18 @@ _SIGNATURES = [
     ("gdn_qk_norm_fwd", _I, [_P] * 8 + [_I] * 4 + [_L] * 4 + [_I, _F, _I, _I, _F, _F, _I, _I, _P]),
     ("gdn_qk_norm_bwd_workspace_bytes", _SZ, [_I] * 4),
     ("gdn_qk_norm_bwd", _I, [_P] * 12 + [_I] * 4 + [_L] * 8 + [_I, _F, _I, _I, _F, _F, _I, _I, _P, _SZ, _P]),
+    ("gdn_layer_norm_fwd", _I, [_P] * 6 + [_I] * 2 + [_L] * 2 + [_F] + [_I] * 3 + [_P]),
+    ("gdn_layer_norm_bwd_workspace_bytes", _SZ, [_I] * 2),
+    ("gdn_layer_norm_bwd", _I, [_P] * 7 + [_I] * 2 + [_L, _F] + [_I] * 2 + [_P, _SZ, _P]),
+    ("gdn_conv_fwd", _I, [_P] * 7 + [_I] * 5 + [_L] + [_I] * 2 + [_P]),
+    ("gdn_conv_bwd_workspace_bytes", _SZ, [_I] * 4),
+    ("gdn_conv_bwd", _I, [_P] * 11 + [_I] * 5 + [_L] * 2 + [_I] * 2 + [_P, _SZ, _P]),
+    ("gdn_conv_update", _I, [_P] * 8 + [_I] * 5 + [_L] + [_I] * 2 + [_P]),
+    ("gdn_scan_carry_rows", _L, [_I] * 4),
+    ("gdn_scan_workspace_bytes", _SZ, [_I] * 5),
+    ("gdn_scan_fwd", _I, [_P] * 7 + [_I] * 4 + [_L] + [_I] * 3 + [_P, _SZ, _P]),
+    ("gdn_scan_bwd", _I, [_P] * 9 + [_I] * 4 + [_L] + [_I] * 3 + [_P, _SZ, _P]),
+    ("gdn_scan_update", _I, [_P] * 7 + [_I] * 4 + [_L] + [_I] * 3 + [_P]),
 ]
 
 _lib = None
@@ -639,3 +651,286 @@ def gdn_kda_chunk_bwd(q, k, v, g, beta, do, h0=None, dhT=None, cu_seqlens=None, 
           dv, N, _DTYPE.get(q.dtype, -1), _DTYPE.get(gd, -1), _adr(workspace),
           workspace.numel() * workspace.element_size() if workspace is not None else 0)
     return dq, dk_, dv_, dg, db, dh0
+
+
+def _rows_of(t, name):
+    """Stride between the rows of t [..., d] with contiguous channels."""
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"gdn: the last dimension of {name} must be contiguous")
+    if len(shape) == 2:
+        return strides[0] if shape[0] > 1 else 0
+    return _token_stride(t, name, 1) if t.numel() else 0
+
+
+def _bytes(workspace):
+    return workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def gdn_layer_norm_fwd(x, weight=None, bias=None, *, residual=None, eps=1e-5, out_dtype=None, y=None, sum_out=None, stream=None):
+    """Layer norm of the rows of x [..., d] (fp32 or bf16; rows may be strided), after adding residual [...,d] (the dtype of x, or fp32)
+    where given. weight, bias [d] fp32 or None (ones, zeros). Returns y (dense, out_dtype, default the dtype of x) and
+    the sum as it was normalised (dense, the residual's dtype; None without a residual)."""
+    shape, dtype = x.shape, x.dtype
+    if len(shape) < 1 or dtype not in _IN:
+        raise ValueError(f"gdn: x must be [..., d] float32 or bfloat16, got {tuple(shape)} {dtype}")
+    d = shape[-1]
+    _expect(weight, "weight", (d,), _F32)
+    _expect(bias, "bias", (d,), _F32)
+    _expect(residual, "residual", shape, (dtype, torch.float32))
+    _expect(y, "y", shape, _IN)
+    if residual is None and sum_out is not None:
+        raise ValueError("gdn: sum_out needs a residual")
+    dev = x.device
+    if residual is not None:
+        _expect(sum_out, "sum_out", shape, (residual.dtype,))
+        _same_gpu(dev, residual=residual)
+    _dense_on(dev, weight=weight, bias=bias, y=y, sum_out=sum_out)
+    rows = x.numel() // d if d else 0
+    xs = _rows_of(x, "x")
+    rs = _rows_of(residual, "residual") if residual is not None else 0
+    if y is None:
+        y = _new(shape, out_dtype or dtype, dev, stream)
+    if residual is not None and sum_out is None:
+        sum_out = _new(shape, residual.dtype, dev, stream)
+    _call("gdn_layer_norm_fwd", dev, stream, _adr(x), _adr(residual), _adr(weight), _adr(bias), _adr(y), _adr(sum_out), rows, d,
+          xs, rs, eps, _DTYPE[dtype], -1 if residual is None else _DTYPE[residual.dtype], _DTYPE.get(y.dtype, -1))
+    return y, sum_out
+
+
+def gdn_layer_norm_bwd_workspace_bytes(rows, d) -> int:
+    return lib().gdn_layer_norm_bwd_workspace_bytes(rows, d)
+
+
+def gdn_layer_norm_bwd(s, dy, weight=None, *, ds=None, eps=1e-5, need_dw=None, dx=None, workspace=None, stream=None):
+    """Backward pass of gdn_layer_norm_fwd: s [..., d] is what was normalised (its sum, or its x without a residual), dy the gradient of y
+    (dense, fp32 or bf16), ds the gradient that reaches the sum elsewhere (dense, the dtype of s) or None. Returns dx (dense, the
+    dtype of s), the gradient of x and residual alike, and the gradients of weight and bias (fp32 [d], None unless need_dw;
+    default: where a weight is given)."""
+    shape, dtype = s.shape, s.dtype
+    if len(shape) < 1 or dtype not in _IN:
+        raise ValueError(f"gdn: s must be [..., d] float32 or bfloat16, got {tuple(shape)} {dtype}")
+    d = shape[-1]
+    _expect(dy, "dy", shape, _IN)
+    _expect(weight, "weight", (d,), _F32)
+    _expect(ds, "ds", shape, (dtype,))
+    _expect(dx, "dx", shape, (dtype,))
+    dev = s.device
+    _dense_on(dev, dy=dy, weight=weight, ds=ds, dx=dx, workspace=workspace)
+    rows = s.numel() // d if d else 0
+    xs = _rows_of(s, "s")
+    if dx is None:
+        dx = _new(shape, dtype, dev, stream)
+    dw = db = None
+    if need_dw or (need_dw is None and weight is not None):
+        dw, db = _new((d,), torch.float32, dev, stream), _new((d,), torch.float32, dev, stream)
+        need = gdn_layer_norm_bwd_workspace_bytes(rows, d)
+        if workspace is None and need:
+            workspace = _new((need,), torch.uint8, dev, stream)
+    _call("gdn_layer_norm_bwd", dev, stream, _adr(s), _adr(dy), _adr(ds), _adr(weight), _adr(dx), _adr(dw), _adr(db), rows, d, xs, eps,
+          _DTYPE[dtype], _DTYPE[dy.dtype], _adr(workspace), _bytes(workspace))
+    return dx, dw, db
+
+
+_ACT = {None: 0, "silu": 1}
+
+
+def _check_sequences(x, cu_seqlens):
+    """Sizes of x [B, T, D] and its sequences."""
+    if x.dim() != 3 or x.dtype not in _IN:
+        raise ValueError(f"gdn: x must be [B, T, D] float32 or bfloat16, got {tuple(x.shape)} {x.dtype}")
+    B, T, D = x.shape
+    if cu_seqlens is None:
+        return B, T, D, B
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.dtype != torch.int32:
+        raise ValueError("gdn: cu_seqlens must be a 1-D int32 tensor of N + 1 >= 2 offsets")
+    return B, T, D, cu_seqlens.numel() - 1
+
+
+def _check_conv(x, weight, bias, activation):
+    if activation not in _ACT:
+        raise ValueError(f"gdn: activation must be None or 'silu', got {activation!r}")
+    if weight.dim() != 2:
+        raise ValueError(f"gdn: weight must be [D, width], got shape {tuple(weight.shape)}")
+    D, W = x.shape[-1], weight.shape[1]
+    _expect(weight, "weight", (D, W), _F32)
+    _expect(bias, "bias", (D,), _F32)
+    return W
+
+
+def gdn_conv_fwd(x, weight, bias=None, window0=None, cu_seqlens=None, *, activation=None, y=None, windowT=None,
+                 output_final_window=True, stream=None):
+    """Causal convolution per channel over x [B, T, D] (fp32 or bf16; tokens may be strided) with weight [D, W] fp32, W in 2 .. 4
+    (weight[:, -1] meets the token itself), bias [D] fp32 or None, then activation None or "silu". window0 [N, W-1, D] (the dtype
+    of x): the inputs before each sequence, or None (zeros). cu_seqlens int32 [N+1]: packed sequences (B = 1).
+    Returns y [B, T, D] (dense; rows that no sequence covers are not written) and the windows behind the sequences [N, W-1, D] (None
+    unless output_final_window)."""
+    B, T, D, N = _check_sequences(x, cu_seqlens)
+    W = _check_conv(x, weight, bias, activation)
+    dtype, dev = x.dtype, x.device
+    _expect(window0, "window0", (N, W - 1, D), (dtype,))
+    _expect(y, "y", x.shape, (dtype,))
+    _expect(windowT, "windowT", (N, W - 1, D), (dtype,))
+    _dense_on(dev, weight=weight, bias=bias, window0=window0, cu_seqlens=cu_seqlens, y=y, windowT=windowT)
+    xs = _rows_of(x, "x")
+    if y is None:
+        y = _new((B, T, D), dtype, dev, stream)
+    if windowT is None and output_final_window:
+        windowT = _new((N, W - 1, D), dtype, dev, stream)
+    _call("gdn_conv_fwd", dev, stream, _adr(x), _adr(weight), _adr(bias), _adr(window0), _adr(cu_seqlens), _adr(y), _adr(windowT),
+          B, T, N, D, W, xs, _ACT[activation], _DTYPE[dtype])
+    return y, windowT
+
+
+def gdn_conv_bwd_workspace_bytes(B, T, D, width) -> int:
+    return lib().gdn_conv_bwd_workspace_bytes(B, T, D, width)
+
+
+def gdn_conv_bwd(x, weight, dy, bias=None, window0=None, dwindowT=None, cu_seqlens=None, *, activation=None, need_dw=True,
+                 need_dwindow0=True, dx=None, workspace=None, stream=None):
+    """Backward pass of gdn_conv_fwd: from dy [B, T, D] (dense) and dwindowT [N, W-1, D] or None, both of the dtype of x, returns dx (that
+    dtype; a given one may have strided tokens, as of a fused gradient), dweight [D, W] fp32 (None unless need_dw), dbias [D] fp32 (None
+    without a bias too) and dwindow0 [N, W-1, D] (None unless need_dwindow0)."""
+    B, T, D, N = _check_sequences(x, cu_seqlens)
+    W = _check_conv(x, weight, bias, activation)
+    dtype, dev = x.dtype, x.device
+    _expect(dy, "dy", x.shape, (dtype,))
+    _expect(window0, "window0", (N, W - 1, D), (dtype,))
+    _expect(dwindowT, "dwindowT", (N, W - 1, D), (dtype,))
+    _expect(dx, "dx", x.shape, (dtype,))
+    _same_gpu(dev, dx=dx)
+    _dense_on(dev, weight=weight, dy=dy, bias=bias, window0=window0, dwindowT=dwindowT, cu_seqlens=cu_seqlens, workspace=workspace)
+    xs = _rows_of(x, "x")
+    if dx is None:
+        dx = _new((B, T, D), dtype, dev, stream)
+    dxs = _rows_of(dx, "dx")
+    dw = db = None
+    if need_dw:
+        dw = _new((D, W), torch.float32, dev, stream)
+        if bias is not None:
+            db = _new((D,), torch.float32, dev, stream)
+        need = gdn_conv_bwd_workspace_bytes(B, T, D, W)
+        if workspace is None and need:
+            workspace = _new((need,), torch.uint8, dev, stream)
+    dwin = _new((N, W - 1, D), dtype, dev, stream) if need_dwindow0 else None
+    _call("gdn_conv_bwd", dev, stream, _adr(x), _adr(weight), _adr(bias), _adr(window0), _adr(dy), _adr(dwindowT), _adr(cu_seqlens),
+          _adr(dx), _adr(dw), _adr(db), _adr(dwin), B, T, N, D, W, xs, dxs, _ACT[activation], _DTYPE[dtype], _adr(workspace),
+          _bytes(workspace))
+    return dx, dw, db, dwin
+
+
+def _check_runs(x, slots, cu_seqlens, out_slots):
+    if x.dim() != 2 or x.dtype not in _IN:
+        raise ValueError(f"gdn: x must be [T, D] float32 or bfloat16, got {tuple(x.shape)} {x.dtype}")
+    T, D = x.shape
+    if slots.dim() != 1 or slots.dtype != torch.int32:
+        raise ValueError("gdn: slots must be a 1-D int32 tensor")
+    N = slots.numel()
+    if cu_seqlens is None and T != N:
+        raise ValueError(f"gdn: {T} tokens for {N} sequences without cu_seqlens")
+    _expect(cu_seqlens, "cu_seqlens", (N + 1,), (torch.int32,))
+    _expect(out_slots, "out_slots", (T,), (torch.int32,))
+    return T, D, N
+
+
+def gdn_conv_update(x, weight, bias, windows, slots, cu_seqlens=None, out_slots=None, y=None, *, activation=None, stream=None):
+    """gdn_conv_fwd for runs of tokens on a pool of windows: x [T, D] (tokens may be strided), windows [n_slots, W-1, D] of the dtype of x,
+    updated in place; slots, cu_seqlens and out_slots as in gdn_recurrent_fwd. Returns y [T, D]; rows that no sequence covers
+    are not written."""
+    T, D, N = _check_runs(x, slots, cu_seqlens, out_slots)
+    W = _check_conv(x, weight, bias, activation)
+    dtype, dev = x.dtype, x.device
+    if windows.dim() != 3:
+        raise ValueError(f"gdn: windows must be [n_slots, width - 1, D], got shape {tuple(windows.shape)}")
+    _expect(windows, "windows", (windows.shape[0], W - 1, D), (dtype,))
+    _expect(y, "y", (T, D), (dtype,))
+    _dense_on(dev, weight=weight, bias=bias, windows=windows, slots=slots, cu_seqlens=cu_seqlens, out_slots=out_slots, y=y)
+    xs = _rows_of(x, "x")
+    if y is None:
+        y = _new((T, D), dtype, dev, stream)
+    _call("gdn_conv_update", dev, stream, _adr(x), _adr(weight), _adr(bias), _adr(windows), _adr(slots), _adr(cu_seqlens),
+          _adr(out_slots), _adr(y), T, N, D, W, windows.shape[0], xs, _ACT[activation], _DTYPE[dtype])
+    return y
+
+
+def gdn_scan_workspace_bytes(B, T, N, D, varlen) -> int:
+    return lib().gdn_scan_workspace_bytes(B, T, N, D, int(bool(varlen)))
+
+
+def gdn_scan_carry_rows(B, T, N, varlen) -> int:
+    return lib().gdn_scan_carry_rows(B, T, N, int(bool(varlen)))
+
+
+def gdn_scan_fwd(x, g, h0=None, cu_seqlens=None, *, blend=False, h=None, hT=None, out_dtype=None, output_final_state=True,
+                 keep_carries=False, workspace=None, stream=None):
+    """Gated linear recurrence per channel over x [B, T, D] (fp32 or bf16; tokens may be strided): h_t = a_t h_{t-1} + x_t, or with blend
+    a_t h_{t-1} + (1 - a_t) x_t, a = exp(g), g [B, T, D] fp32 <= 0. h0 [N, D] fp32 or None (zeros); cu_seqlens int32 [N+1]: packed
+    sequences (B = 1). Returns h [B, T, D] (out_dtype, default the dtype of x; rows that no sequence covers are not written), the
+    final states [N, D] fp32 (None unless output_final_state) and, with keep_carries, what gdn_scan_bwd takes of this
+    pass (fp32, a row per 256 tokens), else None."""
+    B, T, D, N = _check_sequences(x, cu_seqlens)
+    dtype, dev = x.dtype, x.device
+    _expect(g, "g", (B, T, D), _F32)
+    _expect(h0, "h0", (N, D), _F32)
+    _expect(h, "h", (B, T, D), _IN)
+    _expect(hT, "hT", (N, D), _F32)
+    _dense_on(dev, g=g, h0=h0, cu_seqlens=cu_seqlens, h=h, hT=hT, workspace=workspace)
+    xs = _rows_of(x, "x")
+    if h is None:
+        h = _new((B, T, D), out_dtype or dtype, dev, stream)
+    if hT is None and output_final_state:
+        hT = _new((N, D), torch.float32, dev, stream)
+    carries = None
+    if keep_carries:
+        carries = _new((gdn_scan_carry_rows(B, T, N, cu_seqlens is not None), D), torch.float32, dev, stream)
+    if workspace is None:
+        need = gdn_scan_workspace_bytes(B, T, N, D, cu_seqlens is not None)
+        if need:
+            workspace = _new((need,), torch.uint8, dev, stream)
+    _call("gdn_scan_fwd", dev, stream, _adr(x), _adr(g), _adr(h0), _adr(cu_seqlens), _adr(h), _adr(hT), _adr(carries), B, T, N, D, xs,
+          int(blend), _DTYPE[dtype], _DTYPE.get(h.dtype, -1), _adr(workspace), _bytes(workspace))
+    return h, hT, carries
+
+
+def gdn_scan_bwd(x, g, dh, carries, dhT=None, cu_seqlens=None, *, blend=False, need_dh0=True, workspace=None, stream=None):
+    """Backward pass of gdn_scan_fwd on the same x, g and cu_seqlens and the carries that it returned: from dh [B, T, D] (dense, the dtype
+    of h) and dhT [N, D] fp32 or None returns dx [B, T, D] (the dtype of x), dg [B, T, D] fp32 and dh0 [N, D] fp32 (None unless
+    need_dh0)."""
+    B, T, D, N = _check_sequences(x, cu_seqlens)
+    dtype, dev = x.dtype, x.device
+    _expect(g, "g", (B, T, D), _F32)
+    _expect(dh, "dh", (B, T, D), (dtype, torch.float32))
+    _expect(dhT, "dhT", (N, D), _F32)
+    _expect(carries, "carries", (gdn_scan_carry_rows(B, T, N, cu_seqlens is not None), D), _F32)
+    _dense_on(dev, g=g, dh=dh, carries=carries, dhT=dhT, cu_seqlens=cu_seqlens, workspace=workspace)
+    xs = _rows_of(x, "x")
+    dx = _new((B, T, D), dtype, dev, stream)
+    dg = _new((B, T, D), torch.float32, dev, stream)
+    dh0 = _new((N, D), torch.float32, dev, stream) if need_dh0 else None
+    if workspace is None:
+        need = gdn_scan_workspace_bytes(B, T, N, D, cu_seqlens is not None)
+        if need:
+            workspace = _new((need,), torch.uint8, dev, stream)
+    _call("gdn_scan_bwd", dev, stream, _adr(x), _adr(g), _adr(carries), _adr(dh), _adr(dhT), _adr(cu_seqlens), _adr(dx), _adr(dg),
+          _adr(dh0), B, T, N, D, xs, int(blend), _DTYPE[dtype], _DTYPE[dh.dtype], _adr(workspace), _bytes(workspace))
+    return dx, dg, dh0
+
+
+def gdn_scan_update(x, g, states, slots, cu_seqlens=None, out_slots=None, h=None, *, blend=False, out_dtype=None, stream=None):
+    """gdn_scan_fwd for runs of tokens on a pool of states: x [T, D] (tokens may be strided), g [T, D] fp32, states [n_slots, D] fp32, updated
+    in place; slots, cu_seqlens and out_slots as in gdn_recurrent_fwd. Returns h [T, D] (out_dtype, default the dtype of x); rows
+    that no sequence covers are not written."""
+    T, D, N = _check_runs(x, slots, cu_seqlens, out_slots)
+    dtype, dev = x.dtype, x.device
+    _expect(g, "g", (T, D), _F32)
+    if states.dim() != 2:
+        raise ValueError(f"gdn: states must be [n_slots, D], got shape {tuple(states.shape)}")
+    _expect(states, "states", (states.shape[0], D), _F32)
+    _expect(h, "h", (T, D), _IN)
+    _dense_on(dev, g=g, states=states, slots=slots, cu_seqlens=cu_seqlens, out_slots=out_slots, h=h)
+    xs = _rows_of(x, "x")
+    if h is None:
+        h = _new((T, D), out_dtype or dtype, dev, stream)
+    _call("gdn_scan_update", dev, stream, _adr(x), _adr(g), _adr(states), _adr(slots), _adr(cu_seqlens), _adr(out_slots), _adr(h), T, N,
+          D, states.shape[0], xs, int(blend), _DTYPE[dtype], _DTYPE.get(h.dtype, -1))
+    return h

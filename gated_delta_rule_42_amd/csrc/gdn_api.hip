@@ -2,6 +2,7 @@
 // kernel dispatch. Every check runs before any HIP call, so a rejected call launches
 // nothing and touches no device state.
 #include "gdn.h"
+#include "gdn_block.h"
 #include "gdn_internal.h"
 
 #include <cstdlib>
@@ -646,4 +647,281 @@ GDN_EXPORT int gdn_qk_norm_bwd(const void* q, const void* k, const void* dq_out,
     p.dqw = dq_weight; p.dkw = dk_weight;
     p.partial = static_cast<float*>(workspace);
     return gdn::launch_qk_norm(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+// ------------------------------------------------------------------------------------------ layer norm
+namespace {
+bool dtype_ok(int t) { return t == GDN_F32 || t == GDN_BF16; }
+int per16(int dtype) { return dtype == GDN_BF16 ? 8 : 4; }   // elements of 16 bytes
+
+// Rows of layer norm: a row takes 16 lanes up to 128 channels and at most a lane per 8 channels past that, fewer than 2^32 in all.
+int layer_norm_shape(int rows, int d) {
+    if (d < 8 || d > 16384 || d % 8) return GDN_ERR_UNSUPPORTED;
+    if (rows < 0 || rows >= 1 << 28 || (long long)rows * d >= 1LL << 35) return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+}  // namespace
+
+GDN_EXPORT int gdn_layer_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias, void* y,
+                                  void* sum, int rows, int d, int64_t x_stride, int64_t residual_stride, float eps,
+                                  int dtype, int sum_dtype, int out_dtype, void* stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return GDN_ERR_DTYPE;
+    if (residual && sum_dtype != GDN_F32 && !(sum_dtype == GDN_BF16 && dtype == GDN_BF16)) return GDN_ERR_DTYPE;
+    const int sc = layer_norm_shape(rows, d);
+    if (sc != GDN_OK) return sc;
+    if (!(eps > 0.f) || x_stride < 0 || residual_stride < 0) return GDN_ERR_SHAPE;
+    if (rows > 0 && (!x || !y || (residual && !sum))) return GDN_ERR_NULL;
+    const void* al16[] = {x, residual, weight, bias, y, sum};
+    for (const void* q : al16)
+        if (!aligned(q, 16)) return GDN_ERR_ALIGN;
+    if (x_stride % per16(dtype) || (residual && residual_stride % per16(sum_dtype))) return GDN_ERR_ALIGN;
+    gdn::LayerNormProblem p{};
+    p.x = x; p.residual = residual; p.weight = weight; p.bias = bias; p.y = y; p.sum = sum;
+    p.rows = rows; p.d = d; p.x_row = x_stride; p.r_row = residual_stride; p.eps = eps;
+    p.x_bf16 = dtype == GDN_BF16;
+    p.s_bf16 = residual ? sum_dtype == GDN_BF16 : p.x_bf16;
+    p.y_bf16 = out_dtype == GDN_BF16;
+    return gdn::launch_layer_norm_fwd(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+GDN_EXPORT size_t gdn_layer_norm_bwd_workspace_bytes(int rows, int d) {
+    if (layer_norm_shape(rows, d) != GDN_OK) return 0;
+    return (size_t)gdn::layer_norm_parts(rows, d) * 2 * d * sizeof(float);
+}
+
+GDN_EXPORT int gdn_layer_norm_bwd(const void* sum, const void* dy, const void* dsum, const float* weight, void* dx,
+                                  float* dweight, float* dbias, int rows, int d, int64_t sum_stride, float eps,
+                                  int dtype, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return GDN_ERR_DTYPE;
+    const int sc = layer_norm_shape(rows, d);
+    if (sc != GDN_OK) return sc;
+    if (!(eps > 0.f) || sum_stride < 0) return GDN_ERR_SHAPE;
+    if (rows > 0 && (!sum || !dy || !dx)) return GDN_ERR_NULL;
+    const void* al16[] = {sum, dy, dsum, weight, dx};
+    for (const void* q : al16)
+        if (!aligned(q, 16)) return GDN_ERR_ALIGN;
+    if (sum_stride % per16(dtype)) return GDN_ERR_ALIGN;
+    if (!aligned(dweight, 4) || !aligned(dbias, 4)) return GDN_ERR_ALIGN;
+    if (dweight || dbias) {
+        const size_t need = gdn_layer_norm_bwd_workspace_bytes(rows, d);
+        if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return GDN_ERR_ALIGN;
+    }
+    gdn::LayerNormProblem p{};
+    p.x = sum; p.dy = dy; p.dsum = dsum; p.weight = weight; p.dx = dx; p.dweight = dweight; p.dbias = dbias;
+    p.partial = static_cast<float*>(workspace);
+    p.rows = rows; p.d = d; p.x_row = sum_stride; p.eps = eps;
+    p.x_bf16 = p.s_bf16 = dtype == GDN_BF16;
+    p.y_bf16 = out_dtype == GDN_BF16;
+    return gdn::launch_layer_norm_bwd(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+// ------------------------------------------------------------------------------------------ convolution, scan
+namespace {
+// Sizes of the operators per channel: B rows of T tokens, or with cu_seqlens N sequences in one row.
+int channel_shape(int B, int T, int N, int D, bool varlen) {
+    if (D < 8 || D % 8 || D > 1 << 20) return GDN_ERR_UNSUPPORTED;
+    if (B < 1 || T < 0 || N < 1 || (varlen ? B != 1 : N != B)) return GDN_ERR_SHAPE;
+    const long long tokens = (long long)B * T;   // < 2^62
+    if (tokens > 1 << 28 || tokens * D > 1LL << 36 || N > 1 << 24 || (long long)N * D > 1LL << 31) return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+// Sizes of runs on a pool; fewer than 2^32 threads of 4 channels in all.
+int pool_shape(int T, int N, int D, int n_slots, bool varlen) {
+    if (D < 8 || D % 8 || D > 1 << 20) return GDN_ERR_UNSUPPORTED;
+    if (T < 0 || N < 0 || n_slots < 0 || (!varlen && T != N)) return GDN_ERR_SHAPE;
+    if (T > 1 << 28 || (long long)T * D > 1LL << 36) return GDN_ERR_SHAPE;
+    if ((long long)N * ((D + 2047) / 2048) >= 1 << 22) return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+int conv_kind(int width, int activation, int dtype) {
+    if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
+    if (width < 2 || width > 4 || (activation != GDN_ACT_NONE && activation != GDN_ACT_SILU)) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+template <size_t N16, size_t N4>
+bool all_aligned(const void* const (&p16)[N16], const void* const (&p4)[N4]) {
+    for (const void* p : p16)
+        if (!aligned(p, 16)) return false;
+    for (const void* p : p4)
+        if (!aligned(p, 4)) return false;
+    return true;
+}
+}  // namespace
+
+GDN_EXPORT int gdn_conv_fwd(const void* x, const float* weight, const float* bias, const void* window0,
+                            const int32_t* cu_seqlens, void* y, void* windowT, int B, int T, int N, int D, int width,
+                            int64_t x_stride, int activation, int dtype, void* stream) {
+    int st = conv_kind(width, activation, dtype);
+    if (st == GDN_OK) st = channel_shape(B, T, N, D, cu_seqlens != nullptr);
+    if (st != GDN_OK) return st;
+    if (x_stride < 0) return GDN_ERR_SHAPE;
+    const int tokens = B * T;
+    if ((tokens > 0 && (!x || !y)) || !weight) return GDN_ERR_NULL;
+    if (!all_aligned({x, weight, window0, y, windowT}, {bias, cu_seqlens}) || x_stride % per16(dtype)) return GDN_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_offsets(cu_seqlens, N, T, s, true);
+    if (st != GDN_OK) return st;
+    gdn::ConvProblem p{};
+    p.x = x; p.weight = weight; p.bias = bias; p.window0 = window0; p.cu_seqlens = cu_seqlens; p.y = y; p.windowT = windowT;
+    p.x_row = x_stride; p.tokens = tokens; p.T = T; p.N = N; p.D = D; p.W = width;
+    p.bf16 = dtype == GDN_BF16; p.silu = activation == GDN_ACT_SILU;
+    return gdn::launch_conv_fwd(p, s) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+GDN_EXPORT size_t gdn_conv_bwd_workspace_bytes(int B, int T, int D, int width) {
+    if (width < 2 || width > 4 || channel_shape(B, T, B, D, false) != GDN_OK) return 0;
+    return (size_t)gdn::conv_parts(B * T, D) * D * (width + 1) * sizeof(float);
+}
+
+GDN_EXPORT int gdn_conv_bwd(const void* x, const float* weight, const float* bias, const void* window0, const void* dy,
+                            const void* dwindowT, const int32_t* cu_seqlens, void* dx, float* dweight, float* dbias,
+                            void* dwindow0, int B, int T, int N, int D, int width, int64_t x_stride, int64_t dx_stride,
+                            int activation, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = conv_kind(width, activation, dtype);
+    if (st == GDN_OK) st = channel_shape(B, T, N, D, cu_seqlens != nullptr);
+    if (st != GDN_OK) return st;
+    const int tokens = B * T;
+    // rows of dx must not lie over each other
+    if (x_stride < 0 || dx_stride < 0 || (tokens > 1 && dx_stride < D)) return GDN_ERR_SHAPE;
+    if ((tokens > 0 && (!x || !dy || !dx)) || !weight) return GDN_ERR_NULL;
+    if (!all_aligned({x, weight, window0, dy, dwindowT, dx, dwindow0}, {bias, cu_seqlens, dweight, dbias}) ||
+        x_stride % per16(dtype) || dx_stride % per16(dtype))
+        return GDN_ERR_ALIGN;
+    if (dweight || dbias) {
+        const size_t need = gdn_conv_bwd_workspace_bytes(B, T, D, width);
+        if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return GDN_ERR_ALIGN;
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_offsets(cu_seqlens, N, T, s, true);
+    if (st != GDN_OK) return st;
+    gdn::ConvProblem p{};
+    p.x = x; p.weight = weight; p.bias = bias; p.window0 = window0; p.cu_seqlens = cu_seqlens;
+    p.dy = dy; p.dwindowT = dwindowT; p.dx = dx; p.dweight = dweight; p.dbias = dbias; p.dwindow0 = dwindow0;
+    p.partial = static_cast<float*>(workspace);
+    p.x_row = x_stride; p.dx_row = dx_stride; p.tokens = tokens; p.T = T; p.N = N; p.D = D; p.W = width;
+    p.bf16 = dtype == GDN_BF16; p.silu = activation == GDN_ACT_SILU;
+    return gdn::launch_conv_bwd(p, s) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+GDN_EXPORT int gdn_conv_update(const void* x, const float* weight, const float* bias, void* windows, const int32_t* slots,
+                               const int32_t* cu_seqlens, const int32_t* out_slots, void* y, int T, int N, int D, int width,
+                               int n_slots, int64_t x_stride, int activation, int dtype, void* stream) {
+    int st = conv_kind(width, activation, dtype);
+    if (st == GDN_OK) st = pool_shape(T, N, D, n_slots, cu_seqlens != nullptr);
+    if (st != GDN_OK) return st;
+    if (x_stride < 0) return GDN_ERR_SHAPE;
+    if (T == 0 || N == 0) return GDN_OK;   // no token: nothing to read or write
+    if (!x || !weight || !slots || !y || (!windows && n_slots > 0)) return GDN_ERR_NULL;
+    if (!all_aligned({x, weight, windows, y}, {bias, slots, cu_seqlens, out_slots}) || x_stride % per16(dtype))
+        return GDN_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_offsets(cu_seqlens, N, T, s, true);
+    if (st != GDN_OK) return st;
+    gdn::ConvProblem p{};
+    p.x = x; p.weight = weight; p.bias = bias; p.pool = windows; p.slots = slots; p.cu_seqlens = cu_seqlens;
+    p.out_slots = out_slots; p.y = y; p.x_row = x_stride; p.tokens = T; p.T = T; p.N = N; p.D = D; p.W = width;
+    p.n_slots = n_slots; p.bf16 = dtype == GDN_BF16; p.silu = activation == GDN_ACT_SILU;
+    return gdn::launch_conv_update(p, s) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+namespace {
+int scan_shape(int B, int T, int N, int D, bool varlen) {
+    const int st = channel_shape(B, T, N, D, varlen);
+    if (st != GDN_OK) return st;
+    const gdn::ScanLayout w = gdn::scan_layout(B * T, T, N, D, varlen);
+    // at most 512 threads per tile of 64 channels, fewer than 2^32 in all
+    if (w.rows * ((D + gdn::kScanChannels - 1) / gdn::kScanChannels) >= 1 << 23) return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+// Checks shared by both directions of the scan; fills the shared part of the problem.
+int check_scan(const void* x, const float* g, const int32_t* cu, int B, int T, int N, int D, int64_t x_stride, int blend,
+               int dtype, int h_dtype, void* ws, size_t ws_bytes, gdn::ScanProblem* p) {
+    if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
+    if (h_dtype != GDN_F32 && !(h_dtype == GDN_BF16 && dtype == GDN_BF16)) return GDN_ERR_DTYPE;
+    const int st = scan_shape(B, T, N, D, cu != nullptr);
+    if (st != GDN_OK) return st;
+    if (x_stride < 0) return GDN_ERR_SHAPE;
+    const int tokens = B * T;
+    if (tokens > 0 && (!x || !g)) return GDN_ERR_NULL;
+    if (!all_aligned({x, g}, {cu}) || x_stride % per16(dtype)) return GDN_ERR_ALIGN;
+    const gdn::ScanLayout w = gdn::scan_layout(tokens, T, N, D, cu != nullptr);
+    if (w.total > 0 && (!ws || ws_bytes < w.total)) return GDN_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return GDN_ERR_ALIGN;
+    gdn::ScanProblem& P = *p;
+    P.x = x; P.g = g; P.cu_seqlens = cu; P.x_row = x_stride; P.rows = w.rows;
+    P.tokens = tokens; P.T = T; P.N = N; P.D = D; P.ncb = (D + gdn::kScanChannels - 1) / gdn::kScanChannels;
+    P.bf16 = dtype == GDN_BF16; P.h_bf16 = h_dtype == GDN_BF16; P.blend = blend != 0;
+    if (w.total > 0) {
+        char* b = static_cast<char*>(ws);
+        P.ticket = reinterpret_cast<int32_t*>(b);
+        P.base = cu ? reinterpret_cast<int32_t*>(b + w.off_base) : nullptr;
+        P.agg = reinterpret_cast<uint64_t*>(b + w.off_agg);
+        P.pref = reinterpret_cast<float*>(b + w.off_pref);
+    }
+    return GDN_OK;
+}
+}  // namespace
+
+GDN_EXPORT int64_t gdn_scan_carry_rows(int B, int T, int N, int varlen) {
+    if (channel_shape(B, T, N, 8, varlen != 0) != GDN_OK) return 0;
+    return gdn::scan_layout(B * T, T, N, 8, varlen != 0).rows;
+}
+
+GDN_EXPORT size_t gdn_scan_workspace_bytes(int B, int T, int N, int D, int varlen) {
+    if (scan_shape(B, T, N, D, varlen != 0) != GDN_OK) return 0;
+    return gdn::scan_layout(B * T, T, N, D, varlen != 0).total;
+}
+
+GDN_EXPORT int gdn_scan_fwd(const void* x, const float* g, const float* h0, const int32_t* cu_seqlens, void* h, float* hT,
+                            float* carries, int B, int T, int N, int D, int64_t x_stride, int blend, int dtype, int h_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    gdn::ScanProblem p{};
+    int st = check_scan(x, g, cu_seqlens, B, T, N, D, x_stride, blend, dtype, h_dtype, workspace, workspace_bytes, &p);
+    if (st != GDN_OK) return st;
+    if (p.tokens > 0 && !h) return GDN_ERR_NULL;
+    if (!all_aligned({h, hT}, {h0, carries})) return GDN_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_offsets(cu_seqlens, N, T, s, true);
+    if (st != GDN_OK) return st;
+    p.h0 = h0; p.h = h; p.hT = hT; p.carries = carries;
+    return gdn::launch_scan_fwd(p, s) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+GDN_EXPORT int gdn_scan_bwd(const void* x, const float* g, const float* carries, const void* dh, const float* dhT,
+                            const int32_t* cu_seqlens, void* dx, float* dg, float* dh0, int B, int T, int N, int D,
+                            int64_t x_stride, int blend, int dtype, int h_dtype, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    gdn::ScanProblem p{};
+    int st = check_scan(x, g, cu_seqlens, B, T, N, D, x_stride, blend, dtype, h_dtype, workspace, workspace_bytes, &p);
+    if (st != GDN_OK) return st;
+    if ((p.tokens > 0 && (!dh || !dx || !dg)) || !carries) return GDN_ERR_NULL;
+    if (!all_aligned({dh, dx, dg, dh0}, {carries, dhT})) return GDN_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_offsets(cu_seqlens, N, T, s, true);
+    if (st != GDN_OK) return st;
+    p.carries = const_cast<float*>(carries); p.dh = dh; p.dhT = dhT; p.dx = dx; p.dg = dg; p.dh0 = dh0;
+    return gdn::launch_scan_bwd(p, s) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+GDN_EXPORT int gdn_scan_update(const void* x, const float* g, float* states, const int32_t* slots, const int32_t* cu_seqlens,
+                               const int32_t* out_slots, void* h, int T, int N, int D, int n_slots, int64_t x_stride,
+                               int blend, int dtype, int h_dtype, void* stream) {
+    if (!dtype_ok(dtype)) return GDN_ERR_DTYPE;
+    if (h_dtype != GDN_F32 && !(h_dtype == GDN_BF16 && dtype == GDN_BF16)) return GDN_ERR_DTYPE;
+    int st = pool_shape(T, N, D, n_slots, cu_seqlens != nullptr);
+    if (st != GDN_OK) return st;
+    if (x_stride < 0) return GDN_ERR_SHAPE;
+    if (T == 0 || N == 0) return GDN_OK;   // no token: nothing to read or write
+    if (!x || !g || !slots || !h || (!states && n_slots > 0)) return GDN_ERR_NULL;
+    if (!all_aligned({x, g, states, h}, {slots, cu_seqlens, out_slots}) || x_stride % per16(dtype)) return GDN_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = debug_check_offsets(cu_seqlens, N, T, s, true);
+    if (st != GDN_OK) return st;
+    gdn::ScanProblem p{};
+    p.x = x; p.g = g; p.pool = states; p.slots = slots; p.cu_seqlens = cu_seqlens; p.out_slots = out_slots; p.h = h;
+    p.x_row = x_stride; p.tokens = T; p.T = T; p.N = N; p.D = D; p.n_slots = n_slots;
+    p.bf16 = dtype == GDN_BF16; p.h_bf16 = h_dtype == GDN_BF16; p.blend = blend != 0;
+    return gdn::launch_scan_update(p, s) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }

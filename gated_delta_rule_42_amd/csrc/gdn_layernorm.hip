@@ -1,0 +1,360 @@
+// Layer norm with the residual sum in the same pass, and its gradients, for gfx950.
+//
+// Per row of d channels:
+//     s = x + r, rounded to the sum's type (or x alone),   m = sum s / d,   v = sum (s - m)^2 / d,
+//     xh = (s - m) (v + eps)^(-1/2),   y = w xh + b.
+// Backward, with g = w dy and rs = (v + eps)^(-1/2):
+//     dx = rs (g - sum g / d - xh sum(g xh) / d) + ds,   dw = sum over rows of dy xh,   db = sum over rows of dy.
+// The backward pass has to read s anyway and computes m and v from it again, so nothing but s is kept between the two.
+// Both directions are bound by bytes: each row is loaded once, held in registers and written once. Sums are fp32, the variance
+// that of the centred values.
+//
+// A row takes L lanes with P pieces of 8 channels each (channels 8 (lane + L j) + 0..7), so every load and store is
+// 16 bytes wide and neighbouring lanes cover whole cache lines. L is 16, 32 or 64 lanes of one wave, whose sums are
+// exchanges between lanes, or, for rows past 2048 channels, four or eight waves, which join their sums in LDS.
+#include <type_traits>
+
+#include "gdn_block.h"
+#include "gdn_row.h"
+
+namespace gdn {
+
+// Sums over the L lanes of a row, of two values at a time. red: two buffers that turn, so that one barrier per sum is enough.
+template <int L>
+struct RowSums {
+    static constexpr int W = L / 64;                     // waves of a row (0: part of one)
+    static constexpr int RED = W > 1 ? 2 * 2 * W : 1;    // floats per row group
+    float* red;
+    int turn = 0;
+    __device__ __forceinline__ RowSums(float* r) : red(r) {}
+    __device__ __forceinline__ void sum2(float& a, float& b) {
+        a = row_sum<(L > 64 ? 64 : L)>(a);
+        b = row_sum<(L > 64 ? 64 : L)>(b);
+        if constexpr (W > 1) {
+            const int wave = (threadIdx.x >> 6) % W;
+            float* r = red + 2 * W * turn;
+            if ((threadIdx.x & 63) == 0) {
+                r[wave] = a;
+                r[W + wave] = b;
+            }
+            __syncthreads();
+            a = b = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                a += r[w];
+                b += r[W + w];
+            }
+            turn ^= 1;
+        }
+    }
+    __device__ __forceinline__ float sum(float a) {
+        float z = 0.f;
+        sum2(a, z);
+        return a;
+    }
+};
+
+// Threads of a forward work-group: four waves, or a row's eight.
+constexpr int ln_fwd_threads(int L) { return L > 256 ? L : 256; }
+
+template <typename TX, typename TS, typename TY, int L, int P, bool NT>
+__global__ __launch_bounds__(ln_fwd_threads(L)) void layer_norm_fwd_kernel(LayerNormProblem p) {
+    __shared__ float red[RowSums<L>::RED];
+    RowSums<L> rs(red);
+    const int l = threadIdx.x % L;
+    const long row = (long)blockIdx.x * (ln_fwd_threads(L) / L) + threadIdx.x / L;
+    const bool ok = row < p.rows;
+    const TX* xp = static_cast<const TX*>(p.x) + row * p.x_row;
+    const TS* rp = static_cast<const TS*>(p.residual) + row * p.r_row;
+    Raw8<TX> xr[P];
+    Raw8<TS> rr[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        const int c = 8 * (l + L * j);
+        xr[j].zero();
+        if (ok && c < p.d) xr[j].load(xp + c);
+    }
+    if (p.residual) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const int c = 8 * (l + L * j);
+            rr[j].zero();
+            if (ok && c < p.d) rr[j].load(rp + c);
+        }
+    }
+    float v[P][8], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        const int c = 8 * (l + L * j);
+        xr[j].get(v[j]);
+        if (p.residual) {
+            float t[8];
+            rr[j].get(t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = to_f32(from_f32<TS>(v[j][e] + t[e]));
+            if (ok && c < p.d) store8<NT>(static_cast<TS*>(p.sum) + row * p.d + c, v[j]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += v[j][e];
+    }
+    const float inv_d = 1.f / p.d, mean = rs.sum(sum) * inv_d;
+    float sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        const bool in = 8 * (l + L * j) < p.d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[j][e] = in ? v[j][e] - mean : 0.f;
+            sq += v[j][e] * v[j][e];
+        }
+    }
+    const float r = 1.f / sqrtf(rs.sum(sq) * inv_d + p.eps);
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        const int c = 8 * (l + L * j);
+        if (ok && c < p.d) {
+            float w[8], b[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 1.f, b[e] = 0.f;
+            Raw8<float> wr;
+            if (p.weight) {
+                wr.load(p.weight + c);
+                wr.get(w);
+            }
+            if (p.bias) {
+                wr.load(p.bias + c);
+                wr.get(b);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * r * w[e] + b[e];
+            store8<NT>(static_cast<TY*>(p.y) + row * p.d + c, v[j]);
+        }
+    }
+}
+
+constexpr int kLnBwdThreads = 512;
+
+// DW: the gradients of weight and bias too. The grid is then layer_norm_parts work-groups, each of which walks its rows with a
+// fixed stride, sums their contributions in registers, then over its row groups in LDS, and writes one partial row
+// [2, d] (weight, bias). No atomics: the same inputs give the same bits.
+template <typename TS, typename TY, int L, int P, bool DW, bool NT>
+__global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LayerNormProblem p) {
+    constexpr int RG = kLnBwdThreads / L;
+    __shared__ float red[RG * RowSums<L>::RED];
+    __shared__ float part[DW ? RG * 2 * 8 * L : 1];
+    const int l = threadIdx.x % L, grp = threadIdx.x / L;
+    RowSums<L> rs(red + grp * RowSums<L>::RED);
+    const float inv_d = 1.f / p.d;
+    float aw[DW ? P : 1][8], ab[DW ? P : 1][8];
+    if constexpr (DW) {
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) aw[j][e] = ab[j][e] = 0.f;
+    }
+    for (long row0 = (long)blockIdx.x * RG; row0 < p.rows; row0 += (long)gridDim.x * RG) {
+        const long row = row0 + grp;
+        const bool ok = row < p.rows;
+        Raw8<TS> xr[P], tr[P];
+        Raw8<TY> gr[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const int c = 8 * (l + L * j);
+            xr[j].zero();
+            gr[j].zero();
+            if (ok && c < p.d) {
+                xr[j].load(static_cast<const TS*>(p.x) + row * p.x_row + c);
+                gr[j].load(static_cast<const TY*>(p.dy) + row * p.d + c);
+            }
+        }
+        if (p.dsum) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const int c = 8 * (l + L * j);
+                if (ok && c < p.d) tr[j].load(static_cast<const TS*>(p.dsum) + row * p.d + c);
+            }
+        }
+        float v[P][8], g[P][8], sum = 0.f, gsum = 0.f;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const int c = 8 * (l + L * j);
+            xr[j].get(v[j]);
+            gr[j].get(g[j]);
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 1.f;
+            if (p.weight && c < p.d) {
+                Raw8<float> wr;
+                wr.load(p.weight + c);
+                wr.get(w);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sum += v[j][e];
+                gsum += g[j][e] * w[e];
+            }
+        }
+        rs.sum2(sum, gsum);
+        const float mean = sum * inv_d, gm = gsum * inv_d;
+        float sq = 0.f, gx = 0.f;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const int c = 8 * (l + L * j);
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 1.f;
+            if (p.weight && c < p.d) {
+                Raw8<float> wr;
+                wr.load(p.weight + c);
+                wr.get(w);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[j][e] = c < p.d ? v[j][e] - mean : 0.f;
+                sq += v[j][e] * v[j][e];
+                gx += g[j][e] * w[e] * v[j][e];
+            }
+        }
+        rs.sum2(sq, gx);
+        const float r = 1.f / sqrtf(sq * inv_d + p.eps), k = gx * r * inv_d;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const int c = 8 * (l + L * j);
+            float w[8], t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 1.f, t[e] = 0.f;
+            if (p.weight && c < p.d) {
+                Raw8<float> wr;
+                wr.load(p.weight + c);
+                wr.get(w);
+            }
+            if (p.dsum && ok && c < p.d) tr[j].get(t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xh = v[j][e] * r;
+                if constexpr (DW) {   // rows past the end hold zeros
+                    aw[j][e] += g[j][e] * xh;
+                    ab[j][e] += g[j][e];
+                }
+                t[e] += r * (g[j][e] * w[e] - gm - xh * k);
+            }
+            if (ok && c < p.d) store8<NT>(static_cast<TS*>(p.dx) + row * p.d + c, t);
+        }
+    }
+    if constexpr (DW) {
+        // piece by piece: the row groups' sums side by side in LDS, then added in their order
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                part[(grp * 2 + 0) * 8 * L + 8 * l + e] = aw[j][e];
+                part[(grp * 2 + 1) * 8 * L + 8 * l + e] = ab[j][e];
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * 8 * L; i += kLnBwdThreads) {
+                const int which = i / (8 * L), c = i % (8 * L);
+                float a = 0.f;
+#pragma unroll
+                for (int q = 0; q < RG; ++q) a += part[(q * 2 + which) * 8 * L + c];
+                if (8 * L * j + c < p.d) p.partial[((long)blockIdx.x * 2 + which) * p.d + 8 * L * j + c] = a;
+            }
+        }
+    }
+}
+
+// A work-group per 16 columns: 16 lanes across them and 64 down the rows, joined in LDS.
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int nparts, long n0, long n1, float* out0, float* out1) {
+    __shared__ float sum[64][17];
+    const int lc = threadIdx.x & 15, lr = threadIdx.x >> 4;
+    const long n = n0 + n1, c = (long)blockIdx.x * 16 + lc;
+    float x[kMaxParts / 64], a = 0.f;
+#pragma unroll
+    for (int j = 0; j < kMaxParts / 64; ++j) {
+        const int i = lr + 64 * j;
+        x[j] = i < nparts && c < n ? partial[(long)i * n + c] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kMaxParts / 64; ++j) a += x[j];
+    sum[lr][lc] = a;
+    __syncthreads();
+#pragma unroll
+    for (int m = 32; m > 0; m /= 2) {
+        if (lr < m) sum[lr][lc] += sum[lr + m][lc];
+        __syncthreads();
+    }
+    if (lr == 0 && c < n) {
+        if (c < n0) {
+            if (out0) out0[c] = sum[0][lc];
+        } else if (out1) {
+            out1[c - n0] = sum[0][lc];
+        }
+    }
+}
+
+hipError_t launch_column_sum(const float* partial, int nparts, long n0, long n1, float* out0, float* out1, hipStream_t s) {
+    return launch(column_sum_kernel, dim3((unsigned)((n0 + n1 + 15) / 16)), dim3(1024), s, partial, nparts, n0, n1, out0, out1);
+}
+
+// Lanes of a row and pieces per lane.
+template <typename F>
+static hipError_t ln_shape(int d, F f) {
+    if (d <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+    if (d <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+    if (d <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    if (d <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+    if (d <= 2048) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+    if (d <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+    if (d <= 8192) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
+}
+static int ln_lanes(int d) { return d <= 128 ? 16 : d <= 256 ? 32 : d <= 2048 ? 64 : d <= 8192 ? 256 : 512; }
+
+template <typename TX, typename TS, typename TY>
+static hipError_t ln_fwd(const LayerNormProblem& p, hipStream_t s) {
+    return ln_shape(p.d, [&](auto lanes, auto pieces) {
+        constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value;
+        constexpr int NT = ln_fwd_threads(L), RG = NT / L;
+        return launch(layer_norm_fwd_kernel<TX, TS, TY, L, P, false>, dim3((unsigned)((p.rows + RG - 1) / RG)), dim3(NT), s, p);
+    });
+}
+
+hipError_t launch_layer_norm_fwd(const LayerNormProblem& p, hipStream_t s) {
+    if (p.rows == 0) return hipSuccess;
+    if (!p.x_bf16) return p.y_bf16 ? ln_fwd<float, float, uint16_t>(p, s) : ln_fwd<float, float, float>(p, s);
+    if (p.s_bf16) return p.y_bf16 ? ln_fwd<uint16_t, uint16_t, uint16_t>(p, s) : ln_fwd<uint16_t, uint16_t, float>(p, s);
+    return p.y_bf16 ? ln_fwd<uint16_t, float, uint16_t>(p, s) : ln_fwd<uint16_t, float, float>(p, s);
+}
+
+// Work-groups (and partial rows) of the backward pass with gradients of weight and bias: one per CU, but no more than there
+// are groups of rows.
+int layer_norm_parts(long rows, int d) {
+    const int rg = kLnBwdThreads / ln_lanes(d);
+    const long blocks = (rows + rg - 1) / rg;
+    return (int)(blocks < 256 ? blocks : 256);
+}
+
+template <typename TS, typename TY>
+static hipError_t ln_bwd(const LayerNormProblem& p, hipStream_t s) {
+    return ln_shape(p.d, [&](auto lanes, auto pieces) {
+        constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value;
+        if (!p.dweight && !p.dbias) {
+            if (p.rows == 0) return hipSuccess;
+            const dim3 grid((unsigned)((p.rows + kLnBwdThreads / L - 1) / (kLnBwdThreads / L)));
+            return launch(layer_norm_bwd_kernel<TS, TY, L, P, false, false>, grid, dim3(kLnBwdThreads), s, p);
+        }
+        const int parts = layer_norm_parts(p.rows, p.d);
+        if (parts > 0) {
+            const hipError_t e = launch(layer_norm_bwd_kernel<TS, TY, L, P, true, false>, dim3((unsigned)parts), dim3(kLnBwdThreads), s, p);
+            if (e != hipSuccess) return e;
+        }
+        return launch_column_sum(p.partial, parts, p.d, p.d, p.dweight, p.dbias, s);
+    });
+}
+
+hipError_t launch_layer_norm_bwd(const LayerNormProblem& p, hipStream_t s) {
+    if (p.s_bf16) return p.y_bf16 ? ln_bwd<uint16_t, uint16_t>(p, s) : ln_bwd<uint16_t, float>(p, s);
+    return p.y_bf16 ? ln_bwd<float, uint16_t>(p, s) : ln_bwd<float, float>(p, s);
+}
+
+}  // namespace gdn

@@ -16,6 +16,7 @@
 // digits in fp32), reduced to half a revolution, and their cosines and sines kept in LDS for all heads.
 #include "gdn_device.h"
 #include "gdn_internal.h"
+#include "gdn_row.h"
 
 namespace gdn {
 
@@ -26,61 +27,8 @@ constexpr int kNormThreads = 256;
 
 enum { ROPE_NONE = 0, ROPE_HALF = 1, ROPE_PAIRS = 2 };
 
-// Eight consecutive channels as they lie in memory, and as fp32: rows wait for their turn as loaded, which halves the
-// registers of bf16 rows in flight.
-template <typename T> struct Raw8;
-template <> struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = *reinterpret_cast<const float4*>(p);
-        b = *reinterpret_cast<const float4*>(p + 4);
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
-};
-template <> struct Raw8<uint16_t> {
-    uint4 a;
-    __device__ __forceinline__ void load(const uint16_t* p) { a = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = bf16_lo_half(w[e]);
-            x[2 * e + 1] = bf16_hi_half(w[e]);
-        }
-    }
-};
-// NT: past the caches, in the calls of many rows (NP = 4), whose outputs mostly exceed the L2 (the 32768-token call above: 57 us
+// Outputs are stored past the caches (NT) in the calls of many rows (NP = 4), whose outputs mostly exceed the L2 (the 32768-token call above: 57 us
 // against 61). The rule counts rows, not bytes: very short rows go past the caches too.
-template <bool NT, typename T>
-__device__ __forceinline__ void store_piece(void* p, const T& x) {
-    if constexpr (NT) __builtin_nontemporal_store(x, static_cast<T*>(p));
-    else *static_cast<T*>(p) = x;
-}
-template <bool NT>
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-    store_piece<NT>(p, f32x4_t{x[0], x[1], x[2], x[3]});
-    store_piece<NT>(p + 4, f32x4_t{x[4], x[5], x[6], x[7]});
-}
-template <bool NT>
-__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
-    store_piece<NT>(p, u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                               pack_bf16x2(x[6], x[7])});
-}
-
-// Sum over the G lanes of a row, in every lane.
-template <int G>
-__device__ __forceinline__ float row_sum(float x) {
-    x += dpp_f32<0xB1>(x);    // quad_perm [1,0,3,2]
-    x += dpp_f32<0x4E>(x);    // quad_perm [2,3,0,1]
-    x += dpp_f32<0x141>(x);   // row_half_mirror
-    if constexpr (G >= 16) x += dpp_f32<0x140>(x);   // row_mirror
-    if constexpr (G >= 32) x += __shfl_xor(x, 16, 64);
-    return x;
-}
 
 // The rows of a work-group and their angles. A block of RB consecutive rows (row = token * (Hq + Hk) + head, queries
 // first) touches at most RB / 2 + 2 tokens, since a token has two rows at least.

@@ -1,0 +1,516 @@
+// Gated linear recurrence per channel: a scan over long sequences, its gradients, and its form on a pool of states, for gfx950.
+//
+// Per sequence and channel, a_t = exp(g_t):
+//     h_t = a_t h_{t-1} + b_t,   b_t = x_t, or (blend) (1 - a_t) x_t.
+// Backward, with D_t the gradient reaching h_t and E_t = a_t D_t what it passes on to h_{t-1}:
+//     D_t = dh_t + E_{t+1},   E_{len+1} = dhT,   dx = D or (1 - a) D,   dg = E_t h_{t-1} or E_t (h_{t-1} - x_t),   dh0 = E_1.
+// Four operations an element against 8 (forward) or 14 (backward) bytes in bf16: bound by bytes, if the sequence is cut. A run of tokens
+// maps the state entering it to the one leaving it by h -> A h + H, and such maps compose, so every thread first forms the
+// map of its few tokens (8 channels wide, as loaded, in registers), the maps of a tile of 256 tokens x 64 channels are joined in LDS, and
+// with the state entering the tile known each thread runs its tokens again from registers: inputs are read once, outputs
+// written once.
+// The state entering a tile comes from the tiles before it, in the same launch: a tile publishes its own map as soon as it has it, and its
+// final state once it knows what enters. One that waits reads the eight tiles before it and goes on from the last
+// final state through the maps behind it. It always takes the same sums in the same order, wherever it finds the state, so the
+// bits do not depend on timing. Tiles are numbered by a ticket drawn at the start of a work-group, and a tile waits for
+// lower tickets only, whose work-groups run already and publish their maps without waiting: every wait ends. The words that pass
+// between work-groups are single relaxed atomics at device scope that hold their own mark (all ones: not there yet), so nothing has to be
+// fenced. The backward pass walks the tiles the other way; the states entering them are kept by the forward one.
+#include "gdn_block.h"
+#include "gdn_row.h"
+
+namespace gdn {
+
+constexpr uint32_t kNotYet = 0xffffffffu;
+constexpr int kLookBack = 8;
+
+// a value that is never the mark (any NaN becomes the ordinary one)
+__device__ __forceinline__ float publishable(float x) { return x == x ? x : __uint_as_float(0x7fc00000u); }
+__device__ __forceinline__ void publish_map(uint64_t* p, float A, float H) {
+    const uint64_t w = (uint64_t)__float_as_uint(publishable(H)) << 32 | __float_as_uint(publishable(A));
+    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish_state(float* p, float h) {
+    __hip_atomic_store(reinterpret_cast<uint32_t*>(p), __float_as_uint(publishable(h)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// What leaves the tile before this one, for column `col` of every lane. step: the distance of the tile before it in rows
+// (-1 forward, 1 backward); before: the number of tiles before it in its sequence (>= 1).
+__device__ __forceinline__ float enter_from(const ScanProblem& p, long row, int step, int before, long col) {
+    const long pitch = (long)p.ncb * kScanChannels;
+    const int depth = min(before, kLookBack);
+    for (;;) {
+        float c = 0.f;
+        bool ok = false;
+        uint32_t state[kLookBack];
+        uint64_t map[kLookBack];
+#pragma unroll
+        for (int j = 0; j < kLookBack; ++j) {
+            const long at = (row + (long)step * (min(j, depth - 1) + 1)) * pitch + col;
+            state[j] = __hip_atomic_load(reinterpret_cast<uint32_t*>(p.pref) + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            map[j] = __hip_atomic_load(p.agg + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (int j = kLookBack - 1; j >= 0; --j) {
+            if (j < depth) {
+                const bool here = state[j] != kNotYet, mapped = (uint32_t)map[j] != kNotYet;
+                const float through = __fmaf_rn(__uint_as_float((uint32_t)map[j]), c, __uint_as_float((uint32_t)(map[j] >> 32)));
+                c = here ? __uint_as_float(state[j]) : through;
+                ok = here || (ok && mapped);
+            }
+        }
+        if (__all(ok)) return c;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
+// The rows of tiles of this call.
+__device__ __forceinline__ long scan_rows(const ScanProblem& p) { return p.base ? min((long)p.base[p.N], p.rows) : p.rows; }
+
+// A tile's place: sequence, number within it, first token, tokens.
+struct ScanTile {
+    int n, s, last, t0, len;   // last: the number of its sequence's last tile
+};
+__device__ __forceinline__ ScanTile scan_tile(const ScanProblem& p, long row, long rows) {
+    ScanTile k;
+    int b, e;
+    if (!p.cu_seqlens) {
+        const int per = max(1, (p.T + kScanTokens - 1) / kScanTokens);
+        k.n = (int)(row / per);
+        k.s = (int)(row - (long)k.n * per);
+        b = k.n * p.T;
+        e = b + p.T;
+    } else {
+        int lo = (int)min(row, (long)p.N - 1);   // without a table every sequence has one tile
+        long first = lo;
+        if (p.base) {
+            lo = 0;
+            int hi = p.N;   // the last n with base[n] <= row
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.base[mid] <= row) lo = mid; else hi = mid;
+            }
+            first = p.base[lo];
+        }
+        k.n = lo;
+        k.s = (int)(row - first);
+        b = min(max(p.cu_seqlens[lo], 0), p.tokens);
+        e = min(max(p.cu_seqlens[lo + 1], b), p.tokens);
+    }
+    k.last = max(0, (e - b - 1) / kScanTokens);
+    if (p.base) k.last = (int)min((long)k.last, rows - 1 - (row - k.s));   // none waits for a tile that is not run
+    k.t0 = b + k.s * kScanTokens;
+    k.len = max(0, min(e - k.t0, kScanTokens));
+    return k;
+}
+
+// This work-group's row of tiles and channel block: in chained calls by ticket. False: none left.
+__device__ __forceinline__ bool scan_place(const ScanProblem& p, long rows, long& row, int& cb, int* lds) {
+    unsigned id = blockIdx.x;
+    if (p.ticket) {
+        if (threadIdx.x == 0) *lds = __hip_atomic_fetch_add(p.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        id = (unsigned)*lds;
+    }
+    row = id / (unsigned)p.ncb;
+    cb = (int)(id - (unsigned)row * (unsigned)p.ncb);
+    return row < rows;
+}
+
+// 1 - e^g: 1 - a loses the digits of a small difference. For g in (-1/2, 1/2) the series to g^9 / 9! (the rest is below 2^-27 of it).
+__device__ __forceinline__ float one_minus_exp(float g, float a) {
+    float s = 1.f / 362880.f;
+    s = __fmaf_rn(s, g, 1.f / 40320.f);
+    s = __fmaf_rn(s, g, 1.f / 5040.f);
+    s = __fmaf_rn(s, g, 1.f / 720.f);
+    s = __fmaf_rn(s, g, 1.f / 120.f);
+    s = __fmaf_rn(s, g, 1.f / 24.f);
+    s = __fmaf_rn(s, g, 1.f / 6.f);
+    s = __fmaf_rn(s, g, 0.5f);
+    s = __fmaf_rn(s, g, 1.f);
+    return fabsf(g) < 0.5f ? -g * s : 1.f - a;
+}
+
+// Clears the marks and the ticket, and lays the tiles of packed sequences out.
+__global__ __launch_bounds__(1024) void scan_setup_kernel(ScanProblem p) {
+    const long words = p.rows * p.ncb * kScanChannels;   // agg: 2 a word, pref: 1
+    const long at = (long)blockIdx.x * 1024 + threadIdx.x, step = (long)gridDim.x * 1024;
+    uint4* a = reinterpret_cast<uint4*>(p.agg);
+    uint4* b = reinterpret_cast<uint4*>(p.pref);
+    const uint4 mark = make_uint4(kNotYet, kNotYet, kNotYet, kNotYet);
+    for (long i = at; i < words / 2; i += step) a[i] = mark;
+    for (long i = at; i < words / 4; i += step) b[i] = mark;
+    if (blockIdx.x != 0) return;
+    if (threadIdx.x == 0) *p.ticket = 0;
+    if (!p.base) return;
+    __shared__ int sum[1024];
+    int before = 0;
+    for (int n0 = 0; n0 < p.N; n0 += 1024) {
+        const int n = n0 + threadIdx.x;
+        int tiles = 0;
+        if (n < p.N) {
+            const int lo = min(max(p.cu_seqlens[n], 0), p.tokens), hi = min(max(p.cu_seqlens[n + 1], lo), p.tokens);
+            tiles = max(1, (hi - lo + kScanTokens - 1) / kScanTokens);
+        }
+        __syncthreads();
+        sum[threadIdx.x] = tiles;
+        __syncthreads();
+        for (int d = 1; d < 1024; d *= 2) {
+            const int add = (int)threadIdx.x >= d ? sum[threadIdx.x - d] : 0;
+            __syncthreads();
+            sum[threadIdx.x] += add;
+            __syncthreads();
+        }
+        // offsets that fall can count more tiles than there are rows: those past the last row are not run
+        if (n < p.N) p.base[n] = (int)min((long)before + sum[threadIdx.x] - tiles, p.rows);
+        before = (int)min((long)before + sum[1023], p.rows);
+    }
+    if (threadIdx.x == 0) p.base[p.N] = before;
+}
+
+// R: tokens per thread; 256 / R groups of 8 lanes, 8 channels a lane.
+template <typename TX, typename TH, int R, bool BLEND>
+__global__ __launch_bounds__(8 * kScanTokens / R) void scan_fwd_kernel(ScanProblem p) {
+    constexpr int G = kScanTokens / R;
+    __shared__ float2 maps[G][kScanChannels];
+    __shared__ float enter[kScanChannels];
+    __shared__ int ticket;
+    const long rows = scan_rows(p);
+    long row;
+    int cb;
+    if (!scan_place(p, rows, row, cb, &ticket)) return;
+    const ScanTile tile = scan_tile(p, row, rows);
+    const int l = threadIdx.x & 7, grp = threadIdx.x >> 3;
+    const long c = (long)cb * kScanChannels + 8 * l;
+    const bool in = c < p.D;
+    const long t0 = (long)tile.t0 + grp * R;
+    const int mine = min(max(tile.len - grp * R, 0), R);   // this thread's tokens
+
+    Raw8<TX> xr[R];
+    Raw8<float> gr[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        xr[i].zero();
+        gr[i].zero();
+        if (in && i < mine) {
+            gr[i].load(p.g + (t0 + i) * p.D + c);
+            xr[i].load(static_cast<const TX*>(p.x) + (t0 + i) * p.x_row + c);
+        }
+    }
+    float a[R][8], b[BLEND ? R : 1][8], A[8], H[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) A[e] = 1.f, H[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {   // tokens past the end: g = 0, x = 0, the state as it is
+        float x[8];
+        gr[i].get(a[i]);
+        xr[i].get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float g = a[i][e];
+            a[i][e] = __expf(g);
+            if constexpr (BLEND) {
+                x[e] *= one_minus_exp(g, a[i][e]);
+                b[i][e] = x[e];
+            }
+            H[e] = __fmaf_rn(a[i][e], H[e], x[e]);
+            A[e] *= a[i][e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) maps[grp][8 * l + e] = make_float2(A[e], H[e]);
+    __syncthreads();
+    if (threadIdx.x < kScanChannels) {
+        const int ch = threadIdx.x;
+        const long col = (long)cb * kScanChannels + ch;
+        const bool real = col < p.D;
+        float At = 1.f, Ht = 0.f;   // the map of the groups before each, in its place
+#pragma unroll 16
+        for (int k = 0; k < G; ++k) {
+            const float2 m = maps[k][ch];
+            maps[k][ch] = make_float2(At, Ht);
+            Ht = __fmaf_rn(m.x, Ht, m.y);
+            At *= m.x;
+        }
+        const long at = row * p.ncb * kScanChannels + col;
+        float h = 0.f;
+        if (tile.s == 0) {
+            if (p.h0 && real) h = p.h0[(long)tile.n * p.D + col];
+        } else {
+            publish_map(p.agg + at, At, Ht);
+            h = enter_from(p, row, -1, tile.s, col);
+        }
+        if (tile.s < tile.last) publish_state(p.pref + at, __fmaf_rn(At, h, Ht));
+        if (p.carries && real) p.carries[row * p.D + col] = h;
+        enter[ch] = h;
+    }
+    __syncthreads();
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float2 m = maps[grp][8 * l + e];
+        h[e] = __fmaf_rn(m.x, enter[8 * l + e], m.y);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        float x[8];
+        if constexpr (!BLEND) xr[i].get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = __fmaf_rn(a[i][e], h[e], BLEND ? b[i][e] : x[e]);
+        if (in && i < mine) store8<false>(static_cast<TH*>(p.h) + (t0 + i) * p.D + c, h);
+    }
+    // the state behind the sequence's last token (or the one it began with, where it has none)
+    if (p.hT && in && tile.s == tile.last && (mine > 0 ? grp * R + mine == tile.len : grp == 0 && tile.len == 0))
+        store8<false>(p.hT + (long)tile.n * p.D + c, h);
+}
+
+template <typename TX, typename TH, int R, bool BLEND>
+__global__ __launch_bounds__(8 * kScanTokens / R) void scan_bwd_kernel(ScanProblem p) {
+    constexpr int G = kScanTokens / R;
+    // of every group: A; H, then the state entering it; the gradient's part of its map, then that of the groups behind it; their A
+    __shared__ float mA[G][kScanChannels], mH[G][kScanChannels], mE[G][kScanChannels], mS[G][kScanChannels];
+    __shared__ float enter[kScanChannels];
+    __shared__ int ticket;
+    const long rows = scan_rows(p);
+    long row;
+    int cb;
+    if (!scan_place(p, rows, row, cb, &ticket)) return;
+    if (p.ticket) row = rows - 1 - row;   // the last tiles first
+    const ScanTile tile = scan_tile(p, row, rows);
+    const int l = threadIdx.x & 7, grp = threadIdx.x >> 3;
+    const long c = (long)cb * kScanChannels + 8 * l;
+    const bool in = c < p.D;
+    const long t0 = (long)tile.t0 + grp * R;
+    const int mine = min(max(tile.len - grp * R, 0), R);
+
+    Raw8<TX> xr[R];
+    Raw8<TH> dr[R];
+    Raw8<float> gr[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        xr[i].zero();
+        dr[i].zero();
+        gr[i].zero();
+        if (in && i < mine) {
+            gr[i].load(p.g + (t0 + i) * p.D + c);
+            xr[i].load(static_cast<const TX*>(p.x) + (t0 + i) * p.x_row + c);
+            dr[i].load(static_cast<const TH*>(p.dh) + (t0 + i) * p.D + c);
+        }
+    }
+    float a[R][8], keep[BLEND ? R : 1][8], A[8], H[8], E[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) A[e] = 1.f, H[e] = E[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        float x[8];
+        gr[i].get(a[i]);
+        xr[i].get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float g = a[i][e];
+            a[i][e] = __expf(g);
+            if constexpr (BLEND) {
+                keep[i][e] = one_minus_exp(g, a[i][e]);
+                x[e] *= keep[i][e];
+            }
+            H[e] = __fmaf_rn(a[i][e], H[e], x[e]);
+            A[e] *= a[i][e];
+        }
+    }
+#pragma unroll
+    for (int i = R - 1; i >= 0; --i) {
+        float d[8];
+        dr[i].get(d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) E[e] = a[i][e] * (d[e] + E[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        mA[grp][8 * l + e] = A[e];
+        mH[grp][8 * l + e] = H[e];
+        mE[grp][8 * l + e] = E[e];
+    }
+    __syncthreads();
+    const int wave = threadIdx.x >> 6, ch = threadIdx.x & 63;
+    const long col = (long)cb * kScanChannels + ch;
+    if (wave == 0) {   // the states entering the groups
+        float h = col < p.D ? p.carries[row * p.D + col] : 0.f;
+#pragma unroll 16
+        for (int k = 0; k < G; ++k) {
+            const float m = mA[k][ch], q = mH[k][ch];
+            mH[k][ch] = h;
+            h = __fmaf_rn(m, h, q);
+        }
+    } else if (wave == 1) {   // the map of the groups behind each, and what comes from the tiles behind this one
+        float At = 1.f, Et = 0.f;
+#pragma unroll 16
+        for (int k = G - 1; k >= 0; --k) {
+            const float m = mA[k][ch], q = mE[k][ch];
+            mS[k][ch] = At;
+            mE[k][ch] = Et;
+            Et = __fmaf_rn(m, Et, q);
+            At *= m;
+        }
+        const long at = row * p.ncb * kScanChannels + col;
+        float d = 0.f;
+        if (tile.s == tile.last) {
+            if (p.dhT && col < p.D) d = p.dhT[(long)tile.n * p.D + col];
+        } else {
+            publish_map(p.agg + at, At, Et);
+            d = enter_from(p, row, 1, tile.last - tile.s, col);
+        }
+        if (tile.s > 0) publish_state(p.pref + at, __fmaf_rn(At, d, Et));
+        enter[ch] = d;
+    }
+    __syncthreads();
+    float h[R][8];   // the state before each token
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[0][e] = mH[grp][8 * l + e];
+#pragma unroll
+    for (int i = 0; i + 1 < R; ++i) {
+        float x[8];
+        xr[i].get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i + 1][e] = __fmaf_rn(a[i][e], h[i][e], BLEND ? keep[i][e] * x[e] : x[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) E[e] = __fmaf_rn(mS[grp][8 * l + e], enter[8 * l + e], mE[grp][8 * l + e]);
+#pragma unroll
+    for (int i = R - 1; i >= 0; --i) {
+        float d[8], x[8], dg[8];
+        dr[i].get(d);
+        xr[i].get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            d[e] += E[e];
+            E[e] = a[i][e] * d[e];
+            dg[e] = E[e] * (BLEND ? h[i][e] - x[e] : h[i][e]);
+            if constexpr (BLEND) d[e] *= keep[i][e];
+        }
+        if (in && i < mine) {
+            store8<false>(static_cast<TX*>(p.dx) + (t0 + i) * p.D + c, d);
+            store8<false>(p.dg + (t0 + i) * p.D + c, dg);
+        }
+    }
+    if (p.dh0 && in && tile.s == 0 && grp == 0) store8<false>(p.dh0 + (long)tile.n * p.D + c, E);
+}
+
+// Runs of tokens on a pool of states: a lane walks its sequence's tokens for four channels. Tokens come four at a time.
+template <typename TX, typename TH, bool BLEND>
+__global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblocks) {
+    const int n = blockIdx.x / cblocks;
+    const long c = ((long)(blockIdx.x % cblocks) * 64 + threadIdx.x) * 4;
+    if (c >= p.D) return;
+    int t0 = n, t1 = n + 1;
+    if (p.cu_seqlens) {   // offsets outside [0, tokens] or falling ones are clamped
+        t0 = min(max(p.cu_seqlens[n], 0), p.tokens);
+        t1 = min(max(p.cu_seqlens[n + 1], t0), p.tokens);
+    }
+    if (t0 >= t1) return;
+    const int slot = p.slots[n];
+    TH* hp = static_cast<TH*>(p.h) + c;
+    float h[4] = {0.f, 0.f, 0.f, 0.f};
+    if (slot < 0 || slot >= p.n_slots) {   // a padded entry: zeros for its tokens, no state touched
+        for (int t = t0; t < t1; ++t) store4c<false>(hp + (long)t * p.D, h);
+        return;
+    }
+    Raw4<float> state;
+    state.load(p.pool + (long)slot * p.D + c);
+    state.get(h);
+    constexpr int TB = 4;
+    for (int tb = t0; tb < t1; tb += TB) {
+        Raw4<TX> xr[TB];
+        Raw4<float> gr[TB];
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+            const long t = min(tb + i, t1 - 1);
+            xr[i].load(static_cast<const TX*>(p.x) + t * p.x_row + c);
+            gr[i].load(p.g + t * p.D + c);
+        }
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+            const int t = tb + i;
+            if (t < t1) {
+                float x[4], g[4];
+                xr[i].get(x);
+                gr[i].get(g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = __expf(g[e]);
+                    h[e] = __fmaf_rn(a, h[e], BLEND ? one_minus_exp(g[e], a) * x[e] : x[e]);
+                }
+                store4c<false>(hp + (long)t * p.D, h);
+                if (p.out_slots) {
+                    const int to = p.out_slots[t];
+                    if (to >= 0 && to < p.n_slots) store4c<false>(p.pool + (long)to * p.D + c, h);
+                }
+            }
+        }
+    }
+    if (!p.out_slots) store4c<false>(p.pool + (long)slot * p.D + c, h);
+}
+
+ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen) {
+    ScanLayout w{};
+    const long ncb = ((long)D + kScanChannels - 1) / kScanChannels;
+    const int longest = varlen ? tokens : T;   // the longest that a sequence can be
+    const long per = longest > kScanTokens ? ((long)T + kScanTokens - 1) / kScanTokens : 1;
+    w.rows = varlen ? (long)N + tokens / kScanTokens : N * per;
+    if (longest <= kScanTokens) return w;
+    const size_t cells = (size_t)w.rows * ncb * kScanChannels;
+    w.off_base = 256;
+    w.off_agg = w.off_base + (varlen ? (((size_t)N + 1) * 4 + 255) / 256 * 256 : 0);
+    w.off_pref = w.off_agg + cells * 8;
+    w.total = w.off_pref + cells * 4;
+    return w;
+}
+
+// The grid of tiles, with the marks cleared first where tiles pass states on.
+static hipError_t scan_setup(const ScanProblem& p, long& tiles, hipStream_t s) {
+    tiles = (p.ticket ? p.rows : (long)p.N) * p.ncb;
+    if (!p.ticket) return hipSuccess;
+    const long blocks = (p.rows * p.ncb * kScanChannels / 2 + 4095) / 4096;
+    return launch(scan_setup_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(1024), s, p);
+}
+
+template <typename TX, typename TH, bool BLEND>
+static hipError_t scan_fwd(const ScanProblem& p, hipStream_t s) {
+    constexpr int R = BLEND || sizeof(TX) == 4 ? 4 : 8;
+    long tiles;
+    const hipError_t e = scan_setup(p, tiles, s);
+    if (e != hipSuccess) return e;
+    return launch(scan_fwd_kernel<TX, TH, R, BLEND>, dim3((unsigned)tiles), dim3(8 * kScanTokens / R), s, p);
+}
+template <typename TX, typename TH, bool BLEND>
+static hipError_t scan_bwd(const ScanProblem& p, hipStream_t s) {
+    long tiles;
+    const hipError_t e = scan_setup(p, tiles, s);
+    if (e != hipSuccess) return e;
+    return launch(scan_bwd_kernel<TX, TH, 4, BLEND>, dim3((unsigned)tiles), dim3(2 * kScanTokens), s, p);
+}
+template <typename TX, typename TH, bool BLEND>
+static hipError_t scan_update(const ScanProblem& p, hipStream_t s) {
+    const int cblocks = (p.D + 255) / 256;
+    return launch(scan_update_kernel<TX, TH, BLEND>, dim3((unsigned)((long)p.N * cblocks)), dim3(64), s, p, cblocks);
+}
+
+hipError_t launch_scan_fwd(const ScanProblem& p, hipStream_t s) {
+    if (p.N == 0) return hipSuccess;
+    if (!p.bf16) return p.blend ? scan_fwd<float, float, true>(p, s) : scan_fwd<float, float, false>(p, s);
+    if (p.h_bf16) return p.blend ? scan_fwd<uint16_t, uint16_t, true>(p, s) : scan_fwd<uint16_t, uint16_t, false>(p, s);
+    return p.blend ? scan_fwd<uint16_t, float, true>(p, s) : scan_fwd<uint16_t, float, false>(p, s);
+}
+hipError_t launch_scan_bwd(const ScanProblem& p, hipStream_t s) {
+    if (p.N == 0) return hipSuccess;
+    if (!p.bf16) return p.blend ? scan_bwd<float, float, true>(p, s) : scan_bwd<float, float, false>(p, s);
+    if (p.h_bf16) return p.blend ? scan_bwd<uint16_t, uint16_t, true>(p, s) : scan_bwd<uint16_t, uint16_t, false>(p, s);
+    return p.blend ? scan_bwd<uint16_t, float, true>(p, s) : scan_bwd<uint16_t, float, false>(p, s);
+}
+hipError_t launch_scan_update(const ScanProblem& p, hipStream_t s) {
+    if (p.N == 0 || p.tokens == 0) return hipSuccess;
+    if (!p.bf16) return p.blend ? scan_update<float, float, true>(p, s) : scan_update<float, float, false>(p, s);
+    if (p.h_bf16) return p.blend ? scan_update<uint16_t, uint16_t, true>(p, s) : scan_update<uint16_t, uint16_t, false>(p, s);
+    return p.blend ? scan_update<uint16_t, float, true>(p, s) : scan_update<uint16_t, float, false>(p, s);
+}
+
+}  // namespace gdn

@@ -40,7 +40,8 @@
  *    during execution surface at the caller's next synchronisation.
  *  - GDN_CHECK=1 in the environment (a debugging aid): every entry point that takes
  *    cu_seqlens first copies it to the host, which synchronises `stream`, and returns
- *    GDN_ERR_SHAPE unless 0 = cu[0] <= cu[1] <= ... <= cu[N] = T (gdn_recurrent_fwd: <= T).
+ *    GDN_ERR_SHAPE unless 0 = cu[0] <= cu[1] <= ... <= cu[N] = T (gdn_recurrent_fwd, gdn_conv_* and
+ *    gdn_scan_*: <= T).
  *  - GDN_SEGMENT_CHUNKS=L in the environment (for tests and tuning) fixes the segment length
  *    of the long-chain split of the bf16 forward pass to L chunks; 0 turns the split off.
  *    Without it the split is chosen from the shape (see gdn_chunk_fwd_workspace_bytes). The
@@ -475,6 +476,130 @@ int gdn_qk_norm_bwd(const void *q, const void *k, const void *dq_out, const void
                     int64_t dq_head_stride, int64_t dk_token_stride, int64_t dk_head_stride, int norm,
                     float eps, int rot, int rope, float q_scale, float rope_scale, int dtype,
                     int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Layer norm with the residual sum in the same pass, as it stands before a block's projections. Per row of d channels:
+ *     s = x + r rounded to the sum's type (without a residual s = x),   m = sum s / d,   v = sum (s - m)^2 / d,
+ *     y = weight * (s - m) (v + eps)^(-1/2) + bias.
+ *
+ *   x           [rows, d] dtype, rows x_stride elements apart, channels contiguous
+ *   residual    [rows, d] sum_dtype (GDN_BF16 only for bf16 x), rows residual_stride apart, or NULL (sum, sum_dtype and
+ *               residual_stride are then not used)
+ *   weight, bias  fp32 [d] or NULL (ones, zeros)
+ *   y           [rows, d] out_dtype, dense
+ *   sum         [rows, d] sum_dtype, dense: s, which the next residual and the backward pass take
+ *   d           a multiple of 8, 8 .. 16384; rows < 2^28, rows * d < 2^35; eps > 0
+ * Pointers and strides are multiples of 16 bytes. y and sum may each be x or residual where that is dense and of the
+ * same type (not both the same one); other overlaps are undefined. Statistics and sums are fp32, the variance that of the centred values.
+ */
+int gdn_layer_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias,
+                       void *y, void *sum, int rows, int d, int64_t x_stride, int64_t residual_stride,
+                       float eps, int dtype, int sum_dtype, int out_dtype, void *stream);
+
+/*
+ * Backward pass of gdn_layer_norm_fwd: from sum (what was normalised: its sum, or its x without a residual; dtype, rows
+ * sum_stride apart), the gradient dy of y (out_dtype, dense) and, where not NULL, the gradient dsum that reaches the
+ * sum elsewhere (dtype, dense): dx [rows, d] (dtype, dense), the gradient of x and of the residual alike, and, where not NULL,
+ * the gradients of weight and bias (fp32 [d]; defined also where those were NULL), sums over the rows in a
+ * fixed order, which take a workspace of gdn_layer_norm_bwd_workspace_bytes(...) bytes, 256-byte aligned (fp32
+ * [work-groups, 2, d]); without them none is used. dx may be dsum, dy or sum where that is dense and of its type.
+ */
+size_t gdn_layer_norm_bwd_workspace_bytes(int rows, int d);
+int gdn_layer_norm_bwd(const void *sum, const void *dy, const void *dsum, const float *weight, void *dx,
+                       float *dweight, float *dbias, int rows, int d, int64_t sum_stride, float eps,
+                       int dtype, int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Short causal convolution per channel, as it stands between the projections and the norm or a recurrence. With u_t the
+ * inputs of one sequence, those before its first token from its window (or zeros), W = width and z the taps' sum
+ *     z_t = bias + sum_{j < W} weight[c, j] u_{t-(W-1)+j},   y_t = z_t (GDN_ACT_NONE) or z_t sigmoid(z_t) (GDN_ACT_SILU).
+ *
+ *   x           [B, T, D] dtype, tokens x_stride elements apart (row b starts b * T * x_stride on), channels contiguous
+ *   weight      fp32 [D, W], W in 2 .. 4 (weight[c, W-1] meets the token itself); bias fp32 [D] or NULL
+ *   window0     [N, W-1, D] dtype: the W-1 inputs before each sequence, oldest first, or NULL (zeros)
+ *   cu_seqlens  int32 [N + 1] device array of packed sequences (then B = 1) or NULL (N = B)
+ *   y           [B, T, D] dtype, dense; windowT [N, W-1, D] dtype: the last W-1 inputs of each sequence (of its window where it
+ *               is shorter), or NULL. Neither may overlap an input
+ *   D           a multiple of 8 up to 2^20; B * T <= 2^28, B * T * D <= 2^36, N <= 2^24, N * D <= 2^31
+ * Offsets outside [0, T] are clamped; rows of y that no sequence covers are left as they were. Pointers (bias: 4 bytes) and
+ * strides are multiples of 16 bytes. Arithmetic is fp32.
+ */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
+int gdn_conv_fwd(const void *x, const float *weight, const float *bias, const void *window0,
+                 const int32_t *cu_seqlens, void *y, void *windowT, int B, int T, int N, int D, int width,
+                 int64_t x_stride, int activation, int dtype, void *stream);
+
+/*
+ * Backward pass of gdn_conv_fwd: from the gradients dy [B, T, D] (dtype, dense) and dwindowT [N, W-1, D] (dtype, or NULL: zero)
+ * of its outputs: dx (dtype, tokens dx_stride >= D apart, so that it can be written into the gradient of a fused
+ * projection), and, where not NULL, dweight fp32 [D, W], dbias fp32 [D] and dwindow0 [N, W-1, D] (dtype), each defined also
+ * where its operand was NULL. The gradients of weight and bias are sums over all tokens in a fixed order and take a workspace of
+ * gdn_conv_bwd_workspace_bytes(...) bytes, 256-byte aligned (fp32 [work-group rows, D (W + 1)]); without them none is
+ * used. dx may not overlap an input.
+ */
+size_t gdn_conv_bwd_workspace_bytes(int B, int T, int D, int width);
+int gdn_conv_bwd(const void *x, const float *weight, const float *bias, const void *window0, const void *dy,
+                 const void *dwindowT, const int32_t *cu_seqlens, void *dx, float *dweight, float *dbias,
+                 void *dwindow0, int B, int T, int N, int D, int width, int64_t x_stride, int64_t dx_stride,
+                 int activation, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_conv_fwd for serving: runs of tokens of N sequences on a pool of windows, as gdn_recurrent_fwd has them for states.
+ *   x [T, D], y [T, D] dtype; windows [n_slots, W-1, D] dtype, updated in place; slots, cu_seqlens and out_slots as in
+ *   gdn_recurrent_fwd (padded entries give zeros; with out_slots the window after token t goes to slot out_slots[t];
+ *   the slots written must be distinct from each other and from those that other sequences read). x and y may not overlap the pool.
+ *   N * ceil(D / 2048) < 2^22. T = 0 or N = 0 does nothing.
+ */
+int gdn_conv_update(const void *x, const float *weight, const float *bias, void *windows,
+                    const int32_t *slots, const int32_t *cu_seqlens, const int32_t *out_slots, void *y,
+                    int T, int N, int D, int width, int n_slots, int64_t x_stride, int activation,
+                    int dtype, void *stream);
+
+/*
+ * Gated linear recurrence per channel, the light companion of the rule: a state of one number per channel. Per sequence,
+ * with a_t = exp(g_t):
+ *     h_t = a_t h_{t-1} + x_t,   or with blend   h_t = a_t h_{t-1} + (1 - a_t) x_t.
+ *
+ *   x           [B, T, D] dtype, tokens x_stride elements apart (row b starts b * T * x_stride on), channels contiguous
+ *   g           fp32 [B, T, D], dense: log a, <= 0 (not checked); -infinity forgets the state
+ *   h0          fp32 [N, D] or NULL (zeros)
+ *   cu_seqlens  int32 [N + 1] device array of packed sequences (then B = 1) or NULL (N = B)
+ *   h           [B, T, D] h_dtype (GDN_BF16 only for bf16 x), dense; hT fp32 [N, D]: the state behind each sequence, or NULL
+ *   carries     fp32 [gdn_scan_carry_rows(...), D] or NULL: the state entering every tile of 256 tokens of a sequence (a sequence
+ *               has one tile at least; those of one sequence follow each other), for the backward pass
+ *   workspace   gdn_scan_workspace_bytes(...) bytes, 256-byte aligned; none where no sequence can be longer than 256 tokens. Its
+ *               contents need not be set and mean nothing afterwards; calls that can run at once need one each
+ *   D           a multiple of 8 up to 2^20; B * T <= 2^28, B * T * D <= 2^36, N <= 2^24, N * D <= 2^31 and tiles *
+ *               ceil(D / 64) < 2^23
+ * Offsets outside [0, T] are clamped; rows of the outputs that no sequence covers are left as they were. x, g, h and hT are aligned
+ * to 16 bytes, h0 and carries to 4; x_stride is a multiple of 16 bytes. States are fp32; 1 - a is formed from g and keeps its digits
+ * where a is near 1. A NaN in x, g or h0, or an infinity in x or h0, makes its channel's states NaN or infinite from there to the sequence's end.
+ * The same inputs give the same bits.
+ */
+int64_t gdn_scan_carry_rows(int B, int T, int N, int varlen);
+size_t gdn_scan_workspace_bytes(int B, int T, int N, int D, int varlen);
+int gdn_scan_fwd(const void *x, const float *g, const float *h0, const int32_t *cu_seqlens, void *h,
+                 float *hT, float *carries, int B, int T, int N, int D, int64_t x_stride, int blend,
+                 int dtype, int h_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Backward pass of gdn_scan_fwd on the same x, g, cu_seqlens and the carries that it left: from the gradients dh [B, T, D]
+ * (h_dtype, dense) and dhT fp32 [N, D] (or NULL: zero) of its outputs: dx [B, T, D] (dtype, dense), dg fp32 [B, T, D] and, where
+ * not NULL, dh0 fp32 [N, D]. Workspace as in gdn_scan_fwd.
+ */
+int gdn_scan_bwd(const void *x, const float *g, const float *carries, const void *dh, const float *dhT,
+                 const int32_t *cu_seqlens, void *dx, float *dg, float *dh0, int B, int T, int N, int D,
+                 int64_t x_stride, int blend, int dtype, int h_dtype, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_scan_fwd for serving: runs of tokens of N sequences on a pool of states fp32 [n_slots, D], updated in place. x [T, D],
+ * g [T, D], h [T, D]; slots, cu_seqlens and out_slots as in gdn_recurrent_fwd (padded entries give zeros). For
+ * prompts of some hundred tokens and more gdn_scan_fwd is faster. N * ceil(D / 2048) < 2^22. T = 0 or N = 0 does nothing.
+ */
+int gdn_scan_update(const void *x, const float *g, float *states, const int32_t *slots,
+                    const int32_t *cu_seqlens, const int32_t *out_slots, void *h, int T, int N, int D,
+                    int n_slots, int64_t x_stride, int blend, int dtype, int h_dtype, void *stream);
 
 #ifdef __cplusplus
 }
