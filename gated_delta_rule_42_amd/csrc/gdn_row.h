@@ -8,6 +8,8 @@ namespace gdn {
 
 // Eight consecutive channels as they lie in memory, and as fp32: rows wait for their turn as loaded, which halves the
 // registers of bf16 rows in flight.
+// hide(): the compiler is made to assume that the words may have changed, so that a later get() unpacks them again instead of keeping fp32 values
+// from an earlier one, twice the registers, all the way.
 template <typename T> struct Raw8;
 template <> struct Raw8<float> {
     float4 a, b;
@@ -16,6 +18,7 @@ template <> struct Raw8<float> {
         b = *reinterpret_cast<const float4*>(p + 4);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void hide() {}
     __device__ __forceinline__ void get(float (&x)[8]) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
@@ -24,6 +27,7 @@ template <> struct Raw8<uint16_t> {
     uint4 a;
     __device__ __forceinline__ void load(const uint16_t* p) { a = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w)); }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll

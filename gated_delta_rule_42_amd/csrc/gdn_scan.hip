@@ -10,7 +10,7 @@
 // with the state entering the tile known each thread runs its tokens again from registers: inputs are read once, outputs
 // written once.
 // The state entering a tile comes from the tiles before it, in the same launch: a tile publishes its own map as soon as it has it, and its
-// final state once it knows what enters. One that waits reads the eight tiles before it and goes on from the last
+// final state once it knows what enters. One that waits reads the four tiles before it and goes on from the last
 // final state through the maps behind it. It always takes the same sums in the same order, wherever it finds the state, so the
 // bits do not depend on timing. Tiles are numbered by a ticket drawn at the start of a work-group, and a tile waits for
 // lower tickets only, whose work-groups run already and publish their maps without waiting: every wait ends. The words that pass
@@ -22,7 +22,7 @@
 namespace gdn {
 
 constexpr uint32_t kNotYet = 0xffffffffu;
-constexpr int kLookBack = 8;
+constexpr int kLookBack = 4;
 
 // a value that is never the mark (any NaN becomes the ordinary one)
 __device__ __forceinline__ float publishable(float x) { return x == x ? x : __uint_as_float(0x7fc00000u); }
@@ -34,9 +34,9 @@ __device__ __forceinline__ void publish_state(float* p, float h) {
     __hip_atomic_store(reinterpret_cast<uint32_t*>(p), __float_as_uint(publishable(h)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// What leaves the tile before this one, for column `col` of every lane. step: the distance of the tile before it in rows
+// What leaves the tile before this one, for column `col` (within a row) of every lane. step: the distance of the tile before it in rows
 // (-1 forward, 1 backward); before: the number of tiles before it in its sequence (>= 1).
-__device__ __forceinline__ float enter_from(const ScanProblem& p, long row, int step, int before, long col) {
+__device__ __forceinline__ float enter_from(const ScanProblem& p, long row, int step, int before, unsigned col) {
     const long pitch = (long)p.ncb * kScanChannels;
     const int depth = min(before, kLookBack);
     for (;;) {
@@ -46,9 +46,9 @@ __device__ __forceinline__ float enter_from(const ScanProblem& p, long row, int 
         uint64_t map[kLookBack];
 #pragma unroll
         for (int j = 0; j < kLookBack; ++j) {
-            const long at = (row + (long)step * (min(j, depth - 1) + 1)) * pitch + col;
-            state[j] = __hip_atomic_load(reinterpret_cast<uint32_t*>(p.pref) + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            map[j] = __hip_atomic_load(p.agg + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const long at = (row + (long)step * (min(j, depth - 1) + 1)) * pitch;
+            state[j] = __hip_atomic_load(reinterpret_cast<uint32_t*>(p.pref) + at + col, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            map[j] = __hip_atomic_load(p.agg + at + col, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
 #pragma unroll
         for (int j = kLookBack - 1; j >= 0; --j) {
@@ -65,7 +65,10 @@ __device__ __forceinline__ float enter_from(const ScanProblem& p, long row, int 
 }
 
 // The rows of tiles of this call.
-__device__ __forceinline__ long scan_rows(const ScanProblem& p) { return p.base ? min((long)p.base[p.N], p.rows) : p.rows; }
+__device__ __forceinline__ long scan_rows(const ScanProblem& p) {
+    if (!p.ticket) return p.N;
+    return p.base ? min((long)p.base[p.N], p.rows) : p.rows;
+}
 
 // A tile's place: sequence, number within it, first token, tokens.
 struct ScanTile {
@@ -104,17 +107,24 @@ __device__ __forceinline__ ScanTile scan_tile(const ScanProblem& p, long row, lo
     return k;
 }
 
-// This work-group's row of tiles and channel block: in chained calls by ticket. False: none left.
-__device__ __forceinline__ bool scan_place(const ScanProblem& p, long rows, long& row, int& cb, int* lds) {
-    unsigned id = blockIdx.x;
-    if (p.ticket) {
-        if (threadIdx.x == 0) *lds = __hip_atomic_fetch_add(p.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        id = (unsigned)*lds;
-    }
-    row = id / (unsigned)p.ncb;
-    cb = (int)(id - (unsigned)row * (unsigned)p.ncb);
-    return row < rows;
+// A work-group's channel block, and its row of tiles: in chained calls the ticket drawn from the block's own counter (one counter for all, and
+// 1,024 work-groups queue 5 us for it). Rows shift by one channel block each, so that the L2 of one XCD, which takes every eighth
+// work-group, does not see the same few channels of every row (32768 x 2048: 113 us without, 106 with it).
+struct ScanPlace {
+    int cb;
+    long row;
+};
+__device__ __forceinline__ ScanPlace scan_place(const ScanProblem& p) {
+    const unsigned id = blockIdx.x, row = id / (unsigned)p.ncb;
+    return ScanPlace{(int)((id + row) % (unsigned)p.ncb), (long)row};
+}
+constexpr int kTicketWords = 16;   // a counter to itself in 64 bytes
+__device__ __forceinline__ long draw_row(const ScanProblem& p, const ScanPlace& place, int* lds) {
+    if (!p.ticket) return place.row;
+    if (threadIdx.x == 0)
+        *lds = __hip_atomic_fetch_add(p.ticket + kTicketWords * place.cb, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*lds);   // one for all: rows and addresses stay scalar
 }
 
 // 1 - e^g: 1 - a loses the digits of a small difference. For g in (-1/2, 1/2) the series to g^9 / 9! (the rest is below 2^-27 of it).
@@ -131,21 +141,21 @@ __device__ __forceinline__ float one_minus_exp(float g, float a) {
     return fabsf(g) < 0.5f ? -g * s : 1.f - a;
 }
 
-// Clears the marks and the ticket, and lays the tiles of packed sequences out.
-__global__ __launch_bounds__(1024) void scan_setup_kernel(ScanProblem p) {
+// Clears the marks and the tickets, and lays the tiles of packed sequences out.
+__global__ __launch_bounds__(256) void scan_setup_kernel(ScanProblem p) {
     const long words = p.rows * p.ncb * kScanChannels;   // agg: 2 a word, pref: 1
-    const long at = (long)blockIdx.x * 1024 + threadIdx.x, step = (long)gridDim.x * 1024;
+    const long at = (long)blockIdx.x * 256 + threadIdx.x, step = (long)gridDim.x * 256;
     uint4* a = reinterpret_cast<uint4*>(p.agg);
     uint4* b = reinterpret_cast<uint4*>(p.pref);
     const uint4 mark = make_uint4(kNotYet, kNotYet, kNotYet, kNotYet);
     for (long i = at; i < words / 2; i += step) a[i] = mark;
     for (long i = at; i < words / 4; i += step) b[i] = mark;
     if (blockIdx.x != 0) return;
-    if (threadIdx.x == 0) *p.ticket = 0;
+    for (int i = threadIdx.x; i < p.ncb; i += 256) p.ticket[kTicketWords * i] = 0;
     if (!p.base) return;
-    __shared__ int sum[1024];
+    __shared__ int sum[256];
     int before = 0;
-    for (int n0 = 0; n0 < p.N; n0 += 1024) {
+    for (int n0 = 0; n0 < p.N; n0 += 256) {
         const int n = n0 + threadIdx.x;
         int tiles = 0;
         if (n < p.N) {
@@ -155,7 +165,7 @@ __global__ __launch_bounds__(1024) void scan_setup_kernel(ScanProblem p) {
         __syncthreads();
         sum[threadIdx.x] = tiles;
         __syncthreads();
-        for (int d = 1; d < 1024; d *= 2) {
+        for (int d = 1; d < 256; d *= 2) {
             const int add = (int)threadIdx.x >= d ? sum[threadIdx.x - d] : 0;
             __syncthreads();
             sum[threadIdx.x] += add;
@@ -163,38 +173,46 @@ __global__ __launch_bounds__(1024) void scan_setup_kernel(ScanProblem p) {
         }
         // offsets that fall can count more tiles than there are rows: those past the last row are not run
         if (n < p.N) p.base[n] = (int)min((long)before + sum[threadIdx.x] - tiles, p.rows);
-        before = (int)min((long)before + sum[1023], p.rows);
+        before = (int)min((long)before + sum[255], p.rows);
     }
     if (threadIdx.x == 0) p.base[p.N] = before;
 }
 
 // R: tokens per thread; 256 / R groups of 8 lanes, 8 channels a lane.
-template <typename TX, typename TH, int R, bool BLEND>
-__global__ __launch_bounds__(8 * kScanTokens / R) void scan_fwd_kernel(ScanProblem p) {
+template <typename TX, typename TH, int R, bool BLEND, bool NT>
+__global__ __launch_bounds__(8 * kScanTokens / R, 4) void scan_fwd_kernel(ScanProblem p) {
     constexpr int G = kScanTokens / R;
     __shared__ float2 maps[G][kScanChannels];
     __shared__ float enter[kScanChannels];
     __shared__ int ticket;
     const long rows = scan_rows(p);
-    long row;
-    int cb;
-    if (!scan_place(p, rows, row, cb, &ticket)) return;
-    const ScanTile tile = scan_tile(p, row, rows);
-    const int l = threadIdx.x & 7, grp = threadIdx.x >> 3;
-    const long c = (long)cb * kScanChannels + 8 * l;
-    const bool in = c < p.D;
-    const long t0 = (long)tile.t0 + grp * R;
-    const int mine = min(max(tile.len - grp * R, 0), R);   // this thread's tokens
-
+    const ScanPlace place = scan_place(p);
+    const int l = threadIdx.x & 7, grp = threadIdx.x >> 3, cb = place.cb;
+    const unsigned c = (unsigned)(cb * kScanChannels + 8 * l);
+    const bool in = c < (unsigned)p.D;
+    // offsets within a tile fit 32 bits (256 tokens of at most 2^20 channels); only x may lie further apart
+    const unsigned at0 = (unsigned)(grp * R) * p.D + c;
     Raw8<TX> xr[R];
     Raw8<float> gr[R];
+    const long row = draw_row(p, place, &ticket);
+    if (row >= rows) return;
+    const ScanTile tile = scan_tile(p, row, rows);
+    const long first = (long)tile.t0 * p.D;
+    const int mine = min(max(tile.len - grp * R, 0), R);   // this thread's tokens
+    // every thread loads: tokens past the end the last one again, channels past the end the first ones, put out of action below. (A branch
+    // around each load, and the compiler waits for it before the next.)
+    const unsigned cl = in ? c : 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         xr[i].zero();
         gr[i].zero();
-        if (in && i < mine) {
-            gr[i].load(p.g + (t0 + i) * p.D + c);
-            xr[i].load(static_cast<const TX*>(p.x) + (t0 + i) * p.x_row + c);
+    }
+    if (tile.len > 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int t = min(grp * R + i, tile.len - 1);
+            gr[i].load(p.g + first + ((unsigned)t * (unsigned)p.D + cl));
+            xr[i].load(static_cast<const TX*>(p.x) + (tile.t0 + t) * p.x_row + cl);
         }
     }
     float a[R][8], b[BLEND ? R : 1][8], A[8], H[8];
@@ -207,7 +225,8 @@ __global__ __launch_bounds__(8 * kScanTokens / R) void scan_fwd_kernel(ScanProbl
         xr[i].get(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float g = a[i][e];
+            const float g = i < mine ? a[i][e] : 0.f;
+            x[e] = i < mine ? x[e] : 0.f;
             a[i][e] = __expf(g);
             if constexpr (BLEND) {
                 x[e] *= one_minus_exp(g, a[i][e]);
@@ -222,8 +241,8 @@ __global__ __launch_bounds__(8 * kScanTokens / R) void scan_fwd_kernel(ScanProbl
     __syncthreads();
     if (threadIdx.x < kScanChannels) {
         const int ch = threadIdx.x;
-        const long col = (long)cb * kScanChannels + ch;
-        const bool real = col < p.D;
+        const unsigned col = (unsigned)(cb * kScanChannels + ch);
+        const bool real = col < (unsigned)p.D;
         float At = 1.f, Ht = 0.f;   // the map of the groups before each, in its place
 #pragma unroll 16
         for (int k = 0; k < G; ++k) {
@@ -245,6 +264,10 @@ __global__ __launch_bounds__(8 * kScanTokens / R) void scan_fwd_kernel(ScanProbl
         enter[ch] = h;
     }
     __syncthreads();
+    if constexpr (!BLEND) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) xr[i].hide();
+    }
     float h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -256,45 +279,50 @@ __global__ __launch_bounds__(8 * kScanTokens / R) void scan_fwd_kernel(ScanProbl
         float x[8];
         if constexpr (!BLEND) xr[i].get(x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = __fmaf_rn(a[i][e], h[e], BLEND ? b[i][e] : x[e]);
-        if (in && i < mine) store8<false>(static_cast<TH*>(p.h) + (t0 + i) * p.D + c, h);
+        for (int e = 0; e < 8; ++e) h[e] = __fmaf_rn(a[i][e], h[e], BLEND ? b[i][e] : i < mine ? x[e] : 0.f);
+        if (in && i < mine) store8<NT>(static_cast<TH*>(p.h) + first + (at0 + i * p.D), h);
     }
     // the state behind the sequence's last token (or the one it began with, where it has none)
     if (p.hT && in && tile.s == tile.last && (mine > 0 ? grp * R + mine == tile.len : grp == 0 && tile.len == 0))
         store8<false>(p.hT + (long)tile.n * p.D + c, h);
 }
 
-template <typename TX, typename TH, int R, bool BLEND>
-__global__ __launch_bounds__(8 * kScanTokens / R) void scan_bwd_kernel(ScanProblem p) {
+template <typename TX, typename TH, int R, bool BLEND, bool NT>
+__global__ __launch_bounds__(8 * kScanTokens / R, (BLEND && sizeof(TX) == 4) ? 2 : 4) void scan_bwd_kernel(ScanProblem p) {
     constexpr int G = kScanTokens / R;
     // of every group: A; H, then the state entering it; the gradient's part of its map, then that of the groups behind it; their A
     __shared__ float mA[G][kScanChannels], mH[G][kScanChannels], mE[G][kScanChannels], mS[G][kScanChannels];
     __shared__ float enter[kScanChannels];
     __shared__ int ticket;
     const long rows = scan_rows(p);
-    long row;
-    int cb;
-    if (!scan_place(p, rows, row, cb, &ticket)) return;
-    if (p.ticket) row = rows - 1 - row;   // the last tiles first
-    const ScanTile tile = scan_tile(p, row, rows);
-    const int l = threadIdx.x & 7, grp = threadIdx.x >> 3;
-    const long c = (long)cb * kScanChannels + 8 * l;
-    const bool in = c < p.D;
-    const long t0 = (long)tile.t0 + grp * R;
-    const int mine = min(max(tile.len - grp * R, 0), R);
-
+    const ScanPlace place = scan_place(p);
+    const int l = threadIdx.x & 7, grp = threadIdx.x >> 3, cb = place.cb;
+    const unsigned c = (unsigned)(cb * kScanChannels + 8 * l);
+    const bool in = c < (unsigned)p.D;
+    const unsigned at0 = (unsigned)(grp * R) * p.D + c;
     Raw8<TX> xr[R];
     Raw8<TH> dr[R];
     Raw8<float> gr[R];
+    const long row = rows - 1 - draw_row(p, place, &ticket);   // the last tiles first
+    if (row < 0) return;
+    const ScanTile tile = scan_tile(p, row, rows);
+    const long first = (long)tile.t0 * p.D;
+    const int mine = min(max(tile.len - grp * R, 0), R);
+    const unsigned cl = in ? c : 0;   // loads as in the forward pass
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         xr[i].zero();
         dr[i].zero();
         gr[i].zero();
-        if (in && i < mine) {
-            gr[i].load(p.g + (t0 + i) * p.D + c);
-            xr[i].load(static_cast<const TX*>(p.x) + (t0 + i) * p.x_row + c);
-            dr[i].load(static_cast<const TH*>(p.dh) + (t0 + i) * p.D + c);
+    }
+    if (tile.len > 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int t = min(grp * R + i, tile.len - 1);
+            const unsigned at = (unsigned)t * (unsigned)p.D + cl;
+            gr[i].load(p.g + first + at);
+            xr[i].load(static_cast<const TX*>(p.x) + (tile.t0 + t) * p.x_row + cl);
+            dr[i].load(static_cast<const TH*>(p.dh) + first + at);
         }
     }
     float a[R][8], keep[BLEND ? R : 1][8], A[8], H[8], E[8];
@@ -307,7 +335,8 @@ __global__ __launch_bounds__(8 * kScanTokens / R) void scan_bwd_kernel(ScanProbl
         xr[i].get(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float g = a[i][e];
+            const float g = i < mine ? a[i][e] : 0.f;
+            x[e] = i < mine ? x[e] : 0.f;
             a[i][e] = __expf(g);
             if constexpr (BLEND) {
                 keep[i][e] = one_minus_exp(g, a[i][e]);
@@ -322,7 +351,7 @@ __global__ __launch_bounds__(8 * kScanTokens / R) void scan_bwd_kernel(ScanProbl
         float d[8];
         dr[i].get(d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) E[e] = a[i][e] * (d[e] + E[e]);
+        for (int e = 0; e < 8; ++e) E[e] = a[i][e] * ((i < mine ? d[e] : 0.f) + E[e]);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -332,9 +361,9 @@ __global__ __launch_bounds__(8 * kScanTokens / R) void scan_bwd_kernel(ScanProbl
     }
     __syncthreads();
     const int wave = threadIdx.x >> 6, ch = threadIdx.x & 63;
-    const long col = (long)cb * kScanChannels + ch;
+    const unsigned col = (unsigned)(cb * kScanChannels + ch);
     if (wave == 0) {   // the states entering the groups
-        float h = col < p.D ? p.carries[row * p.D + col] : 0.f;
+        float h = col < (unsigned)p.D ? p.carries[row * p.D + col] : 0.f;
 #pragma unroll 16
         for (int k = 0; k < G; ++k) {
             const float m = mA[k][ch], q = mH[k][ch];
@@ -354,7 +383,7 @@ __global__ __launch_bounds__(8 * kScanTokens / R) void scan_bwd_kernel(ScanProbl
         const long at = row * p.ncb * kScanChannels + col;
         float d = 0.f;
         if (tile.s == tile.last) {
-            if (p.dhT && col < p.D) d = p.dhT[(long)tile.n * p.D + col];
+            if (p.dhT && col < (unsigned)p.D) d = p.dhT[(long)tile.n * p.D + col];
         } else {
             publish_map(p.agg + at, At, Et);
             d = enter_from(p, row, 1, tile.last - tile.s, col);
@@ -363,33 +392,40 @@ __global__ __launch_bounds__(8 * kScanTokens / R) void scan_bwd_kernel(ScanProbl
         enter[ch] = d;
     }
     __syncthreads();
-    float h[R][8];   // the state before each token
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        xr[i].hide();
+        dr[i].hide();
+    }
+    float h[R][8];   // the state before each token, blended less its x: what E is multiplied with for dg
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[0][e] = mH[grp][8 * l + e];
 #pragma unroll
-    for (int i = 0; i + 1 < R; ++i) {
+    for (int i = 0; i < R; ++i) {
         float x[8];
         xr[i].get(x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i + 1][e] = __fmaf_rn(a[i][e], h[i][e], BLEND ? keep[i][e] * x[e] : x[e]);
+        for (int e = 0; e < 8; ++e) {
+            if (i + 1 < R) h[i + 1][e] = __fmaf_rn(a[i][e], h[i][e], BLEND ? keep[i][e] * x[e] : x[e]);
+            if constexpr (BLEND) h[i][e] -= x[e];
+        }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) E[e] = __fmaf_rn(mS[grp][8 * l + e], enter[8 * l + e], mE[grp][8 * l + e]);
 #pragma unroll
     for (int i = R - 1; i >= 0; --i) {
-        float d[8], x[8], dg[8];
+        float d[8], dg[8];
         dr[i].get(d);
-        xr[i].get(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            d[e] += E[e];
+            d[e] = (i < mine ? d[e] : 0.f) + E[e];
             E[e] = a[i][e] * d[e];
-            dg[e] = E[e] * (BLEND ? h[i][e] - x[e] : h[i][e]);
+            dg[e] = E[e] * h[i][e];
             if constexpr (BLEND) d[e] *= keep[i][e];
         }
         if (in && i < mine) {
-            store8<false>(static_cast<TX*>(p.dx) + (t0 + i) * p.D + c, d);
-            store8<false>(p.dg + (t0 + i) * p.D + c, dg);
+            store8<NT>(static_cast<TX*>(p.dx) + first + (at0 + i * p.D), d);
+            store8<NT>(p.dg + first + (at0 + i * p.D), dg);
         }
     }
     if (p.dh0 && in && tile.s == 0 && grp == 0) store8<false>(p.dh0 + (long)tile.n * p.D + c, E);
@@ -458,7 +494,7 @@ ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen) {
     w.rows = varlen ? (long)N + tokens / kScanTokens : N * per;
     if (longest <= kScanTokens) return w;
     const size_t cells = (size_t)w.rows * ncb * kScanChannels;
-    w.off_base = 256;
+    w.off_base = ((size_t)kTicketWords * 4 * ncb + 255) / 256 * 256;
     w.off_agg = w.off_base + (varlen ? (((size_t)N + 1) * 4 + 255) / 256 * 256 : 0);
     w.off_pref = w.off_agg + cells * 8;
     w.total = w.off_pref + cells * 4;
@@ -469,24 +505,31 @@ ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen) {
 static hipError_t scan_setup(const ScanProblem& p, long& tiles, hipStream_t s) {
     tiles = (p.ticket ? p.rows : (long)p.N) * p.ncb;
     if (!p.ticket) return hipSuccess;
-    const long blocks = (p.rows * p.ncb * kScanChannels / 2 + 4095) / 4096;
-    return launch(scan_setup_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(1024), s, p);
+    const long blocks = (p.rows * p.ncb * kScanChannels / 2 + 511) / 512;   // two stores of 16 bytes a thread, and one
+    return launch(scan_setup_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), s, p);
 }
+
+// Outputs go past the caches where they exceed the L2s together.
+static bool scan_large(const ScanProblem& p) { return (long)p.tokens * p.D >= 1 << 23; }
+constexpr int R = 4;   // tokens per thread
 
 template <typename TX, typename TH, bool BLEND>
 static hipError_t scan_fwd(const ScanProblem& p, hipStream_t s) {
-    constexpr int R = BLEND || sizeof(TX) == 4 ? 4 : 8;
     long tiles;
     const hipError_t e = scan_setup(p, tiles, s);
     if (e != hipSuccess) return e;
-    return launch(scan_fwd_kernel<TX, TH, R, BLEND>, dim3((unsigned)tiles), dim3(8 * kScanTokens / R), s, p);
+    const dim3 grid((unsigned)tiles), block(8 * kScanTokens / R);
+    return scan_large(p) ? launch(scan_fwd_kernel<TX, TH, R, BLEND, true>, grid, block, s, p)
+                         : launch(scan_fwd_kernel<TX, TH, R, BLEND, false>, grid, block, s, p);
 }
 template <typename TX, typename TH, bool BLEND>
 static hipError_t scan_bwd(const ScanProblem& p, hipStream_t s) {
     long tiles;
     const hipError_t e = scan_setup(p, tiles, s);
     if (e != hipSuccess) return e;
-    return launch(scan_bwd_kernel<TX, TH, 4, BLEND>, dim3((unsigned)tiles), dim3(2 * kScanTokens), s, p);
+    const dim3 grid((unsigned)tiles), block(8 * kScanTokens / R);
+    return scan_large(p) ? launch(scan_bwd_kernel<TX, TH, R, BLEND, true>, grid, block, s, p)
+                         : launch(scan_bwd_kernel<TX, TH, R, BLEND, false>, grid, block, s, p);
 }
 template <typename TX, typename TH, bool BLEND>
 static hipError_t scan_update(const ScanProblem& p, hipStream_t s) {

@@ -96,8 +96,8 @@ def test_sizes():
     assert rows(2, 0, 2, False) == rows(2, 1, 2, False) == rows(2, 256, 2, False) == 2 and rows(2, 257, 2, False) == 4
     assert rows(1, 100, 7, True) == 7 and rows(1, 1000, 7, True) == 7 + 3 and rows(1, 100, 7, False) == 0
     assert ws(2, 256, 2, 64, False) == ws(1, 256, 9, 64, True) == 0
-    assert ws(2, 257, 2, 72, False) == 256 + 4 * 128 * 12
-    assert ws(1, 1000, 100, 64, True) == 256 + 512 + 103 * 64 * 12
+    assert ws(2, 257, 2, 72, False) == 256 + 4 * 128 * 12   # counters, then maps and states of 4 x 2 tiles of 64 channels
+    assert ws(1, 1000, 100, 328, True) == 512 + 512 + 103 * 384 * 12
     assert ws(1, 1000, 2, 60, True) == 0 and c_update(T=0, x=None, h=None) == 0 and c_update(T=0, N=0, cu=None, slots=None) == 0
 
 
