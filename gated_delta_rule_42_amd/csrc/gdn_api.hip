@@ -758,7 +758,7 @@ GDN_EXPORT int gdn_conv_fwd(const void* x, const float* weight, const float* bia
     if (x_stride < 0) return GDN_ERR_SHAPE;
     const int tokens = B * T;
     if ((tokens > 0 && (!x || !y)) || !weight) return GDN_ERR_NULL;
-    if (!all_aligned({x, weight, window0, y, windowT}, {bias, cu_seqlens}) || x_stride % per16(dtype)) return GDN_ERR_ALIGN;
+    if (!all_aligned({x, weight, bias, window0, y, windowT}, {cu_seqlens}) || x_stride % per16(dtype)) return GDN_ERR_ALIGN;
     hipStream_t s = static_cast<hipStream_t>(stream);
     st = debug_check_offsets(cu_seqlens, N, T, s, true);
     if (st != GDN_OK) return st;
@@ -771,7 +771,7 @@ GDN_EXPORT int gdn_conv_fwd(const void* x, const float* weight, const float* bia
 
 GDN_EXPORT size_t gdn_conv_bwd_workspace_bytes(int B, int T, int D, int width) {
     if (width < 2 || width > 4 || channel_shape(B, T, B, D, false) != GDN_OK) return 0;
-    return (size_t)gdn::conv_parts(B * T, D) * D * (width + 1) * sizeof(float);
+    return (size_t)gdn::conv_parts(B * T, D, width) * D * (width + 1) * sizeof(float);
 }
 
 GDN_EXPORT int gdn_conv_bwd(const void* x, const float* weight, const float* bias, const void* window0, const void* dy,
@@ -785,7 +785,7 @@ GDN_EXPORT int gdn_conv_bwd(const void* x, const float* weight, const float* bia
     // rows of dx must not lie over each other
     if (x_stride < 0 || dx_stride < 0 || (tokens > 1 && dx_stride < D)) return GDN_ERR_SHAPE;
     if ((tokens > 0 && (!x || !dy || !dx)) || !weight) return GDN_ERR_NULL;
-    if (!all_aligned({x, weight, window0, dy, dwindowT, dx, dwindow0}, {bias, cu_seqlens, dweight, dbias}) ||
+    if (!all_aligned({x, weight, bias, window0, dy, dwindowT, dx, dwindow0}, {cu_seqlens, dweight, dbias}) ||
         x_stride % per16(dtype) || dx_stride % per16(dtype))
         return GDN_ERR_ALIGN;
     if (dweight || dbias) {
@@ -814,7 +814,7 @@ GDN_EXPORT int gdn_conv_update(const void* x, const float* weight, const float* 
     if (x_stride < 0) return GDN_ERR_SHAPE;
     if (T == 0 || N == 0) return GDN_OK;   // no token: nothing to read or write
     if (!x || !weight || !slots || !y || (!windows && n_slots > 0)) return GDN_ERR_NULL;
-    if (!all_aligned({x, weight, windows, y}, {bias, slots, cu_seqlens, out_slots}) || x_stride % per16(dtype))
+    if (!all_aligned({x, weight, bias, windows, y}, {slots, cu_seqlens, out_slots}) || x_stride % per16(dtype))
         return GDN_ERR_ALIGN;
     hipStream_t s = static_cast<hipStream_t>(stream);
     st = debug_check_offsets(cu_seqlens, N, T, s, true);

@@ -57,7 +57,7 @@ struct ConvProblem {
     int tokens, T, N, D, W, n_slots;
     int bf16, silu;
 };
-int conv_parts(int tokens, int D);
+int conv_parts(int tokens, int D, int W);
 hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvProblem& p, hipStream_t s);
 hipError_t launch_conv_update(const ConvProblem& p, hipStream_t s);

@@ -16,11 +16,7 @@
 
 namespace gdn {
 
-template <typename T, int V> struct RawOf;
-template <typename T> struct RawOf<T, 8> { using type = Raw8<T>; };
-template <typename T> struct RawOf<T, 4> { using type = Raw4<T>; };
-template <bool NT, typename T> __device__ __forceinline__ void store_v(T* p, const float (&x)[8]) { store8<NT>(p, x); }
-template <bool NT, typename T> __device__ __forceinline__ void store_v(T* p, const float (&x)[4]) { store4c<NT>(p, x); }
+constexpr int V = 4;   // channels of a lane: 8 in bf16 halve the loads but cost a wave per SIMD (41 us against 46 forward, 12.4 against 13.7 on the pool)
 
 // Where token t stands: its sequence, its position there, the tokens from it to the sequence's end (0: no sequence covers it).
 struct Token {
@@ -57,7 +53,7 @@ struct TileTokens {
     int pos0;                                // the first token's position
     __device__ __forceinline__ TileTokens(const ConvProblem& p, long t0, int count, int* lds) {
         const int lane = threadIdx.x & 63;
-        const Token k = locate_token(p, lane < count && t0 + lane < p.tokens ? (int)(t0 + lane) : -1);
+        const Token k = locate_token(p, lane < count && t0 + lane < p.tokens ? (int)(t0 + lane) : -1);   // -1: none
         covered = __ballot(k.rem > 0);
         starts = __ballot(k.rem > 0 && k.pos == 0);
 #pragma unroll
@@ -71,7 +67,7 @@ struct TileTokens {
 };
 
 // A lane's taps, w[v][j] of its channels.
-template <int V, int W>
+template <int W>
 __device__ __forceinline__ void load_taps(const float* weight, long c, float (&w)[V][W]) {
     float f[V * W];
 #pragma unroll
@@ -85,19 +81,31 @@ __device__ __forceinline__ void load_taps(const float* weight, long c, float (&w
         for (int j = 0; j < W; ++j) w[v][j] = f[v * W + j];
 }
 
+__device__ __forceinline__ void load_bias(const float* bias, long c, float (&b)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) b[v] = 0.f;
+    if (bias) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(bias + c + v);
+            b[v] = a.x; b[v + 1] = a.y; b[v + 2] = a.z; b[v + 3] = a.w;
+        }
+    }
+}
+
 __device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // Row r of sequence n's window (zeros without one).
-template <typename T, int V, int W>
+template <typename T, int W>
 __device__ __forceinline__ void window_row(const ConvProblem& p, const void* window, int n, int r, long c, float (&x)[V]) {
-    typename RawOf<T, V>::type raw;
+    Raw4<T> raw;
     raw.zero();
     if (window) raw.load(static_cast<const T*>(window) + ((long)n * (W - 1) + r) * p.D + c);
     raw.get(x);
 }
 
 // The last W - 1 inputs of sequence n, as they lie in memory.
-template <typename T, int V, int W>
+template <typename T, int W>
 __device__ __forceinline__ void leave_window(const ConvProblem& p, int n, long c) {
     int b = n * p.T, e = b + p.T;
     if (p.cu_seqlens) {
@@ -108,7 +116,7 @@ __device__ __forceinline__ void leave_window(const ConvProblem& p, int n, long c
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {
         const int pos = len - (W - 1) + r;
-        typename RawOf<T, V>::type raw;
+        Raw4<T> raw;
         raw.zero();
         if (pos >= 0) raw.load(static_cast<const T*>(p.x) + (long)(b + pos) * p.x_row + c);
         else if (p.window0) raw.load(static_cast<const T*>(p.window0) + ((long)n * (W - 1) + r + len) * p.D + c);
@@ -116,64 +124,90 @@ __device__ __forceinline__ void leave_window(const ConvProblem& p, int n, long c
     }
 }
 
+// One token of the forward pass from the inputs u[0] .. u[W-1] tokens back.
+template <int W, bool SILU>
+__device__ __forceinline__ void conv_token(const float (&w)[V][W], const float (&b)[V], const float (&u)[W][V], float (&y)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float z = b[v];
+#pragma unroll
+        for (int j = W - 1; j >= 0; --j) z += w[v][W - 1 - j] * u[j][v];
+        y[v] = SILU ? z * sigmoid_f(z) : z;
+    }
+}
+template <int W>
+__device__ __forceinline__ void move_on(float (&u)[W][V]) {
+#pragma unroll
+    for (int j = W - 1; j > 0; --j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) u[j][v] = u[j - 1][v];
+}
+
 // Work-groups in rows of cblocks, which share tokens; those past the `tiles` rows of tiles leave the windows, a wave per sequence.
-template <typename T, int V, int W, int TL, bool NT>
+template <typename T, int W, int TL, bool SILU>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvProblem p, int cblocks, int tiles) {
-    using Raw = typename RawOf<T, V>::type;
+    using Raw = Raw4<T>;
     __shared__ int seq[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // scalar, and so are tokens and masks
     const int by = (int)(blockIdx.x / (unsigned)cblocks), bx = (int)(blockIdx.x - (unsigned)by * (unsigned)cblocks);
-    const long c = ((long)bx * 64 + lane) * V;
-    const bool in = c < p.D;
+    const long c0 = ((long)bx * 64 + lane) * V;
+    const bool in = c0 < p.D;
+    const long c = in ? c0 : 0;   // lanes past the channels go along with the first ones and store nothing
+    const unsigned cb = (unsigned)c * sizeof(T);
     if (by >= tiles) {
         const int n = (by - tiles) * 4 + wave;
-        if (n < p.N && in) leave_window<T, V, W>(p, n, c);
+        if (n < p.N && in) leave_window<T, W>(p, n, c);
         return;
     }
     const long first = ((long)by * 4 + wave) * TL;
     if (first >= p.tokens) return;
     const int t0 = (int)first;
-    const TileTokens<W> tok(p, t0, TL, seq[wave]);
-    if (!in) return;
+    // rows outside the tensor: the nearest one, for no token's sake. (A branch around each load, and the compiler waits for it
+    // before the next.)
     Raw raw[TL + W - 1];
 #pragma unroll
-    for (int i = 0; i < TL + W - 1; ++i) {
-        const int t = t0 - (W - 1) + i;
-        raw[i].zero();
-        if (t >= 0 && t < p.tokens) raw[i].load(static_cast<const T*>(p.x) + t * p.x_row + c);
-    }
+    for (int i = 0; i < TL + W - 1; ++i)
+        raw[i].load(at_byte(static_cast<const T*>(p.x) + (long)min(max(t0 - (W - 1) + i, 0), p.tokens - 1) * p.x_row, cb));
     float w[V][W], b[V];
-    load_taps<V, W>(p.weight, c, w);
+    load_taps<W>(p.weight, c, w);
+    load_bias(p.bias, c, b);
+    const TileTokens<W> tok(p, t0, TL, seq[wave]);
+    T* yp = static_cast<T*>(p.y) + (long)t0 * p.D;
+    float u[W][V], y[V];   // u[k]: the input k tokens back
 #pragma unroll
-    for (int v = 0; v < V; ++v) b[v] = p.bias ? p.bias[c + v] : 0.f;
-    float u[W][V];   // u[k]: the input k tokens back
+    for (int k = 1; k < W; ++k) raw[W - 1 - k].get(u[k]);
+    if (tok.covered == (1ull << TL) - 1 && tok.starts == 0 && tok.pos0 >= W - 1) {   // one sequence, away from its beginning
 #pragma unroll
-    for (int k = 1; k < W; ++k) {
-        if (tok.is(tok.covered, 0) && tok.pos0 < k) window_row<T, V, W>(p, p.window0, tok.seq[0], W - 1 - k + tok.pos0, c, u[k]);
-        else raw[W - 1 - k].get(u[k]);
+        for (int i = 0; i < TL; ++i) {
+            raw[i + W - 1].get(u[0]);
+            conv_token<W, SILU>(w, b, u, y);
+            if (in) store4c<false>(at_byte(yp + (long)i * p.D, cb), y);
+            move_on<W>(u);
+        }
+        return;
     }
+    // sequences begin or end here: token by token, rows read again (they are in the caches), in a loop that takes no registers from the
+    // way above
 #pragma unroll
-    for (int i = 0; i < TL; ++i) {
-        raw[i + W - 1].get(u[0]);
+    for (int k = 1; k < W; ++k)
+        if (tok.is(tok.covered, 0) && tok.pos0 < k) window_row<T, W>(p, p.window0, tok.seq[0], W - 1 - k + tok.pos0, c, u[k]);
+    const int count = min(TL, p.tokens - t0);
+    const T* xp = static_cast<const T*>(p.x) + (long)t0 * p.x_row;
+    Raw next;
+    next.load(at_byte(xp, cb));
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+        next.get(u[0]);
+        next.load(at_byte(xp + (long)min(i + 1, count - 1) * p.x_row, cb));
         if (tok.is(tok.covered, i)) {
             if (i > 0 && tok.is(tok.starts, i)) {
 #pragma unroll
-                for (int j = 1; j < W; ++j) window_row<T, V, W>(p, p.window0, tok.seq[i], W - 1 - j, c, u[j]);
+                for (int j = 1; j < W; ++j) window_row<T, W>(p, p.window0, tok.seq[i], W - 1 - j, c, u[j]);
             }
-            float y[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float z = b[v];
-#pragma unroll
-                for (int j = W - 1; j >= 0; --j) z += w[v][W - 1 - j] * u[j][v];
-                y[v] = p.silu ? z * sigmoid_f(z) : z;
-            }
-            store_v<NT>(static_cast<T*>(p.y) + (long)(t0 + i) * p.D + c, y);
+            conv_token<W, SILU>(w, b, u, y);
+            if (in) store4c<false>(at_byte(yp + (long)i * p.D, cb), y);
         }
-#pragma unroll
-        for (int j = W - 1; j > 0; --j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) u[j][v] = u[j - 1][v];
+        move_on<W>(u);
     }
 }
 
@@ -187,11 +221,12 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
         e0 = min(max(p.cu_seqlens[n + 1], b0), p.tokens);
     }
     const int len = e0 - b0;
-    float w[4][W], g[W - 1][4], u[2 * W - 2][4];
-    load_taps<4, W>(p.weight, c, w);
+    float w[4][W], b[4], g[W - 1][4], u[2 * W - 2][4];
+    load_taps<W>(p.weight, c, w);
+    load_bias(p.bias, c, b);
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {
-        window_row<T, 4, W>(p, p.window0, n, r, c, u[r]);
+        window_row<T, W>(p, p.window0, n, r, c, u[r]);
         Raw4<T> raw;
         raw.zero();
         if (r < len) raw.load(static_cast<const T*>(p.x) + (long)(b0 + r) * p.x_row + c);
@@ -209,7 +244,7 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 if (p.silu) {
-                    float z = p.bias ? p.bias[c + v] : 0.f;
+                    float z = b[v];
 #pragma unroll
                     for (int j = 0; j < W; ++j) z += w[v][j] * u[t + j][v];
                     const float s = sigmoid_f(z);
@@ -224,7 +259,7 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
     for (int r = 0; r < W - 1; ++r) {
         if (p.dwindowT && r >= len) {
             float d[4];
-            window_row<T, 4, W>(p, p.dwindowT, n, r - len, c, d);
+            window_row<T, W>(p, p.dwindowT, n, r - len, c, d);
 #pragma unroll
             for (int v = 0; v < 4; ++v) g[r][v] += d[v];
         }
@@ -232,127 +267,190 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
     }
 }
 
-constexpr int kConvBwdTokens = 16;   // tokens of a wave's tile
-
-// Rows of work-groups below `parts` walk the rows of tiles with that stride, sum their contributions to dw and db in
-// registers, then over their four waves in LDS, and write a partial row each [D, W], [D]; those past them take the
-// windows' gradients. No atomics: the same inputs give the same bits.
-template <typename T, int W, bool DW, bool NT>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblocks, int parts) {
-    constexpr int TL = kConvBwdTokens, ROWS = TL + W - 1;
+// Backward, a wave walks a run of tokens, blocks of BL at a time, the next block's rows in flight while the current one is worked on. It
+// carries the last W - 1 inputs and dz; a token's dx is complete W - 1 tokens later, so that a run goes W - 1 tokens past its end (where
+// its sequence does). Run lengths are multiples of BL less W - 1: whole blocks.
+//
+// Rows of work-groups below `parts` take four runs each, sum their contributions to dw and db in registers, then over the waves in
+// LDS, and write a partial row [D, W], [D]; those past them take the windows' gradients. No atomics: the same inputs give the same bits.
+constexpr int kConvBlock = 4;   // BL: with 8 in bf16 two waves fit a SIMD instead of three (packed 8054 x 6144: 85 us against 69)
+template <typename T, int W, bool SILU, bool DW>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblocks, int parts, int run) {
+    constexpr int BL = kConvBlock, H = W - 1;
     __shared__ float part[DW ? 4 : 1][DW ? 64 * 4 * (W + 1) : 1];
     __shared__ int seq[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // scalar, and so are tokens and masks
     const int by = (int)(blockIdx.x / (unsigned)cblocks), bx = (int)(blockIdx.x - (unsigned)by * (unsigned)cblocks);
-    const long c = ((long)bx * 64 + lane) * 4;
-    const bool in = c < p.D;
+    const long c0 = ((long)bx * 64 + lane) * 4;
+    const bool in = c0 < p.D;
+    const long c = in ? c0 : 0;   // lanes past the channels go along with the first ones and store nothing
+    const unsigned cb = (unsigned)c * sizeof(T);
     if (by >= parts) {
         const int n = (by - parts) * 4 + wave;
         if (n < p.N && in) window_gradient<T, W>(p, n, c);
         return;
     }
     float w[4][W], b[4], dw[4][W], db[4];
+    load_taps<W>(p.weight, c, w);
+    load_bias(p.bias, c, b);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-        b[v] = db[v] = 0.f;
+        db[v] = 0.f;
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[v][j] = dw[v][j] = 0.f;
+        for (int j = 0; j < W; ++j) dw[v][j] = 0.f;
     }
-    if (in) {
-        load_taps<4, W>(p.weight, c, w);
-        if (p.bias)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) b[v] = p.bias[c + v];
-    }
-    const long ntiles = ((long)p.tokens + TL - 1) / TL;
-    for (long tile = (long)by * 4 + wave; tile < ntiles; tile += (long)parts * 4) {
-        const int t0 = (int)(tile * TL);
-        const TileTokens<W> tok(p, t0, ROWS, seq[wave]);
-        if (!in) continue;
-        Raw4<T> xr[ROWS + W - 1], gr[ROWS];   // xr: tokens t0 - (W - 1) .., gr: tokens t0 ..
-#pragma unroll
-        for (int i = 0; i < ROWS + W - 1; ++i) {
-            const long t = (long)t0 - (W - 1) + i;
-            xr[i].zero();
-            if (t >= 0 && t < p.tokens) xr[i].load(static_cast<const T*>(p.x) + t * p.x_row + c);
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const long t = (long)t0 + i;
-            gr[i].zero();
-            if (t < p.tokens) gr[i].load(static_cast<const T*>(p.dy) + t * p.D + c);
-        }
+    const long begin = ((long)by * 4 + wave) * run;
+    if (begin < p.tokens) {
+        const int r0 = (int)begin, r1 = (int)min(begin + run, (long)p.tokens), last = p.tokens - 1;
+        const T* xp = static_cast<const T*>(p.x);
+        const T* gp = static_cast<const T*>(p.dy);
+        T* dxp = static_cast<T*>(p.dx);
         float u[W][4], dz[W][4];   // u[k]: the input k tokens back; dz[k]: k tokens back
+        Raw4<T> xr[BL], gr[BL], xn[BL], gn[BL];
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) dz[k][v] = 0.f;
+        for (int i = 0; i < BL; ++i) {   // rows past the tensor: the last one, for no token's sake
+            xr[i].load(at_byte(xp + (long)min(r0 + i, last) * p.x_row, cb));
+            gr[i].load(at_byte(gp + (long)min(r0 + i, last) * p.D, cb));
+        }
 #pragma unroll
         for (int k = 1; k < W; ++k) {
-            if (tok.is(tok.covered, 0) && tok.pos0 < k) window_row<T, 4, W>(p, p.window0, tok.seq[0], W - 1 - k + tok.pos0, c, u[k]);
-            else xr[W - 1 - k].get(u[k]);
+            Raw4<T> before;
+            before.load(at_byte(xp + (long)max(r0 - k, 0) * p.x_row, cb));
+            before.get(u[k]);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) dz[k][v] = 0.f;
         }
+        // the tokens base - H .. of masks and seq; every SPAN tokens they are looked up anew
+        constexpr int SPAN = (64 - H) / BL * BL;
+        int base = r0;
+        TileTokens<W> tok(p, (long)r0 - H, 64, seq[wave]);
+        if (tok.is(tok.covered, H)) {
+            const Token k = locate_token(p, r0);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-#pragma unroll
-            for (int j = W - 1; j > 0; --j)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) dz[j][v] = dz[j - 1][v];
-            xr[i + W - 1].get(u[0]);
-            // a token behind the tile matters only where the tile's last one belongs to the same sequence
-            if (tok.is(tok.covered, i) && (i < TL || !(tok.starts >> TL & ((2ull << (i - TL)) - 1)))) {
-                if (i > 0 && tok.is(tok.starts, i)) {
-#pragma unroll
-                    for (int j = 1; j < W; ++j) window_row<T, 4, W>(p, p.window0, tok.seq[i], W - 1 - j, c, u[j]);
-                }
-                gr[i].get(dz[0]);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    if (p.silu) {
-                        float z = b[v];
-#pragma unroll
-                        for (int j = W - 1; j >= 0; --j) z += w[v][W - 1 - j] * u[j][v];
-                        const float s = sigmoid_f(z);
-                        dz[0][v] *= s * (1.f + z * (1.f - s));
-                    }
-                    if (DW && i < TL) {
-                        db[v] += dz[0][v];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[v][W - 1 - j] += dz[0][v] * u[j][v];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) dz[0][v] = 0.f;
+            for (int j = 1; j < W; ++j)
+                if (k.pos < j) window_row<T, W>(p, p.window0, k.n, H - j + k.pos, c, u[j]);
+        }
+        for (int t0 = r0; t0 < r1 + H; t0 += BL) {
+            if (t0 - base == SPAN) {
+                base = t0;
+                tok = TileTokens<W>(p, (long)t0 - H, 64, seq[wave]);
             }
-            if (i >= W - 1) {   // the token W - 1 back has all of its terms: dz[W - 1] is its own, dz[W - 1 - m] that m tokens on
-                const int o = i - (W - 1);
-                if (tok.is(tok.covered, o)) {
-                    float dx[4];
-                    int rem = W;   // tokens of its sequence from it on, W for that or more
+            const int s = t0 - base, own = r1 - t0;   // tokens i < own are the run's own
 #pragma unroll
-                    for (int r = 0; r < W - 1; ++r)
-                        if (tok.is(tok.ends[r], o)) rem = r + 1;
+            for (int i = 0; i < BL; ++i) {
+                xn[i].load(at_byte(xp + (long)min(t0 + BL + i, last) * p.x_row, cb));
+                gn[i].load(at_byte(gp + (long)min(t0 + BL + i, last) * p.D, cb));
+            }
+            // bits: the H tokens before the block (before the run, whatever they are), then the block's
+            const unsigned all = (1u << (H + BL)) - 1, before = (1u << H) - 1;
+            const unsigned covered = (unsigned)(tok.covered >> s) | (t0 == r0 ? before : 0u);
+            const bool plain = (covered & all) == all && ((unsigned)(tok.starts >> (s + H)) & (all >> H)) == 0 &&
+                               ((unsigned)(tok.ends[0] >> s) & (all >> 1)) == 0 && own + H >= BL;
+            if (plain) {   // inside one sequence, its end no nearer than this block's: no token needs a look at the masks
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) dx[v] = w[v][W - 1] * dz[W - 1][v];
+                for (int i = 0; i < BL; ++i) {
+                    float d[4];
+                    xr[i].get(u[0]);
+                    gr[i].get(d);
+                    const float mine = i < own ? 1.f : 0.f;
 #pragma unroll
-                    for (int m = 1; m < W; ++m)
-                        if (m < rem)
+                    for (int v = 0; v < 4; ++v) {
+                        if constexpr (SILU) {
+                            float z = b[v];
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) dx[v] += w[v][W - 1 - m] * dz[W - 1 - m][v];
-                    if (p.dwindowT && rem < W) {
-                        float d[4];
-                        window_row<T, 4, W>(p, p.dwindowT, tok.seq[o], W - 1 - rem, c, d);
+                            for (int j = W - 1; j >= 0; --j) z += w[v][W - 1 - j] * u[j][v];
+                            const float sg = sigmoid_f(z);
+                            d[v] *= sg * (1.f + z * (1.f - sg));
+                        }
+                        dz[0][v] = d[v];
+                        if constexpr (DW) {
+                            const float dm = BL - i > H ? d[v] : d[v] * mine;
+                            db[v] += dm;
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) dx[v] += d[v];
+                            for (int j = 0; j < W; ++j) dw[v][W - 1 - j] += dm * u[j][v];
+                        }
                     }
-                    store4c<NT>(static_cast<T*>(p.dx) + (long)(t0 + i - (W - 1)) * p.dx_row + c, dx);
+                    if (i >= H || t0 > r0) {   // the token H back has all of its terms
+                        float dx[4];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            dx[v] = w[v][W - 1] * dz[W - 1][v];
+#pragma unroll
+                            for (int m = 1; m < W; ++m) dx[v] += w[v][W - 1 - m] * dz[W - 1 - m][v];
+                        }
+                        if (in) store4c<false>(at_byte(dxp + (long)(t0 + i - H) * p.dx_row, cb), dx);
+                    }
+                    move_on<W>(u);
+                    move_on<W>(dz);
+                }
+            } else {   // token by token, rows read again (they are in the caches), in a loop that takes no registers from the way above
+                Raw4<T> xt, gt;
+                xt.load(at_byte(xp + (long)min(t0, last) * p.x_row, cb));
+                gt.load(at_byte(gp + (long)min(t0, last) * p.D, cb));
+#pragma unroll 1
+                for (int i = 0; i < BL; ++i) {
+                    const int t = t0 + i, at = s + H + i;   // at: the token's bit
+                    float d[4];
+                    xt.get(u[0]);
+                    gt.get(d);
+                    xt.load(at_byte(xp + (long)min(t + 1, last) * p.x_row, cb));
+                    gt.load(at_byte(gp + (long)min(t + 1, last) * p.D, cb));
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) dz[0][v] = 0.f;
+                    // a token behind the run matters only where the run's last one belongs to the same sequence
+                    const bool reach = i < own || (t < r1 + H && !(tok.starts >> (at - (i - own)) & ((2ull << (i - own)) - 1)));
+                    if (tok.is(tok.covered, at) && reach) {
+                        if (t > r0 && tok.is(tok.starts, at)) {
+#pragma unroll
+                            for (int j = 1; j < W; ++j) window_row<T, W>(p, p.window0, tok.seq[at], H - j, c, u[j]);
+                        }
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            dz[0][v] = d[v];
+                            if constexpr (SILU) {
+                                float z = b[v];
+#pragma unroll
+                                for (int j = W - 1; j >= 0; --j) z += w[v][W - 1 - j] * u[j][v];
+                                const float sg = sigmoid_f(z);
+                                dz[0][v] *= sg * (1.f + z * (1.f - sg));
+                            }
+                            if (DW && i < own) {
+                                db[v] += dz[0][v];
+#pragma unroll
+                                for (int j = 0; j < W; ++j) dw[v][W - 1 - j] += dz[0][v] * u[j][v];
+                            }
+                        }
+                    }
+                    if (t - H >= r0 && t - H < r1 && tok.is(tok.covered, at - H)) {
+                        float dx[4];
+                        int rem = W;   // tokens of its sequence from it on, W for that or more
+#pragma unroll
+                        for (int r = 0; r < H; ++r)
+                            if (tok.is(tok.ends[r], at - H)) rem = r + 1;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) dx[v] = w[v][W - 1] * dz[W - 1][v];
+#pragma unroll
+                        for (int m = 1; m < W; ++m)
+                            if (m < rem)
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) dx[v] += w[v][W - 1 - m] * dz[W - 1 - m][v];
+                        if (p.dwindowT && rem < W) {
+                            float e[4];
+                            window_row<T, W>(p, p.dwindowT, tok.seq[at - H], H - rem, c, e);
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) dx[v] += e[v];
+                        }
+                        if (in) store4c<false>(at_byte(dxp + (long)(t - H) * p.dx_row, cb), dx);
+                    }
+                    move_on<W>(u);
+                    move_on<W>(dz);
                 }
             }
 #pragma unroll
-            for (int j = W - 1; j > 0; --j)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) u[j][v] = u[j - 1][v];
+            for (int i = 0; i < BL; ++i) {
+                xr[i] = xn[i];
+                gr[i] = gn[i];
+            }
         }
     }
     if constexpr (DW) {
@@ -378,9 +476,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
 
 // Runs of tokens on a pool of windows: a lane walks its sequence's tokens for V channels. The window stays as loaded, so its rows
 // are moved, never rounded. Tokens come four at a time.
-template <typename T, int V, int W>
+template <typename T, int W>
 __global__ __launch_bounds__(256) void conv_update_kernel(ConvProblem p, int cblocks) {
-    using Raw = typename RawOf<T, V>::type;
+    using Raw = Raw4<T>;
     const int n = blockIdx.x / cblocks;
     const long c = ((long)(blockIdx.x % cblocks) * 256 + threadIdx.x) * V;
     if (c >= p.D) return;
@@ -396,7 +494,7 @@ __global__ __launch_bounds__(256) void conv_update_kernel(ConvProblem p, int cbl
     if (slot < 0 || slot >= p.n_slots) {   // a padded entry: zeros for its tokens, no window touched
 #pragma unroll
         for (int v = 0; v < V; ++v) y[v] = 0.f;
-        for (int t = t0; t < t1; ++t) store_v<false>(yp + (long)t * p.D, y);
+        for (int t = t0; t < t1; ++t) store4c<false>(yp + (long)t * p.D, y);
         return;
     }
     T* pool = static_cast<T*>(p.pool) + c;
@@ -405,9 +503,8 @@ __global__ __launch_bounds__(256) void conv_update_kernel(ConvProblem p, int cbl
 #pragma unroll
     for (int k = 1; k < W; ++k) u[k].load(pool + slot * slot_size + (long)(W - 1 - k) * p.D);
     float w[V][W], b[V];
-    load_taps<V, W>(p.weight, c, w);
-#pragma unroll
-    for (int v = 0; v < V; ++v) b[v] = p.bias ? p.bias[c + v] : 0.f;
+    load_taps<W>(p.weight, c, w);
+    load_bias(p.bias, c, b);
     constexpr int TB = 4;
     for (int tb = t0; tb < t1; tb += TB) {
         Raw x[TB];
@@ -428,7 +525,7 @@ __global__ __launch_bounds__(256) void conv_update_kernel(ConvProblem p, int cbl
                     for (int j = W - 1; j >= 0; --j) z += w[v][W - 1 - j] * f[j][v];
                     y[v] = p.silu ? z * sigmoid_f(z) : z;
                 }
-                store_v<false>(yp + (long)t * p.D, y);
+                store4c<false>(yp + (long)t * p.D, y);
 #pragma unroll
                 for (int k = W - 1; k > 0; --k) u[k] = u[k - 1];
                 if (p.out_slots) {
@@ -453,64 +550,72 @@ static hipError_t conv_taps(int W, F f) {
     return f(std::integral_constant<int, 4>{});
 }
 
-template <typename T, int V>
+template <typename T>
 static hipError_t conv_fwd(const ConvProblem& p, hipStream_t s) {
     return conv_taps(p.W, [&](auto taps) {
-        constexpr int W = decltype(taps)::value, TL = 16;
+        constexpr int W = decltype(taps)::value, TL = 12;
         const int tiles = (int)(((long)p.tokens + 4 * TL - 1) / (4 * TL));
         const int cblocks = (p.D + 64 * V - 1) / (64 * V);
         const long groups = (long)cblocks * (tiles + (p.windowT ? (p.N + 3) / 4 : 0));
         if (groups == 0) return hipSuccess;
-        return launch(conv_fwd_kernel<T, V, W, TL, false>, dim3((unsigned)groups), dim3(256), s, p, cblocks, tiles);
+        const dim3 grid((unsigned)groups), block(256);
+        if (p.silu) return launch(conv_fwd_kernel<T, W, TL, true>, grid, block, s, p, cblocks, tiles);
+        return launch(conv_fwd_kernel<T, W, TL, false>, grid, block, s, p, cblocks, tiles);
     });
 }
 
 hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t s) {
-    return p.bf16 ? conv_fwd<uint16_t, 8>(p, s) : conv_fwd<float, 4>(p, s);
+    return p.bf16 ? conv_fwd<uint16_t>(p, s) : conv_fwd<float>(p, s);
 }
 
-// Rows of work-groups (and partial rows) of the backward pass: enough to fill the device, but no more than there are rows
-// of tiles.
-int conv_parts(int tokens, int D) {
-    const long rows = ((long)tokens + 4 * kConvBwdTokens - 1) / (4 * kConvBwdTokens);
-    const long cblocks = (D + 255) / 256, want = (768 + cblocks - 1) / cblocks;
-    const long cap = rows < want ? rows : want;
-    return (int)(cap < kMaxParts ? cap : kMaxParts);
+// Tokens of a run of the backward pass: as many waves as the device holds at once (three a SIMD, in fp32 two), whole blocks less W - 1, four
+// blocks at least (so that few tokens still spread).
+static int conv_run(int tokens, int D, int W, int bf16) {
+    const long cblocks = (D + 255) / 256, most = 4L * kMaxParts;   // at most kMaxParts rows of four runs
+    long waves = ((bf16 ? 3072 : 2048) + cblocks - 1) / cblocks;
+    waves = waves < most ? waves : most;
+    const long len = (tokens + waves - 1) / waves, blocks = (len + W - 1 + kConvBlock - 1) / kConvBlock;
+    return (int)((blocks > 4 ? blocks : 4) * kConvBlock - (W - 1));
 }
+static int conv_rows(int tokens, int run) { return (int)(((long)tokens + 4L * run - 1) / (4L * run)); }
+// Rows of partial sums of the backward pass (of bf16 calls; fp32 ones have no more).
+int conv_parts(int tokens, int D, int W) { return conv_rows(tokens, conv_run(tokens, D, W, 1)); }
 
-template <typename T>
+template <typename T, int W, bool SILU>
 static hipError_t conv_bwd(const ConvProblem& p, hipStream_t s) {
+    const bool dw = p.dweight || p.dbias;
+    const int run = conv_run(p.tokens, p.D, W, p.bf16), parts = conv_rows(p.tokens, run), cblocks = (p.D + 255) / 256;
+    const long groups = (long)cblocks * (parts + (p.dwindow0 ? (p.N + 3) / 4 : 0));
+    if (groups > 0) {
+        const dim3 grid((unsigned)groups), block(256);
+        const hipError_t e = dw ? launch(conv_bwd_kernel<T, W, SILU, true>, grid, block, s, p, cblocks, parts, run)
+                                : launch(conv_bwd_kernel<T, W, SILU, false>, grid, block, s, p, cblocks, parts, run);
+        if (e != hipSuccess) return e;
+    }
+    if (!dw) return hipSuccess;
+    return launch_column_sum(p.partial, parts, (long)p.D * W, p.D, p.dweight, p.dbias, s);
+}
+
+hipError_t launch_conv_bwd(const ConvProblem& p, hipStream_t s) {
     return conv_taps(p.W, [&](auto taps) {
         constexpr int W = decltype(taps)::value;
-        const bool dw = p.dweight || p.dbias;
-        const int parts = conv_parts(p.tokens, p.D);
-        const int cblocks = (p.D + 255) / 256;
-        const long groups = (long)cblocks * (parts + (p.dwindow0 ? (p.N + 3) / 4 : 0));
-        if (groups > 0) {
-            const dim3 grid((unsigned)groups);
-            const hipError_t e = dw ? launch(conv_bwd_kernel<T, W, true, false>, grid, dim3(256), s, p, cblocks, parts)
-                                    : launch(conv_bwd_kernel<T, W, false, false>, grid, dim3(256), s, p, cblocks, parts);
-            if (e != hipSuccess) return e;
-        }
-        if (!dw) return hipSuccess;
-        return launch_column_sum(p.partial, parts, (long)p.D * W, p.D, p.dweight, p.dbias, s);
+        if (p.bf16) return p.silu ? conv_bwd<uint16_t, W, true>(p, s) : conv_bwd<uint16_t, W, false>(p, s);
+        return p.silu ? conv_bwd<float, W, true>(p, s) : conv_bwd<float, W, false>(p, s);
     });
 }
 
-hipError_t launch_conv_bwd(const ConvProblem& p, hipStream_t s) { return p.bf16 ? conv_bwd<uint16_t>(p, s) : conv_bwd<float>(p, s); }
-
-template <typename T, int V>
+template <typename T>
 static hipError_t conv_update(const ConvProblem& p, hipStream_t s) {
     return conv_taps(p.W, [&](auto taps) {
         constexpr int W = decltype(taps)::value;
         const int cblocks = (p.D + 256 * V - 1) / (256 * V);
-        return launch(conv_update_kernel<T, V, W>, dim3((unsigned)((long)p.N * cblocks)), dim3(256), s, p, cblocks);
+        return launch(conv_update_kernel<T, W>, dim3((unsigned)((long)p.N * cblocks)), dim3(256), s, p, cblocks);
     });
 }
 
 hipError_t launch_conv_update(const ConvProblem& p, hipStream_t s) {
     if (p.N == 0 || p.tokens == 0) return hipSuccess;
-    return p.bf16 ? conv_update<uint16_t, 8>(p, s) : conv_update<float, 4>(p, s);
+    return p.bf16 ? conv_update<uint16_t>(p, s) : conv_update<float>(p, s);
 }
 
 }  // namespace gdn

@@ -57,7 +57,7 @@ struct RowSums {
 // Threads of a forward work-group: four waves, or a row's eight.
 constexpr int ln_fwd_threads(int L) { return L > 256 ? L : 256; }
 
-template <typename TX, typename TS, typename TY, int L, int P, bool NT>
+template <typename TX, typename TS, typename TY, int L, int P>
 __global__ __launch_bounds__(ln_fwd_threads(L)) void layer_norm_fwd_kernel(LayerNormProblem p) {
     __shared__ float red[RowSums<L>::RED];
     RowSums<L> rs(red);
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(ln_fwd_threads(L)) void layer_norm_fwd_kernel(Layer
             rr[j].get(t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j][e] = to_f32(from_f32<TS>(v[j][e] + t[e]));
-            if (ok && c < p.d) store8<NT>(static_cast<TS*>(p.sum) + row * p.d + c, v[j]);
+            if (ok && c < p.d) store8<false>(static_cast<TS*>(p.sum) + row * p.d + c, v[j]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum += v[j][e];
@@ -127,17 +127,20 @@ __global__ __launch_bounds__(ln_fwd_threads(L)) void layer_norm_fwd_kernel(Layer
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * r * w[e] + b[e];
-            store8<NT>(static_cast<TY*>(p.y) + row * p.d + c, v[j]);
+            store8<false>(static_cast<TY*>(p.y) + row * p.d + c, v[j]);
         }
     }
 }
 
-constexpr int kLnBwdThreads = 512;
+constexpr int kLnBwdThreads = 512;   // eight waves
 
+// Rows stay as loaded and are unpacked again for each of the three passes over them (two sums each, then the outputs), which leaves room
+// for a lane's weights and sums in registers. Weights read again for every row and pass went through the vector cache at more bytes than the
+// rows themselves: 8192 x 2048 38.8 us a call, 32.6 with them in registers; rows loaded one ahead then gain nothing (33.7).
 // DW: the gradients of weight and bias too. The grid is then layer_norm_parts work-groups, each of which walks its rows with a
 // fixed stride, sums their contributions in registers, then over its row groups in LDS, and writes one partial row
 // [2, d] (weight, bias). No atomics: the same inputs give the same bits.
-template <typename TS, typename TY, int L, int P, bool DW, bool NT>
+template <typename TS, typename TY, int L, int P, bool DW>
 __global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LayerNormProblem p) {
     constexpr int RG = kLnBwdThreads / L;
     __shared__ float red[RG * RowSums<L>::RED];
@@ -152,47 +155,54 @@ __global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LayerNorm
 #pragma unroll
             for (int e = 0; e < 8; ++e) aw[j][e] = ab[j][e] = 0.f;
     }
+    float w[P][8];
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[j][e] = 1.f;
+    if (p.weight) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const int c = 8 * (l + L * j);
+            Raw8<float> r;
+            r.load(p.weight + (c < p.d ? c : 0));
+            r.get(w[j]);
+        }
+    }
     for (long row0 = (long)blockIdx.x * RG; row0 < p.rows; row0 += (long)gridDim.x * RG) {
-        const long row = row0 + grp;
+        const long row = row0 + grp, rl = min(row, p.rows - 1);
         const bool ok = row < p.rows;
+        // rows and channels past the end load the last row, the first channels, and are put out of action below
         Raw8<TS> xr[P], tr[P];
         Raw8<TY> gr[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            const int c = 8 * (l + L * j);
-            xr[j].zero();
-            gr[j].zero();
-            if (ok && c < p.d) {
-                xr[j].load(static_cast<const TS*>(p.x) + row * p.x_row + c);
-                gr[j].load(static_cast<const TY*>(p.dy) + row * p.d + c);
-            }
+            const int c = 8 * (l + L * j), cl = c < p.d ? c : 0;
+            xr[j].load(static_cast<const TS*>(p.x) + rl * p.x_row + cl);
+            gr[j].load(static_cast<const TY*>(p.dy) + rl * p.d + cl);
+            tr[j].zero();
         }
         if (p.dsum) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const int c = 8 * (l + L * j);
-                if (ok && c < p.d) tr[j].load(static_cast<const TS*>(p.dsum) + row * p.d + c);
+                const int c = 8 * (l + L * j), cl = c < p.d ? c : 0;
+                tr[j].load(static_cast<const TS*>(p.dsum) + rl * p.d + cl);
             }
         }
-        float v[P][8], g[P][8], sum = 0.f, gsum = 0.f;
+        float sum = 0.f, gsum = 0.f;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             const int c = 8 * (l + L * j);
-            xr[j].get(v[j]);
-            gr[j].get(g[j]);
-            float w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 1.f;
-            if (p.weight && c < p.d) {
-                Raw8<float> wr;
-                wr.load(p.weight + c);
-                wr.get(w);
-            }
+            float x[8], g[8];
+            xr[j].get(x);
+            gr[j].get(g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                sum += v[j][e];
-                gsum += g[j][e] * w[e];
+                sum += c < p.d ? x[e] : 0.f;
+                gsum += c < p.d ? g[e] * w[j][e] : 0.f;
             }
+            xr[j].hide();
+            gr[j].hide();
         }
         rs.sum2(sum, gsum);
         const float mean = sum * inv_d, gm = gsum * inv_d;
@@ -200,45 +210,37 @@ __global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LayerNorm
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             const int c = 8 * (l + L * j);
-            float w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 1.f;
-            if (p.weight && c < p.d) {
-                Raw8<float> wr;
-                wr.load(p.weight + c);
-                wr.get(w);
-            }
+            float x[8], g[8];
+            xr[j].get(x);
+            gr[j].get(g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[j][e] = c < p.d ? v[j][e] - mean : 0.f;
-                sq += v[j][e] * v[j][e];
-                gx += g[j][e] * w[e] * v[j][e];
+                const float v = c < p.d ? x[e] - mean : 0.f;
+                sq += v * v;
+                gx += c < p.d ? g[e] * w[j][e] * v : 0.f;
             }
+            xr[j].hide();
+            gr[j].hide();
         }
         rs.sum2(sq, gx);
         const float r = 1.f / sqrtf(sq * inv_d + p.eps), k = gx * r * inv_d;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             const int c = 8 * (l + L * j);
-            float w[8], t[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 1.f, t[e] = 0.f;
-            if (p.weight && c < p.d) {
-                Raw8<float> wr;
-                wr.load(p.weight + c);
-                wr.get(w);
-            }
-            if (p.dsum && ok && c < p.d) tr[j].get(t);
+            float x[8], g[8], t[8];
+            xr[j].get(x);
+            gr[j].get(g);
+            tr[j].get(t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float xh = v[j][e] * r;
-                if constexpr (DW) {   // rows past the end hold zeros
-                    aw[j][e] += g[j][e] * xh;
-                    ab[j][e] += g[j][e];
+                const float xh = (x[e] - mean) * r;
+                if constexpr (DW) {
+                    aw[j][e] += ok ? g[e] * xh : 0.f;
+                    ab[j][e] += ok ? g[e] : 0.f;
                 }
-                t[e] += r * (g[j][e] * w[e] - gm - xh * k);
+                t[e] += r * (g[e] * w[j][e] - gm - xh * k);
             }
-            if (ok && c < p.d) store8<NT>(static_cast<TS*>(p.dx) + row * p.d + c, t);
+            if (ok && c < p.d) store8<false>(static_cast<TS*>(p.dx) + row * p.d + c, t);
         }
     }
     if constexpr (DW) {
@@ -263,23 +265,26 @@ __global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LayerNorm
     }
 }
 
-// A work-group per 16 columns: 16 lanes across them and 64 down the rows, joined in LDS.
+// A work-group per C columns: C lanes across them and 1024 / C down the rows, joined in LDS. Few columns take 16, for more work-groups
+// (4096 columns of 256 rows 4.0 us), many take 64, for whole cache lines.
+template <int C>
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int nparts, long n0, long n1, float* out0, float* out1) {
-    __shared__ float sum[64][17];
-    const int lc = threadIdx.x & 15, lr = threadIdx.x >> 4;
-    const long n = n0 + n1, c = (long)blockIdx.x * 16 + lc;
-    float x[kMaxParts / 64], a = 0.f;
+    constexpr int R = 1024 / C;
+    __shared__ float sum[R][C + 1];
+    const int lc = threadIdx.x % C, lr = threadIdx.x / C;
+    const long n = n0 + n1, c = (long)blockIdx.x * C + lc, at = min(c, n - 1);
+    float a = 0.f;
+    for (int i0 = lr; i0 < nparts; i0 += 8 * R) {   // eight rows at a time in flight
+        float x[8];
 #pragma unroll
-    for (int j = 0; j < kMaxParts / 64; ++j) {
-        const int i = lr + 64 * j;
-        x[j] = i < nparts && c < n ? partial[(long)i * n + c] : 0.f;
+        for (int j = 0; j < 8; ++j) x[j] = partial[(long)min(i0 + R * j, nparts - 1) * n + at];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a += i0 + R * j < nparts ? x[j] : 0.f;
     }
-#pragma unroll
-    for (int j = 0; j < kMaxParts / 64; ++j) a += x[j];
     sum[lr][lc] = a;
     __syncthreads();
 #pragma unroll
-    for (int m = 32; m > 0; m /= 2) {
+    for (int m = R / 2; m > 0; m /= 2) {
         if (lr < m) sum[lr][lc] += sum[lr + m][lc];
         __syncthreads();
     }
@@ -293,7 +298,9 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, 
 }
 
 hipError_t launch_column_sum(const float* partial, int nparts, long n0, long n1, float* out0, float* out1, hipStream_t s) {
-    return launch(column_sum_kernel, dim3((unsigned)((n0 + n1 + 15) / 16)), dim3(1024), s, partial, nparts, n0, n1, out0, out1);
+    const long n = n0 + n1;
+    if (n < 16384) return launch(column_sum_kernel<16>, dim3((unsigned)((n + 15) / 16)), dim3(1024), s, partial, nparts, n0, n1, out0, out1);
+    return launch(column_sum_kernel<64>, dim3((unsigned)((n + 63) / 64)), dim3(1024), s, partial, nparts, n0, n1, out0, out1);
 }
 
 // Lanes of a row and pieces per lane.
@@ -308,14 +315,12 @@ static hipError_t ln_shape(int d, F f) {
     if (d <= 8192) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
     return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
 }
-static int ln_lanes(int d) { return d <= 128 ? 16 : d <= 256 ? 32 : d <= 2048 ? 64 : d <= 8192 ? 256 : 512; }
-
 template <typename TX, typename TS, typename TY>
 static hipError_t ln_fwd(const LayerNormProblem& p, hipStream_t s) {
     return ln_shape(p.d, [&](auto lanes, auto pieces) {
         constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value;
         constexpr int NT = ln_fwd_threads(L), RG = NT / L;
-        return launch(layer_norm_fwd_kernel<TX, TS, TY, L, P, false>, dim3((unsigned)((p.rows + RG - 1) / RG)), dim3(NT), s, p);
+        return launch(layer_norm_fwd_kernel<TX, TS, TY, L, P>, dim3((unsigned)((p.rows + RG - 1) / RG)), dim3(NT), s, p);
     });
 }
 
@@ -325,6 +330,8 @@ hipError_t launch_layer_norm_fwd(const LayerNormProblem& p, hipStream_t s) {
     if (p.s_bf16) return p.y_bf16 ? ln_fwd<uint16_t, uint16_t, uint16_t>(p, s) : ln_fwd<uint16_t, uint16_t, float>(p, s);
     return p.y_bf16 ? ln_fwd<uint16_t, float, uint16_t>(p, s) : ln_fwd<uint16_t, float, float>(p, s);
 }
+
+static int ln_lanes(int d) { return d <= 128 ? 16 : d <= 256 ? 32 : d <= 2048 ? 64 : d <= 8192 ? 256 : 512; }
 
 // Work-groups (and partial rows) of the backward pass with gradients of weight and bias: one per CU, but no more than there
 // are groups of rows.
@@ -337,15 +344,15 @@ int layer_norm_parts(long rows, int d) {
 template <typename TS, typename TY>
 static hipError_t ln_bwd(const LayerNormProblem& p, hipStream_t s) {
     return ln_shape(p.d, [&](auto lanes, auto pieces) {
-        constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value;
+        constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value, RG = kLnBwdThreads / L;
         if (!p.dweight && !p.dbias) {
             if (p.rows == 0) return hipSuccess;
-            const dim3 grid((unsigned)((p.rows + kLnBwdThreads / L - 1) / (kLnBwdThreads / L)));
-            return launch(layer_norm_bwd_kernel<TS, TY, L, P, false, false>, grid, dim3(kLnBwdThreads), s, p);
+            const long groups = (p.rows + RG - 1) / RG;
+            return launch(layer_norm_bwd_kernel<TS, TY, L, P, false>, dim3((unsigned)groups), dim3(kLnBwdThreads), s, p);
         }
         const int parts = layer_norm_parts(p.rows, p.d);
         if (parts > 0) {
-            const hipError_t e = launch(layer_norm_bwd_kernel<TS, TY, L, P, true, false>, dim3((unsigned)parts), dim3(kLnBwdThreads), s, p);
+            const hipError_t e = launch(layer_norm_bwd_kernel<TS, TY, L, P, true>, dim3((unsigned)parts), dim3(kLnBwdThreads), s, p);
             if (e != hipSuccess) return e;
         }
         return launch_column_sum(p.partial, parts, p.d, p.d, p.dweight, p.dbias, s);

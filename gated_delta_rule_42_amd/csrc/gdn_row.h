@@ -80,6 +80,15 @@ __device__ __forceinline__ void store4c(uint16_t* p, const float (&x)[4]) {
     store_piece<NT>(p, u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])});
 }
 
+// A row at a scalar address (the same in every lane) and a lane's byte offset in it: the empty asm keeps the compiler from adding the two
+// parts the other way round, which costs a pair of registers and an addition a load.
+typedef __attribute__((address_space(1))) char* global_char_ptr;
+template <typename T> __device__ __forceinline__ T* at_byte(T* row, unsigned byte) {
+    uint64_t r = reinterpret_cast<uint64_t>(row);
+    asm("" : "+s"(r));
+    return (T*)((global_char_ptr)r + byte);
+}
+
 // Sum over groups of G lanes, in every lane.
 template <int G>
 __device__ __forceinline__ float row_sum(float x) {

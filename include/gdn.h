@@ -521,8 +521,8 @@ int gdn_layer_norm_bwd(const void *sum, const void *dy, const void *dsum, const 
  *   y           [B, T, D] dtype, dense; windowT [N, W-1, D] dtype: the last W-1 inputs of each sequence (of its window where it
  *               is shorter), or NULL. Neither may overlap an input
  *   D           a multiple of 8 up to 2^20; B * T <= 2^28, B * T * D <= 2^36, N <= 2^24, N * D <= 2^31
- * Offsets outside [0, T] are clamped; rows of y that no sequence covers are left as they were. Pointers (bias: 4 bytes) and
- * strides are multiples of 16 bytes. Arithmetic is fp32.
+ * Offsets outside [0, T] are clamped; rows of y that no sequence covers are left as they were. Pointers (cu_seqlens and the
+ * gradients of weight and bias: 4 bytes) and strides are multiples of 16 bytes. Arithmetic is fp32.
  */
 typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
 int gdn_conv_fwd(const void *x, const float *weight, const float *bias, const void *window0,
