@@ -225,19 +225,26 @@ def test_against_oracle(B, T, cu, D, W, dtype, silu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,W", [(520, 4), (8200, 4), (8200, 2), (8200, 3)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_many_tiles(dtype):
-    """More tiles than rows of work-groups, long and short sequences."""
-    D, W = 520, 4
-    cu = [0, 700, 703, 703, 2900, 3001, 7001]
-    print(f"[gpu] conv packed {cu} D={D} {dtype}", flush=True)
-    x = make(77, 1, 7001, 6, D, W, dtype)
+def test_many_tiles(D, W, dtype):
+    """More tiles than waves, or runs of so many tokens that what is known of them is looked up anew within a run; long sequences beside
+    stretches of short ones, which begin and end at every place of a block."""
+    gen = torch.Generator().manual_seed(D + W)
+    lens = [700, 3, 0, 2197] + torch.randint(0, 40, (60,), generator=gen).tolist() + [101] + torch.randint(60, 70, (20,), generator=gen).tolist() + [1, 2500]
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    T, N = cu[-1] + 2, len(lens)   # two rows behind the last sequence
+    print(f"[gpu] conv packed {N} sequences, {T} tokens, D={D} W={W} {dtype}", flush=True)
+    x = make(77, 1, T, N, D, W, dtype)
     t = {n: a.cuda() for n, a in x.items()}
     cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
     y, wT = gb.gdn_conv_fwd(t["x"], t["w"], t["b"], t["w0"], cut, activation="silu")
-    keep = slice(0, 16)   # channels are independent of each other; the oracle takes some from each end
-    g = gb.gdn_conv_bwd(t["x"], t["w"], t["dy"], t["b"], t["w0"], t["dwT"], cut, activation="silu")
-    for keep in (slice(0, 8), slice(512, 520)):
+    dx = torch.full_like(t["x"], 7.0)
+    g = gb.gdn_conv_bwd(t["x"], t["w"], t["dy"], t["b"], t["w0"], t["dwT"], cut, activation="silu", dx=dx)
+    assert (dx[:, cu[-1]:] == 7).all()
+    only = gb.gdn_conv_bwd(t["x"], t["w"], t["dy"], t["b"], t["w0"], t["dwT"], cut, activation="silu", need_dw=False, dx=torch.full_like(dx, 7.0))
+    assert torch.equal(only[0], dx) and torch.equal(only[3], g[3])
+    for keep in (slice(0, 4), slice(256, 260), slice(D - 4, D)):   # channels are independent of each other
         s = {n: (a[keep] if n in ("w", "b") else a[..., keep]) for n, a in x.items()}
         check_fwd(s["x"], s["w"], s["b"], s["w0"], cu, True, y[..., keep], wT[..., keep])
         check_bwd(s["x"], s["w"], s["b"], s["w0"], s["dy"], s["dwT"], cu, True, g[0][..., keep], g[1][keep], g[2][keep], g[3][..., keep])
