@@ -850,7 +850,7 @@ int check_scan(const void* x, const float* g, const int32_t* cu, int B, int T, i
     if (w.total > 0 && (!ws || ws_bytes < w.total)) return GDN_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return GDN_ERR_ALIGN;
     gdn::ScanProblem& P = *p;
-    P.x = x; P.g = g; P.cu_seqlens = cu; P.x_row = x_stride; P.rows = w.rows;
+    P.x = x; P.g = g; P.cu_seqlens = cu; P.x_row = x_stride; P.rows = w.rows; P.tile = w.tile;
     P.tokens = tokens; P.T = T; P.N = N; P.D = D; P.ncb = (D + gdn::kScanChannels - 1) / gdn::kScanChannels;
     P.bf16 = dtype == GDN_BF16; P.h_bf16 = h_dtype == GDN_BF16; P.blend = blend != 0;
     if (w.total > 0) {

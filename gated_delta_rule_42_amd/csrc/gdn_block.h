@@ -62,9 +62,9 @@ hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvProblem& p, hipStream_t s);
 hipError_t launch_conv_update(const ConvProblem& p, hipStream_t s);
 
-// Gated linear recurrence per channel (gdn_scan.hip). A sequence is cut into tiles of kScanTokens tokens (one at least); row r of
+// Gated linear recurrence per channel (gdn_scan.hip). A sequence is cut into tiles of `tile` tokens (one tile at least); row r of
 // the tiles is tile s of sequence n, r = base[n] + s.
-constexpr int kScanTokens = 256, kScanChannels = 64;
+constexpr int kScanChannels = 64;
 struct ScanProblem {
     const void* x;               // [tokens, D], token stride x_row
     const float* g;              // [tokens, D], dense
@@ -87,11 +87,12 @@ struct ScanProblem {
     uint64_t* agg;               // [rows, 64 ncb] a tile's map of what enters it to what leaves it
     float* pref;                 // [rows, 64 ncb] what leaves a tile
     long x_row, rows;            // rows: an upper bound with cu_seqlens
-    int tokens, T, N, D, ncb, n_slots;
+    int tokens, T, N, D, ncb, tile, n_slots;
     int bf16, h_bf16, blend;     // types of x (and dx), of h (and dh)
 };
-// Rows of tiles (an upper bound with cu_seqlens), and the workspace of a scan.
+// Tokens of a tile, rows of tiles (an upper bound with cu_seqlens), and the workspace of a scan.
 struct ScanLayout {
+    int tile;
     long rows;
     size_t off_base, off_agg, off_pref, total;   // total 0: one tile per sequence, no workspace
 };

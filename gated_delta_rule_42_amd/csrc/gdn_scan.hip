@@ -6,7 +6,7 @@
 //     D_t = dh_t + E_{t+1},   E_{len+1} = dhT,   dx = D or (1 - a) D,   dg = E_t h_{t-1} or E_t (h_{t-1} - x_t),   dh0 = E_1.
 // Four operations an element against 8 (forward) or 14 (backward) bytes in bf16: bound by bytes, if the sequence is cut. A run of tokens
 // maps the state entering it to the one leaving it by h -> A h + H, and such maps compose, so every thread first forms the
-// map of its few tokens (8 channels wide, as loaded, in registers), the maps of a tile of 256 tokens x 64 channels are joined in LDS, and
+// map of its few tokens (8 channels wide, as loaded, in registers), the maps of a tile of 256 tokens (or 32) x 64 channels are joined in LDS, and
 // with the state entering the tile known each thread runs its tokens again from registers: inputs are read once, outputs
 // written once.
 // The state entering a tile comes from the tiles before it, in the same launch: a tile publishes its own map as soon as it has it, and its
@@ -78,7 +78,7 @@ __device__ __forceinline__ ScanTile scan_tile(const ScanProblem& p, long row, lo
     ScanTile k;
     int b, e;
     if (!p.cu_seqlens) {
-        const int per = max(1, (p.T + kScanTokens - 1) / kScanTokens);
+        const int per = max(1, (p.T + p.tile - 1) / p.tile);
         k.n = (int)(row / per);
         k.s = (int)(row - (long)k.n * per);
         b = k.n * p.T;
@@ -100,10 +100,10 @@ __device__ __forceinline__ ScanTile scan_tile(const ScanProblem& p, long row, lo
         b = min(max(p.cu_seqlens[lo], 0), p.tokens);
         e = min(max(p.cu_seqlens[lo + 1], b), p.tokens);
     }
-    k.last = max(0, (e - b - 1) / kScanTokens);
+    k.last = max(0, (e - b - 1) / p.tile);
     if (p.base) k.last = (int)min((long)k.last, rows - 1 - (row - k.s));   // none waits for a tile that is not run
-    k.t0 = b + k.s * kScanTokens;
-    k.len = max(0, min(e - k.t0, kScanTokens));
+    k.t0 = b + k.s * p.tile;
+    k.len = max(0, min(e - k.t0, p.tile));
     return k;
 }
 
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(256) void scan_setup_kernel(ScanProblem p) {
         int tiles = 0;
         if (n < p.N) {
             const int lo = min(max(p.cu_seqlens[n], 0), p.tokens), hi = min(max(p.cu_seqlens[n + 1], lo), p.tokens);
-            tiles = max(1, (hi - lo + kScanTokens - 1) / kScanTokens);
+            tiles = max(1, (hi - lo + p.tile - 1) / p.tile);
         }
         __syncthreads();
         sum[threadIdx.x] = tiles;
@@ -178,10 +178,13 @@ __global__ __launch_bounds__(256) void scan_setup_kernel(ScanProblem p) {
     if (threadIdx.x == 0) p.base[p.N] = before;
 }
 
-// R: tokens per thread; 256 / R groups of 8 lanes, 8 channels a lane.
-template <typename TX, typename TH, int R, bool BLEND, bool NT>
-__global__ __launch_bounds__(8 * kScanTokens / R, 4) void scan_fwd_kernel(ScanProblem p) {
-    constexpr int G = kScanTokens / R;
+constexpr int R = 4;   // tokens per thread
+constexpr int scan_threads(int TOK) { return 8 * TOK / R; }
+
+// TOK: tokens of a tile; TOK / R groups of 8 lanes, 8 channels a lane.
+template <typename TX, typename TH, int TOK, bool BLEND, bool NT>
+__global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProblem p) {
+    constexpr int G = TOK / R;
     __shared__ float2 maps[G][kScanChannels];
     __shared__ float enter[kScanChannels];
     __shared__ int ticket;
@@ -289,9 +292,9 @@ __global__ __launch_bounds__(8 * kScanTokens / R, 4) void scan_fwd_kernel(ScanPr
 
 // Two work-groups per CU, where a token's a and operands fit 128 registers a thread; blended, with 1 - a kept too, one (4 x 2048 x 2048 in bf16
 // 65 us, against 90 at 128 registers and 68 with 1 - a formed again; fp32 82, 168, 89).
-template <typename TX, typename TH, int R, bool BLEND, bool NT>
-__global__ __launch_bounds__(8 * kScanTokens / R, BLEND ? 2 : 4) void scan_bwd_kernel(ScanProblem p) {
-    constexpr int G = kScanTokens / R;
+template <typename TX, typename TH, int TOK, bool BLEND, bool NT>
+__global__ __launch_bounds__(scan_threads(TOK), BLEND ? 2 : 4) void scan_bwd_kernel(ScanProblem p) {
+    constexpr int G = TOK / R;
     // of every group: A; H, then the state entering it; the gradient's part of its map, then that of the groups behind it; their A
     __shared__ float mA[G][kScanChannels], mH[G][kScanChannels], mE[G][kScanChannels], mS[G][kScanChannels];
     __shared__ float enter[kScanChannels];
@@ -372,7 +375,8 @@ __global__ __launch_bounds__(8 * kScanTokens / R, BLEND ? 2 : 4) void scan_bwd_k
             mH[k][ch] = h;
             h = __fmaf_rn(m, h, q);
         }
-    } else if (wave == 1) {   // the map of the groups behind each, and what comes from the tiles behind this one
+    }
+    if (wave == (G > 8 ? 1 : 0)) {   // the map of the groups behind each, and what comes from the tiles behind this one
         float At = 1.f, Et = 0.f;
 #pragma unroll 16
         for (int k = G - 1; k >= 0; --k) {
@@ -488,13 +492,16 @@ __global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblo
     if (!p.out_slots) store4c<false>(p.pool + (long)slot * p.D + c, h);
 }
 
+// Tiles of 256 tokens, or of 32 where that leaves most of them empty: rows of at most 32 tokens, packed sequences of fewer than 64
+// on average (8192 tokens of 2048 channels in sequences of 16: 205 us forward in tiles of 256).
 ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen) {
     ScanLayout w{};
     const long ncb = ((long)D + kScanChannels - 1) / kScanChannels;
     const int longest = varlen ? tokens : T;   // the longest that a sequence can be
-    const long per = longest > kScanTokens ? ((long)T + kScanTokens - 1) / kScanTokens : 1;
-    w.rows = varlen ? (long)N + tokens / kScanTokens : N * per;
-    if (longest <= kScanTokens) return w;
+    w.tile = varlen ? (tokens > 256 && tokens < 64L * N ? 32 : 256) : (T <= 32 ? 32 : 256);
+    const long per = longest > w.tile ? ((long)T + w.tile - 1) / w.tile : 1;
+    w.rows = varlen ? (long)N + tokens / w.tile : N * per;
+    if (longest <= w.tile) return w;
     const size_t cells = (size_t)w.rows * ncb * kScanChannels;
     w.off_base = ((size_t)kTicketWords * 4 * ncb + 255) / 256 * 256;
     w.off_agg = w.off_base + (varlen ? (((size_t)N + 1) * 4 + 255) / 256 * 256 : 0);
@@ -513,25 +520,26 @@ static hipError_t scan_setup(const ScanProblem& p, long& tiles, hipStream_t s) {
 
 // Outputs go past the caches where they exceed the L2s together.
 static bool scan_large(const ScanProblem& p) { return (long)p.tokens * p.D >= 1 << 23; }
-constexpr int R = 4;   // tokens per thread
 
 template <typename TX, typename TH, bool BLEND>
 static hipError_t scan_fwd(const ScanProblem& p, hipStream_t s) {
     long tiles;
     const hipError_t e = scan_setup(p, tiles, s);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)tiles), block(8 * kScanTokens / R);
-    return scan_large(p) ? launch(scan_fwd_kernel<TX, TH, R, BLEND, true>, grid, block, s, p)
-                         : launch(scan_fwd_kernel<TX, TH, R, BLEND, false>, grid, block, s, p);
+    const dim3 grid((unsigned)tiles), block(scan_threads(p.tile));
+    if (p.tile == 32) return launch(scan_fwd_kernel<TX, TH, 32, BLEND, false>, grid, block, s, p);
+    return scan_large(p) ? launch(scan_fwd_kernel<TX, TH, 256, BLEND, true>, grid, block, s, p)
+                         : launch(scan_fwd_kernel<TX, TH, 256, BLEND, false>, grid, block, s, p);
 }
 template <typename TX, typename TH, bool BLEND>
 static hipError_t scan_bwd(const ScanProblem& p, hipStream_t s) {
     long tiles;
     const hipError_t e = scan_setup(p, tiles, s);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)tiles), block(8 * kScanTokens / R);
-    return scan_large(p) ? launch(scan_bwd_kernel<TX, TH, R, BLEND, true>, grid, block, s, p)
-                         : launch(scan_bwd_kernel<TX, TH, R, BLEND, false>, grid, block, s, p);
+    const dim3 grid((unsigned)tiles), block(scan_threads(p.tile));
+    if (p.tile == 32) return launch(scan_bwd_kernel<TX, TH, 32, BLEND, false>, grid, block, s, p);
+    return scan_large(p) ? launch(scan_bwd_kernel<TX, TH, 256, BLEND, true>, grid, block, s, p)
+                         : launch(scan_bwd_kernel<TX, TH, 256, BLEND, false>, grid, block, s, p);
 }
 template <typename TX, typename TH, bool BLEND>
 static hipError_t scan_update(const ScanProblem& p, hipStream_t s) {

@@ -565,14 +565,15 @@ int gdn_conv_update(const void *x, const float *weight, const float *bias, void 
  *   h0          fp32 [N, D] or NULL (zeros)
  *   cu_seqlens  int32 [N + 1] device array of packed sequences (then B = 1) or NULL (N = B)
  *   h           [B, T, D] h_dtype (GDN_BF16 only for bf16 x), dense; hT fp32 [N, D]: the state behind each sequence, or NULL
- *   carries     fp32 [gdn_scan_carry_rows(...), D] or NULL: the state entering every tile of 256 tokens of a sequence (a sequence
- *               has one tile at least; those of one sequence follow each other), for the backward pass
- *   workspace   gdn_scan_workspace_bytes(...) bytes, 256-byte aligned; none where no sequence can be longer than 256 tokens. Its
+ *   carries     fp32 [gdn_scan_carry_rows(...), D] or NULL: the state entering every tile of a sequence, for the backward pass. A tile has 256
+ *               tokens, or 32 for rows of at most 32 tokens and for more than 256 packed tokens in sequences of fewer than 64 on average; a sequence has
+ *               one tile at least, those of one sequence follow each other, and rows past the last tile are not written
+ *   workspace   gdn_scan_workspace_bytes(...) bytes, 256-byte aligned; none where no sequence can be longer than a tile. Its
  *               contents need not be set and mean nothing afterwards; calls that can run at once need one each
  *   D           a multiple of 8 up to 2^20; B * T <= 2^28, B * T * D <= 2^36, N <= 2^24, N * D <= 2^31 and tiles *
  *               ceil(D / 64) < 2^23
- * Offsets outside [0, T] are clamped; rows of the outputs that no sequence covers are left as they were. x, g, h and hT are aligned
- * to 16 bytes, h0 and carries to 4; x_stride is a multiple of 16 bytes. States are fp32; 1 - a is formed from g and keeps its digits
+ * Offsets outside [0, T] are clamped; rows of the outputs that no sequence covers are left as they were. hT may be h0; h may not overlap
+ * an input. x, g, h and hT are aligned to 16 bytes, h0 and carries to 4; x_stride is a multiple of 16 bytes. States are fp32; 1 - a is formed from g and keeps its digits
  * where a is near 1. A NaN in x, g or h0, or an infinity in x or h0, makes its channel's states NaN or infinite from there to the sequence's end.
  * The same inputs give the same bits.
  */

@@ -95,9 +95,10 @@ def test_sizes():
     rows, ws = gb.gdn_scan_carry_rows, gb.gdn_scan_workspace_bytes
     assert rows(2, 0, 2, False) == rows(2, 1, 2, False) == rows(2, 256, 2, False) == 2 and rows(2, 257, 2, False) == 4
     assert rows(1, 100, 7, True) == 7 and rows(1, 1000, 7, True) == 7 + 3 and rows(1, 100, 7, False) == 0
+    assert rows(1, 1000, 15, True) == 15 + 3 and rows(1, 1000, 16, True) == 16 + 31   # fewer than 64 tokens a sequence: tiles of 32
     assert ws(2, 256, 2, 64, False) == ws(1, 256, 9, 64, True) == 0
     assert ws(2, 257, 2, 72, False) == 256 + 4 * 128 * 12   # counters, then maps and states of 4 x 2 tiles of 64 channels
-    assert ws(1, 1000, 100, 328, True) == 512 + 512 + 103 * 384 * 12
+    assert ws(1, 1000, 100, 328, True) == 512 + 512 + 131 * 384 * 12
     assert ws(1, 1000, 2, 60, True) == 0 and c_update(T=0, x=None, h=None) == 0 and c_update(T=0, N=0, cu=None, slots=None) == 0
 
 
@@ -166,7 +167,9 @@ SHAPES = [
     # B, T, cu, D
     (1, 1, None, 8), (2, 7, None, 72), (3, 256, None, 64), (2, 0, None, 64), (2, 257, None, 136), (1, 3000, None, 40), (5, 600, None, 64),
     (1, 90, [0, 1, 1, 3, 20, 36, 37, 52, 90], 72), (1, 256, [0, 0, 0, 256], 64), (1, 1100, [0, 0, 256, 513, 513, 514, 1026, 1090, 1090], 72),
-    (1, 5000, [0, 4700, 4701, 5000], 24),
+    (1, 5000, [0, 4700, 4701, 5000], 24), (4, 32, None, 72), (4, 33, None, 72), (3, 20, None, 136),
+    # tiles of 32 tokens, one long sequence among short ones
+    (1, 900, [0, 0, 31, 63, 96, 97, 97, 300, 332, 333, 365, 370, 380, 390, 400, 890], 72),
 ]
 
 
@@ -214,6 +217,29 @@ def test_many_tiles_at_once():
     inside(h[..., at], rh, eh, "h")
     inside(hT[..., at], rT, eT, "hT")
     rx, rg, r0, ex, eg, e0 = SC.backward(s["x"], s["g"], s["h0"], s["dh"], s["dhT"], None, False)
+    inside(dx[..., at], rx, ex, "dx")
+    inside(dg[..., at], rg, eg, "dg")
+    inside(dh0[..., at], r0, e0, "dh0")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("blend", [False, True])
+def test_many_short_sequences(blend):
+    """Tiles of 32 tokens, more than the device holds at once, some sequences of many tiles; sampled channels against the oracle."""
+    gen = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 40, (400,), generator=gen).tolist() + [1500] + torch.randint(0, 40, (300,), generator=gen).tolist() + [64, 65, 63, 700]
+    cu, D = np.concatenate([[0], np.cumsum(lens)]).tolist(), 1032
+    print(f"[gpu] scan {len(lens)} sequences, {cu[-1]} tokens, D={D} blend={blend}", flush=True)
+    x = make(9, 1, cu[-1] + 3, len(lens), D, "bf16")
+    t = {n: a.cuda() for n, a in x.items()}
+    h, hT, car = gb.gdn_scan_fwd(t["x"], t["g"], t["h0"], cut(cu), blend=blend, keep_carries=True)
+    dx, dg, dh0 = gb.gdn_scan_bwd(t["x"], t["g"], t["dh"], car, t["dhT"], cut(cu), blend=blend)
+    at = [0, 63, 64, 1031]
+    s = {n: a[..., at] for n, a in x.items()}
+    rh, rT, eh, eT = SC.forward(s["x"], s["g"], s["h0"], cu, blend)
+    inside(h[..., at], rh, eh, "h")
+    inside(hT[..., at], rT, eT, "hT")
+    rx, rg, r0, ex, eg, e0 = SC.backward(s["x"], s["g"], s["h0"], s["dh"], s["dhT"], cu, blend)
     inside(dx[..., at], rx, ex, "dx")
     inside(dg[..., at], rg, eg, "dg")
     inside(dh0[..., at], r0, e0, "dh0")
@@ -293,19 +319,22 @@ def test_bad_offsets_stay_inside_and_end(blend, monkeypatch):
     """Offsets that fall or leave [0, T] are clamped, also where they count more tiles than there is room for."""
     x = make(6, 1, 1000, 5, 64, "bf16")
     t = {n: a.cuda() for n, a in x.items()}
-    for offsets in ([-5, 600, 3, 2000000000, 0, 1000], [0, 1000, 0, 1000, 0, 1000], [1000, 0, 0, 0, 0, 0]):
+    for offsets in ([-5, 600, 3, 2000000000, 0, 1000], [0, 1000, 0, 1000, 0, 1000], [1000, 0, 0, 0, 0, 0], [0, 1000] * 10):
+        n = len(offsets) - 1   # 19 of them: tiles of 32
+        t["h0"], t["dhT"] = torch.ones(n, 64, device="cuda"), torch.ones(n, 64, device="cuda")
         h = torch.zeros_like(t["x"])
         _, hT, car = gb.gdn_scan_fwd(t["x"], t["g"], t["h0"], cut(offsets), blend=blend, h=h, keep_carries=True)
         car = torch.nan_to_num(car, 0.0, 0.0, 0.0)   # rows past the last tile hold anything
         gb.gdn_scan_bwd(t["x"], t["g"], t["dh"], car, t["dhT"], cut(offsets), blend=blend)
         torch.cuda.synchronize()
         assert torch.isfinite(h.float()).all()
+    t["h0"] = x["h0"].cuda()
     slots = torch.arange(5, dtype=torch.int32, device="cuda")
     gb.gdn_scan_update(t["x"][0], t["g"][0], t["h0"].clone(), slots, cut([-5, 600, 3, 2000000000, 0, 1000]), blend=blend)
     monkeypatch.setenv("GDN_CHECK", "1")
     gb.gdn_scan_fwd(t["x"], t["g"], t["h0"], cut([0, 3, 3, 500, 600, 999]))
     bad = cut([0, 600, 3, 700, 800, 1000])
-    for f in (lambda: gb.gdn_scan_fwd(t["x"], t["g"], t["h0"], bad), lambda: gb.gdn_scan_bwd(t["x"], t["g"], t["dh"], car, None, bad),
+    for f in (lambda: gb.gdn_scan_fwd(t["x"], t["g"], t["h0"], bad), lambda: gb.gdn_scan_bwd(t["x"], t["g"], t["dh"], torch.zeros(8, 64, device="cuda"), None, bad),
               lambda: gb.gdn_scan_update(t["x"][0], t["g"][0], t["h0"], slots, bad)):
         with pytest.raises(gb.GDNError):
             f()
