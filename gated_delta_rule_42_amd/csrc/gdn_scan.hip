@@ -492,13 +492,14 @@ __global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblo
     if (!p.out_slots) store4c<false>(p.pool + (long)slot * p.D + c, h);
 }
 
-// Tiles of 256 tokens, or of 32 where that leaves most of them empty: rows of at most 32 tokens, packed sequences of fewer than 64
-// on average (8192 tokens of 2048 channels in sequences of 16: 205 us forward in tiles of 256).
+// Tiles of 256 tokens, or of 32 where that leaves most of them empty: rows of at most 32 tokens, and sequences of fewer than 128 (on average, where
+// they are packed) in calls that fill the device (8192 tokens of 2048 channels forward, in tiles of 256 and 32: sequences of 16 tokens 205 and 45 us, of
+// 64 62 and 37, of 128 39 and 38, of 256 31 and 41). In small calls one tile a sequence saves the pass that clears the marks.
 ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen) {
     ScanLayout w{};
     const long ncb = ((long)D + kScanChannels - 1) / kScanChannels;
     const int longest = varlen ? tokens : T;   // the longest that a sequence can be
-    w.tile = varlen ? (tokens > 256 && tokens < 64L * N ? 32 : 256) : (T <= 32 ? 32 : 256);
+    w.tile = longest <= 32 || (tokens >= (varlen ? 257 : 4096) && tokens < 128L * N) ? 32 : 256;
     const long per = longest > w.tile ? ((long)T + w.tile - 1) / w.tile : 1;
     w.rows = varlen ? (long)N + tokens / w.tile : N * per;
     if (longest <= w.tile) return w;

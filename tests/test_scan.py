@@ -95,7 +95,9 @@ def test_sizes():
     rows, ws = gb.gdn_scan_carry_rows, gb.gdn_scan_workspace_bytes
     assert rows(2, 0, 2, False) == rows(2, 1, 2, False) == rows(2, 256, 2, False) == 2 and rows(2, 257, 2, False) == 4
     assert rows(1, 100, 7, True) == 7 and rows(1, 1000, 7, True) == 7 + 3 and rows(1, 100, 7, False) == 0
-    assert rows(1, 1000, 15, True) == 15 + 3 and rows(1, 1000, 16, True) == 16 + 31   # fewer than 64 tokens a sequence: tiles of 32
+    # fewer than 128 tokens a sequence: tiles of 32, where the call is large enough
+    assert rows(1, 1024, 8, True) == 8 + 4 and rows(1, 1023, 8, True) == 8 + 31 and rows(1, 256, 8, True) == 8 + 1 and rows(1, 32, 2, True) == 2 + 1
+    assert rows(64, 64, 64, False) == 128 and rows(63, 64, 63, False) == 63 and rows(64, 128, 64, False) == 64
     assert ws(2, 256, 2, 64, False) == ws(1, 256, 9, 64, True) == 0
     assert ws(2, 257, 2, 72, False) == 256 + 4 * 128 * 12   # counters, then maps and states of 4 x 2 tiles of 64 channels
     assert ws(1, 1000, 100, 328, True) == 512 + 512 + 131 * 384 * 12
@@ -167,7 +169,7 @@ SHAPES = [
     # B, T, cu, D
     (1, 1, None, 8), (2, 7, None, 72), (3, 256, None, 64), (2, 0, None, 64), (2, 257, None, 136), (1, 3000, None, 40), (5, 600, None, 64),
     (1, 90, [0, 1, 1, 3, 20, 36, 37, 52, 90], 72), (1, 256, [0, 0, 0, 256], 64), (1, 1100, [0, 0, 256, 513, 513, 514, 1026, 1090, 1090], 72),
-    (1, 5000, [0, 4700, 4701, 5000], 24), (4, 32, None, 72), (4, 33, None, 72), (3, 20, None, 136),
+    (1, 5000, [0, 4700, 4701, 5000], 24), (4, 32, None, 72), (4, 33, None, 72), (3, 20, None, 136), (65, 70, None, 24),
     # tiles of 32 tokens, one long sequence among short ones
     (1, 900, [0, 0, 31, 63, 96, 97, 97, 300, 332, 333, 365, 370, 380, 390, 400, 890], 72),
 ]
