@@ -663,6 +663,12 @@ def _rows_of(t, name):
     return _token_stride(t, name, 1) if t.numel() else 0
 
 
+def _check_sizes(*sizes):
+    """Sizes reach the C ABI as 32-bit integers."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"gdn: a size of {sizes} exceeds 2^31 - 1")
+
+
 def _bytes(workspace):
     return workspace.numel() * workspace.element_size() if workspace is not None else 0
 
@@ -675,6 +681,8 @@ def gdn_layer_norm_fwd(x, weight=None, bias=None, *, residual=None, eps=1e-5, ou
     if len(shape) < 1 or dtype not in _IN:
         raise ValueError(f"gdn: x must be [..., d] float32 or bfloat16, got {tuple(shape)} {dtype}")
     d = shape[-1]
+    rows = x.numel() // d if d else 0
+    _check_sizes(rows, d)
     _expect(weight, "weight", (d,), _F32)
     _expect(bias, "bias", (d,), _F32)
     _expect(residual, "residual", shape, (dtype, torch.float32))
@@ -686,7 +694,6 @@ def gdn_layer_norm_fwd(x, weight=None, bias=None, *, residual=None, eps=1e-5, ou
         _expect(sum_out, "sum_out", shape, (residual.dtype,))
         _same_gpu(dev, residual=residual)
     _dense_on(dev, weight=weight, bias=bias, y=y, sum_out=sum_out)
-    rows = x.numel() // d if d else 0
     xs = _rows_of(x, "x")
     rs = _rows_of(residual, "residual") if residual is not None else 0
     if y is None:
@@ -711,13 +718,14 @@ def gdn_layer_norm_bwd(s, dy, weight=None, *, ds=None, eps=1e-5, need_dw=None, d
     if len(shape) < 1 or dtype not in _IN:
         raise ValueError(f"gdn: s must be [..., d] float32 or bfloat16, got {tuple(shape)} {dtype}")
     d = shape[-1]
+    rows = s.numel() // d if d else 0
+    _check_sizes(rows, d)
     _expect(dy, "dy", shape, _IN)
     _expect(weight, "weight", (d,), _F32)
     _expect(ds, "ds", shape, (dtype,))
     _expect(dx, "dx", shape, (dtype,))
     dev = s.device
     _dense_on(dev, dy=dy, weight=weight, ds=ds, dx=dx, workspace=workspace)
-    rows = s.numel() // d if d else 0
     xs = _rows_of(s, "s")
     if dx is None:
         dx = _new(shape, dtype, dev, stream)
@@ -740,11 +748,13 @@ def _check_sequences(x, cu_seqlens):
     if x.dim() != 3 or x.dtype not in _IN:
         raise ValueError(f"gdn: x must be [B, T, D] float32 or bfloat16, got {tuple(x.shape)} {x.dtype}")
     B, T, D = x.shape
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    _check_sizes(B, T, D, N)
     if cu_seqlens is None:
-        return B, T, D, B
+        return B, T, D, N
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.dtype != torch.int32:
         raise ValueError("gdn: cu_seqlens must be a 1-D int32 tensor of N + 1 >= 2 offsets")
-    return B, T, D, cu_seqlens.numel() - 1
+    return B, T, D, N
 
 
 def _check_conv(x, weight, bias, activation):
@@ -823,6 +833,7 @@ def _check_runs(x, slots, cu_seqlens, out_slots):
     if x.dim() != 2 or x.dtype not in _IN:
         raise ValueError(f"gdn: x must be [T, D] float32 or bfloat16, got {tuple(x.shape)} {x.dtype}")
     T, D = x.shape
+    _check_sizes(T, D, slots.numel())
     if slots.dim() != 1 or slots.dtype != torch.int32:
         raise ValueError("gdn: slots must be a 1-D int32 tensor")
     N = slots.numel()
@@ -842,6 +853,7 @@ def gdn_conv_update(x, weight, bias, windows, slots, cu_seqlens=None, out_slots=
     dtype, dev = x.dtype, x.device
     if windows.dim() != 3:
         raise ValueError(f"gdn: windows must be [n_slots, width - 1, D], got shape {tuple(windows.shape)}")
+    _check_sizes(windows.shape[0])
     _expect(windows, "windows", (windows.shape[0], W - 1, D), (dtype,))
     _expect(y, "y", (T, D), (dtype,))
     _dense_on(dev, weight=weight, bias=bias, windows=windows, slots=slots, cu_seqlens=cu_seqlens, out_slots=out_slots, y=y)
@@ -925,6 +937,7 @@ def gdn_scan_update(x, g, states, slots, cu_seqlens=None, out_slots=None, h=None
     _expect(g, "g", (T, D), _F32)
     if states.dim() != 2:
         raise ValueError(f"gdn: states must be [n_slots, D], got shape {tuple(states.shape)}")
+    _check_sizes(states.shape[0])
     _expect(states, "states", (states.shape[0], D), _F32)
     _expect(h, "h", (T, D), _IN)
     _dense_on(dev, g=g, states=states, slots=slots, cu_seqlens=cu_seqlens, out_slots=out_slots, h=h)

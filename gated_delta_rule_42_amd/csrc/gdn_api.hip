@@ -675,6 +675,7 @@ GDN_EXPORT int gdn_layer_norm_fwd(const void* x, const void* residual, const flo
     for (const void* q : al16)
         if (!aligned(q, 16)) return GDN_ERR_ALIGN;
     if (x_stride % per16(dtype) || (residual && residual_stride % per16(sum_dtype))) return GDN_ERR_ALIGN;
+    if (rows > 0 && residual && y == sum) return GDN_ERR_SHAPE;
     gdn::LayerNormProblem p{};
     p.x = x; p.residual = residual; p.weight = weight; p.bias = bias; p.y = y; p.sum = sum;
     p.rows = rows; p.d = d; p.x_row = x_stride; p.r_row = residual_stride; p.eps = eps;
@@ -759,6 +760,8 @@ GDN_EXPORT int gdn_conv_fwd(const void* x, const float* weight, const float* bia
     const int tokens = B * T;
     if ((tokens > 0 && (!x || !y)) || !weight) return GDN_ERR_NULL;
     if (!all_aligned({x, weight, bias, window0, y, windowT}, {cu_seqlens}) || x_stride % per16(dtype)) return GDN_ERR_ALIGN;
+    // other work-groups still read them
+    if ((tokens > 0 && y == x) || (windowT && windowT == window0)) return GDN_ERR_SHAPE;
     hipStream_t s = static_cast<hipStream_t>(stream);
     st = debug_check_offsets(cu_seqlens, N, T, s, true);
     if (st != GDN_OK) return st;
@@ -793,6 +796,8 @@ GDN_EXPORT int gdn_conv_bwd(const void* x, const float* weight, const float* bia
         if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return GDN_ERR_ALIGN;
     }
+    // other work-groups still read them
+    if ((tokens > 0 && (dx == x || dx == dy)) || (dwindow0 && (dwindow0 == window0 || dwindow0 == dwindowT))) return GDN_ERR_SHAPE;
     hipStream_t s = static_cast<hipStream_t>(stream);
     st = debug_check_offsets(cu_seqlens, N, T, s, true);
     if (st != GDN_OK) return st;

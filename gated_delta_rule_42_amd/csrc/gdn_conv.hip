@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvProblem p, int cblock
         for (int i = 0; i < TL; ++i) {
             raw[i + W - 1].get(u[0]);
             conv_token<W, SILU>(w, b, u, y);
-            if (in) store4c<false>(at_byte(yp + (long)i * p.D, cb), y);
+            if (in) store4c(at_byte(yp + (long)i * p.D, cb), y);
             move_on<W>(u);
         }
         return;
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvProblem p, int cblock
                 for (int j = 1; j < W; ++j) window_row<T, W>(p, p.window0, tok.seq[i], W - 1 - j, c, u[j]);
             }
             conv_token<W, SILU>(w, b, u, y);
-            if (in) store4c<false>(at_byte(yp + (long)i * p.D, cb), y);
+            if (in) store4c(at_byte(yp + (long)i * p.D, cb), y);
         }
         move_on<W>(u);
     }
@@ -221,7 +221,7 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
         e0 = min(max(p.cu_seqlens[n + 1], b0), p.tokens);
     }
     const int len = e0 - b0;
-    float w[4][W], b[4], g[W - 1][4], u[2 * W - 2][4];
+    float w[V][W], b[V], g[W - 1][V], u[2 * W - 2][V];
     load_taps<W>(p.weight, c, w);
     load_bias(p.bias, c, b);
 #pragma unroll
@@ -232,17 +232,17 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
         if (r < len) raw.load(static_cast<const T*>(p.x) + (long)(b0 + r) * p.x_row + c);
         raw.get(u[W - 1 + r]);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) g[r][v] = 0.f;
+        for (int v = 0; v < V; ++v) g[r][v] = 0.f;
     }
 #pragma unroll
     for (int t = 0; t < W - 1; ++t) {
         if (t < len) {
             Raw4<T> raw;
-            float dz[4];
+            float dz[V];
             raw.load(static_cast<const T*>(p.dy) + (long)(b0 + t) * p.D + c);
             raw.get(dz);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
+            for (int v = 0; v < V; ++v) {
                 if (p.silu) {
                     float z = b[v];
 #pragma unroll
@@ -258,12 +258,12 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {
         if (p.dwindowT && r >= len) {
-            float d[4];
+            float d[V];
             window_row<T, W>(p, p.dwindowT, n, r - len, c, d);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) g[r][v] += d[v];
+            for (int v = 0; v < V; ++v) g[r][v] += d[v];
         }
-        store4c<false>(static_cast<T*>(p.dwindow0) + ((long)n * (W - 1) + r) * p.D + c, g[r]);
+        store4c(static_cast<T*>(p.dwindow0) + ((long)n * (W - 1) + r) * p.D + c, g[r]);
     }
 }
 
@@ -277,11 +277,11 @@ constexpr int kConvBlock = 4;   // BL: with 8 in bf16 two waves fit a SIMD inste
 template <typename T, int W, bool SILU, bool DW>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblocks, int parts, int run) {
     constexpr int BL = kConvBlock, H = W - 1;
-    __shared__ float part[DW ? 4 : 1][DW ? 64 * 4 * (W + 1) : 1];
+    __shared__ float part[DW ? 4 : 1][DW ? 64 * V * (W + 1) : 1];
     __shared__ int seq[4][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // scalar, and so are tokens and masks
     const int by = (int)(blockIdx.x / (unsigned)cblocks), bx = (int)(blockIdx.x - (unsigned)by * (unsigned)cblocks);
-    const long c0 = ((long)bx * 64 + lane) * 4;
+    const long c0 = ((long)bx * 64 + lane) * V;
     const bool in = c0 < p.D;
     const long c = in ? c0 : 0;   // lanes past the channels go along with the first ones and store nothing
     const unsigned cb = (unsigned)c * sizeof(T);
@@ -290,11 +290,11 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
         if (n < p.N && in) window_gradient<T, W>(p, n, c);
         return;
     }
-    float w[4][W], b[4], dw[4][W], db[4];
+    float w[V][W], b[V], dw[V][W], db[V];
     load_taps<W>(p.weight, c, w);
     load_bias(p.bias, c, b);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
+    for (int v = 0; v < V; ++v) {
         db[v] = 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[v][j] = 0.f;
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
         const T* xp = static_cast<const T*>(p.x);
         const T* gp = static_cast<const T*>(p.dy);
         T* dxp = static_cast<T*>(p.dx);
-        float u[W][4], dz[W][4];   // u[k]: the input k tokens back; dz[k]: k tokens back
+        float u[W][V], dz[W][V];   // u[k]: the input k tokens back; dz[k]: k tokens back
         Raw4<T> xr[BL], gr[BL], xn[BL], gn[BL];
 #pragma unroll
         for (int i = 0; i < BL; ++i) {   // rows past the tensor: the last one, for no token's sake
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
             before.load(at_byte(xp + (long)max(r0 - k, 0) * p.x_row, cb));
             before.get(u[k]);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) dz[k][v] = 0.f;
+            for (int v = 0; v < V; ++v) dz[k][v] = 0.f;
         }
         // the tokens base - H .. of masks and seq; every SPAN tokens they are looked up anew
         constexpr int SPAN = (64 - H) / BL * BL;
@@ -349,12 +349,11 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
             if (plain) {   // inside one sequence, its end no nearer than this block's: no token needs a look at the masks
 #pragma unroll
                 for (int i = 0; i < BL; ++i) {
-                    float d[4];
+                    float d[V];
                     xr[i].get(u[0]);
                     gr[i].get(d);
-                    const float mine = i < own ? 1.f : 0.f;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
+                    for (int v = 0; v < V; ++v) {
                         if constexpr (SILU) {
                             float z = b[v];
 #pragma unroll
@@ -363,22 +362,24 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
                             d[v] *= sg * (1.f + z * (1.f - sg));
                         }
                         dz[0][v] = d[v];
-                        if constexpr (DW) {
-                            const float dm = BL - i > H ? d[v] : d[v] * mine;
-                            db[v] += dm;
+                    }
+                    if (DW && (BL - i > H || i < own)) {
 #pragma unroll
-                            for (int j = 0; j < W; ++j) dw[v][W - 1 - j] += dm * u[j][v];
+                        for (int v = 0; v < V; ++v) {
+                            db[v] += d[v];
+#pragma unroll
+                            for (int j = 0; j < W; ++j) dw[v][W - 1 - j] += d[v] * u[j][v];
                         }
                     }
                     if (i >= H || t0 > r0) {   // the token H back has all of its terms
-                        float dx[4];
+                        float dx[V];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
+                        for (int v = 0; v < V; ++v) {
                             dx[v] = w[v][W - 1] * dz[W - 1][v];
 #pragma unroll
                             for (int m = 1; m < W; ++m) dx[v] += w[v][W - 1 - m] * dz[W - 1 - m][v];
                         }
-                        if (in) store4c<false>(at_byte(dxp + (long)(t0 + i - H) * p.dx_row, cb), dx);
+                        if (in) store4c(at_byte(dxp + (long)(t0 + i - H) * p.dx_row, cb), dx);
                     }
                     move_on<W>(u);
                     move_on<W>(dz);
@@ -390,13 +391,13 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
 #pragma unroll 1
                 for (int i = 0; i < BL; ++i) {
                     const int t = t0 + i, at = s + H + i;   // at: the token's bit
-                    float d[4];
+                    float d[V];
                     xt.get(u[0]);
                     gt.get(d);
                     xt.load(at_byte(xp + (long)min(t + 1, last) * p.x_row, cb));
                     gt.load(at_byte(gp + (long)min(t + 1, last) * p.D, cb));
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) dz[0][v] = 0.f;
+                    for (int v = 0; v < V; ++v) dz[0][v] = 0.f;
                     // a token behind the run matters only where the run's last one belongs to the same sequence
                     const bool reach = i < own || (t < r1 + H && !(tok.starts >> (at - (i - own)) & ((2ull << (i - own)) - 1)));
                     if (tok.is(tok.covered, at) && reach) {
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
                             for (int j = 1; j < W; ++j) window_row<T, W>(p, p.window0, tok.seq[at], H - j, c, u[j]);
                         }
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
+                        for (int v = 0; v < V; ++v) {
                             dz[0][v] = d[v];
                             if constexpr (SILU) {
                                 float z = b[v];
@@ -422,25 +423,25 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
                         }
                     }
                     if (t - H >= r0 && t - H < r1 && tok.is(tok.covered, at - H)) {
-                        float dx[4];
+                        float dx[V];
                         int rem = W;   // tokens of its sequence from it on, W for that or more
 #pragma unroll
                         for (int r = 0; r < H; ++r)
                             if (tok.is(tok.ends[r], at - H)) rem = r + 1;
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) dx[v] = w[v][W - 1] * dz[W - 1][v];
+                        for (int v = 0; v < V; ++v) dx[v] = w[v][W - 1] * dz[W - 1][v];
 #pragma unroll
                         for (int m = 1; m < W; ++m)
                             if (m < rem)
 #pragma unroll
-                                for (int v = 0; v < 4; ++v) dx[v] += w[v][W - 1 - m] * dz[W - 1 - m][v];
+                                for (int v = 0; v < V; ++v) dx[v] += w[v][W - 1 - m] * dz[W - 1 - m][v];
                         if (p.dwindowT && rem < W) {
-                            float e[4];
+                            float e[V];
                             window_row<T, W>(p, p.dwindowT, tok.seq[at - H], H - rem, c, e);
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) dx[v] += e[v];
+                            for (int v = 0; v < V; ++v) dx[v] += e[v];
                         }
-                        if (in) store4c<false>(at_byte(dxp + (long)(t - H) * p.dx_row, cb), dx);
+                        if (in) store4c(at_byte(dxp + (long)(t - H) * p.dx_row, cb), dx);
                     }
                     move_on<W>(u);
                     move_on<W>(dz);
@@ -454,18 +455,18 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
         }
     }
     if constexpr (DW) {
-        float* mine = part[wave] + lane * 4 * (W + 1);
+        float* mine = part[wave] + lane * V * (W + 1);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
+        for (int v = 0; v < V; ++v) {
 #pragma unroll
             for (int j = 0; j < W; ++j) mine[v * (W + 1) + j] = dw[v][j];
             mine[v * (W + 1) + W] = db[v];
         }
         __syncthreads();
         float* row = p.partial + (long)by * p.D * (W + 1);
-        for (int i = threadIdx.x; i < 256 * (W + 1); i += 256) {
+        for (int i = threadIdx.x; i < 64 * V * (W + 1); i += 256) {
             const int ch = i / (W + 1), j = i % (W + 1);
-            const long cc = (long)bx * 256 + ch;
+            const long cc = (long)bx * 64 * V + ch;
             if (cc < p.D) {
                 const float a = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
                 row[j < W ? cc * W + j : (long)p.D * W + cc] = a;
@@ -494,7 +495,7 @@ __global__ __launch_bounds__(256) void conv_update_kernel(ConvProblem p, int cbl
     if (slot < 0 || slot >= p.n_slots) {   // a padded entry: zeros for its tokens, no window touched
 #pragma unroll
         for (int v = 0; v < V; ++v) y[v] = 0.f;
-        for (int t = t0; t < t1; ++t) store4c<false>(yp + (long)t * p.D, y);
+        for (int t = t0; t < t1; ++t) store4c(yp + (long)t * p.D, y);
         return;
     }
     T* pool = static_cast<T*>(p.pool) + c;
@@ -525,7 +526,7 @@ __global__ __launch_bounds__(256) void conv_update_kernel(ConvProblem p, int cbl
                     for (int j = W - 1; j >= 0; --j) z += w[v][W - 1 - j] * f[j][v];
                     y[v] = p.silu ? z * sigmoid_f(z) : z;
                 }
-                store4c<false>(yp + (long)t * p.D, y);
+                store4c(yp + (long)t * p.D, y);
 #pragma unroll
                 for (int k = W - 1; k > 0; --k) u[k] = u[k - 1];
                 if (p.out_slots) {
@@ -571,7 +572,7 @@ hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t s) {
 // Tokens of a run of the backward pass: as many waves as the device holds at once (three a SIMD, in fp32 two), whole blocks less W - 1, four
 // blocks at least (so that few tokens still spread).
 static int conv_run(int tokens, int D, int W, int bf16) {
-    const long cblocks = (D + 255) / 256, most = 4L * kMaxParts;   // at most kMaxParts rows of four runs
+    const long cblocks = (D + 64 * V - 1) / (64 * V), most = 4L * kMaxParts;   // at most kMaxParts rows of four runs
     long waves = ((bf16 ? 3072 : 2048) + cblocks - 1) / cblocks;
     waves = waves < most ? waves : most;
     const long len = (tokens + waves - 1) / waves, blocks = (len + W - 1 + kConvBlock - 1) / kConvBlock;
@@ -584,7 +585,7 @@ int conv_parts(int tokens, int D, int W) { return conv_rows(tokens, conv_run(tok
 template <typename T, int W, bool SILU>
 static hipError_t conv_bwd(const ConvProblem& p, hipStream_t s) {
     const bool dw = p.dweight || p.dbias;
-    const int run = conv_run(p.tokens, p.D, W, p.bf16), parts = conv_rows(p.tokens, run), cblocks = (p.D + 255) / 256;
+    const int run = conv_run(p.tokens, p.D, W, p.bf16), parts = conv_rows(p.tokens, run), cblocks = (p.D + 64 * V - 1) / (64 * V);
     const long groups = (long)cblocks * (parts + (p.dwindow0 ? (p.N + 3) / 4 : 0));
     if (groups > 0) {
         const dim3 grid((unsigned)groups), block(256);

@@ -36,7 +36,6 @@ template <> struct Raw8<uint16_t> {
             x[2 * e + 1] = bf16_hi_half(w[e]);
         }
     }
-    __device__ __forceinline__ void put(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = a; }
 };
 // NT: past the caches.
 template <bool NT, typename T>
@@ -73,11 +72,9 @@ template <> struct Raw4<uint16_t> {
     }
     __device__ __forceinline__ void put(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = a; }
 };
-template <bool NT>
-__device__ __forceinline__ void store4c(float* p, const float (&x)[4]) { store_piece<NT>(p, f32x4_t{x[0], x[1], x[2], x[3]}); }
-template <bool NT>
+__device__ __forceinline__ void store4c(float* p, const float (&x)[4]) { store_piece<false>(p, f32x4_t{x[0], x[1], x[2], x[3]}); }
 __device__ __forceinline__ void store4c(uint16_t* p, const float (&x)[4]) {
-    store_piece<NT>(p, u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])});
+    store_piece<false>(p, u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])});
 }
 
 // A row at a scalar address (the same in every lane) and a lane's byte offset in it: the empty asm keeps the compiler from adding the two

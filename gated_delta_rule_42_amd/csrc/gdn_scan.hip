@@ -453,7 +453,7 @@ __global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblo
     TH* hp = static_cast<TH*>(p.h) + c;
     float h[4] = {0.f, 0.f, 0.f, 0.f};
     if (slot < 0 || slot >= p.n_slots) {   // a padded entry: zeros for its tokens, no state touched
-        for (int t = t0; t < t1; ++t) store4c<false>(hp + (long)t * p.D, h);
+        for (int t = t0; t < t1; ++t) store4c(hp + (long)t * p.D, h);
         return;
     }
     Raw4<float> state;
@@ -481,15 +481,15 @@ __global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblo
                     const float a = __expf(g[e]);
                     h[e] = __fmaf_rn(a, h[e], BLEND ? one_minus_exp(g[e], a) * x[e] : x[e]);
                 }
-                store4c<false>(hp + (long)t * p.D, h);
+                store4c(hp + (long)t * p.D, h);
                 if (p.out_slots) {
                     const int to = p.out_slots[t];
-                    if (to >= 0 && to < p.n_slots) store4c<false>(p.pool + (long)to * p.D + c, h);
+                    if (to >= 0 && to < p.n_slots) store4c(p.pool + (long)to * p.D + c, h);
                 }
             }
         }
     }
-    if (!p.out_slots) store4c<false>(p.pool + (long)slot * p.D + c, h);
+    if (!p.out_slots) store4c(p.pool + (long)slot * p.D + c, h);
 }
 
 // Tiles of 256 tokens, or of 32 where that leaves most of them empty: rows of at most 32 tokens, and sequences of fewer than 128 (on average, where

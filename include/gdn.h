@@ -490,7 +490,7 @@ int gdn_qk_norm_bwd(const void *q, const void *k, const void *dq_out, const void
  *   sum         [rows, d] sum_dtype, dense: s, which the next residual and the backward pass take
  *   d           a multiple of 8, 8 .. 16384; rows < 2^28, rows * d < 2^35; eps > 0
  * Pointers and strides are multiples of 16 bytes. y and sum may each be x or residual where that is dense and of the
- * same type (not both the same one); other overlaps are undefined. Statistics and sums are fp32, the variance that of the centred values.
+ * same type (both the same one is refused, GDN_ERR_SHAPE); other overlaps are undefined. Statistics and sums are fp32, the variance that of the centred values.
  */
 int gdn_layer_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias,
                        void *y, void *sum, int rows, int d, int64_t x_stride, int64_t residual_stride,
@@ -519,7 +519,7 @@ int gdn_layer_norm_bwd(const void *sum, const void *dy, const void *dsum, const 
  *   window0     [N, W-1, D] dtype: the W-1 inputs before each sequence, oldest first, or NULL (zeros)
  *   cu_seqlens  int32 [N + 1] device array of packed sequences (then B = 1) or NULL (N = B)
  *   y           [B, T, D] dtype, dense; windowT [N, W-1, D] dtype: the last W-1 inputs of each sequence (of its window where it
- *               is shorter), or NULL. Neither may overlap an input
+ *               is shorter), or NULL. Neither may overlap an input (y = x, windowT = window0: GDN_ERR_SHAPE)
  *   D           a multiple of 8 up to 2^20; B * T <= 2^28, B * T * D <= 2^36, N <= 2^24, N * D <= 2^31
  * Offsets outside [0, T] are clamped; rows of y that no sequence covers are left as they were. Pointers (cu_seqlens and the
  * gradients of weight and bias: 4 bytes) and strides are multiples of 16 bytes. Arithmetic is fp32.
@@ -535,7 +535,7 @@ int gdn_conv_fwd(const void *x, const float *weight, const float *bias, const vo
  * projection), and, where not NULL, dweight fp32 [D, W], dbias fp32 [D] and dwindow0 [N, W-1, D] (dtype), each defined also
  * where its operand was NULL. The gradients of weight and bias are sums over all tokens in a fixed order and take a workspace of
  * gdn_conv_bwd_workspace_bytes(...) bytes, 256-byte aligned (fp32 [work-group rows, D (W + 1)]); without them none is
- * used. dx may not overlap an input.
+ * used. The outputs may not overlap the inputs (dx = x, dx = dy, dwindow0 = window0, dwindow0 = dwindowT: GDN_ERR_SHAPE).
  */
 size_t gdn_conv_bwd_workspace_bytes(int B, int T, int D, int width);
 int gdn_conv_bwd(const void *x, const float *weight, const float *bias, const void *window0, const void *dy,
@@ -587,7 +587,7 @@ int gdn_scan_fwd(const void *x, const float *g, const float *h0, const int32_t *
 /*
  * Backward pass of gdn_scan_fwd on the same x, g, cu_seqlens and the carries that it left: from the gradients dh [B, T, D]
  * (h_dtype, dense) and dhT fp32 [N, D] (or NULL: zero) of its outputs: dx [B, T, D] (dtype, dense), dg fp32 [B, T, D] and, where
- * not NULL, dh0 fp32 [N, D]. Workspace as in gdn_scan_fwd.
+ * not NULL, dh0 fp32 [N, D]. Workspace as in gdn_scan_fwd. The outputs may not overlap the inputs.
  */
 int gdn_scan_bwd(const void *x, const float *g, const float *carries, const void *dh, const float *dhT,
                  const int32_t *cu_seqlens, void *dx, float *dg, float *dh0, int B, int T, int N, int D,

@@ -102,6 +102,14 @@ def test_update_refuses(kw, status):
     assert c_update(**kw) == status
 
 
+def test_outputs_over_inputs_are_refused():
+    q, r, s = P + 4096, P + 8192, P + 12288
+    for kw in (dict(), dict(y=q, w0=r, wT=r)):
+        assert c_fwd(**kw) == -2
+    for kw in (dict(dy=q), dict(dx=q, dy=q), dict(dy=q, dx=r, w0=s, dw0=s), dict(dy=q, dx=r, dwT=s, dw0=s)):
+        assert c_bwd(**kw) == -2
+
+
 def test_nothing_to_do_is_ok():
     assert c_fwd(T=0, x=None, y=None) == 0
     assert c_update(T=0, x=None, y=None, win=None) == 0
@@ -122,6 +130,10 @@ def test_binding_refuses_on_the_host():
             gb.gdn_conv_fwd(*args, **kw)
     with pytest.raises(ValueError, match="dy has dtype"):
         gb.gdn_conv_bwd(x, w, m(2, 8, 64, dt=torch.bfloat16))
+    with pytest.raises(ValueError, match="exceeds"):
+        gb.gdn_conv_fwd(m(1, (1 << 32) + 8, 64), w)
+    with pytest.raises(ValueError, match="exceeds"):
+        gb.gdn_conv_update(m(8, 64), w, None, m((1 << 32) + 5, 3, 64), m(8, dt=i32))
     good = dict(x=m(8, 64), weight=w, bias=None, windows=m(5, 3, 64), slots=m(8, dt=i32))
     for change, text in ((dict(x=m(1, 8, 64)), r"\[T, D\]"), (dict(windows=m(5, 2, 64)), "windows has shape"), (dict(windows=m(5, 64)), "windows must"),
                          (dict(slots=m(3, dt=i32)), "without cu_seqlens"), (dict(slots=m(8)), "slots must"),
@@ -285,6 +297,24 @@ def test_nan_stays_with_its_sequence():
     assert torch.equal(y[:, rest], y0[:, rest]) and torch.equal(dx[:, rest], dx0[:, rest])
     assert torch.equal(wT[[0, 2]], w0[[0, 2]]) and torch.equal(dw[[0, 2]], dw0[[0, 2]])
     assert torch.isnan(y[:, 5:9]).all() and torch.isnan(dx[:, 5:9]).all() and torch.isnan(dw[1]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_infinite_gradients_count_once(W):
+    """An infinite gradient makes its channel's sums infinite, wherever the token lies in a wave's run, and no NaN."""
+    T, D = 64, 64
+    x = make(25, 1, T, 1, D, W, "f32")
+    t = {n: a.cuda() for n, a in x.items()}
+    dy = t["dy"].clone()
+    dy[0, torch.arange(T), torch.arange(T)] = float("inf")   # token t: channel t
+    _, dw0, db0, _ = gb.gdn_conv_bwd(t["x"], t["w"], t["dy"], t["b"], t["w0"])
+    dx, dw, db, _ = gb.gdn_conv_bwd(t["x"], t["w"], dy, t["b"], t["w0"])
+    assert (db == float("inf")).all()
+    u = torch.cat([t["w0"], t["x"]], 1)[0]
+    for j in range(W):
+        assert torch.equal(dw[:, j], torch.sign(u[torch.arange(T) + j, torch.arange(T)]) * float("inf"))
+    assert torch.isinf(dx[0, torch.arange(T), torch.arange(T)]).all() and torch.isfinite(dw0).all() and torch.isfinite(db0).all()
 
 
 @pytest.mark.gpu

@@ -61,7 +61,7 @@ SHARED = [(dict(dtype=2), -3), (dict(od=-1), -3), (dict(d=60), -5), (dict(d=0), 
 @pytest.mark.parametrize("kw,status", SHARED + [
     (dict(r=P, s=P, sd=2), -3), (dict(r=P, s=P, sd=1, dtype=0), -3), (dict(xs=-64), -2), (dict(rs=-64), -2), (dict(x=None), -1),
     (dict(y=None), -1), (dict(r=P), -1), (dict(x=P + 8), -4), (dict(y=P + 8), -4), (dict(b=P + 4), -4), (dict(xs=65), -4),
-    (dict(r=P, s=P, rs=68), -4), (dict(r=P, s=P + 4), -4)])
+    (dict(r=P, s=P, rs=68), -4), (dict(r=P, s=P + 4), -4), (dict(r=P, s=P), -2)])
 def test_fwd_refuses(kw, status):
     assert c_fwd(**kw) == status
 
@@ -89,6 +89,10 @@ def test_binding_refuses_on_the_host():
             ((m(2, 64),), {}, "on a GPU")):
         with pytest.raises(ValueError, match=text):
             gb.gdn_layer_norm_fwd(*args, **kw)
+    with pytest.raises(ValueError, match="exceeds"):
+        gb.gdn_layer_norm_fwd(m((1 << 32) + 8, 64))
+    with pytest.raises(ValueError, match="exceeds"):
+        gb.gdn_layer_norm_bwd(m((1 << 32) + 8, 64), m((1 << 32) + 8, 64))
     for args, kw, text in (((m(2, 64), m(2, 32)), {}, "dy has shape"), ((m(2, 64), m(2, 64)), dict(ds=m(2, 64, dt=torch.bfloat16)), "ds has dtype"),
                            ((m(2, 64), m(2, 64)), {}, "on a GPU")):
         with pytest.raises(ValueError, match=text):

@@ -116,6 +116,10 @@ def test_binding_refuses_on_the_host():
                        ((x, g, m(2, 300, 64, dt=torch.bfloat16), m(4, 64)), "dh has dtype"), ((x, g, x, m(4, 64)), "on a GPU")):
         with pytest.raises(ValueError, match=text):
             gb.gdn_scan_bwd(*args)
+    with pytest.raises(ValueError, match="exceeds"):
+        gb.gdn_scan_fwd(m(1, (1 << 32) + 8, 64), m(1, (1 << 32) + 8, 64))
+    with pytest.raises(ValueError, match="exceeds"):
+        gb.gdn_scan_update(m(8, 64), m(8, 64), m((1 << 32) + 5, 64), m(8, dt=i32))
     good = dict(x=m(8, 64), g=m(8, 64), states=m(5, 64), slots=m(8, dt=i32))
     for change, text in ((dict(x=m(1, 8, 64)), r"\[T, D\]"), (dict(states=m(5, 32)), "states has shape"), (dict(states=m(5, 1, 64)), "states must"),
                          (dict(g=m(8, 32)), "g has shape"), (dict(slots=m(3, dt=i32)), "without cu_seqlens"), (dict(), "on a GPU")):
