@@ -179,6 +179,10 @@ __global__ __launch_bounds__(256) void scan_setup_kernel(ScanProblem p) {
 }
 
 constexpr int R = 4;   // tokens per thread
+// as Raw8's hide(), for what is computed from them
+__device__ __forceinline__ void hide(Raw8<float>& r) {
+    asm volatile("" : "+v"(r.a.x), "+v"(r.a.y), "+v"(r.a.z), "+v"(r.a.w), "+v"(r.b.x), "+v"(r.b.y), "+v"(r.b.z), "+v"(r.b.w));
+}
 constexpr int scan_threads(int TOK) { return 8 * TOK / R; }
 
 // TOK: tokens of a tile; TOK / R groups of 8 lanes, 8 channels a lane.
@@ -290,10 +294,11 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
         store8<false>(p.hT + (long)tile.n * p.D + c, h);
 }
 
-// Two work-groups per CU, where a token's a and operands fit 128 registers a thread; blended, with 1 - a kept too, one (4 x 2048 x 2048 in bf16
-// 65 us, against 90 at 128 registers and 68 with 1 - a formed again; fp32 82, 168, 89).
+// Two work-groups per CU at 128 registers a thread. Blended, a and 1 - a together do not fit: both are formed again from g, and the gradient's
+// part of a tile's map is summed forward, so that a is not kept for it either (4 x 2048 x 2048 in bf16 60 us; with both kept and one work-group per CU
+// 64, half the size 29 and 34). fp32 blended spills even so and has one work-group per CU (84 us against 102).
 template <typename TX, typename TH, int TOK, bool BLEND, bool NT>
-__global__ __launch_bounds__(scan_threads(TOK), BLEND ? 2 : 4) void scan_bwd_kernel(ScanProblem p) {
+__global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4) void scan_bwd_kernel(ScanProblem p) {
     constexpr int G = TOK / R;
     // of every group: A; H, then the state entering it; the gradient's part of its map, then that of the groups behind it; their A
     __shared__ float mA[G][kScanChannels], mH[G][kScanChannels], mE[G][kScanChannels], mS[G][kScanChannels];
@@ -330,33 +335,34 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND ? 2 : 4) void scan_bwd_ker
             dr[i].load(static_cast<const TH*>(p.dh) + first + at);
         }
     }
-    float a[R][8], keep[BLEND ? R : 1][8], A[8], H[8], E[8];
+    float a[BLEND ? 1 : R][8], A[8], H[8], E[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) A[e] = 1.f, H[e] = E[e] = 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        float x[8];
-        gr[i].get(a[i]);
+        float g[8], x[8], d[8];
+        gr[i].get(g);
         xr[i].get(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float g = i < mine ? a[i][e] : 0.f;
-            x[e] = i < mine ? x[e] : 0.f;
-            a[i][e] = __expf(g);
-            if constexpr (BLEND) {
-                keep[i][e] = one_minus_exp(g, a[i][e]);
-                x[e] *= keep[i][e];
-            }
-            H[e] = __fmaf_rn(a[i][e], H[e], x[e]);
-            A[e] *= a[i][e];
-        }
-    }
-#pragma unroll
-    for (int i = R - 1; i >= 0; --i) {
-        float d[8];
         dr[i].get(d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) E[e] = a[i][e] * ((i < mine ? d[e] : 0.f) + E[e]);
+        for (int e = 0; e < 8; ++e) {
+            if (i >= mine) g[e] = x[e] = d[e] = 0.f;
+            const float at = __expf(g[e]);
+            if constexpr (BLEND) x[e] *= one_minus_exp(g[e], at);
+            else a[i][e] = at;
+            H[e] = __fmaf_rn(at, H[e], x[e]);
+            A[e] *= at;
+            if constexpr (BLEND) E[e] = __fmaf_rn(A[e], d[e], E[e]);
+        }
+    }
+    if constexpr (!BLEND) {
+#pragma unroll
+        for (int i = R - 1; i >= 0; --i) {
+            float d[8];
+            dr[i].get(d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) E[e] = a[i][e] * ((i < mine ? d[e] : 0.f) + E[e]);
+        }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -402,39 +408,52 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND ? 2 : 4) void scan_bwd_ker
     for (int i = 0; i < R; ++i) {
         xr[i].hide();
         dr[i].hide();
+        if constexpr (BLEND) hide(gr[i]);
     }
-    float h[R][8];   // the state before each token, blended less its x: what E is multiplied with for dg
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[0][e] = mH[grp][8 * l + e];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        float x[8];
-        xr[i].get(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (i + 1 < R) h[i + 1][e] = __fmaf_rn(a[i][e], h[i][e], BLEND ? keep[i][e] * x[e] : x[e]);
-            if constexpr (BLEND) h[i][e] -= x[e];
-        }
-    }
+    // backward over the tokens for D, which takes the place of dh, then forward for the states
+    float D[R][8], h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) E[e] = __fmaf_rn(mS[grp][8 * l + e], enter[8 * l + e], mE[grp][8 * l + e]);
 #pragma unroll
     for (int i = R - 1; i >= 0; --i) {
-        float d[8], dg[8];
-        dr[i].get(d);
+        float g[8];
+        gr[i].get(g);
+        dr[i].get(D[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            d[e] = (i < mine ? d[e] : 0.f) + E[e];
-            E[e] = a[i][e] * d[e];
-            dg[e] = E[e] * h[i][e];
-            if constexpr (BLEND) d[e] *= keep[i][e];
-        }
-        if (in && i < mine) {
-            store8<NT>(static_cast<TX*>(p.dx) + first + (at0 + i * p.D), d);
-            store8<NT>(p.dg + first + (at0 + i * p.D), dg);
+            D[i][e] = (i < mine ? D[i][e] : 0.f) + E[e];
+            E[e] = (BLEND ? __expf(i < mine ? g[e] : 0.f) : a[i][e]) * D[i][e];
         }
     }
     if (p.dh0 && in && tile.s == 0 && grp == 0) store8<false>(p.dh0 + (long)tile.n * p.D + c, E);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if constexpr (BLEND) hide(gr[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = mH[grp][8 * l + e];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {   // tokens past the end are the last ones: what becomes of h there meets nobody
+        float g[8], x[8];
+        gr[i].get(g);
+        xr[i].get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float at = BLEND ? __expf(g[e]) : a[i][e], Et = at * D[i][e];
+            if constexpr (BLEND) {
+                const float keep = one_minus_exp(g[e], at);
+                g[e] = Et * (h[e] - x[e]);
+                D[i][e] *= keep;
+                x[e] *= keep;
+            } else {
+                g[e] = Et * h[e];
+            }
+            h[e] = __fmaf_rn(at, h[e], x[e]);
+        }
+        if (in && i < mine) {
+            store8<NT>(static_cast<TX*>(p.dx) + first + (at0 + i * p.D), D[i]);
+            store8<NT>(p.dg + first + (at0 + i * p.D), g);
+        }
+    }
 }
 
 // Runs of tokens on a pool of states: a lane walks its sequence's tokens for four channels. Tokens come four at a time.
