@@ -81,7 +81,7 @@ struct ScanProblem {
     float* pool;                 // runs on a pool: [n_slots, D]
     const int32_t* slots;        // [N]
     const int32_t* out_slots;    // [tokens] or NULL
-    // workspace, where a sequence can have more than one tile (else ticket NULL)
+    // workspace, where tiles pass states on between work-groups (else ticket NULL)
     int32_t* ticket;
     int32_t* base;               // [N + 1] first tile of each sequence (cu_seqlens only)
     uint64_t* agg;               // [rows, 64 ncb] a tile's map of what enters it to what leaves it
@@ -94,7 +94,7 @@ struct ScanProblem {
 struct ScanLayout {
     int tile;
     long rows;
-    size_t off_base, off_agg, off_pref, total;   // total 0: one tile per sequence, no workspace
+    size_t off_base, off_agg, off_pref, total;   // total 0: a work-group walks a sequence's tiles, no workspace
 };
 ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen);
 hipError_t launch_scan_fwd(const ScanProblem& p, hipStream_t s);

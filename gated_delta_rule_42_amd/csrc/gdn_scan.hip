@@ -15,7 +15,8 @@
 // bits do not depend on timing. Tiles are numbered by a ticket drawn at the start of a work-group, and a tile waits for
 // lower tickets only, whose work-groups run already and publish their maps without waiting: every wait ends. The words that pass
 // between work-groups are single relaxed atomics at device scope that hold their own mark (all ones: not there yet), so nothing has to be
-// fenced. The backward pass walks the tiles the other way; the states entering them are kept by the forward one.
+// fenced. Where sequences are short, one work-group walks a sequence's tiles instead and keeps the state itself. The backward pass takes the
+// tiles the other way; the states entering them are kept by the forward one.
 #include "gdn_block.h"
 #include "gdn_row.h"
 
@@ -64,7 +65,7 @@ __device__ __forceinline__ float enter_from(const ScanProblem& p, long row, int 
     }
 }
 
-// The rows of tiles of this call.
+// The rows of tiles of this call; where one work-group walks a whole sequence, its sequences.
 __device__ __forceinline__ long scan_rows(const ScanProblem& p) {
     if (!p.ticket) return p.N;
     return p.base ? min((long)p.base[p.N], p.rows) : p.rows;
@@ -73,37 +74,49 @@ __device__ __forceinline__ long scan_rows(const ScanProblem& p) {
 // A tile's place: sequence, number within it, first token, tokens.
 struct ScanTile {
     int n, s, last, t0, len;   // last: the number of its sequence's last tile
+    int begin, end;            // the sequence's tokens
+    long row;                  // of the carries
+    // on to tile `to` of the same sequence
+    __device__ __forceinline__ void move(const ScanProblem& p, int to) {
+        row += to - s;
+        s = to;
+        t0 = begin + s * p.tile;
+        len = max(0, min(end - t0, p.tile));
+    }
 };
-__device__ __forceinline__ ScanTile scan_tile(const ScanProblem& p, long row, long rows) {
+// walk: row is a sequence, and the tile its first or (back) its last. The tiles of sequence n then begin at row n + begin / tile.
+__device__ __forceinline__ ScanTile scan_tile(const ScanProblem& p, long row, long rows, bool back) {
     ScanTile k;
-    int b, e;
-    if (!p.cu_seqlens) {
-        const int per = max(1, (p.T + p.tile - 1) / p.tile);
+    const bool walk = !p.ticket;
+    const int per = max(1, (p.T + p.tile - 1) / p.tile);
+    k.s = 0;
+    if (walk) {
+        k.n = (int)row;
+    } else if (!p.cu_seqlens) {
         k.n = (int)(row / per);
         k.s = (int)(row - (long)k.n * per);
-        b = k.n * p.T;
-        e = b + p.T;
     } else {
-        int lo = (int)min(row, (long)p.N - 1);   // without a table every sequence has one tile
-        long first = lo;
-        if (p.base) {
-            lo = 0;
-            int hi = p.N;   // the last n with base[n] <= row
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (p.base[mid] <= row) lo = mid; else hi = mid;
-            }
-            first = p.base[lo];
+        int lo = 0, hi = p.N;   // the last n with base[n] <= row
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.base[mid] <= row) lo = mid; else hi = mid;
         }
         k.n = lo;
-        k.s = (int)(row - first);
-        b = min(max(p.cu_seqlens[lo], 0), p.tokens);
-        e = min(max(p.cu_seqlens[lo + 1], b), p.tokens);
+        k.s = (int)(row - p.base[lo]);
     }
-    k.last = max(0, (e - b - 1) / p.tile);
+    if (p.cu_seqlens) {
+        k.begin = min(max(p.cu_seqlens[k.n], 0), p.tokens);
+        k.end = min(max(p.cu_seqlens[k.n + 1], k.begin), p.tokens);
+    } else {
+        k.begin = k.n * p.T;
+        k.end = k.begin + p.T;
+    }
+    k.last = max(0, (k.end - k.begin - 1) / p.tile);
     if (p.base) k.last = (int)min((long)k.last, rows - 1 - (row - k.s));   // none waits for a tile that is not run
-    k.t0 = b + k.s * p.tile;
-    k.len = max(0, min(e - k.t0, p.tile));
+    k.row = !walk ? row - k.s : !p.cu_seqlens ? row * per : row + k.begin / p.tile;
+    const int at = walk && back ? k.last : k.s;
+    k.s = 0;
+    k.move(p, at);
     return k;
 }
 
@@ -194,16 +207,21 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
     __shared__ int ticket;
     const long rows = scan_rows(p);
     const ScanPlace place = scan_place(p);
-    const int l = threadIdx.x & 7, grp = threadIdx.x >> 3, cb = place.cb;
+    const int cb = place.cb;
+    const long row = draw_row(p, place, &ticket);
+    if (row >= rows) return;
+    ScanTile tile = scan_tile(p, row, rows, false);
+    float state = 0.f;   // walking, a lane of the first wave's channel: what leaves the tile
+  for (;;) {
+    unsigned thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));   // what is computed from it is not kept from one tile to the next
+    const int l = thread & 7, grp = thread >> 3;
     const unsigned c = (unsigned)(cb * kScanChannels + 8 * l);
     const bool in = c < (unsigned)p.D;
     // offsets within a tile fit 32 bits (256 tokens of at most 2^20 channels); only x may lie further apart
     const unsigned at0 = (unsigned)(grp * R) * p.D + c;
     Raw8<TX> xr[R];
     Raw8<float> gr[R];
-    const long row = draw_row(p, place, &ticket);
-    if (row >= rows) return;
-    const ScanTile tile = scan_tile(p, row, rows);
     const long first = (long)tile.t0 * p.D;
     const int mine = min(max(tile.len - grp * R, 0), R);   // this thread's tokens
     // every thread loads: tokens past the end the last one again, channels past the end the first ones, put out of action below. (A branch
@@ -246,8 +264,8 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
 #pragma unroll
     for (int e = 0; e < 8; ++e) maps[grp][8 * l + e] = make_float2(A[e], H[e]);
     __syncthreads();
-    if (threadIdx.x < kScanChannels) {
-        const int ch = threadIdx.x;
+    if (thread < kScanChannels) {
+        const int ch = thread;
         const unsigned col = (unsigned)(cb * kScanChannels + ch);
         const bool real = col < (unsigned)p.D;
         float At = 1.f, Ht = 0.f;   // the map of the groups before each, in its place
@@ -259,15 +277,16 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
             At *= m.x;
         }
         const long at = row * p.ncb * kScanChannels + col;
-        float h = 0.f;
+        float h = state;
         if (tile.s == 0) {
             if (p.h0 && real) h = p.h0[(long)tile.n * p.D + col];
-        } else {
+        } else if (p.ticket) {
             publish_map(p.agg + at, At, Ht);
             h = enter_from(p, row, -1, tile.s, col);
         }
-        if (tile.s < tile.last) publish_state(p.pref + at, __fmaf_rn(At, h, Ht));
-        if (p.carries && real) p.carries[row * p.D + col] = h;
+        state = __fmaf_rn(At, h, Ht);
+        if (p.ticket && tile.s < tile.last) publish_state(p.pref + at, state);
+        if (p.carries && real) p.carries[tile.row * p.D + col] = h;
         enter[ch] = h;
     }
     __syncthreads();
@@ -292,6 +311,9 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
     // the state behind the sequence's last token (or the one it began with, where it has none)
     if (p.hT && in && tile.s == tile.last && (mine > 0 ? grp * R + mine == tile.len : grp == 0 && tile.len == 0))
         store8<false>(p.hT + (long)tile.n * p.D + c, h);
+    if (p.ticket || tile.s == tile.last) break;
+    tile.move(p, tile.s + 1);
+  }
 }
 
 // Two work-groups per CU at 128 registers a thread. Blended, a and 1 - a together do not fit: both are formed again from g, and the gradient's
@@ -306,16 +328,21 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
     __shared__ int ticket;
     const long rows = scan_rows(p);
     const ScanPlace place = scan_place(p);
-    const int l = threadIdx.x & 7, grp = threadIdx.x >> 3, cb = place.cb;
+    const int cb = place.cb;
+    const long row = rows - 1 - draw_row(p, place, &ticket);   // the last tiles first
+    if (row < 0) return;
+    ScanTile tile = scan_tile(p, row, rows, true);
+    float back = 0.f;   // walking: what leaves the tile, as in the forward pass
+  for (;;) {
+    unsigned thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));   // what is computed from it is not kept from one tile to the next
+    const int l = thread & 7, grp = thread >> 3;
     const unsigned c = (unsigned)(cb * kScanChannels + 8 * l);
     const bool in = c < (unsigned)p.D;
     const unsigned at0 = (unsigned)(grp * R) * p.D + c;
     Raw8<TX> xr[R];
     Raw8<TH> dr[R];
     Raw8<float> gr[R];
-    const long row = rows - 1 - draw_row(p, place, &ticket);   // the last tiles first
-    if (row < 0) return;
-    const ScanTile tile = scan_tile(p, row, rows);
     const long first = (long)tile.t0 * p.D;
     const int mine = min(max(tile.len - grp * R, 0), R);
     const unsigned cl = in ? c : 0;   // loads as in the forward pass
@@ -371,10 +398,10 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
         mE[grp][8 * l + e] = E[e];
     }
     __syncthreads();
-    const int wave = threadIdx.x >> 6, ch = threadIdx.x & 63;
+    const int wave = thread >> 6, ch = thread & 63;
     const unsigned col = (unsigned)(cb * kScanChannels + ch);
     if (wave == 0) {   // the states entering the groups
-        float h = col < (unsigned)p.D ? p.carries[row * p.D + col] : 0.f;
+        float h = col < (unsigned)p.D ? p.carries[tile.row * p.D + col] : 0.f;
 #pragma unroll 16
         for (int k = 0; k < G; ++k) {
             const float m = mA[k][ch], q = mH[k][ch];
@@ -393,14 +420,15 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
             At *= m;
         }
         const long at = row * p.ncb * kScanChannels + col;
-        float d = 0.f;
+        float d = back;
         if (tile.s == tile.last) {
             if (p.dhT && col < (unsigned)p.D) d = p.dhT[(long)tile.n * p.D + col];
-        } else {
+        } else if (p.ticket) {
             publish_map(p.agg + at, At, Et);
             d = enter_from(p, row, 1, tile.last - tile.s, col);
         }
-        if (tile.s > 0) publish_state(p.pref + at, __fmaf_rn(At, d, Et));
+        back = __fmaf_rn(At, d, Et);
+        if (p.ticket && tile.s > 0) publish_state(p.pref + at, back);
         enter[ch] = d;
     }
     __syncthreads();
@@ -454,6 +482,9 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
             store8<NT>(p.dg + first + (at0 + i * p.D), g);
         }
     }
+    if (p.ticket || tile.s == 0) break;
+    tile.move(p, tile.s - 1);
+  }
 }
 
 // Runs of tokens on a pool of states: a lane walks its sequence's tokens for four channels. Tokens come four at a time.
@@ -514,14 +545,19 @@ __global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblo
 // Tiles of 256 tokens, or of 32 where that leaves most of them empty: rows of at most 32 tokens, and sequences of fewer than 128 (on average, where
 // they are packed) in calls that fill the device (8192 tokens of 2048 channels forward, in tiles of 256 and 32: sequences of 16 tokens 205 and 45 us, of
 // 64 62 and 37, of 128 39 and 38, of 256 31 and 41). In small calls one tile a sequence saves the pass that clears the marks.
+// Where no sequence can have more than two tiles (four of 32 tokens) one work-group walks them all, which saves that pass and the wait for other
+// work-groups (1 x 512 x 2048, a call: 17.5 and 13.5 us, backward 18.5 and 15.0; 128 x 64 x 2048 in tiles of 32: 31.9 and 27.8, 50.1 and 48.4), as long as
+// the device holds all of them at once (64 x 512 x 2048: 98 and 99, backward 183 and 206). Three tiles gain no more (8 x 700 x 1024: 17.9 and
+// 15.7, backward 20.6 and 22.8), but packed sequences are as a rule far shorter than all of them together: there the call may have four.
 ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen) {
     ScanLayout w{};
     const long ncb = ((long)D + kScanChannels - 1) / kScanChannels;
     const int longest = varlen ? tokens : T;   // the longest that a sequence can be
-    w.tile = longest <= 32 || (tokens >= (varlen ? 257 : 4096) && tokens < 128L * N) ? 32 : 256;
-    const long per = longest > w.tile ? ((long)T + w.tile - 1) / w.tile : 1;
+    const bool large = varlen ? tokens > 1024 || (tokens > 256 && N > 16) : tokens >= 4096;
+    w.tile = longest <= 32 || (large && tokens < 128L * N) ? 32 : 256;
+    const long per = T > w.tile ? ((long)T + w.tile - 1) / w.tile : 1;
     w.rows = varlen ? (long)N + tokens / w.tile : N * per;
-    if (longest <= w.tile) return w;
+    if (w.tile == 32 ? longest <= 128 : longest <= w.tile || (longest <= (varlen && N > 1 ? 1024 : 512) && N * ncb <= 512)) return w;
     const size_t cells = (size_t)w.rows * ncb * kScanChannels;
     w.off_base = ((size_t)kTicketWords * 4 * ncb + 255) / 256 * 256;
     w.off_agg = w.off_base + (varlen ? (((size_t)N + 1) * 4 + 255) / 256 * 256 : 0);

@@ -568,8 +568,8 @@ int gdn_conv_update(const void *x, const float *weight, const float *bias, void 
  *   carries     fp32 [gdn_scan_carry_rows(...), D] or NULL: the state entering every tile of a sequence, for the backward pass. A tile has 256
  *               tokens, or 32 where no sequence can have more and, in calls of 4096 tokens (packed: 257) and more, where sequences have fewer than 128
  *               on average; a sequence has
- *               one tile at least, those of one sequence follow each other, and rows past the last tile are not written
- *   workspace   gdn_scan_workspace_bytes(...) bytes, 256-byte aligned; none where no sequence can be longer than a tile. Its
+ *               one tile at least, those of one sequence follow each other, and rows that are no tile's are not written
+ *   workspace   gdn_scan_workspace_bytes(...) bytes, 256-byte aligned; none (0) where all sequences are short. Its
  *               contents need not be set and mean nothing afterwards; calls that can run at once need one each
  *   D           a multiple of 8 up to 2^20; B * T <= 2^28, B * T * D <= 2^36, N <= 2^24, N * D <= 2^31 and tiles *
  *               ceil(D / 64) < 2^23

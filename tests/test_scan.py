@@ -69,7 +69,7 @@ KIND = [(dict(dtype=2), -3), (dict(hd=2), -3), (dict(dtype=0, hd=1), -3), (dict(
         (dict(xs=-64), -2), (dict(xs=65), -4), (dict(x=P + 8), -4), (dict(g=P + 4), -4), (dict(x=None), -1), (dict(g=None), -1), (dict(T=-1), -2)]
 SEQ = KIND + [(dict(B=0, N=0), -2), (dict(N=3), -2), (dict(cu=P), -2), (dict(B=1, N=0, cu=P), -2), (dict(T=1 << 28), -2),
               (dict(B=1, N=1, T=1 << 28, D=512), -2), (dict(B=1, N=(1 << 24) + 1, cu=P), -2), (dict(B=1 << 23, N=1 << 23, T=1), -2),
-              (dict(B=1, N=2, cu=P + 2), -4), (dict(T=257), -6), (dict(T=257, ws=P, wb=1000), -6), (dict(T=257, ws=P + 16, wb=1 << 30), -4)]
+              (dict(B=1, N=2, cu=P + 2), -4), (dict(T=600), -6), (dict(T=600, ws=P, wb=1000), -6), (dict(T=600, ws=P + 16, wb=1 << 30), -4)]
 
 
 @pytest.mark.parametrize("kw,status", SEQ + [(dict(h=None), -1), (dict(h=P + 8), -4), (dict(hT=P + 8), -4), (dict(h0=P + 2), -4), (dict(car=P + 2), -4)])
@@ -96,10 +96,12 @@ def test_sizes():
     assert rows(2, 0, 2, False) == rows(2, 1, 2, False) == rows(2, 256, 2, False) == 2 and rows(2, 257, 2, False) == 4
     assert rows(1, 100, 7, True) == 7 and rows(1, 1000, 7, True) == 7 + 3 and rows(1, 100, 7, False) == 0
     # fewer than 128 tokens a sequence: tiles of 32, where the call is large enough
-    assert rows(1, 1024, 8, True) == 8 + 4 and rows(1, 1023, 8, True) == 8 + 31 and rows(1, 256, 8, True) == 8 + 1 and rows(1, 32, 2, True) == 2 + 1
+    assert rows(1, 1024, 8, True) == 8 + 4 and rows(1, 1025, 9, True) == 9 + 32 and rows(1, 1023, 16, True) == 16 + 3 and rows(1, 1023, 17, True) == 17 + 31 and rows(1, 256, 8, True) == 8 + 1 and rows(1, 32, 2, True) == 2 + 1
     assert rows(64, 64, 64, False) == 128 and rows(63, 64, 63, False) == 63 and rows(64, 128, 64, False) == 64
     assert ws(2, 256, 2, 64, False) == ws(1, 256, 9, 64, True) == 0
-    assert ws(2, 257, 2, 72, False) == 256 + 4 * 128 * 12   # counters, then maps and states of 4 x 2 tiles of 64 channels
+    assert ws(2, 512, 2, 72, False) == ws(1, 1024, 2, 72, True) == ws(1, 512, 1, 72, True) == ws(64, 100, 64, 72, False) == 0   # walked
+    assert ws(2, 513, 2, 72, False) == 256 + 6 * 128 * 12   # counters, then maps and states of 6 x 2 tiles of 64 channels
+    assert ws(17, 512, 17, 2048, False) == 2048 + 34 * 2048 * 12 and ws(16, 512, 16, 2048, False) == 0
     assert ws(1, 1000, 100, 328, True) == 512 + 512 + 131 * 384 * 12
     assert ws(1, 1000, 2, 60, True) == 0 and c_update(T=0, x=None, h=None) == 0 and c_update(T=0, N=0, cu=None, slots=None) == 0
 
@@ -174,7 +176,11 @@ SHAPES = [
     (1, 1, None, 8), (2, 7, None, 72), (3, 256, None, 64), (2, 0, None, 64), (2, 257, None, 136), (1, 3000, None, 40), (5, 600, None, 64),
     (1, 90, [0, 1, 1, 3, 20, 36, 37, 52, 90], 72), (1, 256, [0, 0, 0, 256], 64), (1, 1100, [0, 0, 256, 513, 513, 514, 1026, 1090, 1090], 72),
     (1, 5000, [0, 4700, 4701, 5000], 24), (4, 32, None, 72), (4, 33, None, 72), (3, 20, None, 136), (65, 70, None, 24),
+    # two tiles walked by one work-group, and up to four of 32 tokens
+    (3, 512, None, 72), (1, 510, [0, 7, 510], 72), (1, 500, [0, 0, 490], 40), (1, 420, [0, 130, 390], 24), (1, 400, [0, 400], 136), (48, 127, None, 40),
+    (1, 900, [0, 700, 900], 40), (1, 1024, [0, 0, 3, 1000], 72), (1, 1000, [0, 30, 31, 500, 510, 520, 530, 540, 980], 72),
     # tiles of 32 tokens, one long sequence among short ones
+    (1, 1050, [0, 0, 31, 63, 96, 97, 97, 300, 332, 333, 365, 370, 380, 390, 400, 1040], 72),
     (1, 900, [0, 0, 31, 63, 96, 97, 97, 300, 332, 333, 365, 370, 380, 390, 400, 890], 72),
 ]
 
@@ -325,6 +331,14 @@ def test_bad_offsets_stay_inside_and_end(blend, monkeypatch):
     """Offsets that fall or leave [0, T] are clamped, also where they count more tiles than there is room for."""
     x = make(6, 1, 1000, 5, 64, "bf16")
     t = {n: a.cuda() for n, a in x.items()}
+    short = {n: a[:, :500].contiguous() if n in ("x", "g", "dh") else a for n, a in t.items()}   # walked
+    for offsets in ([-5, 600, 3, 500], [0, 500, 0, 500], [500, 0, 0, 700]):
+        h = torch.zeros_like(short["x"])
+        _, hT, car = gb.gdn_scan_fwd(short["x"], short["g"], torch.ones(3, 64, device="cuda"), cut(offsets), blend=blend, h=h, keep_carries=True)
+        car = torch.nan_to_num(car, 0.0, 0.0, 0.0)
+        gb.gdn_scan_bwd(short["x"], short["g"], short["dh"], car, torch.ones(3, 64, device="cuda"), cut(offsets), blend=blend)
+        torch.cuda.synchronize()
+        assert torch.isfinite(h.float()).all()
     for offsets in ([-5, 600, 3, 2000000000, 0, 1000], [0, 1000, 0, 1000, 0, 1000], [1000, 0, 0, 0, 0, 0], [0, 1000] * 10):
         n = len(offsets) - 1   # 19 of them: tiles of 32
         t["h0"], t["dhT"] = torch.ones(n, 64, device="cuda"), torch.ones(n, 64, device="cuda")
