@@ -272,7 +272,8 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
 // its sequence does). Run lengths are multiples of BL less W - 1: whole blocks.
 //
 // Rows of work-groups below `parts` take four runs each, sum their contributions to dw and db in registers, then over the waves in
-// LDS, and write a partial row [D, W], [D]; those past them take the windows' gradients. No atomics: the same inputs give the same bits.
+// LDS, and write a partial row [D, W], [D] (the gradients themselves if there is only one); those past them take the windows' gradients. No
+// atomics: the same inputs give the same bits.
 constexpr int kConvBlock = 4;   // BL: with 8 in bf16 two waves fit a SIMD instead of three (packed 8054 x 6144: 85 us against 69)
 template <typename T, int W, bool SILU, bool DW>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblocks, int parts, int run) {
@@ -463,13 +464,18 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
             mine[v * (W + 1) + W] = db[v];
         }
         __syncthreads();
-        float* row = p.partial + (long)by * p.D * (W + 1);
+        float* rw = parts > 1 ? p.partial + (long)by * p.D * (W + 1) : p.dweight;
+        float* rb = parts > 1 ? rw + (long)p.D * W : p.dbias;
         for (int i = threadIdx.x; i < 64 * V * (W + 1); i += 256) {
             const int ch = i / (W + 1), j = i % (W + 1);
             const long cc = (long)bx * 64 * V + ch;
             if (cc < p.D) {
                 const float a = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
-                row[j < W ? cc * W + j : (long)p.D * W + cc] = a;
+                if (j < W) {
+                    if (rw) rw[cc * W + j] = a;
+                } else if (rb) {
+                    rb[cc] = a;
+                }
             }
         }
     }
@@ -570,13 +576,14 @@ hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t s) {
 }
 
 // Tokens of a run of the backward pass: as many waves as the device holds at once (three a SIMD, in fp32 two), whole blocks less W - 1, four
-// blocks at least (so that few tokens still spread).
+// blocks at least (so that few tokens still spread). Up to some 240 tokens are four runs, however short: one partial row, which nobody has to sum.
 static int conv_run(int tokens, int D, int W, int bf16) {
     const long cblocks = (D + 64 * V - 1) / (64 * V), most = 4L * kMaxParts;   // at most kMaxParts rows of four runs
     long waves = ((bf16 ? 3072 : 2048) + cblocks - 1) / cblocks;
     waves = waves < most ? waves : most;
     const long len = (tokens + waves - 1) / waves, blocks = (len + W - 1 + kConvBlock - 1) / kConvBlock;
-    return (int)((blocks > 4 ? blocks : 4) * kConvBlock - (W - 1));
+    const long each = ((tokens + 3) / 4 + W - 1 + kConvBlock - 1) / kConvBlock, least = each <= 16 ? each : 4;
+    return (int)((blocks > least ? blocks : least) * kConvBlock - (W - 1));
 }
 static int conv_rows(int tokens, int run) { return (int)(((long)tokens + 4L * run - 1) / (4L * run)); }
 // Rows of partial sums of the backward pass (of bf16 calls; fp32 ones have no more).
@@ -593,7 +600,7 @@ static hipError_t conv_bwd(const ConvProblem& p, hipStream_t s) {
                                 : launch(conv_bwd_kernel<T, W, SILU, false>, grid, block, s, p, cblocks, parts, run);
         if (e != hipSuccess) return e;
     }
-    if (!dw) return hipSuccess;
+    if (!dw || parts == 1) return hipSuccess;
     return launch_column_sum(p.partial, parts, (long)p.D * W, p.D, p.dweight, p.dbias, s);
 }
 

@@ -136,13 +136,17 @@ constexpr int kLnBwdThreads = 512;   // eight waves
 
 // Rows stay as loaded and are unpacked again for each of the three passes over them (two sums each, then the outputs), which leaves room
 // for a lane's weights and sums in registers. Weights read again for every row and pass went through the vector cache at more bytes than the
-// rows themselves: 8192 x 2048 38.8 us a call, 32.6 with them in registers; rows loaded one ahead then gain nothing (33.7).
+// rows themselves: 8192 x 2048 38.8 us a call, 32.6 with them in registers.
+// AHEAD: the next row is loaded while the current one is worked on, where the registers allow. Rows of several waves wait at barriers and gain most
+// (bf16: 4096 x 4096 39 -> 34 us, 2048 x 8192 41 -> 38; fp32: 4096 x 4096 57 -> 53); of the work-groups with eight rows and more only those with
+// short rows of bf16 gain (262144 x 64 47 -> 42, 32768 x 512 31 -> 29; 8192 x 2048 31.4 and 32.2, fp32 262144 x 64 49 and 52).
 // DW: the gradients of weight and bias too. The grid is then layer_norm_parts work-groups, each of which walks its rows with a
 // fixed stride, sums their contributions in registers, then over its row groups in LDS, and writes one partial row
 // [2, d] (weight, bias). No atomics: the same inputs give the same bits.
 template <typename TS, typename TY, int L, int P, bool DW>
 __global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LayerNormProblem p) {
     constexpr int RG = kLnBwdThreads / L;
+    constexpr bool AHEAD = DW && (L > 64 ? P * (2 * sizeof(TS) + sizeof(TY)) <= 24 : P <= 2 && sizeof(TS) + sizeof(TY) < 8);
     __shared__ float red[RG * RowSums<L>::RED];
     __shared__ float part[DW ? RG * 2 * 8 * L : 1];
     const int l = threadIdx.x % L, grp = threadIdx.x / L;
@@ -169,25 +173,38 @@ __global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LayerNorm
             r.get(w[j]);
         }
     }
-    for (long row0 = (long)blockIdx.x * RG; row0 < p.rows; row0 += (long)gridDim.x * RG) {
-        const long row = row0 + grp, rl = min(row, p.rows - 1);
-        const bool ok = row < p.rows;
-        // rows and channels past the end load the last row, the first channels, and are put out of action below
-        Raw8<TS> xr[P], tr[P];
-        Raw8<TY> gr[P];
+    Raw8<TS> xn[AHEAD ? P : 1], tn[AHEAD ? P : 1];
+    Raw8<TY> gn[AHEAD ? P : 1];
+    // rows and channels past the end load the last row, the first channels, and are put out of action below
+    auto load = [&](long row, Raw8<TS> (&x)[P], Raw8<TY> (&g)[P], Raw8<TS> (&t)[P]) {
+        const long rl = min(row, p.rows - 1);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             const int c = 8 * (l + L * j), cl = c < p.d ? c : 0;
-            xr[j].load(static_cast<const TS*>(p.x) + rl * p.x_row + cl);
-            gr[j].load(static_cast<const TY*>(p.dy) + rl * p.d + cl);
-            tr[j].zero();
+            x[j].load(static_cast<const TS*>(p.x) + rl * p.x_row + cl);
+            g[j].load(static_cast<const TY*>(p.dy) + rl * p.d + cl);
+            t[j].zero();
         }
         if (p.dsum) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const int c = 8 * (l + L * j), cl = c < p.d ? c : 0;
-                tr[j].load(static_cast<const TS*>(p.dsum) + rl * p.d + cl);
+                t[j].load(static_cast<const TS*>(p.dsum) + rl * p.d + cl);
             }
+        }
+    };
+    if constexpr (AHEAD) load((long)blockIdx.x * RG + grp, xn, gn, tn);
+    for (long row0 = (long)blockIdx.x * RG; row0 < p.rows; row0 += (long)gridDim.x * RG) {
+        const long row = row0 + grp;
+        const bool ok = row < p.rows;
+        Raw8<TS> xr[P], tr[P];
+        Raw8<TY> gr[P];
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) xr[j] = xn[j], gr[j] = gn[j], tr[j] = tn[j];
+            if (row0 + (long)gridDim.x * RG < p.rows) load(row + (long)gridDim.x * RG, xn, gn, tn);
+        } else {
+            load(row, xr, gr, tr);
         }
         float sum = 0.f, gsum = 0.f;
 #pragma unroll
@@ -259,7 +276,9 @@ __global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LayerNorm
                 float a = 0.f;
 #pragma unroll
                 for (int q = 0; q < RG; ++q) a += part[(q * 2 + which) * 8 * L + c];
-                if (8 * L * j + c < p.d) p.partial[((long)blockIdx.x * 2 + which) * p.d + 8 * L * j + c] = a;
+                // a single work-group's sums are the gradients
+                float* out = gridDim.x > 1 ? p.partial + ((long)blockIdx.x * 2 + which) * p.d : which ? p.dbias : p.dweight;
+                if (out && 8 * L * j + c < p.d) out[8 * L * j + c] = a;
             }
         }
     }
@@ -334,11 +353,11 @@ hipError_t launch_layer_norm_fwd(const LayerNormProblem& p, hipStream_t s) {
 static int ln_lanes(int d) { return d <= 128 ? 16 : d <= 256 ? 32 : d <= 2048 ? 64 : d <= 8192 ? 256 : 512; }
 
 // Work-groups (and partial rows) of the backward pass with gradients of weight and bias: one per CU, but no more than there
-// are groups of rows.
+// are groups of rows; one for two groups, which saves the launch that sums partial rows.
 int layer_norm_parts(long rows, int d) {
     const int rg = kLnBwdThreads / ln_lanes(d);
     const long blocks = (rows + rg - 1) / rg;
-    return (int)(blocks < 256 ? blocks : 256);
+    return (int)(blocks == 2 ? 1 : blocks < 256 ? blocks : 256);
 }
 
 template <typename TS, typename TY>
@@ -353,7 +372,7 @@ static hipError_t ln_bwd(const LayerNormProblem& p, hipStream_t s) {
         const int parts = layer_norm_parts(p.rows, p.d);
         if (parts > 0) {
             const hipError_t e = launch(layer_norm_bwd_kernel<TS, TY, L, P, true>, dim3((unsigned)parts), dim3(kLnBwdThreads), s, p);
-            if (e != hipSuccess) return e;
+            if (e != hipSuccess || parts == 1) return e;
         }
         return launch_column_sum(p.partial, parts, p.d, p.d, p.dweight, p.dbias, s);
     });
