@@ -579,7 +579,7 @@ hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t s) {
 // blocks at least (so that few tokens still spread). Up to some 240 tokens are four runs, however short: one partial row, which nobody has to sum.
 static int conv_run(int tokens, int D, int W, int bf16) {
     const long cblocks = (D + 64 * V - 1) / (64 * V), most = 4L * kMaxParts;   // at most kMaxParts rows of four runs
-    long waves = ((bf16 ? 3072 : 2048) + cblocks - 1) / cblocks;
+    long waves = ((bf16 ? 3 : 2) * 1024L + cblocks - 1) / cblocks;
     waves = waves < most ? waves : most;
     const long len = (tokens + waves - 1) / waves, blocks = (len + W - 1 + kConvBlock - 1) / kConvBlock;
     const long each = ((tokens + 3) / 4 + W - 1 + kConvBlock - 1) / kConvBlock, least = each <= 16 ? each : 4;
