@@ -871,7 +871,7 @@ int check_scan(const void* x, const float* g, const int32_t* cu, int B, int T, i
 
 GDN_EXPORT int64_t gdn_scan_carry_rows(int B, int T, int N, int varlen) {
     if (channel_shape(B, T, N, 8, varlen != 0) != GDN_OK) return 0;
-    return gdn::scan_layout(B * T, T, N, 8, varlen != 0).rows;
+    return gdn::scan_layout(B * T, T, N, 8, varlen != 0).carry_rows;
 }
 
 GDN_EXPORT size_t gdn_scan_workspace_bytes(int B, int T, int N, int D, int varlen) {

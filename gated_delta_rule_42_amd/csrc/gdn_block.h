@@ -93,7 +93,7 @@ struct ScanProblem {
 // Tokens of a tile, rows of tiles (an upper bound with cu_seqlens), and the workspace of a scan.
 struct ScanLayout {
     int tile;
-    long rows;
+    long rows, carry_rows;
     size_t off_base, off_agg, off_pref, total;   // total 0: a work-group walks a sequence's tiles, no workspace
 };
 ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen);

@@ -154,8 +154,47 @@ __device__ __forceinline__ float one_minus_exp(float g, float a) {
     return fabsf(g) < 0.5f ? -g * s : 1.f - a;
 }
 
-// Clears the marks and the tickets, and lays the tiles of packed sequences out.
+// Lays the tiles of packed sequences out, by one work-group: K sequences a thread at a time.
+template <int K>
+__device__ __forceinline__ void lay_tiles_out(const ScanProblem& p, int* sum) {
+    int before = 0;
+    for (int n0 = 0; n0 < p.N; n0 += 256 * K) {
+        const int n = n0 + K * threadIdx.x;
+        int cu[K + 1], tiles[K], mine = 0;
+#pragma unroll
+        for (int i = 0; i <= K; ++i) cu[i] = p.cu_seqlens[min(n + i, p.N)];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int lo = min(max(cu[i], 0), p.tokens), hi = min(max(cu[i + 1], lo), p.tokens);
+            tiles[i] = n + i < p.N ? max(1, (hi - lo + p.tile - 1) / p.tile) : 0;
+            mine += tiles[i];
+        }
+        mine = (int)min((long)mine, p.rows);   // fewer than 2^23: the sums fit
+        __syncthreads();
+        sum[threadIdx.x] = mine;
+        __syncthreads();
+        for (int d = 1; d < 256; d *= 2) {
+            const int add = (int)threadIdx.x >= d ? sum[threadIdx.x - d] : 0;
+            __syncthreads();
+            sum[threadIdx.x] += add;
+            __syncthreads();
+        }
+        // offsets that fall can count more tiles than there are rows: those past the last row are not run
+        long first = (long)before + sum[threadIdx.x] - mine;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            if (n + i < p.N) p.base[n + i] = (int)min(first, p.rows);
+            first += tiles[i];
+        }
+        before = (int)min((long)before + sum[255], p.rows);
+    }
+    if (threadIdx.x == 0) p.base[p.N] = before;
+}
+
+// Clears the marks and the tickets, and lays the tiles of packed sequences out: 16 sequences a thread where they are many (a call on 8192
+// sequences 340 -> 311 us), one where they are few (8 sequences, both directions 55.5 -> 53.5).
 __global__ __launch_bounds__(256) void scan_setup_kernel(ScanProblem p) {
+    __shared__ int sum[256];
     const long words = p.rows * p.ncb * kScanChannels;   // agg: 2 a word, pref: 1
     const long at = (long)blockIdx.x * 256 + threadIdx.x, step = (long)gridDim.x * 256;
     uint4* a = reinterpret_cast<uint4*>(p.agg);
@@ -166,29 +205,8 @@ __global__ __launch_bounds__(256) void scan_setup_kernel(ScanProblem p) {
     if (blockIdx.x != 0) return;
     for (int i = threadIdx.x; i < p.ncb; i += 256) p.ticket[kTicketWords * i] = 0;
     if (!p.base) return;
-    __shared__ int sum[256];
-    int before = 0;
-    for (int n0 = 0; n0 < p.N; n0 += 256) {
-        const int n = n0 + threadIdx.x;
-        int tiles = 0;
-        if (n < p.N) {
-            const int lo = min(max(p.cu_seqlens[n], 0), p.tokens), hi = min(max(p.cu_seqlens[n + 1], lo), p.tokens);
-            tiles = max(1, (hi - lo + p.tile - 1) / p.tile);
-        }
-        __syncthreads();
-        sum[threadIdx.x] = tiles;
-        __syncthreads();
-        for (int d = 1; d < 256; d *= 2) {
-            const int add = (int)threadIdx.x >= d ? sum[threadIdx.x - d] : 0;
-            __syncthreads();
-            sum[threadIdx.x] += add;
-            __syncthreads();
-        }
-        // offsets that fall can count more tiles than there are rows: those past the last row are not run
-        if (n < p.N) p.base[n] = (int)min((long)before + sum[threadIdx.x] - tiles, p.rows);
-        before = (int)min((long)before + sum[255], p.rows);
-    }
-    if (threadIdx.x == 0) p.base[p.N] = before;
+    if (p.N <= 512) lay_tiles_out<1>(p, sum);
+    else lay_tiles_out<16>(p, sum);
 }
 
 constexpr int R = 4;   // tokens per thread
@@ -548,16 +566,19 @@ __global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblo
 // Where no sequence can have more than two tiles (four of 32 tokens) one work-group walks them all, which saves that pass and the wait for other
 // work-groups (1 x 512 x 2048, a call: 17.5 and 13.5 us, backward 18.5 and 15.0; 128 x 64 x 2048 in tiles of 32: 31.9 and 27.8, 50.1 and 48.4), as long as
 // the device holds all of them at once (64 x 512 x 2048: 98 and 99, backward 183 and 206). Three tiles gain no more (8 x 700 x 1024: 17.9 and
-// 15.7, backward 20.6 and 22.8), but packed sequences are as a rule far shorter than all of them together: there the call may have four.
+// 15.7, backward 20.6 and 22.8), but packed sequences are as a rule far shorter than all of them together: there the call may have four, which goes
+// before tiles of 32 (40 sequences of 25 tokens, 512 channels: 17.7 and 13.3, backward 18.2 and 14.4).
 ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen) {
     ScanLayout w{};
     const long ncb = ((long)D + kScanChannels - 1) / kScanChannels;
     const int longest = varlen ? tokens : T;   // the longest that a sequence can be
-    const bool large = varlen ? tokens > 1024 || (tokens > 256 && N > 16) : tokens >= 4096;
-    w.tile = longest <= 32 || (large && tokens < 128L * N) ? 32 : 256;
+    const bool brief = longest <= 32 || (tokens >= (varlen ? 257 : 4096) && tokens < 128L * N), at_once = N * ncb <= 512;
+    const bool few = varlen && N > 1 && tokens <= 1024 && at_once;
+    w.tile = brief && !(few && longest > 32) ? 32 : 256;
     const long per = T > w.tile ? ((long)T + w.tile - 1) / w.tile : 1;
+    w.carry_rows = varlen ? (long)N + tokens / (brief ? 32 : 256) : N * per;   // whatever the channels are
     w.rows = varlen ? (long)N + tokens / w.tile : N * per;
-    if (w.tile == 32 ? longest <= 128 : longest <= w.tile || (longest <= (varlen && N > 1 ? 1024 : 512) && N * ncb <= 512)) return w;
+    if (w.tile == 32 ? longest <= 128 : longest <= 256 || few || (longest <= 512 && at_once)) return w;
     const size_t cells = (size_t)w.rows * ncb * kScanChannels;
     w.off_base = ((size_t)kTicketWords * 4 * ncb + 255) / 256 * 256;
     w.off_agg = w.off_base + (varlen ? (((size_t)N + 1) * 4 + 255) / 256 * 256 : 0);

@@ -565,10 +565,9 @@ int gdn_conv_update(const void *x, const float *weight, const float *bias, void 
  *   h0          fp32 [N, D] or NULL (zeros)
  *   cu_seqlens  int32 [N + 1] device array of packed sequences (then B = 1) or NULL (N = B)
  *   h           [B, T, D] h_dtype (GDN_BF16 only for bf16 x), dense; hT fp32 [N, D]: the state behind each sequence, or NULL
- *   carries     fp32 [gdn_scan_carry_rows(...), D] or NULL: the state entering every tile of a sequence, for the backward pass. A tile has 256
- *               tokens, or 32 where no sequence can have more and, in calls of 4096 tokens (packed: 257) and more, where sequences have fewer than 128
- *               on average; a sequence has
- *               one tile at least, those of one sequence follow each other, and rows that are no tile's are not written
+ *   carries     fp32 [gdn_scan_carry_rows(...), D] or NULL: the state entering every tile of a sequence, for the backward pass. A tile
+ *               has 256 tokens, or 32 where sequences are short on average; a sequence has one tile at least, those of one sequence
+ *               follow each other, and rows that are no tile's are not written
  *   workspace   gdn_scan_workspace_bytes(...) bytes, 256-byte aligned; none (0) where all sequences are short. Its
  *               contents need not be set and mean nothing afterwards; calls that can run at once need one each
  *   D           a multiple of 8 up to 2^20; B * T <= 2^28, B * T * D <= 2^36, N <= 2^24, N * D <= 2^31 and tiles *

@@ -96,13 +96,13 @@ def test_sizes():
     assert rows(2, 0, 2, False) == rows(2, 1, 2, False) == rows(2, 256, 2, False) == 2 and rows(2, 257, 2, False) == 4
     assert rows(1, 100, 7, True) == 7 and rows(1, 1000, 7, True) == 7 + 3 and rows(1, 100, 7, False) == 0
     # fewer than 128 tokens a sequence: tiles of 32, where the call is large enough
-    assert rows(1, 1024, 8, True) == 8 + 4 and rows(1, 1025, 9, True) == 9 + 32 and rows(1, 1023, 16, True) == 16 + 3 and rows(1, 1023, 17, True) == 17 + 31 and rows(1, 256, 8, True) == 8 + 1 and rows(1, 32, 2, True) == 2 + 1
+    assert rows(1, 1024, 8, True) == 8 + 4 and rows(1, 1025, 9, True) == 9 + 32 and rows(1, 1023, 8, True) == 8 + 31 and rows(1, 1023, 7, True) == 7 + 3 and rows(1, 256, 8, True) == 8 + 1 and rows(1, 32, 2, True) == 2 + 1
     assert rows(64, 64, 64, False) == 128 and rows(63, 64, 63, False) == 63 and rows(64, 128, 64, False) == 64
     assert ws(2, 256, 2, 64, False) == ws(1, 256, 9, 64, True) == 0
     assert ws(2, 512, 2, 72, False) == ws(1, 1024, 2, 72, True) == ws(1, 512, 1, 72, True) == ws(64, 100, 64, 72, False) == 0   # walked
     assert ws(2, 513, 2, 72, False) == 256 + 6 * 128 * 12   # counters, then maps and states of 6 x 2 tiles of 64 channels
     assert ws(17, 512, 17, 2048, False) == 2048 + 34 * 2048 * 12 and ws(16, 512, 16, 2048, False) == 0
-    assert ws(1, 1000, 100, 328, True) == 512 + 512 + 131 * 384 * 12
+    assert ws(1, 1000, 100, 328, True) == 512 + 512 + 131 * 384 * 12 and ws(1, 1000, 85, 328, True) == 0
     assert ws(1, 1000, 2, 60, True) == 0 and c_update(T=0, x=None, h=None) == 0 and c_update(T=0, N=0, cu=None, slots=None) == 0
 
 
@@ -178,7 +178,7 @@ SHAPES = [
     (1, 5000, [0, 4700, 4701, 5000], 24), (4, 32, None, 72), (4, 33, None, 72), (3, 20, None, 136), (65, 70, None, 24),
     # two tiles walked by one work-group, and up to four of 32 tokens
     (3, 512, None, 72), (1, 510, [0, 7, 510], 72), (1, 500, [0, 0, 490], 40), (1, 420, [0, 130, 390], 24), (1, 400, [0, 400], 136), (48, 127, None, 40),
-    (1, 900, [0, 700, 900], 40), (1, 1024, [0, 0, 3, 1000], 72), (1, 1000, [0, 30, 31, 500, 510, 520, 530, 540, 980], 72),
+    (1, 900, [0, 700, 900], 40), (1, 1024, [0, 0, 3, 1000], 72), (1, 600, [*range(0, 600, 60), 600], 3336), (1, 1000, [0, 30, 31, 500, 510, 520, 530, 540, 980], 72),
     # tiles of 32 tokens, one long sequence among short ones
     (1, 1050, [0, 0, 31, 63, 96, 97, 97, 300, 332, 333, 365, 370, 380, 390, 400, 1040], 72),
     (1, 900, [0, 0, 31, 63, 96, 97, 97, 300, 332, 333, 365, 370, 380, 390, 400, 890], 72),
@@ -255,6 +255,17 @@ def test_many_short_sequences(blend):
     inside(dx[..., at], rx, ex, "dx")
     inside(dg[..., at], rg, eg, "dg")
     inside(dh0[..., at], r0, e0, "dh0")
+
+
+@pytest.mark.gpu
+def test_thousands_of_sequences():
+    """More sequences than one step of the tiles' layout takes, many of them empty, one of many tiles behind the first thousands."""
+    gen = torch.Generator().manual_seed(8)
+    lens = torch.randint(0, 4, (9001,), generator=gen).tolist()
+    lens[8000] = 300
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    print(f"[gpu] scan {len(lens)} sequences, {cu[-1]} tokens", flush=True)
+    check_pass(make(13, 1, cu[-1], len(lens), 8, "f32"), cu, True)
 
 
 @pytest.mark.gpu
@@ -339,15 +350,17 @@ def test_bad_offsets_stay_inside_and_end(blend, monkeypatch):
         gb.gdn_scan_bwd(short["x"], short["g"], short["dh"], car, torch.ones(3, 64, device="cuda"), cut(offsets), blend=blend)
         torch.cuda.synchronize()
         assert torch.isfinite(h.float()).all()
-    for offsets in ([-5, 600, 3, 2000000000, 0, 1000], [0, 1000, 0, 1000, 0, 1000], [1000, 0, 0, 0, 0, 0], [0, 1000] * 10):
-        n = len(offsets) - 1   # 19 of them: tiles of 32
-        t["h0"], t["dhT"] = torch.ones(n, 64, device="cuda"), torch.ones(n, 64, device="cuda")
-        h = torch.zeros_like(t["x"])
-        _, hT, car = gb.gdn_scan_fwd(t["x"], t["g"], t["h0"], cut(offsets), blend=blend, h=h, keep_carries=True)
-        car = torch.nan_to_num(car, 0.0, 0.0, 0.0)   # rows past the last tile hold anything
-        gb.gdn_scan_bwd(t["x"], t["g"], t["dh"], car, t["dhT"], cut(offsets), blend=blend)
-        torch.cuda.synchronize()
-        assert torch.isfinite(h.float()).all()
+    for T in (1000, 1500):   # walked; passed on between work-groups
+        u = {n: a.cuda() for n, a in make(6, 1, T, 5, 64, "bf16").items()}
+        for offsets in ([-5, 600, 3, 2000000000, 0, T], [0, T, 0, T, 0, T], [T, 0, 0, 0, 0, 0], [0, T] * 10):
+            n = len(offsets) - 1   # 19 of them: tiles of 32
+            h0 = torch.ones(n, 64, device="cuda")
+            h = torch.zeros_like(u["x"])
+            _, hT, car = gb.gdn_scan_fwd(u["x"], u["g"], h0, cut(offsets), blend=blend, h=h, keep_carries=True)
+            car = torch.nan_to_num(car, 0.0, 0.0, 0.0)   # rows past the last tile hold anything
+            gb.gdn_scan_bwd(u["x"], u["g"], u["dh"], car, h0, cut(offsets), blend=blend)
+            torch.cuda.synchronize()
+            assert torch.isfinite(h.float()).all()
     t["h0"] = x["h0"].cuda()
     slots = torch.arange(5, dtype=torch.int32, device="cuda")
     gb.gdn_scan_update(t["x"][0], t["g"][0], t["h0"].clone(), slots, cut([-5, 600, 3, 2000000000, 0, 1000]), blend=blend)
