@@ -654,7 +654,7 @@ namespace {
 bool dtype_ok(int t) { return t == GDN_F32 || t == GDN_BF16; }
 int per16(int dtype) { return dtype == GDN_BF16 ? 8 : 4; }   // elements of 16 bytes
 
-// Rows of layer norm: a row takes 16 lanes up to 128 channels and at most a lane per 8 channels past that, fewer than 2^32 in all.
+// Sizes of layer norm.
 int layer_norm_shape(int rows, int d) {
     if (d < 8 || d > 16384 || d % 8) return GDN_ERR_UNSUPPORTED;
     if (rows < 0 || rows >= 1 << 28 || (long long)rows * d >= 1LL << 35) return GDN_ERR_SHAPE;

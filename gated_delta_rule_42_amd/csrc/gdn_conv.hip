@@ -143,20 +143,23 @@ __device__ __forceinline__ void move_on(float (&u)[W][V]) {
         for (int v = 0; v < V; ++v) u[j][v] = u[j - 1][v];
 }
 
-// Work-groups in rows of cblocks, which share tokens; those past the `tiles` rows of tiles leave the windows, a wave per sequence.
+// Work-groups in rows of cblocks, which share tokens; those past the `tiles` rows of tiles leave the windows, a wave per sequence. TL = 6 tokens a wave:
+// with fewer the rows before a tile weigh more, with more there are fewer waves (4 x 2048 x 6144 bf16, TL 4, 6, 8, 12: 41.5, 38.6, 40.0, 40.5 us; fp32
+// 70.7, 69.8, 71.6, 74.7; 8 x 500 x 2048 9.2, 9.0, 9.7, 10.7). Bound by bytes: 5.2 TB/s.
 template <typename T, int W, int TL, bool SILU>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvProblem p, int cblocks, int tiles) {
     using Raw = Raw4<T>;
     __shared__ int seq[4][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // scalar, and so are tokens and masks
-    const int by = (int)(blockIdx.x / (unsigned)cblocks), bx = (int)(blockIdx.x - (unsigned)by * (unsigned)cblocks);
+    const unsigned id = blockIdx.y * gridDim.x + blockIdx.x;   // y: past 2^32 threads
+    const int by = (int)(id / (unsigned)cblocks), bx = (int)(id - (unsigned)by * (unsigned)cblocks);
     const long c0 = ((long)bx * 64 + lane) * V;
     const bool in = c0 < p.D;
     const long c = in ? c0 : 0;   // lanes past the channels go along with the first ones and store nothing
     const unsigned cb = (unsigned)c * sizeof(T);
     if (by >= tiles) {
         const int n = (by - tiles) * 4 + wave;
-        if (n < p.N && in) leave_window<T, W>(p, n, c);
+        if (p.windowT && n < p.N && in) leave_window<T, W>(p, n, c);
         return;
     }
     const long first = ((long)by * 4 + wave) * TL;
@@ -269,7 +272,8 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
 
 // Backward, a wave walks a run of tokens, blocks of BL at a time, the next block's rows in flight while the current one is worked on. It
 // carries the last W - 1 inputs and dz; a token's dx is complete W - 1 tokens later, so that a run goes W - 1 tokens past its end (where
-// its sequence does). Run lengths are multiples of BL less W - 1: whole blocks.
+// its sequence does). Run lengths are multiples of BL less W - 1: whole blocks. Packed 8054 x 6144 in bf16: 71 us at 4.6 TB/s, the rate of the largest
+// copies, with 40 us of vector instructions close behind (24 an element).
 //
 // Rows of work-groups below `parts` take four runs each, sum their contributions to dw and db in registers, then over the waves in
 // LDS, and write a partial row [D, W], [D] (the gradients themselves if there is only one); those past them take the windows' gradients. No
@@ -482,7 +486,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
 }
 
 // Runs of tokens on a pool of windows: a lane walks its sequence's tokens for V channels. The window stays as loaded, so its rows
-// are moved, never rounded. Tokens come four at a time.
+// are moved, never rounded. Tokens come four at a time. 256 sequences of one token, 12288 channels in bf16: 11.7 us, bound by bytes (4.3 TB/s).
 template <typename T, int W>
 __global__ __launch_bounds__(256) void conv_update_kernel(ConvProblem p, int cblocks) {
     using Raw = Raw4<T>;
@@ -560,12 +564,13 @@ static hipError_t conv_taps(int W, F f) {
 template <typename T>
 static hipError_t conv_fwd(const ConvProblem& p, hipStream_t s) {
     return conv_taps(p.W, [&](auto taps) {
-        constexpr int W = decltype(taps)::value, TL = 12;
+        constexpr int W = decltype(taps)::value, TL = 6;
         const int tiles = (int)(((long)p.tokens + 4 * TL - 1) / (4 * TL));
         const int cblocks = (p.D + 64 * V - 1) / (64 * V);
         const long groups = (long)cblocks * (tiles + (p.windowT ? (p.N + 3) / 4 : 0));
         if (groups == 0) return hipSuccess;
-        const dim3 grid((unsigned)groups), block(256);
+        constexpr long kMost = 1 << 23;   // work-groups along x
+        const dim3 grid((unsigned)(groups < kMost ? groups : kMost), (unsigned)((groups + kMost - 1) / kMost)), block(256);
         if (p.silu) return launch(conv_fwd_kernel<T, W, TL, true>, grid, block, s, p, cblocks, tiles);
         return launch(conv_fwd_kernel<T, W, TL, false>, grid, block, s, p, cblocks, tiles);
     });
@@ -576,13 +581,14 @@ hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t s) {
 }
 
 // Tokens of a run of the backward pass: as many waves as the device holds at once (three a SIMD, in fp32 two), whole blocks less W - 1, four
-// blocks at least (so that few tokens still spread). Up to some 240 tokens are four runs, however short: one partial row, which nobody has to sum.
+// blocks at least (so that few tokens still spread). Up to some 110 tokens are four runs of up to eight blocks: one partial row, which nobody has to
+// sum (100 tokens 18.7 and 16.4 us a call; 230 would take 18.5 and 24).
 static int conv_run(int tokens, int D, int W, int bf16) {
     const long cblocks = (D + 64 * V - 1) / (64 * V), most = 4L * kMaxParts;   // at most kMaxParts rows of four runs
     long waves = ((bf16 ? 3 : 2) * 1024L + cblocks - 1) / cblocks;
     waves = waves < most ? waves : most;
     const long len = (tokens + waves - 1) / waves, blocks = (len + W - 1 + kConvBlock - 1) / kConvBlock;
-    const long each = ((tokens + 3) / 4 + W - 1 + kConvBlock - 1) / kConvBlock, least = each <= 16 ? each : 4;
+    const long each = ((tokens + 3) / 4 + W - 1 + kConvBlock - 1) / kConvBlock, least = each <= 8 ? each : 4;
     return (int)((blocks > least ? blocks : least) * kConvBlock - (W - 1));
 }
 static int conv_rows(int tokens, int run) { return (int)(((long)tokens + 4L * run - 1) / (4L * run)); }

@@ -57,12 +57,14 @@ struct RowSums {
 // Threads of a forward work-group: four waves, or a row's eight.
 constexpr int ln_fwd_threads(int L) { return L > 256 ? L : 256; }
 
+// A row's pieces are in flight together and nothing else is in the way: 8192 x 2048 in bf16 with the residual 23 us, 5.8 TB/s. Weights come from the
+// caches once a row (in registers across rows 32768 x 2048 took 100 to 114 us instead of 95).
 template <typename TX, typename TS, typename TY, int L, int P>
 __global__ __launch_bounds__(ln_fwd_threads(L)) void layer_norm_fwd_kernel(LayerNormProblem p) {
     __shared__ float red[RowSums<L>::RED];
     RowSums<L> rs(red);
     const int l = threadIdx.x % L;
-    const long row = (long)blockIdx.x * (ln_fwd_threads(L) / L) + threadIdx.x / L;
+    const long row = ((long)blockIdx.y * gridDim.x + blockIdx.x) * (ln_fwd_threads(L) / L) + threadIdx.x / L;   // y: past 2^32 threads
     const bool ok = row < p.rows;
     const TX* xp = static_cast<const TX*>(p.x) + row * p.x_row;
     const TS* rp = static_cast<const TS*>(p.residual) + row * p.r_row;
@@ -339,7 +341,10 @@ static hipError_t ln_fwd(const LayerNormProblem& p, hipStream_t s) {
     return ln_shape(p.d, [&](auto lanes, auto pieces) {
         constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value;
         constexpr int NT = ln_fwd_threads(L), RG = NT / L;
-        return launch(layer_norm_fwd_kernel<TX, TS, TY, L, P>, dim3((unsigned)((p.rows + RG - 1) / RG)), dim3(NT), s, p);
+        constexpr long kMost = 1 << 22;   // work-groups along x
+        const long groups = (p.rows + RG - 1) / RG;
+        const dim3 grid((unsigned)(groups < kMost ? groups : kMost), (unsigned)((groups + kMost - 1) / kMost));
+        return launch(layer_norm_fwd_kernel<TX, TS, TY, L, P>, grid, dim3(NT), s, p);
     });
 }
 
@@ -366,8 +371,9 @@ static hipError_t ln_bwd(const LayerNormProblem& p, hipStream_t s) {
         constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value, RG = kLnBwdThreads / L;
         if (!p.dweight && !p.dbias) {
             if (p.rows == 0) return hipSuccess;
+            constexpr long kMost = 1 << 22;   // work-groups, which go on to further rows
             const long groups = (p.rows + RG - 1) / RG;
-            return launch(layer_norm_bwd_kernel<TS, TY, L, P, false>, dim3((unsigned)groups), dim3(kLnBwdThreads), s, p);
+            return launch(layer_norm_bwd_kernel<TS, TY, L, P, false>, dim3((unsigned)(groups < kMost ? groups : kMost)), dim3(kLnBwdThreads), s, p);
         }
         const int parts = layer_norm_parts(p.rows, p.d);
         if (parts > 0) {

@@ -283,6 +283,25 @@ def test_graph_replay_streams_and_repeats():
 
 
 @pytest.mark.gpu
+def test_more_lanes_than_32_bits():
+    """2^32 lanes and more (32 for a row of 136 channels) of one broadcast row; without the weights' gradients backward."""
+    rows, d = (1 << 27) + 40, 136
+    if torch.cuda.mem_get_info()[0] < 110 << 30:
+        pytest.skip("needs 110 GiB")
+    print(f"[gpu] layer norm {rows} x {d}", flush=True)
+    x = torch.randn(1, d, device="cuda").bfloat16()
+    one, _ = gb.gdn_layer_norm_fwd(x)
+    y, _ = gb.gdn_layer_norm_fwd(x.expand(rows, d), y=torch.zeros(rows, d, device="cuda", dtype=torch.bfloat16))
+    at = torch.tensor([0, 1, (1 << 26) - 1, 1 << 26, (1 << 27) - 1, 1 << 27, rows - 1], device="cuda")
+    assert torch.equal(y[at], one.expand(len(at), d))
+    dy = torch.randn(1, d, device="cuda").bfloat16()
+    want, _, _ = gb.gdn_layer_norm_bwd(x, dy)
+    y.copy_(dy.expand(rows, d))
+    dx, _, _ = gb.gdn_layer_norm_bwd(x.expand(rows, d), y, dx=torch.zeros(rows, d, device="cuda", dtype=torch.bfloat16))
+    assert torch.equal(dx[at], want.expand(len(at), d))
+
+
+@pytest.mark.gpu
 def test_rows_past_32_bits():
     """Rows whose elements start past 2^31 (a view of strided rows of 8.6 GB)."""
     big = torch.zeros(33000, 131072, device="cuda", dtype=torch.bfloat16)
