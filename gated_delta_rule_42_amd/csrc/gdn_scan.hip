@@ -230,108 +230,108 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
     if (row >= rows) return;
     ScanTile tile = scan_tile(p, row, rows, false);
     float state = 0.f;   // walking, a lane of the first wave's channel: what leaves the tile
-  for (;;) {
-    unsigned thread = threadIdx.x;
-    asm volatile("" : "+v"(thread));   // what is computed from it is not kept from one tile to the next
-    const int l = thread & 7, grp = thread >> 3;
-    const unsigned c = (unsigned)(cb * kScanChannels + 8 * l);
-    const bool in = c < (unsigned)p.D;
-    // offsets within a tile fit 32 bits (256 tokens of at most 2^20 channels); only x may lie further apart
-    const unsigned at0 = (unsigned)(grp * R) * p.D + c;
-    Raw8<TX> xr[R];
-    Raw8<float> gr[R];
-    const long first = (long)tile.t0 * p.D;
-    const int mine = min(max(tile.len - grp * R, 0), R);   // this thread's tokens
-    // every thread loads: tokens past the end the last one again, channels past the end the first ones, put out of action below. (A branch
-    // around each load, and the compiler waits for it before the next.)
-    const unsigned cl = in ? c : 0;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        xr[i].zero();
-        gr[i].zero();
-    }
-    if (tile.len > 0) {
+    for (;;) {
+        unsigned thread = threadIdx.x;
+        asm volatile("" : "+v"(thread));   // what is computed from it is not kept from one tile to the next
+        const int l = thread & 7, grp = thread >> 3;
+        const unsigned c = (unsigned)(cb * kScanChannels + 8 * l);
+        const bool in = c < (unsigned)p.D;
+        // offsets within a tile fit 32 bits (256 tokens of at most 2^20 channels); only x may lie further apart
+        const unsigned at0 = (unsigned)(grp * R) * p.D + c;
+        Raw8<TX> xr[R];
+        Raw8<float> gr[R];
+        const long first = (long)tile.t0 * p.D;
+        const int mine = min(max(tile.len - grp * R, 0), R);   // this thread's tokens
+        // every thread loads: tokens past the end the last one again, channels past the end the first ones, put out of action below. (A branch
+        // around each load, and the compiler waits for it before the next.)
+        const unsigned cl = in ? c : 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int t = min(grp * R + i, tile.len - 1);
-            gr[i].load(p.g + first + ((unsigned)t * (unsigned)p.D + cl));
-            xr[i].load(static_cast<const TX*>(p.x) + (tile.t0 + t) * p.x_row + cl);
+            xr[i].zero();
+            gr[i].zero();
         }
-    }
-    float a[R][8], b[BLEND ? R : 1][8], A[8], H[8];
+        if (tile.len > 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) A[e] = 1.f, H[e] = 0.f;
+            for (int i = 0; i < R; ++i) {
+                const int t = min(grp * R + i, tile.len - 1);
+                gr[i].load(p.g + first + ((unsigned)t * (unsigned)p.D + cl));
+                xr[i].load(static_cast<const TX*>(p.x) + (tile.t0 + t) * p.x_row + cl);
+            }
+        }
+        float a[R][8], b[BLEND ? R : 1][8], A[8], H[8];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {   // tokens past the end: g = 0, x = 0, the state as it is
-        float x[8];
-        gr[i].get(a[i]);
-        xr[i].get(x);
+        for (int e = 0; e < 8; ++e) A[e] = 1.f, H[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {   // tokens past the end: g = 0, x = 0, the state as it is
+            float x[8];
+            gr[i].get(a[i]);
+            xr[i].get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float g = i < mine ? a[i][e] : 0.f;
+                x[e] = i < mine ? x[e] : 0.f;
+                a[i][e] = __expf(g);
+                if constexpr (BLEND) {
+                    x[e] *= one_minus_exp(g, a[i][e]);
+                    b[i][e] = x[e];
+                }
+                H[e] = __fmaf_rn(a[i][e], H[e], x[e]);
+                A[e] *= a[i][e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) maps[grp][8 * l + e] = make_float2(A[e], H[e]);
+        __syncthreads();
+        if (thread < kScanChannels) {
+            const int ch = thread;
+            const unsigned col = (unsigned)(cb * kScanChannels + ch);
+            const bool real = col < (unsigned)p.D;
+            float At = 1.f, Ht = 0.f;   // the map of the groups before each, in its place
+#pragma unroll 16
+            for (int k = 0; k < G; ++k) {
+                const float2 m = maps[k][ch];
+                maps[k][ch] = make_float2(At, Ht);
+                Ht = __fmaf_rn(m.x, Ht, m.y);
+                At *= m.x;
+            }
+            const long at = row * p.ncb * kScanChannels + col;
+            float h = state;
+            if (tile.s == 0) {
+                if (p.h0 && real) h = p.h0[(long)tile.n * p.D + col];
+            } else if (p.ticket) {
+                publish_map(p.agg + at, At, Ht);
+                h = enter_from(p, row, -1, tile.s, col);
+            }
+            state = __fmaf_rn(At, h, Ht);
+            if (p.ticket && tile.s < tile.last) publish_state(p.pref + at, state);
+            if (p.carries && real) p.carries[tile.row * p.D + col] = h;
+            enter[ch] = h;
+        }
+        __syncthreads();
+        if constexpr (!BLEND) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) xr[i].hide();
+        }
+        float h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float g = i < mine ? a[i][e] : 0.f;
-            x[e] = i < mine ? x[e] : 0.f;
-            a[i][e] = __expf(g);
-            if constexpr (BLEND) {
-                x[e] *= one_minus_exp(g, a[i][e]);
-                b[i][e] = x[e];
-            }
-            H[e] = __fmaf_rn(a[i][e], H[e], x[e]);
-            A[e] *= a[i][e];
+            const float2 m = maps[grp][8 * l + e];
+            h[e] = __fmaf_rn(m.x, enter[8 * l + e], m.y);
         }
-    }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) maps[grp][8 * l + e] = make_float2(A[e], H[e]);
-    __syncthreads();
-    if (thread < kScanChannels) {
-        const int ch = thread;
-        const unsigned col = (unsigned)(cb * kScanChannels + ch);
-        const bool real = col < (unsigned)p.D;
-        float At = 1.f, Ht = 0.f;   // the map of the groups before each, in its place
-#pragma unroll 16
-        for (int k = 0; k < G; ++k) {
-            const float2 m = maps[k][ch];
-            maps[k][ch] = make_float2(At, Ht);
-            Ht = __fmaf_rn(m.x, Ht, m.y);
-            At *= m.x;
+        for (int i = 0; i < R; ++i) {
+            float x[8];
+            if constexpr (!BLEND) xr[i].get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = __fmaf_rn(a[i][e], h[e], BLEND ? b[i][e] : i < mine ? x[e] : 0.f);
+            if (in && i < mine) store8<NT>(static_cast<TH*>(p.h) + first + (at0 + i * p.D), h);
         }
-        const long at = row * p.ncb * kScanChannels + col;
-        float h = state;
-        if (tile.s == 0) {
-            if (p.h0 && real) h = p.h0[(long)tile.n * p.D + col];
-        } else if (p.ticket) {
-            publish_map(p.agg + at, At, Ht);
-            h = enter_from(p, row, -1, tile.s, col);
-        }
-        state = __fmaf_rn(At, h, Ht);
-        if (p.ticket && tile.s < tile.last) publish_state(p.pref + at, state);
-        if (p.carries && real) p.carries[tile.row * p.D + col] = h;
-        enter[ch] = h;
+        // the state behind the sequence's last token (or the one it began with, where it has none)
+        if (p.hT && in && tile.s == tile.last && (mine > 0 ? grp * R + mine == tile.len : grp == 0 && tile.len == 0))
+            store8<false>(p.hT + (long)tile.n * p.D + c, h);
+        if (p.ticket || tile.s == tile.last) break;
+        tile.move(p, tile.s + 1);
     }
-    __syncthreads();
-    if constexpr (!BLEND) {
-#pragma unroll
-        for (int i = 0; i < R; ++i) xr[i].hide();
-    }
-    float h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float2 m = maps[grp][8 * l + e];
-        h[e] = __fmaf_rn(m.x, enter[8 * l + e], m.y);
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        float x[8];
-        if constexpr (!BLEND) xr[i].get(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = __fmaf_rn(a[i][e], h[e], BLEND ? b[i][e] : i < mine ? x[e] : 0.f);
-        if (in && i < mine) store8<NT>(static_cast<TH*>(p.h) + first + (at0 + i * p.D), h);
-    }
-    // the state behind the sequence's last token (or the one it began with, where it has none)
-    if (p.hT && in && tile.s == tile.last && (mine > 0 ? grp * R + mine == tile.len : grp == 0 && tile.len == 0))
-        store8<false>(p.hT + (long)tile.n * p.D + c, h);
-    if (p.ticket || tile.s == tile.last) break;
-    tile.move(p, tile.s + 1);
-  }
 }
 
 // Two work-groups per CU at 128 registers a thread. Blended, a and 1 - a together do not fit: both are formed again from g, and the gradient's
@@ -351,158 +351,158 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
     if (row < 0) return;
     ScanTile tile = scan_tile(p, row, rows, true);
     float back = 0.f;   // walking: what leaves the tile, as in the forward pass
-  for (;;) {
-    unsigned thread = threadIdx.x;
-    asm volatile("" : "+v"(thread));   // what is computed from it is not kept from one tile to the next
-    const int l = thread & 7, grp = thread >> 3;
-    const unsigned c = (unsigned)(cb * kScanChannels + 8 * l);
-    const bool in = c < (unsigned)p.D;
-    const unsigned at0 = (unsigned)(grp * R) * p.D + c;
-    Raw8<TX> xr[R];
-    Raw8<TH> dr[R];
-    Raw8<float> gr[R];
-    const long first = (long)tile.t0 * p.D;
-    const int mine = min(max(tile.len - grp * R, 0), R);
-    const unsigned cl = in ? c : 0;   // loads as in the forward pass
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        xr[i].zero();
-        dr[i].zero();
-        gr[i].zero();
-    }
-    if (tile.len > 0) {
+    for (;;) {
+        unsigned thread = threadIdx.x;
+        asm volatile("" : "+v"(thread));   // what is computed from it is not kept from one tile to the next
+        const int l = thread & 7, grp = thread >> 3;
+        const unsigned c = (unsigned)(cb * kScanChannels + 8 * l);
+        const bool in = c < (unsigned)p.D;
+        const unsigned at0 = (unsigned)(grp * R) * p.D + c;
+        Raw8<TX> xr[R];
+        Raw8<TH> dr[R];
+        Raw8<float> gr[R];
+        const long first = (long)tile.t0 * p.D;
+        const int mine = min(max(tile.len - grp * R, 0), R);
+        const unsigned cl = in ? c : 0;   // loads as in the forward pass
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int t = min(grp * R + i, tile.len - 1);
-            const unsigned at = (unsigned)t * (unsigned)p.D + cl;
-            gr[i].load(p.g + first + at);
-            xr[i].load(static_cast<const TX*>(p.x) + (tile.t0 + t) * p.x_row + cl);
-            dr[i].load(static_cast<const TH*>(p.dh) + first + at);
+            xr[i].zero();
+            dr[i].zero();
+            gr[i].zero();
         }
-    }
-    float a[BLEND ? 1 : R][8], A[8], H[8], E[8];
+        if (tile.len > 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) A[e] = 1.f, H[e] = E[e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        float g[8], x[8], d[8];
-        gr[i].get(g);
-        xr[i].get(x);
-        dr[i].get(d);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (i >= mine) g[e] = x[e] = d[e] = 0.f;
-            const float at = __expf(g[e]);
-            if constexpr (BLEND) x[e] *= one_minus_exp(g[e], at);
-            else a[i][e] = at;
-            H[e] = __fmaf_rn(at, H[e], x[e]);
-            A[e] *= at;
-            if constexpr (BLEND) E[e] = __fmaf_rn(A[e], d[e], E[e]);
+            for (int i = 0; i < R; ++i) {
+                const int t = min(grp * R + i, tile.len - 1);
+                const unsigned at = (unsigned)t * (unsigned)p.D + cl;
+                gr[i].load(p.g + first + at);
+                xr[i].load(static_cast<const TX*>(p.x) + (tile.t0 + t) * p.x_row + cl);
+                dr[i].load(static_cast<const TH*>(p.dh) + first + at);
+            }
         }
-    }
-    if constexpr (!BLEND) {
+        float a[BLEND ? 1 : R][8], A[8], H[8], E[8];
 #pragma unroll
-        for (int i = R - 1; i >= 0; --i) {
-            float d[8];
+        for (int e = 0; e < 8; ++e) A[e] = 1.f, H[e] = E[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float g[8], x[8], d[8];
+            gr[i].get(g);
+            xr[i].get(x);
             dr[i].get(d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) E[e] = a[i][e] * ((i < mine ? d[e] : 0.f) + E[e]);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        mA[grp][8 * l + e] = A[e];
-        mH[grp][8 * l + e] = H[e];
-        mE[grp][8 * l + e] = E[e];
-    }
-    __syncthreads();
-    const int wave = thread >> 6, ch = thread & 63;
-    const unsigned col = (unsigned)(cb * kScanChannels + ch);
-    if (wave == 0) {   // the states entering the groups
-        float h = col < (unsigned)p.D ? p.carries[tile.row * p.D + col] : 0.f;
-#pragma unroll 16
-        for (int k = 0; k < G; ++k) {
-            const float m = mA[k][ch], q = mH[k][ch];
-            mH[k][ch] = h;
-            h = __fmaf_rn(m, h, q);
-        }
-    }
-    if (wave == (G > 8 ? 1 : 0)) {   // the map of the groups behind each, and what comes from the tiles behind this one
-        float At = 1.f, Et = 0.f;
-#pragma unroll 16
-        for (int k = G - 1; k >= 0; --k) {
-            const float m = mA[k][ch], q = mE[k][ch];
-            mS[k][ch] = At;
-            mE[k][ch] = Et;
-            Et = __fmaf_rn(m, Et, q);
-            At *= m;
-        }
-        const long at = row * p.ncb * kScanChannels + col;
-        float d = back;
-        if (tile.s == tile.last) {
-            if (p.dhT && col < (unsigned)p.D) d = p.dhT[(long)tile.n * p.D + col];
-        } else if (p.ticket) {
-            publish_map(p.agg + at, At, Et);
-            d = enter_from(p, row, 1, tile.last - tile.s, col);
-        }
-        back = __fmaf_rn(At, d, Et);
-        if (p.ticket && tile.s > 0) publish_state(p.pref + at, back);
-        enter[ch] = d;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        xr[i].hide();
-        dr[i].hide();
-        if constexpr (BLEND) hide(gr[i]);
-    }
-    // backward over the tokens for D, which takes the place of dh, then forward for the states
-    float D[R][8], h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) E[e] = __fmaf_rn(mS[grp][8 * l + e], enter[8 * l + e], mE[grp][8 * l + e]);
-#pragma unroll
-    for (int i = R - 1; i >= 0; --i) {
-        float g[8];
-        gr[i].get(g);
-        dr[i].get(D[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            D[i][e] = (i < mine ? D[i][e] : 0.f) + E[e];
-            E[e] = (BLEND ? __expf(i < mine ? g[e] : 0.f) : a[i][e]) * D[i][e];
-        }
-    }
-    if (p.dh0 && in && tile.s == 0 && grp == 0) store8<false>(p.dh0 + (long)tile.n * p.D + c, E);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-        if constexpr (BLEND) hide(gr[i]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = mH[grp][8 * l + e];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {   // tokens past the end are the last ones: what becomes of h there meets nobody
-        float g[8], x[8];
-        gr[i].get(g);
-        xr[i].get(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float at = BLEND ? __expf(g[e]) : a[i][e], Et = at * D[i][e];
-            if constexpr (BLEND) {
-                const float keep = one_minus_exp(g[e], at);
-                g[e] = Et * (h[e] - x[e]);
-                D[i][e] *= keep;
-                x[e] *= keep;
-            } else {
-                g[e] = Et * h[e];
+            for (int e = 0; e < 8; ++e) {
+                if (i >= mine) g[e] = x[e] = d[e] = 0.f;
+                const float at = __expf(g[e]);
+                if constexpr (BLEND) x[e] *= one_minus_exp(g[e], at);
+                else a[i][e] = at;
+                H[e] = __fmaf_rn(at, H[e], x[e]);
+                A[e] *= at;
+                if constexpr (BLEND) E[e] = __fmaf_rn(A[e], d[e], E[e]);
             }
-            h[e] = __fmaf_rn(at, h[e], x[e]);
         }
-        if (in && i < mine) {
-            store8<NT>(static_cast<TX*>(p.dx) + first + (at0 + i * p.D), D[i]);
-            store8<NT>(p.dg + first + (at0 + i * p.D), g);
+        if constexpr (!BLEND) {
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) {
+                float d[8];
+                dr[i].get(d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) E[e] = a[i][e] * ((i < mine ? d[e] : 0.f) + E[e]);
+            }
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            mA[grp][8 * l + e] = A[e];
+            mH[grp][8 * l + e] = H[e];
+            mE[grp][8 * l + e] = E[e];
+        }
+        __syncthreads();
+        const int wave = thread >> 6, ch = thread & 63;
+        const unsigned col = (unsigned)(cb * kScanChannels + ch);
+        if (wave == 0) {   // the states entering the groups
+            float h = col < (unsigned)p.D ? p.carries[tile.row * p.D + col] : 0.f;
+#pragma unroll 16
+            for (int k = 0; k < G; ++k) {
+                const float m = mA[k][ch], q = mH[k][ch];
+                mH[k][ch] = h;
+                h = __fmaf_rn(m, h, q);
+            }
+        }
+        if (wave == (G > 8 ? 1 : 0)) {   // the map of the groups behind each, and what comes from the tiles behind this one
+            float At = 1.f, Et = 0.f;
+#pragma unroll 16
+            for (int k = G - 1; k >= 0; --k) {
+                const float m = mA[k][ch], q = mE[k][ch];
+                mS[k][ch] = At;
+                mE[k][ch] = Et;
+                Et = __fmaf_rn(m, Et, q);
+                At *= m;
+            }
+            const long at = row * p.ncb * kScanChannels + col;
+            float d = back;
+            if (tile.s == tile.last) {
+                if (p.dhT && col < (unsigned)p.D) d = p.dhT[(long)tile.n * p.D + col];
+            } else if (p.ticket) {
+                publish_map(p.agg + at, At, Et);
+                d = enter_from(p, row, 1, tile.last - tile.s, col);
+            }
+            back = __fmaf_rn(At, d, Et);
+            if (p.ticket && tile.s > 0) publish_state(p.pref + at, back);
+            enter[ch] = d;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            xr[i].hide();
+            dr[i].hide();
+            if constexpr (BLEND) hide(gr[i]);
+        }
+        // backward over the tokens for D, which takes the place of dh, then forward for the states
+        float D[R][8], h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) E[e] = __fmaf_rn(mS[grp][8 * l + e], enter[8 * l + e], mE[grp][8 * l + e]);
+#pragma unroll
+        for (int i = R - 1; i >= 0; --i) {
+            float g[8];
+            gr[i].get(g);
+            dr[i].get(D[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                D[i][e] = (i < mine ? D[i][e] : 0.f) + E[e];
+                E[e] = (BLEND ? __expf(i < mine ? g[e] : 0.f) : a[i][e]) * D[i][e];
+            }
+        }
+        if (p.dh0 && in && tile.s == 0 && grp == 0) store8<false>(p.dh0 + (long)tile.n * p.D + c, E);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if constexpr (BLEND) hide(gr[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = mH[grp][8 * l + e];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {   // tokens past the end are the last ones: what becomes of h there meets nobody
+            float g[8], x[8];
+            gr[i].get(g);
+            xr[i].get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float at = BLEND ? __expf(g[e]) : a[i][e], Et = at * D[i][e];
+                if constexpr (BLEND) {
+                    const float keep = one_minus_exp(g[e], at);
+                    g[e] = Et * (h[e] - x[e]);
+                    D[i][e] *= keep;
+                    x[e] *= keep;
+                } else {
+                    g[e] = Et * h[e];
+                }
+                h[e] = __fmaf_rn(at, h[e], x[e]);
+            }
+            if (in && i < mine) {
+                store8<NT>(static_cast<TX*>(p.dx) + first + (at0 + i * p.D), D[i]);
+                store8<NT>(p.dg + first + (at0 + i * p.D), g);
+            }
+        }
+        if (p.ticket || tile.s == 0) break;
+        tile.move(p, tile.s - 1);
     }
-    if (p.ticket || tile.s == 0) break;
-    tile.move(p, tile.s - 1);
-  }
 }
 
 // Runs of tokens on a pool of states: a lane walks its sequence's tokens for four channels. Tokens come four at a time, so that a run waits for memory once
