@@ -5,10 +5,12 @@
 // Backward, with D_t the gradient reaching h_t and E_t = a_t D_t what it passes on to h_{t-1}:
 //     D_t = dh_t + E_{t+1},   E_{len+1} = dhT,   dx = D or (1 - a) D,   dg = E_t h_{t-1} or E_t (h_{t-1} - x_t),   dh0 = E_1.
 // Four operations an element against 8 (forward) or 14 (backward) bytes in bf16: bound by bytes, if the sequence is cut. A run of tokens
-// maps the state entering it to the one leaving it by h -> A h + H, and such maps compose, so every thread first forms the
-// map of its few tokens (8 channels wide, as loaded, in registers), the maps of a tile of 256 tokens (or 32) x 64 channels are joined in LDS, and
-// with the state entering the tile known each thread runs its tokens again from registers: inputs are read once, outputs
-// written once.
+// maps the state entering it to the one leaving it by h -> e^G h + H, G the sum of its gates, and such maps compose, so every thread first
+// forms the map of its few tokens (8 channels wide, as loaded, in registers), the maps of a tile of 256 tokens (or 32) x 64 channels are
+// joined in LDS, and with the state entering the tile known each thread runs its tokens again from registers: inputs are read once,
+// outputs written once.
+// Where a gate is slow, e^G in fp32 has lost the digits of 1 - e^G, and a product of such numbers drifts with the length (32768 blended tokens of
+// g = -1e-6 and a constant input: 1.5e-3 off). So maps go by sums of gates, and where G > -1/2 by K = 1 - e^G: h + (H - K h).
 // The state entering a tile comes from the tiles before it, in the same launch: a tile publishes its own map as soon as it has it, and its
 // final state once it knows what enters. One that waits reads the four tiles before it and goes on from the last
 // final state through the maps behind it. It always takes the same sums in the same order, wherever it finds the state, so the
@@ -25,10 +27,39 @@ namespace gdn {
 constexpr uint32_t kNotYet = 0xffffffffu;
 constexpr int kLookBack = 4;
 
+// 1 - e^g for g in (-1/2, 1/2): the series to g^9 / 9! (the rest is below 2^-27 of it).
+__device__ __forceinline__ float complement(float g) {
+    float s = 1.f / 362880.f;
+    s = __fmaf_rn(s, g, 1.f / 40320.f);
+    s = __fmaf_rn(s, g, 1.f / 5040.f);
+    s = __fmaf_rn(s, g, 1.f / 720.f);
+    s = __fmaf_rn(s, g, 1.f / 120.f);
+    s = __fmaf_rn(s, g, 1.f / 24.f);
+    s = __fmaf_rn(s, g, 1.f / 6.f);
+    s = __fmaf_rn(s, g, 0.5f);
+    s = __fmaf_rn(s, g, 1.f);
+    return -g * s;
+}
+// 1 - e^g, a = e^g: 1 - a loses the digits of a small difference.
+__device__ __forceinline__ float one_minus_exp(float g, float a) {
+    const float k = complement(g);   // always: a branch here costs registers and spills
+    return fabsf(g) < 0.5f ? k : 1.f - a;
+}
+// The factor of a map as one number, with the digits that matter: e^G, or where that is near 1 minus its distance to 1. decay(0) = 1: what is infinite
+// stays so where nothing decays.
+__device__ __forceinline__ float decay(float G) {
+    const float k = complement(G), a = __expf(G);
+    return ((G < 0.f) & (G > -0.5f)) ? -k : a;
+}
+__device__ __forceinline__ float apply(float q, float h, float H) {
+    const float t = __fmaf_rn(q, h, H);
+    return __float_as_int(q) < 0 ? h + t : t;
+}
+
 // a value that is never the mark (any NaN becomes the ordinary one)
 __device__ __forceinline__ float publishable(float x) { return x == x ? x : __uint_as_float(0x7fc00000u); }
-__device__ __forceinline__ void publish_map(uint64_t* p, float A, float H) {
-    const uint64_t w = (uint64_t)__float_as_uint(publishable(H)) << 32 | __float_as_uint(publishable(A));
+__device__ __forceinline__ void publish_map(uint64_t* p, float q, float H) {
+    const uint64_t w = (uint64_t)__float_as_uint(publishable(H)) << 32 | __float_as_uint(publishable(q));
     __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void publish_state(float* p, float h) {
@@ -55,7 +86,7 @@ __device__ __forceinline__ float enter_from(const ScanProblem& p, long row, int 
         for (int j = kLookBack - 1; j >= 0; --j) {
             if (j < depth) {
                 const bool here = state[j] != kNotYet, mapped = (uint32_t)map[j] != kNotYet;
-                const float through = __fmaf_rn(__uint_as_float((uint32_t)map[j]), c, __uint_as_float((uint32_t)(map[j] >> 32)));
+                const float through = apply(__uint_as_float((uint32_t)map[j]), c, __uint_as_float((uint32_t)(map[j] >> 32)));
                 c = here ? __uint_as_float(state[j]) : through;
                 ok = here || (ok && mapped);
             }
@@ -140,20 +171,6 @@ __device__ __forceinline__ long draw_row(const ScanProblem& p, const ScanPlace& 
     return __builtin_amdgcn_readfirstlane(*lds);   // one for all: rows and addresses stay scalar
 }
 
-// 1 - e^g: 1 - a loses the digits of a small difference. For g in (-1/2, 1/2) the series to g^9 / 9! (the rest is below 2^-27 of it).
-__device__ __forceinline__ float one_minus_exp(float g, float a) {
-    float s = 1.f / 362880.f;
-    s = __fmaf_rn(s, g, 1.f / 40320.f);
-    s = __fmaf_rn(s, g, 1.f / 5040.f);
-    s = __fmaf_rn(s, g, 1.f / 720.f);
-    s = __fmaf_rn(s, g, 1.f / 120.f);
-    s = __fmaf_rn(s, g, 1.f / 24.f);
-    s = __fmaf_rn(s, g, 1.f / 6.f);
-    s = __fmaf_rn(s, g, 0.5f);
-    s = __fmaf_rn(s, g, 1.f);
-    return fabsf(g) < 0.5f ? -g * s : 1.f - a;
-}
-
 // Lays the tiles of packed sequences out, by one work-group: K sequences a thread at a time.
 template <int K>
 __device__ __forceinline__ void lay_tiles_out(const ScanProblem& p, int* sum) {
@@ -215,13 +232,24 @@ __device__ __forceinline__ void hide(Raw8<float>& r) {
     asm volatile("" : "+v"(r.a.x), "+v"(r.a.y), "+v"(r.a.z), "+v"(r.a.w), "+v"(r.b.x), "+v"(r.b.y), "+v"(r.b.z), "+v"(r.b.w));
 }
 constexpr int scan_threads(int TOK) { return 8 * TOK / R; }
+// A wave's threads form the maps of eight groups, and as lanes of one channel each they join them; the first wave joins the waves' maps, and hands
+// every wave what enters it. What all waves read of another is written between the two barriers of a tile or by it alone, so that a
+// work-group that walks needs no third one.
+constexpr int kGroups = 8;
+__device__ __forceinline__ void wave_fence() {   // between LDS writes of some lanes and reads of others of the same wave
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
-// TOK: tokens of a tile; TOK / R groups of 8 lanes, 8 channels a lane. 32768 x 2048 in bf16, blended: 99 us, 5.6 TB/s.
+// TOK: tokens of a tile; TOK / R groups of 8 lanes, 8 channels a lane. 32768 x 2048 in bf16, blended: 101 us, 5.3 TB/s (1.5 us of it for factors
+// with the digits of slow gates).
 template <typename TX, typename TH, int TOK, bool BLEND, bool NT>
 __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProblem p) {
-    constexpr int G = TOK / R;
-    __shared__ float2 maps[G][kScanChannels];
-    __shared__ float enter[kScanChannels];
+    constexpr int G = TOK / R, W = G / kGroups;
+    __shared__ float2 maps[G][kScanChannels];    // of every group: G, then the state entering it; H
+    __shared__ float sums[W][kScanChannels];     // of every wave's groups together: G
+    __shared__ float2 waves[W][kScanChannels];   // factor and H
+    __shared__ float enter[W][kScanChannels];    // the state entering it
     __shared__ int ticket;
     const long rows = scan_rows(p);
     const ScanPlace place = scan_place(p);
@@ -258,9 +286,9 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
                 xr[i].load(static_cast<const TX*>(p.x) + (tile.t0 + t) * p.x_row + cl);
             }
         }
-        float a[R][8], b[BLEND ? R : 1][8], A[8], H[8];
+        float a[R][8], b[BLEND ? R : 1][8], S[8], H[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) A[e] = 1.f, H[e] = 0.f;
+        for (int e = 0; e < 8; ++e) S[e] = H[e] = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {   // tokens past the end: g = 0, x = 0, the state as it is
             float x[8];
@@ -276,48 +304,75 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
                     b[i][e] = x[e];
                 }
                 H[e] = __fmaf_rn(a[i][e], H[e], x[e]);
-                A[e] *= a[i][e];
+                S[e] += g;
             }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) maps[grp][8 * l + e] = make_float2(A[e], H[e]);
+        for (int e = 0; e < 8; ++e) maps[grp][8 * l + e] = make_float2(S[e], H[e]);
+        wave_fence();
+        const int wave = __builtin_amdgcn_readfirstlane(thread >> 6), ch = thread & 63, g0 = kGroups * wave;
+        float qk[kGroups], hk[kGroups];
+        {
+            float St = 0.f, Ht = 0.f;
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                const float2 m = maps[g0 + k][ch];
+                qk[k] = decay(m.x);
+                hk[k] = m.y;
+                Ht = apply(qk[k], Ht, m.y);
+                St += m.x;
+            }
+            sums[wave][ch] = St;
+            waves[wave][ch] = make_float2(decay(St), Ht);
+        }
         __syncthreads();
-        if (thread < kScanChannels) {
-            const int ch = thread;
+        if (wave == 0) {
             const unsigned col = (unsigned)(cb * kScanChannels + ch);
             const bool real = col < (unsigned)p.D;
-            float At = 1.f, Ht = 0.f;   // the map of the groups before each, in its place
-#pragma unroll 16
-            for (int k = 0; k < G; ++k) {
-                const float2 m = maps[k][ch];
-                maps[k][ch] = make_float2(At, Ht);
-                Ht = __fmaf_rn(m.x, Ht, m.y);
-                At *= m.x;
+            float St = 0.f, Ht = 0.f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const float2 m = waves[k][ch];
+                Ht = apply(m.x, Ht, m.y);
+                St += sums[k][ch];
             }
+            const float q = decay(St);
             const long at = row * p.ncb * kScanChannels + col;
             float h = state;
             if (tile.s == 0) {
                 if (p.h0 && real) h = p.h0[(long)tile.n * p.D + col];
             } else if (p.ticket) {
-                publish_map(p.agg + at, At, Ht);
+                publish_map(p.agg + at, q, Ht);
                 h = enter_from(p, row, -1, tile.s, col);
             }
-            state = __fmaf_rn(At, h, Ht);
+            state = apply(q, h, Ht);
             if (p.ticket && tile.s < tile.last) publish_state(p.pref + at, state);
+            // blended, the map's: the last tokens' own factors would add their rounding to it, call by call
+            if (BLEND && p.hT && real && tile.s == tile.last) p.hT[(long)tile.n * p.D + col] = state;
             if (p.carries && real) p.carries[tile.row * p.D + col] = h;
-            enter[ch] = h;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                enter[k][ch] = h;
+                h = apply(waves[k][ch].x, h, waves[k][ch].y);
+            }
         }
         __syncthreads();
+        {
+            float h = enter[wave][ch];
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                maps[g0 + k][ch].x = h;
+                h = apply(qk[k], h, hk[k]);
+            }
+        }
+        wave_fence();
         if constexpr (!BLEND) {
 #pragma unroll
             for (int i = 0; i < R; ++i) xr[i].hide();
         }
         float h[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 m = maps[grp][8 * l + e];
-            h[e] = __fmaf_rn(m.x, enter[8 * l + e], m.y);
-        }
+        for (int e = 0; e < 8; ++e) h[e] = maps[grp][8 * l + e].x;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             float x[8];
@@ -327,7 +382,7 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
             if (in && i < mine) store8<NT>(static_cast<TH*>(p.h) + first + (at0 + i * p.D), h);
         }
         // the state behind the sequence's last token (or the one it began with, where it has none)
-        if (p.hT && in && tile.s == tile.last && (mine > 0 ? grp * R + mine == tile.len : grp == 0 && tile.len == 0))
+        if (!BLEND && p.hT && in && tile.s == tile.last && (mine > 0 ? grp * R + mine == tile.len : grp == 0 && tile.len == 0))
             store8<false>(p.hT + (long)tile.n * p.D + c, h);
         if (p.ticket || tile.s == tile.last) break;
         tile.move(p, tile.s + 1);
@@ -339,10 +394,12 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
 // 64, half the size 29 and 34). fp32 blended spills even so and has one work-group per CU (84 us against 102).
 template <typename TX, typename TH, int TOK, bool BLEND, bool NT>
 __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4) void scan_bwd_kernel(ScanProblem p) {
-    constexpr int G = TOK / R;
-    // of every group: A; H, then the state entering it; the gradient's part of its map, then that of the groups behind it; their A
-    __shared__ float mA[G][kScanChannels], mH[G][kScanChannels], mE[G][kScanChannels], mS[G][kScanChannels];
-    __shared__ float enter[kScanChannels];
+    constexpr int G = TOK / R, W = G / kGroups;
+    // of every group: G, then its factor; H, then the state entering it; the gradient's part of its map, then the gradient entering it
+    __shared__ float mQ[G][kScanChannels], mH[G][kScanChannels], mE[G][kScanChannels];
+    // of every wave's groups together: G, factor, H, the gradient's part
+    __shared__ float wS[W][kScanChannels], wQ[W][kScanChannels], wH[W][kScanChannels], wE[W][kScanChannels];
+    __shared__ float enter[W][kScanChannels];   // the gradient entering it
     __shared__ int ticket;
     const long rows = scan_rows(p);
     const ScanPlace place = scan_place(p);
@@ -380,9 +437,9 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
                 dr[i].load(static_cast<const TH*>(p.dh) + first + at);
             }
         }
-        float a[BLEND ? 1 : R][8], A[8], H[8], E[8];
+        float a[BLEND ? 1 : R][8], A[8], S[8], H[8], E[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) A[e] = 1.f, H[e] = E[e] = 0.f;
+        for (int e = 0; e < 8; ++e) A[e] = 1.f, S[e] = H[e] = E[e] = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             float g[8], x[8], d[8];
@@ -396,8 +453,11 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
                 if constexpr (BLEND) x[e] *= one_minus_exp(g[e], at);
                 else a[i][e] = at;
                 H[e] = __fmaf_rn(at, H[e], x[e]);
-                A[e] *= at;
-                if constexpr (BLEND) E[e] = __fmaf_rn(A[e], d[e], E[e]);
+                S[e] += g[e];
+                if constexpr (BLEND) {
+                    A[e] *= at;
+                    E[e] = __fmaf_rn(A[e], d[e], E[e]);
+                }
             }
         }
         if constexpr (!BLEND) {
@@ -411,45 +471,74 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            mA[grp][8 * l + e] = A[e];
+            mQ[grp][8 * l + e] = S[e];
             mH[grp][8 * l + e] = H[e];
             mE[grp][8 * l + e] = E[e];
         }
-        __syncthreads();
-        const int wave = thread >> 6, ch = thread & 63;
+        wave_fence();
+        const int wave = __builtin_amdgcn_readfirstlane(thread >> 6), ch = thread & 63, g0 = kGroups * wave;
         const unsigned col = (unsigned)(cb * kScanChannels + ch);
-        if (wave == 0) {   // the states entering the groups
-            float h = col < (unsigned)p.D ? p.carries[tile.row * p.D + col] : 0.f;
-#pragma unroll 16
-            for (int k = 0; k < G; ++k) {
-                const float m = mA[k][ch], q = mH[k][ch];
-                mH[k][ch] = h;
-                h = __fmaf_rn(m, h, q);
+        float h = col < (unsigned)p.D ? p.carries[tile.row * p.D + col] : 0.f;
+        {
+            float St = 0.f, Ht = 0.f, Et = 0.f;
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                const float m = mQ[g0 + k][ch], q = decay(m);
+                mQ[g0 + k][ch] = q;
+                Ht = apply(q, Ht, mH[g0 + k][ch]);
+                St += m;
             }
+#pragma unroll
+            for (int k = kGroups - 1; k >= 0; --k) Et = apply(mQ[g0 + k][ch], Et, mE[g0 + k][ch]);
+            wS[wave][ch] = St;
+            wQ[wave][ch] = decay(St);
+            wH[wave][ch] = Ht;
+            wE[wave][ch] = Et;
         }
-        if (wave == (G > 8 ? 1 : 0)) {   // the map of the groups behind each, and what comes from the tiles behind this one
-            float At = 1.f, Et = 0.f;
-#pragma unroll 16
-            for (int k = G - 1; k >= 0; --k) {
-                const float m = mA[k][ch], q = mE[k][ch];
-                mS[k][ch] = At;
-                mE[k][ch] = Et;
-                Et = __fmaf_rn(m, Et, q);
-                At *= m;
+        __syncthreads();
+        if (wave == 0) {   // what comes from the tiles behind this one
+            float St = 0.f, Et = 0.f;
+#pragma unroll
+            for (int k = W - 1; k >= 0; --k) {
+                Et = apply(wQ[k][ch], Et, wE[k][ch]);
+                St += wS[k][ch];
             }
+            const float q = decay(St);
             const long at = row * p.ncb * kScanChannels + col;
             float d = back;
             if (tile.s == tile.last) {
                 if (p.dhT && col < (unsigned)p.D) d = p.dhT[(long)tile.n * p.D + col];
             } else if (p.ticket) {
-                publish_map(p.agg + at, At, Et);
+                publish_map(p.agg + at, q, Et);
                 d = enter_from(p, row, 1, tile.last - tile.s, col);
             }
-            back = __fmaf_rn(At, d, Et);
+            back = apply(q, d, Et);
             if (p.ticket && tile.s > 0) publish_state(p.pref + at, back);
-            enter[ch] = d;
+#pragma unroll
+            for (int k = W - 1; k >= 0; --k) {
+                enter[k][ch] = d;
+                d = apply(wQ[k][ch], d, wE[k][ch]);
+            }
+        }
+        // the states entering the groups
+        for (int k = 0; k < wave; ++k) h = apply(wQ[k][ch], h, wH[k][ch]);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const float m = mH[g0 + k][ch];
+            mH[g0 + k][ch] = h;
+            h = apply(mQ[g0 + k][ch], h, m);
         }
         __syncthreads();
+        {
+            float d = enter[wave][ch];
+#pragma unroll
+            for (int k = kGroups - 1; k >= 0; --k) {
+                const float m = mE[g0 + k][ch];
+                mE[g0 + k][ch] = d;
+                d = apply(mQ[g0 + k][ch], d, m);
+            }
+        }
+        wave_fence();
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             xr[i].hide();
@@ -457,9 +546,9 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
             if constexpr (BLEND) hide(gr[i]);
         }
         // backward over the tokens for D, which takes the place of dh, then forward for the states
-        float D[R][8], h[8];
+        float D[R][8], hs[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) E[e] = __fmaf_rn(mS[grp][8 * l + e], enter[8 * l + e], mE[grp][8 * l + e]);
+        for (int e = 0; e < 8; ++e) E[e] = mE[grp][8 * l + e];
 #pragma unroll
         for (int i = R - 1; i >= 0; --i) {
             float g[8];
@@ -476,9 +565,9 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
         for (int i = 0; i < R; ++i)
             if constexpr (BLEND) hide(gr[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = mH[grp][8 * l + e];
+        for (int e = 0; e < 8; ++e) hs[e] = mH[grp][8 * l + e];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {   // tokens past the end are the last ones: what becomes of h there meets nobody
+        for (int i = 0; i < R; ++i) {   // tokens past the end are the last ones: what becomes of the state there meets nobody
             float g[8], x[8];
             gr[i].get(g);
             xr[i].get(x);
@@ -487,13 +576,13 @@ __global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4
                 const float at = BLEND ? __expf(g[e]) : a[i][e], Et = at * D[i][e];
                 if constexpr (BLEND) {
                     const float keep = one_minus_exp(g[e], at);
-                    g[e] = Et * (h[e] - x[e]);
+                    g[e] = Et * (hs[e] - x[e]);
                     D[i][e] *= keep;
                     x[e] *= keep;
                 } else {
-                    g[e] = Et * h[e];
+                    g[e] = Et * hs[e];
                 }
-                h[e] = __fmaf_rn(at, h[e], x[e]);
+                hs[e] = __fmaf_rn(at, hs[e], x[e]);
             }
             if (in && i < mine) {
                 store8<NT>(static_cast<TX*>(p.dx) + first + (at0 + i * p.D), D[i]);
@@ -547,8 +636,8 @@ __global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblo
                 gr[i].get(g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float a = __expf(g[e]);
-                    h[e] = __fmaf_rn(a, h[e], BLEND ? one_minus_exp(g[e], a) * x[e] : x[e]);
+                    const float q = decay(g[e]);
+                    h[e] = apply(q, h[e], BLEND ? one_minus_exp(g[e], q) * x[e] : x[e]);
                 }
                 store4c(hp + (long)t * p.D, h);
                 if (p.out_slots) {

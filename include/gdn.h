@@ -572,9 +572,12 @@ int gdn_conv_update(const void *x, const float *weight, const float *bias, void 
  *               contents need not be set and mean nothing afterwards; calls that can run at once need one each
  *   D           a multiple of 8 up to 2^20; B * T <= 2^28, B * T * D <= 2^36, N <= 2^24, N * D <= 2^31 and tiles *
  *               ceil(D / 64) < 2^23
- * Offsets outside [0, T] are clamped; rows of the outputs that no sequence covers are left as they were. hT may be h0; h may not overlap
- * an input. x, g, h and hT are aligned to 16 bytes, h0 and carries to 4; x_stride is a multiple of 16 bytes. States are fp32; 1 - a is formed from g and keeps its digits
- * where a is near 1. A NaN in x, g or h0, or an infinity in x or h0, makes its channel's states NaN or infinite from there to the sequence's end.
+ * Offsets outside [0, T] are clamped; rows of the outputs that no sequence covers are left as they were. hT may be h0; h may not
+ * overlap an input. x, g, h and hT are aligned to 16 bytes, h0 and carries to 4; x_stride is a multiple of 16 bytes. States are fp32.
+ * 1 - a is formed from g and keeps its digits where a is near 1, and so does the decay of many tokens, which goes by the sum of their
+ * gates: errors do not grow with the length but for the rounding of the states themselves, once a tile. Blended, h0 = x = c stays c
+ * to some 2^-20 of it, and hT, which does not pass through the last tokens one by one, may differ from the last h in its last digits.
+ * A NaN in x, g or h0, or an infinity in x or h0, makes its channel's states NaN or infinite from there to the sequence's end.
  * The same inputs give the same bits.
  */
 int64_t gdn_scan_carry_rows(int B, int T, int N, int varlen);
