@@ -51,9 +51,9 @@ __device__ __forceinline__ float decay(float G) {
     const float k = complement(G), a = __expf(G);
     return ((G < 0.f) & (G > -0.5f)) ? -k : a;
 }
+// One map applied. (Chosen before the sum, which shortens the chains of maps: 1 x 262144 x 64 204 us otherwise, 192 so.)
 __device__ __forceinline__ float apply(float q, float h, float H) {
-    const float t = __fmaf_rn(q, h, H);
-    return __float_as_int(q) < 0 ? h + t : t;
+    return __fmaf_rn(q, h, H) + (__float_as_int(q) < 0 ? h : 0.f);
 }
 
 // a value that is never the mark (any NaN becomes the ordinary one)
@@ -389,11 +389,13 @@ __global__ __launch_bounds__(scan_threads(TOK), 4) void scan_fwd_kernel(ScanProb
     }
 }
 
-// Two work-groups per CU at 128 registers a thread. Blended, a and 1 - a together do not fit: both are formed again from g, and the gradient's
-// part of a tile's map is summed forward, so that a is not kept for it either (4 x 2048 x 2048 in bf16 60 us; with both kept and one work-group per CU
-// 64, half the size 29 and 34). fp32 blended spills even so and has one work-group per CU (84 us against 102).
+// Two work-groups per CU at 128 registers a thread for bf16 x. Blended, a and 1 - a together do not fit: both are formed again from g, and the
+// gradient's part of a tile's map is summed forward, so that a is not kept for it either (4 x 2048 x 2048 in bf16 60 us; with both kept and one
+// work-group per CU 64, half the size 29 and 34). fp32 x spills even so and has one work-group per CU (us, one and two: blended 4 x 2048 x 2048 84 and
+// 102; plain 80 and 84, 1 x 262144 x 64 194 and 238, 64 packed sequences of 128 x 2048 90 and 85). bf16 x with an fp32 h spills 7 registers without
+// blend and keeps two (4 x 2048 x 2048 64 and 64, packed 70 and 79; 1 x 262144 x 64 232 and 190).
 template <typename TX, typename TH, int TOK, bool BLEND, bool NT>
-__global__ __launch_bounds__(scan_threads(TOK), BLEND && sizeof(TX) == 4 ? 2 : 4) void scan_bwd_kernel(ScanProblem p) {
+__global__ __launch_bounds__(scan_threads(TOK), sizeof(TX) == 4 ? 2 : 4) void scan_bwd_kernel(ScanProblem p) {
     constexpr int G = TOK / R, W = G / kGroups;
     // of every group: G, then its factor; H, then the state entering it; the gradient's part of its map, then the gradient entering it
     __shared__ float mQ[G][kScanChannels], mH[G][kScanChannels], mE[G][kScanChannels];
