@@ -464,3 +464,25 @@ def test_offsets_past_32_bits():
     ref, after = CV.run(z["x"][0], z["w"], None, z["w0"], [0], [0, 2], None, False)
     assert np.abs(y.cpu().double().numpy() - ref).max() <= 2.0 ** -8 * np.abs(ref).max() + 1e-5
     assert np.array_equal(pool[89999].cpu().double().numpy(), after[0]) and not pool[:89999].any()
+
+
+@pytest.mark.gpu
+def test_more_work_groups_than_one_row_of_the_grid():
+    """Forward work-groups past 2^23, which go on in the grid's second row: 24 tokens each of 8 channels; a broadcast token, so that all
+    rows behind the first W - 1 are alike, and a window behind the end."""
+    T, D, W = 24 * (1 << 23) + 1000, 8, 4
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GiB")
+    print(f"[gpu] conv T={T} D={D}", flush=True)
+    x = make(3, 1, 1, 1, D, W, "bf16")
+    t = {n: a.cuda() for n, a in x.items()}
+    y = torch.zeros(1, T, D, device="cuda", dtype=torch.bfloat16)
+    _, wT = gb.gdn_conv_fwd(t["x"].expand(1, T, D), t["w"], t["b"], t["w0"], activation="silu", y=y)
+    n = W + 2
+    want, _ = gb.gdn_conv_fwd(t["x"].expand(1, n, D).contiguous(), t["w"], t["b"], t["w0"], activation="silu")
+    check_fwd(x["x"].expand(1, n, D), x["w"], x["b"], x["w0"], None, True, want, None)
+    assert torch.equal(y[:, :W], want[:, :W]) and torch.equal(wT, t["x"].expand(1, W - 1, D))
+    edge = 24 * (1 << 23)
+    for lo, hi in ((W, 5000), (edge - 5000, edge + 1000), ((1 << 27) - 100, (1 << 27) + 100)):
+        assert torch.equal(y[0, lo:hi], want[0, n - 1].expand(hi - lo, D)), lo
+    assert torch.equal(y[0, W:].amin(0), want[0, n - 1]) and torch.equal(y[0, W:].amax(0), want[0, n - 1])
