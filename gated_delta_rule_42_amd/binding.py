@@ -879,7 +879,7 @@ def gdn_scan_fwd(x, g, h0=None, cu_seqlens=None, *, blend=False, h=None, hT=None
     a_t h_{t-1} + (1 - a_t) x_t, a = exp(g), g [B, T, D] fp32 <= 0. h0 [N, D] fp32 or None (zeros); cu_seqlens int32 [N+1]: packed
     sequences (B = 1). Returns h [B, T, D] (out_dtype, default the dtype of x; rows that no sequence covers are not written), the
     final states [N, D] fp32 (None unless output_final_state) and, with keep_carries, what gdn_scan_bwd takes of this
-    pass (fp32, a row per tile of 256 or 32 tokens), else None."""
+    pass (fp32, a row per tile of 256 tokens, or of 32 where the sequences, empty ones among them, are short on average), else None."""
     B, T, D, N = _check_sequences(x, cu_seqlens)
     dtype, dev = x.dtype, x.device
     _expect(g, "g", (B, T, D), _F32)

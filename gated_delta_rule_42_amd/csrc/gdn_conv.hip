@@ -144,7 +144,7 @@ __device__ __forceinline__ void move_on(float (&u)[W][V]) {
 }
 
 // Work-groups in rows of cblocks, which share tokens; those past the `tiles` rows of tiles leave the windows, a wave per sequence. TL = 6 tokens a wave:
-// with fewer the rows before a tile weigh more, with more there are fewer waves (4 x 2048 x 6144 bf16, TL 4, 6, 8, 12: 41.5, 38.6, 40.0, 40.5 us; fp32
+// with fewer the rows before a tile weigh more, with more there are fewer waves (kernels, 4 x 2048 x 6144 bf16, TL 4, 6, 8, 12: 41.5, 38.6, 40.0, 40.5 us; fp32
 // 70.7, 69.8, 71.6, 74.7; 8 x 500 x 2048 9.2, 9.0, 9.7, 10.7). Bound by bytes: 5.2 TB/s.
 template <typename T, int W, int TL, bool SILU>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvProblem p, int cblocks, int tiles) {
@@ -272,8 +272,8 @@ __device__ __forceinline__ void window_gradient(const ConvProblem& p, int n, lon
 
 // Backward, a wave walks a run of tokens, blocks of BL at a time, the next block's rows in flight while the current one is worked on. It
 // carries the last W - 1 inputs and dz; a token's dx is complete W - 1 tokens later, so that a run goes W - 1 tokens past its end (where
-// its sequence does). Run lengths are multiples of BL less W - 1: whole blocks. Packed 8054 x 6144 in bf16: 71 us at 4.6 TB/s, the rate of the largest
-// copies, with 40 us of vector instructions close behind (24 an element).
+// its sequence does). Run lengths are multiples of BL less W - 1: whole blocks. Packed 8053 x 6144 in bf16: 71 us at 4.6 TB/s (a copy of as many
+// bytes 5.3), with 40 us of vector instructions close behind (24 an element).
 //
 // Rows of work-groups below `parts` take four runs each, sum their contributions to dw and db in registers, then over the waves in
 // LDS, and write a partial row [D, W], [D] (the gradients themselves if there is only one); those past them take the windows' gradients. No
@@ -486,7 +486,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, int cblock
 }
 
 // Runs of tokens on a pool of windows: a lane walks its sequence's tokens for V channels. The window stays as loaded, so its rows
-// are moved, never rounded. Tokens come four at a time. 256 sequences of one token, 12288 channels in bf16: 11.7 us, bound by bytes (4.3 TB/s).
+// are moved, never rounded. Tokens come four at a time. 256 sequences of one token, 12288 channels in bf16: 11.9 us, bound by bytes (4.2 TB/s, a
+// copy of as many bytes 4.4).
 template <typename T, int W>
 __global__ __launch_bounds__(256) void conv_update_kernel(ConvProblem p, int cblocks) {
     using Raw = Raw4<T>;

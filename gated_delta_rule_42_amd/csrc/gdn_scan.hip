@@ -11,7 +11,8 @@
 // outputs written once.
 // Where a gate is slow, e^G in fp32 has lost the digits of 1 - e^G, and a product of such numbers drifts with the length (32768 blended tokens of
 // g = -1e-6 and a constant input: 1.5e-3 off). So maps go by sums of gates, and where G > -1/2 by K = 1 - e^G: h + (H - K h).
-// The state entering a tile comes from the tiles before it, in the same launch: a tile publishes its own map as soon as it has it, and its
+// The state entering a tile comes from the tiles before it, in the same launch, as in the published single-pass scan with decoupled look-back (D. Merrill,
+// M. Garland, 2016): a tile publishes its own map as soon as it has it, and its
 // final state once it knows what enters. One that waits reads the four tiles before it and goes on from the last
 // final state through the maps behind it. It always takes the same sums in the same order, wherever it finds the state, so the
 // bits do not depend on timing. Tiles are numbered by a ticket drawn at the start of a work-group, and a tile waits for
@@ -597,7 +598,7 @@ __global__ __launch_bounds__(scan_threads(TOK), sizeof(TX) == 4 ? 2 : 4) void sc
 }
 
 // Runs of tokens on a pool of states: a lane walks its sequence's tokens for four channels. Tokens come four at a time, so that a run waits for memory once
-// in four (24 runs of 5 tokens, 2048 channels: 4.2 us).
+// in four (24 runs of 5 tokens, 2048 channels: 4.9 us).
 template <typename TX, typename TH, bool BLEND>
 __global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblocks) {
     const int n = blockIdx.x / cblocks;
@@ -653,13 +654,14 @@ __global__ __launch_bounds__(64) void scan_update_kernel(ScanProblem p, int cblo
 }
 
 // Tiles of 256 tokens, or of 32 where that leaves most of them empty: rows of at most 32 tokens, and sequences of fewer than 128 (on average, where
-// they are packed) in calls that fill the device (8192 tokens of 2048 channels forward, in tiles of 256 and 32: sequences of 16 tokens 205 and 45 us, of
-// 64 62 and 37, of 128 39 and 38, of 256 31 and 41). In small calls one tile a sequence saves the pass that clears the marks.
+// they are packed) in calls that fill the device (8192 tokens of 2048 channels forward, in tiles of 256 and 32: sequences of 16 tokens 235 and 48 us, of
+// 64 68 and 37, of 128 44 and 39, of 256 33 and 41). In small calls one tile a sequence saves the pass that clears the marks. Empty sequences count in the
+// average, since their number is all that the host knows: one of 32768 x 2048 alone 102 us, beside 255 empty ones 219, beside 256, in tiles of 32, 300.
 // Where no sequence can have more than two tiles (four of 32 tokens) one work-group walks them all, which saves that pass and the wait for other
-// work-groups (1 x 512 x 2048, a call: 17.5 and 13.5 us, backward 18.5 and 15.0; 128 x 64 x 2048 in tiles of 32: 31.9 and 27.8, 50.1 and 48.4), as long as
-// the device holds all of them at once (64 x 512 x 2048: 98 and 99, backward 183 and 206). Three tiles gain no more (8 x 700 x 1024: 17.9 and
-// 15.7, backward 20.6 and 22.8), but packed sequences are as a rule far shorter than all of them together: there the call may have four, which goes
-// before tiles of 32 (40 sequences of 25 tokens, 512 channels: 17.7 and 13.3, backward 18.2 and 14.4).
+// work-groups (1 x 512 x 2048, a call: 14.6 and 10.6 us, backward 17.3 and 13.5; 128 x 64 x 2048 in tiles of 32: 32.1 and 29.7, 51.7 and 47.3), as long as
+// the device holds all of them at once (64 x 512 x 2048: 98 and 103, backward 183 and 205). Three tiles gain no more (8 x 700 x 1024: 16.5 and
+// 16.3, backward 21.1 and 23.6), but packed sequences are as a rule far shorter than all of them together: there the call may have four, which goes
+// before tiles of 32 (40 sequences of 25 tokens, 512 channels: 15.2 passed on, 11.1 walked, backward 17.4 and 14.0).
 ScanLayout scan_layout(int tokens, int T, int N, int D, int varlen) {
     ScanLayout w{};
     const long ncb = ((long)D + kScanChannels - 1) / kScanChannels;

@@ -502,7 +502,9 @@ int gdn_layer_norm_fwd(const void *x, const void *residual, const float *weight,
  * sum elsewhere (dtype, dense): dx [rows, d] (dtype, dense), the gradient of x and of the residual alike, and, where not NULL,
  * the gradients of weight and bias (fp32 [d]; defined also where those were NULL), sums over the rows in a
  * fixed order, which take a workspace of gdn_layer_norm_bwd_workspace_bytes(...) bytes, 256-byte aligned (fp32
- * [work-groups, 2, d]); without them none is used. dx may be dsum, dy or sum where that is dense and of its type.
+ * [work-groups, 2, d]); without them none is used. They are fp32 sums: a lane's share one after another (rows *
+ * max(d, 64) / 2^19 + 2 rows at most), then trees; off by up to that many and 80 times 2^-24 of the sum of magnitudes, as a rule by far
+ * less. dx may be dsum, dy or sum where that is dense and of its type.
  */
 size_t gdn_layer_norm_bwd_workspace_bytes(int rows, int d);
 int gdn_layer_norm_bwd(const void *sum, const void *dy, const void *dsum, const float *weight, void *dx,
@@ -535,7 +537,9 @@ int gdn_conv_fwd(const void *x, const float *weight, const float *bias, const vo
  * projection), and, where not NULL, dweight fp32 [D, W], dbias fp32 [D] and dwindow0 [N, W-1, D] (dtype), each defined also
  * where its operand was NULL. The gradients of weight and bias are sums over all tokens in a fixed order and take a workspace of
  * gdn_conv_bwd_workspace_bytes(...) bytes, 256-byte aligned (fp32 [work-group rows, D (W + 1)]); without them none is
- * used. The outputs may not overlap the inputs (dx = x, dx = dy, dwindow0 = window0, dwindow0 = dwindowT: GDN_ERR_SHAPE).
+ * used. They are fp32 sums: a lane's share one after another (B T ceil(D / 256) / 2048 + 32 tokens at most), then trees; off by up to
+ * that many and 80 times 2^-24 of the sum of magnitudes, as a rule by far less. The outputs may not overlap the inputs (dx = x, dx = dy,
+ * dwindow0 = window0, dwindow0 = dwindowT: GDN_ERR_SHAPE).
  */
 size_t gdn_conv_bwd_workspace_bytes(int B, int T, int D, int width);
 int gdn_conv_bwd(const void *x, const float *weight, const float *bias, const void *window0, const void *dy,
@@ -566,7 +570,8 @@ int gdn_conv_update(const void *x, const float *weight, const float *bias, void 
  *   cu_seqlens  int32 [N + 1] device array of packed sequences (then B = 1) or NULL (N = B)
  *   h           [B, T, D] h_dtype (GDN_BF16 only for bf16 x), dense; hT fp32 [N, D]: the state behind each sequence, or NULL
  *   carries     fp32 [gdn_scan_carry_rows(...), D] or NULL: the state entering every tile of a sequence, for the backward pass. A tile
- *               has 256 tokens, or 32 where sequences are short on average; a sequence has one tile at least, those of one sequence
+ *               has 256 tokens, or 32 where sequences are short on average (fewer than 128 tokens, empty ones counted: 32768 tokens
+ *               beside 256 empty sequences run in tiles of 32, three times as long as alone); a sequence has one tile at least, those of one sequence
  *               follow each other, and rows that are no tile's are not written
  *   workspace   gdn_scan_workspace_bytes(...) bytes, 256-byte aligned; none (0) where all sequences are short. Its
  *               contents need not be set and mean nothing afterwards; calls that can run at once need one each
@@ -589,7 +594,8 @@ int gdn_scan_fwd(const void *x, const float *g, const float *h0, const int32_t *
 /*
  * Backward pass of gdn_scan_fwd on the same x, g, cu_seqlens and the carries that it left: from the gradients dh [B, T, D]
  * (h_dtype, dense) and dhT fp32 [N, D] (or NULL: zero) of its outputs: dx [B, T, D] (dtype, dense), dg fp32 [B, T, D] and, where
- * not NULL, dh0 fp32 [N, D]. Workspace as in gdn_scan_fwd. The outputs may not overlap the inputs.
+ * not NULL, dh0 fp32 [N, D]. Workspace as in gdn_scan_fwd. The outputs may not overlap the inputs. A NaN or an infinity in dh or dhT
+ * makes its channel's gradients NaN or infinite from there to the sequence's beginning.
  */
 int gdn_scan_bwd(const void *x, const float *g, const float *carries, const void *dh, const float *dhT,
                  const int32_t *cu_seqlens, void *dx, float *dg, float *dh0, int B, int T, int N, int D,
