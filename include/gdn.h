@@ -582,6 +582,8 @@ int gdn_conv_update(const void *x, const float *weight, const float *bias, void 
  * 1 - a is formed from g and keeps its digits where a is near 1, and so does the decay of many tokens, which goes by the sum of their
  * gates: errors do not grow with the length but for the rounding of the states themselves, once a tile. Blended, h0 = x = c stays c
  * to some 2^-20 of it, and hT, which does not pass through the last tokens one by one, may differ from the last h in its last digits.
+ * Without blend hT is the last h, whose last tokens (four at most) take a rounded to fp32: for single tokens, call after call, use
+ * gdn_scan_update, which does not.
  * A NaN in x, g or h0, or an infinity in x or h0, makes its channel's states NaN or infinite from there to the sequence's end.
  * The same inputs give the same bits.
  */

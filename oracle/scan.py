@@ -8,7 +8,9 @@ backward D_t = dh_t + E_{t+1}, E_t = a_t D_t, dx = D or (1 - a) D, dg = E (h_{t-
 The bound: let u = 2^-24. In a step, a is off by (1.5 |g| + 3) u of itself (the product g log2 e, the exponential), 1 - a by 12 u
 (the series: nine roundings; past |g| = 1/2, at most (1.5 |g| + 3) a / (1 - a) + 1 < 8), products and sums by a few u of the magnitudes.
 With hbar the recurrence of magnitudes (hbar_t = a hbar_{t-1} + |b_t|), a step adds at most (2 |g| + 16) u hbar_t, and what was off before
-decays with a. Evaluating stretches as maps first and joining them takes each step's a once more in another order: twice that.
+decays with a. Evaluating stretches as maps first and joining them takes each step's a once more in another order: twice that. A map's factor goes by
+the sum G of its n gates, at most 3 additions in a group of four tokens, 8 over groups and 8 over waves one after another, each off by u |G| at most: with
+|G| < 88 (beyond, it is taken for zero) that is less than the 32 n u + 4 |G| u which its steps have.
 Below 2^-126 fp32 has no full digits and results may be taken for zero: an exponential (g < -87) or a product is then off by 2^-126
 itself, whatever its size, so every step adds 4 (1 + hbar) 2^-126, and a product with a factor m that much times m.
 """

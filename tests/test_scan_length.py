@@ -110,3 +110,34 @@ def test_slow_decays(T, cu, blend):
     off = np.abs(dg[0, begin:].double().cpu().numpy() / want - 1) / U
     print(f"      dg: off by {off.max():.1f} u", flush=True)
     assert (off <= 2 * (2 * tiles + 32 * np.abs(G1 * n) + 54 + 16)).all(), "dg"
+
+
+@pytest.mark.parametrize("T,cu", [(1500, None), (2000, [0, 700, 1400, 2000]), (500, None)])
+@pytest.mark.parametrize("blend", [False, True])
+def test_infinities_stay_with_their_channel_and_sequence(T, cu, blend):
+    """An infinite input leaves no finite state behind it in its sequence, an infinite gradient none before it; every other channel and
+    sequence has the bits that it has without them."""
+    print(f"[gpu] scan infinities T={T} cu={cu} blend={blend}", flush=True)
+    D, N, t = 72, 1 if cu is None else len(cu) - 1, 450 if cu is None else 850
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x, g, h0, dh, dhT = r(1, T, D), -r(1, T, D).square() * gates(D, 6).abs().cuda() * 300, r(N, D), r(1, T, D), r(N, D)
+
+    def run():
+        h, hT, car = gb.gdn_scan_fwd(x, g, h0, cut(cu), blend=blend, keep_carries=True)
+        return h, hT, *gb.gdn_scan_bwd(x, g, dh, car, dhT, cut(cu), blend=blend)
+
+    h, hT, dx, dg, dh0 = run()
+    assert all(torch.isfinite(a).all() for a in (h, hT, dx, dg, dh0))
+    x[0, t, 5], dh[0, t, 9] = float("inf"), -float("inf")
+    h2, hT2, dx2, dg2, dh02 = run()
+    n, lo, hi = (0, 0, T) if cu is None else (1, 700, 1400)
+    bad, back = torch.zeros(T, D, dtype=torch.bool, device="cuda"), torch.zeros(T, D, dtype=torch.bool, device="cuda")
+    bad[t:hi, 5], back[lo:t + 1, 9] = True, True
+    assert torch.equal(~torch.isfinite(h2[0]), bad) and torch.equal(h2[0][~bad], h[0][~bad])
+    assert torch.equal(~torch.isfinite(dx2[0]), back) and torch.equal(dx2[0][~back], dx[0][~back])
+    last, first = torch.zeros(N, D, dtype=torch.bool, device="cuda"), torch.zeros(N, D, dtype=torch.bool, device="cuda")
+    last[n, 5], first[n, 9] = True, True
+    assert torch.equal(~torch.isfinite(hT2), last) and torch.equal(hT2[~last], hT[~last])
+    assert torch.equal(~torch.isfinite(dh02), first) and torch.equal(dh02[~first], dh0[~first])
+    assert not torch.isfinite(dg2[0][back]).any() and torch.equal(dg2[0, :, [4, 6, 8, 10]], dg[0, :, [4, 6, 8, 10]])
